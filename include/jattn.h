@@ -86,7 +86,9 @@ enum {
   JATTN_ERR_TIMEOUT = 6,     /* device: a bounded pipeline wait expired */
   JATTN_ERR_UNSUPPORTED = 7, /* device is not sm_103 / no kernel image */
   JATTN_ERR_TOO_LARGE = 8,   /* jattn_fwd_noalloc: problem needs more than the library's scratch */
-  JATTN_ERR_ROPE = 9         /* device: a rotary position at or beyond the cos/sin tables' rows */
+  JATTN_ERR_ROPE = 9,        /* device: a rotary position at or beyond the cos/sin tables' rows */
+  JATTN_ERR_PAGES = 10,      /* device: a page table entry that is no page of the cache */
+  JATTN_ERR_LENGTH = 11      /* device: a cached length or position outside its sequence's pages */
 };
 
 typedef struct {
@@ -305,6 +307,100 @@ int jattn_bwd_mxfp8(const jattn_params_t* p, const int64_t* q_off, const int64_t
                     const float* lse, const uint8_t* dout, const uint8_t* dout_scales, uint16_t* dq, uint16_t* dk,
                     uint16_t* dv, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Paged key/value cache. No counterpart in the pages: a serving counterpart of
+ * the jagged forward, for a model whose sequences (user histories) grow by a
+ * few rows between calls.
+ *
+ * Layout. k and v are page buffers [n_pages, H, page_size, D], H the number of
+ * key/value heads, D 64 or 128, page_size a power of two from 8 to 4096.
+ * Position pos of sequence b lies in row pos % page_size of page
+ * page_table[b * max_pages + pos / page_size] (device int32); entries past
+ * the sequence's last position are never read. Sequences may share pages that
+ * are only read. Format:
+ *   JATTN_CACHE_BF16   k and v hold bf16 rows; the scales are NULL.
+ *   JATTN_CACHE_MXFP8  k and v hold E4M3 codes (uint8), k_scales / v_scales
+ *     [n_pages, H, page_size, D/32] one E8M0 exponent for 32 neighbouring
+ *     values of a row (rows arrive one at a time, so blocks do not span rows
+ *     as jattn_mxfp8_quantize's do). With amax the block's largest magnitude:
+ *     E = max(0, floor(log2(amax)) - 8 + 127), code = E4M3(x / 2^(E - 127)),
+ *     nearest even, saturated to +-448. A block that holds a NaN or an infinity
+ *     gets E = 255 (E8M0's NaN) and reads back as NaN; codes 0x7f / 0xff (E4M3's
+ *     own NaN) are never written.
+ * Buffers are device memory, k and v 16-byte and the scales 4-byte aligned.
+ *
+ * Errors that only the device sees land in the status word at `workspace`
+ * (256 bytes, zero before its first use, read with jattn_get_status): nothing
+ * outside the buffers is read or written. The status word is only written on
+ * errors, so calls that run at the same time may share it. */
+enum { JATTN_CACHE_BF16 = 0, JATTN_CACHE_MXFP8 = 1 };
+
+typedef struct {
+  int64_t n_pages; /* 1 .. 2^31 - 1 */
+  int page_size;
+  int H;           /* key/value heads */
+  int D;
+  int format;      /* JATTN_CACHE_* */
+  void* k;
+  void* v;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+} jattn_cache_t;
+
+/* Write new rows into the cache: row i of sequence b of the jagged bf16 rows
+ * k, v [total, H, D] (off: int64 [B+1] device prefix sums; NULL: one row per
+ * sequence, total == B) goes to position start[b] + i (start: int64 [B] device,
+ * the sequence's cached length before the call; negative: the sequence's rows
+ * are skipped). Rows at and behind off[B] are skipped, so a batch may be
+ * padded. With rope_cos / rope_sin (fp32 [rope_rows, D/2], 16-byte aligned; NULL
+ * for none) keys are rotated as by jattn_rope at their own position, in fp32,
+ * before the one rounding to the cache's format; a position at or beyond
+ * rope_rows sets JATTN_ERR_ROPE and its key is stored as it came. A position
+ * past max_pages * page_size sets JATTN_ERR_LENGTH, a bad table entry
+ * JATTN_ERR_PAGES; such rows are not written. Two rows of one call must not go
+ * to the same place (which of them stays is not specified). Return codes as
+ * jattn_rope. */
+int jattn_cache_append(const jattn_cache_t* cache, int64_t B, int64_t total, const int64_t* off, const int64_t* start,
+                       const int32_t* page_table, int64_t max_pages, const uint16_t* k, const uint16_t* v,
+                       const float* rope_cos, const float* rope_sin, int64_t rope_rows, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Read cached rows back as jagged bf16 rows k, v [total, H, D], for the jagged
+ * forward: row i of sequence b (off as above, not NULL) is position start[b] +
+ * i (start NULL: 0; negative: the sequence's rows are left as they were). MXFP8
+ * values are code * 2^(E - 127) rounded to bf16 (exact but for values below
+ * bf16's subnormals or above its largest). Rows at and behind off[B] are left
+ * as they were; rows of a bad page read as zeros (JATTN_ERR_PAGES). */
+int jattn_cache_read(const jattn_cache_t* cache, int64_t B, int64_t total, const int64_t* off, const int64_t* start,
+                     const int32_t* page_table, int64_t max_pages, uint16_t* k, uint16_t* v, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* Attention of a few new query rows per sequence over the cache: the jagged
+ * forward's function (activations, masks, scale, norm_by_lkv of `p`) with
+ * sequence b's keys and values its cached positions 0 .. kv_lens[b] - 1
+ * (device int64 [B], the new rows included). p->H is the number of query
+ * heads, a multiple G of cache->H; query head h reads key/value head h / G.
+ * p->D == cache->D. q [p->total_q, H, D] holds Lq(b) = q_off[b+1] - q_off[b]
+ * rows per sequence (q_off NULL: one each, total_q == B); the last of them
+ * stands at the last cached position (delta = kv_lens[b] - Lq(b)).
+ * p->total_kv is an upper bound of kv_lens (at most max_pages * page_size); a
+ * length outside [0, p->total_kv] sets JATTN_ERR_LENGTH and counts as 0.
+ * Writes o [total_q, H, D] bf16 and, for JATTN_SOFTMAX, lse [total_q, H] fp32.
+ * A row that no key is allowed for gets o = 0, lse = -inf. Rows behind
+ * q_off[B] are left as they were. Cached values at positions that a row's mask
+ * excludes never reach it, whatever they are.
+ *
+ * No gradient: this is a serving operator. It serves any Lq, but is made for
+ * few rows (Lq * G up to about 64); long prompts go through jattn_cache_read
+ * and jattn_fwd.
+ *
+ * scratch: jattn_decode_scratch_size bytes, 256-byte aligned, of any content;
+ * calls that run at the same time need one each. Results do not depend on it
+ * and are the same from call to call. */
+int jattn_decode_scratch_size(const jattn_params_t* p, const jattn_cache_t* cache, size_t* bytes);
+int jattn_decode(const jattn_params_t* p, const jattn_cache_t* cache, const int64_t* q_off, const int64_t* kv_lens,
+                 const int32_t* page_table, int64_t max_pages, const uint16_t* q, uint16_t* o, float* lse,
+                 void* scratch, size_t scratch_bytes, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Longest-first tile schedule ("GEM Training" post, GDPA section: valid tiles
  * are precomputed, empty ones skipped, and the rest spread over the SMs so
  * no SM gets a much longer share). Builds the schedule the kernels use into
@@ -340,8 +436,8 @@ int jattn_partition(int64_t B, const int64_t* q_off, const int64_t* kv_off, int 
 int64_t jattn_max_tiles(const jattn_params_t* p, int row_tile, int transposed);
 
 /* Synchronises `stream`, then reads and clears the device status word of
- * `workspace` into *device_status (JATTN_OK or JATTN_ERR_OFFSETS /
- * JATTN_ERR_TIMEOUT). Returns JATTN_ERR_CUDA if the stream reports an error. */
+ * `workspace` into *device_status (JATTN_OK or one of the codes marked
+ * "device" above). Returns JATTN_ERR_CUDA if the stream reports an error. */
 int jattn_get_status(void* workspace, void* stream, int* device_status);
 
 /* Static, human-readable name of a return / status code. */

@@ -15,6 +15,8 @@ the computation runs in its CUDA kernels):
   block of a jagged tensor; ``forward_mxfp8(qm, km, vm, q_off, kv_off, ...)``:
   the softmax forward on such operands (block-scaled FP8 tensor-core products).
 * ``schedule(...)``: the device-built longest-first tile list.
+* ``paged_cache``, ``cache_append``, ``cache_read``, ``decode``: a paged
+  key/value cache for serving and the attention of new rows over it (``paged``).
 
 Activations (``act``): "softmax", "silu", "gelu" (tanh form) or "gelu_poly"
 (its degree-6 Taylor polynomial on the FMA pipe, for |scores| <= 1).
@@ -275,10 +277,15 @@ def schedule(q_off, kv_off, H, D=128, causal=False, window=0, row_tile=128, col_
 
 
 def device_status(device=None) -> int:
-    """Read and clear the device status word of the cached workspace (syncs)."""
+    """Read and clear the device's status words: the cached workspace's and, if
+    that is clean, the paged-cache operators' (syncs)."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     key = dev.index if dev.index is not None else torch.cuda.current_device()
-    ws = _ws_cache.get(key)
-    if ws is None:
-        return 0
-    return B.get_status(ws.data_ptr(), _stream(dev))
+    code = 0
+    for block in (_ws_cache.get(key), _status_blocks.get(key)):
+        if block is not None and code == 0:
+            code = B.get_status(block.data_ptr(), _stream(dev))
+    return code
+
+
+from .paged import PagedCache, _status_blocks, cache_append, cache_read, decode, paged_cache  # noqa: E402

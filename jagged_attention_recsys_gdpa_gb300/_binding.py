@@ -27,6 +27,10 @@ EXPORTED = (
     "jattn_mxfp8_quantize",
     "jattn_fwd_mxfp8",
     "jattn_bwd_mxfp8",
+    "jattn_cache_append",
+    "jattn_cache_read",
+    "jattn_decode",
+    "jattn_decode_scratch_size",
     "jattn_schedule",
     "jattn_partition",
     "jattn_max_tiles",
@@ -50,6 +54,23 @@ class Params(ctypes.Structure):
         ("window", ctypes.c_int),
         ("scale", ctypes.c_float),
         ("norm_by_lkv", ctypes.c_int),
+    ]
+
+
+CACHE_BF16, CACHE_MXFP8 = 0, 1
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [
+        ("n_pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int),
+        ("H", ctypes.c_int),
+        ("D", ctypes.c_int),
+        ("format", ctypes.c_int),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
     ]
 
 
@@ -105,6 +126,15 @@ def load(path: str | None = None):
     lib.jattn_bwd_mxfp8.restype = i32
     lib.jattn_bwd_rope_workspace_size.argtypes = [P, i64, ctypes.POINTER(ctypes.c_size_t)]
     lib.jattn_bwd_rope_workspace_size.restype = i32
+    C = ctypes.POINTER(Cache)
+    lib.jattn_cache_append.argtypes = [C, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, i64, vp, ctypes.c_size_t, vp]
+    lib.jattn_cache_append.restype = i32
+    lib.jattn_cache_read.argtypes = [C, i64, i64, vp, vp, vp, i64, vp, vp, vp, ctypes.c_size_t, vp]
+    lib.jattn_cache_read.restype = i32
+    lib.jattn_decode_scratch_size.argtypes = [P, C, ctypes.POINTER(ctypes.c_size_t)]
+    lib.jattn_decode_scratch_size.restype = i32
+    lib.jattn_decode.argtypes = [P, C, vp, vp, vp, i64, vp, vp, vp, vp, ctypes.c_size_t, vp, ctypes.c_size_t, vp]
+    lib.jattn_decode.restype = i32
     lib.jattn_schedule.argtypes = [P, vp, vp, i32, i32, i32, vp, i64, vp, vp, ctypes.c_size_t, vp]
     lib.jattn_schedule.restype = i32
     lib.jattn_partition.argtypes = [i64, vp, vp, i32, i32, i32, vp, vp]
@@ -211,6 +241,35 @@ def rope(p: Params, q_off, kv_off, keys: bool, inverse: bool, x, y, rope_cos, ro
     check(load().jattn_rope(ctypes.byref(p), ptr(q_off), ptr(kv_off), int(bool(keys)), int(bool(inverse)), ptr(x),
                             ptr(y), ptr(rope_cos), ptr(rope_sin), int(rope_cos.shape[0]), ws, ws_bytes, stream),
           "jattn_rope")
+
+
+def cache(n_pages, page_size, H, D, fmt, k, v, k_scales, v_scales) -> Cache:
+    return Cache(int(n_pages), int(page_size), int(H), int(D), int(fmt), ptr(k), ptr(v), ptr(k_scales), ptr(v_scales))
+
+
+def cache_append(c: Cache, B: int, total: int, off, start, page_table, k, v, cos, sin, ws, ws_bytes: int, stream: int):
+    check(load().jattn_cache_append(ctypes.byref(c), B, total, ptr(off), ptr(start), ptr(page_table),
+                                    page_table.shape[1], ptr(k), ptr(v), ptr(cos), ptr(sin),
+                                    0 if cos is None else cos.shape[0], ws, ws_bytes, stream), "jattn_cache_append")
+
+
+def cache_read(c: Cache, B: int, total: int, off, start, page_table, k, v, ws, ws_bytes: int, stream: int):
+    check(load().jattn_cache_read(ctypes.byref(c), B, total, ptr(off), ptr(start), ptr(page_table),
+                                  page_table.shape[1], ptr(k), ptr(v), ws, ws_bytes, stream), "jattn_cache_read")
+
+
+def decode_scratch_size(p: Params, c: Cache) -> int:
+    n = ctypes.c_size_t(0)
+    check(load().jattn_decode_scratch_size(ctypes.byref(p), ctypes.byref(c), ctypes.byref(n)),
+          "jattn_decode_scratch_size")
+    return int(n.value)
+
+
+def decode(p: Params, c: Cache, q_off, kv_lens, page_table, q, o, lse, scratch, scratch_bytes: int, ws,
+           ws_bytes: int, stream: int):
+    check(load().jattn_decode(ctypes.byref(p), ctypes.byref(c), ptr(q_off), ptr(kv_lens), ptr(page_table),
+                              page_table.shape[1], ptr(q), ptr(o), ptr(lse), scratch, scratch_bytes, ws, ws_bytes,
+                              stream), "jattn_decode")
 
 
 def schedule(p: Params, q_off, kv_off, row_tile, col_tile, transposed, tiles, max_tiles, n_tiles, ws, ws_bytes,

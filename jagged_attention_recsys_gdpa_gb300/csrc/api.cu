@@ -12,6 +12,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/jattn.h"
+#include "cache.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "sched.h"
@@ -867,6 +868,158 @@ int jattn_rope(const jattn_params_t* p, const int64_t* q_off, const int64_t* kv_
   return e == cudaSuccess ? JATTN_OK : cuda_fail("rotary kernel launch", e);
 }
 
+namespace jattn {
+namespace {
+
+bool aligned4(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; }
+
+int check_cache(const jattn_cache_t* c) {
+  if (!c) return JATTN_ERR_INVALID;
+  if (c->n_pages < 1 || c->n_pages > INT32_MAX || c->H < 1 || (c->D != 64 && c->D != 128)) return JATTN_ERR_INVALID;
+  if (c->page_size < 8 || c->page_size > 4096 || (c->page_size & (c->page_size - 1))) return JATTN_ERR_INVALID;
+  if (c->format != JATTN_CACHE_BF16 && c->format != JATTN_CACHE_MXFP8) return JATTN_ERR_INVALID;
+  if (static_cast<int64_t>(c->H) * c->D * 2 >= (int64_t(1) << 31)) return JATTN_ERR_INVALID;
+  if (!c->k || !c->v) return JATTN_ERR_INVALID;
+  if ((c->format == JATTN_CACHE_MXFP8) != (c->k_scales && c->v_scales)) return JATTN_ERR_INVALID;
+  if (c->format == JATTN_CACHE_BF16 && (c->k_scales || c->v_scales)) return JATTN_ERR_INVALID;
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scales) || !aligned4(c->v_scales))
+    return JATTN_ERR_ALIGN;
+  return JATTN_OK;
+}
+
+// Sequences and page tables: positions of a sequence stay below 2^31.
+int check_pages(const jattn_cache_t* c, int64_t B, const int32_t* page_table, int64_t max_pages) {
+  if (B < 1 || B > INT32_MAX || !page_table || max_pages < 1 || max_pages > INT32_MAX / c->page_size)
+    return JATTN_ERR_INVALID;
+  return JATTN_OK;
+}
+
+int check_status_ws(const void* ws, size_t ws_bytes) {
+  return !ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < 256 ? JATTN_ERR_WORKSPACE : JATTN_OK;
+}
+
+// Total rows of a copy: its 16-byte pieces are numbered by the blocks of a
+// one-dimensional grid of 256 threads.
+bool too_many_rows(const jattn_cache_t* c, int64_t total) {
+  return total > INT32_MAX || total * c->H * (c->D / 8) > (int64_t(INT32_MAX) - 1) * 256;
+}
+
+CacheView cache_view(const jattn_cache_t* c, const int32_t* page_table, int64_t max_pages) {
+  CacheView v{};
+  v.k = c->k;
+  v.v = c->v;
+  v.ks = c->k_scales;
+  v.vs = c->v_scales;
+  v.n_pages = c->n_pages;
+  v.H = c->H;
+  while ((1 << v.page_shift) < c->page_size) ++v.page_shift;
+  v.page_mask = c->page_size - 1;
+  v.table = page_table;
+  v.max_pages = max_pages;
+  return v;
+}
+
+int check_decode(const jattn_params_t* p, const jattn_cache_t* c) {
+  int rc = check_params(p);
+  if (rc != JATTN_OK) return rc;
+  if ((rc = check_cache(c)) != JATTN_OK) return rc;
+  if (p->D != c->D || p->H % c->H) return JATTN_ERR_INVALID;
+  return JATTN_OK;
+}
+
+}  // namespace
+}  // namespace jattn
+
+int jattn_cache_append(const jattn_cache_t* c, int64_t B, int64_t total, const int64_t* off, const int64_t* start,
+                       const int32_t* page_table, int64_t max_pages, const uint16_t* k, const uint16_t* v,
+                       const float* rope_cos, const float* rope_sin, int64_t rope_rows, void* ws, size_t ws_bytes,
+                       void* stream) {
+  int rc = check_cache(c);
+  if (rc != JATTN_OK) return rc;
+  if ((rc = check_pages(c, B, page_table, max_pages)) != JATTN_OK) return rc;
+  if (!start || total < 0 || too_many_rows(c, total) || (!off && total != B)) return JATTN_ERR_INVALID;
+  if (total > 0 && (!k || !v)) return JATTN_ERR_INVALID;
+  if ((rope_cos || rope_sin) && (rc = check_rope(rope_cos, rope_sin, rope_rows)) != JATTN_OK) return rc;
+  if (!aligned16(k) || !aligned16(v)) return JATTN_ERR_ALIGN;
+  if ((rc = check_status_ws(ws, ws_bytes)) != JATTN_OK) return rc;
+  DeviceInfo dev;
+  if ((rc = device_info(dev)) != JATTN_OK) return rc;
+  clear_stale_error();
+  if (total == 0) return JATTN_OK;
+  const cudaError_t e = launch_cache_append(
+      cache_view(c, page_table, max_pages), c->format == JATTN_CACHE_MXFP8, B, total, off, start, k, v, c->D, rope_cos,
+      rope_sin, rope_cos ? static_cast<int>(rope_rows) : 0, static_cast<DevStatus*>(ws),
+      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? JATTN_OK : cuda_fail("cache append launch", e);
+}
+
+int jattn_cache_read(const jattn_cache_t* c, int64_t B, int64_t total, const int64_t* off, const int64_t* start,
+                     const int32_t* page_table, int64_t max_pages, uint16_t* k, uint16_t* v, void* ws,
+                     size_t ws_bytes, void* stream) {
+  int rc = check_cache(c);
+  if (rc != JATTN_OK) return rc;
+  if ((rc = check_pages(c, B, page_table, max_pages)) != JATTN_OK) return rc;
+  if (!off || total < 0 || too_many_rows(c, total) || (total > 0 && (!k || !v))) return JATTN_ERR_INVALID;
+  if (!aligned16(k) || !aligned16(v)) return JATTN_ERR_ALIGN;
+  if ((rc = check_status_ws(ws, ws_bytes)) != JATTN_OK) return rc;
+  DeviceInfo dev;
+  if ((rc = device_info(dev)) != JATTN_OK) return rc;
+  clear_stale_error();
+  if (total == 0) return JATTN_OK;
+  const cudaError_t e = launch_cache_read(cache_view(c, page_table, max_pages), c->format == JATTN_CACHE_MXFP8, B,
+                                          total, off, start, k, v, c->D, static_cast<DevStatus*>(ws),
+                                          static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? JATTN_OK : cuda_fail("cache read launch", e);
+}
+
+int jattn_decode_scratch_size(const jattn_params_t* p, const jattn_cache_t* c, size_t* bytes) {
+  if (!bytes) return JATTN_ERR_INVALID;
+  const int rc = check_decode(p, c);
+  if (rc != JATTN_OK) return rc;
+  *bytes = 256;
+  return JATTN_OK;
+}
+
+int jattn_decode(const jattn_params_t* p, const jattn_cache_t* c, const int64_t* q_off, const int64_t* kv_lens,
+                 const int32_t* page_table, int64_t max_pages, const uint16_t* q, uint16_t* o, float* lse,
+                 void* scratch, size_t scratch_bytes, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_decode(p, c);
+  if (rc != JATTN_OK) return rc;
+  if ((rc = check_pages(c, p->B, page_table, max_pages)) != JATTN_OK) return rc;
+  if (!kv_lens || p->total_kv > max_pages * c->page_size || (!q_off && p->total_q != p->B)) return JATTN_ERR_INVALID;
+  if (p->total_q > 0 && (!q || !o || (p->act == JATTN_SOFTMAX && !lse))) return JATTN_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(o)) return JATTN_ERR_ALIGN;
+  if ((rc = check_status_ws(ws, ws_bytes)) != JATTN_OK) return rc;
+  size_t need = 0;
+  if ((rc = jattn_decode_scratch_size(p, c, &need)) != JATTN_OK) return rc;
+  if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) || scratch_bytes < need) return JATTN_ERR_WORKSPACE;
+  DeviceInfo dev;
+  if ((rc = device_info(dev)) != JATTN_OK) return rc;
+  clear_stale_error();
+  if (p->total_q == 0) return JATTN_OK;
+  DecodeArgs a{};
+  a.cache = cache_view(c, page_table, max_pages);
+  a.q_off = q_off;
+  a.kv_lens = kv_lens;
+  a.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  a.o = reinterpret_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  a.B = p->B;
+  a.total_q = p->total_q;
+  a.max_kv = p->total_kv;
+  a.Hq = p->H;
+  a.G = p->H / c->H;
+  a.act = p->act;
+  a.mask = p->mask;
+  a.window = (p->mask & (JATTN_MASK_WINDOW | JATTN_MASK_BLOCK)) ? p->window : 0;
+  a.norm_by_lkv = p->norm_by_lkv;
+  a.scale = p->scale > 0.0f ? p->scale : 1.0f / std::sqrt(static_cast<float>(p->D));
+  a.scale_log2 = a.scale * 1.4426950408889634f;
+  a.status = static_cast<DevStatus*>(ws);
+  const cudaError_t e = launch_decode(p->D, c->format == JATTN_CACHE_MXFP8, a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? JATTN_OK : cuda_fail("decode kernel launch", e);
+}
+
 int jattn_schedule(const jattn_params_t* p, const int64_t* q_off, const int64_t* kv_off, int row_tile,
                    int col_tile, int transposed, int32_t* tiles, int64_t max_tiles, int32_t* n_tiles, void* ws,
                    size_t ws_bytes, void* stream) {
@@ -917,6 +1070,8 @@ const char* jattn_error_string(int code) {
     case JATTN_ERR_UNSUPPORTED: return "device is not sm_103";
     case JATTN_ERR_TOO_LARGE: return "problem needs more scratch than the allocation-free entry point holds";
     case JATTN_ERR_ROPE: return "a rotary position lies at or beyond the cos/sin tables' rows";
+    case JATTN_ERR_PAGES: return "a page table entry is no page of the cache";
+    case JATTN_ERR_LENGTH: return "a cached length or position lies outside its sequence's pages";
     default: return "unknown error code";
   }
 }

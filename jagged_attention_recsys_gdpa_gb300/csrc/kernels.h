@@ -3,11 +3,14 @@
 #include <cstdint>
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace jattn {
 
 struct AttnArgs;
+struct CacheView;
+struct DecodeArgs;
 struct DevStatus;
 
 // Forward: schedule rows are blocks of fwd_rows_per_item() query rows. `split`
@@ -107,5 +110,14 @@ cudaError_t launch_mx_quant(const int64_t* off, int B, int H, int D, int64_t max
 // Row-major [rows, half] cos / sin tables to pair-major [half, rows] copies.
 cudaError_t launch_rope_transpose(const float* cos_t, const float* sin_t, int rows, int half, float* cos_pm,
                                   float* sin_pm, cudaStream_t stream);
+
+// Paged cache (cache.cu): jagged bf16 rows into and out of the pages.
+cudaError_t launch_cache_append(const CacheView& c, bool mx, int64_t B, int64_t total, const int64_t* off,
+                                const int64_t* start, const void* k, const void* v, int D, const float* cos_t,
+                                const float* sin_t, int rope_rows, DevStatus* status, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheView& c, bool mx, int64_t B, int64_t total, const int64_t* off,
+                              const int64_t* start, void* k, void* v, int D, DevStatus* status, cudaStream_t stream);
+// Attention over the paged cache (decode.cu).
+cudaError_t launch_decode(int D, bool mx, const DecodeArgs& a, cudaStream_t stream);
 
 }  // namespace jattn
