@@ -384,7 +384,8 @@ int jattn_cache_read(const jattn_cache_t* cache, int64_t B, int64_t total, const
  * stands at the last cached position (delta = kv_lens[b] - Lq(b)).
  * p->total_kv is an upper bound of kv_lens (at most max_pages * page_size); a
  * length outside [0, p->total_kv] sets JATTN_ERR_LENGTH and counts as 0.
- * Writes o [total_q, H, D] bf16 and, for JATTN_SOFTMAX, lse [total_q, H] fp32.
+ * Writes o [total_q, H, D] bf16 (which must not overlap q) and, for
+ * JATTN_SOFTMAX, lse [total_q, H] fp32. Rows of a bad page count as zeros.
  * A row that no key is allowed for gets o = 0, lse = -inf. Rows behind
  * q_off[B] are left as they were. Cached values at positions that a row's mask
  * excludes never reach it, whatever they are.

@@ -924,6 +924,8 @@ int check_decode(const jattn_params_t* p, const jattn_cache_t* c) {
   if (rc != JATTN_OK) return rc;
   if ((rc = check_cache(c)) != JATTN_OK) return rc;
   if (p->D != c->D || p->H % c->H) return JATTN_ERR_INVALID;
+  // positions, windows and their sums stay within 32 bits
+  if (p->total_q > (int64_t(1) << 30) || p->total_kv > (int64_t(1) << 30)) return JATTN_ERR_INVALID;
   return JATTN_OK;
 }
 
@@ -976,7 +978,8 @@ int jattn_decode_scratch_size(const jattn_params_t* p, const jattn_cache_t* c, s
   if (!bytes) return JATTN_ERR_INVALID;
   const int rc = check_decode(p, c);
   if (rc != JATTN_OK) return rc;
-  *bytes = 256;
+  *bytes = al256(decode_scratch_bytes(p->D, c->format == JATTN_CACHE_MXFP8, p->B, p->total_q, p->total_kv, p->H / c->H,
+                                      c->H));
   return JATTN_OK;
 }
 
@@ -987,7 +990,7 @@ int jattn_decode(const jattn_params_t* p, const jattn_cache_t* c, const int64_t*
   if (rc != JATTN_OK) return rc;
   if ((rc = check_pages(c, p->B, page_table, max_pages)) != JATTN_OK) return rc;
   if (!kv_lens || p->total_kv > max_pages * c->page_size || (!q_off && p->total_q != p->B)) return JATTN_ERR_INVALID;
-  if (p->total_q > 0 && (!q || !o || (p->act == JATTN_SOFTMAX && !lse))) return JATTN_ERR_INVALID;
+  if (p->total_q > 0 && (!q || !o || q == o || (p->act == JATTN_SOFTMAX && !lse))) return JATTN_ERR_INVALID;
   if (!aligned16(q) || !aligned16(o)) return JATTN_ERR_ALIGN;
   if ((rc = check_status_ws(ws, ws_bytes)) != JATTN_OK) return rc;
   size_t need = 0;
@@ -1011,12 +1014,13 @@ int jattn_decode(const jattn_params_t* p, const jattn_cache_t* c, const int64_t*
   a.G = p->H / c->H;
   a.act = p->act;
   a.mask = p->mask;
-  a.window = (p->mask & (JATTN_MASK_WINDOW | JATTN_MASK_BLOCK)) ? p->window : 0;
+  a.window = (p->mask & (JATTN_MASK_WINDOW | JATTN_MASK_BLOCK)) ? std::min(p->window, 1 << 30) : 0;
   a.norm_by_lkv = p->norm_by_lkv;
   a.scale = p->scale > 0.0f ? p->scale : 1.0f / std::sqrt(static_cast<float>(p->D));
   a.scale_log2 = a.scale * 1.4426950408889634f;
   a.status = static_cast<DevStatus*>(ws);
-  const cudaError_t e = launch_decode(p->D, c->format == JATTN_CACHE_MXFP8, a, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_decode(p->D, c->format == JATTN_CACHE_MXFP8, a, scratch,
+                                      static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? JATTN_OK : cuda_fail("decode kernel launch", e);
 }
 

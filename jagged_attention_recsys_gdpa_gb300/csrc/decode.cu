@@ -1,10 +1,28 @@
 // Attention of a few new query rows per sequence over the paged cache.
 //
-// For query row i of sequence b (position kv_len - Lq + i), head h of group
-// h / G: s_j = scale <q, k_j>, o = sum_j w(s_j) v_j over the allowed cached
-// positions j, w the softmax (kept as a running maximum m, sum l and
-// accumulator) or a pointwise activation. One warp per query row and head,
-// lanes over the head dimension.
+// For query row i of sequence b (position kv_len - Lq + i) and query head h of
+// key/value head h / G:  s_j = scale <q, k_j>,  o = sum_j w(s_j) v_j  over the
+// allowed cached positions j. Softmax keeps a running maximum m, sum l and
+// accumulator O per row (exponents in base 2); pointwise activations only O.
+//
+// Bound. Every cached row is read once and meets the Lq * G query rows of its
+// sequence and head, 4 D operations per 2 rows of 2 D bytes: for up to some 60
+// rows the cache's bytes bound the call, not the tensor cores. So the layout
+// serves the copies: each worker keeps its own ring of stages in shared
+// memory, filled with 16-byte asynchronous copies straight from the pages
+// (any page size, rows past a sequence's keys filled with zeros), and the
+// products are warp-level MMAs whose 16 rows hold the query rows; a 128-row
+// tcgen05 tile would be mostly padding here and would need operands and
+// accumulators staged through TMEM for nothing.
+//
+// Split. A unit is one (sequence, tile of 16 WM query rows, key/value head);
+// its keys go in steps of a fixed number of positions. All units' steps are
+// numbered through, and every worker (WM warps) takes one contiguous run of
+// equal length, wherever it begins and ends: long histories are split, short
+// ones share a worker, and no worker has more than any other. A unit that lies
+// within one run is finished there; of any other, each run writes its piece
+// (m, l, O in fp32) to scratch, and a second kernel joins the pieces in their
+// order. Results do not depend on what runs when.
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -15,6 +33,18 @@
 namespace jattn {
 namespace {
 
+constexpr int kWarps = 4;     // per CTA
+constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 3;    // steps held per worker
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxCtas = 152 * kCtasPerSm;
+constexpr int kMinSteps = 2;  // per worker, as long as there are few steps in all
+constexpr int kJoinThreads = 256;
+constexpr float kLn2 = 0.6931471805599453f;
+// The running maximum moves when a row's scores exceed it by more than 2^kSlack,
+// so that most steps rescale nothing; weights then reach 2^kSlack at most.
+constexpr float kSlack = 8.0f;
+
 __device__ __forceinline__ float activate(float s, int act) {
   if (act == JATTN_GELU_POLY) return gelu_poly(s);
   // silu(s) = s / (1 + e^-s); s/2 (1 + tanh u) = s / (1 + e^-2u)
@@ -22,96 +52,827 @@ __device__ __forceinline__ float activate(float s, int act) {
   return __fdividef(s, 1.0f + __expf(-u));
 }
 
-template <int D, bool MX>
-__global__ void __launch_bounds__(128) decode_kernel(DecodeArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (a.q_off != nullptr)
-    check_offsets(a.q_off, a.B, a.total_q, w * 32 + lane, static_cast<int64_t>(gridDim.x) * 128, a.status);
-  const int64_t r = w / a.Hq;
-  const int h = static_cast<int>(w % a.Hq);
-  if (r >= a.total_q) return;
-  int64_t b = r, i = 0, lq = 1;
+// ---------------------------------------------------------------- plan
+// One sequence's share of the work: its query rows in tiles of `tile` rows, and
+// the steps of `step` keys that cover the keys its rows may see.
+struct Seq {
+  int64_t q0;   // first query row
+  int lq, n;    // query rows, cached rows
+  int lo, hi;   // keys that any of its rows may see
+  int k0;       // first step's first key
+  int steps;    // at least 1: a unit without keys still writes its rows
+  uint32_t units;
+};
+
+__device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b, int tile, int step) {
+  Seq s;
+  s.q0 = b;
+  s.lq = 1;
   if (a.q_off != nullptr) {
-    if (r >= a.q_off[a.B]) return;
-    int64_t lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi + 1) >> 1;
-      if (a.q_off[mid] <= r) lo = mid;
-      else hi = mid - 1;
+    s.q0 = __ldg(a.q_off + b);
+    const int64_t end = __ldg(a.q_off + b + 1);
+    // rows outside the tensor or offsets that decrease: the sequence has no rows
+    s.lq = s.q0 >= 0 && end >= s.q0 && end <= a.total_q ? static_cast<int>(end - s.q0) : 0;
+  }
+  const int64_t n = __ldg(a.kv_lens + b);
+  s.n = n >= 0 && n <= a.max_kv ? static_cast<int>(n) : 0;
+  int unused;
+  key_interval(0, s.n - s.lq, s.n, a.mask, a.window, s.lo, unused);
+  key_interval(s.lq - 1, s.n - s.lq, s.n, a.mask, a.window, unused, s.hi);
+  s.lo = min(s.lo, s.n);
+  s.hi = max(s.hi, s.lo);
+  s.k0 = s.lo / step * step;
+  s.steps = max(1, (s.hi - s.k0 + step - 1) / step);
+  const int64_t rows = static_cast<int64_t>(s.lq) * a.G;
+  s.units = static_cast<uint32_t>((rows + tile - 1) / tile) * a.cache.H;
+  return s;
+}
+
+// A worker's place in the numbering of all steps.
+struct Place {
+  Seq s;
+  int b;
+  uint32_t u;  // unit within the sequence: tile * H + head
+  int t;       // step within the unit
+};
+
+__device__ __forceinline__ void advance(Place& p, const DecodeArgs& a, int tile, int step) {
+  if (++p.t < p.s.steps) return;
+  p.t = 0;
+  if (++p.u < p.s.units) return;
+  p.u = 0;
+  do {
+    if (++p.b >= a.B) return;  // behind the last step: never used
+    p.s = seq_of(a, p.b, tile, step);
+  } while (p.s.units == 0);
+}
+
+__device__ __forceinline__ int64_t warp_inclusive(int64_t x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// The number of all steps, and the place of step `first`. Every warp of the
+// CTA calls it; each thread sums the steps of one stretch of sequences.
+__device__ __forceinline__ int64_t total_steps(const DecodeArgs& a, int tile, int step, int64_t* start /* [kThreads + 1] */) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t c = (a.B + kThreads - 1) / kThreads;
+  int64_t sum = 0;
+  for (int64_t b = tid * c; b < min(a.B, (tid + 1) * c); ++b) {
+    const Seq s = seq_of(a, static_cast<int>(b), tile, step);
+    sum += static_cast<int64_t>(s.units) * s.steps;
+    if (blockIdx.x == 0) {  // the one check of what the host cannot see
+      const int64_t n = a.kv_lens[b];
+      if (n < 0 || n > a.max_kv) record_error(a.status, JATTN_ERR_LENGTH, 85, static_cast<int>(b));
+      if (a.q_off != nullptr) check_offsets(a.q_off, b + 1, a.total_q, b, a.B, a.status);
     }
-    b = lo;
-    i = r - a.q_off[lo];
-    lq = a.q_off[lo + 1] - a.q_off[lo];
-    if (i < 0 || i >= lq) return;
   }
-  int64_t n = a.kv_lens[b];
-  if (n < 0 || n > a.max_kv) {
-    record_error(a.status, JATTN_ERR_LENGTH, 85, static_cast<int>(b));
-    n = 0;
-  }
-  int lo, hi;
-  key_interval(static_cast<int>(i), static_cast<int>(n - lq), static_cast<int>(n), a.mask, a.window, lo, hi);
-  constexpr int E = D / 32;
-  float q[E], acc[E];
-  const int64_t qrow = (r * a.Hq + h) * D;
+  const int64_t inc = warp_inclusive(sum, lane);
+  __shared__ int64_t warp_sum[kWarps];
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int64_t before = 0, all = 0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = __bfloat162float(a.q[qrow + lane * E + e]);
-    acc[e] = 0.0f;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += warp_sum[w];
+    all += warp_sum[w];
   }
-  float m = -INFINITY, l = 0.0f;
-  for (int j = lo; j < hi; ++j) {
-    int64_t row = cache_row(a.cache, b, j, a.status);
+  start[tid] = before + inc - sum;
+  __syncthreads();
+  return all;
+}
+
+__device__ __forceinline__ Place find_place(const DecodeArgs& a, int tile, int step, const int64_t* start, int64_t first) {
+  const int lane = threadIdx.x & 31;
+  const int64_t c = (a.B + kThreads - 1) / kThreads;
+  int before = 0;  // stretches that begin at or before `first`
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) before += __popc(__ballot_sync(0xffffffffu, start[i * 32 + lane] <= first));
+  int64_t at = start[before - 1];  // the last of them holds it: those behind begin later
+  Place p;
+  for (int64_t b = (before - 1) * c;; b += 32) {
+    const int64_t mine = b + lane;
+    int64_t steps = 0;
+    if (mine < a.B) {
+      const Seq s = seq_of(a, static_cast<int>(mine), tile, step);
+      steps = static_cast<int64_t>(s.units) * s.steps;
+    }
+    const int64_t end = at + warp_inclusive(steps, lane);
+    const uint32_t over = __ballot_sync(0xffffffffu, end > first);
+    if (over != 0) {
+      const int i = __ffs(over) - 1;
+      at = __shfl_sync(0xffffffffu, end - steps, i);
+      p.b = static_cast<int>(b + i);
+      break;
+    }
+    at = __shfl_sync(0xffffffffu, end, 31);
+    if (b + 32 >= a.B) {  // cannot be: `first` is below the total
+      p.b = static_cast<int>(a.B - 1);
+      at = first;
+      break;
+    }
+  }
+  p.s = seq_of(a, p.b, tile, step);
+  p.u = static_cast<uint32_t>((first - at) / p.s.steps);
+  p.t = static_cast<int>((first - at) % p.s.steps);
+  return p;
+}
+
+// ---------------------------------------------------------------- layout
+template <int D, bool MX>
+struct Layout {
+  static constexpr int row = D * (MX ? 1 : 2);           // bytes of a K or V row
+  static constexpr int chunks = row / 16;
+  static constexpr int sub = !MX && D == 128 ? 16 : 32;  // keys per product block
+  static constexpr int keys = 4096 / row;                // keys of a step, per warp: 4 KB of K, 4 KB of V
+  static constexpr int scale = MX ? D / 32 : 0;          // scale bytes per row
+  static constexpr int stage = 8192 + 2 * keys * scale;  // bytes of a stage, per warp
+  static_assert(keys % sub == 0, "a step holds whole product blocks");
+};
+
+// Byte offset of 16-byte piece `chunk` of row r: pieces are permuted so that the
+// eight rows of an 8x8 matrix load lie in different banks.
+template <int D, bool MX>
+__device__ __forceinline__ uint32_t piece_at(int r, int chunk) {
+  using L = Layout<D, MX>;
+  const int x = L::chunks >= 8 ? r & 7 : (r >> 1) & 3;
+  return static_cast<uint32_t>(r * L::row + ((chunk ^ x) << 4));
+}
+
+// ---------------------------------------------------------------- E4M3 to bf16
+// The four codes of a word as two bf16 pairs (bytes 0 and 2, bytes 1 and 3): the
+// code's exponent and mantissa bits go to the low exponent and high mantissa
+// bits, which makes a bf16 of 2^-120 times the value, subnormals included. The
+// scale's factor 2^(e - 127 + 120) makes up for it in one exact product.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u); }
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r =
+      __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// bf16 factors 2^(e - 7) of two exponents (bytes 0 and 2 of x). bf16 ends at
+// 2^127, so exponents above kMaxE (values above 2^16) are cut there and the rest
+// follows as a second factor: only product blocks that hold one pay for it.
+constexpr uint32_t kMaxE = 134;
+__device__ __forceinline__ uint32_t factor2(uint32_t x) { return (__vminu2(x, kMaxE * 0x10001u) + 0x00780078u) << 7; }
+__device__ __forceinline__ uint32_t rest1(uint32_t e) {
+  return e == 255u ? 0x7fc0u : e > kMaxE ? (e - kMaxE + 127u) << 7 : 0x3f80u;
+}
+__device__ __forceinline__ uint32_t rest2(uint32_t x) { return rest1(x & 0xffu) | (rest1(x >> 16) << 16); }
+__device__ __forceinline__ bool any_large(uint32_t w) { return __vcmpgtu4(w, kMaxE * 0x01010101u) != 0; }
+// Byte j of w twice, and byte j of w0 and w1, in bytes 0 and 2.
+__device__ __forceinline__ uint32_t same_byte(uint32_t w, int j) { return __byte_perm(w, 0u, 0x4040u + 0x0101u * j); }
+__device__ __forceinline__ uint32_t byte_pair(uint32_t w0, uint32_t w1, int j) {
+  return __byte_perm(w0, w1, 0x4400u + 0x1111u * j) & 0x00ff00ffu;
+}
+
+// ---------------------------------------------------------------- kernel
+// The exponents of a row in the bytes of a word (D = 64: two, in the low half).
+template <int D>
+__device__ __forceinline__ uint32_t scale_word(uint32_t scales, int r) {
+  uint32_t w;
+  if constexpr (D == 128) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(scales + r * 4) : "memory");
+  } else {
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(scales + r * 2) : "memory");
+    w = x;
+  }
+  return w;
+}
+
+// What the accumulator is multiplied by at the end.
+__device__ __forceinline__ float out_factor(const DecodeArgs& a, float l, int n) {
+  if (a.act == JATTN_SOFTMAX) return l == 0.0f ? 0.0f : 1.0f / l;
+  return a.norm_by_lkv ? (n > 0 ? 1.0f / static_cast<float>(n) : 0.0f) : 1.0f;
+}
+
+// Two (bf16: neighbouring; codes: four neighbouring, in the order 0 2 1 3)
+// columns of a cached row, as the threads hold them.
+template <bool MX>
+__device__ __forceinline__ void columns(const void* buf, const uint8_t* scales, int64_t row, int D, int j, int c,
+                                        float (&x)[4]) {
+  if constexpr (!MX) {
+    const uint32_t* p = static_cast<const uint32_t*>(buf) + (row * D >> 1) + j * 4;  // columns 8 j ...: two tiles
+    const uint32_t w0 = __ldg(p + c), w1 = __ldg(p + 4 + c);
+    x[0] = __uint_as_float(w0 << 16);
+    x[1] = __uint_as_float(w0 & 0xffff0000u);
+    x[2] = __uint_as_float(w1 << 16);
+    x[3] = __uint_as_float(w1 & 0xffff0000u);
+  } else {
+    const uint32_t w = __ldg(static_cast<const uint32_t*>(buf) + (row * D >> 2) + j * 2 + c);  // piece j / 2
+    const float s = e8m0_value(__ldg(scales + row * (D / 32) + j / 4));
+    const float2 a = e4m3x2_value(w & 0xffffu), b = e4m3x2_value(w >> 16);
+    x[0] = a.x * s;
+    x[1] = b.x * s;
+    x[2] = a.y * s;
+    x[3] = b.y * s;
+  }
+}
+
+// Products of a zero weight and an infinite or NaN value are NaN, and so are
+// sums over two parts of a weight: where a value that is not finite lies among a
+// piece's keys, the products above give NaN in its column for every row, also
+// for rows whose mask excludes it. Accumulators that are not finite (`bad`, one
+// bit each) are summed again one key at a time, over the allowed keys alone.
+template <int D, bool MX>
+__device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int h, int64_t row_base, int n_steps,
+                                       int step, const uint32_t (&q)[D / 16][4], float (&o)[D / 8][4], float m0,
+                                       float m1, int lo0, int hi0, int lo1, int hi1) {
+  float x = 0.0f;  // stays 0 unless something is not finite
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j) x += (o[j][0] - o[j][0]) + (o[j][1] - o[j][1]) + (o[j][2] - o[j][2]) + (o[j][3] - o[j][3]);
+  if (!__any_sync(0xffffffffu, x != 0.0f)) return;
+  const int c = threadIdx.x & 3;
+  uint64_t bad = 0;
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (o[j][e] - o[j][e] == 0.0f) continue;
+      bad |= uint64_t(1) << (4 * j + e);
+      o[j][e] = 0.0f;
+    }
+  }
+  const float u0 = m0 == -INFINITY ? 0.0f : m0, u1 = m1 == -INFINITY ? 0.0f : m1;
+  const int first = max(at.s.k0 + (at.t - n_steps + 1) * step, at.s.lo), end = min(at.s.k0 + (at.t + 1) * step, at.s.hi);
+  for (int pos = first; pos < end; ++pos) {
+    int64_t row = cache_row(a.cache, at.b, pos, a.status);
     if (row < 0) continue;
-    row += static_cast<int64_t>(h / a.G) << a.cache.page_shift;
-    float kx[E], vx[E];
+    row += static_cast<int64_t>(h) << a.cache.page_shift;
+    float s0 = 0.0f, s1 = 0.0f, k[4];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int64_t at = row * D + lane * E + e;
-      if constexpr (MX) {
-        kx[e] = e4m3x2_value(static_cast<const uint8_t*>(a.cache.k)[at]).x * e8m0_value(a.cache.ks[at / 32]);
-        vx[e] = e4m3x2_value(static_cast<const uint8_t*>(a.cache.v)[at]).x * e8m0_value(a.cache.vs[at / 32]);
-      } else {
-        kx[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.cache.k)[at]);
-        vx[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(a.cache.v)[at]);
+    for (int kk = 0; kk < D / 16; ++kk) {
+      columns<MX>(a.cache.k, a.cache.ks, row, D, 2 * kk, c, k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int sh = (e & 1) ? 0 : 16;
+        s0 = fmaf(__uint_as_float((q[kk][(e >> 1) * 2] << sh) & 0xffff0000u), k[e], s0);
+        s1 = fmaf(__uint_as_float((q[kk][(e >> 1) * 2 + 1] << sh) & 0xffff0000u), k[e], s1);
       }
     }
-    float s = 0.0f;
+    s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
+    s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
+    s0 += __shfl_xor_sync(0xffffffffu, s0, 2);
+    s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
+    const bool soft = a.act == JATTN_SOFTMAX;
+    const float p0 = soft ? ex2_approx(s0 * a.scale_log2 - u0) : activate(s0 * a.scale, a.act);
+    const float p1 = soft ? ex2_approx(s1 * a.scale_log2 - u1) : activate(s1 * a.scale, a.act);
+    const bool in0 = pos >= lo0 && pos < hi0, in1 = pos >= lo1 && pos < hi1;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], kx[e], s);
+    for (int j = 0; j < D / 8; j += 2) {
+      float v[4];
+      columns<MX>(a.cache.v, a.cache.vs, row, D, j, c, v);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    float p, corr = 1.0f;
-    if (a.act == JATTN_SOFTMAX) {
-      const float t = s * a.scale_log2, m_new = fmaxf(m, t), m_use = m_new == -INFINITY ? 0.0f : m_new;
-      corr = ex2_approx(m - m_use);
-      p = ex2_approx(t - m_use);
-      m = m_new;
-      l = fmaf(l, corr, p);
-    } else {
-      p = activate(s * a.scale, a.act);
+      for (int e = 0; e < 4; ++e) {
+        float(&t)[4] = o[j + (e >> 1)];
+        const int i = 4 * (j + (e >> 1)) + (e & 1);
+        if (in0 && (bad >> i & 1)) t[e & 1] = fmaf(p0, v[e], t[e & 1]);
+        if (in1 && (bad >> (i + 2) & 1)) t[2 + (e & 1)] = fmaf(p1, v[e], t[2 + (e & 1)]);
+      }
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], corr, p * vx[e]);
   }
-  float c = 1.0f;
-  if (a.act == JATTN_SOFTMAX) {
-    c = l == 0.0f ? 0.0f : 1.0f / l;
-    if (lane == 0) a.lse[r * a.Hq + h] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
-  } else if (a.norm_by_lkv) {
-    c = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
-  }
+}
+
+// Scratch: for each worker a piece of the unit that its run begins inside of
+// (slot 0) and of the unit that it leaves unfinished (slot 1), and what has to be
+// joined: the unit of slot 1 with the following workers' slots 0.
+struct Scratch {
+  float* acc;  // [workers][2][rows][D]
+  float2* ml;  // [workers][2][rows]: m, l
+  int4* join;  // [workers]: pieces (0: nothing to join), sequence, tile, head
+};
+
+__host__ __device__ inline size_t scratch_bytes(int workers, int rows, int D) {
+  return static_cast<size_t>(workers) * (16 + 2 * static_cast<size_t>(rows) * (8 + 4 * static_cast<size_t>(D)));
+}
+
+__host__ __device__ inline Scratch carve(void* base, int workers, int rows, int D) {
+  Scratch s;
+  s.acc = static_cast<float*>(base);
+  s.ml = reinterpret_cast<float2*>(s.acc + static_cast<size_t>(workers) * 2 * rows * D);
+  s.join = reinterpret_cast<int4*>(s.ml + static_cast<size_t>(workers) * 2 * rows);
+  return s;
+}
+
+template <int WM>
+__device__ __forceinline__ void worker_sync(int worker) {
+  if constexpr (WM == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(worker + 1), "n"(WM * 32) : "memory");
+}
+
+// Copies one step's rows (and scales) into a stage. Rows outside [lo, hi) and
+// rows of a bad page become zeros and are not looked up.
+template <int D, bool MX, int WM>
+__device__ __forceinline__ void load_step(const DecodeArgs& a, const Place& p, uint32_t stage, int tid) {
+  using L = Layout<D, MX>;
+  constexpr int step = L::keys * WM, threads = WM * 32;
+  const int h = static_cast<int>(p.u % static_cast<uint32_t>(a.cache.H));
+  const int64_t head = static_cast<int64_t>(h) << a.cache.page_shift;
+  const int pos0 = p.s.k0 + p.t * step;
+  const char* k = static_cast<const char*>(a.cache.k);
+  const char* v = static_cast<const char*>(a.cache.v);
+  const bool one_page = a.cache.page_mask + 1 >= step;  // steps and pages are both aligned powers of two
+  int64_t base = -1;
+  if (one_page && pos0 < p.s.hi && p.s.lo < p.s.hi) base = cache_row(a.cache, p.b, max(pos0, p.s.lo), a.status);
+  if (one_page && base >= 0) base += head + pos0 - max(pos0, p.s.lo);
+  constexpr int per = threads / L::chunks;  // rows per pass of the worker's threads
 #pragma unroll
-  for (int e = 0; e < E; ++e) a.o[qrow + lane * E + e] = __float2bfloat16(acc[e] * c);
+  for (int i = 0; i < step / per; ++i) {
+    const int r = i * per + tid / L::chunks, chunk = tid % L::chunks, pos = pos0 + r;
+    int64_t row = -1;
+    if (pos >= p.s.lo && pos < p.s.hi) {
+      if (one_page) {
+        row = base < 0 ? -1 : base + r;
+      } else {
+        row = cache_row(a.cache, p.b, pos, a.status);
+        if (row >= 0) row += head;
+      }
+    }
+    const int64_t at = row < 0 ? 0 : row * L::row + chunk * 16;
+    const uint32_t to = stage + piece_at<D, MX>(r, chunk);
+    cp_async16(to, k + at, row < 0 ? 0 : 16);
+    cp_async16(to + 4096 * WM, v + at, row < 0 ? 0 : 16);
+  }
+  if constexpr (MX) {
+    // one word of exponents: a row's four (D = 128), or two rows' (D = 64; both in one page). Of a pair with one row
+    // outside [lo, hi) the other row's bytes come along: masked where they are used.
+    constexpr int rows = 4 / L::scale, words = step / rows;
+#pragma unroll
+    for (int i = 0; i < (words + threads - 1) / threads; ++i) {
+      const int w = i * threads + tid, pos = pos0 + w * rows;
+      if (words % threads != 0 && w >= words) break;
+      int64_t row = -1;
+      if (pos + rows > p.s.lo && pos < p.s.hi) {
+        if (one_page) {
+          row = base < 0 ? -1 : base + w * rows;
+        } else {
+          row = cache_row(a.cache, p.b, pos, a.status);
+          if (row >= 0) row += head;
+        }
+      }
+      const int64_t at = row < 0 ? 0 : row * L::scale;
+      const uint32_t to = stage + 8192 * WM + w * 4;
+      cp_async4(to, a.cache.ks + at, row < 0 ? 0 : 4);
+      cp_async4(to + words * 4, a.cache.vs + at, row < 0 ? 0 : 4);
+    }
+  }
+}
+
+template <int D, bool MX, int WM>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(DecodeArgs a, void* scratch) {
+  using L = Layout<D, MX>;
+  constexpr int step = L::keys * WM, tile = 16 * WM, KS = D / 16, NT = L::sub / 8;
+  extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ int64_t start[kThreads];
+  const int tid = threadIdx.x % (WM * 32), lane = threadIdx.x & 31, c = lane & 3;
+  const int in_cta = threadIdx.x / (WM * 32), warp_m = tid >> 5;
+  const int workers = gridDim.x * (kWarps / WM), me = blockIdx.x * (kWarps / WM) + in_cta;
+  const Scratch sc = carve(scratch, workers, tile, D);
+
+  const int64_t total = total_steps(a, tile, step, start);
+  const int64_t share = max((total + workers - 1) / workers, static_cast<int64_t>(kMinSteps));
+  const int64_t first = me * share, last = min(first + share, total);  // this worker's run [first, last)
+  if (first >= last) {
+    if (tid == 0) sc.join[me] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  Place in = find_place(a, tile, step, start, first);  // the step that is copied next
+  Place at = in;                                       // the step that is computed next
+  int64_t to_load = last - first;
+  const uint32_t ring = smem_u32(smem) + in_cta * (kStages * L::stage * WM);
+  int load_stage = 0;
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (to_load > 0) {
+      load_step<D, MX, WM>(a, in, ring + load_stage * (L::stage * WM), tid);
+      if (--to_load > 0) advance(in, a, tile, step);
+    }
+    cp_async_commit();
+    ++load_stage;
+  }
+
+  uint32_t q[KS][4];
+  float o[D / 8][4];
+  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+  int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;        // keys that this thread's two rows may see
+  int all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;  // that every row, and that any row, of the warp's tile may see
+  bool fresh = true;
+  int64_t unit_first = 0;  // the first step of the unit at `at` that this run holds, counted within the run
+  int stage_no = 0;
+  for (int64_t done = 0; done < last - first; ++done) {
+    cp_async_wait<kStages - 2>();
+    worker_sync<WM>(in_cta);
+    if (to_load > 0) {
+      load_step<D, MX, WM>(a, in, ring + load_stage * (L::stage * WM), tid);
+      if (--to_load > 0) advance(in, a, tile, step);
+    }
+    cp_async_commit();
+    load_stage = load_stage + 1 == kStages ? 0 : load_stage + 1;
+
+    const int h = static_cast<int>(at.u % static_cast<uint32_t>(a.cache.H));
+    const int64_t rows = static_cast<int64_t>(at.s.lq) * a.G;
+    const int64_t row_base = static_cast<int64_t>(at.u / static_cast<uint32_t>(a.cache.H)) * tile + warp_m * 16;
+    const bool live = row_base < rows;  // the warp's 16 rows hold one at least
+    if (fresh) {
+      fresh = false;
+      unit_first = done;
+      m0 = m1 = -INFINITY;
+      l0 = l1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+      if (live) {
+        const int64_t r0 = row_base + (lane >> 2), r1 = r0 + 8;
+        const int delta = at.s.n - at.s.lq;
+        // rows behind the last one take its interval and zeros for their query
+        const int64_t end = rows - 1;
+        key_interval(static_cast<int>(min(r0, end) / a.G), delta, at.s.n, a.mask, a.window, lo0, hi0);
+        key_interval(static_cast<int>(min(r1, end) / a.G), delta, at.s.n, a.mask, a.window, lo1, hi1);
+        key_interval(static_cast<int>(row_base / a.G), delta, at.s.n, a.mask, a.window, any_lo, all_hi);
+        key_interval(static_cast<int>(min(row_base + 15, end) / a.G), delta, at.s.n, a.mask, a.window, all_lo, any_hi);
+        const uint32_t* q0 = nullptr;
+        const uint32_t* q1 = nullptr;
+        if (r0 < rows)
+          q0 = reinterpret_cast<const uint32_t*>(a.q + ((at.s.q0 + r0 / a.G) * a.Hq + h * a.G + r0 % a.G) * D);
+        if (r1 < rows)
+          q1 = reinterpret_cast<const uint32_t*>(a.q + ((at.s.q0 + r1 / a.G) * a.Hq + h * a.G + r1 % a.G) * D);
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) {
+          // bf16: columns 2c, 2c + 1 and 2c + 8, 2c + 9 of the 16; codes: columns 4c, 4c + 2 and 4c + 1, 4c + 3, the
+          // order in which a word of four codes becomes bf16 pairs
+          const int w0 = MX ? kk * 8 + 2 * c : kk * 8 + c, w1 = MX ? w0 + 1 : w0 + 4;
+          uint32_t x0 = q0 ? __ldg(q0 + w0) : 0u, x1 = q1 ? __ldg(q1 + w0) : 0u;
+          uint32_t y0 = q0 ? __ldg(q0 + w1) : 0u, y1 = q1 ? __ldg(q1 + w1) : 0u;
+          if constexpr (MX) {
+            const uint32_t s0 = __byte_perm(x0, y0, 0x5410), s1 = __byte_perm(x1, y1, 0x5410);
+            y0 = __byte_perm(x0, y0, 0x7632);
+            y1 = __byte_perm(x1, y1, 0x7632);
+            x0 = s0;
+            x1 = s1;
+          }
+          q[kk][0] = x0;
+          q[kk][1] = x1;
+          q[kk][2] = y0;
+          q[kk][3] = y1;
+        }
+      }
+    }
+
+    const uint32_t ks = ring + stage_no * (L::stage * WM), vs = ks + 4096 * WM;
+    const uint32_t ksc = ks + 8192 * WM, vsc = ksc + step * L::scale;
+#pragma unroll 1
+    for (int sb = 0; sb < step / L::sub; ++sb) {
+      const int r_base = sb * L::sub, pos0 = at.s.k0 + at.t * step + r_base;
+      if (!live || pos0 >= any_hi || pos0 + L::sub <= any_lo) continue;
+      const bool partial = pos0 < all_lo || pos0 + L::sub > all_hi;
+      // ---- scores
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+        const int r = r_base + nt * 8 + (lane & 7);
+        if constexpr (!MX) {
+#pragma unroll
+          for (int kk = 0; kk < KS; kk += 2) {
+            uint32_t x[4];
+            ldmatrix4(x, ks + piece_at<D, MX>(r, 2 * kk + (lane >> 3)));
+            mma_bf16(s[nt], q[kk], x[0], x[1]);
+            mma_bf16(s[nt], q[kk + 1], x[2], x[3]);
+          }
+        } else {
+          const uint32_t e = scale_word<D>(ksc, r_base + nt * 8 + (lane >> 2));
+          const bool large = __any_sync(0xffffffffu, any_large(e));
+#pragma unroll
+          for (int kk = 0; kk < KS; kk += 4) {
+            uint32_t x[4];
+            ldmatrix4(x, ks + piece_at<D, MX>(r, kk + (lane >> 3)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t eb = same_byte(e, (kk + i) / 2), f = factor2(eb);
+              uint32_t b0 = mul2(codes_lo(x[i]), f), b1 = mul2(codes_hi(x[i]), f);
+              if (large) {
+                const uint32_t g = rest2(eb);
+                b0 = mul2(b0, g);
+                b1 = mul2(b1, g);
+              }
+              mma_bf16(s[nt], q[kk + i], b0, b1);
+            }
+          }
+        }
+      }
+      // ---- weights
+      if (a.act == JATTN_SOFTMAX) {
+        float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[nt][e] *= a.scale_log2;
+            if (partial) {
+              const int pos = pos0 + nt * 8 + 2 * c + (e & 1);
+              if (pos < (e < 2 ? lo0 : lo1) || pos >= (e < 2 ? hi0 : hi1)) s[nt][e] = -INFINITY;
+            }
+          }
+          t0 = fmaxf(t0, fmaxf(s[nt][0], s[nt][1]));
+          t1 = fmaxf(t1, fmaxf(s[nt][2], s[nt][3]));
+        }
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
+        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
+        if (__any_sync(0xffffffffu, t0 > m0 + kSlack || t1 > m1 + kSlack)) {
+          const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+          const float c0 = m0 == n0 ? 1.0f : ex2_approx(m0 - n0), c1 = m1 == n1 ? 1.0f : ex2_approx(m1 - n1);
+          m0 = n0;
+          m1 = n1;
+          l0 *= c0;
+          l1 *= c1;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            o[j][0] *= c0;
+            o[j][1] *= c0;
+            o[j][2] *= c1;
+            o[j][3] *= c1;
+          }
+        }
+        const float u0 = m0 == -INFINITY ? 0.0f : m0, u1 = m1 == -INFINITY ? 0.0f : m1;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          s[nt][0] = ex2_approx(s[nt][0] - u0);
+          s[nt][1] = ex2_approx(s[nt][1] - u0);
+          s[nt][2] = ex2_approx(s[nt][2] - u1);
+          s[nt][3] = ex2_approx(s[nt][3] - u1);
+          l0 += s[nt][0] + s[nt][1];
+          l1 += s[nt][2] + s[nt][3];
+        }
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[nt][e] = activate(s[nt][e] * a.scale, a.act);
+            const int pos = pos0 + nt * 8 + 2 * c + (e & 1);
+            if (partial && (pos < (e < 2 ? lo0 : lo1) || pos >= (e < 2 ? hi0 : hi1))) s[nt][e] = 0.0f;
+          }
+        }
+      }
+      // ---- O += P V, with P as two bf16 parts (its rounding to one would be as large as the output's own)
+#pragma unroll
+      for (int g = 0; g < L::sub / 16; ++g) {
+        uint32_t ph[4], pl[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = s[2 * g + (i >> 1)][(i & 1) * 2], y = s[2 * g + (i >> 1)][(i & 1) * 2 + 1];
+          ph[i] = pack_bf16x2(x, y);
+          pl[i] = bf16x2_lo(x, y, ph[i]);
+        }
+        const int r = r_base + g * 16 + (lane & 15);
+        if constexpr (!MX) {
+#pragma unroll
+          for (int j = 0; j < D / 8; j += 2) {
+            uint32_t x[4];
+            ldmatrix4_trans(x, vs + piece_at<D, MX>(r, j + (lane >> 4)));
+            mma_bf16(o[j], ph, x[0], x[1]);
+            mma_bf16(o[j + 1], ph, x[2], x[3]);
+            mma_bf16(o[j], pl, x[0], x[1]);
+            mma_bf16(o[j + 1], pl, x[2], x[3]);
+          }
+        } else {
+          const int rk = r_base + g * 16 + 2 * c;
+          uint32_t e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            e[i] = scale_word<D>(vsc, rk + (i >> 1) * 8 + (i & 1));
+            // a row that nothing was copied for may have its neighbour's page's exponents: its codes are zeros
+            const int pos = pos0 + g * 16 + 2 * c + (i >> 1) * 8 + (i & 1);
+            if (partial && (pos < at.s.lo || pos >= at.s.hi)) e[i] = 0u;
+          }
+          const bool large = __any_sync(0xffffffffu, any_large(e[0]) || any_large(e[1]) || any_large(e[2]) || any_large(e[3]));
+#pragma unroll
+          for (int j = 0; j < D / 16; j += 2) {  // one block of 32 columns: pieces j and j + 1
+            uint32_t x[4];
+            ldmatrix4_trans(x, vs + piece_at<D, MX>(r, j + (lane >> 4)));
+            const uint32_t ea = byte_pair(e[0], e[1], j / 2), eb = byte_pair(e[2], e[3], j / 2);
+            const uint32_t fa = factor2(ea), fb = factor2(eb);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t b[4] = {mul2(codes_lo(x[2 * i]), fa), mul2(codes_lo(x[2 * i + 1]), fb),
+                               mul2(codes_hi(x[2 * i]), fa), mul2(codes_hi(x[2 * i + 1]), fb)};
+              if (large) {
+                const uint32_t ga = rest2(ea), gb = rest2(eb);
+                b[0] = mul2(b[0], ga);
+                b[1] = mul2(b[1], gb);
+                b[2] = mul2(b[2], ga);
+                b[3] = mul2(b[3], gb);
+              }
+              float(&even)[4] = o[2 * (j + i)];
+              float(&odd)[4] = o[2 * (j + i) + 1];
+              mma_bf16(even, ph, b[0], b[1]);
+              mma_bf16(odd, ph, b[2], b[3]);
+              mma_bf16(even, pl, b[0], b[1]);
+              mma_bf16(odd, pl, b[2], b[3]);
+            }
+          }
+        }
+      }
+    }
+    stage_no = stage_no + 1 == kStages ? 0 : stage_no + 1;
+
+    // ---- the unit's, or the run's, last step
+    const bool unit_ends = at.t == at.s.steps - 1, run_ends = done == last - first - 1;
+    if (unit_ends || run_ends) {
+      const bool whole = unit_ends && at.t == static_cast<int>(done - unit_first);  // all of its steps were in this run
+      if (live) {
+        repair<D, MX>(a, at, h, row_base, static_cast<int>(done - unit_first) + 1, step, q, o, m0, m1, lo0, hi0, lo1, hi1);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int64_t r = row_base + (lane >> 2) + half * 8;
+          if (r >= rows) continue;
+          const float m = half ? m1 : m0, l = half ? l1 : l0;
+          if (whole) {
+            const int64_t out = (at.s.q0 + r / a.G) * a.Hq + h * a.G + r % a.G;
+            const float f = out_factor(a, l, at.s.n);
+            if (a.act == JATTN_SOFTMAX && c == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D);
+#pragma unroll
+            for (int j = 0; j < D / 8; j += 2) {
+              const float x0 = o[j][2 * half] * f, x1 = o[j][2 * half + 1] * f;
+              const float y0 = o[j + 1][2 * half] * f, y1 = o[j + 1][2 * half + 1] * f;
+              if constexpr (MX) {  // columns 4c, 4c + 2 (even) and 4c + 1, 4c + 3 (odd) of a piece
+                *reinterpret_cast<uint2*>(dst + j * 4 + 2 * c) = make_uint2(pack_bf16x2(x0, y0), pack_bf16x2(x1, y1));
+              } else {
+                dst[j * 4 + c] = pack_bf16x2(x0, x1);
+                dst[j * 4 + 4 + c] = pack_bf16x2(y0, y1);
+              }
+            }
+          } else {
+            // slot 1 if the unit's first step is in this run
+            const int slot = at.t == static_cast<int>(done - unit_first) ? 1 : 0;
+            const int64_t row = (static_cast<int64_t>(me) * 2 + slot) * tile + warp_m * 16 + (lane >> 2) + half * 8;
+            if (c == 0) sc.ml[row] = make_float2(m, l);
+            float* dst = sc.acc + row * D;
+#pragma unroll
+            for (int j = 0; j < D / 8; j += 2) {
+              const float* x = &o[j][2 * half];
+              const float* y = &o[j + 1][2 * half];
+              if constexpr (MX) {
+                *reinterpret_cast<float4*>(dst + j * 8 + 4 * c) = make_float4(x[0], y[0], x[1], y[1]);
+              } else {
+                *reinterpret_cast<float2*>(dst + j * 8 + 2 * c) = make_float2(x[0], x[1]);
+                *reinterpret_cast<float2*>(dst + j * 8 + 8 + 2 * c) = make_float2(y[0], y[1]);
+              }
+            }
+          }
+        }
+      }
+      if (run_ends && tid == 0) {
+        int4 j = make_int4(0, 0, 0, 0);
+        if (!unit_ends && at.t == static_cast<int>(done - unit_first)) {  // begun here, finished by later workers
+          const int64_t end = last + (at.s.steps - 1 - at.t);             // number of the unit's end
+          j = make_int4(static_cast<int>((end - 1) / share - me) + 1, at.b,
+                        static_cast<int>(at.u / static_cast<uint32_t>(a.cache.H)), h);
+        }
+        sc.join[me] = j;
+      }
+      fresh = true;
+    }
+    if (!run_ends) advance(at, a, tile, step);
+  }
+}
+
+// One CTA per worker: joins the pieces of the unit that the worker left
+// unfinished, if it did. A warp takes a row, or a share of a row's pieces; its
+// lanes take the columns.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(DecodeArgs a, void* scratch, int workers, int tile) {
+  const Scratch sc = carve(scratch, workers, tile, D);
+  const int4 j = sc.join[blockIdx.x];
+  if (j.x == 0) return;
+  constexpr int E = D / 32, W = kJoinThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t q0 = j.y, lq = 1;
+  if (a.q_off != nullptr) {
+    q0 = a.q_off[j.y];
+    lq = a.q_off[j.y + 1] - q0;
+  }
+  const int64_t r0 = static_cast<int64_t>(j.z) * tile;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(tile), lq * a.G - r0));
+  const int ways = rows >= W ? 1 : W / rows;  // warps per row
+  __shared__ float part[W][D + 1];
+  auto slot = [&](int p) { return (static_cast<int64_t>(blockIdx.x) + p) * 2 + (p == 0 ? 1 : 0); };
+  for (int base = 0; base < rows; base += W / ways) {
+    const int r = base + warp / ways, way = warp % ways;
+    const bool on = warp / ways < W / ways && r < rows;
+    float acc[E], l = 0.0f, m = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    if (on) {
+      if (a.act == JATTN_SOFTMAX) {
+        for (int p = lane; p < j.x; p += 32) m = fmaxf(m, sc.ml[slot(p) * tile + r].x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      }
+      const float use = m == -INFINITY ? 0.0f : m;
+#pragma unroll 4
+      for (int p = way; p < j.x; p += ways) {
+        const int64_t row = slot(p) * tile + r;
+        float w = 1.0f;
+        if (a.act == JATTN_SOFTMAX) {
+          const float2 ml = sc.ml[row];
+          w = ex2_approx(ml.x - use);
+          l = fmaf(w, ml.y, l);
+        }
+        const float* x = sc.acc + row * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[e], acc[e]);
+      }
+    }
+    if (ways > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
+      if (lane == 0) part[warp][D] = l;
+      __syncthreads();
+      if (on && way == 0) {
+        for (int o = 1; o < ways; ++o) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += part[warp + o][lane * E + e];
+          l += part[warp + o][D];
+        }
+      }
+    }
+    if (on && way == 0) {
+      const int64_t row = r0 + r, out = (q0 + row / a.G) * a.Hq + j.w * a.G + row % a.G;
+      const float f = out_factor(a, l, static_cast<int>(a.kv_lens[j.y]));
+      if (a.act == JATTN_SOFTMAX && lane == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D + lane * E);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * f, acc[e + 1] * f);
+    }
+  }
+}
+
+struct Shape {
+  int wm, ctas, workers, tile;
+};
+
+// Warps per worker: one row tile of 16 rows each, as many as an average
+// sequence has rows per key/value head (at most four: 64 rows). CTAs: two per
+// SM, fewer where the largest possible number of steps leaves some without work.
+Shape shape_of(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H) {
+  Shape s;
+  const int64_t rows = (total_q + B - 1) / B * G;
+  s.wm = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  s.tile = 16 * s.wm;
+  const int64_t step = 4096 / (D * (mx ? 1 : 2)) * s.wm;
+  // tiles of all sequences: each has at most one that is not full
+  const int64_t tiles = total_q * G / s.tile + (total_q < B ? total_q : B);
+  const int64_t per_worker = kMinSteps, per_cta = per_worker * (kWarps / s.wm);
+  const double steps = static_cast<double>(tiles) * H * static_cast<double>((max_kv + step - 1) / step + 2);
+  s.ctas = steps / per_cta >= kMaxCtas ? kMaxCtas : static_cast<int>(steps / per_cta) + 1;
+  s.workers = s.ctas * (kWarps / s.wm);
+  return s;
+}
+
+template <int D, bool MX, int WM>
+cudaError_t launch(const DecodeArgs& a, const Shape& s, void* scratch, cudaStream_t stream) {
+  constexpr int smem = kStages * Layout<D, MX>::stage * kWarps;
+  const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, MX, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  decode_kernel<D, MX, WM><<<s.ctas, kThreads, smem, stream>>>(a, scratch);
+  return cudaGetLastError();
+}
+
+template <int D, bool MX>
+cudaError_t launch_wm(const DecodeArgs& a, const Shape& s, void* scratch, cudaStream_t stream) {
+  if (s.wm == 1) return launch<D, MX, 1>(a, s, scratch, stream);
+  if (s.wm == 2) return launch<D, MX, 2>(a, s, scratch, stream);
+  return launch<D, MX, 4>(a, s, scratch, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_decode(int D, bool mx, const DecodeArgs& a, cudaStream_t stream) {
-  const auto kernel = D == 64 ? (mx ? decode_kernel<64, true> : decode_kernel<64, false>)
-                              : (mx ? decode_kernel<128, true> : decode_kernel<128, false>);
-  kernel<<<static_cast<unsigned>((a.total_q * a.Hq + 3) / 4), 128, 0, stream>>>(a);
+size_t decode_scratch_bytes(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H) {
+  const Shape s = shape_of(D, mx, B, total_q, max_kv, G, H);
+  return scratch_bytes(s.workers, s.tile, D);
+}
+
+cudaError_t launch_decode(int D, bool mx, const DecodeArgs& a, void* scratch, cudaStream_t stream) {
+  const Shape s = shape_of(D, mx, a.B, a.total_q, a.max_kv, a.G, a.cache.H);
+  cudaError_t e = D == 64 ? (mx ? launch_wm<64, true>(a, s, scratch, stream) : launch_wm<64, false>(a, s, scratch, stream))
+                          : (mx ? launch_wm<128, true>(a, s, scratch, stream) : launch_wm<128, false>(a, s, scratch, stream));
+  if (e != cudaSuccess) return e;
+  const auto join = D == 64 ? join_kernel<64> : join_kernel<128>;
+  join<<<s.workers, kJoinThreads, 0, stream>>>(a, scratch, s.workers, s.tile);
   return cudaGetLastError();
 }
 

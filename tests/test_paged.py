@@ -78,7 +78,7 @@ def test_decode_checks(lib):
     for kw, want in [(dict(p=params(H=3)), 1), (dict(p=params(D=64)), 1), (dict(p=params(total_kv=65)), 1),
                      (dict(p=params(total_q=3)), 1), (dict(p=params(act=7)), 1), (dict(p=params(mask=2)), 1),
                      (dict(p=params(norm_by_lkv=1)), 1), (dict(lens=None), 1), (dict(table=None), 1), (dict(pages=0), 1),
-                     (dict(q=None), 1), (dict(o=None), 1), (dict(lse=None), 1), (dict(q=F + 8), 4), (dict(o=F + 2), 4),
+                     (dict(q=None), 1), (dict(o=None), 1), (dict(o=F), 1), (dict(lse=None), 1), (dict(q=F + 8), 4), (dict(o=F + 2), 4),
                      (dict(scratch=None), 3), (dict(scratch=F + 16), 3), (dict(scratch_bytes=0), 3), (dict(ws=None), 3),
                      (dict(ws=F + 8), 3), (dict(ws_bytes=64), 3)]:
         assert decode(**kw) == want, kw
