@@ -326,7 +326,7 @@ int jattn_bwd_mxfp8(const jattn_params_t* p, const int64_t* q_off, const int64_t
  *     nearest even, saturated to +-448. A block that holds a NaN or an infinity
  *     gets E = 255 (E8M0's NaN) and reads back as NaN; codes 0x7f / 0xff (E4M3's
  *     own NaN) are never written.
- * Buffers are device memory, k and v 16-byte and the scales 4-byte aligned.
+ * Buffers are device memory and 16-byte aligned.
  *
  * Errors that only the device sees land in the status word at `workspace`
  * (256 bytes, zero before its first use, read with jattn_get_status): nothing
@@ -385,7 +385,8 @@ int jattn_cache_read(const jattn_cache_t* cache, int64_t B, int64_t total, const
  * p->total_kv is an upper bound of kv_lens (at most max_pages * page_size); a
  * length outside [0, p->total_kv] sets JATTN_ERR_LENGTH and counts as 0.
  * Writes o [total_q, H, D] bf16 (which must not overlap q) and, for
- * JATTN_SOFTMAX, lse [total_q, H] fp32. Rows of a bad page count as zeros.
+ * JATTN_SOFTMAX, lse [total_q, H] fp32. A sequence with a bad page among
+ * those it needs sets JATTN_ERR_PAGES; its rows are unspecified.
  * A row that no key is allowed for gets o = 0, lse = -inf. Rows behind
  * q_off[B] are left as they were. Cached values at positions that a row's mask
  * excludes never reach it, whatever they are.

@@ -871,8 +871,6 @@ int jattn_rope(const jattn_params_t* p, const int64_t* q_off, const int64_t* kv_
 namespace jattn {
 namespace {
 
-bool aligned4(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 3u) == 0; }
-
 int check_cache(const jattn_cache_t* c) {
   if (!c) return JATTN_ERR_INVALID;
   if (c->n_pages < 1 || c->n_pages > INT32_MAX || c->H < 1 || (c->D != 64 && c->D != 128)) return JATTN_ERR_INVALID;
@@ -882,7 +880,7 @@ int check_cache(const jattn_cache_t* c) {
   if (!c->k || !c->v) return JATTN_ERR_INVALID;
   if ((c->format == JATTN_CACHE_MXFP8) != (c->k_scales && c->v_scales)) return JATTN_ERR_INVALID;
   if (c->format == JATTN_CACHE_BF16 && (c->k_scales || c->v_scales)) return JATTN_ERR_INVALID;
-  if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scales) || !aligned4(c->v_scales))
+  if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scales) || !aligned16(c->v_scales))
     return JATTN_ERR_ALIGN;
   return JATTN_OK;
 }
@@ -917,6 +915,23 @@ CacheView cache_view(const jattn_cache_t* c, const int32_t* page_table, int64_t 
   v.table = page_table;
   v.max_pages = max_pages;
   return v;
+}
+
+// Pages as {D, page_size, H, n_pages}; boxes of one head's rows, 128 bytes (64
+// for codes at D = 64) by box_rows, swizzled over their width.
+int make_page_map(CUtensorMap* m, const jattn_cache_t* c, void* pages, int box_rows) {
+  const bool mx = c->format == JATTN_CACHE_MXFP8;
+  const cuuint64_t row = static_cast<cuuint64_t>(c->D) * (mx ? 1 : 2);
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->D), static_cast<cuuint64_t>(c->page_size),
+                              static_cast<cuuint64_t>(c->H), static_cast<cuuint64_t>(c->n_pages)};
+  const cuuint64_t strides[3] = {row, row * c->page_size, row * c->page_size * c->H};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(mx ? c->D : 64), static_cast<cuuint32_t>(box_rows), 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(m, mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pages, dims,
+                              strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              mx && c->D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? JATTN_OK : JATTN_ERR_CUDA;
 }
 
 int check_decode(const jattn_params_t* p, const jattn_cache_t* c) {
@@ -998,6 +1013,7 @@ int jattn_decode(const jattn_params_t* p, const jattn_cache_t* c, const int64_t*
   if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) || scratch_bytes < need) return JATTN_ERR_WORKSPACE;
   DeviceInfo dev;
   if ((rc = device_info(dev)) != JATTN_OK) return rc;
+  if ((rc = encoder()) != JATTN_OK) return rc;
   clear_stale_error();
   if (p->total_q == 0) return JATTN_OK;
   DecodeArgs a{};
@@ -1018,9 +1034,14 @@ int jattn_decode(const jattn_params_t* p, const jattn_cache_t* c, const int64_t*
   a.norm_by_lkv = p->norm_by_lkv;
   a.scale = p->scale > 0.0f ? p->scale : 1.0f / std::sqrt(static_cast<float>(p->D));
   a.scale_log2 = a.scale * 1.4426950408889634f;
+  a.timeout_ns = g_timeout_ns;
   a.status = static_cast<DevStatus*>(ws);
-  const cudaError_t e = launch_decode(p->D, c->format == JATTN_CACHE_MXFP8, a, scratch,
-                                      static_cast<cudaStream_t>(stream));
+  const bool mx = c->format == JATTN_CACHE_MXFP8;
+  const int box = decode_box_rows(p->D, mx, p->B, p->total_q, p->total_kv, a.G, c->H, c->page_size);
+  CUtensorMap mk, mv;
+  if (make_page_map(&mk, c, c->k, box) || make_page_map(&mv, c, c->v, box))
+    return cuda_fail("cuTensorMapEncodeTiled", cudaErrorInvalidValue);
+  const cudaError_t e = launch_decode(p->D, mx, a, mk, mv, scratch, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? JATTN_OK : cuda_fail("decode kernel launch", e);
 }
 

@@ -37,6 +37,7 @@ struct DecodeArgs {
   int Hq, G;       // query heads, query heads per key/value head
   int act, mask, window, norm_by_lkv;
   float scale, scale_log2;
+  uint64_t timeout_ns;
   DevStatus* status;
 };
 

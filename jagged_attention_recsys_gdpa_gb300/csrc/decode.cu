@@ -9,8 +9,8 @@
 // sequence and head, 4 D operations per 2 rows of 2 D bytes: for up to some 60
 // rows the cache's bytes bound the call, not the tensor cores. So the layout
 // serves the copies: each worker keeps its own ring of stages in shared
-// memory, filled with 16-byte asynchronous copies straight from the pages
-// (any page size, rows past a sequence's keys filled with zeros), and the
+// memory, filled by TMA straight from the pages (a step's rows are one piece of
+// a page, or one piece each of several small pages, issued by a lane each), and the
 // products are warp-level MMAs whose 16 rows hold the query rows; a 128-row
 // tcgen05 tile would be mostly padding here and would need operands and
 // accumulators staged through TMEM for nothing.
@@ -186,21 +186,29 @@ __device__ __forceinline__ Place find_place(const DecodeArgs& a, int tile, int s
 template <int D, bool MX>
 struct Layout {
   static constexpr int row = D * (MX ? 1 : 2);           // bytes of a K or V row
-  static constexpr int chunks = row / 16;
+  static constexpr int line = row < 128 ? row : 128;     // bytes of a copied box's row
   static constexpr int sub = !MX && D == 128 ? 16 : 32;  // keys per product block
   static constexpr int keys = 4096 / row;                // keys of a step, per warp: 4 KB of K, 4 KB of V
   static constexpr int scale = MX ? D / 32 : 0;          // scale bytes per row
-  static constexpr int stage = 8192 + 2 * keys * scale;  // bytes of a stage, per warp
   static_assert(keys % sub == 0, "a step holds whole product blocks");
 };
 
-// Byte offset of 16-byte piece `chunk` of row r: pieces are permuted so that the
-// eight rows of an 8x8 matrix load lie in different banks.
+// Shared memory of a CTA: [worker][stage] K rows then V rows (1024-byte aligned,
+// in TMA's 128- or 64-byte swizzle), [worker][stage] K then V exponents, then
+// [worker][stage] barriers: copied, and read by all of the worker's warps.
 template <int D, bool MX>
+constexpr int smem_bytes() {
+  return 1024 + kWarps * kStages * (8192 + 2 * Layout<D, MX>::keys * Layout<D, MX>::scale + 16);
+}
+
+// Byte offset of 16-byte piece `chunk` of row r in a step of STEP rows: rows of
+// 256 bytes lie as two boxes of 128; the swizzle puts the eight rows of an 8x8
+// matrix load into different banks.
+template <int D, bool MX, int STEP>
 __device__ __forceinline__ uint32_t piece_at(int r, int chunk) {
   using L = Layout<D, MX>;
-  const int x = L::chunks >= 8 ? r & 7 : (r >> 1) & 3;
-  return static_cast<uint32_t>(r * L::row + ((chunk ^ x) << 4));
+  if constexpr (L::line == 64) return static_cast<uint32_t>(r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4));
+  else return static_cast<uint32_t>((chunk >> 3) * (STEP * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4));
 }
 
 // ---------------------------------------------------------------- E4M3 to bf16
@@ -360,75 +368,86 @@ __host__ __device__ inline Scratch carve(void* base, int workers, int rows, int 
   return s;
 }
 
+// Where the warps of one worker meet once, before its first copy.
 template <int WM>
-__device__ __forceinline__ void worker_sync(int worker) {
-  if constexpr (WM == 1) __syncwarp();
-  else asm volatile("bar.sync %0, %1;" ::"r"(worker + 1), "n"(WM * 32) : "memory");
+__device__ __forceinline__ void worker_barrier(int worker) {
+  asm volatile("bar.sync %0, %1;" ::"r"(worker + 1), "n"(WM * 32) : "memory");
 }
 
-// Copies one step's rows (and scales) into a stage. Rows outside [lo, hi) and
-// rows of a bad page become zeros and are not looked up.
-template <int D, bool MX, int WM>
-__device__ __forceinline__ void load_step(const DecodeArgs& a, const Place& p, uint32_t stage, int tid) {
-  using L = Layout<D, MX>;
-  constexpr int step = L::keys * WM, threads = WM * 32;
-  const int h = static_cast<int>(p.u % static_cast<uint32_t>(a.cache.H));
-  const int64_t head = static_cast<int64_t>(h) << a.cache.page_shift;
-  const int pos0 = p.s.k0 + p.t * step;
-  const char* k = static_cast<const char*>(a.cache.k);
-  const char* v = static_cast<const char*>(a.cache.v);
-  const bool one_page = a.cache.page_mask + 1 >= step;  // steps and pages are both aligned powers of two
-  int64_t base = -1;
-  if (one_page && pos0 < p.s.hi && p.s.lo < p.s.hi) base = cache_row(a.cache, p.b, max(pos0, p.s.lo), a.status);
-  if (one_page && base >= 0) base += head + pos0 - max(pos0, p.s.lo);
-  constexpr int per = threads / L::chunks;  // rows per pass of the worker's threads
-#pragma unroll
-  for (int i = 0; i < step / per; ++i) {
-    const int r = i * per + tid / L::chunks, chunk = tid % L::chunks, pos = pos0 + r;
-    int64_t row = -1;
-    if (pos >= p.s.lo && pos < p.s.hi) {
-      if (one_page) {
-        row = base < 0 ? -1 : base + r;
-      } else {
-        row = cache_row(a.cache, p.b, pos, a.status);
-        if (row >= 0) row += head;
-      }
+// Bounded wait; false (and the status set) when it runs out.
+__device__ __forceinline__ bool wait_full(const DecodeArgs& a, uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (globaltimer_ns() - t0 > a.timeout_ns) {
+      record_error(a.status, JATTN_ERR_TIMEOUT, 86, blockIdx.x);
+      return false;
     }
-    const int64_t at = row < 0 ? 0 : row * L::row + chunk * 16;
-    const uint32_t to = stage + piece_at<D, MX>(r, chunk);
-    cp_async16(to, k + at, row < 0 ? 0 : 16);
-    cp_async16(to + 4096 * WM, v + at, row < 0 ? 0 : 16);
+  }
+  return true;
+}
+
+// A step's rows are copied as boxes of min(page size, step) rows; lane i < boxes
+// takes box i. Its table entry, or kNoBox where no key lies that any row sees.
+constexpr int64_t kNoBox = INT64_MIN;
+__device__ __forceinline__ int64_t box_page(const DecodeArgs& a, const Place& p, int step, int box, int lane) {
+  const int first = p.s.k0 + p.t * step + lane * box;
+  if (lane * box >= step || p.s.lo >= p.s.hi || first >= p.s.hi || first + box <= p.s.lo) return kNoBox;
+  return __ldg(a.cache.table + p.b * a.cache.max_pages + (first >> a.cache.page_shift));
+}
+
+template <int D, bool MX, int WM>
+__device__ __forceinline__ void load_step(const DecodeArgs& a, const CUtensorMap* k_map, const CUtensorMap* v_map,
+                                          const Place& p, int64_t page, uint32_t stage, uint32_t scales, uint64_t* bar,
+                                          int box, int lane) {
+  using L = Layout<D, MX>;
+  constexpr int step = L::keys * WM;
+  const bool ok = page >= 0 && page < a.cache.n_pages;
+  if (page != kNoBox && !ok) record_error(a.status, JATTN_ERR_PAGES, 80, p.b);
+  const uint32_t n = __popc(__ballot_sync(0xffffffffu, ok));
+  if (lane == 0) mbar_arrive_expect_tx(bar, n * static_cast<uint32_t>(box * 2 * (L::row + L::scale)));
+  __syncwarp();
+  if (!ok) return;
+  const int h = static_cast<int>(p.u % static_cast<uint32_t>(a.cache.H));
+  const int r = lane * box, y = (p.s.k0 + p.t * step + r) & a.cache.page_mask;
+  const uint32_t b = smem_u32(bar);
+#pragma unroll
+  for (int x = 0; x < L::row / L::line; ++x) {
+    const uint32_t to = stage + x * (step * L::line) + r * L::line;
+    tma_load_4d(to, k_map, b, x * 64, y, h, static_cast<int>(page));
+    tma_load_4d(to + 4096 * WM, v_map, b, x * 64, y, h, static_cast<int>(page));
   }
   if constexpr (MX) {
-    // one word of exponents: a row's four (D = 128), or two rows' (D = 64; both in one page). Of a pair with one row
-    // outside [lo, hi) the other row's bytes come along: masked where they are used.
-    constexpr int rows = 4 / L::scale, words = step / rows;
-#pragma unroll
-    for (int i = 0; i < (words + threads - 1) / threads; ++i) {
-      const int w = i * threads + tid, pos = pos0 + w * rows;
-      if (words % threads != 0 && w >= words) break;
-      int64_t row = -1;
-      if (pos + rows > p.s.lo && pos < p.s.hi) {
-        if (one_page) {
-          row = base < 0 ? -1 : base + w * rows;
-        } else {
-          row = cache_row(a.cache, p.b, pos, a.status);
-          if (row >= 0) row += head;
-        }
-      }
-      const int64_t at = row < 0 ? 0 : row * L::scale;
-      const uint32_t to = stage + 8192 * WM + w * 4;
-      cp_async4(to, a.cache.ks + at, row < 0 ? 0 : 4);
-      cp_async4(to + words * 4, a.cache.vs + at, row < 0 ? 0 : 4);
-    }
+    const int64_t at = (((page * a.cache.H + h) << a.cache.page_shift) + y) * L::scale;
+    bulk_load(scales + r * L::scale, a.cache.ks + at, box * L::scale, b);
+    bulk_load(scales + (step + r) * L::scale, a.cache.vs + at, box * L::scale, b);
   }
 }
 
+// Zeros for the V rows of a step outside [lo, hi): what their places hold has
+// to be finite to vanish under a weight of zero.
+template <int D, int WM>
+__device__ __forceinline__ void clear_rows(uint32_t vs, int pos0, int lo, int hi, int lane) {
+  using L = Layout<D, false>;
+  constexpr int step = L::keys * WM;
+  for (int i = lane; i < 4096 * WM / 16; i += 32) {
+    const int r = i % step;  // any piece of row r: the swizzle stays within the row
+    if (pos0 + r >= lo && pos0 + r < hi) continue;
+    const int chunk = i / step;
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vs + piece_at<D, false, step>(r, chunk)), "r"(0u)
+                 : "memory");
+  }
+  fence_proxy_async();
+  __syncwarp();
+}
+
 template <int D, bool MX, int WM>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(DecodeArgs a, void* scratch) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                  void* scratch) {
   using L = Layout<D, MX>;
   constexpr int step = L::keys * WM, tile = 16 * WM, KS = D / 16, NT = L::sub / 8;
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ unsigned char smem_raw[];
   __shared__ int64_t start[kThreads];
   const int tid = threadIdx.x % (WM * 32), lane = threadIdx.x & 31, c = lane & 3;
   const int in_cta = threadIdx.x / (WM * 32), warp_m = tid >> 5;
@@ -444,17 +463,39 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(DecodeArgs
   }
   Place in = find_place(a, tile, step, start, first);  // the step that is copied next
   Place at = in;                                       // the step that is computed next
-  int64_t to_load = last - first;
-  const uint32_t ring = smem_u32(smem) + in_cta * (kStages * L::stage * WM);
-  int load_stage = 0;
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) {
-    if (to_load > 0) {
-      load_step<D, MX, WM>(a, in, ring + load_stage * (L::stage * WM), tid);
-      if (--to_load > 0) advance(in, a, tile, step);
+  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t ring = smem + in_cta * (kStages * 8192 * WM);
+  const uint32_t scale_ring = smem + kWarps * kStages * 8192 + in_cta * (kStages * 2 * step * L::scale);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + (smem - smem_u32(smem_raw)) +
+                                               kWarps * kStages * (8192 + 2 * L::keys * L::scale)) +
+                   in_cta * (2 * kStages);
+  uint64_t* empty = full + kStages;
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, WM);
     }
-    cp_async_commit();
-    ++load_stage;
+    fence_mbar_init();
+    fence_proxy_async();
+  }
+  if constexpr (WM == 1) __syncwarp();
+  else worker_barrier<WM>(in_cta);
+  const int box = min(step, a.cache.page_mask + 1);
+  int64_t loaded = 0;  // steps whose copies have been issued (by the worker's first warp)
+  int64_t page = kNoBox;
+  if (warp_m == 0) {
+    page = box_page(a, in, step, box, lane);
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+      if (loaded < last - first) {
+        load_step<D, MX, WM>(a, &k_map, &v_map, in, page, ring + s * (8192 * WM), scale_ring + s * (2 * step * L::scale),
+                             full + s, box, lane);
+        if (++loaded < last - first) {
+          advance(in, a, tile, step);
+          page = box_page(a, in, step, box, lane);
+        }
+      }
+    }
   }
 
   uint32_t q[KS][4];
@@ -465,15 +506,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(DecodeArgs
   bool fresh = true;
   int64_t unit_first = 0;  // the first step of the unit at `at` that this run holds, counted within the run
   int stage_no = 0;
-  for (int64_t done = 0; done < last - first; ++done) {
-    cp_async_wait<kStages - 2>();
-    worker_sync<WM>(in_cta);
-    if (to_load > 0) {
-      load_step<D, MX, WM>(a, in, ring + load_stage * (L::stage * WM), tid);
-      if (--to_load > 0) advance(in, a, tile, step);
+  uint32_t phase = 0;
+  bool ok = true;
+  int64_t done = 0;
+  for (; done < last - first; ++done) {
+    if (!wait_full(a, full + stage_no, phase)) {
+      ok = false;
+      break;
     }
-    cp_async_commit();
-    load_stage = load_stage + 1 == kStages ? 0 : load_stage + 1;
+    if (warp_m == 0 && loaded < last - first) {
+      // the stage after the one in flight was read in the step before this one
+      const int s = stage_no == 0 ? kStages - 1 : stage_no - 1;
+      if constexpr (WM == 1) {
+        __syncwarp();
+      } else {
+        if (loaded >= kStages && !wait_full(a, empty + s, static_cast<uint32_t>(loaded / kStages - 1) & 1u)) {
+          ok = false;
+          break;
+        }
+      }
+      load_step<D, MX, WM>(a, &k_map, &v_map, in, page, ring + s * (8192 * WM), scale_ring + s * (2 * step * L::scale),
+                           full + s, box, lane);
+      if (++loaded < last - first) {
+        advance(in, a, tile, step);
+        page = box_page(a, in, step, box, lane);
+      }
+    }
 
     const int h = static_cast<int>(at.u % static_cast<uint32_t>(a.cache.H));
     const int64_t rows = static_cast<int64_t>(at.s.lq) * a.G;
@@ -523,11 +581,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(DecodeArgs
       }
     }
 
-    const uint32_t ks = ring + stage_no * (L::stage * WM), vs = ks + 4096 * WM;
-    const uint32_t ksc = ks + 8192 * WM, vsc = ksc + step * L::scale;
+    const uint32_t ks = ring + stage_no * (8192 * WM), vs = ks + 4096 * WM;
+    const uint32_t ksc = scale_ring + stage_no * (2 * step * L::scale), vsc = ksc + step * L::scale;
+    const int step0 = at.s.k0 + at.t * step;
+    if constexpr (!MX) {
+      if (live && (step0 < at.s.lo || step0 + step > at.s.hi)) clear_rows<D, WM>(vs, step0, at.s.lo, at.s.hi, lane);
+    }
 #pragma unroll 1
     for (int sb = 0; sb < step / L::sub; ++sb) {
-      const int r_base = sb * L::sub, pos0 = at.s.k0 + at.t * step + r_base;
+      const int r_base = sb * L::sub, pos0 = step0 + r_base;
       if (!live || pos0 >= any_hi || pos0 + L::sub <= any_lo) continue;
       const bool partial = pos0 < all_lo || pos0 + L::sub > all_hi;
       // ---- scores
@@ -540,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(DecodeArgs
 #pragma unroll
           for (int kk = 0; kk < KS; kk += 2) {
             uint32_t x[4];
-            ldmatrix4(x, ks + piece_at<D, MX>(r, 2 * kk + (lane >> 3)));
+            ldmatrix4(x, ks + piece_at<D, MX, step>(r, 2 * kk + (lane >> 3)));
             mma_bf16(s[nt], q[kk], x[0], x[1]);
             mma_bf16(s[nt], q[kk + 1], x[2], x[3]);
           }
@@ -550,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(DecodeArgs
 #pragma unroll
           for (int kk = 0; kk < KS; kk += 4) {
             uint32_t x[4];
-            ldmatrix4(x, ks + piece_at<D, MX>(r, kk + (lane >> 3)));
+            ldmatrix4(x, ks + piece_at<D, MX, step>(r, kk + (lane >> 3)));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t eb = same_byte(e, (kk + i) / 2), f = factor2(eb);
@@ -636,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(DecodeArgs
 #pragma unroll
           for (int j = 0; j < D / 8; j += 2) {
             uint32_t x[4];
-            ldmatrix4_trans(x, vs + piece_at<D, MX>(r, j + (lane >> 4)));
+            ldmatrix4_trans(x, vs + piece_at<D, MX, step>(r, j + (lane >> 4)));
             mma_bf16(o[j], ph, x[0], x[1]);
             mma_bf16(o[j + 1], ph, x[2], x[3]);
             mma_bf16(o[j], pl, x[0], x[1]);
@@ -648,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(DecodeArgs
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             e[i] = scale_word<D>(vsc, rk + (i >> 1) * 8 + (i & 1));
-            // a row that nothing was copied for may have its neighbour's page's exponents: its codes are zeros
+            // rows outside the sequence hold anything: codes are always finite, exponents are made so
             const int pos = pos0 + g * 16 + 2 * c + (i >> 1) * 8 + (i & 1);
             if (partial && (pos < at.s.lo || pos >= at.s.hi)) e[i] = 0u;
           }
@@ -656,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(DecodeArgs
 #pragma unroll
           for (int j = 0; j < D / 16; j += 2) {  // one block of 32 columns: pieces j and j + 1
             uint32_t x[4];
-            ldmatrix4_trans(x, vs + piece_at<D, MX>(r, j + (lane >> 4)));
+            ldmatrix4_trans(x, vs + piece_at<D, MX, step>(r, j + (lane >> 4)));
             const uint32_t ea = byte_pair(e[0], e[1], j / 2), eb = byte_pair(e[2], e[3], j / 2);
             const uint32_t fa = factor2(ea), fb = factor2(eb);
 #pragma unroll
@@ -681,7 +743,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(DecodeArgs
         }
       }
     }
-    stage_no = stage_no + 1 == kStages ? 0 : stage_no + 1;
+    if constexpr (WM > 1) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty + stage_no);
+    }
+    if (++stage_no == kStages) {
+      stage_no = 0;
+      phase ^= 1u;
+    }
 
     // ---- the unit's, or the run's, last step
     const bool unit_ends = at.t == at.s.steps - 1, run_ends = done == last - first - 1;
@@ -746,6 +815,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) decode_kernel(DecodeArgs
       fresh = true;
     }
     if (!run_ends) advance(at, a, tile, step);
+  }
+  if (!ok) {
+    // a wait ran out: nothing to join here, and no copy may be in flight when the CTA ends
+    if (tid == 0) sc.join[me] = make_int4(0, 0, 0, 0);
+    if (warp_m == 0) {
+      for (int64_t i = done; i < loaded; ++i)
+        (void)wait_full(a, full + static_cast<int>(i % kStages), static_cast<uint32_t>(i / kStages) & 1u);
+    }
   }
 }
 
@@ -844,19 +921,21 @@ Shape shape_of(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G
 }
 
 template <int D, bool MX, int WM>
-cudaError_t launch(const DecodeArgs& a, const Shape& s, void* scratch, cudaStream_t stream) {
-  constexpr int smem = kStages * Layout<D, MX>::stage * kWarps;
+cudaError_t launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, const Shape& s, void* scratch,
+                   cudaStream_t stream) {
+  constexpr int smem = smem_bytes<D, MX>();
   const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, MX, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  decode_kernel<D, MX, WM><<<s.ctas, kThreads, smem, stream>>>(a, scratch);
+  decode_kernel<D, MX, WM><<<s.ctas, kThreads, smem, stream>>>(a, k, v, scratch);
   return cudaGetLastError();
 }
 
 template <int D, bool MX>
-cudaError_t launch_wm(const DecodeArgs& a, const Shape& s, void* scratch, cudaStream_t stream) {
-  if (s.wm == 1) return launch<D, MX, 1>(a, s, scratch, stream);
-  if (s.wm == 2) return launch<D, MX, 2>(a, s, scratch, stream);
-  return launch<D, MX, 4>(a, s, scratch, stream);
+cudaError_t launch_wm(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, const Shape& s, void* scratch,
+                      cudaStream_t stream) {
+  if (s.wm == 1) return launch<D, MX, 1>(a, k, v, s, scratch, stream);
+  if (s.wm == 2) return launch<D, MX, 2>(a, k, v, s, scratch, stream);
+  return launch<D, MX, 4>(a, k, v, s, scratch, stream);
 }
 
 }  // namespace
@@ -866,10 +945,18 @@ size_t decode_scratch_bytes(int D, bool mx, int64_t B, int64_t total_q, int64_t 
   return scratch_bytes(s.workers, s.tile, D);
 }
 
-cudaError_t launch_decode(int D, bool mx, const DecodeArgs& a, void* scratch, cudaStream_t stream) {
+int decode_box_rows(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H, int page_size) {
+  const Shape s = shape_of(D, mx, B, total_q, max_kv, G, H);
+  const int step = 4096 / (D * (mx ? 1 : 2)) * s.wm;
+  return step < page_size ? step : page_size;
+}
+
+cudaError_t launch_decode(int D, bool mx, const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, void* scratch,
+                          cudaStream_t stream) {
   const Shape s = shape_of(D, mx, a.B, a.total_q, a.max_kv, a.G, a.cache.H);
-  cudaError_t e = D == 64 ? (mx ? launch_wm<64, true>(a, s, scratch, stream) : launch_wm<64, false>(a, s, scratch, stream))
-                          : (mx ? launch_wm<128, true>(a, s, scratch, stream) : launch_wm<128, false>(a, s, scratch, stream));
+  cudaError_t e;
+  if (D == 64) e = mx ? launch_wm<64, true>(a, k, v, s, scratch, stream) : launch_wm<64, false>(a, k, v, s, scratch, stream);
+  else e = mx ? launch_wm<128, true>(a, k, v, s, scratch, stream) : launch_wm<128, false>(a, k, v, s, scratch, stream);
   if (e != cudaSuccess) return e;
   const auto join = D == 64 ? join_kernel<64> : join_kernel<128>;
   join<<<s.workers, kJoinThreads, 0, stream>>>(a, scratch, s.workers, s.tile);

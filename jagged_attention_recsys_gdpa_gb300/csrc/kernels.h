@@ -117,8 +117,12 @@ cudaError_t launch_cache_append(const CacheView& c, bool mx, int64_t B, int64_t 
                                 const float* sin_t, int rope_rows, DevStatus* status, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheView& c, bool mx, int64_t B, int64_t total, const int64_t* off,
                               const int64_t* start, void* k, void* v, int D, DevStatus* status, cudaStream_t stream);
-// Attention over the paged cache (decode.cu): scratch of decode_scratch_bytes.
+// Attention over the paged cache (decode.cu): scratch of decode_scratch_bytes;
+// k and v map the pages as {D, page_size, H, n_pages} with boxes of 128-byte
+// (codes at D = 64: 64-byte) rows, decode_box_rows of them.
 size_t decode_scratch_bytes(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H);
-cudaError_t launch_decode(int D, bool mx, const DecodeArgs& a, void* scratch, cudaStream_t stream);
+int decode_box_rows(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H, int page_size);
+cudaError_t launch_decode(int D, bool mx, const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, void* scratch,
+                          cudaStream_t stream);
 
 }  // namespace jattn
