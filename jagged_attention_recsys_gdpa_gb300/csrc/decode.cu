@@ -211,76 +211,141 @@ __device__ __forceinline__ uint32_t piece_at(int r, int chunk) {
   else return static_cast<uint32_t>((chunk >> 3) * (STEP * 128) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4));
 }
 
-// ---------------------------------------------------------------- E4M3 to bf16
-// The four codes of a word as two bf16 pairs (bytes 0 and 2, bytes 1 and 3): the
-// code's exponent and mantissa bits go to the low exponent and high mantissa
-// bits, which makes a bf16 of 2^-120 times the value, subnormals included. The
-// scale's factor 2^(e - 127 + 120) makes up for it in one exact product.
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u); }
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u); }
-__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+// ---------------------------------------------------------------- MXFP8 operands
+// Codes become fp16 (one conversion for two, exact), so the products on an MXFP8
+// cache are fp16 MMAs; everything that fp16's range could not hold is kept out
+// of them by powers of two:
+//  * a query row is multiplied by 2^x so that its largest value lies in
+//    [2^14, 2^15): exact but for values below 2^-28 of the largest;
+//  * a K block's scale multiplies the block's fp32 partial score;
+//  * V's scales 2^(e - 127) become fp16 factors 2^(e - R) of the codes, R a
+//    reference exponent of the unit (the accumulators are in units of
+//    2^(R - 127)). From 2^-14 to 2^1 their products are exact; a larger exponent
+//    moves R and rescales the accumulators, and 16 keys with a block below
+//    2^-14 (or of NaN) take bf16 products instead;
+//  * weights are kept at 2^kLift times their value against the row's reference
+//    (the running maximum; for pointwise activations the exponent of their
+//    largest one), so that what fp16 loses below 2^-24 is below 2^-31 of it.
+// bf16 operands throughout cost three times the instructions per code.
+constexpr int kLift = 7;
+
+__device__ __forceinline__ float pow2(int e) {  // 2^e, 0 below fp32's normal range
+  return e < -126 ? 0.0f : __int_as_float((min(e, 127) + 127) << 23);
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r =
       __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-// bf16 factors 2^(e - 7) of two exponents (bytes 0 and 2 of x). bf16 ends at
-// 2^127, so exponents above kMaxE (values above 2^16) are cut there and the rest
-// follows as a second factor: only product blocks that hold one pay for it.
-constexpr uint32_t kMaxE = 134;
-__device__ __forceinline__ uint32_t factor2(uint32_t x) { return (__vminu2(x, kMaxE * 0x10001u) + 0x00780078u) << 7; }
-__device__ __forceinline__ uint32_t rest1(uint32_t e) {
-  return e == 255u ? 0x7fc0u : e > kMaxE ? (e - kMaxE + 127u) << 7 : 0x3f80u;
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t rest2(uint32_t x) { return rest1(x & 0xffu) | (rest1(x >> 16) << 16); }
-__device__ __forceinline__ bool any_large(uint32_t w) { return __vcmpgtu4(w, kMaxE * 0x01010101u) != 0; }
-// Byte j of w twice, and byte j of w0 and w1, in bytes 0 and 2.
-__device__ __forceinline__ uint32_t same_byte(uint32_t w, int j) { return __byte_perm(w, 0u, 0x4040u + 0x0101u * j); }
+__device__ __forceinline__ uint32_t f16x2_lo(float x0, float x1, uint32_t hi) {  // what the pair `hi` leaves out
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  return pack_f16x2(x0 - f.x, x1 - f.y);
+}
+// Byte j of w0 and w1 in the two 16-bit halves.
 __device__ __forceinline__ uint32_t byte_pair(uint32_t w0, uint32_t w1, int j) {
   return __byte_perm(w0, w1, 0x4400u + 0x1111u * j) & 0x00ff00ffu;
 }
+// 2^(e - 127) of byte j of w as fp32 (0 for e = 0: below 2^-118 of anything; e = 255 gives infinity, and with the
+// zero codes of such a block NaN).
+__device__ __forceinline__ float scale_of(uint32_t w, int j) {
+  return __uint_as_float(__byte_perm(w, 0u, (0x0444u | (static_cast<uint32_t>(j) << 12))) >> 1);
+}
+// The four codes of a word as bf16 pairs (bytes 0 and 2, bytes 1 and 3) of 2^-120 times their values: exponent and
+// mantissa bits go to the low exponent and high mantissa bits, subnormals included.
+__device__ __forceinline__ uint32_t codes_even(uint32_t w) { return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u); }
+__device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u); }
+// bf16 pair 2^(e - R + 120) of two exponents (in the halves of x), e <= R + 1; NaN for e = 255.
+__device__ __forceinline__ uint32_t bf16_factors(uint32_t x, int ref) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = static_cast<int>((x >> (16 * i)) & 0xffu);
+    r |= (e == 255 ? 0x7fc0u : static_cast<uint32_t>(max(e - ref + 247, 0)) << 7) << (16 * i);
+  }
+  return r;
+}
 
 // ---------------------------------------------------------------- kernel
-// The exponents of a row in the bytes of a word (D = 64: two, in the low half).
+// The exponents of rows r and r + 1 (r even), each in the low bytes of a word.
 template <int D>
-__device__ __forceinline__ uint32_t scale_word(uint32_t scales, int r) {
-  uint32_t w;
+__device__ __forceinline__ void scale_words(uint32_t scales, int r, uint32_t& w0, uint32_t& w1) {
   if constexpr (D == 128) {
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(scales + r * 4) : "memory");
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(scales + r * 4) : "memory");
   } else {
-    uint16_t x;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(scales + r * 2) : "memory");
-    w = x;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(scales + r * 2) : "memory");
+    w1 = w0 >> 16;
   }
-  return w;
 }
 
-// What the accumulator is multiplied by at the end.
-__device__ __forceinline__ float out_factor(const DecodeArgs& a, float l, int n) {
-  if (a.act == JATTN_SOFTMAX) return l == 0.0f ? 0.0f : 1.0f / l;
-  return a.norm_by_lkv ? (n > 0 ? 1.0f / static_cast<float>(n) : 0.0f) : 1.0f;
+template <int D>
+__device__ __forceinline__ void scale_rows(float (&o)[D / 8][4], float c0, float c1) {
+#pragma unroll
+  for (int j = 0; j < D / 8; ++j) {
+    o[j][0] *= c0;
+    o[j][1] *= c0;
+    o[j][2] *= c1;
+    o[j][3] *= c1;
+  }
 }
 
-// Two (bf16: neighbouring; codes: four neighbouring, in the order 0 2 1 3)
-// columns of a cached row, as the threads hold them.
+// floor(log2 x) of x >= 0, kLeast for anything smaller.
+constexpr float kLeast = -100.0f;
+__device__ __forceinline__ float exponent_of(float x) {
+  return fmaxf(kLeast, static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127));
+}
+// The power of two that brings a row's largest value (of which each of the four
+// lanes of a quad has its part) to [2^14, 2^15).
+__device__ __forceinline__ int lift_of(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+  return x == 0.0f ? 0 : min(14 - (static_cast<int>(__float_as_uint(x) >> 23) - 127), 120);
+}
+
+// Softmax: one over the sum of the weights, 0 for a row that saw no key.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+// Pointwise activations: the normaliser.
+__device__ __forceinline__ float row_norm(const DecodeArgs& a, int n) {
+  return a.norm_by_lkv && n > 0 ? 1.0f / static_cast<float>(n) : 1.0f;
+}
+
+// The four columns of a cached row that a thread holds of 16: of bf16 rows 2c,
+// 2c + 1, 2c + 8, 2c + 9; of codes 4c .. 4c + 3.
 template <bool MX>
-__device__ __forceinline__ void columns(const void* buf, const uint8_t* scales, int64_t row, int D, int j, int c,
+__device__ __forceinline__ void columns(const void* buf, const uint8_t* scales, int64_t row, int D, int kk, int c,
                                         float (&x)[4]) {
   if constexpr (!MX) {
-    const uint32_t* p = static_cast<const uint32_t*>(buf) + (row * D >> 1) + j * 4;  // columns 8 j ...: two tiles
+    const uint32_t* p = static_cast<const uint32_t*>(buf) + row * (D / 2) + kk * 8;
     const uint32_t w0 = __ldg(p + c), w1 = __ldg(p + 4 + c);
     x[0] = __uint_as_float(w0 << 16);
     x[1] = __uint_as_float(w0 & 0xffff0000u);
     x[2] = __uint_as_float(w1 << 16);
     x[3] = __uint_as_float(w1 & 0xffff0000u);
   } else {
-    const uint32_t w = __ldg(static_cast<const uint32_t*>(buf) + (row * D >> 2) + j * 2 + c);  // piece j / 2
-    const float s = e8m0_value(__ldg(scales + row * (D / 32) + j / 4));
+    const uint32_t w = __ldg(static_cast<const uint32_t*>(buf) + row * (D / 4) + kk * 4 + c);
+    const float s = e8m0_value(__ldg(scales + row * (D / 32) + kk / 2));
     const float2 a = e4m3x2_value(w & 0xffffu), b = e4m3x2_value(w >> 16);
     x[0] = a.x * s;
-    x[1] = b.x * s;
-    x[2] = a.y * s;
+    x[1] = a.y * s;
+    x[2] = b.x * s;
     x[3] = b.y * s;
   }
+}
+
+template <bool MX>
+__device__ __forceinline__ float query_value(uint32_t pair, int i) {
+  if constexpr (MX) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&pair));
+    return i ? f.y : f.x;
+  }
+  return __uint_as_float(i ? pair & 0xffff0000u : pair << 16);
 }
 
 // Products of a zero weight and an infinite or NaN value are NaN, and so are
@@ -290,8 +355,9 @@ __device__ __forceinline__ void columns(const void* buf, const uint8_t* scales, 
 // bit each) are summed again one key at a time, over the allowed keys alone.
 template <int D, bool MX>
 __device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int h, int64_t row_base, int n_steps,
-                                       int step, const uint32_t (&q)[D / 16][4], float (&o)[D / 8][4], float m0,
-                                       float m1, int lo0, int hi0, int lo1, int hi1) {
+                                       int step, const uint32_t (&q)[D / 16][4], float f0, float f1,
+                                       float (&o)[D / 8][4], float m0, float m1, float w0, float w1, int lo0,
+                                       int hi0, int lo1, int hi1) {
   float x = 0.0f;  // stays 0 unless something is not finite
 #pragma unroll
   for (int j = 0; j < D / 8; ++j) x += (o[j][0] - o[j][0]) + (o[j][1] - o[j][1]) + (o[j][2] - o[j][2]) + (o[j][3] - o[j][3]);
@@ -316,12 +382,11 @@ __device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int
     float s0 = 0.0f, s1 = 0.0f, k[4];
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-      columns<MX>(a.cache.k, a.cache.ks, row, D, 2 * kk, c, k);
+      columns<MX>(a.cache.k, a.cache.ks, row, D, kk, c, k);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int sh = (e & 1) ? 0 : 16;
-        s0 = fmaf(__uint_as_float((q[kk][(e >> 1) * 2] << sh) & 0xffff0000u), k[e], s0);
-        s1 = fmaf(__uint_as_float((q[kk][(e >> 1) * 2 + 1] << sh) & 0xffff0000u), k[e], s1);
+        s0 = fmaf(query_value<MX>(q[kk][(e >> 1) * 2], e & 1), k[e], s0);
+        s1 = fmaf(query_value<MX>(q[kk][(e >> 1) * 2 + 1], e & 1), k[e], s1);
       }
     }
     s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
@@ -329,19 +394,19 @@ __device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int
     s0 += __shfl_xor_sync(0xffffffffu, s0, 2);
     s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
     const bool soft = a.act == JATTN_SOFTMAX;
-    const float p0 = soft ? ex2_approx(s0 * a.scale_log2 - u0) : activate(s0 * a.scale, a.act);
-    const float p1 = soft ? ex2_approx(s1 * a.scale_log2 - u1) : activate(s1 * a.scale, a.act);
+    const float p0 = soft ? ex2_approx(s0 * f0 - u0) * w0 : activate(s0 * f0, a.act);
+    const float p1 = soft ? ex2_approx(s1 * f1 - u1) * w1 : activate(s1 * f1, a.act);
     const bool in0 = pos >= lo0 && pos < hi0, in1 = pos >= lo1 && pos < hi1;
 #pragma unroll
     for (int j = 0; j < D / 8; j += 2) {
       float v[4];
-      columns<MX>(a.cache.v, a.cache.vs, row, D, j, c, v);
+      columns<MX>(a.cache.v, a.cache.vs, row, D, j / 2, c, v);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float(&t)[4] = o[j + (e >> 1)];
-        const int i = 4 * (j + (e >> 1)) + (e & 1);
-        if (in0 && (bad >> i & 1)) t[e & 1] = fmaf(p0, v[e], t[e & 1]);
-        if (in1 && (bad >> (i + 2) & 1)) t[2 + (e & 1)] = fmaf(p1, v[e], t[2 + (e & 1)]);
+        // codes: columns 4c, 4c + 2 are the first tile's, 4c + 1, 4c + 3 the second's
+        const int t = j + (MX ? e & 1 : e >> 1), x = MX ? e >> 1 : e & 1;
+        if (in0 && (bad >> (4 * t + x) & 1)) o[t][x] = fmaf(p0, v[e], o[t][x]);
+        if (in1 && (bad >> (4 * t + x + 2) & 1)) o[t][x + 2] = fmaf(p1, v[e], o[t][x + 2]);
       }
     }
   }
@@ -502,6 +567,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   float o[D / 8][4];
   float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
   int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;        // keys that this thread's two rows may see
+  float f0 = 0.0f, f1 = 0.0f;                    // what its rows' scores are multiplied by
+  int ref = -1;                                  // MXFP8: V's reference exponent, none yet
   int all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;  // that every row, and that any row, of the warp's tile may see
   bool fresh = true;
   int64_t unit_first = 0;  // the first step of the unit at `at` that this run holds, counted within the run
@@ -561,22 +628,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           q1 = reinterpret_cast<const uint32_t*>(a.q + ((at.s.q0 + r1 / a.G) * a.Hq + h * a.G + r1 % a.G) * D);
 #pragma unroll
         for (int kk = 0; kk < KS; ++kk) {
-          // bf16: columns 2c, 2c + 1 and 2c + 8, 2c + 9 of the 16; codes: columns 4c, 4c + 2 and 4c + 1, 4c + 3, the
-          // order in which a word of four codes becomes bf16 pairs
+          // bf16: columns 2c, 2c + 1 and 2c + 8, 2c + 9 of the 16; codes: columns 4c .. 4c + 3, a word's
           const int w0 = MX ? kk * 8 + 2 * c : kk * 8 + c, w1 = MX ? w0 + 1 : w0 + 4;
-          uint32_t x0 = q0 ? __ldg(q0 + w0) : 0u, x1 = q1 ? __ldg(q1 + w0) : 0u;
-          uint32_t y0 = q0 ? __ldg(q0 + w1) : 0u, y1 = q1 ? __ldg(q1 + w1) : 0u;
-          if constexpr (MX) {
-            const uint32_t s0 = __byte_perm(x0, y0, 0x5410), s1 = __byte_perm(x1, y1, 0x5410);
-            y0 = __byte_perm(x0, y0, 0x7632);
-            y1 = __byte_perm(x1, y1, 0x7632);
-            x0 = s0;
-            x1 = s1;
+          q[kk][0] = q0 ? __ldg(q0 + w0) : 0u;
+          q[kk][1] = q1 ? __ldg(q1 + w0) : 0u;
+          q[kk][2] = q0 ? __ldg(q0 + w1) : 0u;
+          q[kk][3] = q1 ? __ldg(q1 + w1) : 0u;
+        }
+        f0 = f1 = a.act == JATTN_SOFTMAX ? a.scale_log2 : a.scale;
+        if constexpr (MX) {
+          float x0 = 0.0f, x1 = 0.0f;
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float t = fmaxf(fabsf(query_value<false>(q[kk][i], 0)), fabsf(query_value<false>(q[kk][i], 1)));
+              if (i & 1) x1 = fmaxf(x1, t);
+              else x0 = fmaxf(x0, t);
+            }
           }
-          q[kk][0] = x0;
-          q[kk][1] = x1;
-          q[kk][2] = y0;
-          q[kk][3] = y1;
+          const int e0 = lift_of(x0), e1 = lift_of(x1);
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float g = pow2(i & 1 ? e1 : e0);
+              q[kk][i] = pack_f16x2(query_value<false>(q[kk][i], 0) * g, query_value<false>(q[kk][i], 1) * g);
+            }
+          }
+          f0 *= pow2(-e0);
+          f1 *= pow2(-e1);
+          ref = -1;
+          if (a.act != JATTN_SOFTMAX) m0 = m1 = kLeast;
         }
       }
     }
@@ -607,22 +690,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             mma_bf16(s[nt], q[kk + 1], x[2], x[3]);
           }
         } else {
-          const uint32_t e = scale_word<D>(ksc, r_base + nt * 8 + (lane >> 2));
-          const bool large = __any_sync(0xffffffffu, any_large(e));
+          uint32_t e0, e1;  // of this thread's two columns, keys 2c and 2c + 1
+          scale_words<D>(ksc, r_base + nt * 8 + 2 * c, e0, e1);
 #pragma unroll
           for (int kk = 0; kk < KS; kk += 4) {
             uint32_t x[4];
             ldmatrix4(x, ks + piece_at<D, MX, step>(r, kk + (lane >> 3)));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t eb = same_byte(e, (kk + i) / 2), f = factor2(eb);
-              uint32_t b0 = mul2(codes_lo(x[i]), f), b1 = mul2(codes_hi(x[i]), f);
-              if (large) {
-                const uint32_t g = rest2(eb);
-                b0 = mul2(b0, g);
-                b1 = mul2(b1, g);
-              }
-              mma_bf16(s[nt], q[kk + i], b0, b1);
+            for (int i = 0; i < 4; i += 2) {  // one block of 32 columns
+              float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              uint32_t b0, b1;
+              e4m3x4_to_f16(x[i], b0, b1);
+              mma_f16(t, q[kk + i], b0, b1);
+              e4m3x4_to_f16(x[i + 1], b0, b1);
+              mma_f16(t, q[kk + i + 1], b0, b1);
+              const float g0 = scale_of(e0, (kk + i) / 2), g1 = scale_of(e1, (kk + i) / 2);
+              s[nt][0] = fmaf(t[0], g0, s[nt][0]);
+              s[nt][1] = fmaf(t[1], g1, s[nt][1]);
+              s[nt][2] = fmaf(t[2], g0, s[nt][2]);
+              s[nt][3] = fmaf(t[3], g1, s[nt][3]);
             }
           }
         }
@@ -634,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[nt][e] *= a.scale_log2;
+            s[nt][e] *= e < 2 ? f0 : f1;
             if (partial) {
               const int pos = pos0 + nt * 8 + 2 * c + (e & 1);
               if (pos < (e < 2 ? lo0 : lo1) || pos >= (e < 2 ? hi0 : hi1)) s[nt][e] = -INFINITY;
@@ -654,15 +740,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           m1 = n1;
           l0 *= c0;
           l1 *= c1;
-#pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            o[j][0] *= c0;
-            o[j][1] *= c0;
-            o[j][2] *= c1;
-            o[j][3] *= c1;
-          }
+          scale_rows<D>(o, c0, c1);
         }
-        const float u0 = m0 == -INFINITY ? 0.0f : m0, u1 = m1 == -INFINITY ? 0.0f : m1;
+        const float lift = MX ? kLift : 0.0f;
+        const float u0 = m0 == -INFINITY ? 0.0f : m0 - lift, u1 = m1 == -INFINITY ? 0.0f : m1 - lift;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           s[nt][0] = ex2_approx(s[nt][0] - u0);
@@ -677,9 +758,35 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            s[nt][e] = activate(s[nt][e] * a.scale, a.act);
+            s[nt][e] = activate(s[nt][e] * (e < 2 ? f0 : f1), a.act);
             const int pos = pos0 + nt * 8 + 2 * c + (e & 1);
             if (partial && (pos < (e < 2 ? lo0 : lo1) || pos >= (e < 2 ? hi0 : hi1))) s[nt][e] = 0.0f;
+          }
+        }
+        if constexpr (MX) {  // m is the exponent that the row's weights are held against
+          float t0 = 0.0f, t1 = 0.0f;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            t0 = fmaxf(t0, fmaxf(fabsf(s[nt][0]), fabsf(s[nt][1])));
+            t1 = fmaxf(t1, fmaxf(fabsf(s[nt][2]), fabsf(s[nt][3])));
+          }
+          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
+          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
+          t0 = exponent_of(fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2)));
+          t1 = exponent_of(fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2)));
+          if (__any_sync(0xffffffffu, t0 > m0 + kSlack - 1 || t1 > m1 + kSlack - 1)) {
+            const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
+            scale_rows<D>(o, pow2(static_cast<int>(m0 - n0)), pow2(static_cast<int>(m1 - n1)));
+            m0 = n0;
+            m1 = n1;
+          }
+          const float g0 = pow2(kLift - static_cast<int>(m0)), g1 = pow2(kLift - static_cast<int>(m1));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            s[nt][0] *= g0;
+            s[nt][1] *= g0;
+            s[nt][2] *= g1;
+            s[nt][3] *= g1;
           }
         }
       }
@@ -690,8 +797,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float x = s[2 * g + (i >> 1)][(i & 1) * 2], y = s[2 * g + (i >> 1)][(i & 1) * 2 + 1];
-          ph[i] = pack_bf16x2(x, y);
-          pl[i] = bf16x2_lo(x, y, ph[i]);
+          ph[i] = MX ? pack_f16x2(x, y) : pack_bf16x2(x, y);
+          pl[i] = MX ? f16x2_lo(x, y, ph[i]) : bf16x2_lo(x, y, ph[i]);
         }
         const int r = r_base + g * 16 + (lane & 15);
         if constexpr (!MX) {
@@ -705,39 +812,103 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             mma_bf16(o[j + 1], pl, x[2], x[3]);
           }
         } else {
-          const int rk = r_base + g * 16 + 2 * c;
-          uint32_t e[4];
+          uint32_t e[4];  // keys 2c, 2c + 1, 2c + 8, 2c + 9 of the 16
+          scale_words<D>(vsc, r_base + g * 16 + 2 * c, e[0], e[1]);
+          scale_words<D>(vsc, r_base + g * 16 + 2 * c + 8, e[2], e[3]);
+          if (partial) {
+            // rows outside the sequence hold anything: codes are always finite, exponents become the reference
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e[i] = scale_word<D>(vsc, rk + (i >> 1) * 8 + (i & 1));
-            // rows outside the sequence hold anything: codes are always finite, exponents are made so
-            const int pos = pos0 + g * 16 + 2 * c + (i >> 1) * 8 + (i & 1);
-            if (partial && (pos < at.s.lo || pos >= at.s.hi)) e[i] = 0u;
+            for (int i = 0; i < 4; ++i) {
+              const int pos = pos0 + g * 16 + 2 * c + (i >> 1) * 8 + (i & 1);
+              if (pos < at.s.lo || pos >= at.s.hi) e[i] = max(ref, 0) * 0x01010101u;
+            }
           }
-          const bool large = __any_sync(0xffffffffu, any_large(e[0]) || any_large(e[1]) || any_large(e[2]) || any_large(e[3]));
+          uint32_t fa[D / 32], fb[D / 32], out = 0;  // fp16 exponent fields e - R + 15 of pairs of keys
 #pragma unroll
-          for (int j = 0; j < D / 16; j += 2) {  // one block of 32 columns: pieces j and j + 1
+          for (int j = 0; j < D / 32; ++j) {
+            fa[j] = byte_pair(e[0], e[1], j) - static_cast<uint32_t>((ref - 15) * 0x10001);
+            fb[j] = byte_pair(e[2], e[3], j) - static_cast<uint32_t>((ref - 15) * 0x10001);
+            out |= ((fa[j] - 0x00010001u) | (fb[j] - 0x00010001u)) & 0xfff0fff0u;  // not in 1 .. 16
+          }
+          if (__any_sync(0xffffffffu, out != 0 || ref < 0)) {
+            int top = 0;  // the largest exponent but NaN's
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+#pragma unroll
+              for (int j = 0; j < D / 32; ++j) {
+                const int x = static_cast<int>((e[i] >> (8 * j)) & 0xffu);
+                if (x != 255) top = max(top, x);
+              }
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (ref < 0 || top > ref + 1) {
+              if (ref >= 0) scale_rows<D>(o, pow2(ref - top - 1), pow2(ref - top - 1));
+              ref = top + 1;
+            }
+            if (partial) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int pos = pos0 + g * 16 + 2 * c + (i >> 1) * 8 + (i & 1);
+                if (pos < at.s.lo || pos >= at.s.hi) e[i] = ref * 0x01010101u;
+              }
+            }
+            bool small = false;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+              fa[j] = byte_pair(e[0], e[1], j);
+              fb[j] = byte_pair(e[2], e[3], j);
+              const uint32_t sub = static_cast<uint32_t>((ref - 14) * 0x10001);
+              if (((fa[j] - sub) | (fb[j] - sub)) & 0xfff0fff0u) small = true;
+            }
+            if (__any_sync(0xffffffffu, small)) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float x = s[2 * g + (i >> 1)][(i & 1) * 2], y = s[2 * g + (i >> 1)][(i & 1) * 2 + 1];
+                ph[i] = pack_bf16x2(x, y);
+                pl[i] = bf16x2_lo(x, y, ph[i]);
+              }
+#pragma unroll
+              for (int j = 0; j < D / 32; ++j) {
+                const uint32_t ga = bf16_factors(fa[j], ref), gb = bf16_factors(fb[j], ref);
+                uint32_t x[4];
+                ldmatrix4_trans(x, vs + piece_at<D, MX, step>(r, 2 * j + (lane >> 4)));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t a0 = mul_bf16x2(codes_even(x[2 * i]), ga), a1 = mul_bf16x2(codes_even(x[2 * i + 1]), gb);
+                  const uint32_t b0 = mul_bf16x2(codes_odd(x[2 * i]), ga), b1 = mul_bf16x2(codes_odd(x[2 * i + 1]), gb);
+                  mma_bf16(o[4 * j + 2 * i], ph, a0, a1);
+                  mma_bf16(o[4 * j + 2 * i + 1], ph, b0, b1);
+                  mma_bf16(o[4 * j + 2 * i], pl, a0, a1);
+                  mma_bf16(o[4 * j + 2 * i + 1], pl, b0, b1);
+                }
+              }
+              continue;
+            }
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {
+              fa[j] -= static_cast<uint32_t>((ref - 15) * 0x10001);
+              fb[j] -= static_cast<uint32_t>((ref - 15) * 0x10001);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) {  // one block of 32 columns: two 16-byte pieces
             uint32_t x[4];
-            ldmatrix4_trans(x, vs + piece_at<D, MX, step>(r, j + (lane >> 4)));
-            const uint32_t ea = byte_pair(e[0], e[1], j / 2), eb = byte_pair(e[2], e[3], j / 2);
-            const uint32_t fa = factor2(ea), fb = factor2(eb);
+            ldmatrix4_trans(x, vs + piece_at<D, MX, step>(r, 2 * j + (lane >> 4)));
+            const uint32_t ga = fa[j] << 10, gb = fb[j] << 10;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              uint32_t b[4] = {mul2(codes_lo(x[2 * i]), fa), mul2(codes_lo(x[2 * i + 1]), fb),
-                               mul2(codes_hi(x[2 * i]), fa), mul2(codes_hi(x[2 * i + 1]), fb)};
-              if (large) {
-                const uint32_t ga = rest2(ea), gb = rest2(eb);
-                b[0] = mul2(b[0], ga);
-                b[1] = mul2(b[1], gb);
-                b[2] = mul2(b[2], ga);
-                b[3] = mul2(b[3], gb);
-              }
-              float(&even)[4] = o[2 * (j + i)];
-              float(&odd)[4] = o[2 * (j + i) + 1];
-              mma_bf16(even, ph, b[0], b[1]);
-              mma_bf16(odd, ph, b[2], b[3]);
-              mma_bf16(even, pl, b[0], b[1]);
-              mma_bf16(odd, pl, b[2], b[3]);
+              // a word holds two keys of two columns: (key, column) 00 01 10 11
+              uint32_t a0, a1, b0, b1;
+              e4m3x4_to_f16(__byte_perm(x[2 * i], 0u, 0x3120), a0, b0);
+              e4m3x4_to_f16(__byte_perm(x[2 * i + 1], 0u, 0x3120), a1, b1);
+              a0 = mul_f16x2(a0, ga);
+              b0 = mul_f16x2(b0, ga);
+              a1 = mul_f16x2(a1, gb);
+              b1 = mul_f16x2(b1, gb);
+              mma_f16(o[4 * j + 2 * i], ph, a0, a1);
+              mma_f16(o[4 * j + 2 * i + 1], ph, b0, b1);
+              mma_f16(o[4 * j + 2 * i], pl, a0, a1);
+              mma_f16(o[4 * j + 2 * i + 1], pl, b0, b1);
             }
           }
         }
@@ -757,11 +928,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (unit_ends || run_ends) {
       const bool whole = unit_ends && at.t == static_cast<int>(done - unit_first);  // all of its steps were in this run
       if (live) {
-        repair<D, MX>(a, at, h, row_base, static_cast<int>(done - unit_first) + 1, step, q, o, m0, m1, lo0, hi0, lo1, hi1);
+        // what follows has softmax rows divided by their sum l, here and in the pieces (values near fp32's end would
+        // not survive multiplied by it)
         l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        float w0 = 1.0f, w1 = 1.0f;
+        if (a.act == JATTN_SOFTMAX) {
+          w0 = inverse_sum(l0);
+          w1 = inverse_sum(l1);
+          if (MX) m0 -= kLift, m1 -= kLift;
+        } else if (MX) {
+          w0 = pow2(static_cast<int>(m0) - kLift);
+          w1 = pow2(static_cast<int>(m1) - kLift);
+        }
+        scale_rows<D>(o, w0, w1);
+        if (MX && ref >= 0) scale_rows<D>(o, pow2(ref - 127), pow2(ref - 127));
+        repair<D, MX>(a, at, h, row_base, static_cast<int>(done - unit_first) + 1, step, q, f0, f1, o, m0, m1, w0, w1, lo0,
+                      hi0, lo1, hi1);
+        const float norm = a.act == JATTN_SOFTMAX ? 1.0f : row_norm(a, at.s.n);
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const int64_t r = row_base + (lane >> 2) + half * 8;
@@ -769,13 +955,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           const float m = half ? m1 : m0, l = half ? l1 : l0;
           if (whole) {
             const int64_t out = (at.s.q0 + r / a.G) * a.Hq + h * a.G + r % a.G;
-            const float f = out_factor(a, l, at.s.n);
             if (a.act == JATTN_SOFTMAX && c == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
             uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D);
 #pragma unroll
             for (int j = 0; j < D / 8; j += 2) {
-              const float x0 = o[j][2 * half] * f, x1 = o[j][2 * half + 1] * f;
-              const float y0 = o[j + 1][2 * half] * f, y1 = o[j + 1][2 * half + 1] * f;
+              const float x0 = o[j][2 * half] * norm, x1 = o[j][2 * half + 1] * norm;
+              const float y0 = o[j + 1][2 * half] * norm, y1 = o[j + 1][2 * half + 1] * norm;
               if constexpr (MX) {  // columns 4c, 4c + 2 (even) and 4c + 1, 4c + 3 (odd) of a piece
                 *reinterpret_cast<uint2*>(dst + j * 4 + 2 * c) = make_uint2(pack_bf16x2(x0, y0), pack_bf16x2(x1, y1));
               } else {
@@ -844,12 +1029,12 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(DecodeArgs a, void* 
   const int64_t r0 = static_cast<int64_t>(j.z) * tile;
   const int rows = static_cast<int>(min(static_cast<int64_t>(tile), lq * a.G - r0));
   const int ways = rows >= W ? 1 : W / rows;  // warps per row
-  __shared__ float part[W][D + 1];
+  __shared__ float part[W][D];
   auto slot = [&](int p) { return (static_cast<int64_t>(blockIdx.x) + p) * 2 + (p == 0 ? 1 : 0); };
   for (int base = 0; base < rows; base += W / ways) {
     const int r = base + warp / ways, way = warp % ways;
     const bool on = warp / ways < W / ways && r < rows;
-    float acc[E], l = 0.0f, m = -INFINITY;
+    float acc[E], l = 0.0f, m = -INFINITY, use = 0.0f, inv = 1.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
     if (on) {
@@ -857,16 +1042,22 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(DecodeArgs a, void* 
         for (int p = lane; p < j.x; p += 32) m = fmaxf(m, sc.ml[slot(p) * tile + r].x);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        use = m == -INFINITY ? 0.0f : m;
+        for (int p = lane; p < j.x; p += 32) {
+          const float2 ml = sc.ml[slot(p) * tile + r];
+          l = fmaf(ex2_approx(ml.x - use), ml.y, l);
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        inv = inverse_sum(l);
       }
-      const float use = m == -INFINITY ? 0.0f : m;
 #pragma unroll 4
       for (int p = way; p < j.x; p += ways) {
         const int64_t row = slot(p) * tile + r;
         float w = 1.0f;
         if (a.act == JATTN_SOFTMAX) {
           const float2 ml = sc.ml[row];
-          w = ex2_approx(ml.x - use);
-          l = fmaf(w, ml.y, l);
+          w = ex2_approx(ml.x - use) * ml.y * inv;
         }
         const float* x = sc.acc + row * D + lane * E;
 #pragma unroll
@@ -877,19 +1068,17 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(DecodeArgs a, void* 
       __syncthreads();
 #pragma unroll
       for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
-      if (lane == 0) part[warp][D] = l;
       __syncthreads();
       if (on && way == 0) {
         for (int o = 1; o < ways; ++o) {
 #pragma unroll
           for (int e = 0; e < E; ++e) acc[e] += part[warp + o][lane * E + e];
-          l += part[warp + o][D];
         }
       }
     }
     if (on && way == 0) {
       const int64_t row = r0 + r, out = (q0 + row / a.G) * a.Hq + j.w * a.G + row % a.G;
-      const float f = out_factor(a, l, static_cast<int>(a.kv_lens[j.y]));
+      const float f = a.act == JATTN_SOFTMAX ? 1.0f : row_norm(a, static_cast<int>(a.kv_lens[j.y]));
       if (a.act == JATTN_SOFTMAX && lane == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
       uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D + lane * E);
 #pragma unroll

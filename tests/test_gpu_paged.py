@@ -351,6 +351,56 @@ def test_decode_large_scores(fmt):
     check_decode(J, [1000, 37], [2, 1], 4, 2, 128, 32, fmt, scale=3.0, causal=True, seed=51)
 
 
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+@pytest.mark.parametrize("case", ["v_blocks", "v_grows", "v_huge", "v_tiny", "v_zero", "q_rows", "k_huge"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_mxfp8_dynamic_range(case, act, D):
+    """MXFP8 caches whose blocks lie many powers of two apart (within a row, along the sequence, near both ends of the
+    exponents), and query rows far from 1."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    H, Hq, page, lens = 2, 4, 32, [200, 33, 1, 70]
+    cache, table, pages = fill_cache(J, lens, page, H, D, "mxfp8", seed=101)
+    rng = np.random.default_rng(102)
+    ke, ve = cache.k_scales, cache.v_scales
+    shift = {"v_blocks": lambda: torch.randint(-40, 3, ve.shape, device="cuda"),
+             "v_grows": lambda: torch.arange(ve.shape[0] * page, device="cuda").view(-1, 1, page, 1) // 4,
+             "v_huge": lambda: torch.randint(0, 90, ve.shape, device="cuda"),
+             "v_tiny": lambda: torch.randint(-119, -60, ve.shape, device="cuda"),
+             "v_zero": lambda: -1000 * (torch.rand(ve.shape, device="cuda") < 0.3)}.get(case)
+    live = (ve != 255).clone()
+    if shift is not None:
+        torch.manual_seed(5)
+        moved = (ve.int() + shift()).clamp(0, 246).to(torch.uint8)
+        ve.copy_(torch.where(live, moved, ve))
+        if case == "v_zero":
+            dead = (ve == 0).repeat_interleave(32, -1)
+            cache.v[dead] = 0
+    q = torch.randn(4, Hq, D, generator=torch.Generator().manual_seed(3))
+    kw = dict(act=act)
+    if case == "k_huge":
+        ke.copy_(torch.where(live, ke + 60, ke))
+        q = q * 2.0**-60
+    if case == "q_rows":
+        q = q * torch.tensor([2.0**-125, 1e-3, 1.0, 2.0**10])[:, None, None]
+        kw["scale"] = 2.0**-8
+    q = q.to(torch.bfloat16)
+    # the pages' values again, from the exponents as they are now (NaN places are never live)
+    kp, vp = (np.nan_to_num(R.dequantise(c.cpu().numpy(), e.cpu().numpy())) for c, e in ((cache.k, ke), (cache.v, ve)))
+    o, lse = J.decode(q.cuda(), cache, cu(table), cu(np.array(lens)), **kw)
+    assert J.device_status() == 0
+    ro, rl, to, tl = R.decode(np64(q), kp, vp, table, lens, np.arange(5), **kw)
+    # bf16 subnormals: half a step of 2^-133; scores and values this far down underflow in fp32 terms of 2^-126 each
+    floor = 2.0**-134 + 200 * 2.0**-126
+    top = float(torch.finfo(torch.bfloat16).max)
+    over = np.abs(ro) > top  # beyond bf16 (sums of unscaled weights): infinity, of the same sign
+    assert np.all((np64(o)[over] == np.sign(ro[over]) * np.inf) | (np.abs(np64(o)[over] - ro[over]) <= to[over]))
+    assert np.all(np.abs(np64(o) - ro)[~over] <= (to + floor)[~over])
+    if act == "softmax":
+        assert np.all(np.abs(np64(lse) - rl) <= tl)
+
+
 def test_decode_masked_values_never_reach_a_row():
     """Infinities and NaN in K and V at positions that only later rows may see."""
     import jagged_attention_recsys_gdpa_gb300 as J
