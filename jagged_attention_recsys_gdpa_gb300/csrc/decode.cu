@@ -11,18 +11,20 @@
 // serves the copies: each worker keeps its own ring of stages in shared
 // memory, filled by TMA straight from the pages (a step's rows are one piece of
 // a page, or one piece each of several small pages, issued by a lane each), and the
-// products are warp-level MMAs whose 16 rows hold the query rows; a 128-row
-// tcgen05 tile would be mostly padding here and would need operands and
-// accumulators staged through TMEM for nothing.
+// products are warp-level MMAs with keys (then columns) on their 16 rows and
+// the query rows on their 8 columns; a 128-row tcgen05 tile would be mostly
+// padding here and would stage operands and accumulators through TMEM for
+// nothing.
 //
-// Split. A unit is one (sequence, tile of 16 WM query rows, key/value head);
+// Split. A unit is one (sequence, tile of 8 to 64 query rows, key/value head);
 // its keys go in steps of a fixed number of positions. All units' steps are
-// numbered through, and every worker (WM warps) takes one contiguous run of
-// equal length, wherever it begins and ends: long histories are split, short
-// ones share a worker, and no worker has more than any other. A unit that lies
-// within one run is finished there; of any other, each run writes its piece
-// (m, l, O in fp32) to scratch, and a second kernel joins the pieces in their
-// order. Results do not depend on what runs when.
+// numbered through, and every worker (one warp, or as many as its tile needs)
+// takes one contiguous run of equal length, wherever it begins and ends: long
+// histories are split, short ones share a worker, and no worker has more than any
+// other. A unit that lies within one run is finished there; of any other, each run
+// leaves its piece (m, l and O in fp32), the CTA joins those of its workers, and
+// a second kernel those of several CTAs, always in their order. Results do not
+// depend on what runs when.
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -61,7 +63,7 @@ struct Seq {
   int lo, hi;   // keys that any of its rows may see
   int k0;       // first step's first key
   int steps;    // at least 1: a unit without keys still writes its rows
-  uint32_t units;
+  int tiles;    // of query rows; each comes with every head
 };
 
 __device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b, int tile, int step) {
@@ -84,27 +86,28 @@ __device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b, int tile, int 
   s.k0 = s.lo / step * step;
   s.steps = max(1, (s.hi - s.k0 + step - 1) / step);
   const int64_t rows = static_cast<int64_t>(s.lq) * a.G;
-  s.units = static_cast<uint32_t>((rows + tile - 1) / tile) * a.cache.H;
+  s.tiles = static_cast<int>((rows + tile - 1) / tile);
   return s;
 }
 
-// A worker's place in the numbering of all steps.
+// A worker's place in the numbering of all steps: tiles of a sequence, heads of
+// a tile, steps of a head.
 struct Place {
   Seq s;
-  int b;
-  uint32_t u;  // unit within the sequence: tile * H + head
-  int t;       // step within the unit
+  int b, tile, h, t;
 };
 
 __device__ __forceinline__ void advance(Place& p, const DecodeArgs& a, int tile, int step) {
   if (++p.t < p.s.steps) return;
   p.t = 0;
-  if (++p.u < p.s.units) return;
-  p.u = 0;
+  if (++p.h < a.cache.H) return;
+  p.h = 0;
+  if (++p.tile < p.s.tiles) return;
+  p.tile = 0;
   do {
     if (++p.b >= a.B) return;  // behind the last step: never used
     p.s = seq_of(a, p.b, tile, step);
-  } while (p.s.units == 0);
+  } while (p.s.tiles == 0);
 }
 
 __device__ __forceinline__ int64_t warp_inclusive(int64_t x, int lane) {
@@ -118,13 +121,13 @@ __device__ __forceinline__ int64_t warp_inclusive(int64_t x, int lane) {
 
 // The number of all steps, and the place of step `first`. Every warp of the
 // CTA calls it; each thread sums the steps of one stretch of sequences.
-__device__ __forceinline__ int64_t total_steps(const DecodeArgs& a, int tile, int step, int64_t* start /* [kThreads + 1] */) {
+__device__ __forceinline__ int64_t total_steps(const DecodeArgs& a, int tile, int step, int64_t* start) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t c = (a.B + kThreads - 1) / kThreads;
   int64_t sum = 0;
   for (int64_t b = tid * c; b < min(a.B, (tid + 1) * c); ++b) {
     const Seq s = seq_of(a, static_cast<int>(b), tile, step);
-    sum += static_cast<int64_t>(s.units) * s.steps;
+    sum += static_cast<int64_t>(s.tiles) * a.cache.H * s.steps;
     if (blockIdx.x == 0) {  // the one check of what the host cannot see
       const int64_t n = a.kv_lens[b];
       if (n < 0 || n > a.max_kv) record_error(a.status, JATTN_ERR_LENGTH, 85, static_cast<int>(b));
@@ -159,7 +162,7 @@ __device__ __forceinline__ Place find_place(const DecodeArgs& a, int tile, int s
     int64_t steps = 0;
     if (mine < a.B) {
       const Seq s = seq_of(a, static_cast<int>(mine), tile, step);
-      steps = static_cast<int64_t>(s.units) * s.steps;
+      steps = static_cast<int64_t>(s.tiles) * a.cache.H * s.steps;
     }
     const int64_t end = at + warp_inclusive(steps, lane);
     const uint32_t over = __ballot_sync(0xffffffffu, end > first);
@@ -177,8 +180,10 @@ __device__ __forceinline__ Place find_place(const DecodeArgs& a, int tile, int s
     }
   }
   p.s = seq_of(a, p.b, tile, step);
-  p.u = static_cast<uint32_t>((first - at) / p.s.steps);
+  const int64_t unit = (first - at) / p.s.steps;
   p.t = static_cast<int>((first - at) % p.s.steps);
+  p.tile = static_cast<int>(unit / a.cache.H);
+  p.h = static_cast<int>(unit % a.cache.H);
   return p;
 }
 
@@ -273,27 +278,39 @@ __device__ __forceinline__ uint32_t bf16_factors(uint32_t x, int ref) {
   return r;
 }
 
-// ---------------------------------------------------------------- kernel
-// The exponents of rows r and r + 1 (r even), each in the low bytes of a word.
-template <int D>
-__device__ __forceinline__ void scale_words(uint32_t scales, int r, uint32_t& w0, uint32_t& w1) {
-  if constexpr (D == 128) {
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1) : "r"(scales + r * 4) : "memory");
-  } else {
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(scales + r * 2) : "memory");
-    w1 = w0 >> 16;
+// ---------------------------------------------------------------- rows and columns
+// How a warp's products lie in its lanes (l = lane / 4, c = lane % 4): scores
+// and weights as [16 keys x 8 query rows], keys l and l + 8, rows 2c and 2c + 1;
+// accumulators as [16 columns x 8 rows], rows 2c and 2c + 1 again, columns l and
+// l + 8 of the 16 (bf16) or 2l and 2l + 1 (codes). So a lane holds everything of
+// its rows' maxima, sums and factors, and weights turn into the second product's
+// operand by an 8x8 transpose.
+template <bool MX>
+__device__ __forceinline__ int column(int i, int lane) {  // i = 0, 1
+  return MX ? 2 * (lane >> 2) + i : (lane >> 2) + 8 * i;
+}
+
+template <int NT>
+__device__ __forceinline__ void scale_rows(float (&o)[NT][4], float c0, float c1) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    o[j][0] *= c0;
+    o[j][1] *= c1;
+    o[j][2] *= c0;
+    o[j][3] *= c1;
   }
 }
 
-template <int D>
-__device__ __forceinline__ void scale_rows(float (&o)[D / 8][4], float c0, float c1) {
-#pragma unroll
-  for (int j = 0; j < D / 8; ++j) {
-    o[j][0] *= c0;
-    o[j][1] *= c0;
-    o[j][2] *= c1;
-    o[j][3] *= c1;
-  }
+// Reductions over the eight lanes that hold the same rows.
+__device__ __forceinline__ float rows_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float rows_sum(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 4);
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
 // floor(log2 x) of x >= 0, kLeast for anything smaller.
@@ -301,44 +318,36 @@ constexpr float kLeast = -100.0f;
 __device__ __forceinline__ float exponent_of(float x) {
   return fmaxf(kLeast, static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 127));
 }
-// The power of two that brings a row's largest value (of which each of the four
-// lanes of a quad has its part) to [2^14, 2^15).
-__device__ __forceinline__ int lift_of(float x) {
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-  return x == 0.0f ? 0 : min(14 - (static_cast<int>(__float_as_uint(x) >> 23) - 127), 120);
-}
 
 // Softmax: one over the sum of the weights, 0 for a row that saw no key.
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 // Pointwise activations: the normaliser.
 __device__ __forceinline__ float row_norm(const DecodeArgs& a, int n) {
-  return a.norm_by_lkv && n > 0 ? 1.0f / static_cast<float>(n) : 1.0f;
+  return a.act != JATTN_SOFTMAX && a.norm_by_lkv && n > 0 ? 1.0f / static_cast<float>(n) : 1.0f;
 }
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
 
-// The four columns of a cached row that a thread holds of 16: of bf16 rows 2c,
-// 2c + 1, 2c + 8, 2c + 9; of codes 4c .. 4c + 3.
-template <bool MX>
-__device__ __forceinline__ void columns(const void* buf, const uint8_t* scales, int64_t row, int D, int kk, int c,
-                                        float (&x)[4]) {
-  if constexpr (!MX) {
-    const uint32_t* p = static_cast<const uint32_t*>(buf) + row * (D / 2) + kk * 8;
-    const uint32_t w0 = __ldg(p + c), w1 = __ldg(p + 4 + c);
-    x[0] = __uint_as_float(w0 << 16);
-    x[1] = __uint_as_float(w0 & 0xffff0000u);
-    x[2] = __uint_as_float(w1 << 16);
-    x[3] = __uint_as_float(w1 & 0xffff0000u);
+// The exponents of row r (D = 64: in the low half; what lies above is not used).
+template <int D>
+__device__ __forceinline__ uint32_t scale_word(uint32_t scales, int r) {
+  uint32_t w;
+  if constexpr (D == 128) {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(scales + r * 4) : "memory");
   } else {
-    const uint32_t w = __ldg(static_cast<const uint32_t*>(buf) + row * (D / 4) + kk * 4 + c);
-    const float s = e8m0_value(__ldg(scales + row * (D / 32) + kk / 2));
-    const float2 a = e4m3x2_value(w & 0xffffu), b = e4m3x2_value(w >> 16);
-    x[0] = a.x * s;
-    x[1] = a.y * s;
-    x[2] = b.x * s;
-    x[3] = b.y * s;
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(scales + r * 2) : "memory");
+    w = x;
   }
+  return w;
 }
 
+// One value of a cached row.
+template <bool MX>
+__device__ __forceinline__ float cached(const void* buf, const uint8_t* scales, int64_t row, int D, int col) {
+  const int64_t at = row * D + col;
+  if constexpr (!MX) return __bfloat162float(static_cast<const __nv_bfloat16*>(buf)[at]);
+  return e4m3x2_value(static_cast<const uint8_t*>(buf)[at]).x * e8m0_value(scales[at / 32]);
+}
 template <bool MX>
 __device__ __forceinline__ float query_value(uint32_t pair, int i) {
   if constexpr (MX) {
@@ -352,91 +361,153 @@ __device__ __forceinline__ float query_value(uint32_t pair, int i) {
 // sums over two parts of a weight: where a value that is not finite lies among a
 // piece's keys, the products above give NaN in its column for every row, also
 // for rows whose mask excludes it. Accumulators that are not finite (`bad`, one
-// bit each) are summed again one key at a time, over the allowed keys alone.
+// bit each) are summed again one key at a time, over the allowed keys alone, with
+// weights w 2^(s - m) or w act(s).
 template <int D, bool MX>
-__device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int h, int64_t row_base, int n_steps,
-                                       int step, const uint32_t (&q)[D / 16][4], float f0, float f1,
-                                       float (&o)[D / 8][4], float m0, float m1, float w0, float w1, int lo0,
-                                       int hi0, int lo1, int hi1) {
+__device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int n_steps, int step,
+                                       const uint32_t (&q)[D / 16][2], const float (&f)[2], float (&o)[D / 16][4],
+                                       const float (&m)[2], const float (&w)[2], const int (&lo)[2],
+                                       const int (&hi)[2]) {
   float x = 0.0f;  // stays 0 unless something is not finite
 #pragma unroll
-  for (int j = 0; j < D / 8; ++j) x += (o[j][0] - o[j][0]) + (o[j][1] - o[j][1]) + (o[j][2] - o[j][2]) + (o[j][3] - o[j][3]);
+  for (int j = 0; j < D / 16; ++j) x += (o[j][0] - o[j][0]) + (o[j][1] - o[j][1]) + (o[j][2] - o[j][2]) + (o[j][3] - o[j][3]);
   if (!__any_sync(0xffffffffu, x != 0.0f)) return;
-  const int c = threadIdx.x & 3;
-  uint64_t bad = 0;
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  uint32_t bad = 0;
 #pragma unroll
-  for (int j = 0; j < D / 8; ++j) {
+  for (int j = 0; j < D / 16; ++j) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (o[j][e] - o[j][e] == 0.0f) continue;
-      bad |= uint64_t(1) << (4 * j + e);
+      bad |= 1u << (4 * j + e);
       o[j][e] = 0.0f;
     }
   }
-  const float u0 = m0 == -INFINITY ? 0.0f : m0, u1 = m1 == -INFINITY ? 0.0f : m1;
   const int first = max(at.s.k0 + (at.t - n_steps + 1) * step, at.s.lo), end = min(at.s.k0 + (at.t + 1) * step, at.s.hi);
   for (int pos = first; pos < end; ++pos) {
     int64_t row = cache_row(a.cache, at.b, pos, a.status);
     if (row < 0) continue;
-    row += static_cast<int64_t>(h) << a.cache.page_shift;
-    float s0 = 0.0f, s1 = 0.0f, k[4];
-#pragma unroll
+    row += static_cast<int64_t>(at.h) << a.cache.page_shift;
+    float dot = 0.0f;  // of query row lane / 4
+#pragma unroll 1
     for (int kk = 0; kk < D / 16; ++kk) {
-      columns<MX>(a.cache.k, a.cache.ks, row, D, kk, c, k);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s0 = fmaf(query_value<MX>(q[kk][(e >> 1) * 2], e & 1), k[e], s0);
-        s1 = fmaf(query_value<MX>(q[kk][(e >> 1) * 2 + 1], e & 1), k[e], s1);
+        const int col = 16 * kk + (MX ? 4 * c + e : 2 * c + (e & 1) + 8 * (e >> 1));
+        uint32_t pair = 0;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) pair = i == kk ? q[i][e >> 1] : pair;
+        dot = fmaf(query_value<MX>(pair, e & 1), cached<MX>(a.cache.k, a.cache.ks, row, D, col), dot);
       }
     }
-    s0 += __shfl_xor_sync(0xffffffffu, s0, 1);
-    s1 += __shfl_xor_sync(0xffffffffu, s1, 1);
-    s0 += __shfl_xor_sync(0xffffffffu, s0, 2);
-    s1 += __shfl_xor_sync(0xffffffffu, s1, 2);
-    const bool soft = a.act == JATTN_SOFTMAX;
-    const float p0 = soft ? ex2_approx(s0 * f0 - u0) * w0 : activate(s0 * f0, a.act);
-    const float p1 = soft ? ex2_approx(s1 * f1 - u1) * w1 : activate(s1 * f1, a.act);
-    const bool in0 = pos >= lo0 && pos < hi0, in1 = pos >= lo1 && pos < hi1;
+    dot += __shfl_xor_sync(0xffffffffu, dot, 1);
+    dot += __shfl_xor_sync(0xffffffffu, dot, 2);
+    float p[2];
+    bool in[2];
 #pragma unroll
-    for (int j = 0; j < D / 8; j += 2) {
-      float v[4];
-      columns<MX>(a.cache.v, a.cache.vs, row, D, j / 2, c, v);
+    for (int i = 0; i < 2; ++i) {
+      const float s = __shfl_sync(0xffffffffu, dot, (2 * c + i) * 4) * f[i];
+      p[i] = a.act == JATTN_SOFTMAX ? ex2_approx(s - (m[i] == -INFINITY ? 0.0f : m[i])) * w[i] : activate(s, a.act);
+      in[i] = pos >= lo[i] && pos < hi[i];
+    }
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        // codes: columns 4c, 4c + 2 are the first tile's, 4c + 1, 4c + 3 the second's
-        const int t = j + (MX ? e & 1 : e >> 1), x = MX ? e >> 1 : e & 1;
-        if (in0 && (bad >> (4 * t + x) & 1)) o[t][x] = fmaf(p0, v[e], o[t][x]);
-        if (in1 && (bad >> (4 * t + x + 2) & 1)) o[t][x + 2] = fmaf(p1, v[e], o[t][x + 2]);
+        if (in[e & 1] && (bad >> (4 * j + e) & 1u))
+          o[j][e] = fmaf(p[e & 1], cached<MX>(a.cache.v, a.cache.vs, row, D, 16 * j + column<MX>(e >> 1, lane)), o[j][e]);
       }
     }
   }
 }
 
-// Scratch: for each worker a piece of the unit that its run begins inside of
-// (slot 0) and of the unit that it leaves unfinished (slot 1), and what has to be
-// joined: the unit of slot 1 with the following workers' slots 0.
+// ---------------------------------------------------------------- pieces
+// Scratch. [workers][2]: the piece of the unit that the worker's run begins
+// inside of (slot 0), and of the unit that it begins and leaves unfinished
+// (slot 1). The workers of a CTA meet when they are done and join their pieces:
+// a unit that lies within the CTA is finished there. Of the others [ctas][2]
+// hold the CTA's one piece of a unit from an earlier CTA (0) and of one that goes
+// on (1), and join[cta] = (last CTA of the latter, or -1; sequence, tile, head).
 struct Scratch {
-  float* acc;  // [workers][2][rows][D]
-  float2* ml;  // [workers][2][rows]: m, l
-  int4* join;  // [workers]: pieces (0: nothing to join), sequence, tile, head
+  float* acc;   // [workers][2][tile][D], softmax rows divided by l
+  float2* ml;   // [workers][2][tile]: m, l
+  float* cacc;  // [ctas][2][tile][D]
+  float2* cml;
+  int4* join;
 };
 
-__host__ __device__ inline size_t scratch_bytes(int workers, int rows, int D) {
-  return static_cast<size_t>(workers) * (16 + 2 * static_cast<size_t>(rows) * (8 + 4 * static_cast<size_t>(D)));
+__host__ __device__ inline size_t scratch_bytes(int ctas, int per_cta, int tile, int D) {
+  return static_cast<size_t>(ctas) * (16 + static_cast<size_t>(2 + 2 * per_cta) * tile * (8 + 4 * static_cast<size_t>(D)));
 }
 
-__host__ __device__ inline Scratch carve(void* base, int workers, int rows, int D) {
+__host__ __device__ inline Scratch carve(void* base, int ctas, int per_cta, int tile, int D) {
+  const size_t rows = static_cast<size_t>(ctas) * 2 * tile;
   Scratch s;
   s.acc = static_cast<float*>(base);
-  s.ml = reinterpret_cast<float2*>(s.acc + static_cast<size_t>(workers) * 2 * rows * D);
-  s.join = reinterpret_cast<int4*>(s.ml + static_cast<size_t>(workers) * 2 * rows);
+  s.cacc = s.acc + rows * per_cta * D;
+  s.ml = reinterpret_cast<float2*>(s.cacc + rows * D);
+  s.cml = s.ml + rows * per_cta;
+  s.join = reinterpret_cast<int4*>(s.cml + rows);
   return s;
 }
 
+// One row (E of its columns) of n pieces joined by a warp, the pieces' rows
+// given by row(i): m and l of the whole, and its accumulator divided by l.
+template <int E, typename Row>
+__device__ __forceinline__ void join_row(const DecodeArgs& a, const float* acc, const float2* ml, int D, int col, int n,
+                                         Row row, float (&x)[E], float& m, float& l) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = 0.0f;
+  m = -INFINITY;
+  l = 0.0f;
+  float use = 0.0f, inv = 1.0f;
+  if (a.act == JATTN_SOFTMAX) {
+    for (int i = 0; i < n; ++i) m = fmaxf(m, ml[row(i)].x);
+    use = m == -INFINITY ? 0.0f : m;
+    for (int i = 0; i < n; ++i) l = fmaf(ex2_approx(ml[row(i)].x - use), ml[row(i)].y, l);
+    inv = inverse_sum(l);
+  }
+  for (int i = 0; i < n; ++i) {
+    const int64_t r = row(i);
+    const float w = a.act == JATTN_SOFTMAX ? ex2_approx(ml[r].x - use) * ml[r].y * inv : 1.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = fmaf(w, acc[r * D + col + e], x[e]);
+  }
+}
+
+// A finished row of a unit: query row r of the sequence's first row q0.
+template <int E>
+__device__ __forceinline__ void write_row(const DecodeArgs& a, int64_t q0, int64_t r, int h, int D, int col, int n,
+                                          const float (&x)[E], float m, float l) {
+  const int64_t out = (q0 + r / a.G) * a.Hq + h * a.G + r % a.G;
+  const float f = row_norm(a, n);
+  if (a.act == JATTN_SOFTMAX && col == 0) a.lse[out] = lse_of(m, l);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D + col);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(x[e] * f, x[e + 1] * f);
+}
+
+// Query rows of sequence b: its first and their number (the plan has checked them).
+__device__ __forceinline__ int64_t query_rows(const DecodeArgs& a, int b, int64_t& q0) {
+  q0 = a.q_off != nullptr ? a.q_off[b] : b;
+  return a.q_off != nullptr ? a.q_off[b + 1] - q0 : 1;
+}
+
+// What a worker leaves for its CTA.
+struct Left {
+  int head;        // rows of slot 0 (0: none)
+  int head_ends;   // the unit of slot 0 ends in this run
+  int tail;        // rows of slot 1 (0: none)
+  int b, tile, h;  // of slot 1's unit
+  int last_cta;    // where that unit ends
+};
+
+// ---------------------------------------------------------------- kernel
 // Where the warps of one worker meet once, before its first copy.
 template <int WM>
 __device__ __forceinline__ void worker_barrier(int worker) {
-  asm volatile("bar.sync %0, %1;" ::"r"(worker + 1), "n"(WM * 32) : "memory");
+  if constexpr (WM == 1) __syncwarp();
+  else asm volatile("bar.sync %0, %1;" ::"r"(worker + 1), "n"(WM * 32) : "memory");
 }
 
 // Bounded wait; false (and the status set) when it runs out.
@@ -473,7 +544,7 @@ __device__ __forceinline__ void load_step(const DecodeArgs& a, const CUtensorMap
   if (lane == 0) mbar_arrive_expect_tx(bar, n * static_cast<uint32_t>(box * 2 * (L::row + L::scale)));
   __syncwarp();
   if (!ok) return;
-  const int h = static_cast<int>(p.u % static_cast<uint32_t>(a.cache.H));
+  const int h = p.h;
   const int r = lane * box, y = (p.s.k0 + p.t * step + r) & a.cache.page_mask;
   const uint32_t b = smem_u32(bar);
 #pragma unroll
@@ -506,632 +577,686 @@ __device__ __forceinline__ void clear_rows(uint32_t vs, int pos0, int lo, int hi
   __syncwarp();
 }
 
-template <int D, bool MX, int WM>
+template <int D, bool MX, int NR, int WM>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   void* scratch) {
   using L = Layout<D, MX>;
-  constexpr int step = L::keys * WM, tile = 16 * WM, KS = D / 16, NT = L::sub / 8;
+  constexpr int step = L::keys * WM, tile = 8 * NR * WM, KS = D / 16, MT = L::sub / 16, per_cta = kWarps / WM;
   extern __shared__ unsigned char smem_raw[];
   __shared__ int64_t start[kThreads];
+  __shared__ Left left[per_cta];
   const int tid = threadIdx.x % (WM * 32), lane = threadIdx.x & 31, c = lane & 3;
   const int in_cta = threadIdx.x / (WM * 32), warp_m = tid >> 5;
-  const int workers = gridDim.x * (kWarps / WM), me = blockIdx.x * (kWarps / WM) + in_cta;
-  const Scratch sc = carve(scratch, workers, tile, D);
+  const int workers = gridDim.x * per_cta, me = blockIdx.x * per_cta + in_cta;
+  const Scratch sc = carve(scratch, gridDim.x, per_cta, tile, D);
 
   const int64_t total = total_steps(a, tile, step, start);
   const int64_t share = max((total + workers - 1) / workers, static_cast<int64_t>(kMinSteps));
   const int64_t first = me * share, last = min(first + share, total);  // this worker's run [first, last)
-  if (first >= last) {
-    if (tid == 0) sc.join[me] = make_int4(0, 0, 0, 0);
-    return;
-  }
-  Place in = find_place(a, tile, step, start, first);  // the step that is copied next
-  Place at = in;                                       // the step that is computed next
-  const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t ring = smem + in_cta * (kStages * 8192 * WM);
-  const uint32_t scale_ring = smem + kWarps * kStages * 8192 + in_cta * (kStages * 2 * step * L::scale);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + (smem - smem_u32(smem_raw)) +
-                                               kWarps * kStages * (8192 + 2 * L::keys * L::scale)) +
-                   in_cta * (2 * kStages);
-  uint64_t* empty = full + kStages;
-  if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + s, 1);
-      mbar_init(empty + s, WM);
+  if (tid == 0) left[in_cta] = Left{0, 0, 0, 0, 0, 0, 0};
+  if (first < last) {
+    Place in = find_place(a, tile, step, start, first);  // the step that is copied next
+    Place at = in;                                       // the step that is computed next
+    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t ring = smem + in_cta * (kStages * 8192 * WM);
+    const uint32_t scale_ring = smem + kWarps * kStages * 8192 + in_cta * (kStages * 2 * step * L::scale);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + (smem - smem_u32(smem_raw)) +
+                                                 kWarps * kStages * (8192 + 2 * L::keys * L::scale)) +
+                     in_cta * (2 * kStages);
+    uint64_t* empty = full + kStages;
+    if (tid == 0) {
+      for (int s = 0; s < kStages; ++s) {
+        mbar_init(full + s, 1);
+        mbar_init(empty + s, WM);
+      }
+      fence_mbar_init();
+      fence_proxy_async();
     }
-    fence_mbar_init();
-    fence_proxy_async();
-  }
-  if constexpr (WM == 1) __syncwarp();
-  else worker_barrier<WM>(in_cta);
-  const int box = min(step, a.cache.page_mask + 1);
-  int64_t loaded = 0;  // steps whose copies have been issued (by the worker's first warp)
-  int64_t page = kNoBox;
-  if (warp_m == 0) {
-    page = box_page(a, in, step, box, lane);
+    worker_barrier<WM>(in_cta);
+    const int box = min(step, a.cache.page_mask + 1);
+    const int64_t steps = last - first;
+    int64_t loaded = 0;  // steps whose copies have been issued (by the worker's first warp)
+    int64_t page = kNoBox;
+    if (warp_m == 0) {
+      page = box_page(a, in, step, box, lane);
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-      if (loaded < last - first) {
+      for (int s = 0; s < kStages - 1; ++s) {
+        if (loaded < steps) {
+          load_step<D, MX, WM>(a, &k_map, &v_map, in, page, ring + s * (8192 * WM), scale_ring + s * (2 * step * L::scale),
+                               full + s, box, lane);
+          if (++loaded < steps) {
+            advance(in, a, tile, step);
+            page = box_page(a, in, step, box, lane);
+          }
+        }
+      }
+    }
+
+    uint32_t q[NR][KS][2];
+    float o[NR][KS][4], m[NR][2], l[NR][2];
+    float f[NR][2];             // what the rows' scores are multiplied by
+    int lo[NR][2], hi[NR][2];   // keys that they may see
+    int all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;  // that every row, and that any row, of the warp's may see
+    int ref = -1;               // MXFP8: V's reference exponent, none yet
+    bool live = false;          // the warp's rows hold one of the tile's at least
+    int64_t row_base = 0, rows = 0;
+    bool fresh = true;
+    int n_steps = 0;            // of the unit at `at`, in this run, so far
+    int stage_no = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    int64_t done = 0;
+    for (; done < steps; ++done) {
+      if (!wait_full(a, full + stage_no, phase)) {
+        ok = false;
+        break;
+      }
+      if (warp_m == 0 && loaded < steps) {
+        // the stage after the one in flight was read in the step before this one
+        const int s = stage_no == 0 ? kStages - 1 : stage_no - 1;
+        if constexpr (WM == 1) {
+          __syncwarp();
+        } else {
+          if (loaded >= kStages && !wait_full(a, empty + s, static_cast<uint32_t>(loaded / kStages - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+        }
         load_step<D, MX, WM>(a, &k_map, &v_map, in, page, ring + s * (8192 * WM), scale_ring + s * (2 * step * L::scale),
                              full + s, box, lane);
-        if (++loaded < last - first) {
+        if (++loaded < steps) {
           advance(in, a, tile, step);
           page = box_page(a, in, step, box, lane);
         }
       }
-    }
-  }
 
-  uint32_t q[KS][4];
-  float o[D / 8][4];
-  float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-  int lo0 = 0, hi0 = 0, lo1 = 0, hi1 = 0;        // keys that this thread's two rows may see
-  float f0 = 0.0f, f1 = 0.0f;                    // what its rows' scores are multiplied by
-  int ref = -1;                                  // MXFP8: V's reference exponent, none yet
-  int all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;  // that every row, and that any row, of the warp's tile may see
-  bool fresh = true;
-  int64_t unit_first = 0;  // the first step of the unit at `at` that this run holds, counted within the run
-  int stage_no = 0;
-  uint32_t phase = 0;
-  bool ok = true;
-  int64_t done = 0;
-  for (; done < last - first; ++done) {
-    if (!wait_full(a, full + stage_no, phase)) {
-      ok = false;
-      break;
-    }
-    if (warp_m == 0 && loaded < last - first) {
-      // the stage after the one in flight was read in the step before this one
-      const int s = stage_no == 0 ? kStages - 1 : stage_no - 1;
-      if constexpr (WM == 1) {
-        __syncwarp();
-      } else {
-        if (loaded >= kStages && !wait_full(a, empty + s, static_cast<uint32_t>(loaded / kStages - 1) & 1u)) {
-          ok = false;
-          break;
-        }
-      }
-      load_step<D, MX, WM>(a, &k_map, &v_map, in, page, ring + s * (8192 * WM), scale_ring + s * (2 * step * L::scale),
-                           full + s, box, lane);
-      if (++loaded < last - first) {
-        advance(in, a, tile, step);
-        page = box_page(a, in, step, box, lane);
-      }
-    }
-
-    const int h = static_cast<int>(at.u % static_cast<uint32_t>(a.cache.H));
-    const int64_t rows = static_cast<int64_t>(at.s.lq) * a.G;
-    const int64_t row_base = static_cast<int64_t>(at.u / static_cast<uint32_t>(a.cache.H)) * tile + warp_m * 16;
-    const bool live = row_base < rows;  // the warp's 16 rows hold one at least
-    if (fresh) {
-      fresh = false;
-      unit_first = done;
-      m0 = m1 = -INFINITY;
-      l0 = l1 = 0.0f;
+      if (fresh) {
+        fresh = false;
+        n_steps = 0;
+        ref = -1;
+        rows = static_cast<int64_t>(at.s.lq) * a.G;
+        row_base = static_cast<int64_t>(at.tile) * tile + warp_m * (8 * NR);
+        live = row_base < rows;
+        if (live) {
+          const int delta = at.s.n - at.s.lq;
+          const int64_t end = rows - 1;  // rows behind it take its interval, and zeros for their query
+          key_interval(static_cast<int>(row_base / a.G), delta, at.s.n, a.mask, a.window, any_lo, all_hi);
+          key_interval(static_cast<int>(min(row_base + 8 * NR - 1, end) / a.G), delta, at.s.n, a.mask, a.window, all_lo,
+                       any_hi);
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-      if (live) {
-        const int64_t r0 = row_base + (lane >> 2), r1 = r0 + 8;
-        const int delta = at.s.n - at.s.lq;
-        // rows behind the last one take its interval and zeros for their query
-        const int64_t end = rows - 1;
-        key_interval(static_cast<int>(min(r0, end) / a.G), delta, at.s.n, a.mask, a.window, lo0, hi0);
-        key_interval(static_cast<int>(min(r1, end) / a.G), delta, at.s.n, a.mask, a.window, lo1, hi1);
-        key_interval(static_cast<int>(row_base / a.G), delta, at.s.n, a.mask, a.window, any_lo, all_hi);
-        key_interval(static_cast<int>(min(row_base + 15, end) / a.G), delta, at.s.n, a.mask, a.window, all_lo, any_hi);
-        const uint32_t* q0 = nullptr;
-        const uint32_t* q1 = nullptr;
-        if (r0 < rows)
-          q0 = reinterpret_cast<const uint32_t*>(a.q + ((at.s.q0 + r0 / a.G) * a.Hq + h * a.G + r0 % a.G) * D);
-        if (r1 < rows)
-          q1 = reinterpret_cast<const uint32_t*>(a.q + ((at.s.q0 + r1 / a.G) * a.Hq + h * a.G + r1 % a.G) * D);
-#pragma unroll
-        for (int kk = 0; kk < KS; ++kk) {
-          // bf16: columns 2c, 2c + 1 and 2c + 8, 2c + 9 of the 16; codes: columns 4c .. 4c + 3, a word's
-          const int w0 = MX ? kk * 8 + 2 * c : kk * 8 + c, w1 = MX ? w0 + 1 : w0 + 4;
-          q[kk][0] = q0 ? __ldg(q0 + w0) : 0u;
-          q[kk][1] = q1 ? __ldg(q1 + w0) : 0u;
-          q[kk][2] = q0 ? __ldg(q0 + w1) : 0u;
-          q[kk][3] = q1 ? __ldg(q1 + w1) : 0u;
-        }
-        f0 = f1 = a.act == JATTN_SOFTMAX ? a.scale_log2 : a.scale;
-        if constexpr (MX) {
-          float x0 = 0.0f, x1 = 0.0f;
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float t = fmaxf(fabsf(query_value<false>(q[kk][i], 0)), fabsf(query_value<false>(q[kk][i], 1)));
-              if (i & 1) x1 = fmaxf(x1, t);
-              else x0 = fmaxf(x0, t);
-            }
-          }
-          const int e0 = lift_of(x0), e1 = lift_of(x1);
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float g = pow2(i & 1 ? e1 : e0);
-              q[kk][i] = pack_f16x2(query_value<false>(q[kk][i], 0) * g, query_value<false>(q[kk][i], 1) * g);
-            }
-          }
-          f0 *= pow2(-e0);
-          f1 *= pow2(-e1);
-          ref = -1;
-          if (a.act != JATTN_SOFTMAX) m0 = m1 = kLeast;
-        }
-      }
-    }
-
-    const uint32_t ks = ring + stage_no * (8192 * WM), vs = ks + 4096 * WM;
-    const uint32_t ksc = scale_ring + stage_no * (2 * step * L::scale), vsc = ksc + step * L::scale;
-    const int step0 = at.s.k0 + at.t * step;
-    if constexpr (!MX) {
-      if (live && (step0 < at.s.lo || step0 + step > at.s.hi)) clear_rows<D, WM>(vs, step0, at.s.lo, at.s.hi, lane);
-    }
-#pragma unroll 1
-    for (int sb = 0; sb < step / L::sub; ++sb) {
-      const int r_base = sb * L::sub, pos0 = step0 + r_base;
-      if (!live || pos0 >= any_hi || pos0 + L::sub <= any_lo) continue;
-      const bool partial = pos0 < all_lo || pos0 + L::sub > all_hi;
-      // ---- scores
-      float s[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-        const int r = r_base + nt * 8 + (lane & 7);
-        if constexpr (!MX) {
-#pragma unroll
-          for (int kk = 0; kk < KS; kk += 2) {
-            uint32_t x[4];
-            ldmatrix4(x, ks + piece_at<D, MX, step>(r, 2 * kk + (lane >> 3)));
-            mma_bf16(s[nt], q[kk], x[0], x[1]);
-            mma_bf16(s[nt], q[kk + 1], x[2], x[3]);
-          }
-        } else {
-          uint32_t e0, e1;  // of this thread's two columns, keys 2c and 2c + 1
-          scale_words<D>(ksc, r_base + nt * 8 + 2 * c, e0, e1);
-#pragma unroll
-          for (int kk = 0; kk < KS; kk += 4) {
-            uint32_t x[4];
-            ldmatrix4(x, ks + piece_at<D, MX, step>(r, kk + (lane >> 3)));
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {  // one block of 32 columns
-              float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-              uint32_t b0, b1;
-              e4m3x4_to_f16(x[i], b0, b1);
-              mma_f16(t, q[kk + i], b0, b1);
-              e4m3x4_to_f16(x[i + 1], b0, b1);
-              mma_f16(t, q[kk + i + 1], b0, b1);
-              const float g0 = scale_of(e0, (kk + i) / 2), g1 = scale_of(e1, (kk + i) / 2);
-              s[nt][0] = fmaf(t[0], g0, s[nt][0]);
-              s[nt][1] = fmaf(t[1], g1, s[nt][1]);
-              s[nt][2] = fmaf(t[2], g0, s[nt][2]);
-              s[nt][3] = fmaf(t[3], g1, s[nt][3]);
-            }
-          }
-        }
-      }
-      // ---- weights
-      if (a.act == JATTN_SOFTMAX) {
-        float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[nt][e] *= e < 2 ? f0 : f1;
-            if (partial) {
-              const int pos = pos0 + nt * 8 + 2 * c + (e & 1);
-              if (pos < (e < 2 ? lo0 : lo1) || pos >= (e < 2 ? hi0 : hi1)) s[nt][e] = -INFINITY;
-            }
-          }
-          t0 = fmaxf(t0, fmaxf(s[nt][0], s[nt][1]));
-          t1 = fmaxf(t1, fmaxf(s[nt][2], s[nt][3]));
-        }
-        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
-        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-        t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
-        t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
-        if (__any_sync(0xffffffffu, t0 > m0 + kSlack || t1 > m1 + kSlack)) {
-          const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
-          const float c0 = m0 == n0 ? 1.0f : ex2_approx(m0 - n0), c1 = m1 == n1 ? 1.0f : ex2_approx(m1 - n1);
-          m0 = n0;
-          m1 = n1;
-          l0 *= c0;
-          l1 *= c1;
-          scale_rows<D>(o, c0, c1);
-        }
-        const float lift = MX ? kLift : 0.0f;
-        const float u0 = m0 == -INFINITY ? 0.0f : m0 - lift, u1 = m1 == -INFINITY ? 0.0f : m1 - lift;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          s[nt][0] = ex2_approx(s[nt][0] - u0);
-          s[nt][1] = ex2_approx(s[nt][1] - u0);
-          s[nt][2] = ex2_approx(s[nt][2] - u1);
-          s[nt][3] = ex2_approx(s[nt][3] - u1);
-          l0 += s[nt][0] + s[nt][1];
-          l1 += s[nt][2] + s[nt][3];
-        }
-      } else {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[nt][e] = activate(s[nt][e] * (e < 2 ? f0 : f1), a.act);
-            const int pos = pos0 + nt * 8 + 2 * c + (e & 1);
-            if (partial && (pos < (e < 2 ? lo0 : lo1) || pos >= (e < 2 ? hi0 : hi1))) s[nt][e] = 0.0f;
-          }
-        }
-        if constexpr (MX) {  // m is the exponent that the row's weights are held against
-          float t0 = 0.0f, t1 = 0.0f;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            t0 = fmaxf(t0, fmaxf(fabsf(s[nt][0]), fabsf(s[nt][1])));
-            t1 = fmaxf(t1, fmaxf(fabsf(s[nt][2]), fabsf(s[nt][3])));
-          }
-          t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 1));
-          t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
-          t0 = exponent_of(fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2)));
-          t1 = exponent_of(fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2)));
-          if (__any_sync(0xffffffffu, t0 > m0 + kSlack - 1 || t1 > m1 + kSlack - 1)) {
-            const float n0 = fmaxf(m0, t0), n1 = fmaxf(m1, t1);
-            scale_rows<D>(o, pow2(static_cast<int>(m0 - n0)), pow2(static_cast<int>(m1 - n1)));
-            m0 = n0;
-            m1 = n1;
-          }
-          const float g0 = pow2(kLift - static_cast<int>(m0)), g1 = pow2(kLift - static_cast<int>(m1));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            s[nt][0] *= g0;
-            s[nt][1] *= g0;
-            s[nt][2] *= g1;
-            s[nt][3] *= g1;
-          }
-        }
-      }
-      // ---- O += P V, with P as two bf16 parts (its rounding to one would be as large as the output's own)
-#pragma unroll
-      for (int g = 0; g < L::sub / 16; ++g) {
-        uint32_t ph[4], pl[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = s[2 * g + (i >> 1)][(i & 1) * 2], y = s[2 * g + (i >> 1)][(i & 1) * 2 + 1];
-          ph[i] = MX ? pack_f16x2(x, y) : pack_bf16x2(x, y);
-          pl[i] = MX ? f16x2_lo(x, y, ph[i]) : bf16x2_lo(x, y, ph[i]);
-        }
-        const int r = r_base + g * 16 + (lane & 15);
-        if constexpr (!MX) {
-#pragma unroll
-          for (int j = 0; j < D / 8; j += 2) {
-            uint32_t x[4];
-            ldmatrix4_trans(x, vs + piece_at<D, MX, step>(r, j + (lane >> 4)));
-            mma_bf16(o[j], ph, x[0], x[1]);
-            mma_bf16(o[j + 1], ph, x[2], x[3]);
-            mma_bf16(o[j], pl, x[0], x[1]);
-            mma_bf16(o[j + 1], pl, x[2], x[3]);
-          }
-        } else {
-          uint32_t e[4];  // keys 2c, 2c + 1, 2c + 8, 2c + 9 of the 16
-          scale_words<D>(vsc, r_base + g * 16 + 2 * c, e[0], e[1]);
-          scale_words<D>(vsc, r_base + g * 16 + 2 * c + 8, e[2], e[3]);
-          if (partial) {
-            // rows outside the sequence hold anything: codes are always finite, exponents become the reference
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int pos = pos0 + g * 16 + 2 * c + (i >> 1) * 8 + (i & 1);
-              if (pos < at.s.lo || pos >= at.s.hi) e[i] = max(ref, 0) * 0x01010101u;
-            }
-          }
-          uint32_t fa[D / 32], fb[D / 32], out = 0;  // fp16 exponent fields e - R + 15 of pairs of keys
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) {
-            fa[j] = byte_pair(e[0], e[1], j) - static_cast<uint32_t>((ref - 15) * 0x10001);
-            fb[j] = byte_pair(e[2], e[3], j) - static_cast<uint32_t>((ref - 15) * 0x10001);
-            out |= ((fa[j] - 0x00010001u) | (fb[j] - 0x00010001u)) & 0xfff0fff0u;  // not in 1 .. 16
-          }
-          if (__any_sync(0xffffffffu, out != 0 || ref < 0)) {
-            int top = 0;  // the largest exponent but NaN's
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-#pragma unroll
-              for (int j = 0; j < D / 32; ++j) {
-                const int x = static_cast<int>((e[i] >> (8 * j)) & 0xffu);
-                if (x != 255) top = max(top, x);
-              }
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
-            if (ref < 0 || top > ref + 1) {
-              if (ref >= 0) scale_rows<D>(o, pow2(ref - top - 1), pow2(ref - top - 1));
-              ref = top + 1;
-            }
-            if (partial) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int pos = pos0 + g * 16 + 2 * c + (i >> 1) * 8 + (i & 1);
-                if (pos < at.s.lo || pos >= at.s.hi) e[i] = ref * 0x01010101u;
-              }
-            }
-            bool small = false;
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-              fa[j] = byte_pair(e[0], e[1], j);
-              fb[j] = byte_pair(e[2], e[3], j);
-              const uint32_t sub = static_cast<uint32_t>((ref - 14) * 0x10001);
-              if (((fa[j] - sub) | (fb[j] - sub)) & 0xfff0fff0u) small = true;
-            }
-            if (__any_sync(0xffffffffu, small)) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float x = s[2 * g + (i >> 1)][(i & 1) * 2], y = s[2 * g + (i >> 1)][(i & 1) * 2 + 1];
-                ph[i] = pack_bf16x2(x, y);
-                pl[i] = bf16x2_lo(x, y, ph[i]);
-              }
-#pragma unroll
-              for (int j = 0; j < D / 32; ++j) {
-                const uint32_t ga = bf16_factors(fa[j], ref), gb = bf16_factors(fb[j], ref);
-                uint32_t x[4];
-                ldmatrix4_trans(x, vs + piece_at<D, MX, step>(r, 2 * j + (lane >> 4)));
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const uint32_t a0 = mul_bf16x2(codes_even(x[2 * i]), ga), a1 = mul_bf16x2(codes_even(x[2 * i + 1]), gb);
-                  const uint32_t b0 = mul_bf16x2(codes_odd(x[2 * i]), ga), b1 = mul_bf16x2(codes_odd(x[2 * i + 1]), gb);
-                  mma_bf16(o[4 * j + 2 * i], ph, a0, a1);
-                  mma_bf16(o[4 * j + 2 * i + 1], ph, b0, b1);
-                  mma_bf16(o[4 * j + 2 * i], pl, a0, a1);
-                  mma_bf16(o[4 * j + 2 * i + 1], pl, b0, b1);
-                }
-              }
-              continue;
-            }
-#pragma unroll
-            for (int j = 0; j < D / 32; ++j) {
-              fa[j] -= static_cast<uint32_t>((ref - 15) * 0x10001);
-              fb[j] -= static_cast<uint32_t>((ref - 15) * 0x10001);
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) {  // one block of 32 columns: two 16-byte pieces
-            uint32_t x[4];
-            ldmatrix4_trans(x, vs + piece_at<D, MX, step>(r, 2 * j + (lane >> 4)));
-            const uint32_t ga = fa[j] << 10, gb = fb[j] << 10;
+          for (int g = 0; g < NR; ++g) {
+            const float base = a.act == JATTN_SOFTMAX ? a.scale_log2 : a.scale;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              // a word holds two keys of two columns: (key, column) 00 01 10 11
-              uint32_t a0, a1, b0, b1;
-              e4m3x4_to_f16(__byte_perm(x[2 * i], 0u, 0x3120), a0, b0);
-              e4m3x4_to_f16(__byte_perm(x[2 * i + 1], 0u, 0x3120), a1, b1);
-              a0 = mul_f16x2(a0, ga);
-              b0 = mul_f16x2(b0, ga);
-              a1 = mul_f16x2(a1, gb);
-              b1 = mul_f16x2(b1, gb);
-              mma_f16(o[4 * j + 2 * i], ph, a0, a1);
-              mma_f16(o[4 * j + 2 * i + 1], ph, b0, b1);
-              mma_f16(o[4 * j + 2 * i], pl, a0, a1);
-              mma_f16(o[4 * j + 2 * i + 1], pl, b0, b1);
+              const int64_t r = min(row_base + 8 * g + 2 * c + i, end);
+              key_interval(static_cast<int>(r / a.G), delta, at.s.n, a.mask, a.window, lo[g][i], hi[g][i]);
+              m[g][i] = !MX || a.act == JATTN_SOFTMAX ? -INFINITY : kLeast;
+              l[g][i] = 0.0f;
+              f[g][i] = base;
+            }
+#pragma unroll
+            for (int j = 0; j < KS; ++j) o[g][j][0] = o[g][j][1] = o[g][j][2] = o[g][j][3] = 0.0f;
+            // the query row that this lane holds operands of
+            const int64_t r = row_base + 8 * g + (lane >> 2);
+            const uint32_t* src = nullptr;
+            if (r < rows)
+              src = reinterpret_cast<const uint32_t*>(a.q + ((at.s.q0 + r / a.G) * a.Hq + at.h * a.G + r % a.G) * D);
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+              // bf16: columns 2c, 2c + 1 and 2c + 8, 2c + 9 of the 16; codes: columns 4c .. 4c + 3, a word's
+              const int w0 = MX ? kk * 8 + 2 * c : kk * 8 + c, w1 = MX ? w0 + 1 : w0 + 4;
+              q[g][kk][0] = src ? __ldg(src + w0) : 0u;
+              q[g][kk][1] = src ? __ldg(src + w1) : 0u;
+            }
+            if constexpr (MX) {
+              float x = 0.0f;
+#pragma unroll
+              for (int kk = 0; kk < KS; ++kk) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  x = fmaxf(x, fmaxf(fabsf(query_value<false>(q[g][kk][i], 0)), fabsf(query_value<false>(q[g][kk][i], 1))));
+              }
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+              // the power of two that brings the largest value to [2^14, 2^15)
+              const int e = x == 0.0f ? 0 : min(14 - (static_cast<int>(__float_as_uint(x) >> 23) - 127), 120);
+              const float up = pow2(e);
+#pragma unroll
+              for (int kk = 0; kk < KS; ++kk) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                  q[g][kk][i] = pack_f16x2(query_value<false>(q[g][kk][i], 0) * up, query_value<false>(q[g][kk][i], 1) * up);
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) f[g][i] *= pow2(-__shfl_sync(0xffffffffu, e, (2 * c + i) * 4));
             }
           }
         }
       }
-    }
-    if constexpr (WM > 1) {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty + stage_no);
-    }
-    if (++stage_no == kStages) {
-      stage_no = 0;
-      phase ^= 1u;
-    }
+      ++n_steps;
 
-    // ---- the unit's, or the run's, last step
-    const bool unit_ends = at.t == at.s.steps - 1, run_ends = done == last - first - 1;
-    if (unit_ends || run_ends) {
-      const bool whole = unit_ends && at.t == static_cast<int>(done - unit_first);  // all of its steps were in this run
-      if (live) {
-        // what follows has softmax rows divided by their sum l, here and in the pieces (values near fp32's end would
-        // not survive multiplied by it)
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
-        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-        float w0 = 1.0f, w1 = 1.0f;
-        if (a.act == JATTN_SOFTMAX) {
-          w0 = inverse_sum(l0);
-          w1 = inverse_sum(l1);
-          if (MX) m0 -= kLift, m1 -= kLift;
-        } else if (MX) {
-          w0 = pow2(static_cast<int>(m0) - kLift);
-          w1 = pow2(static_cast<int>(m1) - kLift);
+      const uint32_t ks = ring + stage_no * (8192 * WM), vs = ks + 4096 * WM;
+      const uint32_t ksc = scale_ring + stage_no * (2 * step * L::scale), vsc = ksc + step * L::scale;
+      const int step0 = at.s.k0 + at.t * step;
+      if constexpr (!MX) {
+        if (live && (step0 < at.s.lo || step0 + step > at.s.hi)) clear_rows<D, WM>(vs, step0, at.s.lo, at.s.hi, lane);
+      }
+#pragma unroll 1
+      for (int r_base = 0; r_base < step; r_base += L::sub) {
+        const int pos0 = step0 + r_base;
+        if (!live || pos0 >= any_hi || pos0 + L::sub <= any_lo) continue;
+        const bool partial = pos0 < all_lo || pos0 + L::sub > all_hi;
+        // ---- scores
+        float s[MT][NR][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int r = r_base + mt * 16 + (lane & 15);
+          if constexpr (!MX) {
+            float t[2][NR][4];  // two chains of products
+#pragma unroll
+            for (int g = 0; g < NR; ++g) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) t[0][g][e] = t[1][g][e] = 0.0f;
+            }
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) {
+              uint32_t x[4];
+              ldmatrix4(x, ks + piece_at<D, MX, step>(r, 2 * kk + (lane >> 4)));
+#pragma unroll
+              for (int g = 0; g < NR; ++g) mma_bf16(t[kk & 1][g], x, q[g][kk]);
+            }
+#pragma unroll
+            for (int g = 0; g < NR; ++g) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) s[mt][g][e] = t[0][g][e] + t[1][g][e];
+            }
+          } else {
+            const uint32_t e0 = scale_word<D>(ksc, r_base + mt * 16 + (lane >> 2));
+            const uint32_t e1 = scale_word<D>(ksc, r_base + mt * 16 + 8 + (lane >> 2));
+#pragma unroll
+            for (int kk = 0; kk < KS; kk += 2) {  // one block of 32 columns
+              uint32_t w[4], x[4];
+              ldmatrix4(w, ks + piece_at<D, MX, step>(r, kk + (lane >> 4)));
+              float t[NR][4];
+              e4m3x4_to_f16(w[0], x[0], x[2]);
+              e4m3x4_to_f16(w[1], x[1], x[3]);
+#pragma unroll
+              for (int g = 0; g < NR; ++g) mma_f16_first(t[g], x, q[g][kk]);
+              e4m3x4_to_f16(w[2], x[0], x[2]);
+              e4m3x4_to_f16(w[3], x[1], x[3]);
+#pragma unroll
+              for (int g = 0; g < NR; ++g) mma_f16(t[g], x, q[g][kk + 1]);
+              const float g0 = scale_of(e0, kk / 2), g1 = scale_of(e1, kk / 2);
+#pragma unroll
+              for (int g = 0; g < NR; ++g) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  s[mt][g][e] = kk == 0 ? t[g][e] * (e < 2 ? g0 : g1) : fmaf(t[g][e], e < 2 ? g0 : g1, s[mt][g][e]);
+              }
+            }
+          }
         }
-        scale_rows<D>(o, w0, w1);
-        if (MX && ref >= 0) scale_rows<D>(o, pow2(ref - 127), pow2(ref - 127));
-        repair<D, MX>(a, at, h, row_base, static_cast<int>(done - unit_first) + 1, step, q, f0, f1, o, m0, m1, w0, w1, lo0,
-                      hi0, lo1, hi1);
-        const float norm = a.act == JATTN_SOFTMAX ? 1.0f : row_norm(a, at.s.n);
+        // ---- weights
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int64_t r = row_base + (lane >> 2) + half * 8;
-          if (r >= rows) continue;
-          const float m = half ? m1 : m0, l = half ? l1 : l0;
-          if (whole) {
-            const int64_t out = (at.s.q0 + r / a.G) * a.Hq + h * a.G + r % a.G;
-            if (a.act == JATTN_SOFTMAX && c == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
-            uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D);
+        for (int g = 0; g < NR; ++g) {
+          float t[2] = {-INFINITY, -INFINITY};
+          if (a.act == JATTN_SOFTMAX) {
 #pragma unroll
-            for (int j = 0; j < D / 8; j += 2) {
-              const float x0 = o[j][2 * half] * norm, x1 = o[j][2 * half + 1] * norm;
-              const float y0 = o[j + 1][2 * half] * norm, y1 = o[j + 1][2 * half + 1] * norm;
-              if constexpr (MX) {  // columns 4c, 4c + 2 (even) and 4c + 1, 4c + 3 (odd) of a piece
-                *reinterpret_cast<uint2*>(dst + j * 4 + 2 * c) = make_uint2(pack_bf16x2(x0, y0), pack_bf16x2(x1, y1));
-              } else {
-                dst[j * 4 + c] = pack_bf16x2(x0, x1);
-                dst[j * 4 + 4 + c] = pack_bf16x2(y0, y1);
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                s[mt][g][e] *= f[g][e & 1];
+                if (partial) {
+                  const int pos = pos0 + mt * 16 + (lane >> 2) + 8 * (e >> 1);
+                  if (pos < lo[g][e & 1] || pos >= hi[g][e & 1]) s[mt][g][e] = -INFINITY;
+                }
+                t[e & 1] = fmaxf(t[e & 1], s[mt][g][e]);
+              }
+            }
+            t[0] = rows_max(t[0]);
+            t[1] = rows_max(t[1]);
+            if (__any_sync(0xffffffffu, t[0] > m[g][0] + kSlack || t[1] > m[g][1] + kSlack)) {
+              float x[2];
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float n = fmaxf(m[g][i], t[i]);
+                x[i] = m[g][i] == n ? 1.0f : ex2_approx(m[g][i] - n);
+                m[g][i] = n;
+                l[g][i] *= x[i];
+              }
+              scale_rows(o[g], x[0], x[1]);
+            }
+            const float lift = MX ? kLift : 0.0f;
+            const float use[2] = {m[g][0] == -INFINITY ? 0.0f : m[g][0] - lift, m[g][1] == -INFINITY ? 0.0f : m[g][1] - lift};
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                s[mt][g][e] = ex2_approx(s[mt][g][e] - use[e & 1]);
+                l[g][e & 1] += s[mt][g][e];
               }
             }
           } else {
-            // slot 1 if the unit's first step is in this run
-            const int slot = at.t == static_cast<int>(done - unit_first) ? 1 : 0;
-            const int64_t row = (static_cast<int64_t>(me) * 2 + slot) * tile + warp_m * 16 + (lane >> 2) + half * 8;
-            if (c == 0) sc.ml[row] = make_float2(m, l);
-            float* dst = sc.acc + row * D;
 #pragma unroll
-            for (int j = 0; j < D / 8; j += 2) {
-              const float* x = &o[j][2 * half];
-              const float* y = &o[j + 1][2 * half];
-              if constexpr (MX) {
-                *reinterpret_cast<float4*>(dst + j * 8 + 4 * c) = make_float4(x[0], y[0], x[1], y[1]);
-              } else {
-                *reinterpret_cast<float2*>(dst + j * 8 + 2 * c) = make_float2(x[0], x[1]);
-                *reinterpret_cast<float2*>(dst + j * 8 + 8 + 2 * c) = make_float2(y[0], y[1]);
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                s[mt][g][e] = activate(s[mt][g][e] * f[g][e & 1], a.act);
+                const int pos = pos0 + mt * 16 + (lane >> 2) + 8 * (e >> 1);
+                if (partial && (pos < lo[g][e & 1] || pos >= hi[g][e & 1])) s[mt][g][e] = 0.0f;
+                t[e & 1] = fmaxf(t[e & 1], fabsf(s[mt][g][e]));
+              }
+            }
+            if constexpr (MX) {  // m is the exponent that the row's weights are held against
+              t[0] = exponent_of(rows_max(t[0]));
+              t[1] = exponent_of(rows_max(t[1]));
+              if (__any_sync(0xffffffffu, t[0] > m[g][0] + kSlack - 1 || t[1] > m[g][1] + kSlack - 1)) {
+                const float n0 = fmaxf(m[g][0], t[0]), n1 = fmaxf(m[g][1], t[1]);
+                scale_rows(o[g], pow2(static_cast<int>(m[g][0] - n0)), pow2(static_cast<int>(m[g][1] - n1)));
+                m[g][0] = n0;
+                m[g][1] = n1;
+              }
+              const float up[2] = {pow2(kLift - static_cast<int>(m[g][0])), pow2(kLift - static_cast<int>(m[g][1]))};
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[mt][g][e] *= up[e & 1];
+              }
+            }
+          }
+        }
+        // ---- O += V^T P^T, with P as two parts (its rounding to one would be as large as the output's own)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t ph[NR][2], pl[NR][2];
+#pragma unroll
+          for (int g = 0; g < NR; ++g) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float x = s[mt][g][2 * i], y = s[mt][g][2 * i + 1];
+              const uint32_t hi2 = MX ? pack_f16x2(x, y) : pack_bf16x2(x, y);
+              ph[g][i] = movmatrix(hi2);
+              pl[g][i] = movmatrix(MX ? f16x2_lo(x, y, hi2) : bf16x2_lo(x, y, hi2));
+            }
+          }
+          // rows (keys) and pieces of the transposed loads: keys 0-7 of two pieces, then keys 8-15
+          const int r = r_base + mt * 16 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+          if constexpr (!MX) {
+#pragma unroll
+            for (int j = 0; j < KS; ++j) {
+              uint32_t x[4];
+              ldmatrix4_trans(x, vs + piece_at<D, MX, step>(r, 2 * j + half));
+#pragma unroll
+              for (int g = 0; g < NR; ++g) {
+                mma_bf16(o[g][j], x, ph[g]);
+                mma_bf16(o[g][j], x, pl[g]);
+              }
+            }
+          } else {
+            uint32_t e[4];  // keys 2c, 2c + 1, 2c + 8, 2c + 9 of the 16
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              e[i] = scale_word<D>(vsc, r_base + mt * 16 + 2 * c + (i >> 1) * 8 + (i & 1));
+              if (D == 64) e[i] |= e[i] << 16;
+            }
+            if (partial) {
+              // rows outside the sequence hold anything: codes are always finite, exponents become the reference
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int pos = pos0 + mt * 16 + 2 * c + (i >> 1) * 8 + (i & 1);
+                if (pos < at.s.lo || pos >= at.s.hi) e[i] = max(ref, 0) * 0x01010101u;
+              }
+            }
+            // e - (R - 14), byte by byte: 0 .. 15 where fp16 factors do (a byte below borrows and ends up far above)
+            uint32_t d[4], out = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              d[i] = e[i] - static_cast<uint32_t>(ref - 14) * 0x01010101u;
+              out |= d[i];
+            }
+            bool small = false;
+            if (__any_sync(0xffffffffu, (out & 0xf0f0f0f0u) != 0 || ref < 0)) {
+              int top = 0;  // the largest exponent but NaN's
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int x = static_cast<int>((e[i] >> (8 * j)) & 0xffu);
+                  if (x != 255) top = max(top, x);
+                }
+              }
+              top = __reduce_max_sync(0xffffffffu, top);
+              if (ref < 0 || top > ref + 1) {
+                top = max(top, 14);  // R - 14 is no negative byte
+                if (ref >= 0) {
+#pragma unroll
+                  for (int g = 0; g < NR; ++g) scale_rows(o[g], pow2(ref - top - 1), pow2(ref - top - 1));
+                }
+                ref = top + 1;
+              }
+              out = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int pos = pos0 + mt * 16 + 2 * c + (i >> 1) * 8 + (i & 1);
+                if (partial && (pos < at.s.lo || pos >= at.s.hi)) e[i] = ref * 0x01010101u;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int x = static_cast<int>((e[i] >> (8 * j)) & 0xffu) - (ref - 14);
+                  out |= static_cast<uint32_t>(x);
+                }
+                d[i] = e[i] - static_cast<uint32_t>(ref - 14) * 0x01010101u;
+              }
+              small = __any_sync(0xffffffffu, (out & 0xfffffff0u) != 0);
+            }
+            if (small) {  // bf16 products for these 16 keys
+#pragma unroll
+              for (int g = 0; g < NR; ++g) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const float x = s[mt][g][2 * i], y = s[mt][g][2 * i + 1];
+                  const uint32_t hi2 = pack_bf16x2(x, y);
+                  ph[g][i] = movmatrix(hi2);
+                  pl[g][i] = movmatrix(bf16x2_lo(x, y, hi2));
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < D / 32; ++j) {
+                const uint32_t fa = bf16_factors(byte_pair(e[0], e[1], j), ref), fb = bf16_factors(byte_pair(e[2], e[3], j), ref);
+                uint32_t w[4];
+                ldmatrix4_trans(w, vs + piece_at<D, MX, step>(r, 2 * j + half));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t x[4] = {mul_bf16x2(codes_even(w[i]), fa), mul_bf16x2(codes_odd(w[i]), fa),
+                                         mul_bf16x2(codes_even(w[2 + i]), fb), mul_bf16x2(codes_odd(w[2 + i]), fb)};
+#pragma unroll
+                  for (int g = 0; g < NR; ++g) {
+                    mma_bf16(o[g][2 * j + i], x, ph[g]);
+                    mma_bf16(o[g][2 * j + i], x, pl[g]);
+                  }
+                }
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < D / 32; ++j) {  // one block of 32 columns: two 16-byte pieces
+                // fp16 2^(e - R): exponent field e - R + 15
+                const uint32_t fa = byte_pair(d[0], d[1], j) * 1024u + 0x04000400u;
+                const uint32_t fb = byte_pair(d[2], d[3], j) * 1024u + 0x04000400u;
+                uint32_t w[4];
+                ldmatrix4_trans(w, vs + piece_at<D, MX, step>(r, 2 * j + half));
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  // a word holds two keys of two columns: (key, column) 00 01 10 11
+                  uint32_t x[4];
+                  e4m3x4_to_f16(__byte_perm(w[i], 0u, 0x3120), x[0], x[1]);
+                  e4m3x4_to_f16(__byte_perm(w[2 + i], 0u, 0x3120), x[2], x[3]);
+                  x[0] = mul_f16x2(x[0], fa);
+                  x[1] = mul_f16x2(x[1], fa);
+                  x[2] = mul_f16x2(x[2], fb);
+                  x[3] = mul_f16x2(x[3], fb);
+#pragma unroll
+                  for (int g = 0; g < NR; ++g) {
+                    mma_f16(o[g][2 * j + i], x, ph[g]);
+                    mma_f16(o[g][2 * j + i], x, pl[g]);
+                  }
+                }
               }
             }
           }
         }
       }
-      if (run_ends && tid == 0) {
-        int4 j = make_int4(0, 0, 0, 0);
-        if (!unit_ends && at.t == static_cast<int>(done - unit_first)) {  // begun here, finished by later workers
-          const int64_t end = last + (at.s.steps - 1 - at.t);             // number of the unit's end
-          j = make_int4(static_cast<int>((end - 1) / share - me) + 1, at.b,
-                        static_cast<int>(at.u / static_cast<uint32_t>(a.cache.H)), h);
-        }
-        sc.join[me] = j;
+      if constexpr (WM > 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + stage_no);
       }
-      fresh = true;
+      if (++stage_no == kStages) {
+        stage_no = 0;
+        phase ^= 1u;
+      }
+
+      // ---- the unit's, or the run's, last step
+      const bool unit_ends = at.t == at.s.steps - 1, run_ends = done == steps - 1;
+      if (unit_ends || run_ends) {
+        const bool begun = at.t == n_steps - 1;  // the unit's first step is in this run
+        const int slot = begun ? 1 : 0;
+        if (live) {
+          const float norm = row_norm(a, at.s.n);
+#pragma unroll
+          for (int g = 0; g < NR; ++g) {
+            // softmax rows are divided by their sum l here, in the pieces too (values near fp32's end would not
+            // survive multiplied by it)
+            float w[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              l[g][i] = rows_sum(l[g][i]);
+              w[i] = a.act == JATTN_SOFTMAX ? inverse_sum(l[g][i]) : MX ? pow2(static_cast<int>(m[g][i]) - kLift) : 1.0f;
+              if (MX && a.act == JATTN_SOFTMAX) m[g][i] -= kLift;
+            }
+            scale_rows(o[g], w[0], w[1]);
+            if (MX && ref >= 0) scale_rows(o[g], pow2(ref - 127), pow2(ref - 127));
+            repair<D, MX>(a, at, n_steps, step, q[g], f[g], o[g], m[g], w, lo[g], hi[g]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int64_t r = row_base + 8 * g + 2 * c + i;
+              if (r >= rows) continue;
+              if (unit_ends && begun) {  // all of it was in this run
+                const int64_t out = (at.s.q0 + r / a.G) * a.Hq + at.h * a.G + r % a.G;
+                if (a.act == JATTN_SOFTMAX && lane < 4) a.lse[out] = lse_of(m[g][i], l[g][i]);
+                __nv_bfloat16* dst = a.o + out * D;
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                  const float x = o[g][j][i] * norm, y = o[g][j][2 + i] * norm;
+                  if constexpr (MX) {
+                    *reinterpret_cast<uint32_t*>(dst + 16 * j + column<MX>(0, lane)) = pack_bf16x2(x, y);
+                  } else {
+                    dst[16 * j + column<MX>(0, lane)] = __float2bfloat16(x);
+                    dst[16 * j + column<MX>(1, lane)] = __float2bfloat16(y);
+                  }
+                }
+              } else {
+                const int64_t row = (static_cast<int64_t>(me) * 2 + slot) * tile + warp_m * (8 * NR) + 8 * g + 2 * c + i;
+                if (lane < 4) sc.ml[row] = make_float2(m[g][i], l[g][i]);
+                float* dst = sc.acc + row * D;
+#pragma unroll
+                for (int j = 0; j < KS; ++j) {
+                  if constexpr (MX) {
+                    *reinterpret_cast<float2*>(dst + 16 * j + column<MX>(0, lane)) = make_float2(o[g][j][i], o[g][j][2 + i]);
+                  } else {
+                    dst[16 * j + column<MX>(0, lane)] = o[g][j][i];
+                    dst[16 * j + column<MX>(1, lane)] = o[g][j][2 + i];
+                  }
+                }
+              }
+            }
+          }
+        }
+        if (tid == 0 && !(unit_ends && begun)) {
+          const int n = static_cast<int>(min(static_cast<int64_t>(tile), rows - static_cast<int64_t>(at.tile) * tile));
+          Left& x = left[in_cta];
+          if (begun) {
+            const int64_t end = last + (at.s.steps - 1 - at.t);  // number of the unit's end
+            x.tail = n;
+            x.b = at.b;
+            x.tile = at.tile;
+            x.h = at.h;
+            x.last_cta = static_cast<int>((end - 1) / share / per_cta);
+          } else {
+            x.head = n;
+            x.head_ends = unit_ends;
+          }
+        }
+        fresh = true;
+      }
+      if (!run_ends) advance(at, a, tile, step);
     }
-    if (!run_ends) advance(at, a, tile, step);
-  }
-  if (!ok) {
-    // a wait ran out: nothing to join here, and no copy may be in flight when the CTA ends
-    if (tid == 0) sc.join[me] = make_int4(0, 0, 0, 0);
-    if (warp_m == 0) {
-      for (int64_t i = done; i < loaded; ++i)
-        (void)wait_full(a, full + static_cast<int>(i % kStages), static_cast<uint32_t>(i / kStages) & 1u);
+    if (!ok) {
+      // a wait ran out: nothing to join here, and no copy may be in flight when the CTA ends
+      if (tid == 0) left[in_cta] = Left{0, 0, 0, 0, 0, 0, 0};
+      if (warp_m == 0) {
+        for (int64_t i = done; i < loaded; ++i)
+          (void)wait_full(a, full + static_cast<int>(i % kStages), static_cast<uint32_t>(i / kStages) & 1u);
+      }
     }
   }
+
+  // ---- the CTA's pieces: chains of one unit's, each from the incoming unit's (worker 0's slot 0) or from a unit that a
+  // worker began and left (its slot 1), on through the following workers' slots 0
+  __syncthreads();
+  constexpr int E = D / 32;
+  const int warp = threadIdx.x >> 5;
+  int4 going_on = make_int4(-1, 0, 0, 0);
+  for (int begin = -1; begin < per_cta; ++begin) {
+    const int w0 = max(begin, 0), s0 = begin < 0 ? 0 : 1;
+    const Left unit = left[w0];
+    const int n = s0 ? unit.tail : unit.head;
+    if (n == 0) continue;
+    bool ends = s0 == 0 && unit.head_ends;
+    int len = 1;
+    for (int x = w0 + 1; x < per_cta && !ends && left[x].head > 0; ++x) {
+      ++len;
+      ends = left[x].head_ends;
+    }
+    for (int r = warp; r < n; r += kWarps) {
+      const int64_t w_first = static_cast<int64_t>(blockIdx.x) * per_cta + w0;
+      const auto row = [&](int i) { return ((w_first + i) * 2 + (i == 0 ? s0 : 0)) * tile + r; };
+      float x[E], mj, lj;
+      join_row<E>(a, sc.acc, sc.ml, D, lane * E, len, row, x, mj, lj);
+      if (s0 == 1 && ends) {
+        int64_t q0;
+        (void)query_rows(a, unit.b, q0);
+        write_row<E>(a, q0, static_cast<int64_t>(unit.tile) * tile + r, unit.h, D, lane * E,
+                     static_cast<int>(a.kv_lens[unit.b]), x, mj, lj);
+      } else {
+        const int64_t to = (static_cast<int64_t>(blockIdx.x) * 2 + s0) * tile + r;
+        if (lane == 0) sc.cml[to] = make_float2(mj, lj);
+#pragma unroll
+        for (int e = 0; e < E; ++e) sc.cacc[to * D + lane * E + e] = x[e];
+      }
+    }
+    if (s0 == 1 && !ends) going_on = make_int4(unit.last_cta, unit.b, unit.tile, unit.h);
+  }
+  if (threadIdx.x == 0) sc.join[blockIdx.x] = going_on;
 }
 
-// One CTA per worker: joins the pieces of the unit that the worker left
-// unfinished, if it did. A warp takes a row, or a share of a row's pieces; its
-// lanes take the columns.
+// One CTA per CTA of the kernel above: joins the pieces of the unit that went on
+// from it, if one did. D / 4 threads take a row, or a share of a row's pieces.
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(DecodeArgs a, void* scratch, int workers, int tile) {
-  const Scratch sc = carve(scratch, workers, tile, D);
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(DecodeArgs a, void* scratch, int per_cta, int tile) {
+  constexpr int lanes = D / 4, slots = kJoinThreads / lanes;
+  __shared__ float weight[slots][kMaxCtas];
+  __shared__ float2 row_ml[slots];
+  __shared__ float4 part[kJoinThreads];
+  const Scratch sc = carve(scratch, gridDim.x, per_cta, tile, D);
   const int4 j = sc.join[blockIdx.x];
-  if (j.x == 0) return;
-  constexpr int E = D / 32, W = kJoinThreads / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t q0 = j.y, lq = 1;
-  if (a.q_off != nullptr) {
-    q0 = a.q_off[j.y];
-    lq = a.q_off[j.y + 1] - q0;
-  }
+  if (j.x < 0) return;
+  const int n = j.x - static_cast<int>(blockIdx.x) + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int slot = threadIdx.x / lanes, col = (threadIdx.x % lanes) * 4;
+  int64_t q0;
   const int64_t r0 = static_cast<int64_t>(j.z) * tile;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(tile), lq * a.G - r0));
-  const int ways = rows >= W ? 1 : W / rows;  // warps per row
-  __shared__ float part[W][D];
-  auto slot = [&](int p) { return (static_cast<int64_t>(blockIdx.x) + p) * 2 + (p == 0 ? 1 : 0); };
-  for (int base = 0; base < rows; base += W / ways) {
-    const int r = base + warp / ways, way = warp % ways;
-    const bool on = warp / ways < W / ways && r < rows;
-    float acc[E], l = 0.0f, m = -INFINITY, use = 0.0f, inv = 1.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    if (on) {
-      if (a.act == JATTN_SOFTMAX) {
-        for (int p = lane; p < j.x; p += 32) m = fmaxf(m, sc.ml[slot(p) * tile + r].x);
+  const int rows = static_cast<int>(min(static_cast<int64_t>(tile), query_rows(a, j.y, q0) * a.G - r0));
+  const auto place = [&](int i, int r) { return ((static_cast<int64_t>(blockIdx.x) + i) * 2 + (i == 0 ? 1 : 0)) * tile + r; };
+  for (int base = 0; base < rows; base += slots) {
+    const int now = min(slots, rows - base), ways = slots / now;
+    if (a.act == JATTN_SOFTMAX) {
+      for (int r = warp; r < now; r += kJoinThreads / 32) {
+        float m = -INFINITY, l = 0.0f;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, sc.cml[place(i, base + r)].x);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        use = m == -INFINITY ? 0.0f : m;
-        for (int p = lane; p < j.x; p += 32) {
-          const float2 ml = sc.ml[slot(p) * tile + r];
-          l = fmaf(ex2_approx(ml.x - use), ml.y, l);
+        const float use = m == -INFINITY ? 0.0f : m;
+        for (int i = lane; i < n; i += 32) {
+          const float2 ml = sc.cml[place(i, base + r)];
+          const float w = ex2_approx(ml.x - use) * ml.y;
+          weight[r][i] = w;
+          l += w;
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        inv = inverse_sum(l);
-      }
-#pragma unroll 4
-      for (int p = way; p < j.x; p += ways) {
-        const int64_t row = slot(p) * tile + r;
-        float w = 1.0f;
-        if (a.act == JATTN_SOFTMAX) {
-          const float2 ml = sc.ml[row];
-          w = ex2_approx(ml.x - use) * ml.y * inv;
-        }
-        const float* x = sc.acc + row * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(w, x[e], acc[e]);
+        if (lane == 0) row_ml[r] = make_float2(m, l);
       }
     }
-    if (ways > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < E; ++e) part[warp][lane * E + e] = acc[e];
-      __syncthreads();
-      if (on && way == 0) {
-        for (int o = 1; o < ways; ++o) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += part[warp + o][lane * E + e];
-        }
+    __syncthreads();
+    const int r = slot / ways, way = slot % ways;
+    const bool on = r < now;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (on) {
+      const float inv = a.act == JATTN_SOFTMAX ? inverse_sum(row_ml[r].y) : 1.0f;
+#pragma unroll 8
+      for (int i = way; i < n; i += ways) {
+        const float w = a.act == JATTN_SOFTMAX ? weight[r][i] * inv : 1.0f;
+        const float4 y = *reinterpret_cast<const float4*>(sc.cacc + place(i, base + r) * D + col);
+        x.x = fmaf(w, y.x, x.x);
+        x.y = fmaf(w, y.y, x.y);
+        x.z = fmaf(w, y.z, x.z);
+        x.w = fmaf(w, y.w, x.w);
       }
     }
+    part[threadIdx.x] = x;
+    __syncthreads();
     if (on && way == 0) {
-      const int64_t row = r0 + r, out = (q0 + row / a.G) * a.Hq + j.w * a.G + row % a.G;
-      const float f = a.act == JATTN_SOFTMAX ? 1.0f : row_norm(a, static_cast<int>(a.kv_lens[j.y]));
-      if (a.act == JATTN_SOFTMAX && lane == 0) a.lse[out] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D + lane * E);
-#pragma unroll
-      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * f, acc[e + 1] * f);
+      for (int o = 1; o < ways; ++o) {
+        const float4 y = part[threadIdx.x + o * lanes];
+        x.x += y.x;
+        x.y += y.y;
+        x.z += y.z;
+        x.w += y.w;
+      }
+      const float v[4] = {x.x, x.y, x.z, x.w};
+      const float2 ml = a.act == JATTN_SOFTMAX ? row_ml[r] : make_float2(0.0f, 1.0f);
+      write_row<4>(a, q0, r0 + base + r, j.w, D, col, static_cast<int>(a.kv_lens[j.y]), v, ml.x, ml.y);
     }
+    __syncthreads();
   }
 }
 
 struct Shape {
-  int wm, ctas, workers, tile;
+  int nr, wm, ctas, tile;
 };
 
-// Warps per worker: one row tile of 16 rows each, as many as an average
-// sequence has rows per key/value head (at most four: 64 rows). CTAs: two per
-// SM, fewer where the largest possible number of steps leaves some without work.
+// A worker's tile holds an average sequence's rows per key/value head: 8 or 16
+// in one warp, 32 and 64 in two and four. CTAs: two per SM, fewer where the
+// largest possible number of steps leaves some without work.
 Shape shape_of(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H) {
   Shape s;
   const int64_t rows = (total_q + B - 1) / B * G;
+  s.nr = rows <= 8 ? 1 : 2;
   s.wm = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  s.tile = 16 * s.wm;
+  s.tile = 8 * s.nr * s.wm;
   const int64_t step = 4096 / (D * (mx ? 1 : 2)) * s.wm;
   // tiles of all sequences: each has at most one that is not full
   const int64_t tiles = total_q * G / s.tile + (total_q < B ? total_q : B);
-  const int64_t per_worker = kMinSteps, per_cta = per_worker * (kWarps / s.wm);
+  const int64_t per_cta = kMinSteps * (kWarps / s.wm);
   const double steps = static_cast<double>(tiles) * H * static_cast<double>((max_kv + step - 1) / step + 2);
   s.ctas = steps / per_cta >= kMaxCtas ? kMaxCtas : static_cast<int>(steps / per_cta) + 1;
-  s.workers = s.ctas * (kWarps / s.wm);
   return s;
 }
 
-template <int D, bool MX, int WM>
+template <int D, bool MX, int NR, int WM>
 cudaError_t launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, const Shape& s, void* scratch,
                    cudaStream_t stream) {
   constexpr int smem = smem_bytes<D, MX>();
-  const cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, MX, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, MX, NR, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  decode_kernel<D, MX, WM><<<s.ctas, kThreads, smem, stream>>>(a, k, v, scratch);
+  decode_kernel<D, MX, NR, WM><<<s.ctas, kThreads, smem, stream>>>(a, k, v, scratch);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  join_kernel<D><<<s.ctas, kJoinThreads, 0, stream>>>(a, scratch, kWarps / WM, s.tile);
   return cudaGetLastError();
 }
 
 template <int D, bool MX>
-cudaError_t launch_wm(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, const Shape& s, void* scratch,
-                      cudaStream_t stream) {
-  if (s.wm == 1) return launch<D, MX, 1>(a, k, v, s, scratch, stream);
-  if (s.wm == 2) return launch<D, MX, 2>(a, k, v, s, scratch, stream);
-  return launch<D, MX, 4>(a, k, v, s, scratch, stream);
+cudaError_t launch_shape(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, const Shape& s, void* scratch,
+                         cudaStream_t stream) {
+  if (s.nr == 1) return launch<D, MX, 1, 1>(a, k, v, s, scratch, stream);
+  if (s.wm == 1) return launch<D, MX, 2, 1>(a, k, v, s, scratch, stream);
+  if (s.wm == 2) return launch<D, MX, 2, 2>(a, k, v, s, scratch, stream);
+  return launch<D, MX, 2, 4>(a, k, v, s, scratch, stream);
 }
 
 }  // namespace
 
 size_t decode_scratch_bytes(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H) {
   const Shape s = shape_of(D, mx, B, total_q, max_kv, G, H);
-  return scratch_bytes(s.workers, s.tile, D);
+  return scratch_bytes(s.ctas, kWarps / s.wm, s.tile, D);
 }
 
 int decode_box_rows(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H, int page_size) {
@@ -1143,13 +1268,8 @@ int decode_box_rows(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, 
 cudaError_t launch_decode(int D, bool mx, const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, void* scratch,
                           cudaStream_t stream) {
   const Shape s = shape_of(D, mx, a.B, a.total_q, a.max_kv, a.G, a.cache.H);
-  cudaError_t e;
-  if (D == 64) e = mx ? launch_wm<64, true>(a, k, v, s, scratch, stream) : launch_wm<64, false>(a, k, v, s, scratch, stream);
-  else e = mx ? launch_wm<128, true>(a, k, v, s, scratch, stream) : launch_wm<128, false>(a, k, v, s, scratch, stream);
-  if (e != cudaSuccess) return e;
-  const auto join = D == 64 ? join_kernel<64> : join_kernel<128>;
-  join<<<s.workers, kJoinThreads, 0, stream>>>(a, scratch, s.workers, s.tile);
-  return cudaGetLastError();
+  if (D == 64) return mx ? launch_shape<64, true>(a, k, v, s, scratch, stream) : launch_shape<64, false>(a, k, v, s, scratch, stream);
+  return mx ? launch_shape<128, true>(a, k, v, s, scratch, stream) : launch_shape<128, false>(a, k, v, s, scratch, stream);
 }
 
 }  // namespace jattn
