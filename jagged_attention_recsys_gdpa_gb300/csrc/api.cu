@@ -917,17 +917,19 @@ CacheView cache_view(const jattn_cache_t* c, const int32_t* page_table, int64_t 
   return v;
 }
 
-// Pages as {D, page_size, H, n_pages}; boxes of one head's rows, 128 bytes (64
-// for codes at D = 64) by box_rows, swizzled over their width.
-int make_page_map(CUtensorMap* m, const jattn_cache_t* c, void* pages, int box_rows) {
+// Pages as {line, page_size, lines of a row, H, n_pages}, a line being 128 bytes of
+// a row (or the 64 of a row of codes at D = 64); boxes of one head's rows, line by
+// line, swizzled over a line's width.
+int make_page_map(CUtensorMap* m, const jattn_cache_t* c, void* pages, int box_rows, int box_lines) {
   const bool mx = c->format == JATTN_CACHE_MXFP8;
   const cuuint64_t row = static_cast<cuuint64_t>(c->D) * (mx ? 1 : 2);
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c->D), static_cast<cuuint64_t>(c->page_size),
-                              static_cast<cuuint64_t>(c->H), static_cast<cuuint64_t>(c->n_pages)};
-  const cuuint64_t strides[3] = {row, row * c->page_size, row * c->page_size * c->H};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(mx ? c->D : 64), static_cast<cuuint32_t>(box_rows), 1, 1};
-  const cuuint32_t es[4] = {1, 1, 1, 1};
-  const CUresult r = g_encode(m, mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pages, dims,
+  const cuuint32_t line = mx ? c->D : 64, lines = c->D / line;  // elements
+  const cuuint64_t dims[5] = {line, static_cast<cuuint64_t>(c->page_size), lines, static_cast<cuuint64_t>(c->H),
+                              static_cast<cuuint64_t>(c->n_pages)};
+  const cuuint64_t strides[4] = {row, 128, row * c->page_size, row * c->page_size * c->H};
+  const cuuint32_t box[5] = {line, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_lines), 1, 1};
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  const CUresult r = g_encode(m, mx ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, pages, dims,
                               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                               mx && c->D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1037,9 +1039,10 @@ int jattn_decode(const jattn_params_t* p, const jattn_cache_t* c, const int64_t*
   a.timeout_ns = g_timeout_ns;
   a.status = static_cast<DevStatus*>(ws);
   const bool mx = c->format == JATTN_CACHE_MXFP8;
-  const int box = decode_box_rows(p->D, mx, p->B, p->total_q, p->total_kv, a.G, c->H, c->page_size);
+  int rows, lines;
+  decode_box(p->D, mx, p->B, p->total_q, p->total_kv, a.G, c->H, c->page_size, &rows, &lines);
   CUtensorMap mk, mv;
-  if (make_page_map(&mk, c, c->k, box) || make_page_map(&mv, c, c->v, box))
+  if (make_page_map(&mk, c, c->k, rows, lines) || make_page_map(&mv, c, c->v, rows, lines))
     return cuda_fail("cuTensorMapEncodeTiled", cudaErrorInvalidValue);
   const cudaError_t e = launch_decode(p->D, mx, a, mk, mv, scratch, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? JATTN_OK : cuda_fail("decode kernel launch", e);

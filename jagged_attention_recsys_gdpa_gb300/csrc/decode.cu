@@ -37,9 +37,14 @@ namespace {
 
 constexpr int kWarps = 4;     // per CTA
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;    // steps held per worker
-constexpr int kCtasPerSm = 2;
-constexpr int kMaxCtas = 152 * kCtasPerSm;
+constexpr int kSms = 152;
+#ifndef MXC
+#define MXC 3
+#define BFC 3
+#endif
+constexpr int ctas_per_sm(bool mx, int nr) { return nr == 1 ? (mx ? MXC : BFC) : 2; }
+constexpr int stages_of(bool mx, int nr) { return ctas_per_sm(mx, nr) == 2 ? 3 : ctas_per_sm(mx, nr) == 3 ? 2 : 2; }
+constexpr int kMaxCtas = 3 * kSms;
 constexpr int kMinSteps = 2;  // per worker, as long as there are few steps in all
 constexpr int kJoinThreads = 256;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -47,11 +52,16 @@ constexpr float kLn2 = 0.6931471805599453f;
 // so that most steps rescale nothing; weights then reach 2^kSlack at most.
 constexpr float kSlack = 8.0f;
 
+// A condition that seldom holds: its code goes out of the loop's way.
+__device__ __forceinline__ bool rare(bool x) { return __builtin_expect(x, 0); }
+
+// silu(s) = s / (1 + e^-s), and s/2 (1 + tanh u) = s / (1 + e^-2u)
+__device__ __forceinline__ float silu(float s) { return __fdividef(s, 1.0f + __expf(-s)); }
+__device__ __forceinline__ float gelu(float s) {
+  return __fdividef(s, 1.0f + __expf(-2.0f * 0.7978845608028654f * fmaf(0.044715f * s * s, s, s)));
+}
 __device__ __forceinline__ float activate(float s, int act) {
-  if (act == JATTN_GELU_POLY) return gelu_poly(s);
-  // silu(s) = s / (1 + e^-s); s/2 (1 + tanh u) = s / (1 + e^-2u)
-  const float u = act == JATTN_SILU ? s : 2.0f * 0.7978845608028654f * fmaf(0.044715f * s * s, s, s);
-  return __fdividef(s, 1.0f + __expf(-u));
+  return act == JATTN_SILU ? silu(s) : act == JATTN_GELU_TANH ? gelu(s) : gelu_poly(s);
 }
 
 // ---------------------------------------------------------------- plan
@@ -94,11 +104,12 @@ __device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b, int tile, int 
 // a tile, steps of a head.
 struct Place {
   Seq s;
+  const int32_t* table;
   int b, tile, h, t;
 };
 
 __device__ __forceinline__ void advance(Place& p, const DecodeArgs& a, int tile, int step) {
-  if (++p.t < p.s.steps) return;
+  if (!rare(++p.t >= p.s.steps)) return;
   p.t = 0;
   if (++p.h < a.cache.H) return;
   p.h = 0;
@@ -108,6 +119,7 @@ __device__ __forceinline__ void advance(Place& p, const DecodeArgs& a, int tile,
     if (++p.b >= a.B) return;  // behind the last step: never used
     p.s = seq_of(a, p.b, tile, step);
   } while (p.s.tiles == 0);
+  p.table = a.cache.table + p.b * a.cache.max_pages;
 }
 
 __device__ __forceinline__ int64_t warp_inclusive(int64_t x, int lane) {
@@ -180,6 +192,7 @@ __device__ __forceinline__ Place find_place(const DecodeArgs& a, int tile, int s
     }
   }
   p.s = seq_of(a, p.b, tile, step);
+  p.table = a.cache.table + p.b * a.cache.max_pages;
   const int64_t unit = (first - at) / p.s.steps;
   p.t = static_cast<int>((first - at) % p.s.steps);
   p.tile = static_cast<int>(unit / a.cache.H);
@@ -201,9 +214,9 @@ struct Layout {
 // Shared memory of a CTA: [worker][stage] K rows then V rows (1024-byte aligned,
 // in TMA's 128- or 64-byte swizzle), [worker][stage] K then V exponents, then
 // [worker][stage] barriers: copied, and read by all of the worker's warps.
-template <int D, bool MX>
+template <int D, bool MX, int NR>
 constexpr int smem_bytes() {
-  return 1024 + kWarps * kStages * (8192 + 2 * Layout<D, MX>::keys * Layout<D, MX>::scale + 16);
+  return 1024 + kWarps * stages_of(MX, NR) * (8192 + 2 * Layout<D, MX>::keys * Layout<D, MX>::scale + 16);
 }
 
 // Byte offset of 16-byte piece `chunk` of row r in a step of STEP rows: rows of
@@ -223,14 +236,15 @@ __device__ __forceinline__ uint32_t piece_at(int r, int chunk) {
 //  * a query row is multiplied by 2^x so that its largest value lies in
 //    [2^14, 2^15): exact but for values below 2^-28 of the largest;
 //  * a K block's scale multiplies the block's fp32 partial score;
-//  * V's scales 2^(e - 127) become fp16 factors 2^(e - R) of the codes, R a
-//    reference exponent of the unit (the accumulators are in units of
-//    2^(R - 127)). From 2^-14 to 2^1 their products are exact; a larger exponent
-//    moves R and rescales the accumulators, and 16 keys with a block below
-//    2^-14 (or of NaN) take bf16 products instead;
+//  * V's scales 2^(e - 127) become fp16 factors 2^(e - R) of the keys' weights,
+//    one for each block of columns, R a reference exponent of the unit (the
+//    accumulators are in units of 2^(R - 127)). From 2^-14 to 2^1 the factors are
+//    fp16 numbers; a larger exponent moves R and rescales the accumulators, and
+//    16 keys with a block below 2^-14 (or of NaN) take bf16 products instead;
 //  * weights are kept at 2^kLift times their value against the row's reference
 //    (the running maximum; for pointwise activations the exponent of their
-//    largest one), so that what fp16 loses below 2^-24 is below 2^-31 of it.
+//    largest one), so that what fp16 loses at its lower end is 2^-32 of the
+//    reference, 2^-18 under the smallest factor.
 // bf16 operands throughout cost three times the instructions per code.
 constexpr int kLift = 7;
 
@@ -250,14 +264,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ uint32_t f16x2_lo(float x0, float x1, uint32_t hi) {  // what the pair `hi` leaves out
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  return pack_f16x2(x0 - f.x, x1 - f.y);
-}
-// Byte j of w0 and w1 in the two 16-bit halves.
-__device__ __forceinline__ uint32_t byte_pair(uint32_t w0, uint32_t w1, int j) {
-  return __byte_perm(w0, w1, 0x4400u + 0x1111u * j) & 0x00ff00ffu;
-}
 // 2^(e - 127) of byte j of w as fp32 (0 for e = 0: below 2^-118 of anything; e = 255 gives infinity, and with the
 // zero codes of such a block NaN).
 __device__ __forceinline__ float scale_of(uint32_t w, int j) {
@@ -267,17 +273,6 @@ __device__ __forceinline__ float scale_of(uint32_t w, int j) {
 // mantissa bits go to the low exponent and high mantissa bits, subnormals included.
 __device__ __forceinline__ uint32_t codes_even(uint32_t w) { return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u); }
 __device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u); }
-// bf16 pair 2^(e - R + 120) of two exponents (in the halves of x), e <= R + 1; NaN for e = 255.
-__device__ __forceinline__ uint32_t bf16_factors(uint32_t x, int ref) {
-  uint32_t r = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = static_cast<int>((x >> (16 * i)) & 0xffu);
-    r |= (e == 255 ? 0x7fc0u : static_cast<uint32_t>(max(e - ref + 247, 0)) << 7) << (16 * i);
-  }
-  return r;
-}
-
 // ---------------------------------------------------------------- rows and columns
 // How a warp's products lie in its lanes (l = lane / 4, c = lane % 4): scores
 // and weights as [16 keys x 8 query rows], keys l and l + 8, rows 2c and 2c + 1;
@@ -298,6 +293,20 @@ __device__ __forceinline__ void scale_rows(float (&o)[NT][4], float c0, float c1
     o[j][1] *= c1;
     o[j][2] *= c0;
     o[j][3] *= c1;
+  }
+}
+
+// Weights of keys first, first + 8, ... outside a row's [lo, hi) become `none`.
+template <int MT, int NR>
+__device__ __forceinline__ void mask_keys(float (&s)[MT][NR][4], int g, int first, const int (&lo)[2], const int (&hi)[2],
+                                          float none) {
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int pos = first + mt * 16 + 8 * (e >> 1);
+      if (pos < lo[e & 1] || pos >= hi[e & 1]) s[mt][g][e] = none;
+    }
   }
 }
 
@@ -371,7 +380,7 @@ __device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int
   float x = 0.0f;  // stays 0 unless something is not finite
 #pragma unroll
   for (int j = 0; j < D / 16; ++j) x += (o[j][0] - o[j][0]) + (o[j][1] - o[j][1]) + (o[j][2] - o[j][2]) + (o[j][3] - o[j][3]);
-  if (!__any_sync(0xffffffffu, x != 0.0f)) return;
+  if (!rare(__any_sync(0xffffffffu, x != 0.0f))) return;
   const int lane = threadIdx.x & 31, c = lane & 3;
   uint32_t bad = 0;
 #pragma unroll
@@ -512,7 +521,7 @@ __device__ __forceinline__ void worker_barrier(int worker) {
 
 // Bounded wait; false (and the status set) when it runs out.
 __device__ __forceinline__ bool wait_full(const DecodeArgs& a, uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (!rare(!mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (globaltimer_ns() - t0 > a.timeout_ns) {
@@ -523,13 +532,14 @@ __device__ __forceinline__ bool wait_full(const DecodeArgs& a, uint64_t* bar, ui
   return true;
 }
 
-// A step's rows are copied as boxes of min(page size, step) rows; lane i < boxes
-// takes box i. Its table entry, or kNoBox where no key lies that any row sees.
+// A step's rows are copied as boxes of min(page size, step) rows: one, or
+// several by a lane each. A lane's table entry, or kNoBox where no key lies that
+// any row sees.
 constexpr int64_t kNoBox = INT64_MIN;
 __device__ __forceinline__ int64_t box_page(const DecodeArgs& a, const Place& p, int step, int box, int lane) {
-  const int first = p.s.k0 + p.t * step + lane * box;
-  if (lane * box >= step || p.s.lo >= p.s.hi || first >= p.s.hi || first + box <= p.s.lo) return kNoBox;
-  return __ldg(a.cache.table + p.b * a.cache.max_pages + (first >> a.cache.page_shift));
+  const int r = box == step ? 0 : lane * box, first = p.s.k0 + p.t * step + r;
+  if (r >= step || p.s.lo >= p.s.hi || first >= p.s.hi || first + box <= p.s.lo) return kNoBox;
+  return __ldg(p.table + (first >> a.cache.page_shift));
 }
 
 template <int D, bool MX, int WM>
@@ -539,38 +549,47 @@ __device__ __forceinline__ void load_step(const DecodeArgs& a, const CUtensorMap
   using L = Layout<D, MX>;
   constexpr int step = L::keys * WM;
   const bool ok = page >= 0 && page < a.cache.n_pages;
-  if (page != kNoBox && !ok) record_error(a.status, JATTN_ERR_PAGES, 80, p.b);
-  const uint32_t n = __popc(__ballot_sync(0xffffffffu, ok));
-  if (lane == 0) mbar_arrive_expect_tx(bar, n * static_cast<uint32_t>(box * 2 * (L::row + L::scale)));
-  __syncwarp();
-  if (!ok) return;
-  const int h = p.h;
-  const int r = lane * box, y = (p.s.k0 + p.t * step + r) & a.cache.page_mask;
+  if (rare(page != kNoBox && !ok)) record_error(a.status, JATTN_ERR_PAGES, 80, p.b);
   const uint32_t b = smem_u32(bar);
-#pragma unroll
-  for (int x = 0; x < L::row / L::line; ++x) {
-    const uint32_t to = stage + x * (step * L::line) + r * L::line;
-    tma_load_4d(to, k_map, b, x * 64, y, h, static_cast<int>(page));
-    tma_load_4d(to + 4096 * WM, v_map, b, x * 64, y, h, static_cast<int>(page));
-  }
-  if constexpr (MX) {
-    const int64_t at = (((page * a.cache.H + h) << a.cache.page_shift) + y) * L::scale;
-    bulk_load(scales + r * L::scale, a.cache.ks + at, box * L::scale, b);
-    bulk_load(scales + (step + r) * L::scale, a.cache.vs + at, box * L::scale, b);
+  const auto copy = [&](int r, int lines) {  // the box of step rows r ..., by `lines` copies
+    const int y = (p.s.k0 + p.t * step + r) & a.cache.page_mask;
+    for (int x = 0; x < lines; ++x) {
+      const uint32_t to = stage + x * (step * L::line) + r * L::line;
+      tma_load_5d(to, k_map, b, 0, y, x, p.h, static_cast<int>(page));
+      tma_load_5d(to + 4096 * WM, v_map, b, 0, y, x, p.h, static_cast<int>(page));
+    }
+    if constexpr (MX) {
+      const int64_t at = (((page * a.cache.H + p.h) << a.cache.page_shift) + y) * L::scale;
+      bulk_load(scales + r * L::scale, a.cache.ks + at, box * L::scale, b);
+      bulk_load(scales + (step + r) * L::scale, a.cache.vs + at, box * L::scale, b);
+    }
+  };
+  if (!rare(box != step)) {  // the same page in every lane
+    if (elect_one()) {
+      mbar_arrive_expect_tx(bar, ok ? step * 2 * (L::row + L::scale) : 0);
+      if (ok) copy(0, 1);
+    }
+    __syncwarp();
+  } else {
+    const uint32_t n = __popc(__ballot_sync(0xffffffffu, ok));
+    if (lane == 0) mbar_arrive_expect_tx(bar, n * static_cast<uint32_t>(box * 2 * (L::row + L::scale)));
+    __syncwarp();
+    if (ok) copy(lane * box, L::row / L::line);  // boxes of one line: a step's lines lie apart
   }
 }
 
-// Zeros for the V rows of a step outside [lo, hi): what their places hold has
-// to be finite to vanish under a weight of zero.
-template <int D, int WM>
+// Zeros for the V rows of a step outside [lo, hi): what their places hold (rows
+// past the sequence's, or whatever was there where no box was copied) has to be
+// finite to vanish under a weight of zero.
+template <int D, bool MX, int WM>
 __device__ __forceinline__ void clear_rows(uint32_t vs, int pos0, int lo, int hi, int lane) {
-  using L = Layout<D, false>;
+  using L = Layout<D, MX>;
   constexpr int step = L::keys * WM;
   for (int i = lane; i < 4096 * WM / 16; i += 32) {
     const int r = i % step;  // any piece of row r: the swizzle stays within the row
     if (pos0 + r >= lo && pos0 + r < hi) continue;
     const int chunk = i / step;
-    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vs + piece_at<D, false, step>(r, chunk)), "r"(0u)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vs + piece_at<D, MX, step>(r, chunk)), "r"(0u)
                  : "memory");
   }
   fence_proxy_async();
@@ -578,11 +597,12 @@ __device__ __forceinline__ void clear_rows(uint32_t vs, int pos0, int lo, int hi
 }
 
 template <int D, bool MX, int NR, int WM>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(MX, NR))
     decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   void* scratch) {
   using L = Layout<D, MX>;
   constexpr int step = L::keys * WM, tile = 8 * NR * WM, KS = D / 16, MT = L::sub / 16, per_cta = kWarps / WM;
+  constexpr int kStages = stages_of(MX, NR);
   extern __shared__ unsigned char smem_raw[];
   __shared__ int64_t start[kThreads];
   __shared__ Left left[per_cta];
@@ -615,8 +635,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     }
     worker_barrier<WM>(in_cta);
     const int box = min(step, a.cache.page_mask + 1);
-    const int64_t steps = last - first;
-    int64_t loaded = 0;  // steps whose copies have been issued (by the worker's first warp)
+    const int steps = static_cast<int>(last - first);
+    int loaded = 0;  // steps whose copies have been issued (by the worker's first warp)
     int64_t page = kNoBox;
     if (warp_m == 0) {
       page = box_page(a, in, step, box, lane);
@@ -636,6 +656,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     uint32_t q[NR][KS][2];
     float o[NR][KS][4], m[NR][2], l[NR][2];
     float f[NR][2];             // what the rows' scores are multiplied by
+    float up[NR][2];            // MXFP8, pointwise: and their weights
     int lo[NR][2], hi[NR][2];   // keys that they may see
     int all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;  // that every row, and that any row, of the warp's may see
     int ref = -1;               // MXFP8: V's reference exponent, none yet
@@ -646,9 +667,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     int stage_no = 0;
     uint32_t phase = 0;
     bool ok = true;
-    int64_t done = 0;
+    int done = 0;
     for (; done < steps; ++done) {
-      if (!wait_full(a, full + stage_no, phase)) {
+      if (rare(!wait_full(a, full + stage_no, phase))) {
         ok = false;
         break;
       }
@@ -671,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         }
       }
 
-      if (fresh) {
+      if (rare(fresh)) {
         fresh = false;
         n_steps = 0;
         ref = -1;
@@ -694,6 +715,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               m[g][i] = !MX || a.act == JATTN_SOFTMAX ? -INFINITY : kLeast;
               l[g][i] = 0.0f;
               f[g][i] = base;
+              up[g][i] = pow2(kLift - static_cast<int>(kLeast));
             }
 #pragma unroll
             for (int j = 0; j < KS; ++j) o[g][j][0] = o[g][j][1] = o[g][j][2] = o[g][j][3] = 0.0f;
@@ -739,9 +761,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const uint32_t ks = ring + stage_no * (8192 * WM), vs = ks + 4096 * WM;
       const uint32_t ksc = scale_ring + stage_no * (2 * step * L::scale), vsc = ksc + step * L::scale;
       const int step0 = at.s.k0 + at.t * step;
-      if constexpr (!MX) {
-        if (live && (step0 < at.s.lo || step0 + step > at.s.hi)) clear_rows<D, WM>(vs, step0, at.s.lo, at.s.hi, lane);
-      }
+      if (rare(live && (step0 < at.s.lo || step0 + step > at.s.hi))) clear_rows<D, MX, WM>(vs, step0, at.s.lo, at.s.hi, lane);
 #pragma unroll 1
       for (int r_base = 0; r_base < step; r_base += L::sub) {
         const int pos0 = step0 + r_base;
@@ -800,23 +820,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         // ---- weights
 #pragma unroll
         for (int g = 0; g < NR; ++g) {
-          float t[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[mt][g][e] *= f[g][e & 1];
+          }
           if (a.act == JATTN_SOFTMAX) {
+            if (rare(partial)) mask_keys<MT>(s, g, pos0 + (lane >> 2), lo[g], hi[g], -INFINITY);
+            float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                s[mt][g][e] *= f[g][e & 1];
-                if (partial) {
-                  const int pos = pos0 + mt * 16 + (lane >> 2) + 8 * (e >> 1);
-                  if (pos < lo[g][e & 1] || pos >= hi[g][e & 1]) s[mt][g][e] = -INFINITY;
-                }
-                t[e & 1] = fmaxf(t[e & 1], s[mt][g][e]);
-              }
+              for (int i = 0; i < 2; ++i) t[i] = fmax3(t[i], s[mt][g][i], s[mt][g][2 + i]);
             }
             t[0] = rows_max(t[0]);
             t[1] = rows_max(t[1]);
-            if (__any_sync(0xffffffffu, t[0] > m[g][0] + kSlack || t[1] > m[g][1] + kSlack)) {
+            if (rare(__any_sync(0xffffffffu, t[0] > m[g][0] + kSlack || t[1] > m[g][1] + kSlack))) {
               float x[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
@@ -838,51 +857,69 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               }
             }
           } else {
+            if (a.act == JATTN_SILU) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
+              for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                s[mt][g][e] = activate(s[mt][g][e] * f[g][e & 1], a.act);
-                const int pos = pos0 + mt * 16 + (lane >> 2) + 8 * (e >> 1);
-                if (partial && (pos < lo[g][e & 1] || pos >= hi[g][e & 1])) s[mt][g][e] = 0.0f;
-                t[e & 1] = fmaxf(t[e & 1], fabsf(s[mt][g][e]));
+                for (int e = 0; e < 4; ++e) s[mt][g][e] = silu(s[mt][g][e]);
+              }
+            } else if (a.act == JATTN_GELU_TANH) {
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[mt][g][e] = gelu(s[mt][g][e]);
+              }
+            } else {
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[mt][g][e] = gelu_poly(s[mt][g][e]);
               }
             }
+            if (rare(partial)) mask_keys<MT>(s, g, pos0 + (lane >> 2), lo[g], hi[g], 0.0f);
             if constexpr (MX) {  // m is the exponent that the row's weights are held against
+              float t[2] = {0.0f, 0.0f};
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) t[i] = fmax3(t[i], fabsf(s[mt][g][i]), fabsf(s[mt][g][2 + i]));
+              }
               t[0] = exponent_of(rows_max(t[0]));
               t[1] = exponent_of(rows_max(t[1]));
-              if (__any_sync(0xffffffffu, t[0] > m[g][0] + kSlack - 1 || t[1] > m[g][1] + kSlack - 1)) {
+              if (rare(__any_sync(0xffffffffu, t[0] > m[g][0] + kSlack - 1 || t[1] > m[g][1] + kSlack - 1))) {
                 const float n0 = fmaxf(m[g][0], t[0]), n1 = fmaxf(m[g][1], t[1]);
                 scale_rows(o[g], pow2(static_cast<int>(m[g][0] - n0)), pow2(static_cast<int>(m[g][1] - n1)));
                 m[g][0] = n0;
                 m[g][1] = n1;
+                up[g][0] = pow2(kLift - static_cast<int>(n0));
+                up[g][1] = pow2(kLift - static_cast<int>(n1));
               }
-              const float up[2] = {pow2(kLift - static_cast<int>(m[g][0])), pow2(kLift - static_cast<int>(m[g][1]))};
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[mt][g][e] *= up[e & 1];
+                for (int e = 0; e < 4; ++e) s[mt][g][e] *= up[g][e & 1];
               }
             }
           }
         }
-        // ---- O += V^T P^T, with P as two parts (its rounding to one would be as large as the output's own)
+        // ---- O += V^T P^T
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          uint32_t ph[NR][2], pl[NR][2];
-#pragma unroll
-          for (int g = 0; g < NR; ++g) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float x = s[mt][g][2 * i], y = s[mt][g][2 * i + 1];
-              const uint32_t hi2 = MX ? pack_f16x2(x, y) : pack_bf16x2(x, y);
-              ph[g][i] = movmatrix(hi2);
-              pl[g][i] = movmatrix(MX ? f16x2_lo(x, y, hi2) : bf16x2_lo(x, y, hi2));
-            }
-          }
           // rows (keys) and pieces of the transposed loads: keys 0-7 of two pieces, then keys 8-15
           const int r = r_base + mt * 16 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
           if constexpr (!MX) {
+            // P as two bf16 parts: its rounding to one would be as large as the output's own
+            uint32_t ph[NR][2], pl[NR][2];
+#pragma unroll
+            for (int g = 0; g < NR; ++g) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float x = s[mt][g][2 * i], y = s[mt][g][2 * i + 1];
+                const uint32_t both = pack_bf16x2(x, y);
+                ph[g][i] = movmatrix(both);
+                pl[g][i] = movmatrix(bf16x2_lo(x, y, both));
+              }
+            }
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
               uint32_t x[4];
@@ -894,94 +931,104 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               }
             }
           } else {
-            uint32_t e[4];  // keys 2c, 2c + 1, 2c + 8, 2c + 9 of the 16
+            uint32_t e[2];  // of this lane's keys of the 16, lane / 4 and 8 more
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              e[i] = scale_word<D>(vsc, r_base + mt * 16 + 2 * c + (i >> 1) * 8 + (i & 1));
+            for (int i = 0; i < 2; ++i) {
+              e[i] = scale_word<D>(vsc, r_base + mt * 16 + 8 * i + (lane >> 2));
               if (D == 64) e[i] |= e[i] << 16;
             }
-            if (partial) {
-              // rows outside the sequence hold anything: codes are always finite, exponents become the reference
+            if (rare(partial)) {
+              // rows outside the sequence have codes of zero and any exponents: these become the reference
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int pos = pos0 + mt * 16 + 2 * c + (i >> 1) * 8 + (i & 1);
+              for (int i = 0; i < 2; ++i) {
+                const int pos = pos0 + mt * 16 + 8 * i + (lane >> 2);
                 if (pos < at.s.lo || pos >= at.s.hi) e[i] = max(ref, 0) * 0x01010101u;
               }
             }
             // e - (R - 14), byte by byte: 0 .. 15 where fp16 factors do (a byte below borrows and ends up far above)
-            uint32_t d[4], out = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              d[i] = e[i] - static_cast<uint32_t>(ref - 14) * 0x01010101u;
-              out |= d[i];
-            }
+            uint32_t d[2] = {e[0] - static_cast<uint32_t>(ref - 14) * 0x01010101u,
+                             e[1] - static_cast<uint32_t>(ref - 14) * 0x01010101u};
             bool small = false;
-            if (__any_sync(0xffffffffu, (out & 0xf0f0f0f0u) != 0 || ref < 0)) {
-              int top = 0;  // the largest exponent but NaN's
+            if (rare(__any_sync(0xffffffffu, ((d[0] | d[1]) & 0xf0f0f0f0u) != 0 || ref < 0))) {
+              int top = 14;  // the largest exponent but NaN's (R - 14 is no negative byte)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int x = static_cast<int>((e[i] >> (8 * j)) & 0xffu);
-                  if (x != 255) top = max(top, x);
-                }
+              for (int j = 0; j < 8; ++j) {
+                const int x = static_cast<int>((e[j & 1] >> (8 * (j >> 1))) & 0xffu);
+                if (x != 255) top = max(top, x);
               }
               top = __reduce_max_sync(0xffffffffu, top);
               if (ref < 0 || top > ref + 1) {
-                top = max(top, 14);  // R - 14 is no negative byte
                 if (ref >= 0) {
 #pragma unroll
                   for (int g = 0; g < NR; ++g) scale_rows(o[g], pow2(ref - top - 1), pow2(ref - top - 1));
                 }
                 ref = top + 1;
               }
-              out = 0;
+              uint32_t out = 0;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int pos = pos0 + mt * 16 + 2 * c + (i >> 1) * 8 + (i & 1);
+              for (int i = 0; i < 2; ++i) {
+                const int pos = pos0 + mt * 16 + 8 * i + (lane >> 2);
                 if (partial && (pos < at.s.lo || pos >= at.s.hi)) e[i] = ref * 0x01010101u;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int x = static_cast<int>((e[i] >> (8 * j)) & 0xffu) - (ref - 14);
-                  out |= static_cast<uint32_t>(x);
-                }
+                for (int j = 0; j < 4; ++j) out |= ((e[i] >> (8 * j)) & 0xffu) - static_cast<uint32_t>(ref - 14);
                 d[i] = e[i] - static_cast<uint32_t>(ref - 14) * 0x01010101u;
               }
               small = __any_sync(0xffffffffu, (out & 0xfffffff0u) != 0);
             }
-            if (small) {  // bf16 products for these 16 keys
-#pragma unroll
-              for (int g = 0; g < NR; ++g) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const float x = s[mt][g][2 * i], y = s[mt][g][2 * i + 1];
-                  const uint32_t hi2 = pack_bf16x2(x, y);
-                  ph[g][i] = movmatrix(hi2);
-                  pl[g][i] = movmatrix(bf16x2_lo(x, y, hi2));
-                }
-              }
-#pragma unroll
+            if (rare(small)) {  // bf16 products for these 16 keys
+#pragma unroll 1
               for (int j = 0; j < D / 32; ++j) {
-                const uint32_t fa = bf16_factors(byte_pair(e[0], e[1], j), ref), fb = bf16_factors(byte_pair(e[2], e[3], j), ref);
-                uint32_t w[4];
-                ldmatrix4_trans(w, vs + piece_at<D, MX, step>(r, 2 * j + half));
+                float w[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const uint32_t x[4] = {mul_bf16x2(codes_even(w[i]), fa), mul_bf16x2(codes_odd(w[i]), fa),
-                                         mul_bf16x2(codes_even(w[2 + i]), fb), mul_bf16x2(codes_odd(w[2 + i]), fb)};
+                  const int x = static_cast<int>((e[i] >> (8 * j)) & 0xffu);
+                  w[i] = x == 255 ? __int_as_float(0x7fc00000) : pow2(x - ref);
+                }
+                uint32_t v[4];
+                ldmatrix4_trans(v, vs + piece_at<D, MX, step>(r, 2 * j + half));
 #pragma unroll
-                  for (int g = 0; g < NR; ++g) {
-                    mma_bf16(o[g][2 * j + i], x, ph[g]);
-                    mma_bf16(o[g][2 * j + i], x, pl[g]);
+                for (int g = 0; g < NR; ++g) {
+                  uint32_t ph[2], pl[2];
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    const float x = s[mt][g][2 * i] * w[i], y = s[mt][g][2 * i + 1] * w[i];
+                    const uint32_t both = pack_bf16x2(x, y);
+                    ph[i] = movmatrix(both);
+                    pl[i] = movmatrix(bf16x2_lo(x, y, both));
+                  }
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    // 2^120 makes up for the codes' exponent bias
+                    const uint32_t x[4] = {mul_bf16x2(codes_even(v[i]), 0x7b807b80u), mul_bf16x2(codes_odd(v[i]), 0x7b807b80u),
+                                           mul_bf16x2(codes_even(v[2 + i]), 0x7b807b80u),
+                                           mul_bf16x2(codes_odd(v[2 + i]), 0x7b807b80u)};
+#pragma unroll
+                    for (int jj = 0; jj < D / 32; ++jj) {
+                      if (jj != j) continue;
+                      mma_bf16(o[g][2 * jj + i], x, ph);
+                      mma_bf16(o[g][2 * jj + i], x, pl);
+                    }
                   }
                 }
               }
             } else {
+              // P in fp16 (half a step is 2^-11 of it, an eighth of the output's), then by the keys' 2^(e - R)
+              uint32_t p[NR][2];
+#pragma unroll
+              for (int g = 0; g < NR; ++g) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) p[g][i] = pack_f16x2(s[mt][g][2 * i], s[mt][g][2 * i + 1]);
+              }
 #pragma unroll
               for (int j = 0; j < D / 32; ++j) {  // one block of 32 columns: two 16-byte pieces
-                // fp16 2^(e - R): exponent field e - R + 15
-                const uint32_t fa = byte_pair(d[0], d[1], j) * 1024u + 0x04000400u;
-                const uint32_t fb = byte_pair(d[2], d[3], j) * 1024u + 0x04000400u;
+                uint32_t pj[NR][2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  // fp16 2^(e - R), twice: exponent field e - R + 15
+                  const uint32_t x = __byte_perm(d[i], 0u, 0x4040u + 0x0101u * j) * 1024u + 0x04000400u;
+#pragma unroll
+                  for (int g = 0; g < NR; ++g) pj[g][i] = movmatrix(mul_f16x2(p[g][i], x));
+                }
                 uint32_t w[4];
                 ldmatrix4_trans(w, vs + piece_at<D, MX, step>(r, 2 * j + half));
 #pragma unroll
@@ -990,15 +1037,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                   uint32_t x[4];
                   e4m3x4_to_f16(__byte_perm(w[i], 0u, 0x3120), x[0], x[1]);
                   e4m3x4_to_f16(__byte_perm(w[2 + i], 0u, 0x3120), x[2], x[3]);
-                  x[0] = mul_f16x2(x[0], fa);
-                  x[1] = mul_f16x2(x[1], fa);
-                  x[2] = mul_f16x2(x[2], fb);
-                  x[3] = mul_f16x2(x[3], fb);
 #pragma unroll
-                  for (int g = 0; g < NR; ++g) {
-                    mma_f16(o[g][2 * j + i], x, ph[g]);
-                    mma_f16(o[g][2 * j + i], x, pl[g]);
-                  }
+                  for (int g = 0; g < NR; ++g) mma_f16(o[g][2 * j + i], x, pj[g]);
                 }
               }
             }
@@ -1016,7 +1056,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
       // ---- the unit's, or the run's, last step
       const bool unit_ends = at.t == at.s.steps - 1, run_ends = done == steps - 1;
-      if (unit_ends || run_ends) {
+      if (rare(unit_ends || run_ends)) {
         const bool begun = at.t == n_steps - 1;  // the unit's first step is in this run
         const int slot = begun ? 1 : 0;
         if (live) {
@@ -1093,8 +1133,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       // a wait ran out: nothing to join here, and no copy may be in flight when the CTA ends
       if (tid == 0) left[in_cta] = Left{0, 0, 0, 0, 0, 0, 0};
       if (warp_m == 0) {
-        for (int64_t i = done; i < loaded; ++i)
-          (void)wait_full(a, full + static_cast<int>(i % kStages), static_cast<uint32_t>(i / kStages) & 1u);
+        for (int i = done; i < loaded; ++i) (void)wait_full(a, full + i % kStages, static_cast<uint32_t>(i / kStages) & 1u);
       }
     }
   }
@@ -1227,14 +1266,15 @@ Shape shape_of(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G
   const int64_t tiles = total_q * G / s.tile + (total_q < B ? total_q : B);
   const int64_t per_cta = kMinSteps * (kWarps / s.wm);
   const double steps = static_cast<double>(tiles) * H * static_cast<double>((max_kv + step - 1) / step + 2);
-  s.ctas = steps / per_cta >= kMaxCtas ? kMaxCtas : static_cast<int>(steps / per_cta) + 1;
+  const int most = kSms * ctas_per_sm(mx, s.nr);
+  s.ctas = steps / per_cta >= most ? most : static_cast<int>(steps / per_cta) + 1;
   return s;
 }
 
 template <int D, bool MX, int NR, int WM>
 cudaError_t launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, const Shape& s, void* scratch,
                    cudaStream_t stream) {
-  constexpr int smem = smem_bytes<D, MX>();
+  constexpr int smem = smem_bytes<D, MX, NR>();
   cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, MX, NR, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   decode_kernel<D, MX, NR, WM><<<s.ctas, kThreads, smem, stream>>>(a, k, v, scratch);
@@ -1259,10 +1299,12 @@ size_t decode_scratch_bytes(int D, bool mx, int64_t B, int64_t total_q, int64_t 
   return scratch_bytes(s.ctas, kWarps / s.wm, s.tile, D);
 }
 
-int decode_box_rows(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H, int page_size) {
+void decode_box(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H, int page_size, int* rows,
+                int* lines) {
   const Shape s = shape_of(D, mx, B, total_q, max_kv, G, H);
-  const int step = 4096 / (D * (mx ? 1 : 2)) * s.wm;
-  return step < page_size ? step : page_size;
+  const int row = D * (mx ? 1 : 2), step = 4096 / row * s.wm;
+  *rows = step < page_size ? step : page_size;
+  *lines = step <= page_size && row > 128 ? row / 128 : 1;
 }
 
 cudaError_t launch_decode(int D, bool mx, const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, void* scratch,

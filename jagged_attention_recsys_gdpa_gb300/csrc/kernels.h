@@ -118,10 +118,11 @@ cudaError_t launch_cache_append(const CacheView& c, bool mx, int64_t B, int64_t 
 cudaError_t launch_cache_read(const CacheView& c, bool mx, int64_t B, int64_t total, const int64_t* off,
                               const int64_t* start, void* k, void* v, int D, DevStatus* status, cudaStream_t stream);
 // Attention over the paged cache (decode.cu): scratch of decode_scratch_bytes;
-// k and v map the pages as {D, page_size, H, n_pages} with boxes of 128-byte
-// (codes at D = 64: 64-byte) rows, decode_box_rows of them.
+// k and v map the pages as {line, page_size, lines of a row, H, n_pages}, lines
+// of 128 bytes (codes at D = 64: 64), with boxes of decode_box's rows and lines.
 size_t decode_scratch_bytes(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H);
-int decode_box_rows(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H, int page_size);
+void decode_box(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H, int page_size, int* rows,
+                int* lines);
 cudaError_t launch_decode(int D, bool mx, const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, void* scratch,
                           cudaStream_t stream);
 

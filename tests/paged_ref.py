@@ -25,7 +25,7 @@ def e4m3_codes(x):
 
 
 def e4m3_values(codes):
-    return np.where(codes & 128, -1.0, 1.0) * E4M3[codes & 127]
+    return np.where(codes & 128, -1.0, 1.0) * np.append(E4M3, np.nan)[codes & 127]
 
 
 def quantise(x):
@@ -87,8 +87,10 @@ def allowed(lq, n, causal, window, block):
 
 
 def decode(q, k_pages, v_pages, table, kv_lens, q_off, act="softmax", causal=False, window=0, block=0, norm=False,
-           scale=None):
-    """q float64 [total, Hq, D]; pages float64. Returns o, lse and the elementwise bounds described in bounds()."""
+           scale=None, part=2.0**-16, floor=0.0):
+    """q float64 [total, Hq, D]; pages float64. Returns o, lse and the elementwise bounds described in weights();
+    ``part`` and ``floor``: how far a weight may be off as an operand of the second product, as a share of itself and of
+    the row's largest."""
     total, Hq, D = q.shape
     H = k_pages.shape[1]
     G = Hq // H
@@ -108,13 +110,14 @@ def decode(q, k_pages, v_pages, table, kv_lens, q_off, act="softmax", causal=Fal
             for h in range(Hq):
                 kk, vv = k[keep, h // G], v[keep, h // G]
                 s = scale * (kk @ q[r, h])
-                w, err = weights(s, scale * (np.abs(kk) @ np.abs(q[r, h])), act, len(s))
+                w, err = weights(s, scale * (np.abs(kk) @ np.abs(q[r, h])), act, len(s), part)
                 if act == "softmax":
                     top = s.max()
                     lse[r, h] = top + np.log(np.exp(s - top).sum())
                     # each term is off by a factor within err; the logarithm's own and the final rounding
                     lse_tol[r, h] = err.max() + 2.0**-20 * (1 + abs(lse[r, h]))
                     w, err = np.exp(s - lse[r, h]), np.exp(s - lse[r, h]) * (err + err.max())
+                err = err + floor * np.abs(w).max()
                 c = 1.0 / n if norm else 1.0
                 o[r, h] = c * (w @ vv)
                 # rounding to bf16 (2^-8 relative) behind the sum's own error
@@ -123,12 +126,13 @@ def decode(q, k_pages, v_pages, table, kv_lens, q_off, act="softmax", causal=Fal
     return o, lse, o_tol, lse_tol
 
 
-def weights(s, a, act, n):
+def weights(s, a, act, n, part):
     """(w, bound of its error): products of bf16 values are exact in fp32, so a score of D <= 128 terms summed in fp32
     is off by at most 2^-16 a, a = scale * sum |q_d k_d| (128 roundings of 2^-23). An exponential (or sigmoid) of it in
     fp32 adds its argument's rounding (2^-22 of |s| + 16, the running maximum's place) and 2^-20; weights enter the
-    second product as two bf16 parts (2^-16) and are summed in fp32 (n roundings of 2^-23)."""
-    rel = 2.0**-20 + 2.0**-22 * (np.abs(s) + 16) + 2.0**-16 + n * 2.0**-23
+    second product as two bf16 parts (2^-16) or, for an MXFP8 cache, rounded to fp16 (half a step: 2^-11), and are
+    summed in fp32 (n roundings of 2^-23)."""
+    rel = 2.0**-20 + 2.0**-22 * (np.abs(s) + 16) + part + n * 2.0**-23
     if act == "softmax":
         return None, rel + 2.0**-16 * a
     w = activate(s, act)

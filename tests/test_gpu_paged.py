@@ -54,7 +54,7 @@ def fill_cache(J, lens, page, H, D, fmt, seed, garbage=True, extra_cols=0, std=1
             if garbage:
                 dead = np.broadcast_to(~live[:, None, :], (n_pages, H, page))
                 codes = codes.copy()
-                codes[dead], e[dead] = 0x55, 255
+                codes[dead], e[dead] = 0x7f, 255
             bufs.append((torch.from_numpy(codes).cuda(), torch.from_numpy(e).cuda()))
         pages.append(y)
     cache = J.PagedCache(bufs[0][0], bufs[1][0], bufs[0][1], bufs[1][1])
@@ -262,6 +262,13 @@ def test_append_and_read_report_bad_places(fmt):
 
 
 # ------------------------------------------------------------------ decode
+def weight_parts(fmt, spread=4):
+    """MXFP8: weights are held in fp16 at 2^7 times their share of the row's largest and multiplied by their V block's
+    2^-spread: half a step is 2^-11, or 2^-25 absolute below fp16's normal range, 2^(-25 - 7 + spread) of the largest.
+    (Normal values: block maxima of 32 lie within 2^4.)"""
+    return {} if fmt == "bf16" else dict(part=2.0**-11, floor=2.0 ** (spread - 32))
+
+
 def check_decode(J, lens, lq, Hq, H, D, page, fmt, seed=21, act="softmax", causal=False, window=0, block=0, norm=False,
                  scale=None, extra_rows=0, max_kv=None, one_row=False):
     clear(J)
@@ -276,7 +283,8 @@ def check_decode(J, lens, lq, Hq, H, D, page, fmt, seed=21, act="softmax", causa
     o, lse = J.decode(q.cuda(), cache, cu(table), cu(np.asarray(lens, np.int64)), q_off=None if one_row else cu(q_off),
                       norm_by_lkv=norm, scale=scale, out=out, lse=lse0, max_kv=max_kv, **kw)
     assert J.device_status() == 0
-    ro, rl, to, tl = R.decode(np64(q), pages[0], pages[1], table, lens, q_off, norm=norm, scale=scale, **kw)
+    ro, rl, to, tl = R.decode(np64(q), pages[0], pages[1], table, lens, q_off, norm=norm, scale=scale,
+                              **weight_parts(fmt), **kw)
     n = int(q_off[-1])
     go = np64(o)
     assert np.all(np.isfinite(go))
@@ -390,7 +398,8 @@ def test_decode_mxfp8_dynamic_range(case, act, D):
     kp, vp = (np.nan_to_num(R.dequantise(c.cpu().numpy(), e.cpu().numpy())) for c, e in ((cache.k, ke), (cache.v, ve)))
     o, lse = J.decode(q.cuda(), cache, cu(table), cu(np.array(lens)), **kw)
     assert J.device_status() == 0
-    ro, rl, to, tl = R.decode(np64(q), kp, vp, table, lens, np.arange(5), **kw)
+    # V blocks may lie 2^14 below the unit's largest (below that, bf16 products hold the weights in two parts)
+    ro, rl, to, tl = R.decode(np64(q), kp, vp, table, lens, np.arange(5), **weight_parts("mxfp8", 14), **kw)
     # bf16 subnormals: half a step of 2^-133; scores and values this far down underflow in fp32 terms of 2^-126 each
     floor = 2.0**-134 + 200 * 2.0**-126
     top = float(torch.finfo(torch.bfloat16).max)
