@@ -896,10 +896,10 @@ int check_status_ws(const void* ws, size_t ws_bytes) {
   return !ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < 256 ? JATTN_ERR_WORKSPACE : JATTN_OK;
 }
 
-// Total rows of a copy: its 16-byte pieces are numbered by the blocks of a
-// one-dimensional grid of 256 threads.
+// Total rows of a copy: at least one to a CTA of a one-dimensional grid, and the
+// 16-byte pieces of a row counted in 32 bits.
 bool too_many_rows(const jattn_cache_t* c, int64_t total) {
-  return total > INT32_MAX || total * c->H * (c->D / 8) > (int64_t(INT32_MAX) - 1) * 256;
+  return total > INT32_MAX || static_cast<int64_t>(c->H) * (c->D / 8) > (1 << 24);
 }
 
 CacheView cache_view(const jattn_cache_t* c, const int32_t* page_table, int64_t max_pages) {

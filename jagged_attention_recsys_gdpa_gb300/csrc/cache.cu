@@ -1,11 +1,15 @@
 // The paged key/value cache: writing new rows (as they are, or quantised to
 // MXFP8, keys optionally rotated) and reading rows back as jagged bf16.
 //
-// Both are bandwidth-bound copies. One thread holds one 16-byte piece (8
-// values) of a row and head, K and V together; consecutive threads hold
-// consecutive pieces, so jagged rows move in whole lines and page rows in
-// 128- or 256-byte runs. MXFP8: four neighbouring threads hold the 32 values
-// of a block, whose largest magnitude is a maximum over two shuffles.
+// Both are copies, bound by memory. A CTA takes a few consecutive jagged rows:
+// a thread per row finds its sequence and its place in the cache while the other
+// loads are on their way, then every thread moves kUnits units (K and V of each),
+// so that enough loads are in flight. Consecutive threads hold consecutive units,
+// so jagged rows move in whole lines and page rows in runs of a head's row. A unit
+// is 16 bytes of bf16; quantising, the 32 values of one block (its largest
+// magnitude needs no exchange between threads, and packed 16-bit arithmetic does
+// most of the work: with 8 values a thread the instructions, not memory, were the
+// bound); reading MXFP8 back, 16 codes.
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -17,6 +21,7 @@ namespace jattn {
 namespace {
 
 constexpr int kCacheBlock = 256;
+constexpr int kMaxRows = 64;  // rows of a CTA
 
 // The sequence of jagged row r and its index in it: false (nothing to do) for
 // rows behind the last sequence.
@@ -26,54 +31,40 @@ __device__ __forceinline__ bool find_row(const int64_t* off, int64_t B, int64_t 
     i = 0;
     return r < B;
   }
-  if (r >= off[B]) return false;
+  if (r >= __ldg(off + B)) return false;
   int64_t lo = 0, hi = B - 1;  // the last b in [0, B) with off[b] <= r
   while (lo < hi) {
     const int64_t mid = (lo + hi + 1) >> 1;
-    if (off[mid] <= r) lo = mid;
+    if (__ldg(off + mid) <= r) lo = mid;
     else hi = mid - 1;
   }
   b = lo;
-  i = r - off[lo];
-  return i >= 0 && r < off[lo + 1];  // false where the offsets are no prefix sums
+  i = r - __ldg(off + lo);
+  return i >= 0 && r < __ldg(off + lo + 1);  // false where the offsets are no prefix sums
 }
 
-// Position start[b] + i within the sequence's pages: false for an inactive
-// sequence (start < 0) or, with the status set, past its pages.
-__device__ __forceinline__ bool place(const CacheView& c, const int64_t* start, int64_t b, int64_t i, int64_t& pos,
-                                      DevStatus* status) {
-  const int64_t s = start != nullptr ? start[b] : 0;
-  if (s < 0) return false;
+// Where a jagged row lies in the cache.
+struct Row {
+  int64_t at;  // row of the [n_pages * H * page_size, D] view, head 0; or one of the next two
+  int64_t pos;
+};
+constexpr int64_t kSkip = -2, kBadPage = -1;
+
+__device__ __forceinline__ Row place(const CacheView& c, const int64_t* off, const int64_t* start, int64_t B, int64_t r,
+                                     DevStatus* status) {
+  int64_t b, i;
+  if (!find_row(off, B, r, b, i)) return Row{kSkip, 0};
+  const int64_t s = start != nullptr ? __ldg(start + b) : 0;
+  if (s < 0) return Row{kSkip, 0};  // an inactive sequence
   const int64_t cap = c.max_pages << c.page_shift;
   if (s > cap || i >= cap - s) {
     record_error(status, JATTN_ERR_LENGTH, 82, static_cast<int>(b));
-    return false;
+    return Row{kSkip, 0};
   }
-  pos = s + i;
-  return true;
+  return Row{cache_row(c, b, s + i, status), s + i};
 }
 
-// 8 values to E4M3 codes with the block's shared exponent (the Microscaling
-// rule of jattn_mxfp8_quantize, one scale per 32 neighbours of a row). A block
-// that holds a NaN or an infinity gets exponent 255, which makes it NaN. The
-// four threads of a block are neighbouring lanes and all call this.
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], uint32_t& e) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(x[q]) & 0x7fffffffu);
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  const uint32_t field = m >> 23;
-  e = field == 255u ? 255u : field > 8u ? field - 8u : 0u;
-  if (e == 255u) return make_uint2(0u, 0u);
-  const float inv = __uint_as_float((254u - e) << 23);  // 2^(127 - e), exact
-  uint2 w;
-  w.x = pack_e4m3x2(x[0] * inv, x[1] * inv) | (pack_e4m3x2(x[2] * inv, x[3] * inv) << 16);
-  w.y = pack_e4m3x2(x[4] * inv, x[5] * inv) | (pack_e4m3x2(x[6] * inv, x[7] * inv) << 16);
-  return w;
-}
-
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
+__device__ __forceinline__ void unpack8(const uint4& w, float* x) {
   const uint32_t in[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -82,137 +73,277 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
   }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+__device__ __forceinline__ uint4 pack8(const float* x) {
   return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                     pack_bf16x2(x[6], x[7]));
 }
 
-template <bool MX>
-__global__ void __launch_bounds__(kCacheBlock)
-    append_kernel(CacheView c, int64_t B, int64_t total, const int64_t* __restrict__ off,
-                  const int64_t* __restrict__ start, const uint4* __restrict__ k, const uint4* __restrict__ v, int D,
-                  const float* __restrict__ cos_t, const float* __restrict__ sin_t, int rope_rows,
-                  DevStatus* status) {
-  const int per_head = D / 8, per_row = c.H * per_head;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kCacheBlock + threadIdx.x;
-  if (off != nullptr) check_offsets(off, B, total, t, static_cast<int64_t>(gridDim.x) * kCacheBlock, status);
-  const int64_t r = t / per_row;
-  const int hp = static_cast<int>(t % per_row), h = hp / per_head, piece = hp % per_head;
-  int64_t b = 0, i = 0, pos = 0, row = -1;
-  if (r < total && find_row(off, B, r, b, i) && place(c, start, b, i, pos, status))
-    row = cache_row(c, b, pos, status);
-  uint4 kw = make_uint4(0u, 0u, 0u, 0u), vw = kw;
-  if (row >= 0) {
-    row += static_cast<int64_t>(h) << c.page_shift;
-    kw = k[t];
-    vw = v[t];
-  }
-  float x[8];
-  const bool rot = cos_t != nullptr;
-  if (rot) {
-    unpack8(kw, x);
-    const bool ok = row >= 0 && pos < rope_rows;
-    if (row >= 0 && !ok) record_error(status, JATTN_ERR_ROPE, 83, rope_rows);
-    if (ok) {
-      const float4 c4 = *reinterpret_cast<const float4*>(cos_t + pos * (D / 2) + 4 * piece);
-      const float4 s4 = *reinterpret_cast<const float4*>(sin_t + pos * (D / 2) + 4 * piece);
-      const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+// N values (their pairs from `pair` on) rotated by the table rows c, s. Each
+// product and the sum is rounded by itself, so that the rows are those of the
+// written-out formula bit for bit.
+template <int N>
+__device__ __forceinline__ void rotate(float (&x)[N], const float* c, const float* s, int pair) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        // each product and the sum rounded by themselves, so that the rows are
-        // those of the written-out formula bit for bit
-        const float a = x[2 * e], d = x[2 * e + 1];
-        x[2 * e] = __fsub_rn(__fmul_rn(a, cs[e]), __fmul_rn(d, sn[e]));
-        x[2 * e + 1] = __fadd_rn(__fmul_rn(a, sn[e]), __fmul_rn(d, cs[e]));
+  for (int e = 0; e < N / 2; e += 4) {
+    const float4 c4 = __ldg(reinterpret_cast<const float4*>(c + pair + e));
+    const float4 s4 = __ldg(reinterpret_cast<const float4*>(s + pair + e));
+    const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = x[2 * (e + i)], d = x[2 * (e + i) + 1];
+      x[2 * (e + i)] = __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(d, sn[i]));
+      x[2 * (e + i) + 1] = __fadd_rn(__fmul_rn(a, sn[i]), __fmul_rn(d, cs[i]));
+    }
+  }
+}
+
+// The exponent of a block whose largest magnitude has the fp32 exponent field
+// given (the Microscaling rule of jattn_mxfp8_quantize, one scale per 32
+// neighbours of a row). A block with a NaN or an infinity gets 255: NaN.
+__device__ __forceinline__ uint32_t block_exponent(uint32_t field) {
+  return field == 255u ? 255u : field > 8u ? field - 8u : 0u;
+}
+
+// 32 bf16 values (packed) to codes. The scale 2^(127 - e) is a bf16 number and
+// the products are exact down to bf16's subnormals, far below the smallest code.
+__device__ __forceinline__ uint32_t quantise32(const uint4 (&w)[4], uint4 (&codes)[2]) {
+  const uint32_t* in = reinterpret_cast<const uint32_t*>(w);
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = __vmaxu2(m, in[i] & 0x7fff7fffu);
+  const uint32_t e = block_exponent(max(m & 0xffffu, m >> 16) >> 7);
+  const uint32_t inv = e == 255u ? 0u : (254u - e) * 0x00800080u;
+  uint32_t* out = reinterpret_cast<uint32_t*>(codes);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    uint32_t half[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&in[2 * i + j]),
+                                       *reinterpret_cast<const __nv_bfloat162*>(&inv));
+      const uint32_t p = *reinterpret_cast<const uint32_t*>(&y);
+      half[j] = pack_e4m3x2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
+    }
+    out[i] = e == 255u ? 0u : half[0] | (half[1] << 16);
+  }
+  return e;
+}
+
+// The same of 32 fp32 values.
+__device__ __forceinline__ uint32_t quantise32(const float (&x)[32], uint4 (&codes)[2]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+  const uint32_t e = block_exponent(m >> 23);
+  const float inv = __uint_as_float((254u - min(e, 254u)) << 23);
+  uint32_t* out = reinterpret_cast<uint32_t*>(codes);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = pack_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
+                       (pack_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
+    out[i] = e == 255u ? 0u : w;
+  }
+  return e;
+}
+
+struct AppendArgs {
+  CacheView c;
+  const int64_t* off;
+  const int64_t* start;
+  const uint4* k;
+  const uint4* v;
+  const float* cos_t;  // nullptr: no rotation
+  const float* sin_t;
+  int64_t B, total;
+  int D, rope_rows, rows;  // rows of a CTA
+  DevStatus* status;
+};
+
+template <bool MX, int N>
+__global__ void __launch_bounds__(kCacheBlock) append_kernel(AppendArgs a) {
+  constexpr int P = MX ? 4 : 1;  // 16-byte pieces of a unit
+  __shared__ Row row[kMaxRows];
+  const int per_head = a.D / (8 * P), per_row = a.c.H * per_head;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(a.rows), a.total - row0)), units = rows * per_row;
+  if (a.off != nullptr)
+    check_offsets(a.off, a.B, a.total, static_cast<int64_t>(blockIdx.x) * kCacheBlock + threadIdx.x,
+                  static_cast<int64_t>(gridDim.x) * kCacheBlock, a.status);
+  for (int base = 0; base < units; base += kCacheBlock * N) {
+    uint4 k[N][P], v[N][P];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = base + i * kCacheBlock + static_cast<int>(threadIdx.x);
+      if (u >= units) break;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        k[i][p] = __ldcs(a.k + (row0 * per_row + u) * P + p);
+        v[i][p] = __ldcs(a.v + (row0 * per_row + u) * P + p);
+      }
+    }
+    if (base == 0) {
+      if (static_cast<int>(threadIdx.x) < rows) {
+        row[threadIdx.x] = place(a.c, a.off, a.start, a.B, row0 + threadIdx.x, a.status);
+        if (a.cos_t != nullptr && row[threadIdx.x].at >= 0 && row[threadIdx.x].pos >= a.rope_rows)
+          record_error(a.status, JATTN_ERR_ROPE, 83, a.rope_rows);
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = base + i * kCacheBlock + static_cast<int>(threadIdx.x);
+      if (u >= units) break;
+      const int r = u / per_row, hp = u - r * per_row, h = hp / per_head, unit = hp - h * per_head;
+      const Row to = row[r];
+      if (to.at < 0) continue;
+      const int64_t at = (to.at + (static_cast<int64_t>(h) << a.c.page_shift)) * per_head + unit;
+      const bool turn = a.cos_t != nullptr && to.pos < a.rope_rows;
+      const float* cos_row = a.cos_t + to.pos * (a.D / 2);
+      const float* sin_row = a.sin_t + to.pos * (a.D / 2);
+      if constexpr (MX) {
+        uint4 codes[2];
+        uint32_t e;
+        if (turn) {
+          float x[32];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) unpack8(k[i][p], x + 8 * p);
+          rotate<32>(x, cos_row, sin_row, unit * 16);
+          e = quantise32(x, codes);
+        } else {
+          e = quantise32(k[i], codes);
+        }
+        static_cast<uint4*>(a.c.k)[2 * at] = codes[0];
+        static_cast<uint4*>(a.c.k)[2 * at + 1] = codes[1];
+        a.c.ks[at] = static_cast<uint8_t>(e);
+        e = quantise32(v[i], codes);
+        static_cast<uint4*>(a.c.v)[2 * at] = codes[0];
+        static_cast<uint4*>(a.c.v)[2 * at + 1] = codes[1];
+        a.c.vs[at] = static_cast<uint8_t>(e);
+      } else {
+        if (turn) {
+          float x[8];
+          unpack8(k[i][0], x);
+          rotate<8>(x, cos_row, sin_row, unit * 4);
+          k[i][0] = pack8(x);
+        }
+        static_cast<uint4*>(a.c.k)[at] = k[i][0];
+        static_cast<uint4*>(a.c.v)[at] = v[i][0];
       }
     }
   }
-  if constexpr (MX) {
-    if (!rot) unpack8(kw, x);
-    uint32_t e;
-    const uint2 kc = quantise8(x, e);
-    float y[8];
-    unpack8(vw, y);
-    uint32_t ev;
-    const uint2 vc = quantise8(y, ev);
-    if (row >= 0) {
-      const int64_t at = row * per_head + piece;
-      static_cast<uint2*>(c.k)[at] = kc;
-      static_cast<uint2*>(c.v)[at] = vc;
-      if ((piece & 3) == 0) {
-        c.ks[at >> 2] = static_cast<uint8_t>(e);
-        c.vs[at >> 2] = static_cast<uint8_t>(ev);
+}
+
+// 16 codes and their exponent as bf16.
+__device__ __forceinline__ void read16(const uint4& w, float scale, uint4 (&out)[2]) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t* o = reinterpret_cast<uint32_t*>(out);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = e4m3x2_value(in[i] & 0xffffu), y = e4m3x2_value(in[i] >> 16);
+    o[2 * i] = pack_bf16x2(x.x * scale, x.y * scale);
+    o[2 * i + 1] = pack_bf16x2(y.x * scale, y.y * scale);
+  }
+}
+
+struct ReadArgs {
+  CacheView c;
+  const int64_t* off;
+  const int64_t* start;
+  uint4* k;
+  uint4* v;
+  int64_t B, total;
+  int D, rows;
+  DevStatus* status;
+};
+
+template <bool MX, int N>
+__global__ void __launch_bounds__(kCacheBlock) read_kernel(ReadArgs a) {
+  constexpr int P = MX ? 2 : 1;  // 16-byte pieces that a unit becomes
+  __shared__ Row row[kMaxRows];
+  const int per_head = a.D / (8 * P), per_row = a.c.H * per_head;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows;
+  const int rows = static_cast<int>(min(static_cast<int64_t>(a.rows), a.total - row0)), units = rows * per_row;
+  if (static_cast<int>(threadIdx.x) < rows)
+    row[threadIdx.x] = place(a.c, a.off, a.start, a.B, row0 + threadIdx.x, a.status);
+  check_offsets(a.off, a.B, a.total, static_cast<int64_t>(blockIdx.x) * kCacheBlock + threadIdx.x,
+                static_cast<int64_t>(gridDim.x) * kCacheBlock, a.status);
+  __syncthreads();
+  for (int base = 0; base < units; base += kCacheBlock * N) {
+    uint4 k[N], v[N];
+    float ks[N], vs[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int u = base + i * kCacheBlock + static_cast<int>(threadIdx.x);
+      if (u >= units) break;
+      const int r = u / per_row, hp = u - r * per_row, h = hp / per_head, unit = hp - h * per_head;
+      k[i] = v[i] = make_uint4(0u, 0u, 0u, 0u);  // a bad page reads as zeros
+      ks[i] = vs[i] = 0.0f;
+      if (row[r].at < 0) continue;
+      const int64_t at = (row[r].at + (static_cast<int64_t>(h) << a.c.page_shift)) * per_head + unit;
+      k[i] = __ldcs(static_cast<const uint4*>(a.c.k) + at);
+      v[i] = __ldcs(static_cast<const uint4*>(a.c.v) + at);
+      if constexpr (MX) {
+        ks[i] = e8m0_value(__ldg(a.c.ks + at / 2));
+        vs[i] = e8m0_value(__ldg(a.c.vs + at / 2));
       }
     }
-  } else if (row >= 0) {
-    const int64_t at = row * per_head + piece;
-    static_cast<uint4*>(c.k)[at] = rot ? pack8(x) : kw;
-    static_cast<uint4*>(c.v)[at] = vw;
-  }
-}
-
-// One 16-byte piece of a bf16 row, or 8 codes and their scale as bf16.
-template <bool MX>
-__device__ __forceinline__ uint4 read_piece(const void* p, const uint8_t* scales, int64_t at) {
-  if constexpr (!MX) return static_cast<const uint4*>(p)[at];
-  const uint2 w = static_cast<const uint2*>(p)[at];
-  const float s = e8m0_value(scales[at >> 2]);
-  float x[8];
-  const uint32_t in[4] = {w.x & 0xffffu, w.x >> 16, w.y & 0xffffu, w.y >> 16};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = e4m3x2_value(in[e]);
-    x[2 * e] = f.x * s;
-    x[2 * e + 1] = f.y * s;
+    for (int i = 0; i < N; ++i) {
+      const int u = base + i * kCacheBlock + static_cast<int>(threadIdx.x);
+      if (u >= units) break;
+      if (row[u / per_row].at == kSkip) continue;
+      const int64_t to = (row0 * per_row + u) * P;
+      if constexpr (MX) {
+        uint4 x[2];
+        read16(k[i], ks[i], x);
+        __stcs(a.k + to, x[0]);
+        __stcs(a.k + to + 1, x[1]);
+        read16(v[i], vs[i], x);
+        __stcs(a.v + to, x[0]);
+        __stcs(a.v + to + 1, x[1]);
+      } else {
+        __stcs(a.k + to, k[i]);
+        __stcs(a.v + to, v[i]);
+      }
+    }
   }
-  return pack8(x);
 }
 
-template <bool MX>
-__global__ void __launch_bounds__(kCacheBlock)
-    read_kernel(CacheView c, int64_t B, int64_t total, const int64_t* __restrict__ off,
-                const int64_t* __restrict__ start, uint4* __restrict__ k, uint4* __restrict__ v, int D,
-                DevStatus* status) {
-  const int per_head = D / 8, per_row = c.H * per_head;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kCacheBlock + threadIdx.x;
-  if (off != nullptr) check_offsets(off, B, total, t, static_cast<int64_t>(gridDim.x) * kCacheBlock, status);
-  const int64_t r = t / per_row;
-  const int hp = static_cast<int>(t % per_row), h = hp / per_head, piece = hp % per_head;
-  int64_t b, i, pos;
-  if (r >= total || !find_row(off, B, r, b, i) || !place(c, start, b, i, pos, status)) return;
-  const int64_t row = cache_row(c, b, pos, status);
-  uint4 kw = make_uint4(0u, 0u, 0u, 0u), vw = kw;  // a bad page reads as zeros
-  if (row >= 0) {
-    const int64_t at = (row + (static_cast<int64_t>(h) << c.page_shift)) * per_head + piece;
-    kw = read_piece<MX>(c.k, c.ks, at);
-    vw = read_piece<MX>(c.v, c.vs, at);
-  }
-  k[t] = kw;
-  v[t] = vw;
+// Rows of a CTA and its number of CTAs, for `units` units per thread.
+int rows_of(int per_row, int units) {
+  const int r = kCacheBlock * units / per_row;
+  return r < 1 ? 1 : r > kMaxRows ? kMaxRows : r;
 }
+unsigned ctas_of(int64_t total, int rows) { return static_cast<unsigned>((total + rows - 1) / rows); }
 
-unsigned blocks_for(int64_t total, int H, int D) {
-  return static_cast<unsigned>((total * H * (D / 8) + kCacheBlock - 1) / kCacheBlock);
-}
+// One unit per thread while that leaves SMs idle (a few rows), else four (16-byte
+// units) or two (blocks of 32 values).
+bool few_rows(int64_t total, int per_row) { return total * per_row <= int64_t(152) * 2 * kCacheBlock; }
 
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheView& c, bool mx, int64_t B, int64_t total, const int64_t* off,
                                 const int64_t* start, const void* k, const void* v, int D, const float* cos_t,
                                 const float* sin_t, int rope_rows, DevStatus* status, cudaStream_t stream) {
-  const auto kernel = mx ? append_kernel<true> : append_kernel<false>;
-  kernel<<<blocks_for(total, c.H, D), kCacheBlock, 0, stream>>>(c, B, total, off, start, static_cast<const uint4*>(k),
-                                                               static_cast<const uint4*>(v), D, cos_t, sin_t,
-                                                               rope_rows, status);
+  const int per_row = c.H * (D / (mx ? 32 : 8));
+  const int units = few_rows(total, per_row) ? 1 : mx ? 2 : 4;
+  const AppendArgs a{c,     off, start, static_cast<const uint4*>(k), static_cast<const uint4*>(v),
+                     cos_t, sin_t, B,   total, D, rope_rows, rows_of(per_row, units), status};
+  const auto kernel = mx ? (units == 1 ? append_kernel<true, 1> : append_kernel<true, 2>)
+                         : (units == 1 ? append_kernel<false, 1> : append_kernel<false, 4>);
+  kernel<<<ctas_of(total, a.rows), kCacheBlock, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_cache_read(const CacheView& c, bool mx, int64_t B, int64_t total, const int64_t* off,
                               const int64_t* start, void* k, void* v, int D, DevStatus* status,
                               cudaStream_t stream) {
-  const auto kernel = mx ? read_kernel<true> : read_kernel<false>;
-  kernel<<<blocks_for(total, c.H, D), kCacheBlock, 0, stream>>>(c, B, total, off, start, static_cast<uint4*>(k),
-                                                               static_cast<uint4*>(v), D, status);
+  const int per_row = c.H * (D / (mx ? 16 : 8));
+  const int units = few_rows(total, per_row) ? 1 : 4;
+  const ReadArgs a{c, off, start, static_cast<uint4*>(k), static_cast<uint4*>(v), B, total, D, rows_of(per_row, units), status};
+  const auto kernel = mx ? (units == 1 ? read_kernel<true, 1> : read_kernel<true, 4>)
+                         : (units == 1 ? read_kernel<false, 1> : read_kernel<false, 4>);
+  kernel<<<ctas_of(total, a.rows), kCacheBlock, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -25,6 +25,7 @@
 // leaves its piece (m, l and O in fp32), the CTA joins those of its workers, and
 // a second kernel those of several CTAs, always in their order. Results do not
 // depend on what runs when.
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -38,15 +39,13 @@ namespace {
 constexpr int kWarps = 4;     // per CTA
 constexpr int kThreads = kWarps * 32;
 constexpr int kSms = 152;
-#ifndef MXC
-#define MXC 3
-#define BFC 3
-#endif
-constexpr int ctas_per_sm(bool mx, int nr) { return nr == 1 ? (mx ? MXC : BFC) : 2; }
-constexpr int stages_of(bool mx, int nr) { return ctas_per_sm(mx, nr) == 2 ? 3 : ctas_per_sm(mx, nr) == 3 ? 2 : 2; }
+// CTAs per SM and steps held per worker: with 8 rows three CTAs of four warps fit
+// the registers, and two steps each the shared memory; twelve warps hide more
+// than a third step each does (decode_mixed 265 against 290 us, MXFP8 296 and 331).
+constexpr int ctas_per_sm(int nr) { return nr == 1 ? 3 : 2; }
+constexpr int stages_of(int nr) { return nr == 1 ? 2 : 3; }
 constexpr int kMaxCtas = 3 * kSms;
-constexpr int kMinSteps = 2;  // per worker, as long as there are few steps in all
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 constexpr float kLn2 = 0.6931471805599453f;
 // The running maximum moves when a row's scores exceed it by more than 2^kSlack,
 // so that most steps rescale nothing; weights then reach 2^kSlack at most.
@@ -216,7 +215,7 @@ struct Layout {
 // [worker][stage] barriers: copied, and read by all of the worker's warps.
 template <int D, bool MX, int NR>
 constexpr int smem_bytes() {
-  return 1024 + kWarps * stages_of(MX, NR) * (8192 + 2 * Layout<D, MX>::keys * Layout<D, MX>::scale + 16);
+  return 1024 + kWarps * stages_of(NR) * (8192 + 2 * Layout<D, MX>::keys * Layout<D, MX>::scale + 16);
 }
 
 // Byte offset of 16-byte piece `chunk` of row r in a step of STEP rows: rows of
@@ -431,56 +430,76 @@ __device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int
 }
 
 // ---------------------------------------------------------------- pieces
-// Scratch. [workers][2]: the piece of the unit that the worker's run begins
-// inside of (slot 0), and of the unit that it begins and leaves unfinished
-// (slot 1). The workers of a CTA meet when they are done and join their pieces:
-// a unit that lies within the CTA is finished there. Of the others [ctas][2]
-// hold the CTA's one piece of a unit from an earlier CTA (0) and of one that goes
-// on (1), and join[cta] = (last CTA of the latter, or -1; sequence, tile, head).
+// A run leaves at most two pieces: of the unit that it begins inside of (its
+// head) and of the unit that it begins and leaves unfinished (its tail). The
+// workers of a CTA meet when they are done and join theirs: a unit that lies
+// within the CTA is finished there. A run's last piece waits for that in the
+// worker's ring, a head that ended before in scratch: [workers][tile]. Of units
+// that reach over CTAs scratch has [ctas][2]: the CTA's one piece of a unit from
+// an earlier CTA (0) and of one that goes on (1), and join[cta] = (last CTA of
+// the latter, or -1; sequence, tile, head).
 struct Scratch {
-  float* acc;   // [workers][2][tile][D], softmax rows divided by l
-  float2* ml;   // [workers][2][tile]: m, l
+  float* acc;   // [workers][tile][D], softmax rows divided by l
+  float2* ml;   // [workers][tile]: m, l
   float* cacc;  // [ctas][2][tile][D]
   float2* cml;
   int4* join;
 };
 
 __host__ __device__ inline size_t scratch_bytes(int ctas, int per_cta, int tile, int D) {
-  return static_cast<size_t>(ctas) * (16 + static_cast<size_t>(2 + 2 * per_cta) * tile * (8 + 4 * static_cast<size_t>(D)));
+  return static_cast<size_t>(ctas) * (16 + static_cast<size_t>(2 + per_cta) * tile * (8 + 4 * static_cast<size_t>(D)));
 }
 
 __host__ __device__ inline Scratch carve(void* base, int ctas, int per_cta, int tile, int D) {
-  const size_t rows = static_cast<size_t>(ctas) * 2 * tile;
+  const size_t rows = static_cast<size_t>(ctas) * tile;
   Scratch s;
   s.acc = static_cast<float*>(base);
   s.cacc = s.acc + rows * per_cta * D;
-  s.ml = reinterpret_cast<float2*>(s.cacc + rows * D);
+  s.ml = reinterpret_cast<float2*>(s.cacc + rows * 2 * D);
   s.cml = s.ml + rows * per_cta;
-  s.join = reinterpret_cast<int4*>(s.cml + rows);
+  s.join = reinterpret_cast<int4*>(s.cml + rows * 2);
   return s;
 }
 
-// One row (E of its columns) of n pieces joined by a warp, the pieces' rows
-// given by row(i): m and l of the whole, and its accumulator divided by l.
-template <int E, typename Row>
-__device__ __forceinline__ void join_row(const DecodeArgs& a, const float* acc, const float2* ml, int D, int col, int n,
-                                         Row row, float (&x)[E], float& m, float& l) {
+// One row (E of its columns) of up to N pieces, joined by a warp: m and l of the
+// whole, and its accumulator divided by l. at(i): where piece i has its
+// accumulator's row and its m and l (shared or global memory).
+template <int E, int N, typename At>
+__device__ __forceinline__ void join_row(const DecodeArgs& a, int col, int n, At at, float (&x)[E], float& m, float& l) {
+  float y[N][E];
+  float2 ml[N];
 #pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = 0.0f;
+  for (int i = 0; i < N; ++i) {
+    ml[i] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[i][e] = 0.0f;
+    if (i >= n) continue;
+    const float* acc;
+    const float2* stats;
+    at(i, acc, stats);
+    ml[i] = *stats;
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[i][e] = acc[col + e];
+  }
   m = -INFINITY;
   l = 0.0f;
-  float use = 0.0f, inv = 1.0f;
-  if (a.act == JATTN_SOFTMAX) {
-    for (int i = 0; i < n; ++i) m = fmaxf(m, ml[row(i)].x);
-    use = m == -INFINITY ? 0.0f : m;
-    for (int i = 0; i < n; ++i) l = fmaf(ex2_approx(ml[row(i)].x - use), ml[row(i)].y, l);
-    inv = inverse_sum(l);
-  }
-  for (int i = 0; i < n; ++i) {
-    const int64_t r = row(i);
-    const float w = a.act == JATTN_SOFTMAX ? ex2_approx(ml[r].x - use) * ml[r].y * inv : 1.0f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = fmaf(w, acc[r * D + col + e], x[e]);
+  for (int i = 0; i < N; ++i) m = fmaxf(m, ml[i].x);
+  const bool soft = a.act == JATTN_SOFTMAX;
+  const float use = m == -INFINITY ? 0.0f : m;
+  float w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    w[i] = soft ? ex2_approx(ml[i].x - use) * ml[i].y : 1.0f;
+    l += w[i];
+  }
+  const float inv = soft ? inverse_sum(l) : 1.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = fmaf(w[i] * inv, y[i][e], x[e]);
   }
 }
 
@@ -504,10 +523,11 @@ __device__ __forceinline__ int64_t query_rows(const DecodeArgs& a, int b, int64_
 
 // What a worker leaves for its CTA.
 struct Left {
-  int head;        // rows of slot 0 (0: none)
-  int head_ends;   // the unit of slot 0 ends in this run
-  int tail;        // rows of slot 1 (0: none)
-  int b, tile, h;  // of slot 1's unit
+  int head;        // rows of the head (0: none)
+  int head_ends;   // its unit ends in this run
+  int head_last;   // the head is the run's last piece
+  int tail;        // rows of the tail (0: none)
+  int b, tile, h;  // of the tail's unit
   int last_cta;    // where that unit ends
 };
 
@@ -597,12 +617,12 @@ __device__ __forceinline__ void clear_rows(uint32_t vs, int pos0, int lo, int hi
 }
 
 template <int D, bool MX, int NR, int WM>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(MX, NR))
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
     decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   void* scratch) {
   using L = Layout<D, MX>;
   constexpr int step = L::keys * WM, tile = 8 * NR * WM, KS = D / 16, MT = L::sub / 16, per_cta = kWarps / WM;
-  constexpr int kStages = stages_of(MX, NR);
+  constexpr int kStages = stages_of(NR);
   extern __shared__ unsigned char smem_raw[];
   __shared__ int64_t start[kThreads];
   __shared__ Left left[per_cta];
@@ -612,17 +632,19 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MX, NR))
   const Scratch sc = carve(scratch, gridDim.x, per_cta, tile, D);
 
   const int64_t total = total_steps(a, tile, step, start);
-  const int64_t share = max((total + workers - 1) / workers, static_cast<int64_t>(kMinSteps));
+  const int64_t share = (total + workers - 1) / workers;
   const int64_t first = me * share, last = min(first + share, total);  // this worker's run [first, last)
-  if (tid == 0) left[in_cta] = Left{0, 0, 0, 0, 0, 0, 0};
+  if (tid == 0) left[in_cta] = Left{};
+  unsigned char* const smem_base = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+  constexpr int ring_bytes = kStages * 8192 * WM;
+  static_assert(tile * (D * 4 + 8) <= ring_bytes, "a worker's ring holds a piece");
   if (first < last) {
     Place in = find_place(a, tile, step, start, first);  // the step that is copied next
     Place at = in;                                       // the step that is computed next
-    const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t ring = smem + in_cta * (kStages * 8192 * WM);
+    const uint32_t smem = smem_u32(smem_base);
+    const uint32_t ring = smem + in_cta * ring_bytes;
     const uint32_t scale_ring = smem + kWarps * kStages * 8192 + in_cta * (kStages * 2 * step * L::scale);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + (smem - smem_u32(smem_raw)) +
-                                                 kWarps * kStages * (8192 + 2 * L::keys * L::scale)) +
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem_base + kWarps * kStages * (8192 + 2 * L::keys * L::scale)) +
                      in_cta * (2 * kStages);
     uint64_t* empty = full + kStages;
     if (tid == 0) {
@@ -669,30 +691,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MX, NR))
     bool ok = true;
     int done = 0;
     for (; done < steps; ++done) {
-      if (rare(!wait_full(a, full + stage_no, phase))) {
-        ok = false;
-        break;
-      }
-      if (warp_m == 0 && loaded < steps) {
-        // the stage after the one in flight was read in the step before this one
-        const int s = stage_no == 0 ? kStages - 1 : stage_no - 1;
-        if constexpr (WM == 1) {
-          __syncwarp();
-        } else {
-          if (loaded >= kStages && !wait_full(a, empty + s, static_cast<uint32_t>(loaded / kStages - 1) & 1u)) {
-            ok = false;
-            break;
-          }
-        }
-        load_step<D, MX, WM>(a, &k_map, &v_map, in, page, ring + s * (8192 * WM), scale_ring + s * (2 * step * L::scale),
-                             full + s, box, lane);
-        if (++loaded < steps) {
-          advance(in, a, tile, step);
-          page = box_page(a, in, step, box, lane);
-        }
-      }
-
-      if (rare(fresh)) {
+      if (rare(fresh)) {  // its rows arrive while its first step does
         fresh = false;
         n_steps = 0;
         ref = -1;
@@ -754,6 +753,28 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MX, NR))
               for (int i = 0; i < 2; ++i) f[g][i] *= pow2(-__shfl_sync(0xffffffffu, e, (2 * c + i) * 4));
             }
           }
+        }
+      }
+      if (rare(!wait_full(a, full + stage_no, phase))) {
+        ok = false;
+        break;
+      }
+      if (warp_m == 0 && loaded < steps) {
+        // the stage after the one in flight was read in the step before this one
+        const int s = stage_no == 0 ? kStages - 1 : stage_no - 1;
+        if constexpr (WM == 1) {
+          __syncwarp();
+        } else {
+          if (loaded >= kStages && !wait_full(a, empty + s, static_cast<uint32_t>(loaded / kStages - 1) & 1u)) {
+            ok = false;
+            break;
+          }
+        }
+        load_step<D, MX, WM>(a, &k_map, &v_map, in, page, ring + s * (8192 * WM), scale_ring + s * (2 * step * L::scale),
+                             full + s, box, lane);
+        if (++loaded < steps) {
+          advance(in, a, tile, step);
+          page = box_page(a, in, step, box, lane);
         }
       }
       ++n_steps;
@@ -1058,7 +1079,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MX, NR))
       const bool unit_ends = at.t == at.s.steps - 1, run_ends = done == steps - 1;
       if (rare(unit_ends || run_ends)) {
         const bool begun = at.t == n_steps - 1;  // the unit's first step is in this run
-        const int slot = begun ? 1 : 0;
+        // the run's last piece goes to the ring: nothing is copied into it any more, but other warps may still read
+        float* acc = run_ends ? reinterpret_cast<float*>(smem_base + in_cta * ring_bytes)
+                              : sc.acc + static_cast<int64_t>(me) * tile * D;
+        float2* stats = run_ends ? reinterpret_cast<float2*>(acc + tile * D) : sc.ml + static_cast<int64_t>(me) * tile;
+        if (WM > 1 && run_ends) worker_barrier<WM>(in_cta);
         if (live) {
           const float norm = row_norm(a, at.s.n);
 #pragma unroll
@@ -1094,9 +1119,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MX, NR))
                   }
                 }
               } else {
-                const int64_t row = (static_cast<int64_t>(me) * 2 + slot) * tile + warp_m * (8 * NR) + 8 * g + 2 * c + i;
-                if (lane < 4) sc.ml[row] = make_float2(m[g][i], l[g][i]);
-                float* dst = sc.acc + row * D;
+                const int row = warp_m * (8 * NR) + 8 * g + 2 * c + i;
+                if (lane < 4) stats[row] = make_float2(m[g][i], l[g][i]);
+                float* dst = acc + row * D;
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
                   if constexpr (MX) {
@@ -1123,6 +1148,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MX, NR))
           } else {
             x.head = n;
             x.head_ends = unit_ends;
+            x.head_last = run_ends;
           }
         }
         fresh = true;
@@ -1131,48 +1157,61 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MX, NR))
     }
     if (!ok) {
       // a wait ran out: nothing to join here, and no copy may be in flight when the CTA ends
-      if (tid == 0) left[in_cta] = Left{0, 0, 0, 0, 0, 0, 0};
+      if (tid == 0) left[in_cta] = Left{};
       if (warp_m == 0) {
         for (int i = done; i < loaded; ++i) (void)wait_full(a, full + i % kStages, static_cast<uint32_t>(i / kStages) & 1u);
       }
     }
   }
 
-  // ---- the CTA's pieces: chains of one unit's, each from the incoming unit's (worker 0's slot 0) or from a unit that a
-  // worker began and left (its slot 1), on through the following workers' slots 0
+  launch_dependents();  // the join kernel's CTAs may come; they wait for this kernel's end
+  // ---- the CTA's pieces: chains of one unit's, each from the incoming unit's (worker 0's head) or from a unit that a
+  // worker began and left (its tail), on through the following workers' heads
   __syncthreads();
   constexpr int E = D / 32;
   const int warp = threadIdx.x >> 5;
   int4 going_on = make_int4(-1, 0, 0, 0);
+#pragma unroll 1
   for (int begin = -1; begin < per_cta; ++begin) {
-    const int w0 = max(begin, 0), s0 = begin < 0 ? 0 : 1;
+    const int w0 = max(begin, 0);
+    const bool tail = begin >= 0;
     const Left unit = left[w0];
-    const int n = s0 ? unit.tail : unit.head;
+    const int n = tail ? unit.tail : unit.head;
     if (n == 0) continue;
-    bool ends = s0 == 0 && unit.head_ends;
+    bool ends = !tail && unit.head_ends;
     int len = 1;
     for (int x = w0 + 1; x < per_cta && !ends && left[x].head > 0; ++x) {
       ++len;
       ends = left[x].head_ends;
     }
     for (int r = warp; r < n; r += kWarps) {
-      const int64_t w_first = static_cast<int64_t>(blockIdx.x) * per_cta + w0;
-      const auto row = [&](int i) { return ((w_first + i) * 2 + (i == 0 ? s0 : 0)) * tile + r; };
+      const auto at = [&](int i, const float*& acc, const float2*& stats) {
+        const int w = w0 + i;
+        if ((tail && i == 0) || left[w].head_last) {
+          const float* piece = reinterpret_cast<const float*>(smem_base + w * ring_bytes);
+          acc = piece + r * D;
+          stats = reinterpret_cast<const float2*>(piece + tile * D) + r;
+        } else {
+          const int64_t row = (static_cast<int64_t>(blockIdx.x) * per_cta + w) * tile + r;
+          acc = sc.acc + row * D;
+          stats = sc.ml + row;
+        }
+      };
       float x[E], mj, lj;
-      join_row<E>(a, sc.acc, sc.ml, D, lane * E, len, row, x, mj, lj);
-      if (s0 == 1 && ends) {
+      join_row<E, per_cta>(a, lane * E, len, at, x, mj, lj);
+      if (tail && ends) {
         int64_t q0;
         (void)query_rows(a, unit.b, q0);
         write_row<E>(a, q0, static_cast<int64_t>(unit.tile) * tile + r, unit.h, D, lane * E,
                      static_cast<int>(a.kv_lens[unit.b]), x, mj, lj);
       } else {
-        const int64_t to = (static_cast<int64_t>(blockIdx.x) * 2 + s0) * tile + r;
+        const int64_t to = (static_cast<int64_t>(blockIdx.x) * 2 + (tail ? 1 : 0)) * tile + r;
         if (lane == 0) sc.cml[to] = make_float2(mj, lj);
 #pragma unroll
         for (int e = 0; e < E; ++e) sc.cacc[to * D + lane * E + e] = x[e];
       }
     }
-    if (s0 == 1 && !ends) going_on = make_int4(unit.last_cta, unit.b, unit.tile, unit.h);
+    if (tail && !ends) going_on = make_int4(unit.last_cta, unit.b, unit.tile, unit.h);
   }
   if (threadIdx.x == 0) sc.join[blockIdx.x] = going_on;
 }
@@ -1181,11 +1220,12 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(MX, NR))
 // from it, if one did. D / 4 threads take a row, or a share of a row's pieces.
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(DecodeArgs a, void* scratch, int per_cta, int tile) {
-  constexpr int lanes = D / 4, slots = kJoinThreads / lanes;
-  __shared__ float weight[slots][kMaxCtas];
-  __shared__ float2 row_ml[slots];
+  constexpr int lanes = D / 4, slots = kJoinThreads / lanes, some = 8;  // rows at a time
+  __shared__ float2 weight[some][kMaxCtas];  // m and l, then each piece's share of its row
+  __shared__ float2 row_ml[some];
   __shared__ float4 part[kJoinThreads];
   const Scratch sc = carve(scratch, gridDim.x, per_cta, tile, D);
+  wait_for_dependency();
   const int4 j = sc.join[blockIdx.x];
   if (j.x < 0) return;
   const int n = j.x - static_cast<int>(blockIdx.x) + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1194,27 +1234,29 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(DecodeArgs a, void* 
   const int64_t r0 = static_cast<int64_t>(j.z) * tile;
   const int rows = static_cast<int>(min(static_cast<int64_t>(tile), query_rows(a, j.y, q0) * a.G - r0));
   const auto place = [&](int i, int r) { return ((static_cast<int64_t>(blockIdx.x) + i) * 2 + (i == 0 ? 1 : 0)) * tile + r; };
-  for (int base = 0; base < rows; base += slots) {
-    const int now = min(slots, rows - base), ways = slots / now;
+  for (int base = 0; base < rows; base += some) {
+    const int now = min(some, rows - base), ways = slots / now;
     if (a.act == JATTN_SOFTMAX) {
-      for (int r = warp; r < now; r += kJoinThreads / 32) {
+      for (int i = threadIdx.x; i < now * n; i += kJoinThreads) weight[i % now][i / now] = sc.cml[place(i / now, base + i % now)];
+      __syncthreads();
+      if (warp < now) {
         float m = -INFINITY, l = 0.0f;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, sc.cml[place(i, base + r)].x);
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, weight[warp][i].x);
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
         const float use = m == -INFINITY ? 0.0f : m;
         for (int i = lane; i < n; i += 32) {
-          const float2 ml = sc.cml[place(i, base + r)];
+          const float2 ml = weight[warp][i];
           const float w = ex2_approx(ml.x - use) * ml.y;
-          weight[r][i] = w;
+          weight[warp][i].x = w;
           l += w;
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        if (lane == 0) row_ml[r] = make_float2(m, l);
+        if (lane == 0) row_ml[warp] = make_float2(m, l);
       }
+      __syncthreads();
     }
-    __syncthreads();
     const int r = slot / ways, way = slot % ways;
     const bool on = r < now;
     float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1222,7 +1264,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(DecodeArgs a, void* 
       const float inv = a.act == JATTN_SOFTMAX ? inverse_sum(row_ml[r].y) : 1.0f;
 #pragma unroll 8
       for (int i = way; i < n; i += ways) {
-        const float w = a.act == JATTN_SOFTMAX ? weight[r][i] * inv : 1.0f;
+        const float w = a.act == JATTN_SOFTMAX ? weight[r][i].x * inv : 1.0f;
         const float4 y = *reinterpret_cast<const float4*>(sc.cacc + place(i, base + r) * D + col);
         x.x = fmaf(w, y.x, x.x);
         x.y = fmaf(w, y.y, x.y);
@@ -1264,9 +1306,9 @@ Shape shape_of(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G
   const int64_t step = 4096 / (D * (mx ? 1 : 2)) * s.wm;
   // tiles of all sequences: each has at most one that is not full
   const int64_t tiles = total_q * G / s.tile + (total_q < B ? total_q : B);
-  const int64_t per_cta = kMinSteps * (kWarps / s.wm);
+  const int64_t per_cta = kWarps / s.wm;
   const double steps = static_cast<double>(tiles) * H * static_cast<double>((max_kv + step - 1) / step + 2);
-  const int most = kSms * ctas_per_sm(mx, s.nr);
+  const int most = kSms * ctas_per_sm(s.nr);
   s.ctas = steps / per_cta >= most ? most : static_cast<int>(steps / per_cta) + 1;
   return s;
 }
@@ -1275,12 +1317,27 @@ template <int D, bool MX, int NR, int WM>
 cudaError_t launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, const Shape& s, void* scratch,
                    cudaStream_t stream) {
   constexpr int smem = smem_bytes<D, MX, NR>();
-  cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, MX, NR, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  static std::atomic<uint64_t> ready{0};  // devices (at most 64) whose kernel has its shared memory
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(decode_kernel<D, MX, NR, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+  }
   decode_kernel<D, MX, NR, WM><<<s.ctas, kThreads, smem, stream>>>(a, k, v, scratch);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  join_kernel<D><<<s.ctas, kJoinThreads, 0, stream>>>(a, scratch, kWarps / WM, s.tile);
-  return cudaGetLastError();
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(s.ctas);
+  c.blockDim = dim3(kJoinThreads);
+  c.stream = stream;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, join_kernel<D>, a, scratch, kWarps / WM, s.tile);
 }
 
 template <int D, bool MX>

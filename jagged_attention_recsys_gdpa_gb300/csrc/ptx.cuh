@@ -265,6 +265,13 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
 #undef JATTN_R8
 #undef JATTN_W8
 
+// ---------------------------------------------------------------- programmatic launches
+// A kernel launched with programmatic stream serialisation may start once every
+// CTA of the kernel before it has called the first; it sees that kernel's results
+// after the second.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- warp-level products
 // Four 8x8 matrices of 16-bit elements; lanes 8i .. 8i + 7 give matrix i's rows.
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {

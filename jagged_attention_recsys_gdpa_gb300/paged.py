@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import torch
 
+from . import SOFTMAX, _act, _mask, _width
 from . import _binding as B
 
 _FORMATS = {"bf16": B.CACHE_BF16, "mxfp8": B.CACHE_MXFP8}
@@ -93,21 +94,28 @@ def paged_cache(n_pages, page_size, H, D, format="bf16", device="cuda") -> Paged
 
 
 def _check_rows(cache, x, name):
-    if x.dtype != torch.bfloat16 or x.dim() != 3 or x.device != cache._k.device or not x.is_contiguous():
+    if x.dtype is not torch.bfloat16 or x.dim() != 3 or x.device != cache._k.device or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous bf16 tensor [total, H, D] on the cache's device")
 
 
-def _check_index(cache, t, dtype, n, name):
-    if t.dtype != dtype or t.device != cache._k.device or t.dim() != 1 or (n is not None and t.shape[0] != n) \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor [{'B+1' if n is None else n}] on the cache's "
-                         "device")
+def _check_index(cache, t, n, name):
+    if t.dtype is not torch.int64 or t.shape != (n,) or t.device != cache._k.device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int64 tensor [{n}] on the cache's device")
 
 
 def _check_table(cache, t):
-    if t.dtype != torch.int32 or t.dim() != 2 or t.device != cache._k.device or not t.is_contiguous() \
-            or 0 in t.shape:
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.device != cache._k.device or not t.is_contiguous() \
+            or t.numel() == 0:
         raise ValueError("page_table must be a contiguous int32 tensor [B, max_pages] on the cache's device")
+
+
+def _check_rope(cache, rope):
+    cos, sin = rope
+    for t in rope:
+        if t.dtype is not torch.float32 or t.dim() != 2 or t.shape[1] != cache._c.D // 2 or t.shape != cos.shape \
+                or t.device != cache._k.device or not t.is_contiguous():
+            raise ValueError("rope tables must be two contiguous fp32 tensors [rows, D/2] on the cache's device")
+    return cos, sin
 
 
 def _launch(cache, fn, *args):
@@ -115,8 +123,8 @@ def _launch(cache, fn, *args):
     index = cache._k.device.index
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
-            return fn(*args, status_block(index).data_ptr(), 256, torch.cuda.current_stream(index).cuda_stream)
-    return fn(*args, status_block(index).data_ptr(), 256, torch.cuda.current_stream(index).cuda_stream)
+            return _launch(cache, fn, *args)
+    fn(*args, status_block(index).data_ptr(), 256, torch._C._cuda_getCurrentRawStream(index))
 
 
 def cache_append(cache, k, v, page_table, start, off=None, rope=None):
@@ -126,21 +134,21 @@ def cache_append(cache, k, v, page_table, start, off=None, rope=None):
     row per sequence); rows behind off[B] are skipped. With ``rope`` = (cos, sin)
     tables keys are rotated at their own positions before they are stored. See
     jattn_cache_append."""
-    from . import _rope_tables
-
     _check_table(cache, page_table)
     nb = page_table.shape[0]
     _check_rows(cache, k, "k")
     _check_rows(cache, v, "v")
-    if k.shape != v.shape or k.shape[1] != cache.H or k.shape[2] != cache.D:
+    c = cache._c
+    total = k.shape[0]
+    if k.shape != v.shape or k.shape != (total, c.H, c.D):
         raise ValueError("k and v must be [total, H, D] with the cache's H and D")
-    _check_index(cache, start, torch.int64, nb, "start")
+    _check_index(cache, start, nb, "start")
     if off is not None:
-        _check_index(cache, off, torch.int64, nb + 1, "off")
-    elif k.shape[0] != nb:
+        _check_index(cache, off, nb + 1, "off")
+    elif total != nb:
         raise ValueError("without off there must be one row per sequence")
-    cos, sin = _rope_tables(rope, cache.D, k.device) if rope is not None else (None, None)
-    _launch(cache, B.cache_append, cache._c, nb, k.shape[0], off, start, page_table, k, v, cos, sin)
+    cos, sin = _check_rope(cache, rope) if rope is not None else (None, None)
+    _launch(cache, B.cache_append, c, nb, total, off, start, page_table, k, v, cos, sin)
 
 
 def cache_read(cache, page_table, off, start=None, total=None, k=None, v=None):
@@ -150,9 +158,9 @@ def cache_read(cache, page_table, off, start=None, total=None, k=None, v=None):
     off[-1] (a host read) or to the rows of the given outputs. See jattn_cache_read."""
     _check_table(cache, page_table)
     nb = page_table.shape[0]
-    _check_index(cache, off, torch.int64, nb + 1, "off")
+    _check_index(cache, off, nb + 1, "off")
     if start is not None:
-        _check_index(cache, start, torch.int64, nb, "start")
+        _check_index(cache, start, nb, "start")
     for x, name in ((k, "k"), (v, "v")):
         if x is not None:
             _check_rows(cache, x, name)
@@ -178,8 +186,6 @@ def decode(q, cache, page_table, kv_lens, q_off=None, act="softmax", causal=Fals
     the cache's H. Activations, masks and scale as in ``forward``. ``max_kv``
     bounds kv_lens (default: the table's rows). Rows behind q_off[B] are left as
     they were in ``out`` / ``lse``. No gradient. See jattn_decode."""
-    from . import SOFTMAX, _act, _mask, _width
-
     _check_table(cache, page_table)
     nb, max_pages = page_table.shape
     _check_rows(cache, q, "q")
@@ -189,9 +195,9 @@ def decode(q, cache, page_table, kv_lens, q_off=None, act="softmax", causal=Fals
     c = cache._c
     if D != c.D or Hq == 0 or Hq % c.H:
         raise ValueError("q must have the cache's D and a multiple of its heads")
-    _check_index(cache, kv_lens, torch.int64, nb, "kv_lens")
+    _check_index(cache, kv_lens, nb, "kv_lens")
     if q_off is not None:
-        _check_index(cache, q_off, torch.int64, nb + 1, "q_off")
+        _check_index(cache, q_off, nb + 1, "q_off")
     elif total_q != nb:
         raise ValueError("without q_off there must be one query row per sequence")
     rows = max_pages * c.page_size
