@@ -6,10 +6,9 @@
 // loads are on their way, then every thread moves kUnits units (K and V of each),
 // so that enough loads are in flight. Consecutive threads hold consecutive units,
 // so jagged rows move in whole lines and page rows in runs of a head's row. A unit
-// is 16 bytes of bf16; quantising, the 32 values of one block (its largest
-// magnitude needs no exchange between threads, and packed 16-bit arithmetic does
-// most of the work: with 8 values a thread the instructions, not memory, were the
-// bound); reading MXFP8 back, 16 codes.
+// is 16 bytes of bf16 or, of an MXFP8 cache, 16 values: 32 bytes of bf16 in one
+// access and 16 bytes of codes. (Of 8 values the instructions, not memory, were
+// the bound; of the 32 of a block the accesses lay too far apart.)
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -32,11 +31,18 @@ __device__ __forceinline__ bool find_row(const int64_t* off, int64_t B, int64_t 
     return r < B;
   }
   if (r >= __ldg(off + B)) return false;
-  int64_t lo = 0, hi = B - 1;  // the last b in [0, B) with off[b] <= r
+  // the last b in [0, B) with off[b] <= r: seven probes at a time
+  int64_t lo = 0, hi = B - 1;
   while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if (__ldg(off + mid) <= r) lo = mid;
-    else hi = mid - 1;
+    const int64_t step = (hi - lo + 8) >> 3;
+    int64_t below = 0;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      const int64_t at = lo + i * step;
+      if (at <= hi && __ldg(off + at) <= r) below = i;
+    }
+    lo += below * step;
+    hi = min(hi, lo + step - 1);
   }
   b = lo;
   i = r - __ldg(off + lo);
@@ -45,10 +51,10 @@ __device__ __forceinline__ bool find_row(const int64_t* off, int64_t B, int64_t 
 
 // Where a jagged row lies in the cache.
 struct Row {
-  int64_t at;  // row of the [n_pages * H * page_size, D] view, head 0; or one of the next two
+  int64_t at;  // row of the [n_pages * H * page_size, D] view, head 0; negative: none
   int64_t pos;
 };
-constexpr int64_t kSkip = -2, kBadPage = -1;
+constexpr int64_t kSkip = -2;  // -1: a bad page
 
 __device__ __forceinline__ Row place(const CacheView& c, const int64_t* off, const int64_t* start, int64_t B, int64_t r,
                                      DevStatus* status) {
@@ -104,46 +110,68 @@ __device__ __forceinline__ uint32_t block_exponent(uint32_t field) {
   return field == 255u ? 255u : field > 8u ? field - 8u : 0u;
 }
 
-// 32 bf16 values (packed) to codes. The scale 2^(127 - e) is a bf16 number and
-// the products are exact down to bf16's subnormals, far below the smallest code.
-__device__ __forceinline__ uint32_t quantise32(const uint4 (&w)[4], uint4 (&codes)[2]) {
-  const uint32_t* in = reinterpret_cast<const uint32_t*>(w);
+// 16 of a block's 32 values to codes; the neighbouring lane (lane ^ 1) has the
+// other 16, and every lane of the warp calls it. From packed bf16: the scale
+// 2^(127 - e) is a bf16 number and the products are exact down to bf16's
+// subnormals, far below the smallest code.
+__device__ __forceinline__ uint32_t quantise16(const uint4 (&w)[2], uint4& codes) {
+  const uint32_t in[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = __vmaxu2(m, in[i] & 0x7fff7fffu);
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, in[i] & 0x7fff7fffu);
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
   const uint32_t e = block_exponent(max(m & 0xffffu, m >> 16) >> 7);
-  const uint32_t inv = e == 255u ? 0u : (254u - e) * 0x00800080u;
-  uint32_t* out = reinterpret_cast<uint32_t*>(codes);
+  const uint32_t inv = (254u - min(e, 254u)) * 0x00800080u;
+  uint32_t half[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    uint32_t half[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&in[2 * i + j]),
-                                       *reinterpret_cast<const __nv_bfloat162*>(&inv));
-      const uint32_t p = *reinterpret_cast<const uint32_t*>(&y);
-      half[j] = pack_e4m3x2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
-    }
-    out[i] = e == 255u ? 0u : half[0] | (half[1] << 16);
+    const __nv_bfloat162 y =
+        __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&in[i]), *reinterpret_cast<const __nv_bfloat162*>(&inv));
+    const uint32_t p = *reinterpret_cast<const uint32_t*>(&y);
+    half[i] = pack_e4m3x2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u));
   }
+  codes = make_uint4(half[0] | half[1] << 16, half[2] | half[3] << 16, half[4] | half[5] << 16, half[6] | half[7] << 16);
+  if (e == 255u) codes = make_uint4(0u, 0u, 0u, 0u);
   return e;
 }
 
-// The same of 32 fp32 values.
-__device__ __forceinline__ uint32_t quantise32(const float (&x)[32], uint4 (&codes)[2]) {
+// The same from fp32.
+__device__ __forceinline__ uint32_t quantise16(const float (&x)[16], uint4& codes) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
   const uint32_t e = block_exponent(m >> 23);
   const float inv = __uint_as_float((254u - min(e, 254u)) << 23);
-  uint32_t* out = reinterpret_cast<uint32_t*>(codes);
+  uint32_t half[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t w = pack_e4m3x2(x[4 * i] * inv, x[4 * i + 1] * inv) |
-                       (pack_e4m3x2(x[4 * i + 2] * inv, x[4 * i + 3] * inv) << 16);
-    out[i] = e == 255u ? 0u : w;
-  }
+  for (int i = 0; i < 8; ++i) half[i] = pack_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+  codes = make_uint4(half[0] | half[1] << 16, half[2] | half[3] << 16, half[4] | half[5] << 16, half[6] | half[7] << 16);
+  if (e == 255u) codes = make_uint4(0u, 0u, 0u, 0u);
   return e;
+}
+
+// 32 bytes in one access where the base allows it (every offset is a multiple).
+__device__ __forceinline__ void load32(const uint4* p, bool wide, uint4 (&w)[2]) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0].x), "=r"(w[0].y), "=r"(w[0].z), "=r"(w[0].w), "=r"(w[1].x), "=r"(w[1].y), "=r"(w[1].z),
+                   "=r"(w[1].w)
+                 : "l"(p));
+  } else {
+    w[0] = p[0];
+    w[1] = p[1];
+  }
+}
+__device__ __forceinline__ void store32(uint4* p, bool wide, const uint4 (&w)[2]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0].x), "r"(w[0].y),
+                 "r"(w[0].z), "r"(w[0].w), "r"(w[1].x), "r"(w[1].y), "r"(w[1].z), "r"(w[1].w)
+                 : "memory");
+  } else {
+    p[0] = w[0];
+    p[1] = w[1];
+  }
 }
 
 struct AppendArgs {
@@ -156,12 +184,13 @@ struct AppendArgs {
   const float* sin_t;
   int64_t B, total;
   int D, rope_rows, rows;  // rows of a CTA
+  bool wide;               // k and v are 32-byte aligned
   DevStatus* status;
 };
 
 template <bool MX, int N>
 __global__ void __launch_bounds__(kCacheBlock) append_kernel(AppendArgs a) {
-  constexpr int P = MX ? 4 : 1;  // 16-byte pieces of a unit
+  constexpr int P = MX ? 2 : 1;  // 16-byte pieces of a unit
   __shared__ Row row[kMaxRows];
   const int per_head = a.D / (8 * P), per_row = a.c.H * per_head;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows;
@@ -174,52 +203,57 @@ __global__ void __launch_bounds__(kCacheBlock) append_kernel(AppendArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int u = base + i * kCacheBlock + static_cast<int>(threadIdx.x);
-      if (u >= units) break;
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        k[i][p] = __ldcs(a.k + (row0 * per_row + u) * P + p);
-        v[i][p] = __ldcs(a.v + (row0 * per_row + u) * P + p);
+      const int64_t from = (row0 * per_row + u) * P;
+      if constexpr (MX) {
+        k[i][0] = k[i][1] = v[i][0] = v[i][1] = make_uint4(0u, 0u, 0u, 0u);
+        if (u >= units) continue;
+        load32(a.k + from, a.wide, k[i]);
+        load32(a.v + from, a.wide, v[i]);
+      } else {
+        if (u >= units) continue;
+        k[i][0] = __ldcs(a.k + from);
+        v[i][0] = __ldcs(a.v + from);
       }
     }
     if (base == 0) {
       if (static_cast<int>(threadIdx.x) < rows) {
-        row[threadIdx.x] = place(a.c, a.off, a.start, a.B, row0 + threadIdx.x, a.status);
-        if (a.cos_t != nullptr && row[threadIdx.x].at >= 0 && row[threadIdx.x].pos >= a.rope_rows)
-          record_error(a.status, JATTN_ERR_ROPE, 83, a.rope_rows);
+        const Row to = place(a.c, a.off, a.start, a.B, row0 + threadIdx.x, a.status);
+        row[threadIdx.x] = to;
+        if (a.cos_t != nullptr && to.at >= 0 && to.pos >= a.rope_rows) record_error(a.status, JATTN_ERR_ROPE, 83, a.rope_rows);
       }
       __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int u = base + i * kCacheBlock + static_cast<int>(threadIdx.x);
-      if (u >= units) break;
       const int r = u / per_row, hp = u - r * per_row, h = hp / per_head, unit = hp - h * per_head;
-      const Row to = row[r];
-      if (to.at < 0) continue;
+      const Row to = u < units ? row[r] : Row{kSkip, 0};
       const int64_t at = (to.at + (static_cast<int64_t>(h) << a.c.page_shift)) * per_head + unit;
-      const bool turn = a.cos_t != nullptr && to.pos < a.rope_rows;
+      const bool turn = a.cos_t != nullptr && to.at >= 0 && to.pos < a.rope_rows;
       const float* cos_row = a.cos_t + to.pos * (a.D / 2);
       const float* sin_row = a.sin_t + to.pos * (a.D / 2);
       if constexpr (MX) {
-        uint4 codes[2];
-        uint32_t e;
-        if (turn) {
-          float x[32];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) unpack8(k[i][p], x + 8 * p);
-          rotate<32>(x, cos_row, sin_row, unit * 16);
-          e = quantise32(x, codes);
+        uint4 codes_k, codes_v;
+        uint32_t ek, ev;
+        if (a.cos_t != nullptr) {
+          float x[16];
+          unpack8(k[i][0], x);
+          unpack8(k[i][1], x + 8);
+          if (turn) rotate<16>(x, cos_row, sin_row, unit * 8);
+          ek = quantise16(x, codes_k);
         } else {
-          e = quantise32(k[i], codes);
+          ek = quantise16(k[i], codes_k);
         }
-        static_cast<uint4*>(a.c.k)[2 * at] = codes[0];
-        static_cast<uint4*>(a.c.k)[2 * at + 1] = codes[1];
-        a.c.ks[at] = static_cast<uint8_t>(e);
-        e = quantise32(v[i], codes);
-        static_cast<uint4*>(a.c.v)[2 * at] = codes[0];
-        static_cast<uint4*>(a.c.v)[2 * at + 1] = codes[1];
-        a.c.vs[at] = static_cast<uint8_t>(e);
+        ev = quantise16(v[i], codes_v);
+        if (to.at < 0) continue;
+        static_cast<uint4*>(a.c.k)[at] = codes_k;
+        static_cast<uint4*>(a.c.v)[at] = codes_v;
+        if ((unit & 1) == 0) {
+          a.c.ks[at / 2] = static_cast<uint8_t>(ek);
+          a.c.vs[at / 2] = static_cast<uint8_t>(ev);
+        }
       } else {
+        if (to.at < 0) continue;
         if (turn) {
           float x[8];
           unpack8(k[i][0], x);
@@ -253,6 +287,7 @@ struct ReadArgs {
   uint4* v;
   int64_t B, total;
   int D, rows;
+  bool wide;  // k and v are 32-byte aligned
   DevStatus* status;
 };
 
@@ -296,11 +331,9 @@ __global__ void __launch_bounds__(kCacheBlock) read_kernel(ReadArgs a) {
       if constexpr (MX) {
         uint4 x[2];
         read16(k[i], ks[i], x);
-        __stcs(a.k + to, x[0]);
-        __stcs(a.k + to + 1, x[1]);
+        store32(a.k + to, a.wide, x);
         read16(v[i], vs[i], x);
-        __stcs(a.v + to, x[0]);
-        __stcs(a.v + to + 1, x[1]);
+        store32(a.v + to, a.wide, x);
       } else {
         __stcs(a.k + to, k[i]);
         __stcs(a.v + to, v[i]);
@@ -316,19 +349,23 @@ int rows_of(int per_row, int units) {
 }
 unsigned ctas_of(int64_t total, int rows) { return static_cast<unsigned>((total + rows - 1) / rows); }
 
-// One unit per thread while that leaves SMs idle (a few rows), else four (16-byte
-// units) or two (blocks of 32 values).
-bool few_rows(int64_t total, int per_row) { return total * per_row <= int64_t(152) * 2 * kCacheBlock; }
+// One unit per thread up to eight CTAs an SM (read_one_user 3.5 us against 4.0
+// with four), then four; two when quantising, which needs the registers
+// (append_chunks_mxfp8 150 us against 156 with four and 170 with one).
+bool few_rows(int64_t total, int per_row) { return total * per_row <= int64_t(152) * 8 * kCacheBlock; }
+bool wide(const void* k, const void* v) {
+  return ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
+}
 
 }  // namespace
 
 cudaError_t launch_cache_append(const CacheView& c, bool mx, int64_t B, int64_t total, const int64_t* off,
                                 const int64_t* start, const void* k, const void* v, int D, const float* cos_t,
                                 const float* sin_t, int rope_rows, DevStatus* status, cudaStream_t stream) {
-  const int per_row = c.H * (D / (mx ? 32 : 8));
+  const int per_row = c.H * (D / (mx ? 16 : 8));
   const int units = few_rows(total, per_row) ? 1 : mx ? 2 : 4;
-  const AppendArgs a{c,     off, start, static_cast<const uint4*>(k), static_cast<const uint4*>(v),
-                     cos_t, sin_t, B,   total, D, rope_rows, rows_of(per_row, units), status};
+  const AppendArgs a{c,     off, start, static_cast<const uint4*>(k), static_cast<const uint4*>(v), cos_t, sin_t, B, total,
+                     D, rope_rows, rows_of(per_row, units), wide(k, v), status};
   const auto kernel = mx ? (units == 1 ? append_kernel<true, 1> : append_kernel<true, 2>)
                          : (units == 1 ? append_kernel<false, 1> : append_kernel<false, 4>);
   kernel<<<ctas_of(total, a.rows), kCacheBlock, 0, stream>>>(a);
@@ -340,7 +377,8 @@ cudaError_t launch_cache_read(const CacheView& c, bool mx, int64_t B, int64_t to
                               cudaStream_t stream) {
   const int per_row = c.H * (D / (mx ? 16 : 8));
   const int units = few_rows(total, per_row) ? 1 : 4;
-  const ReadArgs a{c, off, start, static_cast<uint4*>(k), static_cast<uint4*>(v), B, total, D, rows_of(per_row, units), status};
+  const ReadArgs a{c, off, start, static_cast<uint4*>(k), static_cast<uint4*>(v), B, total, D, rows_of(per_row, units),
+                   wide(k, v), status};
   const auto kernel = mx ? (units == 1 ? read_kernel<true, 1> : read_kernel<true, 4>)
                          : (units == 1 ? read_kernel<false, 1> : read_kernel<false, 4>);
   kernel<<<ctas_of(total, a.rows), kCacheBlock, 0, stream>>>(a);
