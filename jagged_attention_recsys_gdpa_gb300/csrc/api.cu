@@ -942,7 +942,7 @@ int check_decode(const jattn_params_t* p, const jattn_cache_t* c) {
   if ((rc = check_cache(c)) != JATTN_OK) return rc;
   if (p->D != c->D || p->H % c->H) return JATTN_ERR_INVALID;
   // positions, windows and their sums stay within 32 bits
-  if (p->total_q > (int64_t(1) << 30) || p->total_kv > (int64_t(1) << 30)) return JATTN_ERR_INVALID;
+  if (p->total_q * p->H > (int64_t(1) << 30) || p->total_kv > (int64_t(1) << 30)) return JATTN_ERR_INVALID;
   return JATTN_OK;
 }
 

@@ -94,8 +94,7 @@ __device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b, int tile, int 
   s.hi = max(s.hi, s.lo);
   s.k0 = s.lo / step * step;
   s.steps = max(1, (s.hi - s.k0 + step - 1) / step);
-  const int64_t rows = static_cast<int64_t>(s.lq) * a.G;
-  s.tiles = static_cast<int>((rows + tile - 1) / tile);
+  s.tiles = (s.lq * a.G + tile - 1) / tile;
   return s;
 }
 
@@ -130,17 +129,23 @@ __device__ __forceinline__ int64_t warp_inclusive(int64_t x, int lane) {
   return x;
 }
 
-// The number of all steps, and the place of step `first`. Every warp of the
-// CTA calls it; each thread sums the steps of one stretch of sequences.
-__device__ __forceinline__ int64_t total_steps(const DecodeArgs& a, int tile, int step, int64_t* start) {
+// 32-bit division where the numbers allow it.
+__device__ __forceinline__ int64_t divide(int64_t x, int d) {
+  return (x >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(d)) : x / d;
+}
+
+// The number of all steps; start[i]: the first step of stretch i, a thread's
+// share of the sequences. With a thread per sequence seqs[] keeps them.
+__device__ __forceinline__ int64_t total_steps(const DecodeArgs& a, int tile, int step, int64_t* start, Seq* seqs) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t c = (a.B + kThreads - 1) / kThreads;
+  const int c = static_cast<int>((a.B + kThreads - 1) / kThreads);
   int64_t sum = 0;
-  for (int64_t b = tid * c; b < min(a.B, (tid + 1) * c); ++b) {
+  for (int64_t b = static_cast<int64_t>(tid) * c; b < min(a.B, static_cast<int64_t>(tid + 1) * c); ++b) {
     const Seq s = seq_of(a, static_cast<int>(b), tile, step);
+    if (c == 1) seqs[tid] = s;
     sum += static_cast<int64_t>(s.tiles) * a.cache.H * s.steps;
     if (blockIdx.x == 0) {  // the one check of what the host cannot see
-      const int64_t n = a.kv_lens[b];
+      const int64_t n = __ldg(a.kv_lens + b);
       if (n < 0 || n > a.max_kv) record_error(a.status, JATTN_ERR_LENGTH, 85, static_cast<int>(b));
       if (a.q_off != nullptr) check_offsets(a.q_off, b + 1, a.total_q, b, a.B, a.status);
     }
@@ -160,42 +165,49 @@ __device__ __forceinline__ int64_t total_steps(const DecodeArgs& a, int tile, in
   return all;
 }
 
-__device__ __forceinline__ Place find_place(const DecodeArgs& a, int tile, int step, const int64_t* start, int64_t first) {
+// The place of step `first`, one of those counted.
+__device__ __forceinline__ Place find_place(const DecodeArgs& a, int tile, int step, const int64_t* start, const Seq* seqs,
+                                            int64_t first) {
   const int lane = threadIdx.x & 31;
-  const int64_t c = (a.B + kThreads - 1) / kThreads;
+  const int c = static_cast<int>((a.B + kThreads - 1) / kThreads);
   int before = 0;  // stretches that begin at or before `first`
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) before += __popc(__ballot_sync(0xffffffffu, start[i * 32 + lane] <= first));
   int64_t at = start[before - 1];  // the last of them holds it: those behind begin later
   Place p;
-  for (int64_t b = (before - 1) * c;; b += 32) {
-    const int64_t mine = b + lane;
-    int64_t steps = 0;
-    if (mine < a.B) {
-      const Seq s = seq_of(a, static_cast<int>(mine), tile, step);
-      steps = static_cast<int64_t>(s.tiles) * a.cache.H * s.steps;
+  if (c == 1) {
+    p.b = before - 1;
+    p.s = seqs[p.b];
+  } else {
+    for (int64_t b = static_cast<int64_t>(before - 1) * c;; b += 32) {
+      const int64_t mine = b + lane;
+      int64_t steps = 0;
+      if (mine < a.B) {
+        const Seq s = seq_of(a, static_cast<int>(mine), tile, step);
+        steps = static_cast<int64_t>(s.tiles) * a.cache.H * s.steps;
+      }
+      const int64_t end = at + warp_inclusive(steps, lane);
+      const uint32_t over = __ballot_sync(0xffffffffu, end > first);
+      if (over != 0) {
+        const int i = __ffs(over) - 1;
+        at = __shfl_sync(0xffffffffu, end - steps, i);
+        p.b = static_cast<int>(b + i);
+        break;
+      }
+      at = __shfl_sync(0xffffffffu, end, 31);
+      if (b + 32 >= a.B) {  // cannot be: `first` is below the total
+        p.b = static_cast<int>(a.B - 1);
+        at = first;
+        break;
+      }
     }
-    const int64_t end = at + warp_inclusive(steps, lane);
-    const uint32_t over = __ballot_sync(0xffffffffu, end > first);
-    if (over != 0) {
-      const int i = __ffs(over) - 1;
-      at = __shfl_sync(0xffffffffu, end - steps, i);
-      p.b = static_cast<int>(b + i);
-      break;
-    }
-    at = __shfl_sync(0xffffffffu, end, 31);
-    if (b + 32 >= a.B) {  // cannot be: `first` is below the total
-      p.b = static_cast<int>(a.B - 1);
-      at = first;
-      break;
-    }
+    p.s = seq_of(a, p.b, tile, step);
   }
-  p.s = seq_of(a, p.b, tile, step);
   p.table = a.cache.table + p.b * a.cache.max_pages;
-  const int64_t unit = (first - at) / p.s.steps;
-  p.t = static_cast<int>((first - at) % p.s.steps);
-  p.tile = static_cast<int>(unit / a.cache.H);
-  p.h = static_cast<int>(unit % a.cache.H);
+  const int64_t unit = divide(first - at, p.s.steps);
+  p.t = static_cast<int>(first - at - unit * p.s.steps);
+  p.tile = static_cast<int>(divide(unit, a.cache.H));
+  p.h = static_cast<int>(unit - static_cast<int64_t>(p.tile) * a.cache.H);
   return p;
 }
 
@@ -503,22 +515,23 @@ __device__ __forceinline__ void join_row(const DecodeArgs& a, int col, int n, At
   }
 }
 
-// A finished row of a unit: query row r of the sequence's first row q0.
+// The row of [total_q * Hq, D] that is row r of head h's rows of a sequence
+// whose first query row is q0.
+__device__ __forceinline__ int64_t query_row(const DecodeArgs& a, int64_t q0, int r, int h) {
+  const int i = a.G == 1 ? r : r / a.G;
+  return (q0 + i) * a.Hq + h * a.G + (r - i * a.G);
+}
+
+// A finished row of a unit.
 template <int E>
-__device__ __forceinline__ void write_row(const DecodeArgs& a, int64_t q0, int64_t r, int h, int D, int col, int n,
+__device__ __forceinline__ void write_row(const DecodeArgs& a, int64_t q0, int r, int h, int D, int col, int n,
                                           const float (&x)[E], float m, float l) {
-  const int64_t out = (q0 + r / a.G) * a.Hq + h * a.G + r % a.G;
+  const int64_t out = query_row(a, q0, r, h);
   const float f = row_norm(a, n);
   if (a.act == JATTN_SOFTMAX && col == 0) a.lse[out] = lse_of(m, l);
   uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D + col);
 #pragma unroll
   for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(x[e] * f, x[e + 1] * f);
-}
-
-// Query rows of sequence b: its first and their number (the plan has checked them).
-__device__ __forceinline__ int64_t query_rows(const DecodeArgs& a, int b, int64_t& q0) {
-  q0 = a.q_off != nullptr ? a.q_off[b] : b;
-  return a.q_off != nullptr ? a.q_off[b + 1] - q0 : 1;
 }
 
 // What a worker leaves for its CTA.
@@ -528,7 +541,9 @@ struct Left {
   int head_last;   // the head is the run's last piece
   int tail;        // rows of the tail (0: none)
   int b, tile, h;  // of the tail's unit
-  int last_cta;    // where that unit ends
+  int n;           // its sequence's cached rows
+  int64_t q0;      // and first query row
+  int last_cta;    // where the unit ends
 };
 
 // ---------------------------------------------------------------- kernel
@@ -631,16 +646,20 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
   const int workers = gridDim.x * per_cta, me = blockIdx.x * per_cta + in_cta;
   const Scratch sc = carve(scratch, gridDim.x, per_cta, tile, D);
 
-  const int64_t total = total_steps(a, tile, step, start);
+  unsigned char* const smem_base = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
+  Seq* const seqs = reinterpret_cast<Seq*>(smem_base);  // until the first copies
+  static_assert(sizeof(Seq) * kThreads <= 8192, "the rings hold the sequences");
+  const int64_t total = total_steps(a, tile, step, start, seqs);
   const int64_t share = (total + workers - 1) / workers;
   const int64_t first = me * share, last = min(first + share, total);  // this worker's run [first, last)
   if (tid == 0) left[in_cta] = Left{};
-  unsigned char* const smem_base = smem_raw + (((smem_u32(smem_raw) + 1023u) & ~1023u) - smem_u32(smem_raw));
   constexpr int ring_bytes = kStages * 8192 * WM;
   static_assert(tile * (D * 4 + 8) <= ring_bytes, "a worker's ring holds a piece");
+  Place in{};  // the step that is copied next
+  if (first < last) in = find_place(a, tile, step, start, seqs, first);
+  __syncthreads();
   if (first < last) {
-    Place in = find_place(a, tile, step, start, first);  // the step that is copied next
-    Place at = in;                                       // the step that is computed next
+    Place at = in;  // the step that is computed next
     const uint32_t smem = smem_u32(smem_base);
     const uint32_t ring = smem + in_cta * ring_bytes;
     const uint32_t scale_ring = smem + kWarps * kStages * 8192 + in_cta * (kStages * 2 * step * L::scale);
@@ -683,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
     int all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;  // that every row, and that any row, of the warp's may see
     int ref = -1;               // MXFP8: V's reference exponent, none yet
     bool live = false;          // the warp's rows hold one of the tile's at least
-    int64_t row_base = 0, rows = 0;
+    int row_base = 0, rows = 0;
     bool fresh = true;
     int n_steps = 0;            // of the unit at `at`, in this run, so far
     int stage_no = 0;
@@ -695,22 +714,21 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
         fresh = false;
         n_steps = 0;
         ref = -1;
-        rows = static_cast<int64_t>(at.s.lq) * a.G;
-        row_base = static_cast<int64_t>(at.tile) * tile + warp_m * (8 * NR);
+        rows = at.s.lq * a.G;
+        row_base = at.tile * tile + warp_m * (8 * NR);
         live = row_base < rows;
         if (live) {
           const int delta = at.s.n - at.s.lq;
-          const int64_t end = rows - 1;  // rows behind it take its interval, and zeros for their query
-          key_interval(static_cast<int>(row_base / a.G), delta, at.s.n, a.mask, a.window, any_lo, all_hi);
-          key_interval(static_cast<int>(min(row_base + 8 * NR - 1, end) / a.G), delta, at.s.n, a.mask, a.window, all_lo,
+          const int end = rows - 1;  // rows behind it take its interval, and zeros for their query
+          key_interval(row_base / a.G, delta, at.s.n, a.mask, a.window, any_lo, all_hi);
+          key_interval(min(row_base + 8 * NR - 1, end) / a.G, delta, at.s.n, a.mask, a.window, all_lo,
                        any_hi);
 #pragma unroll
           for (int g = 0; g < NR; ++g) {
             const float base = a.act == JATTN_SOFTMAX ? a.scale_log2 : a.scale;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int64_t r = min(row_base + 8 * g + 2 * c + i, end);
-              key_interval(static_cast<int>(r / a.G), delta, at.s.n, a.mask, a.window, lo[g][i], hi[g][i]);
+              key_interval(min(row_base + 8 * g + 2 * c + i, end) / a.G, delta, at.s.n, a.mask, a.window, lo[g][i], hi[g][i]);
               m[g][i] = !MX || a.act == JATTN_SOFTMAX ? -INFINITY : kLeast;
               l[g][i] = 0.0f;
               f[g][i] = base;
@@ -719,10 +737,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
 #pragma unroll
             for (int j = 0; j < KS; ++j) o[g][j][0] = o[g][j][1] = o[g][j][2] = o[g][j][3] = 0.0f;
             // the query row that this lane holds operands of
-            const int64_t r = row_base + 8 * g + (lane >> 2);
+            const int r = row_base + 8 * g + (lane >> 2);
             const uint32_t* src = nullptr;
-            if (r < rows)
-              src = reinterpret_cast<const uint32_t*>(a.q + ((at.s.q0 + r / a.G) * a.Hq + at.h * a.G + r % a.G) * D);
+            if (r < rows) src = reinterpret_cast<const uint32_t*>(a.q + query_row(a, at.s.q0, r, at.h) * D);
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
               // bf16: columns 2c, 2c + 1 and 2c + 8, 2c + 9 of the 16; codes: columns 4c .. 4c + 3, a word's
@@ -1102,10 +1119,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
             repair<D, MX>(a, at, n_steps, step, q[g], f[g], o[g], m[g], w, lo[g], hi[g]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const int64_t r = row_base + 8 * g + 2 * c + i;
+              const int r = row_base + 8 * g + 2 * c + i;
               if (r >= rows) continue;
               if (unit_ends && begun) {  // all of it was in this run
-                const int64_t out = (at.s.q0 + r / a.G) * a.Hq + at.h * a.G + r % a.G;
+                const int64_t out = query_row(a, at.s.q0, r, at.h);
                 if (a.act == JATTN_SOFTMAX && lane < 4) a.lse[out] = lse_of(m[g][i], l[g][i]);
                 __nv_bfloat16* dst = a.o + out * D;
 #pragma unroll
@@ -1136,7 +1153,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
           }
         }
         if (tid == 0 && !(unit_ends && begun)) {
-          const int n = static_cast<int>(min(static_cast<int64_t>(tile), rows - static_cast<int64_t>(at.tile) * tile));
+          const int n = min(tile, rows - at.tile * tile);
           Left& x = left[in_cta];
           if (begun) {
             const int64_t end = last + (at.s.steps - 1 - at.t);  // number of the unit's end
@@ -1144,7 +1161,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
             x.b = at.b;
             x.tile = at.tile;
             x.h = at.h;
-            x.last_cta = static_cast<int>((end - 1) / share / per_cta);
+            x.n = at.s.n;
+            x.q0 = at.s.q0;
+            x.last_cta = static_cast<int>(share >> 31 == 0 ? divide(end - 1, static_cast<int>(share)) : (end - 1) / share) / per_cta;
           } else {
             x.head = n;
             x.head_ends = unit_ends;
@@ -1171,6 +1190,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
   constexpr int E = D / 32;
   const int warp = threadIdx.x >> 5;
   int4 going_on = make_int4(-1, 0, 0, 0);
+  int turn = 0;  // rows are dealt to the warps in turn
 #pragma unroll 1
   for (int begin = -1; begin < per_cta; ++begin) {
     const int w0 = max(begin, 0);
@@ -1184,7 +1204,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
       ++len;
       ends = left[x].head_ends;
     }
-    for (int r = warp; r < n; r += kWarps) {
+    for (int r = (warp + turn) % kWarps; r < n; r += kWarps) {
       const auto at = [&](int i, const float*& acc, const float2*& stats) {
         const int w = w0 + i;
         if ((tail && i == 0) || left[w].head_last) {
@@ -1200,10 +1220,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
       float x[E], mj, lj;
       join_row<E, per_cta>(a, lane * E, len, at, x, mj, lj);
       if (tail && ends) {
-        int64_t q0;
-        (void)query_rows(a, unit.b, q0);
-        write_row<E>(a, q0, static_cast<int64_t>(unit.tile) * tile + r, unit.h, D, lane * E,
-                     static_cast<int>(a.kv_lens[unit.b]), x, mj, lj);
+        write_row<E>(a, unit.q0, unit.tile * tile + r, unit.h, D, lane * E, unit.n, x, mj, lj);
       } else {
         const int64_t to = (static_cast<int64_t>(blockIdx.x) * 2 + (tail ? 1 : 0)) * tile + r;
         if (lane == 0) sc.cml[to] = make_float2(mj, lj);
@@ -1211,6 +1228,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
         for (int e = 0; e < E; ++e) sc.cacc[to * D + lane * E + e] = x[e];
       }
     }
+    turn += n;
     if (tail && !ends) going_on = make_int4(unit.last_cta, unit.b, unit.tile, unit.h);
   }
   if (threadIdx.x == 0) sc.join[blockIdx.x] = going_on;
@@ -1230,9 +1248,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(DecodeArgs a, void* 
   if (j.x < 0) return;
   const int n = j.x - static_cast<int>(blockIdx.x) + 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int slot = threadIdx.x / lanes, col = (threadIdx.x % lanes) * 4;
-  int64_t q0;
-  const int64_t r0 = static_cast<int64_t>(j.z) * tile;
-  const int rows = static_cast<int>(min(static_cast<int64_t>(tile), query_rows(a, j.y, q0) * a.G - r0));
+  const int64_t q0 = a.q_off != nullptr ? a.q_off[j.y] : j.y;
+  const int lq = a.q_off != nullptr ? static_cast<int>(a.q_off[j.y + 1] - q0) : 1, n_kv = static_cast<int>(a.kv_lens[j.y]);
+  const int r0 = j.z * tile, rows = min(tile, lq * a.G - r0);
   const auto place = [&](int i, int r) { return ((static_cast<int64_t>(blockIdx.x) + i) * 2 + (i == 0 ? 1 : 0)) * tile + r; };
   for (int base = 0; base < rows; base += some) {
     const int now = min(some, rows - base), ways = slots / now;
@@ -1284,7 +1302,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(DecodeArgs a, void* 
       }
       const float v[4] = {x.x, x.y, x.z, x.w};
       const float2 ml = a.act == JATTN_SOFTMAX ? row_ml[r] : make_float2(0.0f, 1.0f);
-      write_row<4>(a, q0, r0 + base + r, j.w, D, col, static_cast<int>(a.kv_lens[j.y]), v, ml.x, ml.y);
+      write_row<4>(a, q0, r0 + base + r, j.w, D, col, n_kv, v, ml.x, ml.y);
     }
     __syncthreads();
   }
