@@ -286,15 +286,19 @@ __device__ __forceinline__ uint32_t codes_even(uint32_t w) { return ((w << 8) & 
 __device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u); }
 // ---------------------------------------------------------------- rows and columns
 // How a warp's products lie in its lanes (l = lane / 4, c = lane % 4): scores
-// and weights as [16 keys x 8 query rows], keys l and l + 8, rows 2c and 2c + 1;
-// accumulators as [16 columns x 8 rows], rows 2c and 2c + 1 again, columns l and
-// l + 8 of the 16 (bf16) or 2l and 2l + 1 (codes). So a lane holds everything of
-// its rows' maxima, sums and factors, and weights turn into the second product's
-// operand by an 8x8 transpose.
+// and weights as [16 keys x 8 query rows], two keys and rows 2c and 2c + 1;
+// accumulators as [16 columns x 8 rows], columns l and l + 8 and rows 2c and
+// 2c + 1 again. So a lane holds everything of its rows' maxima, sums and factors,
+// and weights turn into the second product's operand by an 8x8 transpose, which
+// gives a lane keys 2c, 2c + 1 and 2c + 8, 2c + 9 of the 16 if its two were l and
+// l + 8. Codes come from the transposing load with keys 4c .. 4c + 3 in a word, so
+// there the 16 rows of a key product are taken in the order that makes them
+// those.
 template <bool MX>
-__device__ __forceinline__ int column(int i, int lane) {  // i = 0, 1
-  return MX ? 2 * (lane >> 2) + i : (lane >> 2) + 8 * i;
+__device__ __forceinline__ int key_of(int l, int i) {  // i = 0, 1: the two keys of a lane, of 16
+  return MX ? 4 * (l >> 1) + (l & 1) + 2 * i : l + 8 * i;
 }
+__device__ __forceinline__ int column(int i, int lane) { return (lane >> 2) + 8 * i; }
 
 template <int NT>
 __device__ __forceinline__ void scale_rows(float (&o)[NT][4], float c0, float c1) {
@@ -307,15 +311,16 @@ __device__ __forceinline__ void scale_rows(float (&o)[NT][4], float c0, float c1
   }
 }
 
-// Weights of keys first, first + 8, ... outside a row's [lo, hi) become `none`.
-template <int MT, int NR>
+// Weights of a lane's keys (the first of each 16 is `first`) outside a row's
+// [lo, hi) become `none`.
+template <bool MX, int MT, int NR>
 __device__ __forceinline__ void mask_keys(float (&s)[MT][NR][4], int g, int first, const int (&lo)[2], const int (&hi)[2],
                                           float none) {
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int pos = first + mt * 16 + 8 * (e >> 1);
+      const int pos = first + mt * 16 + (MX ? 2 : 8) * (e >> 1);
       if (pos < lo[e & 1] || pos >= hi[e & 1]) s[mt][g][e] = none;
     }
   }
@@ -435,7 +440,7 @@ __device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (in[e & 1] && (bad >> (4 * j + e) & 1u))
-          o[j][e] = fmaf(p[e & 1], cached<MX>(a.cache.v, a.cache.vs, row, D, 16 * j + column<MX>(e >> 1, lane)), o[j][e]);
+          o[j][e] = fmaf(p[e & 1], cached<MX>(a.cache.v, a.cache.vs, row, D, 16 * j + column(e >> 1, lane)), o[j][e]);
       }
     }
   }
@@ -809,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
         float s[MT][NR][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          const int r = r_base + mt * 16 + (lane & 15);
+          const int r = r_base + mt * 16 + key_of<MX>(lane & 7, (lane >> 3) & 1);
           if constexpr (!MX) {
             float t[2][NR][4];  // two chains of products
 #pragma unroll
@@ -830,8 +835,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
               for (int e = 0; e < 4; ++e) s[mt][g][e] = t[0][g][e] + t[1][g][e];
             }
           } else {
-            const uint32_t e0 = scale_word<D>(ksc, r_base + mt * 16 + (lane >> 2));
-            const uint32_t e1 = scale_word<D>(ksc, r_base + mt * 16 + 8 + (lane >> 2));
+            const uint32_t e0 = scale_word<D>(ksc, r_base + mt * 16 + key_of<true>(lane >> 2, 0));
+            const uint32_t e1 = scale_word<D>(ksc, r_base + mt * 16 + key_of<true>(lane >> 2, 1));
 #pragma unroll
             for (int kk = 0; kk < KS; kk += 2) {  // one block of 32 columns
               uint32_t w[4], x[4];
@@ -864,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
             for (int e = 0; e < 4; ++e) s[mt][g][e] *= f[g][e & 1];
           }
           if (a.act == JATTN_SOFTMAX) {
-            if (rare(partial)) mask_keys<MT>(s, g, pos0 + (lane >> 2), lo[g], hi[g], -INFINITY);
+            if (rare(partial)) mask_keys<MX>(s, g, pos0 + key_of<MX>(lane >> 2, 0), lo[g], hi[g], -INFINITY);
             float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
@@ -914,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
                 for (int e = 0; e < 4; ++e) s[mt][g][e] = gelu_poly(s[mt][g][e]);
               }
             }
-            if (rare(partial)) mask_keys<MT>(s, g, pos0 + (lane >> 2), lo[g], hi[g], 0.0f);
+            if (rare(partial)) mask_keys<MX>(s, g, pos0 + key_of<MX>(lane >> 2, 0), lo[g], hi[g], 0.0f);
             if constexpr (MX) {  // m is the exponent that the row's weights are held against
               float t[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -941,11 +946,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
           }
         }
         // ---- O += V^T P^T
+        if constexpr (!MX) {
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          // rows (keys) and pieces of the transposed loads: keys 0-7 of two pieces, then keys 8-15
-          const int r = r_base + mt * 16 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
-          if constexpr (!MX) {
+          for (int mt = 0; mt < MT; ++mt) {
             // P as two bf16 parts: its rounding to one would be as large as the output's own
             uint32_t ph[NR][2], pl[NR][2];
 #pragma unroll
@@ -958,6 +961,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
                 pl[g][i] = movmatrix(bf16x2_lo(x, y, both));
               }
             }
+            // keys 0-7 of two pieces, then keys 8-15
+            const int r = r_base + mt * 16 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
 #pragma unroll
             for (int j = 0; j < KS; ++j) {
               uint32_t x[4];
@@ -968,62 +973,66 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
                 mma_bf16(o[g][j], x, pl[g]);
               }
             }
-          } else {
-            uint32_t e[2];  // of this lane's keys of the 16, lane / 4 and 8 more
+          }
+        } else {
+          uint32_t e[MT][2], d[MT][2], all = 0;  // exponents of this lane's keys
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              e[i] = scale_word<D>(vsc, r_base + mt * 16 + 8 * i + (lane >> 2));
-              if (D == 64) e[i] |= e[i] << 16;
-            }
-            if (rare(partial)) {
-              // rows outside the sequence have codes of zero and any exponents: these become the reference
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int pos = pos0 + mt * 16 + 8 * i + (lane >> 2);
-                if (pos < at.s.lo || pos >= at.s.hi) e[i] = max(ref, 0) * 0x01010101u;
-              }
-            }
+          for (int i = 0; i < 2 * MT; ++i) {
+            const int key = (i >> 1) * 16 + key_of<true>(lane >> 2, i & 1);
+            uint32_t x = scale_word<D>(vsc, r_base + key);
+            if (D == 64) x |= x << 16;
+            // rows outside the sequence have codes of zero and any exponents: these become the reference
+            if (rare(partial) && (pos0 + key < at.s.lo || pos0 + key >= at.s.hi)) x = max(ref, 0) * 0x01010101u;
+            e[i >> 1][i & 1] = x;
             // e - (R - 14), byte by byte: 0 .. 15 where fp16 factors do (a byte below borrows and ends up far above)
-            uint32_t d[2] = {e[0] - static_cast<uint32_t>(ref - 14) * 0x01010101u,
-                             e[1] - static_cast<uint32_t>(ref - 14) * 0x01010101u};
-            bool small = false;
-            if (rare(__any_sync(0xffffffffu, ((d[0] | d[1]) & 0xf0f0f0f0u) != 0 || ref < 0))) {
-              int top = 14;  // the largest exponent but NaN's (R - 14 is no negative byte)
+            all |= d[i >> 1][i & 1] = x - static_cast<uint32_t>(ref - 14) * 0x01010101u;
+          }
+          bool small = false;
+          if (rare(__any_sync(0xffffffffu, (all & 0xf0f0f0f0u) != 0 || ref < 0))) {
+            int top = 14;  // the largest exponent but NaN's (R - 14 is no negative byte)
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int x = static_cast<int>((e[j & 1] >> (8 * (j >> 1))) & 0xffu);
+            for (int i = 0; i < 2 * MT; ++i) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int x = static_cast<int>((e[i >> 1][i & 1] >> (8 * j)) & 0xffu);
                 if (x != 255) top = max(top, x);
               }
-              top = __reduce_max_sync(0xffffffffu, top);
-              if (ref < 0 || top > ref + 1) {
-                if (ref >= 0) {
-#pragma unroll
-                  for (int g = 0; g < NR; ++g) scale_rows(o[g], pow2(ref - top - 1), pow2(ref - top - 1));
-                }
-                ref = top + 1;
-              }
-              uint32_t out = 0;
-#pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int pos = pos0 + mt * 16 + 8 * i + (lane >> 2);
-                if (partial && (pos < at.s.lo || pos >= at.s.hi)) e[i] = ref * 0x01010101u;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) out |= ((e[i] >> (8 * j)) & 0xffu) - static_cast<uint32_t>(ref - 14);
-                d[i] = e[i] - static_cast<uint32_t>(ref - 14) * 0x01010101u;
-              }
-              small = __any_sync(0xffffffffu, (out & 0xfffffff0u) != 0);
             }
-            if (rare(small)) {  // bf16 products for these 16 keys
-#pragma unroll 1
+            top = __reduce_max_sync(0xffffffffu, top);
+            if (ref < 0 || top > ref + 1) {
+              if (ref >= 0) {
+#pragma unroll
+                for (int g = 0; g < NR; ++g) scale_rows(o[g], pow2(ref - top - 1), pow2(ref - top - 1));
+              }
+              ref = top + 1;
+            }
+            uint32_t out = 0;
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+              uint32_t& x = e[i >> 1][i & 1];
+              const int key = (i >> 1) * 16 + key_of<true>(lane >> 2, i & 1);
+              if (partial && (pos0 + key < at.s.lo || pos0 + key >= at.s.hi)) x = ref * 0x01010101u;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) out |= ((x >> (8 * j)) & 0xffu) - static_cast<uint32_t>(ref - 14);
+              d[i >> 1][i & 1] = x - static_cast<uint32_t>(ref - 14) * 0x01010101u;
+            }
+            small = __any_sync(0xffffffffu, (out & 0xfffffff0u) != 0);
+          }
+          // rows (keys) of two 16-byte pieces for the transposing loads
+          const int r = r_base + (lane & 15), half = lane >> 4;
+          if (rare(small)) {  // bf16 products for these keys
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
               for (int j = 0; j < D / 32; ++j) {
                 float w[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const int x = static_cast<int>((e[i] >> (8 * j)) & 0xffu);
+                  const int x = static_cast<int>((e[mt][i] >> (8 * j)) & 0xffu);
                   w[i] = x == 255 ? __int_as_float(0x7fc00000) : pow2(x - ref);
                 }
                 uint32_t v[4];
-                ldmatrix4_trans(v, vs + piece_at<D, MX, step>(r, 2 * j + half));
+                ldmatrix2_trans_b8(v, vs + piece_at<D, MX, step>(r + mt * 16, 2 * j + half));
 #pragma unroll
                 for (int g = 0; g < NR; ++g) {
                   uint32_t ph[2], pl[2];
@@ -1036,20 +1045,22 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
                   }
 #pragma unroll
                   for (int i = 0; i < 2; ++i) {
-                    // 2^120 makes up for the codes' exponent bias
-                    const uint32_t x[4] = {mul_bf16x2(codes_even(v[i]), 0x7b807b80u), mul_bf16x2(codes_odd(v[i]), 0x7b807b80u),
-                                           mul_bf16x2(codes_even(v[2 + i]), 0x7b807b80u),
-                                           mul_bf16x2(codes_odd(v[2 + i]), 0x7b807b80u)};
+                    uint32_t x[4];
 #pragma unroll
-                    for (int jj = 0; jj < D / 32; ++jj) {
-                      if (jj != j) continue;
-                      mma_bf16(o[g][2 * jj + i], x, ph);
-                      mma_bf16(o[g][2 * jj + i], x, pl);
+                    for (int y = 0; y < 2; ++y) {  // columns l and l + 8; 2^120 makes up for the codes' exponent bias
+                      const uint32_t w4 = __byte_perm(v[2 * i + y], 0u, 0x3120);
+                      x[y] = mul_bf16x2(codes_even(w4), 0x7b807b80u);
+                      x[2 + y] = mul_bf16x2(codes_odd(w4), 0x7b807b80u);
                     }
+                    mma_bf16(o[g][2 * j + i], x, ph);
+                    mma_bf16(o[g][2 * j + i], x, pl);
                   }
                 }
               }
-            } else {
+            }
+          } else {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
               // P in fp16 (half a step is 2^-11 of it, an eighth of the output's), then by the keys' 2^(e - R)
               uint32_t p[NR][2];
 #pragma unroll
@@ -1063,18 +1074,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                   // fp16 2^(e - R), twice: exponent field e - R + 15
-                  const uint32_t x = __byte_perm(d[i], 0u, 0x4040u + 0x0101u * j) * 1024u + 0x04000400u;
+                  const uint32_t x = __byte_perm(d[mt][i], 0u, 0x4040u + 0x0101u * j) * 1024u + 0x04000400u;
 #pragma unroll
                   for (int g = 0; g < NR; ++g) pj[g][i] = movmatrix(mul_f16x2(p[g][i], x));
                 }
                 uint32_t w[4];
-                ldmatrix4_trans(w, vs + piece_at<D, MX, step>(r, 2 * j + half));
+                ldmatrix2_trans_b8(w, vs + piece_at<D, MX, step>(r + mt * 16, 2 * j + half));
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  // a word holds two keys of two columns: (key, column) 00 01 10 11
                   uint32_t x[4];
-                  e4m3x4_to_f16(__byte_perm(w[i], 0u, 0x3120), x[0], x[1]);
-                  e4m3x4_to_f16(__byte_perm(w[2 + i], 0u, 0x3120), x[2], x[3]);
+                  e4m3x4_to_f16(w[2 * i], x[0], x[2]);
+                  e4m3x4_to_f16(w[2 * i + 1], x[1], x[3]);
 #pragma unroll
                   for (int g = 0; g < NR; ++g) mma_f16(o[g][2 * j + i], x, pj[g]);
                 }
@@ -1128,12 +1138,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
                   const float x = o[g][j][i] * norm, y = o[g][j][2 + i] * norm;
-                  if constexpr (MX) {
-                    *reinterpret_cast<uint32_t*>(dst + 16 * j + column<MX>(0, lane)) = pack_bf16x2(x, y);
-                  } else {
-                    dst[16 * j + column<MX>(0, lane)] = __float2bfloat16(x);
-                    dst[16 * j + column<MX>(1, lane)] = __float2bfloat16(y);
-                  }
+                  dst[16 * j + column(0, lane)] = __float2bfloat16(x);
+                  dst[16 * j + column(1, lane)] = __float2bfloat16(y);
                 }
               } else {
                 const int row = warp_m * (8 * NR) + 8 * g + 2 * c + i;
@@ -1141,12 +1147,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
                 float* dst = acc + row * D;
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
-                  if constexpr (MX) {
-                    *reinterpret_cast<float2*>(dst + 16 * j + column<MX>(0, lane)) = make_float2(o[g][j][i], o[g][j][2 + i]);
-                  } else {
-                    dst[16 * j + column<MX>(0, lane)] = o[g][j][i];
-                    dst[16 * j + column<MX>(1, lane)] = o[g][j][2 + i];
-                  }
+                  dst[16 * j + column(0, lane)] = o[g][j][i];
+                  dst[16 * j + column(1, lane)] = o[g][j][2 + i];
                 }
               }
             }

@@ -286,6 +286,14 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                : "r"(addr)
                : "memory");
 }
+// Two 16x16 matrices of bytes, transposed; lanes 16i .. 16i + 15 give matrix i's
+// rows. A lane gets of each columns l and l + 8, rows 4c .. 4c + 3 (l = lane / 4, c = lane % 4).
+__device__ __forceinline__ void ldmatrix2_trans_b8(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
 // Transpose of an 8x8 matrix of 16-bit elements held as lane l: row l / 4, columns 2 (l % 4), + 1.
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t y;
