@@ -247,29 +247,36 @@ def cache(n_pages, page_size, H, D, fmt, k, v, k_scales, v_scales) -> Cache:
     return Cache(int(n_pages), int(page_size), int(H), int(D), int(fmt), ptr(k), ptr(v), ptr(k_scales), ptr(v_scales))
 
 
-def cache_append(c: Cache, B: int, total: int, off, start, page_table, k, v, cos, sin, ws, ws_bytes: int, stream: int):
-    check(load().jattn_cache_append(ctypes.byref(c), B, total, ptr(off), ptr(start), ptr(page_table),
-                                    page_table.shape[1], ptr(k), ptr(v), ptr(cos), ptr(sin),
-                                    0 if cos is None else cos.shape[0], ws, ws_bytes, stream), "jattn_cache_append")
+# The paged-cache calls serve single tokens, where the host's time counts: they take the cache as a reference made
+# once (byref) and addresses of required tensors directly.
+def cache_append(c, B: int, total: int, off, start, page_table, k, v, cos, sin, ws: int, ws_bytes: int, stream: int):
+    rc = (_lib or load()).jattn_cache_append(c, B, total, ptr(off), start.data_ptr(), page_table.data_ptr(),
+                                             page_table.shape[1], k.data_ptr(), v.data_ptr(), ptr(cos), ptr(sin),
+                                             0 if cos is None else cos.shape[0], ws, ws_bytes, stream)
+    if rc:
+        check(rc, "jattn_cache_append")
 
 
-def cache_read(c: Cache, B: int, total: int, off, start, page_table, k, v, ws, ws_bytes: int, stream: int):
-    check(load().jattn_cache_read(ctypes.byref(c), B, total, ptr(off), ptr(start), ptr(page_table),
-                                  page_table.shape[1], ptr(k), ptr(v), ws, ws_bytes, stream), "jattn_cache_read")
+def cache_read(c, B: int, total: int, off, start, page_table, k, v, ws: int, ws_bytes: int, stream: int):
+    rc = (_lib or load()).jattn_cache_read(c, B, total, off.data_ptr(), ptr(start), page_table.data_ptr(),
+                                           page_table.shape[1], k.data_ptr(), v.data_ptr(), ws, ws_bytes, stream)
+    if rc:
+        check(rc, "jattn_cache_read")
 
 
-def decode_scratch_size(p: Params, c: Cache) -> int:
+def decode_scratch_size(p, c) -> int:
     n = ctypes.c_size_t(0)
-    check(load().jattn_decode_scratch_size(ctypes.byref(p), ctypes.byref(c), ctypes.byref(n)),
-          "jattn_decode_scratch_size")
-    return int(n.value)
+    check((_lib or load()).jattn_decode_scratch_size(p, c, ctypes.byref(n)), "jattn_decode_scratch_size")
+    return n.value
 
 
-def decode(p: Params, c: Cache, q_off, kv_lens, page_table, q, o, lse, scratch, scratch_bytes: int, ws,
-           ws_bytes: int, stream: int):
-    check(load().jattn_decode(ctypes.byref(p), ctypes.byref(c), ptr(q_off), ptr(kv_lens), ptr(page_table),
-                              page_table.shape[1], ptr(q), ptr(o), ptr(lse), scratch, scratch_bytes, ws, ws_bytes,
-                              stream), "jattn_decode")
+def decode(p, c, q_off, kv_lens, page_table, q, o, lse, scratch: int, scratch_bytes: int, ws: int, ws_bytes: int,
+           stream: int):
+    rc = (_lib or load()).jattn_decode(p, c, ptr(q_off), kv_lens.data_ptr(), page_table.data_ptr(),
+                                       page_table.shape[1], q.data_ptr(), o.data_ptr(), ptr(lse), scratch,
+                                       scratch_bytes, ws, ws_bytes, stream)
+    if rc:
+        check(rc, "jattn_decode")
 
 
 def schedule(p: Params, q_off, kv_off, row_tile, col_tile, transposed, tiles, max_tiles, n_tiles, ws, ws_bytes,

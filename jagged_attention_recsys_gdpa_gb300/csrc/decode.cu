@@ -981,11 +981,20 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
             const int key = (i >> 1) * 16 + key_of<true>(lane >> 2, i & 1);
             uint32_t x = scale_word<D>(vsc, r_base + key);
             if (D == 64) x |= x << 16;
-            // rows outside the sequence have codes of zero and any exponents: these become the reference
-            if (rare(partial) && (pos0 + key < at.s.lo || pos0 + key >= at.s.hi)) x = max(ref, 0) * 0x01010101u;
             e[i >> 1][i & 1] = x;
+          }
+          if (rare(partial)) {  // rows outside the sequence have codes of zero and any exponents: these become the reference
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+              const int pos = pos0 + (i >> 1) * 16 + key_of<true>(lane >> 2, i & 1);
+              if (pos < at.s.lo || pos >= at.s.hi) e[i >> 1][i & 1] = max(ref, 0) * 0x01010101u;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2 * MT; ++i) {
             // e - (R - 14), byte by byte: 0 .. 15 where fp16 factors do (a byte below borrows and ends up far above)
-            all |= d[i >> 1][i & 1] = x - static_cast<uint32_t>(ref - 14) * 0x01010101u;
+            d[i >> 1][i & 1] = e[i >> 1][i & 1] - static_cast<uint32_t>(ref - 14) * 0x01010101u;
+            all |= d[i >> 1][i & 1];
           }
           bool small = false;
           if (rare(__any_sync(0xffffffffu, (all & 0xf0f0f0f0u) != 0 || ref < 0))) {

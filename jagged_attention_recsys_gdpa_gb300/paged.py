@@ -20,6 +20,8 @@ errors (a bad page, a length past the table) are read with ``device_status``.
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import SOFTMAX, _act, _mask, _width
@@ -48,7 +50,7 @@ class PagedCache:
     """Page buffers k, v [n_pages, H, page_size, D] (bf16, or uint8 E4M3 codes with uint8 E8M0 exponents k_scales,
     v_scales [n_pages, H, page_size, D/32]); the layout is jattn_cache_t's. Holds the tensors it is given."""
 
-    __slots__ = ("_k", "_v", "_k_scales", "_v_scales", "_c")
+    __slots__ = ("_k", "_v", "_k_scales", "_v_scales", "_c", "_ref", "_device", "_index", "_page", "_H", "_D")
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
         mx = k_scales is not None
@@ -67,17 +69,19 @@ class PagedCache:
             raise ValueError("cache buffers must be contiguous")
         self._k, self._v, self._k_scales, self._v_scales = k, v, k_scales, v_scales
         self._c = B.cache(n, page, H, D, B.CACHE_MXFP8 if mx else B.CACHE_BF16, k, v, k_scales, v_scales)
+        self._ref = ctypes.byref(self._c)
+        self._device, self._index, self._page, self._H, self._D = k.device, k.device.index, page, H, D
 
     k = property(lambda self: self._k)
     v = property(lambda self: self._v)
     k_scales = property(lambda self: self._k_scales)
     v_scales = property(lambda self: self._v_scales)
     n_pages = property(lambda self: self._c.n_pages)
-    page_size = property(lambda self: self._c.page_size)
-    H = property(lambda self: self._c.H)
-    D = property(lambda self: self._c.D)
+    page_size = property(lambda self: self._page)
+    H = property(lambda self: self._H)
+    D = property(lambda self: self._D)
     format = property(lambda self: "mxfp8" if self._c.format == B.CACHE_MXFP8 else "bf16")
-    device = property(lambda self: self._k.device)
+    device = property(lambda self: self._device)
 
 
 def paged_cache(n_pages, page_size, H, D, format="bf16", device="cuda") -> PagedCache:
@@ -94,17 +98,17 @@ def paged_cache(n_pages, page_size, H, D, format="bf16", device="cuda") -> Paged
 
 
 def _check_rows(cache, x, name):
-    if x.dtype is not torch.bfloat16 or x.dim() != 3 or x.device != cache._k.device or not x.is_contiguous():
+    if x.dtype is not torch.bfloat16 or x.dim() != 3 or x.device != cache._device or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous bf16 tensor [total, H, D] on the cache's device")
 
 
 def _check_index(cache, t, n, name):
-    if t.dtype is not torch.int64 or t.shape != (n,) or t.device != cache._k.device or not t.is_contiguous():
+    if t.dtype is not torch.int64 or t.shape != (n,) or t.device != cache._device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int64 tensor [{n}] on the cache's device")
 
 
 def _check_table(cache, t):
-    if t.dtype is not torch.int32 or t.dim() != 2 or t.device != cache._k.device or not t.is_contiguous() \
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.device != cache._device or not t.is_contiguous() \
             or t.numel() == 0:
         raise ValueError("page_table must be a contiguous int32 tensor [B, max_pages] on the cache's device")
 
@@ -112,15 +116,15 @@ def _check_table(cache, t):
 def _check_rope(cache, rope):
     cos, sin = rope
     for t in rope:
-        if t.dtype is not torch.float32 or t.dim() != 2 or t.shape[1] != cache._c.D // 2 or t.shape != cos.shape \
-                or t.device != cache._k.device or not t.is_contiguous():
+        if t.dtype is not torch.float32 or t.dim() != 2 or t.shape[1] != cache._D // 2 or t.shape != cos.shape \
+                or t.device != cache._device or not t.is_contiguous():
             raise ValueError("rope tables must be two contiguous fp32 tensors [rows, D/2] on the cache's device")
     return cos, sin
 
 
 def _launch(cache, fn, *args):
     """fn(*args, workspace, its bytes, stream) with the cache's device current."""
-    index = cache._k.device.index
+    index = cache._index
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
             return _launch(cache, fn, *args)
@@ -138,9 +142,8 @@ def cache_append(cache, k, v, page_table, start, off=None, rope=None):
     nb = page_table.shape[0]
     _check_rows(cache, k, "k")
     _check_rows(cache, v, "v")
-    c = cache._c
     total = k.shape[0]
-    if k.shape != v.shape or k.shape != (total, c.H, c.D):
+    if k.shape != v.shape or k.shape != (total, cache._H, cache._D):
         raise ValueError("k and v must be [total, H, D] with the cache's H and D")
     _check_index(cache, start, nb, "start")
     if off is not None:
@@ -148,7 +151,7 @@ def cache_append(cache, k, v, page_table, start, off=None, rope=None):
     elif total != nb:
         raise ValueError("without off there must be one row per sequence")
     cos, sin = _check_rope(cache, rope) if rope is not None else (None, None)
-    _launch(cache, B.cache_append, c, nb, total, off, start, page_table, k, v, cos, sin)
+    _launch(cache, B.cache_append, cache._ref, nb, total, off, start, page_table, k, v, cos, sin)
 
 
 def cache_read(cache, page_table, off, start=None, total=None, k=None, v=None):
@@ -165,13 +168,12 @@ def cache_read(cache, page_table, off, start=None, total=None, k=None, v=None):
         if x is not None:
             _check_rows(cache, x, name)
             total = x.shape[0] if total is None else total
-            if x.shape != (total, cache.H, cache.D):
+            if x.shape != (total, cache._H, cache._D):
                 raise ValueError(f"{name} must be [total, H, D] with the cache's H and D")
     total = int(off[-1].item()) if total is None else int(total)
-    shape = (total, cache.H, cache.D)
-    k = k if k is not None else torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-    v = v if v is not None else torch.empty(shape, dtype=torch.bfloat16, device=cache.device)
-    _launch(cache, B.cache_read, cache._c, nb, total, off, start, page_table, k, v)
+    k = k if k is not None else torch.empty((total, cache._H, cache._D), dtype=torch.bfloat16, device=cache._device)
+    v = v if v is not None else torch.empty_like(k)
+    _launch(cache, B.cache_read, cache._ref, nb, total, off, start, page_table, k, v)
     return k, v
 
 
@@ -192,20 +194,19 @@ def decode(q, cache, page_table, kv_lens, q_off=None, act="softmax", causal=Fals
     if q.requires_grad and torch.is_grad_enabled():
         raise ValueError("decode has no backward pass: call it under torch.no_grad() or on a detached q")
     total_q, Hq, D = q.shape
-    c = cache._c
-    if D != c.D or Hq == 0 or Hq % c.H:
+    if D != cache._D or Hq == 0 or Hq % cache._H:
         raise ValueError("q must have the cache's D and a multiple of its heads")
     _check_index(cache, kv_lens, nb, "kv_lens")
     if q_off is not None:
         _check_index(cache, q_off, nb + 1, "q_off")
     elif total_q != nb:
         raise ValueError("without q_off there must be one query row per sequence")
-    rows = max_pages * c.page_size
+    rows = max_pages * cache._page
     if max_kv is not None and not 0 <= max_kv <= rows:
         raise ValueError("max_kv must lie between 0 and the rows of the page table")
     a, mask = _act(act), _mask(causal, window, block)
-    p = B.params(nb, total_q, rows if max_kv is None else max_kv, Hq, D, a, mask, _width(window, block), scale,
-                 norm_by_lkv)
+    p = ctypes.byref(B.params(nb, total_q, rows if max_kv is None else max_kv, Hq, D, a, mask, _width(window, block),
+                              scale, norm_by_lkv))
     if out is None:
         out = torch.empty_like(q)
     elif out.shape != q.shape:
@@ -215,11 +216,11 @@ def decode(q, cache, page_table, kv_lens, q_off=None, act="softmax", causal=Fals
     if a != SOFTMAX:
         lse = None
     elif lse is None:
-        lse = torch.empty((total_q, Hq), dtype=torch.float32, device=q.device)
+        lse = torch.empty((total_q, Hq), dtype=torch.float32, device=cache._device)
     elif lse.dtype != torch.float32 or lse.shape != (total_q, Hq) or lse.device != q.device \
             or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [total_q, Hq] on the cache's device")
-    n = B.decode_scratch_size(p, c)
-    scratch = torch.empty(n, dtype=torch.uint8, device=q.device)
-    _launch(cache, B.decode, p, c, q_off, kv_lens, page_table, q, out, lse, scratch.data_ptr(), n)
+    n = B.decode_scratch_size(p, cache._ref)
+    scratch = torch.empty(n, dtype=torch.uint8, device=cache._device)
+    _launch(cache, B.decode, p, cache._ref, q_off, kv_lens, page_table, q, out, lse, scratch.data_ptr(), n)
     return out, lse

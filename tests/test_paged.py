@@ -82,10 +82,10 @@ def test_decode_checks(lib):
                      (dict(scratch=None), 3), (dict(scratch=F + 16), 3), (dict(scratch_bytes=0), 3), (dict(ws=None), 3),
                      (dict(ws=F + 8), 3), (dict(ws_bytes=64), 3)]:
         assert decode(**kw) == want, kw
-    n = B.decode_scratch_size(params(), make_cache())
+    n = B.decode_scratch_size(ctypes.byref(params()), ctypes.byref(make_cache()))
     assert n > 0 and n % 256 == 0
     with pytest.raises(B.JattnError):
-        B.decode_scratch_size(params(H=5), make_cache())
+        B.decode_scratch_size(ctypes.byref(params(H=5)), ctypes.byref(make_cache()))
 
 
 def test_error_names(lib):
