@@ -39,11 +39,12 @@ namespace {
 constexpr int kWarps = 4;     // per CTA
 constexpr int kThreads = kWarps * 32;
 constexpr int kSms = 152;
-// CTAs per SM and steps held per worker: with 8 rows three CTAs of four warps fit
-// the registers, and two steps each the shared memory; twelve warps hide more
-// than a third step each does (decode_mixed 265 against 290 us, MXFP8 296 and 331).
-constexpr int ctas_per_sm(int nr) { return nr == 1 ? 3 : 2; }
-constexpr int stages_of(int nr) { return nr == 1 ? 2 : 3; }
+// CTAs per SM and steps held per worker: with 8 rows of 128 columns (or 16 of 64)
+// three CTAs of four warps fit the registers, and two steps each the shared
+// memory; twelve warps hide more than a third step each does (decode_mixed 265
+// against 290 us, MXFP8 296 and 331).
+constexpr int ctas_per_sm(int D, int nr) { return nr * D <= 128 ? 3 : 2; }
+constexpr int stages_of(int D, int nr) { return nr * D <= 128 ? 2 : 3; }
 constexpr int kMaxCtas = 3 * kSms;
 constexpr int kJoinThreads = 512;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -227,7 +228,7 @@ struct Layout {
 // [worker][stage] barriers: copied, and read by all of the worker's warps.
 template <int D, bool MX, int NR>
 constexpr int smem_bytes() {
-  return 1024 + kWarps * stages_of(NR) * (8192 + 2 * Layout<D, MX>::keys * Layout<D, MX>::scale + 16);
+  return 1024 + kWarps * stages_of(D, NR) * (8192 + 2 * Layout<D, MX>::keys * Layout<D, MX>::scale + 16);
 }
 
 // Byte offset of 16-byte piece `chunk` of row r in a step of STEP rows: rows of
@@ -478,25 +479,27 @@ __host__ __device__ inline Scratch carve(void* base, int ctas, int per_cta, int 
   return s;
 }
 
-// One row (E of its columns) of up to N pieces, joined by a warp: m and l of the
-// whole, and its accumulator divided by l. at(i): where piece i has its
-// accumulator's row and its m and l (shared or global memory).
+// One row of up to N pieces, joined by the lanes that share it, E quads of columns
+// each (quad e at col + 4 lanes e): m and l of the whole, and its accumulator
+// divided by l. at(i): where piece i has its accumulator's row and its m and l
+// (shared or global memory).
 template <int E, int N, typename At>
-__device__ __forceinline__ void join_row(const DecodeArgs& a, int col, int n, At at, float (&x)[E], float& m, float& l) {
-  float y[N][E];
+__device__ __forceinline__ void join_row(const DecodeArgs& a, int col, int lanes, int n, At at, float4 (&x)[E], float& m,
+                                         float& l) {
+  float4 y[N][E];
   float2 ml[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     ml[i] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[i][e] = 0.0f;
+    for (int e = 0; e < E; ++e) y[i][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (i >= n) continue;
     const float* acc;
     const float2* stats;
     at(i, acc, stats);
     ml[i] = *stats;
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[i][e] = acc[col + e];
+    for (int e = 0; e < E; ++e) y[i][e] = *reinterpret_cast<const float4*>(acc + col + 4 * lanes * e);
   }
   m = -INFINITY;
   l = 0.0f;
@@ -512,11 +515,14 @@ __device__ __forceinline__ void join_row(const DecodeArgs& a, int col, int n, At
   }
   const float inv = soft ? inverse_sum(l) : 1.0f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) x[e] = 0.0f;
+  for (int e = 0; e < E; ++e) {
+    x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = fmaf(w[i] * inv, y[i][e], x[e]);
+    for (int i = 0; i < N; ++i) {
+      const float f = w[i] * inv;
+      x[e] = make_float4(fmaf(f, y[i][e].x, x[e].x), fmaf(f, y[i][e].y, x[e].y), fmaf(f, y[i][e].z, x[e].z),
+                         fmaf(f, y[i][e].w, x[e].w));
+    }
   }
 }
 
@@ -527,16 +533,17 @@ __device__ __forceinline__ int64_t query_row(const DecodeArgs& a, int64_t q0, in
   return (q0 + i) * a.Hq + h * a.G + (r - i * a.G);
 }
 
-// A finished row of a unit.
+// A finished row of a unit, by the lanes that share it.
 template <int E>
-__device__ __forceinline__ void write_row(const DecodeArgs& a, int64_t q0, int r, int h, int D, int col, int n,
-                                          const float (&x)[E], float m, float l) {
+__device__ __forceinline__ void write_row(const DecodeArgs& a, int64_t q0, int r, int h, int D, int col, int lanes, int n,
+                                          const float4 (&x)[E], float m, float l) {
   const int64_t out = query_row(a, q0, r, h);
   const float f = row_norm(a, n);
   if (a.act == JATTN_SOFTMAX && col == 0) a.lse[out] = lse_of(m, l);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + out * D + col);
 #pragma unroll
-  for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16x2(x[e] * f, x[e + 1] * f);
+  for (int e = 0; e < E; ++e)
+    *reinterpret_cast<uint2*>(a.o + out * D + col + 4 * lanes * e) =
+        make_uint2(pack_bf16x2(x[e].x * f, x[e].y * f), pack_bf16x2(x[e].z * f, x[e].w * f));
 }
 
 // What a worker leaves for its CTA.
@@ -637,12 +644,12 @@ __device__ __forceinline__ void clear_rows(uint32_t vs, int pos0, int lo, int hi
 }
 
 template <int D, bool MX, int NR, int WM>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
     decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   void* scratch) {
   using L = Layout<D, MX>;
   constexpr int step = L::keys * WM, tile = 8 * NR * WM, KS = D / 16, MT = L::sub / 16, per_cta = kWarps / WM;
-  constexpr int kStages = stages_of(NR);
+  constexpr int kStages = stages_of(D, NR);
   extern __shared__ unsigned char smem_raw[];
   __shared__ int64_t start[kThreads];
   __shared__ Left left[per_cta];
@@ -1136,21 +1143,29 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
             scale_rows(o[g], w[0], w[1]);
             if (MX && ref >= 0) scale_rows(o[g], pow2(ref - 127), pow2(ref - 127));
             repair<D, MX>(a, at, n_steps, step, q[g], f[g], o[g], m[g], w, lo[g], hi[g]);
+            const int r0 = row_base + 8 * g;
+            if (unit_ends && begun) {  // all of it was in this run
+              if (a.act == JATTN_SOFTMAX && lane < 4) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int r = row_base + 8 * g + 2 * c + i;
-              if (r >= rows) continue;
-              if (unit_ends && begun) {  // all of it was in this run
-                const int64_t out = query_row(a, at.s.q0, r, at.h);
-                if (a.act == JATTN_SOFTMAX && lane < 4) a.lse[out] = lse_of(m[g][i], l[g][i]);
-                __nv_bfloat16* dst = a.o + out * D;
+                for (int i = 0; i < 2; ++i)
+                  if (r0 + 2 * c + i < rows) a.lse[query_row(a, at.s.q0, r0 + 2 * c + i, at.h)] = lse_of(m[g][i], l[g][i]);
+              }
+              // transposed, a lane has neighbouring columns 2c, 2c + 1 (and 8 more) of row lane / 4
+              const int r = r0 + (lane >> 2);
+              uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + query_row(a, at.s.q0, min(r, rows - 1), at.h) * D) + c;
 #pragma unroll
-                for (int j = 0; j < KS; ++j) {
-                  const float x = o[g][j][i] * norm, y = o[g][j][2 + i] * norm;
-                  dst[16 * j + column(0, lane)] = __float2bfloat16(x);
-                  dst[16 * j + column(1, lane)] = __float2bfloat16(y);
+              for (int j = 0; j < KS; ++j) {
+                const uint32_t x = movmatrix(pack_bf16x2(o[g][j][0] * norm, o[g][j][1] * norm));
+                const uint32_t y = movmatrix(pack_bf16x2(o[g][j][2] * norm, o[g][j][3] * norm));
+                if (r < rows) {
+                  dst[8 * j] = x;
+                  dst[8 * j + 4] = y;
                 }
-              } else {
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                if (r0 + 2 * c + i >= rows) continue;
                 const int row = warp_m * (8 * NR) + 8 * g + 2 * c + i;
                 if (lane < 4) stats[row] = make_float2(m[g][i], l[g][i]);
                 float* dst = acc + row * D;
@@ -1198,10 +1213,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
   // ---- the CTA's pieces: chains of one unit's, each from the incoming unit's (worker 0's head) or from a unit that a
   // worker began and left (its tail), on through the following workers' heads
   __syncthreads();
-  constexpr int E = D / 32;
-  const int warp = threadIdx.x >> 5;
+  constexpr int share_row = 8, E = D / (4 * share_row), groups = kThreads / share_row;  // lanes of a row
+  const int group = threadIdx.x / share_row, col = (threadIdx.x % share_row) * 4;
   int4 going_on = make_int4(-1, 0, 0, 0);
-  int turn = 0;  // rows are dealt to the warps in turn
+  int turn = 0;  // rows are dealt to the groups in turn
 #pragma unroll 1
   for (int begin = -1; begin < per_cta; ++begin) {
     const int w0 = max(begin, 0);
@@ -1215,7 +1230,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
       ++len;
       ends = left[x].head_ends;
     }
-    for (int r = (warp + turn) % kWarps; r < n; r += kWarps) {
+    for (int r = (group + groups - turn % groups) % groups; r < n; r += groups) {
       const auto at = [&](int i, const float*& acc, const float2*& stats) {
         const int w = w0 + i;
         if ((tail && i == 0) || left[w].head_last) {
@@ -1228,15 +1243,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NR))
           stats = sc.ml + row;
         }
       };
-      float x[E], mj, lj;
-      join_row<E, per_cta>(a, lane * E, len, at, x, mj, lj);
+      float4 x[E];
+      float mj, lj;
+      join_row<E, per_cta>(a, col, share_row, len, at, x, mj, lj);
       if (tail && ends) {
-        write_row<E>(a, unit.q0, unit.tile * tile + r, unit.h, D, lane * E, unit.n, x, mj, lj);
+        write_row<E>(a, unit.q0, unit.tile * tile + r, unit.h, D, col, share_row, unit.n, x, mj, lj);
       } else {
         const int64_t to = (static_cast<int64_t>(blockIdx.x) * 2 + (tail ? 1 : 0)) * tile + r;
-        if (lane == 0) sc.cml[to] = make_float2(mj, lj);
+        if (col == 0) sc.cml[to] = make_float2(mj, lj);
 #pragma unroll
-        for (int e = 0; e < E; ++e) sc.cacc[to * D + lane * E + e] = x[e];
+        for (int e = 0; e < E; ++e) *reinterpret_cast<float4*>(sc.cacc + to * D + col + 4 * share_row * e) = x[e];
       }
     }
     turn += n;
@@ -1311,9 +1327,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(DecodeArgs a, void* 
         x.z += y.z;
         x.w += y.w;
       }
-      const float v[4] = {x.x, x.y, x.z, x.w};
+      const float4 v[1] = {x};
       const float2 ml = a.act == JATTN_SOFTMAX ? row_ml[r] : make_float2(0.0f, 1.0f);
-      write_row<4>(a, q0, r0 + base + r, j.w, D, col, n_kv, v, ml.x, ml.y);
+      write_row<1>(a, q0, r0 + base + r, j.w, D, col, lanes, n_kv, v, ml.x, ml.y);
     }
     __syncthreads();
   }
@@ -1323,9 +1339,10 @@ struct Shape {
   int nr, wm, ctas, tile;
 };
 
-// A worker's tile holds an average sequence's rows per key/value head: 8 or 16
-// in one warp, 32 and 64 in two and four. CTAs: two per SM, fewer where the
-// largest possible number of steps leaves some without work.
+// A worker's tile holds an average sequence's rows per key/value head, up to 64:
+// 8 or 16 in one warp (32 of 64 columns in one warp measured slower than in two),
+// 32 and 64 in two and four. CTAs: two or three per SM, fewer where the largest
+// possible number of steps leaves some without work.
 Shape shape_of(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H) {
   Shape s;
   const int64_t rows = (total_q + B - 1) / B * G;
@@ -1337,7 +1354,7 @@ Shape shape_of(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G
   const int64_t tiles = total_q * G / s.tile + (total_q < B ? total_q : B);
   const int64_t per_cta = kWarps / s.wm;
   const double steps = static_cast<double>(tiles) * H * static_cast<double>((max_kv + step - 1) / step + 2);
-  const int most = kSms * ctas_per_sm(s.nr);
+  const int most = kSms * ctas_per_sm(D, s.nr);
   s.ctas = steps / per_cta >= most ? most : static_cast<int>(steps / per_cta) + 1;
   return s;
 }
