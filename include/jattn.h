@@ -386,7 +386,8 @@ int jattn_cache_read(const jattn_cache_t* cache, int64_t B, int64_t total, const
  * length outside [0, p->total_kv] sets JATTN_ERR_LENGTH and counts as 0.
  * Writes o [total_q, H, D] bf16 (which must not overlap q) and, for
  * JATTN_SOFTMAX, lse [total_q, H] fp32. A sequence with a bad page among
- * those it needs sets JATTN_ERR_PAGES; its rows are unspecified.
+ * those it needs sets JATTN_ERR_PAGES; its rows are unspecified, as are those
+ * of a call whose bounded waits ran out (JATTN_ERR_TIMEOUT).
  * A row that no key is allowed for gets o = 0, lse = -inf. Rows behind
  * q_off[B] are left as they were. Cached values at positions that a row's mask
  * excludes never reach it, whatever they are.
@@ -499,8 +500,9 @@ void jattn_profile_events(void* const* events);
 /* Test hook, per host thread (launches made from other threads keep their
  * own settings): after this call, bounded waits in the kernels give up after
  * `timeout_ns` nanoseconds (0 restores the default of two seconds), and
- * flag bit 0 makes the next launches skip the query-tile copy so that the
- * first wait on it runs out. Used to check that an expired wait reports
+ * flag bit 0 makes the next launches skip the query-tile copy (jattn_decode:
+ * every worker's first copy of keys and values) so that the first wait on it
+ * runs out. Used to check that an expired wait reports
  * JATTN_ERR_TIMEOUT and leaves the context usable. Flag bit 1 (bit 2) makes
  * the forward use the column-split (ping-pong) arrangement of its activation
  * warps whatever the shapes, so both can be checked on the same inputs;

@@ -1037,6 +1037,7 @@ int jattn_decode(const jattn_params_t* p, const jattn_cache_t* c, const int64_t*
   a.scale = p->scale > 0.0f ? p->scale : 1.0f / std::sqrt(static_cast<float>(p->D));
   a.scale_log2 = a.scale * 1.4426950408889634f;
   a.timeout_ns = g_timeout_ns;
+  a.debug_flags = g_debug_flags;
   a.status = static_cast<DevStatus*>(ws);
   const bool mx = c->format == JATTN_CACHE_MXFP8;
   int rows, lines;

@@ -38,6 +38,7 @@ struct DecodeArgs {
   int act, mask, window, norm_by_lkv;
   float scale, scale_log2;
   uint64_t timeout_ns;
+  int debug_flags;
   DevStatus* status;
 };
 

@@ -695,7 +695,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
       page = box_page(a, in, step, box, lane);
 #pragma unroll
       for (int s = 0; s < kStages - 1; ++s) {
-        if (loaded < steps) {
+        if (s == 0 && rare(a.debug_flags & 1)) {  // test hook: the first copy never comes
+          if (lane == 0) mbar_arrive_expect_tx(full, 16);
+          if (++loaded < steps) {
+            advance(in, a, tile, step);
+            page = box_page(a, in, step, box, lane);
+          }
+        } else if (loaded < steps) {
           load_step<D, MX, WM>(a, &k_map, &v_map, in, page, ring + s * (8192 * WM), scale_ring + s * (2 * step * L::scale),
                                full + s, box, lane);
           if (++loaded < steps) {

@@ -352,6 +352,110 @@ def test_decode_long_lengths(lens, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+def test_decode_many_sequences(fmt):
+    """More sequences than a CTA has threads (the plan then counts stretches of them), most of them short or empty."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    rng = np.random.default_rng(44)
+    lens = (rng.integers(0, 40, 300) * (rng.random(300) < 0.8)).tolist()
+    check_decode(J, lens, rng.integers(0, 3, 300).tolist(), 2, 1, 64, 16, fmt, seed=45, causal=True)
+    lens = (rng.integers(0, 3, 5000) * (rng.random(5000) < 0.3)).tolist()
+    check_decode(J, lens, [1] * 5000, 1, 1, 64, 8, fmt, seed=46, one_row=True)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+def test_decode_empty_calls(fmt):
+    """No query rows at all; a bound of no cached rows; sequences that share their pages."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    cache, table, _ = fill_cache(J, [40, 70], 16, 2, 64, fmt, seed=47)
+    none = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
+    o, lse = J.decode(none, cache, cu(table), cu(np.array([40, 70])), q_off=cu(np.zeros(3, np.int64)))
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    q = torch.randn(2, 4, 64, device="cuda").to(torch.bfloat16)
+    o, lse = J.decode(q, cache, cu(table), cu(np.zeros(2, np.int64)), max_kv=0)
+    assert bool((o == 0).all()) and bool(torch.isneginf(lse).all())
+    both = np.stack([table[1], table[1]])
+    same = q[:1].expand(2, -1, -1).contiguous()
+    o, lse = J.decode(same, cache, cu(both), cu(np.array([70, 70])))
+    assert torch.equal(o[0], o[1]) and torch.equal(lse[0], lse[1])
+    x = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    J.cache_append(cache, x, x, cu(table), cu(np.zeros(2, np.int64)), off=cu(np.zeros(3, np.int64)))
+    k, v = J.cache_read(cache, cu(table), cu(np.zeros(3, np.int64)))
+    assert k.shape == v.shape == (0, 2, 64)
+    assert J.device_status() == 0
+
+
+def test_expired_wait_reports_timeout_and_context_survives():
+    """Every worker's first copy skipped: the bounded waits run out, the call returns and the next one is right."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+    from jagged_attention_recsys_gdpa_gb300 import _binding as B
+
+    clear(J)
+    for Hq, fmt in ((2, "bf16"), (24, "mxfp8"), (64, "bf16")):  # one, two and four warps a worker
+        cache, table, _ = fill_cache(J, [400, 70, 3], 16, 1, 128, fmt, seed=48)
+        q = torch.randn(3, Hq, 128, device="cuda").to(torch.bfloat16)
+        args = (q, cache, cu(table), cu(np.array([400, 70, 3])))
+        o, lse = J.decode(*args)
+        torch.cuda.synchronize()
+        try:
+            B.debug_set(1, 20_000_000)
+            J.decode(*args)
+            assert J.device_status() == 6
+        finally:
+            B.debug_set(0, 0)
+        o2, lse2 = J.decode(*args)
+        assert J.device_status() == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+def test_rows_at_16_byte_addresses(fmt):
+    """Tensors whose first row lies 16 bytes behind a 32-byte boundary; 2 bytes behind one is refused."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    H, D, page, n = 2, 64, 16, 37
+    flat = torch.randn(2 * n * H * D + 64, generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).cuda()
+    at = lambda t, o: t[o:o + n * H * D].view(n, H, D)  # noqa: E731
+    k, v = at(flat, 8), at(flat, 8 + n * H * D + 16)
+    assert k.data_ptr() % 32 == 16 and v.data_ptr() % 32 == 16
+    table, n_pages = make_table([n], page, 6)
+    off, start = cu(np.array([0, n])), cu(np.array([0]))
+    caches = [J.paged_cache(n_pages, page, H, D, fmt) for _ in range(2)]
+    J.cache_append(caches[0], k, v, cu(table), start, off=off)
+    J.cache_append(caches[1], k.clone(), v.clone(), cu(table), start, off=off)
+    same_bits(snapshot(caches[0]), [None if t is None else t.cpu() for t in snapshot(caches[1])])
+    out = torch.zeros_like(flat)
+    J.cache_read(caches[0], cu(table), off, k=at(out, 8), v=at(out, 8 + n * H * D + 16))
+    want = J.cache_read(caches[0], cu(table), off)
+    assert torch.equal(at(out, 8), want[0]) and torch.equal(at(out, 8 + n * H * D + 16), want[1])
+    assert J.device_status() == 0
+    with pytest.raises(J.JattnError):
+        J.cache_append(caches[0], at(flat, 1), v, cu(table), start, off=off)
+    with pytest.raises(J.JattnError):
+        J.cache_read(caches[0], cu(table), off, k=at(out, 1), v=at(out, 8 + n * H * D + 16))
+    with pytest.raises(J.JattnError):
+        J.decode(at(flat, 1), caches[0], cu(np.repeat(table, n, 0)), torch.ones(n, dtype=torch.int64, device="cuda"))
+
+
+def test_first_call_inside_a_capture_is_refused(monkeypatch):
+    import jagged_attention_recsys_gdpa_gb300 as J
+    from jagged_attention_recsys_gdpa_gb300 import paged
+
+    cache = J.paged_cache(2, 16, 1, 64)
+    table, lens = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int64, device="cuda")
+    q = torch.zeros(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    J.decode(q, cache, table, lens)
+    monkeypatch.setattr(paged, "_status_blocks", {})
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q.add_(0)
+        with pytest.raises(RuntimeError, match="before the capture"):
+            J.decode(q, cache, table, lens)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
 def test_decode_large_scores(fmt):
     """Peaked softmax: score differences of hundreds, a maximum that moves along the length."""
     import jagged_attention_recsys_gdpa_gb300 as J
