@@ -1030,6 +1030,7 @@ int jattn_decode(const jattn_params_t* p, const jattn_cache_t* c, const int64_t*
   a.max_kv = p->total_kv;
   a.Hq = p->H;
   a.G = p->H / c->H;
+  a.g_inverse = static_cast<uint32_t>(((uint64_t(1) << 32) + a.G - 1) / a.G);
   a.act = p->act;
   a.mask = p->mask;
   a.window = (p->mask & (JATTN_MASK_WINDOW | JATTN_MASK_BLOCK)) ? std::min(p->window, 1 << 30) : 0;

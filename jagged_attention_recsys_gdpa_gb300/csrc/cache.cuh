@@ -35,6 +35,7 @@ struct DecodeArgs {
   int64_t B, total_q;
   int64_t max_kv;  // bound of kv_lens
   int Hq, G;       // query heads, query heads per key/value head
+  uint32_t g_inverse;  // 2^32 / G rounded up (G > 1)
   int act, mask, window, norm_by_lkv;
   float scale, scale_log2;
   uint64_t timeout_ns;

@@ -64,6 +64,14 @@ __device__ __forceinline__ float activate(float s, int act) {
   return act == JATTN_SILU ? silu(s) : act == JATTN_GELU_TANH ? gelu(s) : gelu_poly(s);
 }
 
+// Row r of a head's rows: its query, r / G. g_inverse is 2^32 / G rounded up, so
+// the product's high half is at most one too large.
+__device__ __forceinline__ int query_of(const DecodeArgs& a, int r) {
+  if (a.G == 1) return r;
+  const int q = static_cast<int>(__umulhi(static_cast<uint32_t>(r), a.g_inverse));
+  return q * a.G > r ? q - 1 : q;
+}
+
 // ---------------------------------------------------------------- plan
 // One sequence's share of the work: its query rows in tiles of `tile` rows, and
 // the steps of `step` keys that cover the keys its rows may see.
@@ -529,7 +537,7 @@ __device__ __forceinline__ void join_row(const DecodeArgs& a, int col, int lanes
 // The row of [total_q * Hq, D] that is row r of head h's rows of a sequence
 // whose first query row is q0.
 __device__ __forceinline__ int64_t query_row(const DecodeArgs& a, int64_t q0, int r, int h) {
-  const int i = a.G == 1 ? r : r / a.G;
+  const int i = query_of(a, r);
   return (q0 + i) * a.Hq + h * a.G + (r - i * a.G);
 }
 
@@ -559,13 +567,6 @@ struct Left {
 };
 
 // ---------------------------------------------------------------- kernel
-// Where the warps of one worker meet once, before its first copy.
-template <int WM>
-__device__ __forceinline__ void worker_barrier(int worker) {
-  if constexpr (WM == 1) __syncwarp();
-  else asm volatile("bar.sync %0, %1;" ::"r"(worker + 1), "n"(WM * 32) : "memory");
-}
-
 // Bounded wait; false (and the status set) when it runs out.
 __device__ __forceinline__ bool wait_full(const DecodeArgs& a, uint64_t* bar, uint32_t parity) {
   if (!rare(!mbar_try_wait(bar, parity))) return true;
@@ -667,6 +668,20 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
   if (tid == 0) left[in_cta] = Left{};
   constexpr int ring_bytes = kStages * 8192 * WM;
   static_assert(tile * (D * 4 + 8) <= ring_bytes, "a worker's ring holds a piece");
+  // a worker's barriers: copied, read by all of its warps (a stage each), and its warps' meeting at the run's end
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem_base + kWarps * kStages * (8192 + 2 * L::keys * L::scale)) +
+                         in_cta * (2 * kStages * WM);
+  uint64_t* const empty = full + kStages;
+  uint64_t* const met = empty + kStages;  // there are 2 kStages (WM - 1) more where WM > 1
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, WM);
+    }
+    if (WM > 1) mbar_init(met, WM);
+    fence_mbar_init();
+    fence_proxy_async();
+  }
   Place in{};  // the step that is copied next
   if (first < last) in = find_place(a, tile, step, start, seqs, first);
   __syncthreads();
@@ -675,18 +690,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
     const uint32_t smem = smem_u32(smem_base);
     const uint32_t ring = smem + in_cta * ring_bytes;
     const uint32_t scale_ring = smem + kWarps * kStages * 8192 + in_cta * (kStages * 2 * step * L::scale);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem_base + kWarps * kStages * (8192 + 2 * L::keys * L::scale)) +
-                     in_cta * (2 * kStages);
-    uint64_t* empty = full + kStages;
-    if (tid == 0) {
-      for (int s = 0; s < kStages; ++s) {
-        mbar_init(full + s, 1);
-        mbar_init(empty + s, WM);
-      }
-      fence_mbar_init();
-      fence_proxy_async();
-    }
-    worker_barrier<WM>(in_cta);
     const int box = min(step, a.cache.page_mask + 1);
     const int steps = static_cast<int>(last - first);
     int loaded = 0;  // steps whose copies have been issued (by the worker's first warp)
@@ -738,15 +741,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
         if (live) {
           const int delta = at.s.n - at.s.lq;
           const int end = rows - 1;  // rows behind it take its interval, and zeros for their query
-          key_interval(row_base / a.G, delta, at.s.n, a.mask, a.window, any_lo, all_hi);
-          key_interval(min(row_base + 8 * NR - 1, end) / a.G, delta, at.s.n, a.mask, a.window, all_lo,
+          key_interval(query_of(a, row_base), delta, at.s.n, a.mask, a.window, any_lo, all_hi);
+          key_interval(query_of(a, min(row_base + 8 * NR - 1, end)), delta, at.s.n, a.mask, a.window, all_lo,
                        any_hi);
 #pragma unroll
           for (int g = 0; g < NR; ++g) {
             const float base = a.act == JATTN_SOFTMAX ? a.scale_log2 : a.scale;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              key_interval(min(row_base + 8 * g + 2 * c + i, end) / a.G, delta, at.s.n, a.mask, a.window, lo[g][i], hi[g][i]);
+              key_interval(query_of(a, min(row_base + 8 * g + 2 * c + i, end)), delta, at.s.n, a.mask, a.window, lo[g][i], hi[g][i]);
               m[g][i] = !MX || a.act == JATTN_SOFTMAX ? -INFINITY : kLeast;
               l[g][i] = 0.0f;
               f[g][i] = base;
@@ -1132,7 +1135,16 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
         float* acc = run_ends ? reinterpret_cast<float*>(smem_base + in_cta * ring_bytes)
                               : sc.acc + static_cast<int64_t>(me) * tile * D;
         float2* stats = run_ends ? reinterpret_cast<float2*>(acc + tile * D) : sc.ml + static_cast<int64_t>(me) * tile;
-        if (WM > 1 && run_ends) worker_barrier<WM>(in_cta);
+        if constexpr (WM > 1) {
+          if (run_ends) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(met);
+            if (!wait_full(a, met, 0)) {
+              ok = false;
+              break;
+            }
+          }
+        }
         if (live) {
           const float norm = row_norm(a, at.s.n);
 #pragma unroll
