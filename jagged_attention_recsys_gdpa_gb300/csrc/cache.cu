@@ -9,6 +9,10 @@
 // is 16 bytes of bf16 or, of an MXFP8 cache, 16 values: 32 bytes of bf16 in one
 // access and 16 bytes of codes. (Of 8 values the instructions, not memory, were
 // the bound; of the 32 of a block the accesses lay too far apart.)
+//
+// Measured: 213 k rows of 4 heads of 128, keys rotated, bf16 (981 MB) 137 us,
+// 7.1 TB/s; 131 k rows of 8 heads to MXFP8 (822 MB) 150 us, 5.5 TB/s; 213 k rows
+// of 8 heads back from MXFP8 (1.32 GB) 210 us, 6.3 TB/s.
 #include <cstdint>
 
 #include <cuda_fp16.h>
