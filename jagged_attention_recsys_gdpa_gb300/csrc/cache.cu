@@ -199,6 +199,7 @@ __global__ void __launch_bounds__(kCacheBlock) append_kernel(AppendArgs a) {
   const int per_head = a.D / (8 * P), per_row = a.c.H * per_head;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows;
   const int rows = static_cast<int>(min(static_cast<int64_t>(a.rows), a.total - row0)), units = rows * per_row;
+  wait_for_dependency();
   if (a.off != nullptr)
     check_offsets(a.off, a.B, a.total, static_cast<int64_t>(blockIdx.x) * kCacheBlock + threadIdx.x,
                   static_cast<int64_t>(gridDim.x) * kCacheBlock, a.status);
@@ -302,6 +303,7 @@ __global__ void __launch_bounds__(kCacheBlock) read_kernel(ReadArgs a) {
   const int per_head = a.D / (8 * P), per_row = a.c.H * per_head;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows;
   const int rows = static_cast<int>(min(static_cast<int64_t>(a.rows), a.total - row0)), units = rows * per_row;
+  wait_for_dependency();
   if (static_cast<int>(threadIdx.x) < rows)
     row[threadIdx.x] = place(a.c, a.off, a.start, a.B, row0 + threadIdx.x, a.status);
   check_offsets(a.off, a.B, a.total, static_cast<int64_t>(blockIdx.x) * kCacheBlock + threadIdx.x,
@@ -357,6 +359,20 @@ unsigned ctas_of(int64_t total, int rows) { return static_cast<unsigned>((total 
 // with four), then four; two when quantising, which needs the registers
 // (append_chunks_mxfp8 150 us against 156 with four and 170 with one).
 bool few_rows(int64_t total, int per_row) { return total * per_row <= int64_t(152) * 8 * kCacheBlock; }
+// Launched to be set up while the kernel before it ends (it waits for that first).
+template <typename Args>
+cudaError_t launch(void (*kernel)(Args), const Args& a, int64_t total, cudaStream_t stream) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(ctas_of(total, a.rows));
+  c.blockDim = dim3(kCacheBlock);
+  c.stream = stream;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, a);
+}
 bool wide(const void* k, const void* v) {
   return ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
 }
@@ -372,8 +388,7 @@ cudaError_t launch_cache_append(const CacheView& c, bool mx, int64_t B, int64_t 
                      D, rope_rows, rows_of(per_row, units), wide(k, v), status};
   const auto kernel = mx ? (units == 1 ? append_kernel<true, 1> : append_kernel<true, 2>)
                          : (units == 1 ? append_kernel<false, 1> : append_kernel<false, 4>);
-  kernel<<<ctas_of(total, a.rows), kCacheBlock, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch(kernel, a, total, stream);
 }
 
 cudaError_t launch_cache_read(const CacheView& c, bool mx, int64_t B, int64_t total, const int64_t* off,
@@ -385,8 +400,7 @@ cudaError_t launch_cache_read(const CacheView& c, bool mx, int64_t B, int64_t to
                    wide(k, v), status};
   const auto kernel = mx ? (units == 1 ? read_kernel<true, 1> : read_kernel<true, 4>)
                          : (units == 1 ? read_kernel<false, 1> : read_kernel<false, 4>);
-  kernel<<<ctas_of(total, a.rows), kCacheBlock, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch(kernel, a, total, stream);
 }
 
 }  // namespace jattn
