@@ -634,6 +634,13 @@ __device__ __forceinline__ void load_step(const DecodeArgs& a, const CUtensorMap
   }
 }
 
+// The query rows of a unit whose first step is copied next, on their way to L2.
+__device__ __forceinline__ void prefetch_query(const DecodeArgs& a, const Place& p, int tile, int D, int lane) {
+  const int rows = min(tile, p.s.lq * a.G - p.tile * tile), line = 64;  // elements
+  for (int i = lane; i < rows * (D / line); i += 32)
+    prefetch_l2(a.q + query_row(a, p.s.q0, p.tile * tile + i / (D / line), p.h) * D + (i % (D / line)) * line);
+}
+
 // Zeros for the V rows of a step outside [lo, hi): what their places hold (rows
 // past the sequence's, or whatever was there where no box was copied) has to be
 // finite to vanish under a weight of zero.
@@ -731,6 +738,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
     int lo[NR][2], hi[NR][2];   // keys that they may see
     int all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;  // that every row, and that any row, of the warp's may see
     int ref = -1;               // MXFP8: V's reference exponent, none yet
+    bool new_ref = true;        // the unit may still choose its own: nothing is accumulated
     bool live = false;          // the warp's rows hold one of the tile's at least
     int row_base = 0, rows = 0;
     bool fresh = true;
@@ -743,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
       if (rare(fresh)) {  // its rows arrive while its first step does
         fresh = false;
         n_steps = 0;
-        ref = -1;
+        new_ref = true;
         rows = at.s.lq * a.G;
         row_base = at.tile * tile + warp_m * (8 * NR);
         live = row_base < rows;
@@ -777,28 +785,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
               q[g][kk][0] = src ? __ldg(src + w0) : 0u;
               q[g][kk][1] = src ? __ldg(src + w1) : 0u;
             }
-            if constexpr (MX) {
-              float x = 0.0f;
-#pragma unroll
-              for (int kk = 0; kk < KS; ++kk) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  x = fmaxf(x, fmaxf(fabsf(query_value<false>(q[g][kk][i], 0)), fabsf(query_value<false>(q[g][kk][i], 1))));
-              }
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-              // the power of two that brings the largest value to [2^14, 2^15)
-              const int e = x == 0.0f ? 0 : min(14 - (static_cast<int>(__float_as_uint(x) >> 23) - 127), 120);
-              const float up = pow2(e);
-#pragma unroll
-              for (int kk = 0; kk < KS; ++kk) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                  q[g][kk][i] = pack_f16x2(query_value<false>(q[g][kk][i], 0) * up, query_value<false>(q[g][kk][i], 1) * up);
-              }
-#pragma unroll
-              for (int i = 0; i < 2; ++i) f[g][i] *= pow2(-__shfl_sync(0xffffffffu, e, (2 * c + i) * 4));
-            }
           }
         }
       }
@@ -822,6 +808,32 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
         if (++loaded < steps) {
           advance(in, a, tile, step);
           page = box_page(a, in, step, box, lane);
+          if (rare(in.t == 0)) prefetch_query(a, in, tile, D, lane);
+        }
+      }
+      if (MX && rare(n_steps == 0) && live) {  // the rows just loaded, as fp16
+#pragma unroll
+        for (int g = 0; g < NR; ++g) {
+          float x = 0.0f;
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              x = fmax3(x, fabsf(query_value<false>(q[g][kk][i], 0)), fabsf(query_value<false>(q[g][kk][i], 1)));
+          }
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          // the power of two that brings the largest value to [2^14, 2^15)
+          const int e = x == 0.0f ? 0 : min(14 - (static_cast<int>(__float_as_uint(x) >> 23) - 127), 120);
+          const float up_q = pow2(e);
+#pragma unroll
+          for (int kk = 0; kk < KS; ++kk) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              q[g][kk][i] = pack_f16x2(query_value<false>(q[g][kk][i], 0) * up_q, query_value<false>(q[g][kk][i], 1) * up_q);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) f[g][i] *= pow2(-__shfl_sync(0xffffffffu, e, (2 * c + i) * 4));
         }
       }
       ++n_steps;
@@ -1021,8 +1033,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
             d[i >> 1][i & 1] = e[i >> 1][i & 1] - static_cast<uint32_t>(ref - 14) * 0x01010101u;
             all |= d[i >> 1][i & 1];
           }
-          bool small = false;
-          if (rare(__any_sync(0xffffffffu, (all & 0xf0f0f0f0u) != 0 || ref < 0))) {
+          bool small = false, look = (all & 0xf0f0f0f0u) != 0;
+          if (rare(new_ref)) {
+            // a new unit keeps the reference of the one before if all its first exponents lie within 2^7 below it
+            uint32_t every = 0x08080808u;
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) every &= d[i >> 1][i & 1];
+            look = look || every != 0x08080808u || ref < 0;
+          }
+          if (rare(__any_sync(0xffffffffu, look))) {
             int top = 14;  // the largest exponent but NaN's (R - 14 is no negative byte)
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i) {
@@ -1033,8 +1052,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
               }
             }
             top = __reduce_max_sync(0xffffffffu, top);
-            if (ref < 0 || top > ref + 1) {
-              if (ref >= 0) {
+            if (new_ref || top > ref + 1) {
+              if (!new_ref) {
 #pragma unroll
                 for (int g = 0; g < NR; ++g) scale_rows(o[g], pow2(ref - top - 1), pow2(ref - top - 1));
               }
@@ -1052,6 +1071,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
             }
             small = __any_sync(0xffffffffu, (out & 0xfffffff0u) != 0);
           }
+          new_ref = false;
           // rows (keys) of two 16-byte pieces for the transposing loads
           const int r = r_base + (lane & 15), half = lane >> 4;
           if (rare(small)) {  // bf16 products for these keys
@@ -1168,7 +1188,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
               if (MX && a.act == JATTN_SOFTMAX) m[g][i] -= kLift;
             }
             scale_rows(o[g], w[0], w[1]);
-            if (MX && ref >= 0) scale_rows(o[g], pow2(ref - 127), pow2(ref - 127));
+            if (MX && !new_ref) scale_rows(o[g], pow2(ref - 127), pow2(ref - 127));
             repair<D, MX>(a, at, n_steps, step, q[g], f[g], o[g], m[g], w, lo[g], hi[g]);
             const int r0 = row_base + 8 * g;
             if (unit_ends && begun) {  // all of it was in this run

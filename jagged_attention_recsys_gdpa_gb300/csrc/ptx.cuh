@@ -265,6 +265,8 @@ __device__ __forceinline__ uint32_t tmem_ld1(uint32_t taddr) {
 #undef JATTN_R8
 #undef JATTN_W8
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // ---------------------------------------------------------------- programmatic launches
 // A kernel launched with programmatic stream serialisation may start once every
 // CTA of the kernel before it has called the first; it sees that kernel's results
