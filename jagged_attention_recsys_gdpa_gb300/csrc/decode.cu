@@ -362,12 +362,12 @@ __device__ __forceinline__ float exponent_of(float x) {
 }
 
 // Softmax: one over the sum of the weights, 0 for a row that saw no key.
-__device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : __fdividef(1.0f, l); }
 // Pointwise activations: the normaliser.
 __device__ __forceinline__ float row_norm(const DecodeArgs& a, int n) {
   return a.act != JATTN_SOFTMAX && a.norm_by_lkv && n > 0 ? 1.0f / static_cast<float>(n) : 1.0f;
 }
-__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2; }
+__device__ __forceinline__ float lse_of(float m, float l) { return l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2; }
 
 // The exponents of row r (D = 64: in the low half; what lies above is not used).
 template <int D>
@@ -607,7 +607,7 @@ __device__ __forceinline__ void load_step(const DecodeArgs& a, const CUtensorMap
   const bool ok = page >= 0 && page < a.cache.n_pages;
   if (rare(page != kNoBox && !ok)) record_error(a.status, JATTN_ERR_PAGES, 80, p.b);
   const uint32_t b = smem_u32(bar);
-  const auto copy = [&](int r, int lines) {  // the box of step rows r ..., by `lines` copies
+  const auto copy = [&](int r, int lines, int64_t page) {  // the box of step rows r ..., by `lines` copies
     const int y = (p.s.k0 + p.t * step + r) & a.cache.page_mask;
     for (int x = 0; x < lines; ++x) {
       const uint32_t to = stage + x * (step * L::line) + r * L::line;
@@ -623,14 +623,18 @@ __device__ __forceinline__ void load_step(const DecodeArgs& a, const CUtensorMap
   if (!rare(box != step)) {  // the same page in every lane
     if (elect_one()) {
       mbar_arrive_expect_tx(bar, ok ? step * 2 * (L::row + L::scale) : 0);
-      if (ok) copy(0, 1);
+      if (ok) copy(0, 1, page);
     }
     __syncwarp();
   } else {
-    const uint32_t n = __popc(__ballot_sync(0xffffffffu, ok));
-    if (lane == 0) mbar_arrive_expect_tx(bar, n * static_cast<uint32_t>(box * 2 * (L::row + L::scale)));
+    const uint32_t boxes = __ballot_sync(0xffffffffu, ok);
+    const bool me = elect_one();
+    if (me) mbar_arrive_expect_tx(bar, __popc(boxes) * static_cast<uint32_t>(box * 2 * (L::row + L::scale)));
+    for (int i = 0; i * box < step; ++i) {
+      const int64_t pg = __shfl_sync(0xffffffffu, page, i);
+      if (me && (boxes >> i & 1)) copy(i * box, L::row / L::line, pg);  // boxes of one line: a step's lines lie apart
+    }
     __syncwarp();
-    if (ok) copy(lane * box, L::row / L::line);  // boxes of one line: a step's lines lie apart
   }
 }
 
