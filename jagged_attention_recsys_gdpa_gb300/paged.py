@@ -136,12 +136,14 @@ def cache_append(cache, k, v, page_table, start, off=None, rope=None):
     at position start[b] + i (start int64 [B], the length cached before; negative
     skips the sequence). ``off`` int64 [B+1] are the rows' prefix sums (None: one
     row per sequence); rows behind off[B] are skipped. With ``rope`` = (cos, sin)
-    tables keys are rotated at their own positions before they are stored. See
-    jattn_cache_append."""
+    tables keys are rotated at their own positions before they are stored. No
+    gradient. See jattn_cache_append."""
     _check_table(cache, page_table)
     nb = page_table.shape[0]
     _check_rows(cache, k, "k")
     _check_rows(cache, v, "v")
+    if (k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
+        raise ValueError("cache_append has no backward pass: call it under torch.no_grad() or on detached rows")
     total = k.shape[0]
     if k.shape != v.shape or k.shape != (total, cache._H, cache._D):
         raise ValueError("k and v must be [total, H, D] with the cache's H and D")

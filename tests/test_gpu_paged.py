@@ -369,7 +369,7 @@ def test_decode_empty_calls(fmt):
     import jagged_attention_recsys_gdpa_gb300 as J
 
     clear(J)
-    cache, table, _ = fill_cache(J, [40, 70], 16, 2, 64, fmt, seed=47)
+    cache, table, pages = fill_cache(J, [40, 70], 16, 2, 64, fmt, seed=47)
     none = torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     o, lse = J.decode(none, cache, cu(table), cu(np.array([40, 70])), q_off=cu(np.zeros(3, np.int64)))
     assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
@@ -379,7 +379,12 @@ def test_decode_empty_calls(fmt):
     both = np.stack([table[1], table[1]])
     same = q[:1].expand(2, -1, -1).contiguous()
     o, lse = J.decode(same, cache, cu(both), cu(np.array([70, 70])))
-    assert torch.equal(o[0], o[1]) and torch.equal(lse[0], lse[1])
+    # The two sequences lie at different places of the split over workers, so their sums of the same terms are joined
+    # from different pieces: (l0 + l1) + l2 in one, l0 + (l1 + l2) in the other, each with factors 2^(m_i - m) of its
+    # own. A last bit of l, 2^-23 of it, is 2^-23 absolute in the lse and up to a step of o's rounding, so the two
+    # need not be the same bit for bit; either has to lie within the bounds of the 64-bit values.
+    ro, rl, to, tl = R.decode(np64(same), pages[0], pages[1], both, [70, 70], np.arange(3), **weight_parts(fmt))
+    assert np.all(np.abs(np64(o) - ro) <= to) and np.all(np.abs(np64(lse) - rl) <= tl)
     x = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
     J.cache_append(cache, x, x, cu(table), cu(np.zeros(2, np.int64)), off=cu(np.zeros(3, np.int64)))
     k, v = J.cache_read(cache, cu(table), cu(np.zeros(3, np.int64)))
@@ -512,6 +517,43 @@ def test_decode_mxfp8_dynamic_range(case, act, D):
     assert np.all(np.abs(np64(o) - ro)[~over] <= (to + floor)[~over])
     if act == "softmax":
         assert np.all(np.abs(np64(lse) - rl) <= tl)
+
+
+def test_decode_mxfp8_largest_exponent():
+    """V blocks of exponent 254 (the largest number E8M0 has) with codes small enough for finite sums: values up to
+    7 * 2^-9 * 2^127, averaged by softmax weights."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    H, D, page, lens = 2, 128, 32, [200, 33, 1, 70]
+    cache, table, _ = fill_cache(J, lens, page, H, D, "mxfp8", seed=111)
+    g = torch.Generator().manual_seed(112)
+    sign = torch.randint(0, 2, cache.v.shape, generator=g) * 128
+    cache.v.copy_((torch.randint(0, 8, cache.v.shape, generator=g) + sign).to(torch.uint8))
+    cache.v_scales.copy_((254 - torch.randint(0, 4, cache.v_scales.shape, generator=g)).to(torch.uint8))
+    q = torch.randn(4, 2 * H, D, generator=g).to(torch.bfloat16)
+    o, _ = J.decode(q.cuda(), cache, cu(table), cu(np.array(lens)))
+    assert J.device_status() == 0
+    kp, vp = (R.dequantise(c.cpu().numpy(), e.cpu().numpy())
+              for c, e in ((cache.k, cache.k_scales), (cache.v, cache.v_scales)))
+    ro, _, to, _ = R.decode(np64(q), np.nan_to_num(kp), vp, table, lens, np.arange(5), **weight_parts("mxfp8", 4))
+    assert np.all(np.abs(np64(o) - ro) <= to)
+
+
+def test_append_refuses_rows_that_need_a_gradient():
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    cache = J.paged_cache(2, 16, 2, 64)
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    start = torch.zeros(1, dtype=torch.int64, device="cuda")
+    x = torch.randn(1, 2, 64, device="cuda").to(torch.bfloat16)
+    y = x.clone().requires_grad_(True)
+    for k, v in ((y, x), (x, y)):
+        with pytest.raises(ValueError, match="no backward pass"):
+            J.cache_append(cache, k, v, table, start)
+    with torch.no_grad():
+        J.cache_append(cache, y, y, table, start)
+    assert torch.equal(cache.k[0, :, 0], x[0])
 
 
 def test_decode_masked_values_never_reach_a_row():
