@@ -8,17 +8,16 @@
 // Bound. Every cached row is read once and meets the Lq * G query rows of its
 // sequence and head, 4 D operations per 2 rows of 2 D bytes: for up to some 60
 // rows the cache's bytes bound the call, not the tensor cores. So the layout
-// serves the copies: each worker keeps its own ring of stages in shared
-// memory, filled by TMA straight from the pages (a step's rows are one piece of
-// a page, or one piece each of several small pages), and the
-// products are warp-level MMAs with keys (then columns) on their 16 rows and
-// the query rows on their 8 columns; a 128-row tcgen05 tile would be mostly
-// padding here and would stage operands and accumulators through TMEM for
-// nothing.
+// serves the copies: each worker keeps its own ring of stages in shared memory,
+// filled by TMA straight from the pages (a step's rows are one piece of a page, or
+// one piece each of several small pages), and the products are warp-level MMAs with
+// keys (then columns) on their 16 rows and the query rows on their 8 columns; a
+// 128-row tcgen05 tile would be mostly padding here and would stage operands and
+// accumulators through TMEM for nothing.
 //
-// Split. A unit is one (sequence, tile of 8 to 64 query rows, key/value head);
+// Split. A unit is one (sequence, key/value head, tile of 8 or 16 query rows);
 // its keys go in steps of a fixed number of positions. All units' steps are
-// numbered through, and every worker (one warp, or as many as its tile needs)
+// numbered through, and every worker (one warp, or two that share a tile)
 // takes one contiguous run of equal length, wherever it begins and ends: long
 // histories are split, short ones share a worker, and no worker has more than any
 // other. A unit that lies within one run is finished there; of any other, each run
@@ -28,9 +27,9 @@
 //
 // Measured: 64 histories of 50 to 32,000 keys, 8 heads of 128, bf16 (1.78 GB)
 // 264 us, 6.75 TB/s, the rate of a plain copy; 128 of them in MXFP8 (1.49 GB)
-// 257 us, 5.8 TB/s, where the conversions' latency binds (the copies alone take
+// 246 us, 6.05 TB/s, where the conversions' latency binds (the copies alone take
 // 231); 32 query heads on 8, 1,000 to 8,000 keys (615 MB) 100 us; one history of
-// 130,001 keys (67 MB) 20 us; a call that moves next to nothing 10 us.
+// 130,001 keys (67 MB) 19 us; a call that moves next to nothing 9.8 us.
 #include <atomic>
 #include <cstdint>
 
@@ -45,13 +44,12 @@ namespace {
 constexpr int kWarps = 4;     // per CTA
 constexpr int kThreads = kWarps * 32;
 constexpr int kSms = 152;
-// CTAs per SM and steps held per worker: with 8 rows of 128 columns (or 16 of 64)
-// three CTAs of four warps fit the registers, and two steps each the shared
-// memory; twelve warps hide more than a third step each does (decode_mixed 265
-// against 290 us, MXFP8 296 and 331).
-constexpr int ctas_per_sm(int D, int nr) { return nr * D <= 128 ? 3 : 2; }
-constexpr int stages_of(int D, int nr) { return nr * D <= 128 ? 2 : 3; }
-constexpr int kMaxCtas = 3 * kSms;
+// CTAs per SM and steps held per worker: three CTAs of four warps fit the
+// registers, and two steps each the shared memory; twelve warps hide more than a
+// third step each does (decode of 64 histories, 1.78 GB, 265 against 290 us, of 128 in
+// MXFP8 296 against 331).
+constexpr int kCtasPerSm = 3, kStages = 2;
+constexpr int kMaxCtas = kCtasPerSm * kSms;
 // The join's CTAs: rows at a time, and CTAs that share a unit's rows (one history
 // of 130,001 keys 18.5 us against 19.3 with one CTA of 512 threads and all rows).
 constexpr int kJoinThreads = 256, kJoinRows = 2, kJoinCtas = 4;
@@ -89,7 +87,7 @@ struct Seq {
   int lo, hi;   // keys that any of its rows may see
   int k0;       // first step's first key
   int steps;    // at least 1: a unit without keys still writes its rows
-  int tiles;    // of query rows; each comes with every head
+  int tiles;    // of query rows, for every head
 };
 
 __device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b, int tile, int step) {
@@ -115,8 +113,8 @@ __device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b, int tile, int 
   return s;
 }
 
-// A worker's place in the numbering of all steps: tiles of a sequence, heads of
-// a tile, steps of a head.
+// A worker's place in the numbering of all steps: heads of a sequence, tiles of a
+// head (which read the same keys), steps of a tile.
 struct Place {
   Seq s;
   const int32_t* table;
@@ -126,10 +124,10 @@ struct Place {
 __device__ __forceinline__ void advance(Place& p, const DecodeArgs& a, int tile, int step) {
   if (!rare(++p.t >= p.s.steps)) return;
   p.t = 0;
-  if (++p.h < a.cache.H) return;
-  p.h = 0;
   if (++p.tile < p.s.tiles) return;
   p.tile = 0;
+  if (++p.h < a.cache.H) return;
+  p.h = 0;
   do {
     if (++p.b >= a.B) return;  // behind the last step: never used
     p.s = seq_of(a, p.b, tile, step);
@@ -223,8 +221,8 @@ __device__ __forceinline__ Place find_place(const DecodeArgs& a, int tile, int s
   p.table = a.cache.table + p.b * a.cache.max_pages;
   const int64_t unit = divide(first - at, p.s.steps);
   p.t = static_cast<int>(first - at - unit * p.s.steps);
-  p.tile = static_cast<int>(divide(unit, a.cache.H));
-  p.h = static_cast<int>(unit - static_cast<int64_t>(p.tile) * a.cache.H);
+  p.h = static_cast<int>(divide(unit, p.s.tiles));
+  p.tile = static_cast<int>(unit - static_cast<int64_t>(p.h) * p.s.tiles);
   return p;
 }
 
@@ -242,9 +240,9 @@ struct Layout {
 // Shared memory of a CTA: [worker][stage] K rows then V rows (1024-byte aligned,
 // in TMA's 128- or 64-byte swizzle), [worker][stage] K then V exponents, then
 // [worker][stage] barriers: copied, and read by all of the worker's warps.
-template <int D, bool MX, int NR>
+template <int D, bool MX>
 constexpr int smem_bytes() {
-  return 1024 + kWarps * stages_of(D, NR) * (8192 + 2 * Layout<D, MX>::keys * Layout<D, MX>::scale + 16);
+  return 1024 + kWarps * kStages * (8192 + 2 * Layout<D, MX>::keys * Layout<D, MX>::scale + 16);
 }
 
 // Byte offset of 16-byte piece `chunk` of row r in a step of STEP rows: rows of
@@ -665,12 +663,11 @@ __device__ __forceinline__ void clear_rows(uint32_t vs, int pos0, int lo, int hi
 }
 
 template <int D, bool MX, int NR, int WM>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NR))
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   void* scratch) {
   using L = Layout<D, MX>;
   constexpr int step = L::keys * WM, tile = 8 * NR * WM, KS = D / 16, MT = L::sub / 16, per_cta = kWarps / WM;
-  constexpr int kStages = stages_of(D, NR);
   extern __shared__ unsigned char smem_raw[];
   __shared__ int64_t start[kThreads];
   __shared__ Left left[per_cta];
@@ -1393,22 +1390,32 @@ struct Shape {
   int nr, wm, ctas, tile;
 };
 
-// A worker's tile holds an average sequence's rows per key/value head, up to 64:
-// 8 or 16 in one warp (32 of 64 columns in one warp measured slower than in two),
-// 32 and 64 in two and four. CTAs: two or three per SM, fewer where the largest
-// possible number of steps leaves some without work.
+// A tile has 8 rows; 16 of a bf16 cache if an average sequence has more than 8 per
+// key/value head: held by one warp at D = 64 (two groups of 8), by two warps at D
+// = 128. More tiles read the cache again, but a head's follow each other and find
+// it in L2. Measured with tiles of up to 64 rows in one to four warps of two groups
+// each (which leave registers for two CTAs an SM) against this: 300 sequences of
+// 100 to 500 keys, D = 128, 16 / 32 / 64 rows 92 / 125 / 220 us against 83 / 112 /
+// 174 (MXFP8 108 / 191 / 273 against 70 / 104 / 167); 16 of 8,000 to 16,000 keys 138
+// / 176 / 297 against 129 / 168 / 267 (MXFP8 101 / 167 / 278 against 92 / 142 / 250).
+// With 8 rows a bf16 cache's steps are too short to pay for themselves (64 rows of long histories: 469
+// us), with 16 an MXFP8 cache's two warps wait for each other (16 rows: 86 us against
+// 70; only 64 rows of long histories gain, 231 against 250). At D = 64 two warps of
+// a group each take 0 to 7% longer than one of two (134 us against 141).
+// CTAs: three per SM, fewer where the largest possible number of steps leaves some
+// without work.
 Shape shape_of(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H) {
   Shape s;
   const int64_t rows = (total_q + B - 1) / B * G;
-  s.nr = rows <= 8 ? 1 : 2;
-  s.wm = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  s.nr = D == 64 && !mx && rows > 8 ? 2 : 1;
+  s.wm = D == 128 && !mx && rows > 8 ? 2 : 1;
   s.tile = 8 * s.nr * s.wm;
   const int64_t step = 4096 / (D * (mx ? 1 : 2)) * s.wm;
   // tiles of all sequences: each has at most one that is not full
   const int64_t tiles = total_q * G / s.tile + (total_q < B ? total_q : B);
   const int64_t per_cta = kWarps / s.wm;
   const double steps = static_cast<double>(tiles) * H * static_cast<double>((max_kv + step - 1) / step + 2);
-  const int most = kSms * ctas_per_sm(D, s.nr);
+  const int most = kSms * kCtasPerSm;
   s.ctas = steps / per_cta >= most ? most : static_cast<int>(steps / per_cta) + 1;
   return s;
 }
@@ -1416,7 +1423,7 @@ Shape shape_of(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G
 template <int D, bool MX, int NR, int WM>
 cudaError_t launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, const Shape& s, void* scratch,
                    cudaStream_t stream) {
-  constexpr int smem = smem_bytes<D, MX, NR>();
+  constexpr int smem = smem_bytes<D, MX>();
   cudaError_t e;
   static std::atomic<uint64_t> ready{0};  // devices (at most 64) whose kernel has its shared memory
   int dev = 0;
@@ -1446,10 +1453,10 @@ cudaError_t launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap&
 template <int D, bool MX>
 cudaError_t launch_shape(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, const Shape& s, void* scratch,
                          cudaStream_t stream) {
-  if (s.nr == 1) return launch<D, MX, 1, 1>(a, k, v, s, scratch, stream);
-  if (s.wm == 1) return launch<D, MX, 2, 1>(a, k, v, s, scratch, stream);
-  if (s.wm == 2) return launch<D, MX, 2, 2>(a, k, v, s, scratch, stream);
-  return launch<D, MX, 2, 4>(a, k, v, s, scratch, stream);
+  if constexpr (!MX) {
+    if (s.nr == 2 || s.wm == 2) return launch<D, MX, D == 64 ? 2 : 1, D == 64 ? 1 : 2>(a, k, v, s, scratch, stream);
+  }
+  return launch<D, MX, 1, 1>(a, k, v, s, scratch, stream);
 }
 
 }  // namespace

@@ -398,7 +398,7 @@ def test_expired_wait_reports_timeout_and_context_survives():
     from jagged_attention_recsys_gdpa_gb300 import _binding as B
 
     clear(J)
-    for Hq, fmt in ((2, "bf16"), (24, "mxfp8"), (64, "bf16")):  # one, two and four warps a worker
+    for Hq, fmt in ((2, "bf16"), (24, "mxfp8"), (64, "bf16")):  # one warp a worker, three tiles a head, two warps a worker
         cache, table, _ = fill_cache(J, [400, 70, 3], 16, 1, 128, fmt, seed=48)
         q = torch.randn(3, Hq, 128, device="cuda").to(torch.bfloat16)
         args = (q, cache, cu(table), cu(np.array([400, 70, 3])))
