@@ -403,7 +403,7 @@ __device__ __forceinline__ float query_value(uint32_t pair, int i) {
 // for rows whose mask excludes it. Accumulators that are not finite (`bad`, one
 // bit each) are summed again one key at a time, over the allowed keys alone, with
 // weights w 2^(s - m) or w act(s).
-template <int D, bool MX>
+template <int D, bool MX, bool SOFT>
 __device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int n_steps, int step,
                                        const uint32_t (&q)[D / 16][2], const float (&f)[2], float (&o)[D / 16][4],
                                        const float (&m)[2], const float (&w)[2], const int (&lo)[2],
@@ -447,7 +447,7 @@ __device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float s = __shfl_sync(0xffffffffu, dot, (2 * c + i) * 4) * f[i];
-      p[i] = a.act == JATTN_SOFTMAX ? ex2_approx(s - (m[i] == -INFINITY ? 0.0f : m[i])) * w[i] : activate(s, a.act);
+      p[i] = SOFT ? ex2_approx(s - (m[i] == -INFINITY ? 0.0f : m[i])) * w[i] : activate(s, a.act);
       in[i] = pos >= lo[i] && pos < hi[i];
     }
 #pragma unroll
@@ -662,7 +662,7 @@ __device__ __forceinline__ void clear_rows(uint32_t vs, int pos0, int lo, int hi
   __syncwarp();
 }
 
-template <int D, bool MX, int NR, int WM>
+template <int D, bool MX, int NR, int WM, bool SOFT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     decode_kernel(DecodeArgs a, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   void* scratch) {
@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     int all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;  // that every row, and that any row, of the warp's may see
     int ref = -1;               // MXFP8: V's reference exponent, none yet
     bool new_ref = true;        // the unit may still choose its own: nothing is accumulated
-    bool live = false;          // the warp's rows hold one of the tile's at least
+    bool live = WM == 1;        // the warp's rows hold one of the tile's at least
     int row_base = 0, rows = 0;
     bool fresh = true;
     int n_steps = 0;            // of the unit at `at`, in this run, so far
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         new_ref = true;
         rows = at.s.lq * a.G;
         row_base = at.tile * tile + warp_m * (8 * NR);
-        live = row_base < rows;
+        if constexpr (WM > 1) live = row_base < rows;
         if (live) {
           const int delta = at.s.n - at.s.lq;
           const int end = rows - 1;  // rows behind it take its interval, and zeros for their query
@@ -766,11 +766,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                        any_hi);
 #pragma unroll
           for (int g = 0; g < NR; ++g) {
-            const float base = a.act == JATTN_SOFTMAX ? a.scale_log2 : a.scale;
+            const float base = SOFT ? a.scale_log2 : a.scale;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               key_interval(query_of(a, min(row_base + 8 * g + 2 * c + i, end)), delta, at.s.n, a.mask, a.window, lo[g][i], hi[g][i]);
-              m[g][i] = !MX || a.act == JATTN_SOFTMAX ? -INFINITY : kLeast;
+              m[g][i] = !MX || SOFT ? -INFINITY : kLeast;
               l[g][i] = 0.0f;
               f[g][i] = base;
               up[g][i] = pow2(kLift - static_cast<int>(kLeast));
@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[mt][g][e] *= f[g][e & 1];
           }
-          if (a.act == JATTN_SOFTMAX) {
+          if constexpr (SOFT) {
             if (rare(partial)) mask_keys<MX>(s, g, pos0 + key_of<MX>(lane >> 2, 0), lo[g], hi[g], -INFINITY);
             float t[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -916,13 +916,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
               for (int i = 0; i < 2; ++i) t[i] = fmax3(t[i], s[mt][g][i], s[mt][g][2 + i]);
             }
-            t[0] = rows_max(t[0]);
-            t[1] = rows_max(t[1]);
+            // a lane's own keys decide: the maximum over the row is needed only where it moves
             if (rare(__any_sync(0xffffffffu, t[0] > m[g][0] + kSlack || t[1] > m[g][1] + kSlack))) {
               float x[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const float n = fmaxf(m[g][i], t[i]);
+                const float n = fmaxf(m[g][i], rows_max(t[i]));
                 x[i] = m[g][i] == n ? 1.0f : ex2_approx(m[g][i] - n);
                 m[g][i] = n;
                 l[g][i] *= x[i];
@@ -967,10 +966,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) t[i] = fmax3(t[i], fabsf(s[mt][g][i]), fabsf(s[mt][g][2 + i]));
               }
-              t[0] = exponent_of(rows_max(t[0]));
-              t[1] = exponent_of(rows_max(t[1]));
+              t[0] = exponent_of(t[0]);
+              t[1] = exponent_of(t[1]);
               if (rare(__any_sync(0xffffffffu, t[0] > m[g][0] + kSlack - 1 || t[1] > m[g][1] + kSlack - 1))) {
-                const float n0 = fmaxf(m[g][0], t[0]), n1 = fmaxf(m[g][1], t[1]);
+                const float n0 = fmaxf(m[g][0], rows_max(t[0])), n1 = fmaxf(m[g][1], rows_max(t[1]));
                 scale_rows(o[g], pow2(static_cast<int>(m[g][0] - n0)), pow2(static_cast<int>(m[g][1] - n1)));
                 m[g][0] = n0;
                 m[g][1] = n1;
@@ -1188,15 +1187,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               l[g][i] = rows_sum(l[g][i]);
-              w[i] = a.act == JATTN_SOFTMAX ? inverse_sum(l[g][i]) : MX ? pow2(static_cast<int>(m[g][i]) - kLift) : 1.0f;
-              if (MX && a.act == JATTN_SOFTMAX) m[g][i] -= kLift;
+              w[i] = SOFT ? inverse_sum(l[g][i]) : MX ? pow2(static_cast<int>(m[g][i]) - kLift) : 1.0f;
+              if (MX && SOFT) m[g][i] -= kLift;
             }
             scale_rows(o[g], w[0], w[1]);
             if (MX && !new_ref) scale_rows(o[g], pow2(ref - 127), pow2(ref - 127));
-            repair<D, MX>(a, at, n_steps, step, q[g], f[g], o[g], m[g], w, lo[g], hi[g]);
+            repair<D, MX, SOFT>(a, at, n_steps, step, q[g], f[g], o[g], m[g], w, lo[g], hi[g]);
             const int r0 = row_base + 8 * g;
             if (unit_ends && begun) {  // all of it was in this run
-              if (a.act == JATTN_SOFTMAX && lane < 4) {
+              if (SOFT && lane < 4) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                   if (r0 + 2 * c + i < rows) a.lse[query_row(a, at.s.q0, r0 + 2 * c + i, at.h)] = lse_of(m[g][i], l[g][i]);
@@ -1420,8 +1419,8 @@ Shape shape_of(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G
   return s;
 }
 
-template <int D, bool MX, int NR, int WM>
-cudaError_t launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, const Shape& s, void* scratch,
+template <int D, bool MX, int NR, int WM, bool SOFT>
+cudaError_t launch_act(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, const Shape& s, void* scratch,
                    cudaStream_t stream) {
   constexpr int smem = smem_bytes<D, MX>();
   cudaError_t e;
@@ -1429,7 +1428,7 @@ cudaError_t launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap&
   int dev = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if (!(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(decode_kernel<D, MX, NR, WM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    e = cudaFuncSetAttribute(decode_kernel<D, MX, NR, WM, SOFT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     ready.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
@@ -1443,11 +1442,18 @@ cudaError_t launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap&
   c.stream = stream;
   c.attrs = &early;
   c.numAttrs = 1;
-  if ((e = cudaLaunchKernelEx(&c, decode_kernel<D, MX, NR, WM>, a, k, v, scratch)) != cudaSuccess) return e;
+  if ((e = cudaLaunchKernelEx(&c, decode_kernel<D, MX, NR, WM, SOFT>, a, k, v, scratch)) != cudaSuccess) return e;
   c.gridDim = dim3(s.ctas, kJoinCtas);
   c.blockDim = dim3(kJoinThreads);
   c.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&c, join_kernel<D>, a, scratch, kWarps / WM, s.tile);
+}
+
+template <int D, bool MX, int NR, int WM>
+cudaError_t launch(const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, const Shape& s, void* scratch,
+                   cudaStream_t stream) {
+  return a.act == JATTN_SOFTMAX ? launch_act<D, MX, NR, WM, true>(a, k, v, s, scratch, stream)
+                                : launch_act<D, MX, NR, WM, false>(a, k, v, s, scratch, stream);
 }
 
 template <int D, bool MX>
