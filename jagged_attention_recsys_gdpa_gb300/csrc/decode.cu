@@ -26,10 +26,12 @@
 // depend on what runs when.
 //
 // Measured: 64 histories of 50 to 32,000 keys, 8 heads of 128, bf16 (1.78 GB)
-// 264 us, 6.75 TB/s, the rate of a plain copy; 128 of them in MXFP8 (1.49 GB)
-// 246 us, 6.05 TB/s, where the conversions' latency binds (the copies alone take
-// 231); 32 query heads on 8, 1,000 to 8,000 keys (615 MB) 100 us; one history of
-// 130,001 keys (67 MB) 19 us; a call that moves next to nothing 9.8 us.
+// 260 us, 6.85 TB/s, the rate of a plain copy; 128 of them in MXFP8 (1.49 GB)
+// 236 us, 6.3 TB/s (the copies alone take 231); 32 query heads on 8, 1,000 to
+// 8,000 keys (615 MB) 98 us; one history of 130,001 keys (67 MB) 18.5 us; a call
+// that moves next to nothing 9.5 us. Softmax and the pointwise activations have
+// kernels of their own: with both in one, the code is too long for the
+// instruction cache (MXFP8 246 us against 242).
 #include <atomic>
 #include <cstdint>
 
