@@ -3,16 +3,17 @@
 //
 // Both are copies, bound by memory. A CTA takes a few consecutive jagged rows:
 // a thread per row finds its sequence and its place in the cache while the other
-// loads are on their way, then every thread moves kUnits units (K and V of each),
+// loads are on their way, then every thread moves a few units (K and V of each),
 // so that enough loads are in flight. Consecutive threads hold consecutive units,
 // so jagged rows move in whole lines and page rows in runs of a head's row. A unit
 // is 16 bytes of bf16 or, of an MXFP8 cache, 16 values: 32 bytes of bf16 in one
 // access and 16 bytes of codes. (Of 8 values the instructions, not memory, were
 // the bound; of the 32 of a block the accesses lay too far apart.)
 //
-// Measured: 213 k rows of 4 heads of 128, keys rotated, bf16 (981 MB) 137 us,
-// 7.1 TB/s; 131 k rows of 8 heads to MXFP8 (822 MB) 150 us, 5.5 TB/s; 213 k rows
-// of 8 heads back from MXFP8 (1.32 GB) 210 us, 6.3 TB/s.
+// Measured: 213 k rows of 4 heads of 128, keys rotated, bf16 (981 MB) 138 us,
+// 7.1 TB/s; 131 k rows of 8 heads to MXFP8 (822 MB) 128 us, 6.4 TB/s; 213 k rows
+// of 8 heads back from MXFP8 (1.32 GB) 204 us, 6.5 TB/s.
+#include <algorithm>
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -24,7 +25,13 @@ namespace jattn {
 namespace {
 
 constexpr int kCacheBlock = 256;
-constexpr int kMaxRows = 64;  // rows of a CTA
+// Rows of a CTA, one looked up by a thread: what the narrowest rows (one head of 64
+// columns) need to fill its threads.
+constexpr int max_rows(bool mx) { return mx ? 256 : 128; }
+// CTAs per SM that the MXFP8 kernels' registers leave room for, of three, four and
+// five: append of 131 k rows 131 / 127 / 142 us, read of 213 k 216 / 203 / 226. The bf16
+// kernels come to four by themselves.
+constexpr int kCacheCtas = 4;
 
 // The sequence of jagged row r and its index in it: false (nothing to do) for
 // rows behind the last sequence.
@@ -193,9 +200,9 @@ struct AppendArgs {
 };
 
 template <bool MX, int N>
-__global__ void __launch_bounds__(kCacheBlock) append_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kCacheBlock, MX ? kCacheCtas : 0) append_kernel(AppendArgs a) {
   constexpr int P = MX ? 2 : 1;  // 16-byte pieces of a unit
-  __shared__ Row row[kMaxRows];
+  __shared__ Row row[max_rows(MX)];
   const int per_head = a.D / (8 * P), per_row = a.c.H * per_head;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows;
   const int rows = static_cast<int>(min(static_cast<int64_t>(a.rows), a.total - row0)), units = rows * per_row;
@@ -297,9 +304,9 @@ struct ReadArgs {
 };
 
 template <bool MX, int N>
-__global__ void __launch_bounds__(kCacheBlock) read_kernel(ReadArgs a) {
+__global__ void __launch_bounds__(kCacheBlock, MX ? kCacheCtas : 0) read_kernel(ReadArgs a) {
   constexpr int P = MX ? 2 : 1;  // 16-byte pieces that a unit becomes
-  __shared__ Row row[kMaxRows];
+  __shared__ Row row[max_rows(MX)];
   const int per_head = a.D / (8 * P), per_row = a.c.H * per_head;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * a.rows;
   const int rows = static_cast<int>(min(static_cast<int64_t>(a.rows), a.total - row0)), units = rows * per_row;
@@ -348,16 +355,22 @@ __global__ void __launch_bounds__(kCacheBlock) read_kernel(ReadArgs a) {
   }
 }
 
-// Rows of a CTA and its number of CTAs, for `units` units per thread.
-int rows_of(int per_row, int units) {
-  const int r = kCacheBlock * units / per_row;
-  return r < 1 ? 1 : r > kMaxRows ? kMaxRows : r;
+// Rows of a CTA and its number of CTAs, for `units` units per thread. With MXFP8 a
+// CTA takes twice the rows that its threads hold at a time where that leaves at
+// least `waves` times as many CTAs as fit the SMs: a row's lookup (a chain of loads) is then
+// waited for half as often. 131 k rows appended 127 us against 147 (30 k rows 33 against 37,
+// 15 k 16.7 against 18.6); 213 k rows read 204 us against 211, but 60 k 65.9 against
+// 64.7. bf16 rows gain nothing (append 138.9 against 137.9 us).
+int rows_of(int64_t total, int per_row, int units, bool mx, int waves) {
+  const int batches = mx && total * per_row >= int64_t(152) * kCacheCtas * kCacheBlock * units * 2 * waves ? 2 : 1;
+  const int r = kCacheBlock * units * batches / per_row;
+  return r < 1 ? 1 : std::min(r, max_rows(mx));
 }
 unsigned ctas_of(int64_t total, int rows) { return static_cast<unsigned>((total + rows - 1) / rows); }
 
-// One unit per thread up to eight CTAs an SM (read_one_user 3.5 us against 4.0
-// with four), then four; two when quantising, which needs the registers
-// (append_chunks_mxfp8 150 us against 156 with four and 170 with one).
+// One unit per thread up to eight CTAs an SM (1,001 bf16 rows read 3.5 us against
+// 4.0 with four), then four; two when quantising, which needs the registers
+// (131 k rows 150 us against 156 with four and 170 with one).
 bool few_rows(int64_t total, int per_row) { return total * per_row <= int64_t(152) * 8 * kCacheBlock; }
 // Launched to be set up while the kernel before it ends (it waits for that first).
 template <typename Args>
@@ -385,7 +398,7 @@ cudaError_t launch_cache_append(const CacheView& c, bool mx, int64_t B, int64_t 
   const int per_row = c.H * (D / (mx ? 16 : 8));
   const int units = few_rows(total, per_row) ? 1 : mx ? 2 : 4;
   const AppendArgs a{c,     off, start, static_cast<const uint4*>(k), static_cast<const uint4*>(v), cos_t, sin_t, B, total,
-                     D, rope_rows, rows_of(per_row, units), wide(k, v), status};
+                     D, rope_rows, rows_of(total, per_row, units, mx, 1), wide(k, v), status};
   const auto kernel = mx ? (units == 1 ? append_kernel<true, 1> : append_kernel<true, 2>)
                          : (units == 1 ? append_kernel<false, 1> : append_kernel<false, 4>);
   return launch(kernel, a, total, stream);
@@ -396,7 +409,7 @@ cudaError_t launch_cache_read(const CacheView& c, bool mx, int64_t B, int64_t to
                               cudaStream_t stream) {
   const int per_row = c.H * (D / (mx ? 16 : 8));
   const int units = few_rows(total, per_row) ? 1 : 4;
-  const ReadArgs a{c, off, start, static_cast<uint4*>(k), static_cast<uint4*>(v), B, total, D, rows_of(per_row, units),
+  const ReadArgs a{c, off, start, static_cast<uint4*>(k), static_cast<uint4*>(v), B, total, D, rows_of(total, per_row, units, mx, 4),
                    wide(k, v), status};
   const auto kernel = mx ? (units == 1 ? read_kernel<true, 1> : read_kernel<true, 4>)
                          : (units == 1 ? read_kernel<false, 1> : read_kernel<false, 4>);

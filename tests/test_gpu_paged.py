@@ -540,6 +540,48 @@ def test_decode_mxfp8_largest_exponent():
     assert np.all(np.abs(np64(o) - ro) <= to)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("H,D,total", [(1, 64, 1_300_007), (8, 128, 83_001)])
+def test_large_calls_do_what_small_ones_do(H, D, total, fmt):
+    """Calls large enough for several rows and batches a thread against calls of one unit a thread (which the tests above
+    hold to the definitions), bit for bit."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    B, page = 37, 64
+    g = torch.Generator().manual_seed(61)
+    lens = torch.rand(B, generator=g) + 0.05
+    lens = (lens / lens.sum() * total).long()
+    lens[5] = 0
+    lens[-1] += total - lens.sum()
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)])
+    need = (lens + page - 1) // page
+    table = torch.zeros(B, int(need.max()), dtype=torch.int32)
+    pages = torch.randperm(int(need.sum()), generator=g).int()
+    at = 0
+    for b in range(B):
+        table[b, :need[b]] = pages[at:at + int(need[b])]
+        at += int(need[b])
+    k, v = (torch.randn(total, H, D, device="cuda").to(torch.bfloat16) for _ in range(2))
+    rope = tuple(torch.randn(int(lens.max()), D // 2, device="cuda") for _ in range(2))
+    many, one = (J.paged_cache(len(pages), page, H, D, fmt) for _ in range(2))
+    zero = torch.zeros(B, dtype=torch.int64, device="cuda")
+    J.cache_append(one, k, v, table.cuda(), zero, off=off.cuda(), rope=rope)
+    ko, vo = J.cache_read(one, table.cuda(), off.cuda())
+    piece = 300_000 // (H * D // 8)  # rows: fewer than 311,296 units of 8 (or 16) values
+    for b in range(B):
+        for first in range(0, int(lens[b]), piece):
+            n = min(piece, int(lens[b]) - first)
+            rows = slice(int(off[b]) + first, int(off[b]) + first + n)
+            start, o = torch.tensor([first], device="cuda"), torch.tensor([0, n], device="cuda")
+            J.cache_append(many, k[rows], v[rows], table[b:b + 1].cuda(), start, off=o, rope=rope)
+            kr, vr = J.cache_read(many, table[b:b + 1].cuda(), o, start=start)
+            assert torch.equal(kr, ko[rows]) and torch.equal(vr, vo[rows])
+    assert J.device_status() == 0
+    for x, y in ((one.k, many.k), (one.v, many.v), (one.k_scales, many.k_scales), (one.v_scales, many.v_scales)):
+        assert x is None and y is None or torch.equal(x, y)
+
+
 def test_append_refuses_rows_that_need_a_gradient():
     import jagged_attention_recsys_gdpa_gb300 as J
 
