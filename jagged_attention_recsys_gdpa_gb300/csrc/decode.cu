@@ -410,10 +410,13 @@ __device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int
                                        const uint32_t (&q)[D / 16][2], const float (&f)[2], float (&o)[D / 16][4],
                                        const float (&m)[2], const float (&w)[2], const int (&lo)[2],
                                        const int (&hi)[2]) {
-  float x = 0.0f;  // stays 0 unless something is not finite
+  float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // stay 0 unless something is not finite
 #pragma unroll
-  for (int j = 0; j < D / 16; ++j) x += (o[j][0] - o[j][0]) + (o[j][1] - o[j][1]) + (o[j][2] - o[j][2]) + (o[j][3] - o[j][3]);
-  if (!rare(__any_sync(0xffffffffu, x != 0.0f))) return;
+  for (int j = 0; j < D / 16; ++j) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = fmaf(o[j][e], 0.0f, x[e]);
+  }
+  if (!rare(__any_sync(0xffffffffu, (x[0] + x[1]) + (x[2] + x[3]) != 0.0f))) return;
   const int lane = threadIdx.x & 31, c = lane & 3;
   uint32_t bad = 0;
 #pragma unroll
@@ -928,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 m[g][i] = n;
                 l[g][i] *= x[i];
               }
-              scale_rows(o[g], x[0], x[1]);
+              if (!MX || !new_ref) scale_rows(o[g], x[0], x[1]);  // nothing is accumulated before
             }
             const float lift = MX ? kLift : 0.0f;
             const float use[2] = {m[g][0] == -INFINITY ? 0.0f : m[g][0] - lift, m[g][1] == -INFINITY ? 0.0f : m[g][1] - lift};
@@ -972,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               t[1] = exponent_of(t[1]);
               if (rare(__any_sync(0xffffffffu, t[0] > m[g][0] + kSlack - 1 || t[1] > m[g][1] + kSlack - 1))) {
                 const float n0 = fmaxf(m[g][0], rows_max(t[0])), n1 = fmaxf(m[g][1], rows_max(t[1]));
-                scale_rows(o[g], pow2(static_cast<int>(m[g][0] - n0)), pow2(static_cast<int>(m[g][1] - n1)));
+                if (!new_ref) scale_rows(o[g], pow2(static_cast<int>(m[g][0] - n0)), pow2(static_cast<int>(m[g][1] - n1)));
                 m[g][0] = n0;
                 m[g][1] = n1;
                 up[g][0] = pow2(kLift - static_cast<int>(n0));
@@ -1180,7 +1183,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           }
         }
         if (live) {
-          const float norm = row_norm(a, at.s.n);
+          const float norm = SOFT ? 1.0f : row_norm(a, at.s.n);
 #pragma unroll
           for (int g = 0; g < NR; ++g) {
             // softmax rows are divided by their sum l here, in the pieces too (values near fp32's end would not
