@@ -364,6 +364,20 @@ def test_decode_many_sequences(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_many_tiles(D, fmt):
+    """Several tiles of rows per key/value head: of many sequences with few rows each, and of a long history whose
+    tiles are each split over workers and joined."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    rng = np.random.default_rng(71)
+    lens = rng.integers(0, 30, 200).tolist()
+    check_decode(J, lens, rng.integers(0, 9, 200).tolist(), 6, 2, D, 16, fmt, seed=72, causal=True, extra_rows=1)
+    check_decode(J, [2500, 0, 90], [25, 3, 1], 6, 3, D, 64, fmt, seed=73, causal=True, window=2000)
+    check_decode(J, [1300, 700], [50, 3], 2, 2, D, 8, fmt, seed=74, act="silu", norm=True)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
 def test_decode_empty_calls(fmt):
     """No query rows at all; a bound of no cached rows; sequences that share their pages."""
     import jagged_attention_recsys_gdpa_gb300 as J
