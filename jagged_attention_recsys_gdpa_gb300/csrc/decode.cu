@@ -1049,9 +1049,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             look = look || every != 0x08080808u || ref < 0;
           }
           if (rare(__any_sync(0xffffffffu, look))) {
-            int top = 14;  // the largest exponent but NaN's (R - 14 is no negative byte)
+            // The unit's largest exponent but NaN's (R - 14 is no negative byte), of its own keys alone: those outside
+            // hold the reference, which may be that of the unit before and would carry it on.
+            int top = 14;
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i) {
+              const int pos = pos0 + (i >> 1) * 16 + key_of<true>(lane >> 2, i & 1);
+              if (partial && (pos < at.s.lo || pos >= at.s.hi)) continue;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const int x = static_cast<int>((e[i >> 1][i & 1] >> (8 * j)) & 0xffu);

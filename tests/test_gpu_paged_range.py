@@ -1,0 +1,91 @@
+"""Decode from MXFP8 caches whose V exponents lie far apart, between the units
+that one worker takes one after another and within one unit, and NaN blocks and
+codes, against the plain 64-bit reference in paged_ref."""
+import numpy as np
+import pytest
+import torch
+
+from tests import paged_ref as R
+from tests.test_gpu_paged import clear, cu, fill_cache, np64, prefix, weight_parts
+
+pytestmark = pytest.mark.gpu
+
+
+def pages_of(cache):
+    """The float64 pages as they are now (NaN places become zeros: they lie in no sequence)."""
+    return [np.nan_to_num(R.dequantise(c.cpu().numpy(), e.cpu().numpy()))
+            for c, e in ((cache.k, cache.k_scales), (cache.v, cache.v_scales))]
+
+
+def shift_values(cache, by):
+    """V exponents moved by `by` (broadcast); the NaN places stay."""
+    e = cache.v_scales
+    e.copy_(torch.where(e == 255, e, (e.int() + by).clamp(0, 254).to(torch.uint8)))
+
+
+def rows_of(table, lens, page):
+    """(sequence, position, page, place in it) of every cached row."""
+    for b, n in enumerate(lens):
+        for p in range(int(n)):
+            yield b, p, int(table[b, p // page]), p % page
+
+
+def check_repeated(J, cache, table, lens, lq, Hq, rep, spread=4, seed=7, act="softmax", **mask):
+    """The sequences `rep` times over in one call, all copies reading the same pages: every copy within the bounds of
+    the 64-bit values."""
+    D = cache.D
+    q_off = prefix(lq)
+    n = int(q_off[-1])
+    q = torch.randn(n, Hq, D, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16)
+    kp, vp = pages_of(cache)
+    ro, rl, to, tl = R.decode(np64(q), kp, vp, table, lens, q_off, act=act, **weight_parts("mxfp8", spread), **mask)
+    many = torch.from_numpy(np.concatenate([q_off[:-1] + i * n for i in range(rep)] + [[rep * n]])).cuda()
+    o, lse = J.decode(q.cuda().repeat(rep, 1, 1), cache, cu(np.tile(table, (rep, 1))),
+                      cu(np.tile(np.asarray(lens, np.int64), rep)), q_off=many, act=act, **mask)
+    assert J.device_status() == 0
+    ro, to = cu(ro), cu(to)
+    for i in range(0, rep, 32):
+        got = o[i * n:(i + 32) * n].view(-1, n, Hq, D).double()
+        worst = ((got - ro).abs() - to).amax(dim=(2, 3))
+        assert not bool(torch.isnan(got).any()) and float(worst.max()) <= 0, \
+            f"copies {i}..: o off by {float(worst.max())} more than its bound, first at {(worst > 0).nonzero()[:4].tolist()}"
+    if act == "softmax":
+        off = (lse.view(rep, n, Hq).double() - cu(rl)).abs() - cu(tl)
+        assert float(off.max()) <= 0
+
+
+@pytest.mark.parametrize("D,rep,act", [(64, 1024, "softmax"), (64, 1024, "silu"), (128, 768, "softmax")])
+def test_units_with_zero_blocks_leave_the_ones_behind_them_alone(D, rep, act):
+    """Thousands of histories shorter than one product block, 64 query rows a head, so that a worker takes hundreds of
+    units; some V rows are zeros (exponent 0), and the heads' values lie 2^8 apart."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    lens, page, H = [20, 1, 31, 7, 20, 24, 13, 25], 32, 8
+    cache, table, _ = fill_cache(J, lens, page, H, D, "mxfp8", seed=201)
+    shift_values(cache, (8 * (torch.arange(H, device="cuda") % 3)).view(1, H, 1, 1))
+    for b, p, pg, at in rows_of(table, lens, page):
+        if b % 4 == 0 and p % 5 == 2:
+            cache.v[pg, :, at], cache.v_scales[pg, :, at] = 0, 0
+    check_repeated(J, cache, table, lens, [1] * len(lens), 64 * H, rep, act=act)
+
+
+@pytest.mark.parametrize("mask", [{}, dict(causal=True, window=20), dict(causal=True, block=24)],
+                         ids=["none", "window", "block"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("act", ["softmax", "gelu"])
+def test_a_neighbours_large_values_stay_its_own(act, D, mask):
+    """Every other history's values are 2^130 times larger: the ones between them, short or behind a window that begins
+    inside a product block, alone and in a batch of several units a worker."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    lens, page, H = [25, 21, 12, 30] if not mask else [75, 130, 90, 61], 16, 2
+    cache, table, _ = fill_cache(J, lens, page, H, D, "mxfp8", seed=211)
+    for b, p, pg, at in rows_of(table, lens, page):
+        e = cache.v_scales[pg, :, at]
+        cache.v_scales[pg, :, at] = (e.int() + (70 if b % 2 == 0 else -60)).to(torch.uint8)
+    lq = [1, 2, 1, 3]
+    check_repeated(J, cache, table, lens, lq, 4 * H, 1000, act=act, **mask)
+    for b in (1, 3):
+        check_repeated(J, cache, table[b:b + 1], lens[b:b + 1], lq[b:b + 1], 4 * H, 1, act=act, **mask)
