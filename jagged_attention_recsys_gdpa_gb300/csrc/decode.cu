@@ -578,18 +578,24 @@ struct Left {
 };
 
 // ---------------------------------------------------------------- kernel
-// Bounded wait; false (and the status set) when it runs out.
-__device__ __forceinline__ bool wait_full(const DecodeArgs& a, uint64_t* bar, uint32_t parity) {
-  if (!rare(!mbar_try_wait(bar, parity))) return true;
+// Bounded wait of a whole warp; false (and the status set) when it runs out. Each lane tests the barrier and reads the
+// clock by itself, so they vote: a warp goes on or leaves as one, whatever the moment at which a copy lands.
+__device__ __forceinline__ bool wait_full(const DecodeArgs& a, uint64_t* bar, uint32_t parity, uint64_t limit_ns) {
+  bool done = mbar_try_wait(bar, parity);
+  if (!rare(!__all_sync(0xffffffffu, done))) return true;
   const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > a.timeout_ns) {
+  for (;;) {
+    done = done || mbar_try_wait(bar, parity);
+    if (__all_sync(0xffffffffu, done)) return true;
+    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit_ns)) {
       record_error(a.status, JATTN_ERR_TIMEOUT, 86, blockIdx.x);
       return false;
     }
   }
-  return true;
 }
+// A warp that leaves waits for its copies in flight at least this long, however short the limit of its waits: copies
+// that landed later would write into the shared memory of whatever runs there next.
+constexpr uint64_t kDrainNs = 20000000;
 
 // A step's rows are copied as boxes of min(page size, step) rows: one, or several
 // whose table entries the lanes look up and one lane issues in turn (a lane each
@@ -796,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           }
         }
       }
-      if (rare(!wait_full(a, full + stage_no, phase))) {
+      if (rare(!wait_full(a, full + stage_no, phase, a.timeout_ns))) {
         ok = false;
         break;
       }
@@ -806,7 +812,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         if constexpr (WM == 1) {
           __syncwarp();
         } else {
-          if (loaded >= kStages && !wait_full(a, empty + s, static_cast<uint32_t>(loaded / kStages - 1) & 1u)) {
+          if (loaded >= kStages &&
+              !wait_full(a, empty + s, static_cast<uint32_t>(loaded / kStages - 1) & 1u, a.timeout_ns)) {
             ok = false;
             break;
           }
@@ -1180,7 +1187,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           if (run_ends) {
             __syncwarp();
             if (lane == 0) mbar_arrive(met);
-            if (!wait_full(a, met, 0)) {
+            if (!wait_full(a, met, 0, a.timeout_ns)) {
               ok = false;
               break;
             }
@@ -1263,7 +1270,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       // a wait ran out: nothing to join here, and no copy may be in flight when the CTA ends
       if (tid == 0) left[in_cta] = Left{};
       if (warp_m == 0) {
-        for (int i = done; i < loaded; ++i) (void)wait_full(a, full + i % kStages, static_cast<uint32_t>(i / kStages) & 1u);
+        const uint64_t limit = a.timeout_ns > kDrainNs ? a.timeout_ns : kDrainNs;
+        for (int i = done; i < loaded; ++i) (void)wait_full(a, full + i % kStages, static_cast<uint32_t>(i / kStages) & 1u, limit);
       }
     }
   }
