@@ -1070,7 +1070,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               }
             }
             top = __reduce_max_sync(0xffffffffu, top);
-            const int next = min(top + 1, 254);  // 2^(R - 127) has to be an fp32 number
+            // 2^(R - 127) is an fp32 number, and exponent 255 (NaN) lies outside the factors' range: at most 253
+            const int next = min(top + 1, 253);
             if (new_ref || top > ref + 1) {
               if (!new_ref) {
 #pragma unroll

@@ -89,3 +89,34 @@ def test_a_neighbours_large_values_stay_its_own(act, D, mask):
     check_repeated(J, cache, table, lens, lq, 4 * H, 1000, act=act, **mask)
     for b in (1, 3):
         check_repeated(J, cache, table[b:b + 1], lens[b:b + 1], lq[b:b + 1], 4 * H, 1, act=act, **mask)
+
+
+@pytest.mark.parametrize("top", [120, 240, 252, 253, 254])
+def test_a_nan_block_is_nan_beside_the_largest_exponents(top):
+    """A block of exponent 255 (with codes of zero, as append writes it) among blocks up to the largest exponent: its 32
+    columns are NaN for the rows that see it, everything else is as it has to be."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    lens, page, H, D = [90, 40], 32, 2, 128
+    cache, table, _ = fill_cache(J, lens, page, H, D, "mxfp8", seed=221)
+    g = torch.Generator().manual_seed(222)
+    sign = torch.randint(0, 2, cache.v.shape, generator=g) * 128  # codes up to 7 * 2^-9: finite sums
+    cache.v.copy_((torch.randint(0, 8, cache.v.shape, generator=g) + sign).to(torch.uint8))
+    cache.v_scales.copy_((top - torch.randint(0, 4, cache.v_scales.shape, generator=g)).to(torch.uint8))
+    cache.v_scales[table[0, 1], 1, 5, 1] = top
+    kp, vp = pages_of(cache)
+    q = torch.randn(3, 2 * H, D, generator=g).to(torch.bfloat16)
+    q_off = np.array([0, 2, 3])
+    ro, rl, to, tl = R.decode(np64(q), kp, vp, table, lens, q_off, causal=True, **weight_parts("mxfp8", 4))
+    bad = (int(table[0, 89 // page]), 1, 89 % page, 2)  # the last key: the second row of the sequence alone sees it
+    cache.v_scales[bad] = 255
+    cache.v[bad[0], 1, bad[2], 64:96] = 0
+    o, lse = J.decode(q.cuda(), cache, cu(table), cu(np.array(lens)), q_off=cu(q_off), causal=True)
+    assert J.device_status() == 0
+    got = np64(o)
+    assert np.all(np.isnan(got[1, 2:, 64:96]))
+    keep = np.ones(got.shape, bool)
+    keep[1, 2:, 64:96] = False
+    assert np.all(np.abs(got - ro)[keep] <= to[keep])
+    assert np.all(np.abs(np64(lse) - rl) <= tl)
