@@ -268,16 +268,27 @@ __device__ __forceinline__ uint32_t piece_at(int r, int chunk) {
 //    one for each block of columns, R a reference exponent of the unit (the
 //    accumulators are in units of 2^(R - 127)). From 2^-14 to 2^1 the factors are
 //    fp16 numbers; a larger exponent moves R and rescales the accumulators, and
-//    16 keys with a block below 2^-14 (or of NaN) take bf16 products instead;
+//    16 keys with a block below 2^-14 (or of NaN) take bf16 products instead.
+//    All rows of a unit share R, also where their masks differ or a weight
+//    vanishes, so R may not leave behind what a row has: it lies at most kSpan
+//    above the unit's lowest exponent, and larger blocks take the bf16 products
+//    too (past fp32's end the accumulators come out infinite, and repair() sums again);
 //  * weights are kept at 2^kLift times their value against the row's reference
 //    (the running maximum; for pointwise activations the exponent of their
 //    largest one), so that what fp16 loses at its lower end is 2^-32 of the
 //    reference, 2^-18 under the smallest factor.
 // bf16 operands throughout cost three times the instructions per code.
 constexpr int kLift = 7;
+// A row whose blocks all lie kSpan below R keeps fp32 numbers: its largest weight is
+// 2^7 or more, the smallest code 2^-9, so it has 2^-102 or more, 2^24 times the least
+// normal number. Exponents of 0 do not count: their values are below 2^-118, mostly zeros.
+constexpr int kSpan = 100;
+// The lowest exponent of a unit so far, where it has none: nothing is accumulated, or
+// blocks of exponent 0 (or NaN) alone, so that its R (15) means nothing yet.
+constexpr int kNothing = 256, kOnlyZeros = 255;
 
-__device__ __forceinline__ float pow2(int e) {  // 2^e, 0 below fp32's normal range
-  return e < -126 ? 0.0f : __int_as_float((min(e, 127) + 127) << 23);
+__device__ __forceinline__ float pow2(int e) {  // 2^e, 0 below fp32's normal range, infinity above it
+  return e < -126 ? 0.0f : __int_as_float((min(e, 128) + 127) << 23);
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
@@ -752,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     int lo[NR][2], hi[NR][2];   // keys that they may see
     int all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;  // that every row, and that any row, of the warp's may see
     int ref = -1;               // MXFP8: V's reference exponent, none yet
-    bool new_ref = true;        // the unit may still choose its own: nothing is accumulated
+    int low = kNothing;         // MXFP8: the lowest exponent accumulated in this unit, or kNothing, kOnlyZeros
     bool live = WM == 1;        // the warp's rows hold one of the tile's at least
     int row_base = 0, rows = 0;
     bool fresh = true;
@@ -765,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       if (rare(fresh)) {  // its rows arrive while its first step does
         fresh = false;
         n_steps = 0;
-        new_ref = true;
+        low = kNothing;
         rows = at.s.lq * a.G;
         row_base = at.tile * tile + warp_m * (8 * NR);
         if constexpr (WM > 1) live = row_base < rows;
@@ -938,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                 m[g][i] = n;
                 l[g][i] *= x[i];
               }
-              if (!MX || !new_ref) scale_rows(o[g], x[0], x[1]);  // nothing is accumulated before
+              if (!MX || low != kNothing) scale_rows(o[g], x[0], x[1]);  // nothing is accumulated before
             }
             const float lift = MX ? kLift : 0.0f;
             const float use[2] = {m[g][0] == -INFINITY ? 0.0f : m[g][0] - lift, m[g][1] == -INFINITY ? 0.0f : m[g][1] - lift};
@@ -982,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               t[1] = exponent_of(t[1]);
               if (rare(__any_sync(0xffffffffu, t[0] > m[g][0] + kSlack - 1 || t[1] > m[g][1] + kSlack - 1))) {
                 const float n0 = fmaxf(m[g][0], rows_max(t[0])), n1 = fmaxf(m[g][1], rows_max(t[1]));
-                if (!new_ref) scale_rows(o[g], pow2(static_cast<int>(m[g][0] - n0)), pow2(static_cast<int>(m[g][1] - n1)));
+                if (low != kNothing) scale_rows(o[g], pow2(static_cast<int>(m[g][0] - n0)), pow2(static_cast<int>(m[g][1] - n1)));
                 m[g][0] = n0;
                 m[g][1] = n1;
                 up[g][0] = pow2(kLift - static_cast<int>(n0));
@@ -1048,17 +1059,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             all |= d[i >> 1][i & 1];
           }
           bool small = false, look = (all & 0xf0f0f0f0u) != 0;
-          if (rare(new_ref)) {
+          if (rare(low >= kOnlyZeros)) {
             // a new unit keeps the reference of the one before if all its first exponents lie within 2^7 below it
             uint32_t every = 0x08080808u;
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i) every &= d[i >> 1][i & 1];
-            look = look || every != 0x08080808u || ref < 0;
+            look = look || every != 0x08080808u || ref < 0 || low == kOnlyZeros;
           }
           if (rare(__any_sync(0xffffffffu, look))) {
             // The unit's largest exponent but NaN's (R - 14 is no negative byte), of its own keys alone: those outside
             // hold the reference, which may be that of the unit before and would carry it on.
-            int top = 14;
+            int top = 14, bottom = kOnlyZeros;
 #pragma unroll
             for (int i = 0; i < 2 * MT; ++i) {
               const int pos = pos0 + (i >> 1) * 16 + key_of<true>(lane >> 2, i & 1);
@@ -1066,14 +1077,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const int x = static_cast<int>((e[i >> 1][i & 1] >> (8 * j)) & 0xffu);
-                if (x != 255) top = max(top, x);
+                if (x == 255) continue;
+                top = max(top, x);
+                if (x != 0) bottom = min(bottom, x);
               }
             }
             top = __reduce_max_sync(0xffffffffu, top);
+            bottom = __reduce_min_sync(0xffffffffu, bottom);
+            const bool none = low == kNothing, any = low < kOnlyZeros;
             // 2^(R - 127) is an fp32 number, and exponent 255 (NaN) lies outside the factors' range: at most 253
-            const int next = min(top + 1, 253);
-            if (new_ref || top > ref + 1) {
-              if (!new_ref) {
+            int next = any && top <= ref + 1 ? ref : min(top + 1, 253);
+            low = min(any ? min(low, ref - 14) : kOnlyZeros, bottom);  // blocks that were not looked at: ref - 14 or more
+            next = min(next, low + kSpan);
+            if (next != ref) {
+              if (!none) {
 #pragma unroll
                 for (int g = 0; g < NR; ++g) scale_rows(o[g], pow2(ref - next), pow2(ref - next));
               }
@@ -1090,8 +1107,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               d[i >> 1][i & 1] = x - static_cast<uint32_t>(ref - 14) * 0x01010101u;
             }
             small = __any_sync(0xffffffffu, (out & 0xfffffff0u) != 0);
+          } else if (rare(low == kNothing)) {
+            low = ref - 6;
           }
-          new_ref = false;
           // rows (keys) of two 16-byte pieces for the transposing loads
           const int r = r_base + (lane & 15), half = lane >> 4;
           if (rare(small)) {  // bf16 products for these keys
@@ -1208,7 +1226,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               if (MX && SOFT) m[g][i] -= kLift;
             }
             scale_rows(o[g], w[0], w[1]);
-            if (MX && !new_ref) scale_rows(o[g], pow2(ref - 127), pow2(ref - 127));
+            if (MX && low != kNothing) scale_rows(o[g], pow2(ref - 127), pow2(ref - 127));
             repair<D, MX, SOFT>(a, at, n_steps, step, q[g], f[g], o[g], m[g], w, lo[g], hi[g]);
             const int r0 = row_base + 8 * g;
             if (unit_ends && begun) {  // all of it was in this run

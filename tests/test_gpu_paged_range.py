@@ -120,3 +120,79 @@ def test_a_nan_block_is_nan_beside_the_largest_exponents(top):
     keep[1, 2:, 64:96] = False
     assert np.all(np.abs(got - ro)[keep] <= to[keep])
     assert np.all(np.abs(np64(lse) - rl) <= tl)
+
+
+MASKS = {"causal": dict(causal=True), "window": dict(causal=True, window=60), "block": dict(block=49)}
+
+
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+@pytest.mark.parametrize("mask", sorted(MASKS))
+@pytest.mark.parametrize("D", [64, 128])
+def test_large_values_that_other_rows_see(D, mask, act):
+    """Finite values up to 2^150 times a row's own at positions that only other rows of its tile see, at the end (one more
+    for each row), at the start of a window and in another block: every row within the bound of the keys that it sees."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    lens, page, H, lq = [150, 40], 32, 2, [4, 3]
+    for places in ("ends", "early") if mask == "window" else ("ends",):
+        cache, table, _ = fill_cache(J, lens, page, H, D, "mxfp8", seed=231)
+        shift_values(cache, -30)
+        kw = MASKS[mask]
+        for b, n in enumerate(lens):
+            if places == "early":
+                where = [(max(n - lq[b] - 59, 0) + i, e) for i, e in enumerate((239, 200, 160)[:lq[b] - 1])]
+            elif mask == "block":
+                where = [(p, 239) for p in range((n - 1) // 49 * 49, n)] if (n - lq[b]) // 49 != (n - 1) // 49 else []
+            else:
+                where = [(n - 1 - i, e) for i, e in enumerate((239, 200, 160)[:lq[b] - 1])]
+            for p, e in where:
+                cache.v_scales[int(table[b, p // page]), :, p % page] = e
+        check_repeated(J, cache, table, lens, lq, 2 * H, 3, spread=14, act=act, **kw)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("at", [3, 60, 99])
+def test_large_values_whose_weight_vanishes(at, fmt):
+    """A key whose softmax weight is 2^-450 or less and whose values are 2^120 times the others' or more: it adds nothing, and
+    takes nothing away."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    lens, page, H, D = [100], 32, 2, 128
+    cache, table, _ = fill_cache(J, lens, page, H, D, fmt, seed=241)
+    pg, row = int(table[0, at // page]), at % page
+    q = (torch.rand(1, H, D, generator=torch.Generator().manual_seed(4)) + 1.0).to(torch.bfloat16)
+    if fmt == "mxfp8":  # keys of -448 / 2^4 against queries between 1 and 2: a score of -316 or less
+        cache.k[pg, :, row], cache.k_scales[pg, :, row] = 0xfe, 123
+        kp, vp = pages_of(cache)
+    else:
+        cache.k[pg, :, row] = -28.0
+        kp, vp = (np.nan_to_num(np64(x)) for x in (cache.k, cache.v))
+    vp[pg, :, row] = 0.0
+    ro, rl, to, tl = R.decode(np64(q), kp, vp, table, lens, np.array([0, 1]), **weight_parts(fmt, 14))
+    if fmt == "mxfp8":
+        cache.v_scales[pg, :, row] = 246
+    else:
+        cache.v[pg, :, row] *= 2.0**120
+    o, lse = J.decode(q.cuda(), cache, cu(table), cu(np.array(lens)))
+    assert J.device_status() == 0
+    assert np.all(np.abs(np64(o) - ro) <= to) and np.all(np.abs(np64(lse) - rl) <= tl)
+
+
+def test_exponents_that_begin_with_zeros():
+    """Units whose first blocks of keys are all of exponent 0, with and without codes, before values of every size."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    lens, page, H, D = [100, 70, 33], 32, 2, 64
+    for shift in (-90, -30, 0, 60):
+        for codes in (False, True):
+            cache, table, _ = fill_cache(J, lens, page, H, D, "mxfp8", seed=251)
+            shift_values(cache, shift)
+            for b, p, pg, at in rows_of(table, lens, page):
+                if p < 32 or p % 7 == 0:
+                    cache.v_scales[pg, :, at] = 0
+                    if not codes:
+                        cache.v[pg, :, at] = 0
+            check_repeated(J, cache, table, lens, [1, 2, 1], 2 * H, 2, spread=14)
