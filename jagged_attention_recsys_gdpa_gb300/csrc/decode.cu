@@ -294,11 +294,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r =
-      __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -308,10 +303,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 __device__ __forceinline__ float scale_of(uint32_t w, int j) {
   return __uint_as_float(__byte_perm(w, 0u, (0x0444u | (static_cast<uint32_t>(j) << 12))) >> 1);
 }
-// The four codes of a word as bf16 pairs (bytes 0 and 2, bytes 1 and 3) of 2^-120 times their values: exponent and
-// mantissa bits go to the low exponent and high mantissa bits, subnormals included.
-__device__ __forceinline__ uint32_t codes_even(uint32_t w) { return ((w << 8) & 0x80008000u) | ((w << 4) & 0x07f007f0u); }
-__device__ __forceinline__ uint32_t codes_odd(uint32_t w) { return (w & 0x80008000u) | ((w >> 4) & 0x07f007f0u); }
+// fp16 values as bf16, exactly where they are codes' (four significant bits, 2^-9 to 448, or NaN).
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t x) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+  return pack_bf16x2(f.x, f.y);
+}
+
 // ---------------------------------------------------------------- rows and columns
 // How a warp's products lie in its lanes (l = lane / 4, c = lane % 4): scores
 // and weights as [16 keys x 8 query rows], two keys and rows 2c and 2c + 1;
@@ -1139,10 +1136,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                   for (int i = 0; i < 2; ++i) {
                     uint32_t x[4];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {  // columns l and l + 8; 2^120 makes up for the codes' exponent bias
-                      const uint32_t w4 = __byte_perm(v[2 * i + y], 0u, 0x3120);
-                      x[y] = mul_bf16x2(codes_even(w4), 0x7b807b80u);
-                      x[2 + y] = mul_bf16x2(codes_odd(w4), 0x7b807b80u);
+                    for (int y = 0; y < 2; ++y) {  // columns l and l + 8
+                      e4m3x4_to_f16(v[2 * i + y], x[y], x[2 + y]);
+                      x[y] = f16x2_to_bf16x2(x[y]);
+                      x[2 + y] = f16x2_to_bf16x2(x[2 + y]);
                     }
                     mma_bf16(o[g][2 * j + i], x, ph);
                     mma_bf16(o[g][2 * j + i], x, pl);

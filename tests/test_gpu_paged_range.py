@@ -196,3 +196,34 @@ def test_exponents_that_begin_with_zeros():
                     if not codes:
                         cache.v[pg, :, at] = 0
             check_repeated(J, cache, table, lens, [1, 2, 1], 2 * H, 2, spread=14)
+
+
+@pytest.mark.parametrize("low", [False, True], ids=["level", "beside_small_blocks"])
+@pytest.mark.parametrize("code", [0x7f, 0xff])
+def test_nan_codes_are_nan_in_v(code, low):
+    """E4M3's own NaN, which other writers of a wrapped cache may use: the same in decode, whichever products its keys
+    take (blocks far below their neighbours take others), and in cache_read."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    lens, page, H, D = [90], 32, 2, 128
+    cache, table, _ = fill_cache(J, lens, page, H, D, "mxfp8", seed=261)
+    at = lambda p: (int(table[0, p // page]), 0, p % page)  # noqa: E731
+    if low:
+        for p in (64, 80):
+            cache.v_scales[at(p)] = 60
+    kp, vp = pages_of(cache)
+    q = torch.randn(3, H, D, generator=torch.Generator().manual_seed(262)).to(torch.bfloat16)
+    q_off = np.array([0, 3])
+    ro, rl, to, tl = R.decode(np64(q), kp, vp, table, lens, q_off, causal=True, **weight_parts("mxfp8", 14))
+    for p, column in ((88, 7), (89, 100)):  # seen by the last two rows, and by the last
+        cache.v[at(p)][column] = code
+    o, lse = J.decode(q.cuda(), cache, cu(table), cu(np.array(lens)), q_off=cu(q_off), causal=True)
+    assert J.device_status() == 0
+    want = np.zeros(ro.shape, bool)
+    want[1:, 0, 7] = want[2, 0, 100] = True
+    assert np.array_equal(np.isnan(np64(o)), want)
+    assert np.all(np.abs(np64(o) - ro)[~want] <= to[~want])
+    assert np.all(np.abs(np64(lse) - rl) <= tl)
+    _, v = J.cache_read(cache, cu(table), cu(np.array([0, 90])))
+    assert torch.isnan(v).nonzero().tolist() == [[88, 0, 7], [89, 0, 100]]
