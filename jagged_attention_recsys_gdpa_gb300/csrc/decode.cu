@@ -298,10 +298,11 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// 2^(e - 127) of byte j of w as fp32 (0 for e = 0: below 2^-118 of anything; e = 255 gives infinity, and with the
-// zero codes of such a block NaN).
+// 2^(e - 127) of byte j of w as fp32, one unit in the last place larger: so 255, whose exponent field is an infinity's,
+// has a mantissa and is NaN whatever the block's codes are, without a comparison. 2^-23 of every score is a hundredth of
+// what its sum in fp32 may be off. e = 0 gives next to 0.
 __device__ __forceinline__ float scale_of(uint32_t w, int j) {
-  return __uint_as_float(__byte_perm(w, 0u, (0x0444u | (static_cast<uint32_t>(j) << 12))) >> 1);
+  return __uint_as_float(__byte_perm(w, 2u, (0x0554u | (static_cast<uint32_t>(j) << 12))) >> 1);
 }
 // fp16 values as bf16, exactly where they are codes' (four significant bits, 2^-9 to 448, or NaN).
 __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t x) {

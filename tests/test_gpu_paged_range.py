@@ -227,3 +227,49 @@ def test_nan_codes_are_nan_in_v(code, low):
     assert np.all(np.abs(np64(lse) - rl) <= tl)
     _, v = J.cache_read(cache, cu(table), cu(np.array([0, 90])))
     assert torch.isnan(v).nonzero().tolist() == [[88, 0, 7], [89, 0, 100]]
+
+
+@pytest.mark.parametrize("act", ["softmax", "silu"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind", ["k_nan_block", "k_nan_block_of_zeros", "k_nan_code", "k_large", "v_nan_block", "v_nan_code"])
+def test_masked_places_of_an_mxfp8_cache_never_reach_a_row(kind, D, act):
+    """NaN blocks (exponent 255, whatever the codes), NaN codes and very large finite keys at the last position: the last
+    row, which alone sees it, is NaN (but for the large key), the others are within the bounds of the keys they see."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    H, page, lens, lq = 2, 16, [50, 21], 4
+    q = torch.randn(2 * lq, 2 * H, D, generator=torch.Generator().manual_seed(271)).to(torch.bfloat16)
+    q_off = np.array([0, lq, 2 * lq])
+    for mask in (dict(causal=True), dict(causal=True, window=5), dict(causal=True, block=49)):
+        cache, table, pages = fill_cache(J, lens, page, H, D, "mxfp8", seed=272)
+        ro, rl, to, tl = R.decode(np64(q), pages[0], pages[1], table, lens, q_off, act=act, **weight_parts("mxfp8", 14),
+                                  **mask)
+        for b, n in enumerate(lens):
+            at = (int(table[b, (n - 1) // page]), slice(None), (n - 1) % page)
+            codes, e = (cache.k, cache.k_scales) if kind[0] == "k" else (cache.v, cache.v_scales)
+            if "block" in kind:
+                e[at][:, 1] = 255
+            if "zeros" in kind or kind == "v_nan_block":
+                codes[at][:, 32:64] = 0
+            if "code" in kind:
+                codes[at][:, 40] = 0x7f
+            if kind == "k_large":
+                e[at] = 246
+        o, lse = J.decode(q.cuda(), cache, cu(table), cu(np.array(lens)), q_off=cu(q_off), act=act, **mask)
+        assert J.device_status() == 0
+        last = np.zeros(2 * lq, bool)
+        last[[lq - 1, 2 * lq - 1]] = True
+        got = np64(o)
+        assert np.all(np.abs(got - ro)[~last] <= to[~last])
+        bad = np.isnan(got[last])
+        if kind[0] == "v":
+            columns = slice(40, 41) if "code" in kind else slice(32, 64)
+            assert bad[..., columns].all()
+            bad[..., columns] = False
+            assert not bad.any()
+        elif kind != "k_large":
+            assert bad.all()
+        if act == "softmax":
+            assert np.all(np.abs(np64(lse) - rl)[~last] <= tl[~last])
+            assert kind[0] == "v" or kind == "k_large" or np.isnan(np64(lse)[last]).all()
