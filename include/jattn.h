@@ -392,8 +392,8 @@ int jattn_cache_read(const jattn_cache_t* cache, int64_t B, int64_t total, const
  * q_off[B] are left as they were. Cached values at positions that a row's mask
  * excludes never reach it, whatever they are. On an MXFP8 cache scores are
  * formed with the query row's largest value at 2^14: a key block whose values lie
- * below 2^-118 (E = 0) counts as zeros, and one beyond 2^104 may overflow them. A
- * value block of E = 0 counts as zeros beside blocks of E > 125 in its sequence.
+ * beyond 2^104 may overflow them. A value block of E = 0 (values below 2^-118)
+ * counts as zeros beside blocks of E > 125 in its sequence.
  *
  * No gradient: this is a serving operator. It serves any Lq, but is made for
  * few rows (Lq * G up to about 64); long prompts go through jattn_cache_read

@@ -298,11 +298,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// 2^(e - 127) of byte j of w as fp32, one unit in the last place larger: so 255, whose exponent field is an infinity's,
-// has a mantissa and is NaN whatever the block's codes are, without a comparison. 2^-23 of every score is a hundredth of
-// what its sum in fp32 may be off. e = 0 gives next to 0.
+// kScaleUnit 2^(e - 127) of byte j of w as fp32, for every e but 255: the sign and all mantissa bits set make it
+// -(2 - 2^-23) times the power, 2^-24 off, and make 255, whose exponent field is an infinity's, NaN whatever the block's
+// codes are. (One shift and one or; a low mantissa bit set by a byte permutation needs one more register: 128 MXFP8
+// histories 238 us against 233.)
+constexpr float kScaleUnit = -2.0f;
 __device__ __forceinline__ float scale_of(uint32_t w, int j) {
-  return __uint_as_float(__byte_perm(w, 2u, (0x0554u | (static_cast<uint32_t>(j) << 12))) >> 1);
+  return __uint_as_float((j < 3 ? w << (23 - 8 * j) : w >> 1) | 0x807fffffu);
 }
 // fp16 values as bf16, exactly where they are codes' (four significant bits, 2^-9 to 448, or NaN).
 __device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t x) {
@@ -460,7 +462,7 @@ __device__ __forceinline__ void repair(const DecodeArgs& a, const Place& at, int
     bool in[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float s = __shfl_sync(0xffffffffu, dot, (2 * c + i) * 4) * f[i];
+      const float s = __shfl_sync(0xffffffffu, dot, (2 * c + i) * 4) * (MX ? f[i] * kScaleUnit : f[i]);
       p[i] = SOFT ? ex2_approx(s - (m[i] == -INFINITY ? 0.0f : m[i])) * w[i] : activate(s, a.act);
       in[i] = pos >= lo[i] && pos < hi[i];
     }
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
                        any_hi);
 #pragma unroll
           for (int g = 0; g < NR; ++g) {
-            const float base = SOFT ? a.scale_log2 : a.scale;
+            const float base = (SOFT ? a.scale_log2 : a.scale) * (MX ? 1.0f / kScaleUnit : 1.0f);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               key_interval(query_of(a, min(row_base + 8 * g + 2 * c + i, end)), delta, at.s.n, a.mask, a.window, lo[g][i], hi[g][i]);

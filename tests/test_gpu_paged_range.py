@@ -273,3 +273,24 @@ def test_masked_places_of_an_mxfp8_cache_never_reach_a_row(kind, D, act):
         if act == "softmax":
             assert np.all(np.abs(np64(lse) - rl)[~last] <= tl[~last])
             assert kind[0] == "v" or kind == "k_large" or np.isnan(np64(lse)[last]).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_keys_of_the_smallest_exponents(D):
+    """K blocks of exponents 0 to 3 against query rows of 2^120: scores of ordinary size."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    lens, page, H = [60, 1, 35], 16, 2
+    cache, table, _ = fill_cache(J, lens, page, H, D, "mxfp8", seed=281)
+    g = torch.Generator().manual_seed(282)
+    cache.k_scales.copy_(torch.randint(0, 4, cache.k_scales.shape, generator=g).to(torch.uint8))
+    for b, p, pg, at in rows_of(table, lens, page):
+        if p % 3 == 0:
+            cache.k_scales[pg, :, at] = 0
+    kp, vp = pages_of(cache)
+    q = (torch.randn(3, 2 * H, D, generator=g) * 2.0**120).to(torch.bfloat16)
+    ro, rl, to, tl = R.decode(np64(q), kp, vp, table, lens, np.arange(4), scale=2.0**-5, **weight_parts("mxfp8"))
+    o, lse = J.decode(q.cuda(), cache, cu(table), cu(np.array(lens)), scale=2.0**-5)
+    assert J.device_status() == 0
+    assert np.all(np.abs(np64(o) - ro) <= to) and np.all(np.abs(np64(lse) - rl) <= tl)
