@@ -41,7 +41,7 @@ __device__ __forceinline__ bool find_row(const int64_t* off, int64_t B, int64_t 
     i = 0;
     return r < B;
   }
-  if (r >= __ldg(off + B)) return false;
+  if (r >= off[B]) return false;
   // the last b in [0, B) with off[b] <= r: seven probes at a time
   int64_t lo = 0, hi = B - 1;
   while (lo < hi) {
@@ -50,14 +50,14 @@ __device__ __forceinline__ bool find_row(const int64_t* off, int64_t B, int64_t 
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
       const int64_t at = lo + i * step;
-      if (at <= hi && __ldg(off + at) <= r) below = i;
+      if (at <= hi && off[at] <= r) below = i;
     }
     lo += below * step;
     hi = min(hi, lo + step - 1);
   }
   b = lo;
-  i = r - __ldg(off + lo);
-  return i >= 0 && r < __ldg(off + lo + 1);  // false where the offsets are no prefix sums
+  i = r - off[lo];
+  return i >= 0 && r < off[lo + 1];  // false where the offsets are no prefix sums
 }
 
 // Where a jagged row lies in the cache.
@@ -71,7 +71,7 @@ __device__ __forceinline__ Row place(const CacheView& c, const int64_t* off, con
                                      DevStatus* status) {
   int64_t b, i;
   if (!find_row(off, B, r, b, i)) return Row{kSkip, 0};
-  const int64_t s = start != nullptr ? __ldg(start + b) : 0;
+  const int64_t s = start != nullptr ? start[b] : 0;
   if (s < 0) return Row{kSkip, 0};  // an inactive sequence
   const int64_t cap = c.max_pages << c.page_shift;
   if (s > cap || i >= cap - s) {
@@ -102,8 +102,8 @@ template <int N>
 __device__ __forceinline__ void rotate(float (&x)[N], const float* c, const float* s, int pair) {
 #pragma unroll
   for (int e = 0; e < N / 2; e += 4) {
-    const float4 c4 = __ldg(reinterpret_cast<const float4*>(c + pair + e));
-    const float4 s4 = __ldg(reinterpret_cast<const float4*>(s + pair + e));
+    const float4 c4 = *reinterpret_cast<const float4*>(c + pair + e);
+    const float4 s4 = *reinterpret_cast<const float4*>(s + pair + e);
     const float cs[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -162,6 +162,12 @@ __device__ __forceinline__ uint32_t quantise16(const float (&x)[16], uint4& code
   return e;
 }
 
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 load16(const uint4* p) {
+  uint4 w;
+  asm volatile("ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
+  return w;
+}
 // 32 bytes in one access where the base allows it (every offset is a multiple).
 __device__ __forceinline__ void load32(const uint4* p, bool wide, uint4 (&w)[2]) {
   if (wide) {
@@ -223,8 +229,8 @@ __global__ void __launch_bounds__(kCacheBlock, MX ? kCacheCtas : 0) append_kerne
         load32(a.v + from, a.wide, v[i]);
       } else {
         if (u >= units) continue;
-        k[i][0] = __ldcs(a.k + from);
-        v[i][0] = __ldcs(a.v + from);
+        k[i][0] = load16(a.k + from);
+        v[i][0] = load16(a.v + from);
       }
     }
     if (base == 0) {
@@ -328,11 +334,11 @@ __global__ void __launch_bounds__(kCacheBlock, MX ? kCacheCtas : 0) read_kernel(
       ks[i] = vs[i] = 0.0f;
       if (row[r].at < 0) continue;
       const int64_t at = (row[r].at + (static_cast<int64_t>(h) << a.c.page_shift)) * per_head + unit;
-      k[i] = __ldcs(static_cast<const uint4*>(a.c.k) + at);
-      v[i] = __ldcs(static_cast<const uint4*>(a.c.v) + at);
+      k[i] = load16(static_cast<const uint4*>(a.c.k) + at);
+      v[i] = load16(static_cast<const uint4*>(a.c.v) + at);
       if constexpr (MX) {
-        ks[i] = e8m0_value(__ldg(a.c.ks + at / 2));
-        vs[i] = e8m0_value(__ldg(a.c.vs + at / 2));
+        ks[i] = e8m0_value(a.c.ks[at / 2]);
+        vs[i] = e8m0_value(a.c.vs[at / 2]);
       }
     }
 #pragma unroll

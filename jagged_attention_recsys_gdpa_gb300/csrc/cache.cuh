@@ -48,7 +48,7 @@ struct DecodeArgs {
 // status set, where the table's entry is not a page of the cache. pos lies
 // within the table (the caller has checked it against max_pages).
 __device__ __forceinline__ int64_t cache_row(const CacheView& c, int64_t b, int64_t pos, DevStatus* status) {
-  const int32_t page = __ldg(c.table + b * c.max_pages + (pos >> c.page_shift));
+  const int32_t page = c.table[b * c.max_pages + (pos >> c.page_shift)];
   if (page < 0 || page >= c.n_pages) {
     record_error(status, JATTN_ERR_PAGES, 80, static_cast<int>(b));
     return -1;

@@ -97,12 +97,12 @@ __device__ __forceinline__ Seq seq_of(const DecodeArgs& a, int b, int tile, int 
   s.q0 = b;
   s.lq = 1;
   if (a.q_off != nullptr) {
-    s.q0 = __ldg(a.q_off + b);
-    const int64_t end = __ldg(a.q_off + b + 1);
+    s.q0 = a.q_off[b];
+    const int64_t end = a.q_off[b + 1];
     // rows outside the tensor or offsets that decrease: the sequence has no rows
     s.lq = s.q0 >= 0 && end >= s.q0 && end <= a.total_q ? static_cast<int>(end - s.q0) : 0;
   }
-  const int64_t n = __ldg(a.kv_lens + b);
+  const int64_t n = a.kv_lens[b];
   s.n = n >= 0 && n <= a.max_kv ? static_cast<int>(n) : 0;
   int unused;
   key_interval(0, s.n - s.lq, s.n, a.mask, a.window, s.lo, unused);
@@ -162,7 +162,7 @@ __device__ __forceinline__ int64_t total_steps(const DecodeArgs& a, int tile, in
     if (c == 1) seqs[tid] = s;
     sum += static_cast<int64_t>(s.tiles) * a.cache.H * s.steps;
     if (blockIdx.x == 0) {  // the one check of what the host cannot see
-      const int64_t n = __ldg(a.kv_lens + b);
+      const int64_t n = a.kv_lens[b];
       if (n < 0 || n > a.max_kv) record_error(a.status, JATTN_ERR_LENGTH, 85, static_cast<int>(b));
       if (a.q_off != nullptr) check_offsets(a.q_off, b + 1, a.total_q, b, a.B, a.status);
     }
@@ -616,7 +616,7 @@ constexpr int64_t kNoBox = INT64_MIN;
 __device__ __forceinline__ int64_t box_page(const DecodeArgs& a, const Place& p, int step, int box, int lane) {
   const int r = box == step ? 0 : lane * box, first = p.s.k0 + p.t * step + r;
   if (r >= step || p.s.lo >= p.s.hi || first >= p.s.hi || first + box <= p.s.lo) return kNoBox;
-  return __ldg(p.table + (first >> a.cache.page_shift));
+  return p.table[first >> a.cache.page_shift];
 }
 
 template <int D, bool MX, int WM>
@@ -807,8 +807,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             for (int kk = 0; kk < KS; ++kk) {
               // bf16: columns 2c, 2c + 1 and 2c + 8, 2c + 9 of the 16; codes: columns 4c .. 4c + 3, a word's
               const int w0 = MX ? kk * 8 + 2 * c : kk * 8 + c, w1 = MX ? w0 + 1 : w0 + 4;
-              q[g][kk][0] = src ? __ldg(src + w0) : 0u;
-              q[g][kk][1] = src ? __ldg(src + w1) : 0u;
+              q[g][kk][0] = src ? src[w0] : 0u;
+              q[g][kk][1] = src ? src[w1] : 0u;
             }
           }
         }

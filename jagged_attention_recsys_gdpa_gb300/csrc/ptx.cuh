@@ -270,7 +270,9 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 // ---------------------------------------------------------------- programmatic launches
 // A kernel launched with programmatic stream serialisation may start once every
 // CTA of the kernel before it has called the first; it sees that kernel's results
-// after the second.
+// after the second. What it reads of them it reads with plain or volatile loads:
+// read-only ones (__ldg) are for memory that nothing writes while the kernel is
+// resident, and may move before the wait.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
