@@ -85,7 +85,8 @@ enum {
   JATTN_ERR_OFFSETS = 5,     /* device: offsets not a valid prefix sum of the totals */
   JATTN_ERR_TIMEOUT = 6,     /* device: a bounded pipeline wait expired */
   JATTN_ERR_UNSUPPORTED = 7, /* device is not sm_103 / no kernel image */
-  JATTN_ERR_TOO_LARGE = 8,   /* jattn_fwd_noalloc: problem needs more than the library's scratch */
+  JATTN_ERR_TOO_LARGE = 8,   /* jattn_fwd_noalloc: problem needs more than the library's scratch; device:
+                                jattn_decode has more work than it can count */
   JATTN_ERR_ROPE = 9,        /* device: a rotary position at or beyond the cos/sin tables' rows */
   JATTN_ERR_PAGES = 10,      /* device: a page table entry that is no page of the cache */
   JATTN_ERR_LENGTH = 11      /* device: a cached length or position outside its sequence's pages */
@@ -387,7 +388,12 @@ int jattn_cache_read(const jattn_cache_t* cache, int64_t B, int64_t total, const
  * Writes o [total_q, H, D] bf16 (which must not overlap q) and, for
  * JATTN_SOFTMAX, lse [total_q, H] fp32. A sequence with a bad page among
  * those it needs sets JATTN_ERR_PAGES; its rows are unspecified, as are those
- * of a call whose bounded waits ran out (JATTN_ERR_TIMEOUT).
+ * of a call whose bounded waits ran out (JATTN_ERR_TIMEOUT). Offsets that are
+ * no prefix sums set JATTN_ERR_OFFSETS; rows are unspecified, and where
+ * sequences name the same rows so often that the work exceeds any that prefix
+ * sums could give, none is written. Nor is any where the call has 2^31 or more
+ * steps for each worker (3 * 10^14 pairs of query rows and keys at least:
+ * JATTN_ERR_TOO_LARGE).
  * A row that no key is allowed for gets o = 0, lse = -inf. Rows behind
  * q_off[B] are left as they were. Cached values at positions that a row's mask
  * excludes never reach it, whatever they are. On an MXFP8 cache scores are

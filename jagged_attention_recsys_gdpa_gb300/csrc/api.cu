@@ -1098,7 +1098,7 @@ const char* jattn_error_string(int code) {
     case JATTN_ERR_OFFSETS: return "offsets are not a valid prefix sum of the row totals";
     case JATTN_ERR_TIMEOUT: return "a bounded pipeline wait expired";
     case JATTN_ERR_UNSUPPORTED: return "device is not sm_103";
-    case JATTN_ERR_TOO_LARGE: return "problem needs more scratch than the allocation-free entry point holds";
+    case JATTN_ERR_TOO_LARGE: return "more scratch than the allocation-free entry point holds, or more work than a decode call can count";
     case JATTN_ERR_ROPE: return "a rotary position lies at or beyond the cos/sin tables' rows";
     case JATTN_ERR_PAGES: return "a page table entry is no page of the cache";
     case JATTN_ERR_LENGTH: return "a cached length or position lies outside its sequence's pages";

@@ -34,6 +34,8 @@ struct DecodeArgs {
   float* lse;  // softmax only
   int64_t B, total_q;
   int64_t max_kv;  // bound of kv_lens
+  int64_t max_steps;  // bound of all units' steps; a batch that has more is refused with steps_error
+  int steps_error;
   int Hq, G;       // query heads, query heads per key/value head
   uint32_t g_inverse;  // 2^32 / G rounded up (G > 1)
   int act, mask, window, norm_by_lkv;

@@ -32,6 +32,7 @@
 // that moves next to nothing 9.5 us. Softmax and the pointwise activations have
 // kernels of their own: with both in one, the code is too long for the
 // instruction cache (MXFP8 246 us against 242).
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 
@@ -152,7 +153,9 @@ __device__ __forceinline__ int64_t divide(int64_t x, int d) {
 }
 
 // The number of all steps; start[i]: the first step of stretch i, a thread's
-// share of the sequences. With a thread per sequence seqs[] keeps them.
+// share of the sequences. With a thread per sequence seqs[] keeps them. Offsets
+// that are no prefix sums may name the same rows again and again: a batch with
+// more steps than prefix sums could give has none at all.
 __device__ __forceinline__ int64_t total_steps(const DecodeArgs& a, int tile, int step, int64_t* start, Seq* seqs) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = static_cast<int>((a.B + kThreads - 1) / kThreads);
@@ -160,7 +163,7 @@ __device__ __forceinline__ int64_t total_steps(const DecodeArgs& a, int tile, in
   for (int64_t b = static_cast<int64_t>(tid) * c; b < min(a.B, static_cast<int64_t>(tid + 1) * c); ++b) {
     const Seq s = seq_of(a, static_cast<int>(b), tile, step);
     if (c == 1) seqs[tid] = s;
-    sum += static_cast<int64_t>(s.tiles) * a.cache.H * s.steps;
+    sum = min(sum + static_cast<int64_t>(s.tiles) * a.cache.H * s.steps, a.max_steps + 1);
     if (blockIdx.x == 0) {  // the one check of what the host cannot see
       const int64_t n = a.kv_lens[b];
       if (n < 0 || n > a.max_kv) record_error(a.status, JATTN_ERR_LENGTH, 85, static_cast<int>(b));
@@ -179,7 +182,9 @@ __device__ __forceinline__ int64_t total_steps(const DecodeArgs& a, int tile, in
   }
   start[tid] = before + inc - sum;
   __syncthreads();
-  return all;
+  if (all <= a.max_steps) return all;
+  if (blockIdx.x == 0 && tid == 0) record_error(a.status, a.steps_error, 87, 0);
+  return 0;
 }
 
 // The place of step `first`, one of those counted.
@@ -1516,9 +1521,14 @@ void decode_box(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int 
   *lines = step <= page_size && row > 128 ? row / 128 : 1;
 }
 
-cudaError_t launch_decode(int D, bool mx, const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, void* scratch,
+cudaError_t launch_decode(int D, bool mx, DecodeArgs a, const CUtensorMap& k, const CUtensorMap& v, void* scratch,
                           cudaStream_t stream) {
   const Shape s = shape_of(D, mx, a.B, a.total_q, a.max_kv, a.G, a.cache.H);
+  const int64_t step = 4096 / (D * (mx ? 1 : 2)) * s.wm, of_tile = std::max(int64_t(1), (a.max_kv + step - 1) / step);
+  const int64_t most = (a.total_q * a.G / s.tile + std::min(a.total_q, a.B)) * a.cache.H * of_tile;
+  const int64_t counted = static_cast<int64_t>(s.ctas) * (kWarps / s.wm) * INT32_MAX;  // a run's steps in 32 bits
+  a.max_steps = std::min(most, counted);
+  a.steps_error = most <= counted ? JATTN_ERR_OFFSETS : JATTN_ERR_TOO_LARGE;
   if (D == 64) return mx ? launch_shape<64, true>(a, k, v, s, scratch, stream) : launch_shape<64, false>(a, k, v, s, scratch, stream);
   return mx ? launch_shape<128, true>(a, k, v, s, scratch, stream) : launch_shape<128, false>(a, k, v, s, scratch, stream);
 }

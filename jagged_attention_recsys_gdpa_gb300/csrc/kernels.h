@@ -123,7 +123,7 @@ cudaError_t launch_cache_read(const CacheView& c, bool mx, int64_t B, int64_t to
 size_t decode_scratch_bytes(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H);
 void decode_box(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int G, int H, int page_size, int* rows,
                 int* lines);
-cudaError_t launch_decode(int D, bool mx, const DecodeArgs& a, const CUtensorMap& k, const CUtensorMap& v, void* scratch,
+cudaError_t launch_decode(int D, bool mx, DecodeArgs a, const CUtensorMap& k, const CUtensorMap& v, void* scratch,
                           cudaStream_t stream);
 
 }  // namespace jattn
