@@ -81,7 +81,7 @@ enum {
   JATTN_ERR_INVALID = 1,     /* bad argument detected on the host */
   JATTN_ERR_CUDA = 2,        /* a CUDA runtime call failed (launch, attribute) */
   JATTN_ERR_WORKSPACE = 3,   /* workspace missing, too small or misaligned */
-  JATTN_ERR_ALIGN = 4,       /* a value tensor is not 16-byte aligned */
+  JATTN_ERR_ALIGN = 4,       /* a value tensor is not 16-byte aligned (paged cache: or another not to its elements) */
   JATTN_ERR_OFFSETS = 5,     /* device: offsets not a valid prefix sum of the totals */
   JATTN_ERR_TIMEOUT = 6,     /* device: a bounded pipeline wait expired */
   JATTN_ERR_UNSUPPORTED = 7, /* device is not sm_103 / no kernel image */
@@ -327,7 +327,8 @@ int jattn_bwd_mxfp8(const jattn_params_t* p, const int64_t* q_off, const int64_t
  *     nearest even, saturated to +-448. A block that holds a NaN or an infinity
  *     gets E = 255 (E8M0's NaN) and reads back as NaN; codes 0x7f / 0xff (E4M3's
  *     own NaN) are never written.
- * Buffers are device memory and 16-byte aligned.
+ * Buffers are device memory and 16-byte aligned; offsets, lengths, tables and
+ * lse are aligned to their elements.
  *
  * Errors that only the device sees land in the status word at `workspace`
  * (256 bytes, zero before its first use, read with jattn_get_status): nothing
@@ -358,7 +359,8 @@ typedef struct {
  * rope_rows sets JATTN_ERR_ROPE and its key is stored as it came. A position
  * past max_pages * page_size sets JATTN_ERR_LENGTH, a bad table entry
  * JATTN_ERR_PAGES; such rows are not written. Two rows of one call must not go
- * to the same place (which of them stays is not specified). Return codes as
+ * to the same place (which of them stays is not specified), and the cache's k
+ * and v pages must not overlap (JATTN_ERR_INVALID). Return codes as
  * jattn_rope. */
 int jattn_cache_append(const jattn_cache_t* cache, int64_t B, int64_t total, const int64_t* off, const int64_t* start,
                        const int32_t* page_table, int64_t max_pages, const uint16_t* k, const uint16_t* v,
@@ -370,7 +372,8 @@ int jattn_cache_append(const jattn_cache_t* cache, int64_t B, int64_t total, con
  * i (start NULL: 0; negative: the sequence's rows are left as they were). MXFP8
  * values are code * 2^(E - 127) rounded to bf16 (exact but for values below
  * bf16's subnormals or above its largest). Rows at and behind off[B] are left
- * as they were; rows of a bad page read as zeros (JATTN_ERR_PAGES). */
+ * as they were; rows of a bad page read as zeros (JATTN_ERR_PAGES). k and v
+ * must not overlap (JATTN_ERR_INVALID). */
 int jattn_cache_read(const jattn_cache_t* cache, int64_t B, int64_t total, const int64_t* off, const int64_t* start,
                      const int32_t* page_table, int64_t max_pages, uint16_t* k, uint16_t* v, void* workspace,
                      size_t workspace_bytes, void* stream);
@@ -385,8 +388,8 @@ int jattn_cache_read(const jattn_cache_t* cache, int64_t B, int64_t total, const
  * stands at the last cached position (delta = kv_lens[b] - Lq(b)).
  * p->total_kv is an upper bound of kv_lens (at most max_pages * page_size); a
  * length outside [0, p->total_kv] sets JATTN_ERR_LENGTH and counts as 0.
- * Writes o [total_q, H, D] bf16 (which must not overlap q) and, for
- * JATTN_SOFTMAX, lse [total_q, H] fp32. A sequence with a bad page among
+ * Writes o [total_q, H, D] bf16 and, for JATTN_SOFTMAX, lse [total_q, H] fp32;
+ * q, o and lse must not overlap (JATTN_ERR_INVALID). A sequence with a bad page among
  * those it needs sets JATTN_ERR_PAGES; its rows are unspecified, as are those
  * of a call whose bounded waits ran out (JATTN_ERR_TIMEOUT). Offsets that are
  * no prefix sums set JATTN_ERR_OFFSETS; rows are unspecified, and where

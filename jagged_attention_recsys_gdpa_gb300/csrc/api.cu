@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include <cuda.h>
@@ -896,10 +897,30 @@ int check_status_ws(const void* ws, size_t ws_bytes) {
   return !ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < 256 ? JATTN_ERR_WORKSPACE : JATTN_OK;
 }
 
+// What the kernels read and write one by one: int64 (offsets, lengths, places), then 32-bit (tables, LSE).
+bool misplaced(std::initializer_list<const void*> wide, std::initializer_list<const void*> narrow) {
+  uintptr_t w = 0, n = 0;
+  for (const void* p : wide) w |= reinterpret_cast<uintptr_t>(p);
+  for (const void* p : narrow) n |= reinterpret_cast<uintptr_t>(p);
+  return (w & 7u) || (n & 3u);
+}
+
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
+}
+
 // Total rows of a copy: at least one to a CTA of a one-dimensional grid, and the
 // 16-byte pieces of a row counted in 32 bits.
 bool too_many_rows(const jattn_cache_t* c, int64_t total) {
   return total > INT32_MAX || static_cast<int64_t>(c->H) * (c->D / 8) > (1 << 24);
+}
+
+// Bytes of the key (or value) pages.
+int64_t pages_bytes(const jattn_cache_t* c) {
+  const int64_t page = static_cast<int64_t>(c->H) * c->D * c->page_size * (c->format == JATTN_CACHE_MXFP8 ? 1 : 2);
+  constexpr int64_t most = int64_t(1) << 62;
+  return c->n_pages > most / page ? most : c->n_pages * page;
 }
 
 CacheView cache_view(const jattn_cache_t* c, const int32_t* page_table, int64_t max_pages) {
@@ -959,8 +980,9 @@ int jattn_cache_append(const jattn_cache_t* c, int64_t B, int64_t total, const i
   if (!start || total < 0 || too_many_rows(c, total) || (!off && total != B)) return JATTN_ERR_INVALID;
   if (total > 0 && (!k || !v)) return JATTN_ERR_INVALID;
   if ((rope_cos || rope_sin) && (rc = check_rope(rope_cos, rope_sin, rope_rows)) != JATTN_OK) return rc;
-  if (!aligned16(k) || !aligned16(v)) return JATTN_ERR_ALIGN;
+  if (!aligned16(k) || !aligned16(v) || misplaced({off, start}, {page_table})) return JATTN_ERR_ALIGN;
   if ((rc = check_status_ws(ws, ws_bytes)) != JATTN_OK) return rc;
+  if (overlap(c->k, pages_bytes(c), c->v, pages_bytes(c))) return JATTN_ERR_INVALID;
   DeviceInfo dev;
   if ((rc = device_info(dev)) != JATTN_OK) return rc;
   clear_stale_error();
@@ -979,8 +1001,10 @@ int jattn_cache_read(const jattn_cache_t* c, int64_t B, int64_t total, const int
   if (rc != JATTN_OK) return rc;
   if ((rc = check_pages(c, B, page_table, max_pages)) != JATTN_OK) return rc;
   if (!off || total < 0 || too_many_rows(c, total) || (total > 0 && (!k || !v))) return JATTN_ERR_INVALID;
-  if (!aligned16(k) || !aligned16(v)) return JATTN_ERR_ALIGN;
+  if (!aligned16(k) || !aligned16(v) || misplaced({off, start}, {page_table})) return JATTN_ERR_ALIGN;
   if ((rc = check_status_ws(ws, ws_bytes)) != JATTN_OK) return rc;
+  const int64_t bytes = total * c->H * c->D * 2;
+  if (overlap(k, bytes, v, bytes)) return JATTN_ERR_INVALID;
   DeviceInfo dev;
   if ((rc = device_info(dev)) != JATTN_OK) return rc;
   clear_stale_error();
@@ -1008,11 +1032,15 @@ int jattn_decode(const jattn_params_t* p, const jattn_cache_t* c, const int64_t*
   if ((rc = check_pages(c, p->B, page_table, max_pages)) != JATTN_OK) return rc;
   if (!kv_lens || p->total_kv > max_pages * c->page_size || (!q_off && p->total_q != p->B)) return JATTN_ERR_INVALID;
   if (p->total_q > 0 && (!q || !o || q == o || (p->act == JATTN_SOFTMAX && !lse))) return JATTN_ERR_INVALID;
-  if (!aligned16(q) || !aligned16(o)) return JATTN_ERR_ALIGN;
+  if (!aligned16(q) || !aligned16(o) || misplaced({q_off, kv_lens}, {page_table, lse})) return JATTN_ERR_ALIGN;
   if ((rc = check_status_ws(ws, ws_bytes)) != JATTN_OK) return rc;
   size_t need = 0;
   if ((rc = jattn_decode_scratch_size(p, c, &need)) != JATTN_OK) return rc;
   if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) || scratch_bytes < need) return JATTN_ERR_WORKSPACE;
+  const int64_t rows = p->total_q * p->H, lse_bytes = p->act == JATTN_SOFTMAX ? rows * 4 : 0;
+  if (overlap(q, rows * p->D * 2, o, rows * p->D * 2) || overlap(lse, lse_bytes, q, rows * p->D * 2) ||
+      overlap(lse, lse_bytes, o, rows * p->D * 2))
+    return JATTN_ERR_INVALID;
   DeviceInfo dev;
   if ((rc = device_info(dev)) != JATTN_OK) return rc;
   if ((rc = encoder()) != JATTN_OK) return rc;
@@ -1041,10 +1069,10 @@ int jattn_decode(const jattn_params_t* p, const jattn_cache_t* c, const int64_t*
   a.debug_flags = g_debug_flags;
   a.status = static_cast<DevStatus*>(ws);
   const bool mx = c->format == JATTN_CACHE_MXFP8;
-  int rows, lines;
-  decode_box(p->D, mx, p->B, p->total_q, p->total_kv, a.G, c->H, c->page_size, &rows, &lines);
+  int box_rows, box_lines;
+  decode_box(p->D, mx, p->B, p->total_q, p->total_kv, a.G, c->H, c->page_size, &box_rows, &box_lines);
   CUtensorMap mk, mv;
-  if (make_page_map(&mk, c, c->k, rows, lines) || make_page_map(&mv, c, c->v, rows, lines))
+  if (make_page_map(&mk, c, c->k, box_rows, box_lines) || make_page_map(&mv, c, c->v, box_rows, box_lines))
     return cuda_fail("cuTensorMapEncodeTiled", cudaErrorInvalidValue);
   const cudaError_t e = launch_decode(p->D, mx, a, mk, mv, scratch, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? JATTN_OK : cuda_fail("decode kernel launch", e);
@@ -1094,7 +1122,7 @@ const char* jattn_error_string(int code) {
     case JATTN_ERR_INVALID: return "invalid argument";
     case JATTN_ERR_CUDA: return "CUDA runtime error";
     case JATTN_ERR_WORKSPACE: return "workspace missing, too small or not 256-byte aligned";
-    case JATTN_ERR_ALIGN: return "value tensor not 16-byte aligned";
+    case JATTN_ERR_ALIGN: return "value tensor not 16-byte aligned, or another not aligned to its elements";
     case JATTN_ERR_OFFSETS: return "offsets are not a valid prefix sum of the row totals";
     case JATTN_ERR_TIMEOUT: return "a bounded pipeline wait expired";
     case JATTN_ERR_UNSUPPORTED: return "device is not sm_103";

@@ -32,3 +32,26 @@ def test_offsets_that_name_the_same_rows_again_and_again(B, fmt):
     assert bool((out == 5.0).all()) and bool((lse == 5.0).all())
     o, l2 = J.decode(q, cache, table, kv, q_off=cu(np.arange(B + 1)))
     assert J.device_status() == 0 and torch.equal(o, good[0]) and torch.equal(l2, good[1])
+
+
+def test_outputs_that_overlap():
+    """Through the Python calls: outputs that share memory with an input or with each other."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    cache, table, _ = fill_cache(J, [40, 70], 16, 2, 64, "bf16", seed=302)
+    table, kv = cu(table), cu(np.array([40, 70]))
+    flat = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q = flat[:2]
+    for out in (flat[:2], flat[1:]):
+        with pytest.raises(J.JattnError):
+            J.decode(q, cache, table, kv, out=out)
+    with pytest.raises(J.JattnError):
+        J.decode(q, cache, table, kv, lse=flat.view(torch.float32).view(-1)[:4].view(2, 2))
+    off = cu(np.array([0, 1, 2]))
+    with pytest.raises(J.JattnError):
+        J.cache_read(cache, table, off, k=flat[:2], v=flat[1:])
+    one = J.PagedCache(cache.k, cache.k)  # read only is fine
+    J.decode(q, one, table, kv)
+    with pytest.raises(J.JattnError):
+        J.cache_append(one, flat[:2].clone(), flat[:2].clone(), table, cu(np.array([3, 4])))
+    assert J.device_status() == 0
