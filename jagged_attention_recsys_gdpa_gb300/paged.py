@@ -67,6 +67,8 @@ class PagedCache:
                 raise ValueError("scales must be uint8 [n_pages, H, page_size, D/32] on the cache's device")
         if not all(t.is_contiguous() for t in (k, v, k_scales, v_scales) if t is not None):
             raise ValueError("cache buffers must be contiguous")
+        if k.requires_grad or v.requires_grad:
+            raise ValueError("cache buffers take no gradient: pass detached tensors")
         self._k, self._v, self._k_scales, self._v_scales = k, v, k_scales, v_scales
         self._c = B.cache(n, page, H, D, B.CACHE_MXFP8 if mx else B.CACHE_BF16, k, v, k_scales, v_scales)
         self._ref = ctypes.byref(self._c)
@@ -100,6 +102,12 @@ def paged_cache(n_pages, page_size, H, D, format="bf16", device="cuda") -> Paged
 def _check_rows(cache, x, name):
     if x.dtype is not torch.bfloat16 or x.dim() != 3 or x.device != cache._device or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous bf16 tensor [total, H, D] on the cache's device")
+
+
+def _check_no_grad(*outputs):
+    for x in outputs:
+        if x is not None and x.requires_grad and torch.is_grad_enabled():
+            raise ValueError("outputs are written without a gradient: pass tensors that need none")
 
 
 def _check_index(cache, t, n, name):
@@ -172,6 +180,7 @@ def cache_read(cache, page_table, off, start=None, total=None, k=None, v=None):
             total = x.shape[0] if total is None else total
             if x.shape != (total, cache._H, cache._D):
                 raise ValueError(f"{name} must be [total, H, D] with the cache's H and D")
+    _check_no_grad(k, v)
     total = int(off[-1].item()) if total is None else int(total)
     k = k if k is not None else torch.empty((total, cache._H, cache._D), dtype=torch.bfloat16, device=cache._device)
     v = v if v is not None else torch.empty_like(k)
@@ -222,6 +231,7 @@ def decode(q, cache, page_table, kv_lens, q_off=None, act="softmax", causal=Fals
     elif lse.dtype != torch.float32 or lse.shape != (total_q, Hq) or lse.device != q.device \
             or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous fp32 tensor [total_q, Hq] on the cache's device")
+    _check_no_grad(out, lse)
     n = B.decode_scratch_size(p, cache._ref)
     scratch = torch.empty(n, dtype=torch.uint8, device=cache._device)
     _launch(cache, B.decode, p, cache._ref, q_off, kv_lens, page_table, q, out, lse, scratch.data_ptr(), n)

@@ -55,3 +55,29 @@ def test_outputs_that_overlap():
     with pytest.raises(J.JattnError):
         J.cache_append(one, flat[:2].clone(), flat[:2].clone(), table, cu(np.array([3, 4])))
     assert J.device_status() == 0
+
+
+def test_tensors_that_need_a_gradient():
+    """None of the operators has a backward pass: buffers and outputs that need a gradient are refused, as q and new rows
+    are (outputs under no_grad are written)."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    cache, table, _ = fill_cache(J, [40, 70], 16, 2, 64, "bf16", seed=303)
+    table, kv, off = cu(table), cu(np.array([40, 70])), cu(np.array([0, 1, 2]))
+    q = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    leaf = torch.zeros_like(q).requires_grad_(True)
+    lse = torch.zeros(2, 2, device="cuda").requires_grad_(True)
+    for kw in (dict(out=leaf), dict(lse=lse)):
+        with pytest.raises(ValueError, match="gradient"):
+            J.decode(q, cache, table, kv, **kw)
+    for kw in (dict(k=leaf), dict(v=leaf)):
+        with pytest.raises(ValueError, match="gradient"):
+            J.cache_read(cache, table, off, **kw)
+    for k, v in ((cache.k.clone().requires_grad_(True), cache.v), (cache.k, cache.v.clone().requires_grad_(True))):
+        with pytest.raises(ValueError, match="gradient"):
+            J.PagedCache(k, v)
+    with torch.no_grad():
+        J.decode(q, cache, table, kv, out=leaf, lse=lse)
+        J.cache_read(cache, table, off, k=leaf)
+    J.PagedCache(cache.k.clone().requires_grad_(True).detach(), cache.v)
+    assert J.device_status() == 0
