@@ -15,8 +15,10 @@
 Row ``pos`` of sequence b lies in page ``page_table[b, pos // page_size]``.
 Every tensor lies on the cache's device; calls run on that device's current
 stream and allocate only their outputs and scratch (from PyTorch's allocator, so
-calls on several streams, and captured graphs, do not share any). Device-side
-errors (a bad page, a length past the table) are read with ``device_status``.
+calls on several streams, and captured graphs, do not share any). Rows that a call
+leaves as they were (padding behind the last sequence, skipped sequences) hold
+anything in outputs that the call itself allocates. Device-side errors (a bad
+page, a length past the table) are read with ``device_status``.
 """
 from __future__ import annotations
 
