@@ -389,8 +389,8 @@ int jattn_cache_read(const jattn_cache_t* cache, int64_t B, int64_t total, const
  * p->total_kv is an upper bound of kv_lens (at most max_pages * page_size); a
  * length outside [0, p->total_kv] sets JATTN_ERR_LENGTH and counts as 0.
  * Writes o [total_q, H, D] bf16 and, for JATTN_SOFTMAX, lse [total_q, H] fp32;
- * q, o and lse must not overlap (JATTN_ERR_INVALID). A sequence with a bad page among
- * those it needs sets JATTN_ERR_PAGES; its rows are unspecified, as are those
+ * q, o and lse must not overlap (JATTN_ERR_INVALID). A sequence with a bad page
+ * among those it needs sets JATTN_ERR_PAGES; its rows are unspecified, as are those
  * of a call whose bounded waits ran out (JATTN_ERR_TIMEOUT). Offsets that are
  * no prefix sums set JATTN_ERR_OFFSETS; rows are unspecified, and where
  * sequences name the same rows so often that the work exceeds any that prefix
@@ -399,10 +399,12 @@ int jattn_cache_read(const jattn_cache_t* cache, int64_t B, int64_t total, const
  * JATTN_ERR_TOO_LARGE).
  * A row that no key is allowed for gets o = 0, lse = -inf. Rows behind
  * q_off[B] are left as they were. Cached values at positions that a row's mask
- * excludes never reach it, whatever they are. On an MXFP8 cache scores are
- * formed with the query row's largest value at 2^14: a key block whose values lie
- * beyond 2^104 may overflow them. A value block of E = 0 (values below 2^-118)
- * counts as zeros beside blocks of E > 125 in its sequence.
+ * excludes never reach it, whatever they are. Weights enter the second product
+ * as two bf16 parts (2^-16) on a bf16 cache and as one fp16 part (2^-11, half a
+ * step) on an MXFP8 one. There a query row is held in fp16 with its largest value
+ * at 2^14 (values below 2^-28 of that lose bits): a key block whose values lie
+ * beyond 2^104 may overflow its scores. A value block of E = 0 (values below
+ * 2^-118) counts as zeros beside blocks of E > 125 in its sequence.
  *
  * No gradient: this is a serving operator. It serves any Lq, but is made for
  * few rows (Lq * G up to about 64); long prompts go through jattn_cache_read

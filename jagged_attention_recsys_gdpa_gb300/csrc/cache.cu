@@ -11,8 +11,9 @@
 // the bound; of the 32 of a block the accesses lay too far apart.)
 //
 // Measured: 213 k rows of 4 heads of 128, keys rotated, bf16 (981 MB) 138 us,
-// 7.1 TB/s; 131 k rows of 8 heads to MXFP8 (822 MB) 128 us, 6.4 TB/s; 213 k rows
-// of 8 heads back from MXFP8 (1.32 GB) 204 us, 6.5 TB/s.
+// 7.1 TB/s; 131 k rows of 8 heads to MXFP8 (822 MB) 125 us, 6.6 TB/s; 213 k rows
+// of 8 heads back from MXFP8 (1.32 GB) 203 us, 6.5 TB/s, from bf16 (1.74 GB) 252 us,
+// 6.9 TB/s.
 #include <algorithm>
 #include <cstdint>
 

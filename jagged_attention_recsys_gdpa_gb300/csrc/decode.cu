@@ -7,13 +7,15 @@
 //
 // Bound. Every cached row is read once and meets the Lq * G query rows of its
 // sequence and head, 4 D operations per 2 rows of 2 D bytes: for up to some 60
-// rows the cache's bytes bound the call, not the tensor cores. So the layout
+// rows the cache's bytes are the floor, not the tensor cores. So the layout
 // serves the copies: each worker keeps its own ring of stages in shared memory,
 // filled by TMA straight from the pages (a step's rows are one piece of a page, or
 // one piece each of several small pages), and the products are warp-level MMAs with
-// keys (then columns) on their 16 rows and the query rows on their 8 columns; a
-// 128-row tcgen05 tile would be mostly padding here and would stage operands and
-// accumulators through TMEM for nothing.
+// keys (then columns) on their 16 rows and the query rows on their 8 columns. A
+// tcgen05 tile with the query rows on its 128 rows would be mostly padding; with
+// the keys there it would be full, and pay for more than 8 rows a head, which the
+// tiles of 8 and 16 rows here copy (and, of MXFP8, convert) again for every tile.
+// That one has not been built.
 //
 // Split. A unit is one (sequence, key/value head, tile of 8 or 16 query rows);
 // its keys go in steps of a fixed number of positions. All units' steps are
@@ -27,9 +29,9 @@
 //
 // Measured: 64 histories of 50 to 32,000 keys, 8 heads of 128, bf16 (1.78 GB)
 // 260 us, 6.85 TB/s, the rate of a plain copy; 128 of them in MXFP8 (1.49 GB)
-// 236 us, 6.3 TB/s (the copies alone take 231); 32 query heads on 8, 1,000 to
-// 8,000 keys (615 MB) 98 us; one history of 130,001 keys (67 MB) 18.5 us; a call
-// that moves next to nothing 9.5 us. Softmax and the pointwise activations have
+// 233 us, 6.4 TB/s (the copies alone take 220); 32 query heads on 8, 1,000 to
+// 8,000 keys (615 MB) 99 us; one history of 130,001 keys (67 MB) 18.4 us; a call
+// that moves next to nothing 9.4 us. Softmax and the pointwise activations have
 // kernels of their own: with both in one, the code is too long for the
 // instruction cache (MXFP8 246 us against 242).
 #include <algorithm>

@@ -200,7 +200,8 @@ def decode(q, cache, page_table, kv_lens, q_off=None, act="softmax", causal=Fals
     row of a sequence standing at its last cached position. Hq is a multiple of
     the cache's H. Activations, masks and scale as in ``forward``. ``max_kv``
     bounds kv_lens (default: the table's rows). Rows behind q_off[B] are left as
-    they were in ``out`` / ``lse``. No gradient. See jattn_decode."""
+    they were in ``out`` / ``lse``. Weights meet the values as two bf16 parts, or on an
+    MXFP8 cache as one fp16 number. No gradient. See jattn_decode."""
     _check_table(cache, page_table)
     nb, max_pages = page_table.shape
     _check_rows(cache, q, "q")
