@@ -31,7 +31,7 @@
 // 260 us, 6.85 TB/s, the rate of a plain copy; 128 of them in MXFP8 (1.49 GB)
 // 233 us, 6.4 TB/s (the copies alone take 220); 32 query heads on 8, 1,000 to
 // 8,000 keys (615 MB) 99 us; one history of 130,001 keys (67 MB) 18.4 us; a call
-// that moves next to nothing 9.4 us. Softmax and the pointwise activations have
+// that moves next to nothing 9.6 us. Softmax and the pointwise activations have
 // kernels of their own: with both in one, the code is too long for the
 // instruction cache (MXFP8 246 us against 242).
 #include <algorithm>
@@ -156,8 +156,8 @@ __device__ __forceinline__ int64_t divide(int64_t x, int d) {
 
 // The number of all steps; start[i]: the first step of stretch i, a thread's
 // share of the sequences. With a thread per sequence seqs[] keeps them. Offsets
-// that are no prefix sums may name the same rows again and again: a batch with
-// more steps than prefix sums could give has none at all.
+// that are no prefix sums may name the same rows again and again: the number then
+// exceeds a.max_steps, and no worker gets any.
 __device__ __forceinline__ int64_t total_steps(const DecodeArgs& a, int tile, int step, int64_t* start, Seq* seqs) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int c = static_cast<int>((a.B + kThreads - 1) / kThreads);
@@ -184,9 +184,7 @@ __device__ __forceinline__ int64_t total_steps(const DecodeArgs& a, int tile, in
   }
   start[tid] = before + inc - sum;
   __syncthreads();
-  if (all <= a.max_steps) return all;
-  if (blockIdx.x == 0 && tid == 0) record_error(a.status, a.steps_error, 87, 0);
-  return 0;
+  return all;
 }
 
 // The place of step `first`, one of those counted.
@@ -710,7 +708,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   static_assert(sizeof(Seq) * kThreads <= 8192, "the rings hold the sequences");
   wait_for_dependency();
   const int64_t total = total_steps(a, tile, step, start, seqs);
-  const int64_t share = (total + workers - 1) / workers;
+  const int64_t share = total > a.max_steps ? 0 : (total + workers - 1) / workers;
+  if (rare(share == 0) && total > 0 && threadIdx.x == 0) record_error(a.status, a.steps_error, 87, 0);
   const int64_t first = me * share, last = min(first + share, total);  // this worker's run [first, last)
   if (tid == 0) left[in_cta] = Left{};
   constexpr int ring_bytes = kStages * 8192 * WM;
