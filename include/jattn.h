@@ -89,7 +89,8 @@ enum {
                                 jattn_decode has more work than it can count */
   JATTN_ERR_ROPE = 9,        /* device: a rotary position at or beyond the cos/sin tables' rows */
   JATTN_ERR_PAGES = 10,      /* device: a page table entry that is no page of the cache */
-  JATTN_ERR_LENGTH = 11      /* device: a cached length or position outside its sequence's pages */
+  JATTN_ERR_LENGTH = 11,     /* device: a cached length or position outside its sequence's pages */
+  JATTN_ERR_POOL = 12        /* device: a page pool with fewer free pages than a call needs, or no room for those it returns */
 };
 
 typedef struct {
@@ -417,6 +418,174 @@ int jattn_decode_scratch_size(const jattn_params_t* p, const jattn_cache_t* cach
 int jattn_decode(const jattn_params_t* p, const jattn_cache_t* cache, const int64_t* q_off, const int64_t* kv_lens,
                  const int32_t* page_table, int64_t max_pages, const uint16_t* q, uint16_t* o, float* lse,
                  void* scratch, size_t scratch_bytes, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Rows on their way to attention. No counterpart in the pages beyond naming the
+ * query/key normalisation that bounds the scores of JATTN_GELU_POLY: these calls
+ * prepare query and key rows (and rows of a model's width) for it.
+ *
+ * Row tensors are [rows, heads, N] device arrays of `type` with strides in
+ * elements: value (r, h, c) lies at r * row_stride + h * head_stride + c, so a view
+ * of a fused projection is one. Strides of inputs may be anything >= 0 (0: a row
+ * that is broadcast); rows of an output must not overlap each other. rows * heads
+ * < 2^31. Pointers are aligned to their elements; where pointers, strides and N are
+ * multiples of 16 bytes rows move in vectors, else value by value, with the same
+ * results up to the order of sums.
+ *
+ * live_rows (device int64, NULL: all rows): rows at and behind *live_rows are
+ * padding (a batch's last offset is passed here), which takes no part. Their rows in
+ * the outputs are left as they were, or set to zero with zero_behind. A value outside
+ * [0, rows] sets JATTN_ERR_OFFSETS and counts as 0 or as rows. workspace: 256 bytes,
+ * the status word alone, as for the paged cache. */
+enum { JATTN_F32 = 0, JATTN_BF16 = 1, JATTN_F16 = 2 };
+
+typedef struct {
+  int64_t rows;       /* >= 0 */
+  int heads;          /* >= 1 */
+  int N;              /* values of a row: 1 .. 16384 */
+  int type;           /* of x, y, dy and dx */
+  int weight_type;    /* of weight, bias and their gradients: `type` or JATTN_F32 */
+  float eps;          /* > 0 and finite (forward only) */
+  int zero_behind;    /* 0 / 1 */
+} jattn_norm_t;
+
+/* Layer norm of every row: with m = mean(x) and v = mean((x - m)^2),
+ *   rstd = 1 / sqrt(v + eps),  y = (x - m) rstd weight + bias.
+ * weight and bias [N] (NULL: ones, zeros; a bias needs a weight). mean and rstd
+ * fp32 [rows, heads] are written for the backward unless NULL (both). Sums are held
+ * in fp32 about the row's mean, and y is rounded once. y may be x itself (the same
+ * pointer and strides); any other overlap of an output is refused
+ * (JATTN_ERR_INVALID). */
+int jattn_layer_norm(const jattn_norm_t* p, const int64_t* live_rows, const void* x, int64_t x_row_stride,
+                     int64_t x_head_stride, const void* weight, const void* bias, void* y, int64_t y_row_stride,
+                     int64_t y_head_stride, float* mean, float* rstd, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+/* Its backward: with g = dy weight, h = (x - mean) rstd (the forward's statistics),
+ *   dx = rstd (g - mean(g) - h mean(g h)),
+ *   dweight = sum over all rows of dy h,  dbias = sum over all rows of dy,
+ * the sums in fp32, in an order that depends on the sizes and the GPU alone, and
+ * rounded once to weight_type. dweight needs weight and dbias needs dweight; either may
+ * be NULL. dx may be dy or x itself (the same pointer and strides). scratch: jattn_layer_norm_bwd_scratch_size bytes (0 without
+ * dweight), 256-byte aligned, of any content; calls that run at the same time need
+ * one each. The size depends on rows, heads, N and type, and is asked for with the
+ * device current that the call runs on. Without rows dweight and dbias are zero. */
+int jattn_layer_norm_bwd_scratch_size(const jattn_norm_t* p, size_t* bytes);
+int jattn_layer_norm_bwd(const jattn_norm_t* p, const int64_t* live_rows, const void* dy, int64_t dy_row_stride,
+                         int64_t dy_head_stride, const void* x, int64_t x_row_stride, int64_t x_head_stride,
+                         const void* weight, const float* mean, const float* rstd, void* dx, int64_t dx_row_stride,
+                         int64_t dx_head_stride, void* dweight, void* dbias, void* scratch, size_t scratch_bytes,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Rotary positions of rows in either layout, for all columns of a head or its
+ * first ones. With R = 2 * half <= D, c and s row pos of the tables
+ * (fp32 [table_rows, half], 4-byte aligned) and pair m < half the columns
+ *   JATTN_ROTARY_INTERLEAVED  a = x[2m], b = x[2m + 1] (jattn_rope's pairs)
+ *   JATTN_ROTARY_HALF         a = x[m],  b = x[m + half]
+ * y holds a c[m] - b s[m] and a s[m] + b c[m] in their places (`inverse`: with -s, the
+ * transposed rotation, which is the gradient's), computed in fp32 and rounded once,
+ * and columns R .. D-1 as they are in x.
+ *
+ * Positions. off (device int64 [B+1], prefix sums within total rows): row i of
+ * sequence b stands at start[b] + i (start: device int64 [B], NULL: zeros); rows at
+ * and behind off[B] are padding. off NULL: row r stands at start[r] (B == total; start
+ * NULL: at r). A negative start marks rows that are skipped as padding is: left as
+ * they were in y, or set to zero with zero_behind. Offsets that are no prefix sums
+ * set JATTN_ERR_OFFSETS and their rows are skipped; a position at or beyond
+ * table_rows sets JATTN_ERR_ROPE and its row is copied unrotated. y may be x itself
+ * (the same pointer and strides); any other overlap is refused. */
+enum { JATTN_ROTARY_INTERLEAVED = 0, JATTN_ROTARY_HALF = 1 };
+
+typedef struct {
+  int64_t B;          /* sequences (off NULL: total) */
+  int64_t total;      /* rows */
+  int heads;          /* >= 1 */
+  int D;              /* columns of a head: 2 .. 16384 */
+  int half;           /* pairs: 1 .. D / 2 */
+  int type;           /* JATTN_F32 / BF16 / F16 */
+  int layout;         /* JATTN_ROTARY_* */
+  int inverse;        /* 0 / 1 */
+  int zero_behind;    /* 0 / 1 */
+} jattn_rotary_t;
+
+int jattn_rotary(const jattn_rotary_t* p, const int64_t* off, const int64_t* start, const float* cos, const float* sin,
+                 int64_t table_rows, const void* x, int64_t x_row_stride, int64_t x_head_stride, void* y,
+                 int64_t y_row_stride, int64_t y_head_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The tables: cos and sin (fp32 [rows, half], 4-byte aligned) of amplitude * (pos *
+ * theta_m) for pos = first .. first + rows - 1 and m < half, R = 2 * half.
+ *   JATTN_SCALE_NONE    theta_m = base^(-2m / R), amplitude 1
+ *   JATTN_SCALE_LINEAR  theta_m / factor (positions interpolated)
+ *   JATTN_SCALE_NTK     base * factor^(R / (R - 2)) in place of base (half >= 2)
+ *   JATTN_SCALE_YARN    (1 - k) theta_m / factor + k theta_m, where k rises from 0 to 1
+ *                       as the turns original * theta_m / 2 pi of the original context
+ *                       go from beta_slow to beta_fast (Peng et al. 2023, "YaRN"),
+ *                       amplitude 0.1 ln(factor) + 1
+ * theta_m is formed on the host in 64 bits and becomes a 64-bit fraction of a turn per
+ * position; multiples wrap exactly, so far positions keep their accuracy (theta's
+ * own 2^-53 times the position). Values are within 2^-22 amplitude of the exact ones
+ * for positions up to 2^24. rows * half < 2^40. */
+enum { JATTN_SCALE_NONE = 0, JATTN_SCALE_LINEAR = 1, JATTN_SCALE_NTK = 2, JATTN_SCALE_YARN = 3 };
+
+typedef struct {
+  int64_t first;      /* >= 0; first + rows <= 2^31 */
+  int64_t rows;       /* >= 0 */
+  int half;           /* 1 .. 512 */
+  int scaling;        /* JATTN_SCALE_* */
+  double base;        /* > 1 */
+  double factor;      /* >= 1; not read without scaling */
+  double original;    /* YARN: the context that the model was trained on, > 0 */
+  double beta_fast;   /* YARN: > beta_slow >= 0 */
+  double beta_slow;
+} jattn_rotary_tables_t;
+
+int jattn_rotary_tables(const jattn_rotary_tables_t* p, float* cos, float* sin, void* stream);
+
+/* Pages on the GPU: a pool of free pages and the page tables and slots that
+ * requests get from it, without a host round trip. free_pages (device int32
+ * [n_pages]) is a stack of page numbers and *count (device int64) its height; entries
+ * at and above it are not read. A call's calls on one pool are ordered by the
+ * caller (one stream, or events), as those on a cache are.
+ *
+ * jattn_page_assign makes the page table hold rows start[b] .. start[b] + n(b) - 1 of
+ * every sequence, n(b) = off[b+1] - off[b] (off NULL: one row each, total == B): the
+ * first ceil(start[b] / page_size) pages are there already, and each one that is missing
+ * comes from the top of the stack, sequence by sequence in ascending order. A
+ * negative start skips its sequence. slots (device int64 [total], NULL: not wanted):
+ * page * page_size + pos % page_size of each new row, -1 of rows without a page. Rows at
+ * and behind off[B] get -1. What the status word says, and what then happens:
+ *   JATTN_ERR_OFFSETS  offsets that are no prefix sums: those sequences are skipped
+ *   JATTN_ERR_LENGTH   more rows than the table's max_pages hold: the sequence is skipped
+ *   JATTN_ERR_POOL     fewer free pages than the call needs (or a count outside
+ *                      [0, n_pages]): no page is assigned, all slots are -1
+ *   JATTN_ERR_PAGES    a slot's or a free page's number outside [0, n_pages): -1 in its place
+ *
+ * jattn_page_release gives back the pages ceil(keep[b] / page_size) .. ceil(lens[b] /
+ * page_size) - 1 of every sequence that shrinks from lens[b] to keep[b] rows (keep NULL: 0;
+ * a negative lens or keep skips it, and one that does not shrink gives nothing) and
+ * sets their table entries to -1. They are pushed so that the first sequence's first
+ * page is on top: releasing what was just assigned restores the stack. A sequence whose
+ * pages do not fit the table (JATTN_ERR_LENGTH) or that holds an entry which is no
+ * page (JATTN_ERR_PAGES) keeps all it has. More pages than the pool has room for set
+ * JATTN_ERR_POOL, and none is given back. A page that several sequences share is given
+ * back once, by the caller's care.
+ *
+ * page_size: a power of two from 1 to 4096; max_pages * page_size < 2^31. scratch:
+ * jattn_page_scratch_size bytes, 256-byte aligned, of any content, one per call that
+ * may run at the same time. workspace as for the paged cache. Buffers must not overlap. */
+typedef struct {
+  int64_t n_pages;    /* 1 .. 2^31 - 1 */
+  int page_size;
+  int32_t* free_pages;
+  int64_t* count;
+} jattn_page_pool_t;
+
+int jattn_page_scratch_size(int64_t B, size_t* bytes);
+int jattn_page_assign(const jattn_page_pool_t* pool, int64_t B, int64_t total, const int64_t* off, const int64_t* start,
+                      int32_t* page_table, int64_t max_pages, int64_t* slots, void* scratch, size_t scratch_bytes,
+                      void* workspace, size_t workspace_bytes, void* stream);
+int jattn_page_release(const jattn_page_pool_t* pool, int64_t B, const int64_t* lens, const int64_t* keep,
+                       int32_t* page_table, int64_t max_pages, void* scratch, size_t scratch_bytes, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 /* Longest-first tile schedule ("GEM Training" post, GDPA section: valid tiles
  * are precomputed, empty ones skipped, and the rest spread over the SMs so

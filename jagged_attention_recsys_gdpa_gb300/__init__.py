@@ -16,7 +16,10 @@ the computation runs in its CUDA kernels):
   the softmax forward on such operands (block-scaled FP8 tensor-core products).
 * ``schedule(...)``: the device-built longest-first tile list.
 * ``paged_cache``, ``cache_append``, ``cache_read``, ``decode``: a paged
-  key/value cache for serving and the attention of new rows over it (``paged``).
+  key/value cache for serving and the attention of new rows over it (``paged``);
+  ``page_pool``, ``page_assign``, ``page_release``: its page tables, kept on the GPU.
+* ``layer_norm``, ``rotary``, ``rotary_tables``: query/key norm (and rows of a
+  model's width) and rotary positions in either layout, with autograd (``rows``).
 
 Activations (``act``): "softmax", "silu", "gelu" (tanh form) or "gelu_poly"
 (its degree-6 Taylor polynomial on the FMA pipe, for |scores| <= 1).
@@ -278,7 +281,7 @@ def schedule(q_off, kv_off, H, D=128, causal=False, window=0, row_tile=128, col_
 
 def device_status(device=None) -> int:
     """Read and clear the device's status words: the cached workspace's and, if
-    that is clean, the paged-cache operators' (syncs)."""
+    that is clean, the paged-cache and row operators' (syncs)."""
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     key = dev.index if dev.index is not None else torch.cuda.current_device()
     code = 0
@@ -288,4 +291,6 @@ def device_status(device=None) -> int:
     return code
 
 
-from .paged import PagedCache, _status_blocks, cache_append, cache_read, decode, paged_cache  # noqa: E402
+from .paged import (PagedCache, PagePool, _status_blocks, cache_append, cache_read, decode, page_assign,  # noqa: E402
+                    page_pool, page_release, paged_cache)
+from .rows import layer_norm, layer_norm_backward, layer_norm_forward, rotary, rotary_tables  # noqa: E402

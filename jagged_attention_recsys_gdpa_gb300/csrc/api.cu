@@ -16,6 +16,8 @@
 #include "cache.cuh"
 #include "common.cuh"
 #include "kernels.h"
+#include "pages.cuh"
+#include "rows.cuh"
 #include "sched.h"
 
 namespace jattn {
@@ -1104,6 +1106,379 @@ int jattn_schedule(const jattn_params_t* p, const int64_t* q_off, const int64_t*
   return JATTN_OK;
 }
 
+namespace jattn {
+namespace {
+
+constexpr int kMaxRow = 16384;  // values of a layer norm's row, columns of a rotary head
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+
+bool known_type(int t) { return t == JATTN_F32 || t == JATTN_BF16 || t == JATTN_F16; }
+int type_bytes(int t) { return t == JATTN_F32 ? 4 : 2; }
+
+// Memory that a call reads or writes: `bytes` from p on.
+struct Piece {
+  const void* p;
+  int64_t bytes;
+};
+
+// A row tensor [rows, heads, n] of values of `size` bytes as the caller describes it.
+struct RowTensor {
+  const void* p;
+  int64_t row, head;  // strides in values
+};
+
+bool bad_strides(const RowTensor& t) {
+  return t.row < 0 || t.head < 0 || t.row > kMaxStride || t.head > kMaxStride;
+}
+Piece piece(const RowTensor& t, int64_t rows, int64_t heads, int64_t n, int size) {
+  return rows < 1 ? Piece{t.p, 0} : Piece{t.p, ((rows - 1) * t.row + (heads - 1) * t.head + n) * size};
+}
+// Whether rows of an output share memory: one of the strides has to pass over all that the other one spans.
+bool rows_overlap(const RowTensor& t, int64_t rows, int64_t heads, int64_t n) {
+  if (rows < 1) return false;
+  const bool by_head = heads == 1 || t.head >= n, by_row = rows == 1 || t.row >= n;
+  if (!by_head || !by_row) return true;
+  return heads > 1 && rows > 1 && t.row < (heads - 1) * t.head + n && t.head < (rows - 1) * t.row + n;
+}
+bool same_place(const RowTensor& a, const RowTensor& b) { return a.p == b.p && a.row == b.row && a.head == b.head; }
+bool meet(const Piece& a, const Piece& b) { return a.p && b.p && a.bytes > 0 && b.bytes > 0 && overlap(a.p, a.bytes, b.p, b.bytes); }
+bool meet_any(const Piece& a, std::initializer_list<Piece> others) {
+  for (const Piece& b : others)
+    if (meet(a, b)) return true;
+  return false;
+}
+// Rows of n values that move in vectors of 16 bytes.
+bool in_vectors(const RowTensor& t, int64_t rows, int64_t heads, int64_t n, int size) {
+  return aligned16(t.p) && (rows == 1 || t.row * size % 16 == 0) && (heads == 1 || t.head * size % 16 == 0) &&
+         n * size % 16 == 0;
+}
+bool to_elements(const void* p, int size) { return reinterpret_cast<uintptr_t>(p) % size == 0; }
+
+int check_norm(const jattn_norm_t* p) {
+  if (!p || p->rows < 0 || p->heads < 1 || p->N < 1 || p->N > kMaxRow) return JATTN_ERR_INVALID;
+  if (p->rows > INT32_MAX || p->rows * p->heads > INT32_MAX) return JATTN_ERR_INVALID;
+  if (!known_type(p->type) || (p->weight_type != p->type && p->weight_type != JATTN_F32)) return JATTN_ERR_INVALID;
+  if (p->zero_behind != 0 && p->zero_behind != 1) return JATTN_ERR_INVALID;
+  return JATTN_OK;
+}
+
+// What both directions share; x, dy (null: forward) and y (backward: dx) as the caller gave them.
+NormArgs norm_args(const jattn_norm_t& p, const int64_t* live, const RowTensor& x, const RowTensor& dy, const RowTensor& y,
+                   const void* weight, const void* bias, void* ws, bool* vectors) {
+  const int size = type_bytes(p.type);
+  NormArgs a{};
+  a.x = RowsIn{x.p, x.row, x.head};
+  a.dy = RowsIn{dy.p, dy.row, dy.head};
+  a.y = RowsOut{const_cast<void*>(y.p), y.row, y.head};
+  a.w = weight;
+  a.b = bias;
+  a.live = live;
+  a.rows = p.rows;
+  a.heads = p.heads;
+  a.N = p.N;
+  a.eps = p.eps;
+  a.wide_weight = p.weight_type == JATTN_F32;
+  a.zero_behind = p.zero_behind != 0;
+  a.status = static_cast<DevStatus*>(ws);
+  // where a row's stride is all its heads' the rows of all heads follow each other by the head's
+  const auto even = [&](const RowTensor& t) { return !t.p || t.row == p.heads * t.head; };
+  a.split = p.heads;
+  if (even(x) && even(dy) && even(y)) {
+    a.split = 1;
+    a.x.row = x.head;
+    a.dy.row = dy.head;
+    a.y.row = y.head;
+  }
+  *vectors = in_vectors(x, p.rows, p.heads, p.N, size) && in_vectors(y, p.rows, p.heads, p.N, size) &&
+             (!dy.p || in_vectors(dy, p.rows, p.heads, p.N, size)) && aligned16(weight) && aligned16(bias);
+  return a;
+}
+
+}  // namespace
+}  // namespace jattn
+
+int jattn_layer_norm(const jattn_norm_t* p, const int64_t* live_rows, const void* xp, int64_t x_row, int64_t x_head,
+                     const void* weight, const void* bias, void* yp, int64_t y_row, int64_t y_head, float* mean,
+                     float* rstd, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_norm(p);
+  if (rc != JATTN_OK) return rc;
+  if (!(p->eps > 0.0f) || !std::isfinite(p->eps)) return JATTN_ERR_INVALID;
+  const RowTensor x{xp, x_row, x_head}, y{yp, y_row, y_head};
+  if ((p->rows > 0 && (!xp || !yp)) || (bias && !weight) || !mean != !rstd) return JATTN_ERR_INVALID;
+  if (bad_strides(x) || bad_strides(y) || rows_overlap(y, p->rows, p->heads, p->N)) return JATTN_ERR_INVALID;
+  const int size = type_bytes(p->type), wsize = type_bytes(p->weight_type);
+  if (!to_elements(xp, size) || !to_elements(yp, size) || !to_elements(weight, wsize) || !to_elements(bias, wsize) ||
+      misplaced({live_rows}, {mean, rstd}))
+    return JATTN_ERR_ALIGN;
+  if ((rc = check_status_ws(ws, ws_bytes)) != JATTN_OK) return rc;
+  const Piece in = piece(x, p->rows, p->heads, p->N, size), out = piece(y, p->rows, p->heads, p->N, size);
+  const Piece m{mean, p->rows * p->heads * 4}, r{rstd, p->rows * p->heads * 4}, lr{live_rows, 8};
+  const Piece w{weight, int64_t(p->N) * wsize}, b{bias, int64_t(p->N) * wsize};
+  if ((meet(out, in) && !same_place(x, y)) || meet_any(out, {w, b, m, r, lr}) || meet_any(m, {in, w, b, r, lr}) ||
+      meet_any(r, {in, w, b, lr}))
+    return JATTN_ERR_INVALID;
+  DeviceInfo dev;
+  if ((rc = device_info(dev)) != JATTN_OK) return rc;
+  clear_stale_error();
+  if (p->rows == 0) return JATTN_OK;
+  bool vectors;
+  NormArgs a = norm_args(*p, live_rows, x, RowTensor{}, y, weight, bias, ws, &vectors);
+  a.mean = mean;
+  a.rstd = rstd;
+  const cudaError_t e = launch_norm(p->type, vectors, a, dev.sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? JATTN_OK : cuda_fail("layer norm launch", e);
+}
+
+int jattn_layer_norm_bwd_scratch_size(const jattn_norm_t* p, size_t* bytes) {
+  if (!bytes) return JATTN_ERR_INVALID;
+  int rc = check_norm(p);
+  if (rc != JATTN_OK) return rc;
+  DeviceInfo dev;
+  if ((rc = device_info(dev)) != JATTN_OK) return rc;
+  // the two widths of access take grids of their own
+  const int parts = std::max(norm_bwd_parts(p->type, true, p->rows * p->heads, p->N, dev.sms),
+                             norm_bwd_parts(p->type, false, p->rows * p->heads, p->N, dev.sms));
+  *bytes = al256(static_cast<size_t>(parts) * 2 * p->N * sizeof(float));
+  return JATTN_OK;
+}
+
+int jattn_layer_norm_bwd(const jattn_norm_t* p, const int64_t* live_rows, const void* dyp, int64_t dy_row,
+                         int64_t dy_head, const void* xp, int64_t x_row, int64_t x_head, const void* weight,
+                         const float* mean, const float* rstd, void* dxp, int64_t dx_row, int64_t dx_head,
+                         void* dweight, void* dbias, void* scratch, size_t scratch_bytes, void* ws, size_t ws_bytes,
+                         void* stream) {
+  int rc = check_norm(p);
+  if (rc != JATTN_OK) return rc;
+  const RowTensor x{xp, x_row, x_head}, dy{dyp, dy_row, dy_head}, dx{dxp, dx_row, dx_head};
+  if (p->rows > 0 && (!xp || !dyp || !dxp || !mean || !rstd)) return JATTN_ERR_INVALID;
+  if ((dweight && !weight) || (dbias && !dweight)) return JATTN_ERR_INVALID;
+  if (bad_strides(x) || bad_strides(dy) || bad_strides(dx) || rows_overlap(dx, p->rows, p->heads, p->N))
+    return JATTN_ERR_INVALID;
+  const int size = type_bytes(p->type), wsize = type_bytes(p->weight_type);
+  if (!to_elements(xp, size) || !to_elements(dyp, size) || !to_elements(dxp, size) || !to_elements(weight, wsize) ||
+      !to_elements(dweight, wsize) || !to_elements(dbias, wsize) || misplaced({live_rows}, {mean, rstd}))
+    return JATTN_ERR_ALIGN;
+  if ((rc = check_status_ws(ws, ws_bytes)) != JATTN_OK) return rc;
+  DeviceInfo dev;
+  if ((rc = device_info(dev)) != JATTN_OK) return rc;
+  size_t need = 0;
+  if (dweight) {
+    if ((rc = jattn_layer_norm_bwd_scratch_size(p, &need)) != JATTN_OK) return rc;
+    if (need > 0 && (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) || scratch_bytes < need))
+      return JATTN_ERR_WORKSPACE;
+  }
+  const Piece in = piece(x, p->rows, p->heads, p->N, size), grad = piece(dy, p->rows, p->heads, p->N, size);
+  const Piece out = piece(dx, p->rows, p->heads, p->N, size);
+  const Piece m{mean, p->rows * p->heads * 4}, r{rstd, p->rows * p->heads * 4}, lr{live_rows, 8};
+  const Piece w{weight, int64_t(p->N) * wsize}, dw{dweight, int64_t(p->N) * wsize}, db{dbias, int64_t(p->N) * wsize};
+  const Piece sc{scratch, static_cast<int64_t>(need)};
+  if ((meet(out, in) && !same_place(x, dx)) || (meet(out, grad) && !same_place(dy, dx)) ||
+      meet_any(out, {w, m, r, lr, dw, db, sc}) || meet_any(dw, {in, grad, w, m, r, lr, db, sc}) ||
+      meet_any(db, {in, grad, w, m, r, lr, sc}) || meet_any(sc, {in, grad, w, m, r, lr}))
+    return JATTN_ERR_INVALID;
+  clear_stale_error();
+  bool vectors;
+  NormArgs a = norm_args(*p, live_rows, x, dy, dx, weight, nullptr, ws, &vectors);
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.partial = dweight ? static_cast<float*>(scratch) : nullptr;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (p->rows > 0) {
+    const cudaError_t e = launch_norm_bwd(p->type, vectors, a, dev.sms, st);
+    if (e != cudaSuccess) return cuda_fail("layer norm backward launch", e);
+  }
+  if (!dweight) return JATTN_OK;
+  const int parts = p->rows > 0 ? norm_bwd_parts(p->type, vectors, p->rows * p->heads, p->N, dev.sms) : 0;
+  const NormJoinArgs j{a.partial, dweight, dbias, parts, p->N};
+  const cudaError_t e = launch_norm_join(p->weight_type, j, st);
+  return e == cudaSuccess ? JATTN_OK : cuda_fail("layer norm gradient launch", e);
+}
+
+int jattn_rotary(const jattn_rotary_t* p, const int64_t* off, const int64_t* start, const float* cos, const float* sin,
+                 int64_t table_rows, const void* xp, int64_t x_row, int64_t x_head, void* yp, int64_t y_row,
+                 int64_t y_head, void* ws, size_t ws_bytes, void* stream) {
+  if (!p || p->total < 0 || p->total > INT32_MAX || p->heads < 1 || p->D < 2 || p->D > kMaxRow) return JATTN_ERR_INVALID;
+  if (p->half < 1 || p->half > p->D / 2 || !known_type(p->type)) return JATTN_ERR_INVALID;
+  if (off ? p->B < 1 || p->B > INT32_MAX : p->B != p->total) return JATTN_ERR_INVALID;
+  if (static_cast<int64_t>(p->heads) * p->D > (1 << 30)) return JATTN_ERR_INVALID;
+  if ((p->layout != JATTN_ROTARY_INTERLEAVED && p->layout != JATTN_ROTARY_HALF) || (p->inverse != 0 && p->inverse != 1) ||
+      (p->zero_behind != 0 && p->zero_behind != 1))
+    return JATTN_ERR_INVALID;
+  if (!cos || !sin || table_rows < 1 || table_rows > INT32_MAX) return JATTN_ERR_INVALID;
+  const RowTensor x{xp, x_row, x_head}, y{yp, y_row, y_head};
+  if ((p->total > 0 && (!xp || !yp)) || bad_strides(x) || bad_strides(y) || rows_overlap(y, p->total, p->heads, p->D))
+    return JATTN_ERR_INVALID;
+  const int size = type_bytes(p->type);
+  if (!to_elements(xp, size) || !to_elements(yp, size) || misplaced({off, start}, {cos, sin})) return JATTN_ERR_ALIGN;
+  int rc = check_status_ws(ws, ws_bytes);
+  if (rc != JATTN_OK) return rc;
+  const Piece in = piece(x, p->total, p->heads, p->D, size), out = piece(y, p->total, p->heads, p->D, size);
+  const int64_t table = table_rows * p->half * 4;
+  if ((meet(out, in) && !same_place(x, y)) ||
+      meet_any(out, {Piece{cos, table}, Piece{sin, table}, Piece{off, (p->B + 1) * 8}, Piece{start, p->B * 8}}))
+    return JATTN_ERR_INVALID;
+  DeviceInfo dev;
+  if ((rc = device_info(dev)) != JATTN_OK) return rc;
+  clear_stale_error();
+  if (p->total == 0) return JATTN_OK;
+  RotaryArgs a{};
+  a.x = RowsIn{xp, x_row, x_head};
+  a.y = RowsOut{yp, y_row, y_head};
+  a.off = off;
+  a.start = start;
+  a.cos_t = cos;
+  a.sin_t = sin;
+  a.B = p->B;
+  a.total = p->total;
+  a.table_rows = table_rows;
+  a.heads = p->heads;
+  a.D = p->D;
+  a.half = p->half;
+  a.inverse = p->inverse != 0;
+  a.zero_behind = p->zero_behind != 0;
+  a.status = static_cast<DevStatus*>(ws);
+  // units of whole vectors: the pairs' and the copied columns'
+  const bool vectors = in_vectors(x, p->total, p->heads, p->D, size) && in_vectors(y, p->total, p->heads, p->D, size) &&
+                       p->half * size % 16 == 0 && aligned16(cos) && aligned16(sin);
+  const cudaError_t e = launch_rotary(p->type, vectors, p->layout == JATTN_ROTARY_HALF, a, dev.sms,
+                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? JATTN_OK : cuda_fail("rotary positions launch", e);
+}
+
+int jattn_rotary_tables(const jattn_rotary_tables_t* p, float* cos, float* sin, void* stream) {
+  if (!p || p->first < 0 || p->rows < 0 || p->half < 1 || p->half > 512) return JATTN_ERR_INVALID;
+  if (p->first > (int64_t(1) << 31) || p->rows > (int64_t(1) << 31) - p->first) return JATTN_ERR_INVALID;
+  if (!(p->base > 1.0) || !std::isfinite(p->base)) return JATTN_ERR_INVALID;
+  const bool scaled = p->scaling != JATTN_SCALE_NONE;
+  if (p->scaling < JATTN_SCALE_NONE || p->scaling > JATTN_SCALE_YARN) return JATTN_ERR_INVALID;
+  if (scaled && (!(p->factor >= 1.0) || !std::isfinite(p->factor))) return JATTN_ERR_INVALID;
+  if (p->scaling == JATTN_SCALE_NTK && p->half < 2) return JATTN_ERR_INVALID;
+  if (p->scaling == JATTN_SCALE_YARN &&
+      (!(p->original > 0.0) || !std::isfinite(p->original) || !(p->beta_slow >= 0.0) || !(p->beta_fast > p->beta_slow) ||
+       !std::isfinite(p->beta_fast)))
+    return JATTN_ERR_INVALID;
+  if (p->rows > 0 && (!cos || !sin)) return JATTN_ERR_INVALID;
+  if (misplaced({}, {cos, sin})) return JATTN_ERR_ALIGN;
+  const int64_t bytes = p->rows * p->half * 4;
+  if (meet(Piece{cos, bytes}, Piece{sin, bytes})) return JATTN_ERR_INVALID;
+  DeviceInfo dev;
+  const int rc = device_info(dev);
+  if (rc != JATTN_OK) return rc;
+  clear_stale_error();
+  if (p->rows == 0) return JATTN_OK;
+  constexpr double kTwoPi = 6.283185307179586476925;
+  const double R = 2.0 * p->half;
+  const double base = p->scaling == JATTN_SCALE_NTK ? p->base * std::pow(p->factor, R / (R - 2.0)) : p->base;
+  if (!std::isfinite(base)) return JATTN_ERR_INVALID;
+  RotaryTablesArgs a;
+  for (int m = 0; m < p->half; ++m) {
+    double theta = std::pow(base, -2.0 * m / R);
+    if (p->scaling == JATTN_SCALE_LINEAR) theta /= p->factor;
+    if (p->scaling == JATTN_SCALE_YARN) {
+      const double turns = p->original * theta / kTwoPi;
+      const double k = std::min(1.0, std::max(0.0, (turns - p->beta_slow) / (p->beta_fast - p->beta_slow)));
+      theta = (1.0 - k) * theta / p->factor + k * theta;
+    }
+    a.turn[m] = static_cast<uint64_t>(std::ldexp(theta / kTwoPi, 64));  // theta <= 1: below 2^62
+  }
+  a.cos_t = cos;
+  a.sin_t = sin;
+  a.first = p->first;
+  a.rows = p->rows;
+  a.half = p->half;
+  a.amplitude = p->scaling == JATTN_SCALE_YARN ? static_cast<float>(0.1 * std::log(p->factor) + 1.0) : 1.0f;
+  const bool vectors = p->half % 4 == 0 && aligned16(cos) && aligned16(sin);
+  const cudaError_t e = launch_rotary_tables(a, vectors, dev.sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? JATTN_OK : cuda_fail("rotary tables launch", e);
+}
+
+int jattn_page_scratch_size(int64_t B, size_t* bytes) {
+  if (!bytes || B < 1 || B > INT32_MAX) return JATTN_ERR_INVALID;
+  *bytes = al256(page_scratch_bytes(B));
+  return JATTN_OK;
+}
+
+namespace jattn {
+namespace {
+
+// What assigning and giving back check alike; index: what the call reads of 64-bit numbers besides.
+int check_pool(const jattn_page_pool_t* pool, int64_t B, std::initializer_list<Piece> index, int32_t* table,
+               int64_t max_pages, void* scratch, size_t scratch_bytes, void* ws, size_t ws_bytes) {
+  if (!pool || pool->n_pages < 1 || pool->n_pages > INT32_MAX || !pool->free_pages || !pool->count) return JATTN_ERR_INVALID;
+  const int ps = pool->page_size;
+  if (ps < 1 || ps > 4096 || (ps & (ps - 1))) return JATTN_ERR_INVALID;
+  if (B < 1 || B > INT32_MAX || !table || max_pages < 1 || max_pages > INT32_MAX / ps) return JATTN_ERR_INVALID;
+  if (misplaced({pool->count}, {pool->free_pages, table})) return JATTN_ERR_ALIGN;
+  for (const Piece& i : index)
+    if (misplaced({i.p}, {})) return JATTN_ERR_ALIGN;
+  const int rc = check_status_ws(ws, ws_bytes);
+  if (rc != JATTN_OK) return rc;
+  size_t need = 0;
+  (void)jattn_page_scratch_size(B, &need);
+  if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) || scratch_bytes < need) return JATTN_ERR_WORKSPACE;
+  const Piece f{pool->free_pages, pool->n_pages * 4}, c{pool->count, 8}, t{table, B * max_pages * 4},
+      s{scratch, static_cast<int64_t>(need)};
+  if (meet(f, c) || meet(f, t) || meet(f, s) || meet(c, t) || meet(c, s) || meet(t, s)) return JATTN_ERR_INVALID;
+  for (const Piece& i : index)
+    if (meet_any(i, {f, c, t, s})) return JATTN_ERR_INVALID;
+  return JATTN_OK;
+}
+
+PageArgs page_args(const jattn_page_pool_t& pool, int64_t B, int32_t* table, int64_t max_pages, void* scratch, void* ws) {
+  PageArgs a{};
+  a.free_pages = pool.free_pages;
+  a.count = pool.count;
+  a.table = table;
+  a.n_pages = pool.n_pages;
+  a.B = B;
+  a.max_pages = max_pages;
+  a.page_size = pool.page_size;
+  while ((1 << a.page_shift) < pool.page_size) ++a.page_shift;
+  a.scratch = scratch;
+  a.status = static_cast<DevStatus*>(ws);
+  return a;
+}
+
+}  // namespace
+}  // namespace jattn
+
+int jattn_page_assign(const jattn_page_pool_t* pool, int64_t B, int64_t total, const int64_t* off, const int64_t* start,
+                      int32_t* page_table, int64_t max_pages, int64_t* slots, void* scratch, size_t scratch_bytes,
+                      void* ws, size_t ws_bytes, void* stream) {
+  if (!start || total < 0 || total > INT32_MAX || (!off && total != B)) return JATTN_ERR_INVALID;
+  const Piece o{off, (B + 1) * 8}, st{start, B * 8}, sl{slots, total * 8};
+  int rc = check_pool(pool, B, {o, st, sl}, page_table, max_pages, scratch, scratch_bytes, ws, ws_bytes);
+  if (rc != JATTN_OK) return rc;
+  if (meet(sl, o) || meet(sl, st)) return JATTN_ERR_INVALID;
+  DeviceInfo dev;
+  if ((rc = device_info(dev)) != JATTN_OK) return rc;
+  clear_stale_error();
+  PageArgs a = page_args(*pool, B, page_table, max_pages, scratch, ws);
+  a.off = off;
+  a.start = start;
+  a.slots = slots;
+  a.total = total;
+  const cudaError_t e = launch_page_assign(a, dev.sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? JATTN_OK : cuda_fail("page assign launch", e);
+}
+
+int jattn_page_release(const jattn_page_pool_t* pool, int64_t B, const int64_t* lens, const int64_t* keep,
+                       int32_t* page_table, int64_t max_pages, void* scratch, size_t scratch_bytes, void* ws,
+                       size_t ws_bytes, void* stream) {
+  if (!lens) return JATTN_ERR_INVALID;
+  const Piece l{lens, B * 8}, k{keep, B * 8};
+  int rc = check_pool(pool, B, {l, k}, page_table, max_pages, scratch, scratch_bytes, ws, ws_bytes);
+  if (rc != JATTN_OK) return rc;
+  DeviceInfo dev;
+  if ((rc = device_info(dev)) != JATTN_OK) return rc;
+  clear_stale_error();
+  PageArgs a = page_args(*pool, B, page_table, max_pages, scratch, ws);
+  a.start = lens;
+  a.keep = keep;
+  const cudaError_t e = launch_page_release(a, dev.sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? JATTN_OK : cuda_fail("page release launch", e);
+}
+
 int jattn_get_status(void* ws, void* stream, int* device_status) {
   if (!ws || !device_status) return JATTN_ERR_INVALID;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -1130,6 +1505,7 @@ const char* jattn_error_string(int code) {
     case JATTN_ERR_ROPE: return "a rotary position lies at or beyond the cos/sin tables' rows";
     case JATTN_ERR_PAGES: return "a page table entry is no page of the cache";
     case JATTN_ERR_LENGTH: return "a cached length or position lies outside its sequence's pages";
+    case JATTN_ERR_POOL: return "a page pool has fewer free pages than a call needs, or no room for those it returns";
     default: return "unknown error code";
   }
 }

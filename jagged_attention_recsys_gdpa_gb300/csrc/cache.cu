@@ -34,33 +34,6 @@ constexpr int max_rows(bool mx) { return mx ? 256 : 128; }
 // kernels come to four by themselves.
 constexpr int kCacheCtas = 4;
 
-// The sequence of jagged row r and its index in it: false (nothing to do) for
-// rows behind the last sequence.
-__device__ __forceinline__ bool find_row(const int64_t* off, int64_t B, int64_t r, int64_t& b, int64_t& i) {
-  if (off == nullptr) {  // one row per sequence
-    b = r;
-    i = 0;
-    return r < B;
-  }
-  if (r >= off[B]) return false;
-  // the last b in [0, B) with off[b] <= r: seven probes at a time
-  int64_t lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int64_t step = (hi - lo + 8) >> 3;
-    int64_t below = 0;
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-      const int64_t at = lo + i * step;
-      if (at <= hi && off[at] <= r) below = i;
-    }
-    lo += below * step;
-    hi = min(hi, lo + step - 1);
-  }
-  b = lo;
-  i = r - off[lo];
-  return i >= 0 && r < off[lo + 1];  // false where the offsets are no prefix sums
-}
-
 // Where a jagged row lies in the cache.
 struct Row {
   int64_t at;  // row of the [n_pages * H * page_size, D] view, head 0; negative: none

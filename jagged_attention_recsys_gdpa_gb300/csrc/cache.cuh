@@ -67,6 +67,33 @@ __device__ __forceinline__ void check_offsets(const int64_t* off, int64_t B, int
       record_error(status, JATTN_ERR_OFFSETS, 81, static_cast<int>(b));
 }
 
+// The sequence of jagged row r and its index in it: false (nothing to do) for
+// rows behind the last sequence.
+__device__ __forceinline__ bool find_row(const int64_t* off, int64_t B, int64_t r, int64_t& b, int64_t& i) {
+  if (off == nullptr) {  // one row per sequence
+    b = r;
+    i = 0;
+    return r < B;
+  }
+  if (r >= off[B]) return false;
+  // the last b in [0, B) with off[b] <= r: seven probes at a time
+  int64_t lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int64_t step = (hi - lo + 8) >> 3;
+    int64_t below = 0;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      const int64_t at = lo + i * step;
+      if (at <= hi && off[at] <= r) below = i;
+    }
+    lo += below * step;
+    hi = min(hi, lo + step - 1);
+  }
+  b = lo;
+  i = r - off[lo];
+  return i >= 0 && r < off[lo + 1];  // false where the offsets are no prefix sums
+}
+
 // 2^(e - 127) of an E8M0 exponent; 255 stands for NaN.
 __device__ __forceinline__ float e8m0_value(uint32_t e) {
   return __uint_as_float(e == 255u ? 0x7fc00000u : e == 0u ? 0x00400000u : e << 23);

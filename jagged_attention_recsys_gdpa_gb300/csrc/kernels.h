@@ -12,6 +12,11 @@ struct AttnArgs;
 struct CacheView;
 struct DecodeArgs;
 struct DevStatus;
+struct NormArgs;
+struct NormJoinArgs;
+struct RotaryArgs;
+struct RotaryTablesArgs;
+struct PageArgs;
 
 // Forward: schedule rows are blocks of fwd_rows_per_item() query rows. `split`
 // selects the column-split arrangement of the activation warps (for items that
@@ -125,5 +130,21 @@ void decode_box(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int 
                 int* lines);
 cudaError_t launch_decode(int D, bool mx, DecodeArgs a, const CUtensorMap& k, const CUtensorMap& v, void* scratch,
                           cudaStream_t stream);
+
+// Layer norm (norm.cu, norm_bwd.cu) of JATTN_F32 / BF16 / F16 rows; `vectors`: everything is aligned to 16 bytes (or, the
+// weights, to a vector's values). The backward writes norm_bwd_parts partial rows, which launch_norm_join adds.
+cudaError_t launch_norm(int type, bool vectors, const NormArgs& a, int sms, cudaStream_t stream);
+int norm_bwd_parts(int type, bool vectors, int64_t rows, int N, int sms);
+cudaError_t launch_norm_bwd(int type, bool vectors, const NormArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_norm_join(int weight_type, const NormJoinArgs& a, cudaStream_t stream);
+
+// Rotary positions of rows and their tables (rotary.cu); `vectors`: everything is aligned to 16 bytes.
+cudaError_t launch_rotary(int type, bool vectors, bool half_layout, const RotaryArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_rotary_tables(const RotaryTablesArgs& a, bool vectors, int sms, cudaStream_t stream);
+
+// Page pool (pages.cu).
+size_t page_scratch_bytes(int64_t B);
+cudaError_t launch_page_assign(const PageArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_page_release(const PageArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace jattn

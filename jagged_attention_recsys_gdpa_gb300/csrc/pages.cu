@@ -1,0 +1,279 @@
+// The page pool: pages for new rows and their slots, and pages given back, from request lengths on the GPU.
+//
+// Whole numbers throughout, so each order is fixed: the i-th page that a call wants, sequence by sequence, is the i-th
+// from the top of the stack of free pages, and the i-th that it gives back becomes the i-th from the top. One CTA adds
+// the sequences' counts up (and moves the pool's height); then every page and every row finds its sequence by
+// bisection and needs nothing from the others. Small calls do both in that CTA, with one launch: they are bound by
+// latency. Large ones are bound by the slots' stores, 8 bytes a row.
+#include <algorithm>
+#include <cstdint>
+
+#include "cache.cuh"
+#include "kernels.h"
+#include "pages.cuh"
+#include "rows.cuh"
+
+namespace jattn {
+namespace {
+
+constexpr int kPlanBlock = 1024;
+constexpr int kFillBlock = 256;
+constexpr int kFillRows = 8;  // rows of a thread of the large calls
+
+// What the counts' sum leaves in scratch for the pages and rows: the prefix sums follow it.
+struct Plan {
+  int64_t top;    // height of the stack that pages are taken from, or that the pages given back reach
+  int64_t pages;  // pages that move; 0 where the call is refused
+  int64_t ok;
+};
+constexpr int64_t kPlanBytes = 256;
+__device__ __forceinline__ Plan* plan_of(const PageArgs& a) { return static_cast<Plan*>(a.scratch); }
+__device__ __forceinline__ int64_t* first_of(const PageArgs& a) {
+  return reinterpret_cast<int64_t*>(static_cast<char*>(a.scratch) + kPlanBytes);
+}
+
+__device__ __forceinline__ int64_t pages_for(const PageArgs& a, int64_t rows) {
+  return (rows + a.page_size - 1) >> a.page_shift;
+}
+
+// Table entries [low, high) of sequence b that the call moves; false where it is skipped, with the reason recorded.
+struct Span {
+  int64_t low, high;
+};
+template <bool RELEASE>
+__device__ __forceinline__ bool span_of(const PageArgs& a, int64_t b, Span& e) {
+  e.low = e.high = 0;
+  const int64_t cap = a.max_pages << a.page_shift;
+  int64_t from, to;
+  if constexpr (RELEASE) {
+    from = a.keep != nullptr ? a.keep[b] : 0;
+    to = a.start[b];
+    if (from < 0 || to <= from) return false;
+  } else {
+    from = a.start[b];
+    int64_t n = 1;
+    if (a.off != nullptr) {
+      const int64_t first = a.off[b];
+      n = a.off[b + 1] - first;
+      if (first < 0 || n < 0 || n > a.total - first || (b == 0 && first != 0)) {
+        record_error(a.status, JATTN_ERR_OFFSETS, 92, static_cast<int>(b));
+        return false;
+      }
+    }
+    if (from < 0) return false;
+    to = from > cap ? from : from + n;
+  }
+  if (to > cap) {
+    record_error(a.status, JATTN_ERR_LENGTH, 93, static_cast<int>(b));
+    return false;
+  }
+  e.low = pages_for(a, from);
+  e.high = pages_for(a, to);
+  return true;
+}
+
+__device__ __forceinline__ bool is_page(const PageArgs& a, int32_t page, int64_t b) {
+  if (page >= 0 && page < a.n_pages) return true;
+  record_error(a.status, JATTN_ERR_PAGES, 94, static_cast<int>(b));
+  return false;
+}
+
+// Pages that sequence b gives back, counted by the warp's lanes: none if one of its entries is no page.
+__device__ __forceinline__ int64_t pages_back(const PageArgs& a, int64_t b, int lane) {
+  Span e;
+  if (!span_of<true>(a, b, e)) return 0;
+  bool good = true;
+  for (int64_t j = e.low + lane; j < e.high; j += 32) good = is_page(a, a.table[b * a.max_pages + j], b) && good;
+  return __all_sync(0xffffffffu, good) ? e.high - e.low : 0;
+}
+
+// The last b in [low, high] with first[b] <= i.
+__device__ __forceinline__ int64_t bisect(const int64_t* first, int64_t low, int64_t high, int64_t i) {
+  while (low < high) {
+    const int64_t mid = (low + high + 1) >> 1;
+    if (first[mid] <= i) low = mid;
+    else high = mid - 1;
+  }
+  return low;
+}
+
+// Page number i of the call's pages.
+template <bool RELEASE>
+__device__ __forceinline__ void move_page(const PageArgs& a, const int64_t* first, int64_t top, int64_t i) {
+  const int64_t b = bisect(first, 0, a.B - 1, i);
+  Span e;
+  span_of<RELEASE>(a, b, e);
+  int32_t* entry = a.table + b * a.max_pages + e.low + (i - first[b]);
+  int32_t* slot = a.free_pages + (top - 1 - i);
+  if constexpr (RELEASE) {
+    *slot = *entry;
+    *entry = -1;
+  } else {
+    const int32_t page = *slot;
+    *entry = is_page(a, page, b) ? page : -1;
+  }
+}
+
+// Slot of row r of sequence b: from the table where its page was there before, else from the stack.
+__device__ __forceinline__ int64_t slot_of(const PageArgs& a, const int64_t* first, int64_t top, int64_t b, int64_t r) {
+  Span e;
+  if (!span_of<false>(a, b, e)) return -1;
+  const int64_t i = a.off != nullptr ? r - a.off[b] : 0;
+  if (i < 0) return -1;
+  const int64_t pos = a.start[b] + i, j = pos >> a.page_shift;
+  if (j >= e.high) return -1;
+  const int32_t page = j < e.low ? a.table[b * a.max_pages + j] : a.free_pages[top - 1 - (first[b] + j - e.low)];
+  if (!is_page(a, page, b)) return -1;
+  return (static_cast<int64_t>(page) << a.page_shift) + (pos & (a.page_size - 1));
+}
+
+__device__ __forceinline__ int64_t row_slot(const PageArgs& a, const int64_t* first, const Plan& plan, int64_t low,
+                                            int64_t high, int64_t r) {
+  if (!plan.ok) return -1;
+  if (a.off == nullptr) return slot_of(a, first, plan.top, r, r);
+  if (r >= a.off[a.B]) return -1;
+  const int64_t b = bisect(a.off, low, high, r);
+  return r < a.off[b + 1] ? slot_of(a, first, plan.top, b, r) : -1;
+}
+
+__global__ void __launch_bounds__(kFillBlock) page_count_kernel(PageArgs a) {
+  wait_for_dependency();
+  const int lane = threadIdx.x % 32;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kFillBlock / 32);
+  for (int64_t b = static_cast<int64_t>(blockIdx.x) * (kFillBlock / 32) + threadIdx.x / 32; b < a.B; b += warps) {
+    const int64_t n = pages_back(a, b, lane);
+    if (lane == 0) first_of(a)[b] = n;
+  }
+}
+
+// Adds the counts up. SMALL: counts the pages of a release itself, and moves pages and fills slots.
+template <bool RELEASE, bool SMALL>
+__global__ void __launch_bounds__(kPlanBlock) page_plan_kernel(PageArgs a) {
+  __shared__ int64_t warp_sum[32];
+  __shared__ int64_t own[SMALL ? kPlanBlock + 1 : 1];
+  __shared__ Plan plan;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int64_t* first = SMALL ? own : first_of(a);
+  wait_for_dependency();
+  if constexpr (SMALL && RELEASE) {
+    for (int64_t b = warp; b < a.B; b += kPlanBlock / 32) {
+      const int64_t n = pages_back(a, b, lane);
+      if (lane == 0) own[b] = n;
+    }
+    __syncthreads();
+  }
+  int64_t total = 0;
+  for (int64_t base = 0; base < a.B; base += kPlanBlock) {
+    const int64_t b = base + threadIdx.x;
+    int64_t n = 0;
+    if (b < a.B) {
+      if constexpr (RELEASE) {
+        n = first[b];
+      } else {
+        Span e;
+        span_of<false>(a, b, e);
+        n = max(e.high - e.low, int64_t(0));
+      }
+    }
+    int64_t sum = n;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t below = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += below;
+    }
+    if (lane == 31) warp_sum[warp] = sum;
+    __syncthreads();
+    int64_t s = warp_sum[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int64_t below = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s += below;
+    }
+    const int64_t before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+    if (b < a.B) first[b] = total + (warp > 0 ? before : 0) + sum - n;
+    total += __shfl_sync(0xffffffffu, s, 31);
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const int64_t height = *a.count;
+    Plan p;
+    p.ok = height >= 0 && height <= a.n_pages && (RELEASE ? total <= a.n_pages - height : total <= height);
+    if (!p.ok) record_error(a.status, JATTN_ERR_POOL, 95, 0);
+    p.pages = p.ok ? total : 0;
+    p.top = RELEASE ? height + total : height;
+    if (p.pages > 0) *a.count = RELEASE ? height + total : height - total;
+    if constexpr (SMALL) plan = p;
+    else *plan_of(a) = p;
+  }
+  if constexpr (SMALL) {
+    __syncthreads();
+    // slots first: a row's page may be in the table or still on the stack
+    if constexpr (!RELEASE)
+      if (a.slots != nullptr)
+        for (int64_t r = threadIdx.x; r < a.total; r += kPlanBlock)
+          a.slots[r] = row_slot(a, first, plan, 0, a.B - 1, r);
+    for (int64_t i = threadIdx.x; i < plan.pages; i += kPlanBlock) move_page<RELEASE>(a, first, plan.top, i);
+  }
+}
+
+template <bool RELEASE>
+__global__ void __launch_bounds__(kFillBlock) page_fill_kernel(PageArgs a) {
+  __shared__ int64_t ends[2];
+  wait_for_dependency();
+  const Plan plan = *plan_of(a);
+  const int64_t* first = first_of(a);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kFillBlock + threadIdx.x; i < plan.pages;
+       i += static_cast<int64_t>(gridDim.x) * kFillBlock)
+    move_page<RELEASE>(a, first, plan.top, i);
+  if constexpr (!RELEASE) {
+    if (a.slots == nullptr) return;
+    constexpr int64_t kChunk = kFillBlock * kFillRows;
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kChunk; row0 < a.total;
+         row0 += static_cast<int64_t>(gridDim.x) * kChunk) {
+      // the sequences of the chunk's first and last rows bound those between them
+      if (threadIdx.x < 2 && a.off != nullptr)
+        ends[threadIdx.x] = bisect(a.off, 0, a.B - 1, threadIdx.x == 0 ? row0 : min(row0 + kChunk, a.total) - 1);
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kFillRows; ++i) {
+        const int64_t r = row0 + i * kFillBlock + threadIdx.x;
+        if (r < a.total) a.slots[r] = row_slot(a, first, plan, ends[0], ends[1], r);
+      }
+      __syncthreads();
+    }
+  }
+}
+
+int64_t ctas_for(int64_t n, int64_t per_cta, int sms) {
+  return std::max<int64_t>(1, std::min<int64_t>((n + per_cta - 1) / per_cta, static_cast<int64_t>(sms) * (2048 / kFillBlock)));
+}
+
+// Calls that one CTA serves: all sequences in its shared memory, and a few turns of its threads at most for their rows
+// and pages.
+bool small_assign(const PageArgs& a) {
+  return a.B <= kPlanBlock && a.total <= 4 * kPlanBlock;
+}
+bool small_release(const PageArgs& a) {
+  return a.B <= kPlanBlock && a.B * a.max_pages <= 32 * kPlanBlock;
+}
+
+}  // namespace
+
+size_t page_scratch_bytes(int64_t B) { return kPlanBytes + 8 * static_cast<size_t>(B); }
+
+cudaError_t launch_page_assign(const PageArgs& a, int sms, cudaStream_t stream) {
+  if (small_assign(a)) return launch_early(page_plan_kernel<false, true>, a, 1, kPlanBlock, stream);
+  const cudaError_t e = launch_early(page_plan_kernel<false, false>, a, 1, kPlanBlock, stream);
+  if (e != cudaSuccess) return e;
+  return launch_early(page_fill_kernel<false>, a, ctas_for(a.total, kFillBlock * kFillRows, sms), kFillBlock, stream);
+}
+
+cudaError_t launch_page_release(const PageArgs& a, int sms, cudaStream_t stream) {
+  if (small_release(a)) return launch_early(page_plan_kernel<true, true>, a, 1, kPlanBlock, stream);
+  cudaError_t e = launch_early(page_count_kernel, a, ctas_for(a.B, kFillBlock / 32, sms), kFillBlock, stream);
+  if (e == cudaSuccess) e = launch_early(page_plan_kernel<true, false>, a, 1, kPlanBlock, stream);
+  if (e != cudaSuccess) return e;
+  return launch_early(page_fill_kernel<true>, a, ctas_for(a.B * a.max_pages, kFillBlock * 4, sms), kFillBlock, stream);
+}
+
+}  // namespace jattn

@@ -1,0 +1,177 @@
+// Row operators (layer norm, rotary positions): tensors [rows, heads, N] of fp32, bf16 or fp16 with strides, read and
+// written in vectors of 16 bytes where everything is aligned to them, else value by value.
+#pragma once
+#include <cstdint>
+#include <type_traits>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace jattn {
+
+// A strided tensor [rows, heads, N]: strides in elements, N's is 1.
+template <typename P>
+struct RowsView {
+  P data;
+  int64_t row, head;
+};
+using RowsIn = RowsView<const void*>;
+using RowsOut = RowsView<void*>;
+
+struct NormArgs {
+  RowsIn x, dy;       // dy: backward only
+  RowsOut y;          // forward: y, backward: dx
+  const void* w;      // nullptr: ones
+  const void* b;      // forward only; nullptr: zeros
+  float* mean;        // [rows, heads]: written by the forward (nullptr: not kept), read by the backward
+  float* rstd;
+  float* partial;     // backward: [parts][2][N], nullptr: no gradient of the weight is asked for
+  const int64_t* live;  // device: rows that count (nullptr: all)
+  int64_t rows;
+  int heads, N;
+  int split;          // heads whose rows need both strides; 1 where one stride leads through all rows of all heads
+  float eps;
+  bool wide_weight;   // w and b are fp32 whatever x is
+  bool zero_behind;   // rows behind the live ones are set to zero, else left as they are
+  DevStatus* status;
+};
+
+struct NormJoinArgs {
+  const float* partial;
+  void* dw;
+  void* db;  // nullptr: not asked for
+  int parts, N;
+};
+
+struct RotaryArgs {
+  RowsIn x;
+  RowsOut y;
+  const int64_t* off;    // nullptr: every row has a position of its own
+  const int64_t* start;  // nullptr: zeros (with off), the row's number (without)
+  const float* cos_t;
+  const float* sin_t;
+  int64_t B, total, table_rows;
+  int heads, D, half;
+  int rows, copied;      // set by the launch: rows of a CTA, vectors of a head that are copied
+  bool inverse, zero_behind;
+  DevStatus* status;
+};
+
+struct RotaryTablesArgs {
+  uint64_t turn[512];  // per pair: 2^-64 turns a position
+  float* cos_t;
+  float* sin_t;
+  int64_t first, rows;
+  int half;
+  float amplitude;
+};
+
+// A launch that may be set up while the kernel before it ends (kernels call wait_for_dependency first).
+template <typename Args>
+cudaError_t launch_early(void (*kernel)(Args), const Args& a, int64_t ctas, int threads, cudaStream_t stream) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(static_cast<unsigned>(ctas));
+  c.blockDim = dim3(static_cast<unsigned>(threads));
+  c.stream = stream;
+  c.attrs = &early;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, a);
+}
+
+// V neighbouring values as they lie in memory.
+template <typename T, int V>
+using Raw = std::conditional_t<V * sizeof(T) == 16, uint4, T>;
+
+template <typename T, int V>
+__device__ __forceinline__ Raw<T, V> load_raw(const T* p) {
+  static_assert(V == 1 || V * sizeof(T) == 16, "single values or 16 bytes");
+  return *reinterpret_cast<const Raw<T, V>*>(p);
+}
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Raw<T, V>& w, float (&x)[V]) {
+  if constexpr (V == 1) {
+    x[0] = to_float(w);
+  } else {
+    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same_v<T, float>) {
+        x[i] = __uint_as_float(in[i]);
+      } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        x[2 * i] = __uint_as_float(in[i] << 16);
+        x[2 * i + 1] = __uint_as_float(in[i] & 0xffff0000u);
+      } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&in[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      }
+    }
+  }
+}
+
+// V neighbouring values of a table.
+template <int V>
+__device__ __forceinline__ void unpack_table(const float* p, float (&x)[V]) {
+  if constexpr (V == 1) {
+    x[0] = *p;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p + i);
+      x[i] = f.x;
+      x[i + 1] = f.y;
+      x[i + 2] = f.z;
+      x[i + 3] = f.w;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ T from_float(float x) {
+  if constexpr (std::is_same_v<T, float>) return x;
+  else if constexpr (std::is_same_v<T, __nv_bfloat16>) return __float2bfloat16_rn(x);
+  else return __float2half_rn(x);
+}
+
+// Rounded once, to nearest even.
+template <typename T, int V>
+__device__ __forceinline__ void store_values(T* p, const float (&x)[V]) {
+  if constexpr (V == 1) {
+    *p = from_float<T>(x[0]);
+  } else {
+    uint32_t out[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same_v<T, float>) {
+        out[i] = __float_as_uint(x[i]);
+      } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        out[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+      } else {
+        const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+        out[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
+// Rows before the padding: *live, which a prefix sum over `rows` rows ends with (nullptr: all rows).
+__device__ __forceinline__ int64_t live_rows(const int64_t* live, int64_t rows, DevStatus* status) {
+  if (live == nullptr) return rows;
+  const int64_t n = *live;
+  if (n >= 0 && n <= rows) return n;
+  if (blockIdx.x == 0 && threadIdx.x == 0) record_error(status, JATTN_ERR_OFFSETS, 90, 0);
+  return n < 0 ? 0 : rows;
+}
+
+}  // namespace jattn

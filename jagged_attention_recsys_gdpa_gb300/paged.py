@@ -11,6 +11,11 @@
 * ``decode(q, cache, page_table, kv_lens, q_off=..., ...)``: attention of one
   or a few new query rows per sequence over the cache, with ``forward``'s
   activations and masks; query heads may share key/value heads.
+* ``page_pool(n_pages, page_size)``: the cache's free pages, in device memory;
+  ``page_assign(pool, page_table, start, off=...)`` gives sequences the pages
+  that new rows need (before ``cache_append``) and returns the rows' slots,
+  ``page_release(pool, page_table, lens, keep=...)`` takes pages back, both without
+  a host round trip.
 
 Row ``pos`` of sequence b lies in page ``page_table[b, pos // page_size]``.
 Every tensor lies on the cache's device; calls run on that device's current
@@ -40,7 +45,7 @@ def status_block(index: int) -> torch.Tensor:
     t = _status_blocks.get(index)
     if t is None:
         if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("the first paged-cache call on a device cannot be captured into a graph; "
+            raise RuntimeError("the first paged-cache or row-operator call on a device cannot be captured into a graph; "
                                "make one call before the capture")
         t = torch.zeros(256, dtype=torch.uint8, device=torch.device("cuda", index))
         torch.cuda.current_stream(index).synchronize()
@@ -101,6 +106,39 @@ def paged_cache(n_pages, page_size, H, D, format="bf16", device="cuda") -> Paged
     return PagedCache(k, v, ks, vs)
 
 
+class PagePool:
+    """Free pages of a cache with pages of ``page_size`` rows: free_pages int32 [n_pages], of which the first count[0] (int64
+    [1]) are a stack of free pages, the next one to be taken last. Holds the tensors it is given. Calls on one pool follow
+    each other (one stream, or events between streams), as those on a cache do."""
+
+    __slots__ = ("_free", "_count", "_c", "_ref", "_device", "_index", "_page")
+
+    def __init__(self, free_pages, count, page_size):
+        if free_pages.dtype is not torch.int32 or free_pages.dim() != 1 or not free_pages.is_cuda \
+                or free_pages.numel() == 0 or not free_pages.is_contiguous():
+            raise ValueError("free_pages must be a contiguous CUDA int32 tensor [n_pages]")
+        if count.dtype is not torch.int64 or count.shape != (1,) or count.device != free_pages.device:
+            raise ValueError("count must be an int64 tensor [1] on the device of free_pages")
+        if page_size < 1 or page_size > 4096 or page_size & (page_size - 1):
+            raise ValueError("page_size must be a power of two from 1 to 4096")
+        self._free, self._count, self._page = free_pages, count, int(page_size)
+        self._c = B.PagePool(free_pages.numel(), self._page, free_pages.data_ptr(), count.data_ptr())
+        self._ref = ctypes.byref(self._c)
+        self._device, self._index = free_pages.device, free_pages.device.index
+
+    free_pages = property(lambda self: self._free)
+    count = property(lambda self: self._count)
+    n_pages = property(lambda self: self._c.n_pages)
+    page_size = property(lambda self: self._page)
+    device = property(lambda self: self._device)
+
+
+def page_pool(n_pages, page_size, device="cuda") -> PagePool:
+    """A pool whose ``n_pages`` pages are all free; page 0 is taken first."""
+    free = torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device)
+    return PagePool(free, torch.full((1,), n_pages, dtype=torch.int64, device=device), page_size)
+
+
 def _check_rows(cache, x, name):
     if x.dtype is not torch.bfloat16 or x.dim() != 3 or x.device != cache._device or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous bf16 tensor [total, H, D] on the cache's device")
@@ -134,10 +172,13 @@ def _check_rope(cache, rope):
 
 def _launch(cache, fn, *args):
     """fn(*args, workspace, its bytes, stream) with the cache's device current."""
-    index = cache._index
+    launch_on(cache._index, fn, *args)
+
+
+def launch_on(index, fn, *args):
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
-            return _launch(cache, fn, *args)
+            return launch_on(index, fn, *args)
     fn(*args, status_block(index).data_ptr(), 256, torch._C._cuda_getCurrentRawStream(index))
 
 
@@ -239,3 +280,49 @@ def decode(q, cache, page_table, kv_lens, q_off=None, act="softmax", causal=Fals
     scratch = torch.empty(n, dtype=torch.uint8, device=cache._device)
     _launch(cache, B.decode, p, cache._ref, q_off, kv_lens, page_table, q, out, lse, scratch.data_ptr(), n)
     return out, lse
+
+
+def _page_scratch(pool, nb):
+    n = B.page_scratch_size(nb)
+    return torch.empty(n, dtype=torch.uint8, device=pool._device), n
+
+
+def page_assign(pool, page_table, start, off=None, total=None, slots=True):
+    """Give every sequence the pages that its new rows need: rows start[b] .. start[b] + n - 1 (start int64 [B], the rows
+    before, whose pages page_table holds already; negative skips the sequence), n from the prefix sums ``off`` int64 [B+1] (None:
+    one row each). Page numbers are written into page_table int32 [B, max_pages] where they are missing. Returns the new
+    rows' slots int64 [total], page * page_size + place in the page (-1 for rows without one and rows behind off[B]);
+    ``slots`` may be a tensor to write them to, or False for none. ``total`` defaults to off[-1] (a host read) or the rows
+    of ``slots``. Where the pool has too few pages none is assigned (``device_status``). See jattn_page_assign."""
+    _check_table(pool, page_table)
+    nb = page_table.shape[0]
+    _check_index(pool, start, nb, "start")
+    if isinstance(slots, torch.Tensor):
+        total = slots.shape[0] if total is None and slots.dim() == 1 else total
+    if off is None:
+        if total is not None and total != nb:
+            raise ValueError("without off there is one row per sequence")
+        total = nb
+    else:
+        _check_index(pool, off, nb + 1, "off")
+        total = int(off[-1].item()) if total is None else int(total)
+    if isinstance(slots, torch.Tensor):
+        _check_index(pool, slots, total, "slots")
+    else:
+        slots = torch.empty(total, dtype=torch.int64, device=pool._device) if slots else None
+    scratch, n = _page_scratch(pool, nb)
+    launch_on(pool._index, B.page_assign, pool._ref, nb, total, off, start, page_table, slots, scratch, n)
+    return slots
+
+
+def page_release(pool, page_table, lens, keep=None):
+    """Take back the pages of rows keep[b] .. lens[b] - 1 (int64 [B]; keep None: all rows, negative: the sequence is left as it
+    is) that hold none of the rows kept; their entries in page_table become -1. The next page_assign takes them first, the first sequence's first
+    page before all others. See jattn_page_release."""
+    _check_table(pool, page_table)
+    nb = page_table.shape[0]
+    _check_index(pool, lens, nb, "lens")
+    if keep is not None:
+        _check_index(pool, keep, nb, "keep")
+    scratch, n = _page_scratch(pool, nb)
+    launch_on(pool._index, B.page_release, pool._ref, nb, lens, keep, page_table, scratch, n)
