@@ -1164,7 +1164,7 @@ int check_norm(const jattn_norm_t* p) {
 
 // What both directions share; x, dy (null: forward) and y (backward: dx) as the caller gave them.
 NormArgs norm_args(const jattn_norm_t& p, const int64_t* live, const RowTensor& x, const RowTensor& dy, const RowTensor& y,
-                   const void* weight, const void* bias, void* ws, bool* vectors) {
+                   const void* weight, const void* bias, void* ws, NormPath* path) {
   const int size = type_bytes(p.type);
   NormArgs a{};
   a.x = RowsIn{x.p, x.row, x.head};
@@ -1177,6 +1177,7 @@ NormArgs norm_args(const jattn_norm_t& p, const int64_t* live, const RowTensor& 
   a.heads = p.heads;
   a.N = p.N;
   a.eps = p.eps;
+  a.inv_n = 1.0f / static_cast<float>(p.N);
   a.wide_weight = p.weight_type == JATTN_F32;
   a.zero_behind = p.zero_behind != 0;
   a.status = static_cast<DevStatus*>(ws);
@@ -1189,8 +1190,21 @@ NormArgs norm_args(const jattn_norm_t& p, const int64_t* live, const RowTensor& 
     a.dy.row = dy.head;
     a.y.row = y.head;
   }
-  *vectors = in_vectors(x, p.rows, p.heads, p.N, size) && in_vectors(y, p.rows, p.heads, p.N, size) &&
-             (!dy.p || in_vectors(dy, p.rows, p.heads, p.N, size)) && aligned16(weight) && aligned16(bias);
+  if (in_vectors(x, p.rows, p.heads, p.N, size) && in_vectors(y, p.rows, p.heads, p.N, size) &&
+      (!dy.p || in_vectors(dy, p.rows, p.heads, p.N, size)) && aligned16(weight) && aligned16(bias)) {
+    *path = NormPath::kVectors;
+    return a;
+  }
+  // vectors that start before the rows: in all tensors alike, and at the same place in every V-th row
+  const int V = 16 / size;
+  const auto like_x = [&](const RowTensor& t, int64_t row) {
+    return (reinterpret_cast<uintptr_t>(t.p) ^ reinterpret_cast<uintptr_t>(x.p)) % 16 == 0 && (row - a.x.row) % V == 0 &&
+           (a.split == 1 || t.head % V == 0);
+  };
+  const bool even_steps = a.split == 1 || a.x.row % V == 0;
+  *path = even_steps && like_x(x, a.x.row) && like_x(y, a.y.row) && (!dy.p || like_x(dy, a.dy.row)) && p.N <= kMaxRow - V
+              ? NormPath::kShifted
+              : NormPath::kValues;
   return a;
 }
 
@@ -1221,11 +1235,11 @@ int jattn_layer_norm(const jattn_norm_t* p, const int64_t* live_rows, const void
   if ((rc = device_info(dev)) != JATTN_OK) return rc;
   clear_stale_error();
   if (p->rows == 0) return JATTN_OK;
-  bool vectors;
-  NormArgs a = norm_args(*p, live_rows, x, RowTensor{}, y, weight, bias, ws, &vectors);
+  NormPath path;
+  NormArgs a = norm_args(*p, live_rows, x, RowTensor{}, y, weight, bias, ws, &path);
   a.mean = mean;
   a.rstd = rstd;
-  const cudaError_t e = launch_norm(p->type, vectors, a, dev.sms, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_norm(p->type, path, a, dev.sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? JATTN_OK : cuda_fail("layer norm launch", e);
 }
 
@@ -1235,9 +1249,10 @@ int jattn_layer_norm_bwd_scratch_size(const jattn_norm_t* p, size_t* bytes) {
   if (rc != JATTN_OK) return rc;
   DeviceInfo dev;
   if ((rc = device_info(dev)) != JATTN_OK) return rc;
-  // the two widths of access take grids of their own
-  const int parts = std::max(norm_bwd_parts(p->type, true, p->rows * p->heads, p->N, dev.sms),
-                             norm_bwd_parts(p->type, false, p->rows * p->heads, p->N, dev.sms));
+  // each way to read the rows takes a grid of its own
+  int parts = 0;
+  for (const NormPath path : {NormPath::kVectors, NormPath::kShifted, NormPath::kValues})
+    parts = std::max(parts, norm_bwd_parts(p->type, path, p->rows * p->heads, p->N, dev.sms));
   *bytes = al256(static_cast<size_t>(parts) * 2 * p->N * sizeof(float));
   return JATTN_OK;
 }
@@ -1277,18 +1292,18 @@ int jattn_layer_norm_bwd(const jattn_norm_t* p, const int64_t* live_rows, const 
       meet_any(db, {in, grad, w, m, r, lr, sc}) || meet_any(sc, {in, grad, w, m, r, lr}))
     return JATTN_ERR_INVALID;
   clear_stale_error();
-  bool vectors;
-  NormArgs a = norm_args(*p, live_rows, x, dy, dx, weight, nullptr, ws, &vectors);
+  NormPath path;
+  NormArgs a = norm_args(*p, live_rows, x, dy, dx, weight, nullptr, ws, &path);
   a.mean = const_cast<float*>(mean);
   a.rstd = const_cast<float*>(rstd);
   a.partial = dweight ? static_cast<float*>(scratch) : nullptr;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (p->rows > 0) {
-    const cudaError_t e = launch_norm_bwd(p->type, vectors, a, dev.sms, st);
+    const cudaError_t e = launch_norm_bwd(p->type, path, a, dev.sms, st);
     if (e != cudaSuccess) return cuda_fail("layer norm backward launch", e);
   }
   if (!dweight) return JATTN_OK;
-  const int parts = p->rows > 0 ? norm_bwd_parts(p->type, vectors, p->rows * p->heads, p->N, dev.sms) : 0;
+  const int parts = p->rows > 0 ? norm_bwd_parts(p->type, path, p->rows * p->heads, p->N, dev.sms) : 0;
   const NormJoinArgs j{a.partial, dweight, dbias, parts, p->N};
   const cudaError_t e = launch_norm_join(p->weight_type, j, st);
   return e == cudaSuccess ? JATTN_OK : cuda_fail("layer norm gradient launch", e);

@@ -131,11 +131,13 @@ void decode_box(int D, bool mx, int64_t B, int64_t total_q, int64_t max_kv, int 
 cudaError_t launch_decode(int D, bool mx, DecodeArgs a, const CUtensorMap& k, const CUtensorMap& v, void* scratch,
                           cudaStream_t stream);
 
-// Layer norm (norm.cu, norm_bwd.cu) of JATTN_F32 / BF16 / F16 rows; `vectors`: everything is aligned to 16 bytes (or, the
-// weights, to a vector's values). The backward writes norm_bwd_parts partial rows, which launch_norm_join adds.
-cudaError_t launch_norm(int type, bool vectors, const NormArgs& a, int sms, cudaStream_t stream);
-int norm_bwd_parts(int type, bool vectors, int64_t rows, int N, int sms);
-cudaError_t launch_norm_bwd(int type, bool vectors, const NormArgs& a, int sms, cudaStream_t stream);
+// Layer norm (norm.cu, norm_bwd.cu) of JATTN_F32 / BF16 / F16 rows, which are read in vectors of 16 bytes (everything is
+// aligned to them), in vectors that start before the rows (all tensors alike, see norm.cuh) or value by value. The
+// backward writes norm_bwd_parts partial rows, which launch_norm_join adds.
+enum class NormPath { kVectors, kShifted, kValues };
+cudaError_t launch_norm(int type, NormPath path, const NormArgs& a, int sms, cudaStream_t stream);
+int norm_bwd_parts(int type, NormPath path, int64_t rows, int N, int sms);
+cudaError_t launch_norm_bwd(int type, NormPath path, const NormArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_norm_join(int weight_type, const NormJoinArgs& a, cudaStream_t stream);
 
 // Rotary positions of rows and their tables (rotary.cu); `vectors`: everything is aligned to 16 bytes.

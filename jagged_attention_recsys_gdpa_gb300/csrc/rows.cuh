@@ -32,7 +32,7 @@ struct NormArgs {
   int64_t rows;
   int heads, N;
   int split;          // heads whose rows need both strides; 1 where one stride leads through all rows of all heads
-  float eps;
+  float eps, inv_n;   // inv_n: 1 / N
   bool wide_weight;   // w and b are fp32 whatever x is
   bool zero_behind;   // rows behind the live ones are set to zero, else left as they are
   DevStatus* status;
