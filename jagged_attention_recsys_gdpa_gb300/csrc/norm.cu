@@ -11,65 +11,79 @@
 namespace jattn {
 namespace {
 
-#ifndef NT
-#define NT 1024
-#endif
-// Threads of an SM that the registers have to leave room for.
+// Threads of an SM, for which the registers have to leave room: what keeps memory busy without more streams than it
+// likes. Rows of up to 32 lanes of 16 bf16 values: 512 threads 68 us on norm_histories, 768 and 1,024 78 and 79; longer ones
+// (60 M values in rows of 2,048 / 8,192): 512 threads 44 / 52 us, 1,024 38 / 42; fp32 (8 values a lane, rows of 1,024): 512 in
+// CTAs of 512 43 us, 768 in CTAs of 256 39.
 template <typename A, typename S>
-constexpr int kThreads = A::V * S::K <= 8 ? NT : A::V * S::K <= 16 ? 768 : 512;
+constexpr int kThreads = S::L <= 32 || A::V == 1 ? 512 : A::V * S::K <= 8 ? 768 : A::V * S::K <= 16 ? 1024 : 512;
+template <typename A>
+constexpr int kWide = A::V == 4 ? 256 : 512;
 
 template <typename A, typename S>
 __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBlock)) norm_kernel(NormArgs a) {
   using T = typename A::Type;
-  constexpr int V = A::V, L = S::L, K = S::K, G = S::kGroups;
-  constexpr bool SHIFT = A::SHIFT, KEPT = K * V <= 16;  // weights in registers
-  __shared__ float slots1[kSumWarps<L>][1], slots2[kSumWarps<L>][2];
-  const int lane = threadIdx.x % L;
+  constexpr int V = A::V, L = S::L, K = S::K, G = S::kGroups, E = K * V;
+  constexpr bool SHIFT = A::SHIFT, KEPT = E <= 16;  // weights in registers
+  extern __shared__ __align__(16) char ring[];
+  __shared__ float slots1[G][kSumWarps<L>][1], slots2[G][kSumWarps<L>][2];
+  const int lane = threadIdx.x % L, group = threadIdx.x / L;
   wait_for_dependency();
-  const int64_t live = live_rows(a.live, a.rows, a.status) * a.heads, total = a.rows * a.heads;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
-  int64_t r = static_cast<int64_t>(blockIdx.x) * G + threadIdx.x / L;
+  const uint32_t live = static_cast<uint32_t>(live_rows(a.live, a.rows, a.status) * a.heads);
+  const uint32_t total = static_cast<uint32_t>(a.rows * a.heads);
+  const uint32_t step = gridDim.x * G;
+  uint32_t r = blockIdx.x * G + group;
   const T* const x = static_cast<const T*>(a.x.data);
   T* const y = static_cast<T*>(a.y.data);
   const int first = lane * V - (SHIFT ? shift_of<T, V>(a.x.data, row_at(a.x, a.split, r)) : 0);  // column of vector 0
-  float w[KEPT ? K : 1][V], b[KEPT ? K : 1][V];
+  float w[KEPT ? E : V], b[KEPT ? E : V];
   if constexpr (KEPT)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, w[k]);
-      load_weight<T, V, SHIFT>(a.b, a.wide_weight, first + k * L * V, a.N, 0.0f, b[k]);
+      load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, k));
+      load_weight<T, V, SHIFT>(a.b, a.wide_weight, first + k * L * V, a.N, 0.0f, vector_of<V>(b, k));
     }
-  Raw<T, V> next[K];
-  const auto load = [&](int64_t row) {
-    const T* from = x + row_at(a.x, a.split, row);
-#pragma unroll
-    for (int k = 0; k < K; ++k) next[k] = load_at<T, V, SHIFT>(from, first + k * L * V, a.N);
+  RowQueue<A, S, 1> queue;
+  constexpr int kAhead = decltype(queue)::kAhead;
+  const auto fetch = [&](uint32_t row, int slot) {
+    if (row < live) queue.fetch(ring, slot, x, x + row_at(a.x, a.split, row), first, a.N);
+    copies_commit();
   };
-  if (r < live) load(r);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(r + i * step, i);
+  int slot = 0, free_slot = kAhead;
   // the rows of a warp, and of a CTA that shares one, end together
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * G; base < total; base += step, r += step) {
-    float v[K][V], s1[1] = {0.0f}, s2[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      unpack<T, V>(next[k], v[k]);
-#pragma unroll
-      for (int i = 0; i < V; ++i) s1[0] += v[k][i];
+  for (uint32_t base = blockIdx.x * G; base < total; base += step, r += step) {
+    float v[E], s1[1], s2[2];
+    if constexpr (kAhead == 0) fetch(r, 0);
+    copies_wait<kAhead == 0 ? 0 : kAhead - 1>();
+    queue.take(ring, slot, first, a.N, v);
+    if constexpr (kAhead > 0) {
+      fetch(r + kAhead * step, free_slot);
+      slot = slot == kAhead ? 0 : slot + 1;
+      free_slot = free_slot == kAhead ? 0 : free_slot + 1;
     }
-    if (r + step < live) load(r + step);
-    row_sum<L, 1>(s1, slots1);
+    if constexpr (SHIFT)
+#pragma unroll
+      for (int k = 0; k < K; ++k) clear_outside<T, V, SHIFT>(first + k * L * V, a.N, vector_of<V>(v, k));
+    uint64_t sum = f2(0.0f, 0.0f);
+    pairwise<E>([&](int i, int j) { sum = fadd2(sum, pair(v, i, j)); });
+    s1[0] = both(sum);
+    row_sum<L, 1>(s1, slots1[group]);
     const float m = s1[0] * a.inv_n;
+    pairwise<E>([&](int i, int j) { unpair(fadd2(pair(v, i, j), f2(-m, -m)), v, i, j); });
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) v[k][i] -= m;
-      clear_outside<T, V, SHIFT>(first + k * L * V, a.N, v[k]);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        s2[0] += v[k][i];
-        s2[1] = fmaf(v[k][i], v[k][i], s2[1]);
-      }
-    }
-    row_sum<L, 2>(s2, slots2);
+    for (int k = 0; k < K; ++k) clear_outside<T, V, SHIFT>(first + k * L * V, a.N, vector_of<V>(v, k));
+    uint64_t square = f2(0.0f, 0.0f);
+    sum = square;
+    pairwise<E>([&](int i, int j) {
+      const uint64_t d = pair(v, i, j);
+      sum = fadd2(sum, d);
+      square = ffma2(d, d, square);
+    });
+    s2[0] = both(sum);
+    s2[1] = both(square);
+    row_sum<L, 2>(s2, slots2[group]);
     const float off = s2[0] * a.inv_n;
     const float rstd = rsqrtf(fmaxf(fmaf(-off, off, s2[1] * a.inv_n), 0.0f) + a.eps);
     if (r >= total || (r >= live && !a.zero_behind)) continue;
@@ -78,25 +92,27 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
       a.rstd[r] = r < live ? rstd : 0.0f;
     }
     T* to = y + row_at(a.y, a.split, r);
-    const float shift = -off * rstd;
+    const uint64_t scale = f2(rstd, rstd), shift = f2(-off * rstd, -off * rstd);
+    if constexpr (KEPT) {
+      pairwise<E>([&](int i, int j) {
+        unpair(ffma2(ffma2(pair(v, i, j), scale, shift), pair(w, i, j), pair(b, i, j)), v, i, j);
+      });
+    } else {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = first + k * L * V;
-      float out[V];
-      if constexpr (KEPT) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = fmaf(fmaf(v[k][i], rstd, shift), w[k][i], b[k][i]);
-      } else {
-        load_weight<T, V, SHIFT>(a.w, a.wide_weight, c, a.N, 1.0f, w[0]);
-        load_weight<T, V, SHIFT>(a.b, a.wide_weight, c, a.N, 0.0f, b[0]);
-#pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = fmaf(fmaf(v[k][i], rstd, shift), w[0][i], b[0][i]);
+      for (int k = 0; k < K; ++k) {
+        load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, 0));
+        load_weight<T, V, SHIFT>(a.b, a.wide_weight, first + k * L * V, a.N, 0.0f, vector_of<V>(b, 0));
+        float(&d)[V] = vector_of<V>(v, k);
+        pairwise<V>([&](int i, int j) {
+          unpair(ffma2(ffma2(pair(d, i, j), scale, shift), pair(w, i, j), pair(b, i, j)), d, i, j);
+        });
       }
-      if (r >= live)
-#pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = 0.0f;
-      store_at<T, V, SHIFT>(to, c, a.N, out);
     }
+    if (r >= live)
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) store_at<T, V, SHIFT>(to, first + k * L * V, a.N, vector_of<V>(v, k));
   }
 }
 
@@ -105,10 +121,11 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
 cudaError_t launch_norm(int type, NormPath path, const NormArgs& a, int sms, cudaStream_t stream) {
   return with_norm_access(type, path, [&](auto access) {
     using A = decltype(access);
-    return with_norm_shape<A::V>(norm_vectors<A>(a.N), [&](auto shape) {
+    return with_norm_shape<A::V, 256, kWide<A>>(norm_vectors<A>(a.N), [&](auto shape) {
       using S = decltype(shape);
       const int64_t most = static_cast<int64_t>(sms) * std::max(1, kThreads<A, S> / S::kBlock);
-      return launch_early(norm_kernel<A, S>, a, norm_ctas<A, S>(a.rows * a.heads, most), S::kBlock, stream);
+      return launch_early(norm_kernel<A, S>, a, norm_ctas<A, S>(a.rows * a.heads, most), S::kBlock, stream,
+                          RowQueue<A, S, 1>::kBytes);
     });
   });
 }

@@ -7,10 +7,8 @@
 
 namespace jattn {
 
-constexpr int kNormBlock = 256;
-
-// Sums of C values over the L lanes of a row, in a fixed order, to all of them: L up to 32 neighbouring lanes, or the
-// whole CTA of L threads, which meets at one barrier. A CTA's warps read each other's partial sums behind the barrier, so
+// Sums of C values over the L lanes of a row, in a fixed order, to all of them: up to 32 neighbouring lanes, or whole warps,
+// which meet at a barrier of their group's. A group's warps read each other's partial sums behind the barrier, so
 // the same `slots` may be written again only behind the next one: callers take two in turn.
 template <int L>
 constexpr int kSumWarps = L > 32 ? L / 32 : 1;
@@ -22,10 +20,11 @@ __device__ __forceinline__ void row_sum(float (&x)[C], float (&slots)[kSumWarps<
 #pragma unroll
     for (int c = 0; c < C; ++c) x[c] += __shfl_xor_sync(0xffffffffu, x[c], d);
   if constexpr (L > 32) {
+    const int warp = threadIdx.x % L / 32;
     if (threadIdx.x % 32 == 0)
 #pragma unroll
-      for (int c = 0; c < C; ++c) slots[threadIdx.x / 32][c] = x[c];
-    __syncthreads();
+      for (int c = 0; c < C; ++c) slots[warp][c] = x[c];
+    asm volatile("bar.sync %0, %1;" ::"r"(static_cast<int>(threadIdx.x) / L + 1), "n"(L) : "memory");
     const int at = threadIdx.x % kSumWarps<L>;
 #pragma unroll
     for (int c = 0; c < C; ++c) x[c] = slots[at][c];
@@ -36,6 +35,31 @@ __device__ __forceinline__ void row_sum(float (&x)[C], float (&slots)[kSumWarps<
   }
 }
 
+// Arithmetic on the E values of a lane two at a time (f32x2): half the instructions, which are what short rows are bound by.
+template <int E, typename F>
+__device__ __forceinline__ void pairwise(F&& f) {
+#pragma unroll
+  for (int i = 0; i + 1 < E; i += 2) f(i, i + 1);
+  if constexpr (E % 2) f(E - 1, E - 1);
+}
+// Two neighbours of an array as a pair; of the last one of an odd number and nothing.
+template <int E>
+__device__ __forceinline__ uint64_t pair(const float (&x)[E], int i, int j) {
+  return f2(x[i], i == j ? 0.0f : x[j]);
+}
+template <int E>
+__device__ __forceinline__ void unpair(uint64_t p, float (&x)[E], int i, int j) {
+  float lo, hi;
+  f2_split(p, lo, hi);
+  x[i] = lo;
+  if (i != j) x[j] = hi;
+}
+__device__ __forceinline__ float both(uint64_t p) {
+  float lo, hi;
+  f2_split(p, lo, hi);
+  return lo + hi;
+}
+
 // Rows whose values do not start at 16-byte boundaries (an odd N): the first vector of a row begins `shift` values before it.
 // Rows that are a multiple of V apart share their shift, so a group of lanes that takes every V-th row (or a multiple) has
 // the same columns in each, and only the vectors at a row's ends are read and written value by value.
@@ -44,19 +68,61 @@ __device__ __forceinline__ bool whole(int c, int n) {
   return c >= 0 && c + V <= n;
 }
 
-template <typename T, int V, bool SHIFT>
-__device__ __forceinline__ Raw<T, V> load_at(const T* row, int c, int n) {
-  Raw<T, V> w{};
-  if (!SHIFT ? c < n : whole<T, V>(c, n)) {
-    w = load_raw<T, V>(row + c);
-  } else if constexpr (SHIFT) {
-    T* v = reinterpret_cast<T*>(&w);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (c + i >= 0 && c + i < n) v[i] = row[c + i];
+// Rows on their way: every thread copies its own K vectors of a row into its own places in shared memory, kAhead rows
+// ahead, and reads them back itself, so no barrier is needed and no registers wait for memory. A vector that ends behind its
+// row is filled up with zeros; one that starts before it brings values of the row before, but for the first bytes of the
+// tensor, which are fetched one by one. Single values (V == 1) wait in registers, one row ahead.
+template <typename A, typename S, int TENSORS>
+struct RowQueue {
+  using T = typename A::Type;
+  static constexpr int V = A::V, L = S::L, K = S::K;
+  static constexpr int kSlot = K * S::kBlock * 16;  // bytes of a row, or of a CTA's rows
+  // as many as shared memory holds: none of the longest fp32 rows of two tensors
+  static constexpr int kAhead = V == 1 ? 1 : std::min(2, (200 << 10) / (kSlot * TENSORS) - 1), kSlots = kAhead + 1;
+  static constexpr int kBytes = V == 1 ? 0 : kSlots * kSlot;
+
+  Raw<T, V> next[V == 1 ? K : 1];
+
+  static __device__ __forceinline__ uint4* place(char* ring, int slot, int k) {
+    return reinterpret_cast<uint4*>(ring) + (slot * K + k) * S::kBlock + threadIdx.x;
   }
-  return w;
-}
+  // Row at `row`, of which this lane's first vector starts at column `first`; base: the tensor's first value.
+  __device__ __forceinline__ void fetch(char* ring, int slot, const T* base, const T* row, int first, int n) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = first + k * L * V;
+      if constexpr (V == 1) {
+        if (c < n) next[k] = row[c];
+      } else {
+        uint4* to = place(ring, slot, k);
+        const T* from = row + c;
+        if (A::SHIFT && from < base && c < n) {
+          T* v = reinterpret_cast<T*>(to);
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (c + i >= 0 && c + i < n) v[i] = row[c + i];
+        } else if (!A::SHIFT) {
+          if (c < n) copy_async16(to, from);
+        } else if (c < n) {
+          copy_async16(to, from, min(n - c, V) * static_cast<int>(sizeof(T)));
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void take(char* ring, int slot, int first, int n, float (&x)[K * V]) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float(&v)[V] = *reinterpret_cast<float(*)[V]>(&x[k * V]);
+      Raw<T, V> w{};
+      if constexpr (V == 1) {
+        if (first + k * L < n) w = next[k];
+      } else {
+        if (first + k * L * V < n) w = *place(ring, slot, k);
+      }
+      unpack<T, V>(w, v);
+    }
+  }
+};
 
 template <typename T, int V, bool SHIFT>
 __device__ __forceinline__ void store_at(T* row, int c, int n, const float (&x)[V]) {
@@ -78,6 +144,12 @@ __device__ __forceinline__ void clear_outside(int c, int n, float (&x)[V]) {
     if (!(SHIFT && c + i >= 0 && c + i < n)) x[i] = 0.0f;
 }
 
+// Vector k of a lane's K vectors of V values.
+template <int V, int E>
+__device__ __forceinline__ float (&vector_of(float (&x)[E], int k))[V] {
+  return *reinterpret_cast<float(*)[V]>(&x[k * V]);
+}
+
 // Values before the row in its first vector.
 template <typename T, int V>
 __device__ __forceinline__ int shift_of(const void* base, int64_t at) {
@@ -86,9 +158,9 @@ __device__ __forceinline__ int shift_of(const void* base, int64_t at) {
 
 // Where row r (of all heads) lies.
 template <typename P>
-__device__ __forceinline__ int64_t row_at(const RowsView<P>& t, int split, int64_t r) {
+__device__ __forceinline__ int64_t row_at(const RowsView<P>& t, int split, uint32_t r) {
   if (split == 1) return r * t.row;
-  const int64_t outer = static_cast<uint32_t>(r) / static_cast<uint32_t>(split);
+  const uint32_t outer = r / static_cast<uint32_t>(split);
   return outer * t.row + (r - outer * split) * t.head;
 }
 
@@ -110,39 +182,37 @@ __device__ __forceinline__ void load_weight(const void* w, bool wide, int c, int
 }
 
 // Lanes of a row, vectors of a lane and threads of a CTA.
-template <int L_, int K_>
+template <int L_, int K_, int NARROW, int WIDE>
 struct NormShape {
   static constexpr int L = L_, K = K_;
-  static constexpr int kBlock = L > 32 ? L : kNormBlock;
+  static constexpr int kBlock = L <= 32 ? NARROW : L > WIDE ? L : WIDE;
   static constexpr int kGroups = kBlock / L;  // rows of a CTA at a time
 };
 
-// Calls f(shape) with the smallest shape whose L * K vectors hold a row of n.
-template <int V, typename F>
+// Calls f(shape) with the smallest shape whose L * K vectors hold a row of n, in CTAs of NARROW threads for rows of up
+// to a warp's lanes, else of WIDE.
+template <int V, int NARROW, int WIDE, typename F>
 cudaError_t with_norm_shape(int n, F&& f) {
   if constexpr (V == 1) {
-    if (n <= 8) return f(NormShape<8, 1>{});
-    if (n <= 32) return f(NormShape<32, 1>{});
-    if (n <= 128) return f(NormShape<32, 4>{});
-    if (n <= 512) return f(NormShape<32, 16>{});
-    if (n <= 2048) return f(NormShape<128, 16>{});
-    if (n <= 8192) return f(NormShape<512, 16>{});
-    return f(NormShape<1024, 16>{});
+    if (n <= 8) return f(NormShape<8, 1, NARROW, WIDE>{});
+    if (n <= 32) return f(NormShape<32, 1, NARROW, WIDE>{});
+    if (n <= 128) return f(NormShape<32, 4, NARROW, WIDE>{});
+    if (n <= 512) return f(NormShape<32, 16, NARROW, WIDE>{});
+    if (n <= 2048) return f(NormShape<128, 16, NARROW, WIDE>{});
+    if (n <= 8192) return f(NormShape<512, 16, NARROW, WIDE>{});
+    return f(NormShape<1024, 16, NARROW, WIDE>{});
   } else {
-#ifndef NK
-#define NK 1
-#endif
-    if (n <= 4) return f(NormShape<4, 1>{});
-    if (n <= 8) return f(NormShape<8 / NK, NK>{});
-    if (n <= 16) return f(NormShape<16 / NK, NK>{});
-    if (n <= 32) return f(NormShape<32, 1>{});
-    if (n <= 64) return f(NormShape<32, 2>{});
-    if (n <= 128) return f(NormShape<64, 2>{});
-    if (n <= 256) return f(NormShape<128, 2>{});
-    if (n <= 512) return f(NormShape<256, 2>{});
-    if (n <= 1024) return f(NormShape<512, 2>{});
-    if (n <= 2048) return f(NormShape<1024, 2>{});
-    return f(NormShape<1024, 4>{});
+    if (n <= 4) return f(NormShape<4, 1, NARROW, WIDE>{});
+    if (n <= 8) return f(NormShape<4, 2, NARROW, WIDE>{});
+    if (n <= 16) return f(NormShape<8, 2, NARROW, WIDE>{});
+    if (n <= 32) return f(NormShape<16, 2, NARROW, WIDE>{});
+    if (n <= 64) return f(NormShape<32, 2, NARROW, WIDE>{});
+    if (n <= 128) return f(NormShape<64, 2, NARROW, WIDE>{});
+    if (n <= 256) return f(NormShape<128, 2, NARROW, WIDE>{});
+    if (n <= 512) return f(NormShape<256, 2, NARROW, WIDE>{});
+    if (n <= 1024) return f(NormShape<512, 2, NARROW, WIDE>{});
+    if (V == 8 || n <= 2048) return f(NormShape<1024, 2, NARROW, WIDE>{});
+    return f(NormShape<1024, 4, NARROW, WIDE>{});
   }
 }
 

@@ -11,132 +11,150 @@
 namespace jattn {
 namespace {
 
-#ifndef BT
-#define BT 768
-#endif
+// Threads of an SM, for which the registers have to leave room, in CTAs of 256 (rows of up to 32 lanes: with 512 the
+// registers spill, 129 us against 103 on norm_back_histories) or 512, whose groups join their sums: with a CTA for each
+// row of 1,024 the partial rows were 10 MB and adding them took a fifth of the call (61 us against 77).
+constexpr int kNarrow = 256, kWide = 512;
 template <typename A, typename S>
-constexpr int kThreads = A::V * S::K <= 8 ? BT : 512;
+constexpr int kThreads = A::V * S::K > 8 || S::L > 32 ? 512 : 768;
 
 template <typename A, typename S>
 __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBlock)) norm_bwd_kernel(NormArgs a) {
   using T = typename A::Type;
-  constexpr int V = A::V, L = S::L, K = S::K, G = S::kGroups;
-  constexpr bool SHIFT = A::SHIFT, KEPT = K * V <= 16;
-  __shared__ float slots[2][kSumWarps<L>][3];
-  __shared__ float joined[G > 1 ? G : 1][G > 1 ? L * K * V + V : 1];
+  constexpr int V = A::V, L = S::L, K = S::K, G = S::kGroups, E = K * V;
+  constexpr bool SHIFT = A::SHIFT, KEPT = E <= 16;
+  extern __shared__ __align__(16) char ring[];
+  __shared__ float slots[G][2][kSumWarps<L>][3];
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
   wait_for_dependency();
-  const int64_t live = live_rows(a.live, a.rows, a.status) * a.heads, total = a.rows * a.heads;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
-  int64_t r = static_cast<int64_t>(blockIdx.x) * G + group;
+  const uint32_t live = static_cast<uint32_t>(live_rows(a.live, a.rows, a.status) * a.heads);
+  const uint32_t total = static_cast<uint32_t>(a.rows * a.heads);
+  const uint32_t step = gridDim.x * G;
+  uint32_t r = blockIdx.x * G + group;
   const T* const x = static_cast<const T*>(a.x.data);
   const T* const dy = static_cast<const T*>(a.dy.data);
   T* const dx = static_cast<T*>(a.y.data);
-  const int before = SHIFT ? shift_of<T, V>(a.x.data, row_at(a.x, a.split, r)) : 0;
-  const int first = lane * V - before;
-  float w[KEPT ? K : 1][V], dw[K][V], db[K][V];
+  const int first = lane * V - (SHIFT ? shift_of<T, V>(a.x.data, row_at(a.x, a.split, r)) : 0);  // column of vector 0
+  float w[KEPT ? E : V], dw[E], db[E];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if constexpr (KEPT) load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, w[k]);
+  for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
+  if constexpr (KEPT)
 #pragma unroll
-    for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.0f;
-  }
-  Raw<T, V> next_x[K], next_dy[K];
+    for (int k = 0; k < K; ++k)
+      load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, k));
+  RowQueue<A, S, 2> queue_x, queue_dy;
+  constexpr int kAhead = decltype(queue_x)::kAhead;
+  char* const ring_dy = ring + queue_x.kBytes;
   float next_m = 0.0f, next_rstd = 0.0f;
-  const auto load = [&](int64_t row) {
-    const T* from_x = x + row_at(a.x, a.split, row);
-    const T* from_dy = dy + row_at(a.dy, a.split, row);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      next_x[k] = load_at<T, V, SHIFT>(from_x, first + k * L * V, a.N);
-      next_dy[k] = load_at<T, V, SHIFT>(from_dy, first + k * L * V, a.N);
+  const auto fetch = [&](uint32_t row, int slot) {
+    if (row < live) {
+      queue_x.fetch(ring, slot, x, x + row_at(a.x, a.split, row), first, a.N);
+      queue_dy.fetch(ring_dy, slot, dy, dy + row_at(a.dy, a.split, row), first, a.N);
     }
+    copies_commit();
+  };
+  const auto fetch_stats = [&](uint32_t row) {
+    if (row >= live) return;
     next_m = a.mean[row];
     next_rstd = a.rstd[row];
   };
-  if (r < live) load(r);
-  int turn = 0;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * G; base < total; base += step, r += step, turn ^= 1) {
-    float d[K][V], g[K][V], s[3] = {0.0f, 0.0f, 0.0f};
+  fetch_stats(r);
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(r + i * step, i);
+  int turn = 0, slot = 0, free_slot = kAhead;
+  for (uint32_t base = blockIdx.x * G; base < total; base += step, r += step, turn ^= 1) {
+    float d[E], g[E], s[3];
     const float m = next_m, rstd = next_rstd;
+    fetch_stats(r + step);
+    if constexpr (kAhead == 0) fetch(r, 0);
+    copies_wait<kAhead == 0 ? 0 : kAhead - 1>();
+    queue_x.take(ring, slot, first, a.N, d);
+    queue_dy.take(ring_dy, slot, first, a.N, g);
+    if constexpr (kAhead > 0) {
+      fetch(r + kAhead * step, free_slot);
+      slot = slot == kAhead ? 0 : slot + 1;
+      free_slot = free_slot == kAhead ? 0 : free_slot + 1;
+    }
+    if constexpr (SHIFT)
+#pragma unroll
+      for (int k = 0; k < K; ++k) clear_outside<T, V, SHIFT>(first + k * L * V, a.N, vector_of<V>(g, k));
+    pairwise<E>([&](int i, int j) { unpair(fadd2(pair(d, i, j), f2(-m, -m)), d, i, j); });
+#pragma unroll
+    for (int k = 0; k < K; ++k) clear_outside<T, V, SHIFT>(first + k * L * V, a.N, vector_of<V>(d, k));
+    uint64_t s0 = f2(0.0f, 0.0f), s1 = s0, s2 = s0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      unpack<T, V>(next_x[k], d[k]);
-      unpack<T, V>(next_dy[k], g[k]);
+      if constexpr (!KEPT)
+        load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, 0));
+      pairwise<V>([&](int i, int j) {
+        const uint64_t dd = pair(vector_of<V>(d, k), i, j);
+        const uint64_t gw = fmul2(pair(vector_of<V>(g, k), i, j), pair(vector_of<V>(w, KEPT ? k : 0), i, j));
+        s0 = fadd2(s0, dd);
+        s1 = fadd2(s1, gw);
+        s2 = ffma2(gw, dd, s2);
+      });
     }
-    if (r + step < live) load(r + step);
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if constexpr (!KEPT) load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, w[0]);
-#pragma unroll
-      for (int i = 0; i < V; ++i) d[k][i] -= m;
-      clear_outside<T, V, SHIFT>(first + k * L * V, a.N, d[k]);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float gw = g[k][i] * w[KEPT ? k : 0][i];
-        s[0] += d[k][i];
-        s[1] += gw;
-        s[2] = fmaf(gw, d[k][i], s[2]);
-      }
-    }
-    row_sum<L, 3>(s, slots[turn]);
+    s[0] = both(s0);
+    s[1] = both(s1);
+    s[2] = both(s2);
+    row_sum<L, 3>(s, slots[group][turn]);
     if (r >= total || (r >= live && !a.zero_behind)) continue;
     T* to = dx + row_at(a.y, a.split, r);
-    const float off = s[0] * a.inv_n, shift = -off * rstd;
-    const float mgh = rstd * fmaf(-off, s[1], s[2]) * a.inv_n;
-    const float mg = -rstd * (s[1] * a.inv_n), mh = -rstd * mgh;
+    if (r >= live) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = first + k * L * V;
-      float out[V];
-      if (r < live) {
-        if constexpr (!KEPT) load_weight<T, V, SHIFT>(a.w, a.wide_weight, c, a.N, 1.0f, w[0]);
+      for (int i = 0; i < E; ++i) d[i] = 0.0f;
+    } else {
+      const float off = s[0] * a.inv_n, t = -off * rstd;
+      const float mgh = rstd * fmaf(-off, s[1], s[2]) * a.inv_n;
+      const float mg = -rstd * (s[1] * a.inv_n), mh = -rstd * mgh;
+      const uint64_t scale = f2(rstd, rstd), shift = f2(t, t), mg2 = f2(mg, mg), mh2 = f2(mh, mh);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float h = fmaf(d[k][i], rstd, shift), gw = g[k][i] * w[KEPT ? k : 0][i];
-          dw[k][i] = fmaf(g[k][i], h, dw[k][i]);
-          db[k][i] += g[k][i];
-          out[i] = fmaf(h, mh, fmaf(gw, rstd, mg));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) out[i] = 0.0f;
+      for (int k = 0; k < K; ++k) {
+        if constexpr (!KEPT)
+          load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, 0));
+        pairwise<V>([&](int i, int j) {
+          const uint64_t gg = pair(vector_of<V>(g, k), i, j);
+          const uint64_t h = ffma2(pair(vector_of<V>(d, k), i, j), scale, shift);
+          const uint64_t gw = fmul2(gg, pair(vector_of<V>(w, KEPT ? k : 0), i, j));
+          unpair(ffma2(gg, h, pair(vector_of<V>(dw, k), i, j)), vector_of<V>(dw, k), i, j);
+          unpair(fadd2(gg, pair(vector_of<V>(db, k), i, j)), vector_of<V>(db, k), i, j);
+          unpair(ffma2(h, mh2, ffma2(gw, scale, mg2)), vector_of<V>(d, k), i, j);
+        });
       }
-      store_at<T, V, SHIFT>(to, c, a.N, out);
     }
+#pragma unroll
+    for (int k = 0; k < K; ++k) store_at<T, V, SHIFT>(to, first + k * L * V, a.N, vector_of<V>(d, k));
   }
   if (a.partial == nullptr) return;
   launch_dependents();
   float* to = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
+  float* joined = reinterpret_cast<float*>(ring);  // [groups][N], where rows have been
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
+    if constexpr (G > 1) __syncthreads();
+    float* own = G > 1 ? joined + group * a.N : to + half * a.N;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = first + k * L * V + i;
+        if (c >= 0 && c < a.N) own[c] = half == 0 ? dw[k * V + i] : db[k * V + i];
+      }
     if constexpr (G > 1) {
-      if (half == 1) __syncthreads();
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int c = first + k * L * V + i;
-          if (c >= 0 && c < a.N) joined[group][c] = half == 0 ? dw[k][i] : db[k][i];
-        }
       __syncthreads();
       for (int c = threadIdx.x; c < a.N; c += S::kBlock) {
         float t = 0.0f;
 #pragma unroll
-        for (int i = 0; i < G; ++i) t += joined[i][c];
+        for (int i = 0; i < G; ++i) t += joined[i * a.N + c];
         to[half * a.N + c] = t;
       }
-    } else {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int c = first + k * L * V + i;
-          if (c >= 0 && c < a.N) to[half * a.N + c] = half == 0 ? dw[k][i] : db[k][i];
-        }
     }
   }
 }
+
+// Dynamic shared memory: the rows on their way, then the groups' sums.
+template <typename A, typename S>
+constexpr int kShared = std::max(2 * RowQueue<A, S, 2>::kBytes, S::kGroups > 1 ? S::kBlock * S::K * A::V * 4 : 0);
 
 // dw and db from the partial rows [parts][2][N]: 32 neighbouring columns a CTA, the parts dealt to its warps in turn.
 constexpr int kJoinWarps = 16;
@@ -148,6 +166,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) norm_join_kernel(NormJoinArgs
   wait_for_dependency();
   float s = 0.0f;
   if (c < 2 * a.N)
+#pragma unroll 8
     for (int p = warp; p < a.parts; p += kJoinWarps) s += a.partial[static_cast<int64_t>(p) * 2 * a.N + c];
   part[warp][lane] = s;
   __syncthreads();
@@ -170,7 +189,7 @@ int norm_bwd_parts(int type, NormPath path, int64_t rows, int N, int sms) {
   int64_t parts = 0;
   with_norm_access(type, path, [&](auto access) {
     using A = decltype(access);
-    return with_norm_shape<A::V>(norm_vectors<A>(N), [&](auto shape) {
+    return with_norm_shape<A::V, kNarrow, kWide>(norm_vectors<A>(N), [&](auto shape) {
       parts = bwd_ctas<A, decltype(shape)>(rows, sms);
       return cudaSuccess;
     });
@@ -181,9 +200,10 @@ int norm_bwd_parts(int type, NormPath path, int64_t rows, int N, int sms) {
 cudaError_t launch_norm_bwd(int type, NormPath path, const NormArgs& a, int sms, cudaStream_t stream) {
   return with_norm_access(type, path, [&](auto access) {
     using A = decltype(access);
-    return with_norm_shape<A::V>(norm_vectors<A>(a.N), [&](auto shape) {
+    return with_norm_shape<A::V, kNarrow, kWide>(norm_vectors<A>(a.N), [&](auto shape) {
       using S = decltype(shape);
-      return launch_early(norm_bwd_kernel<A, S>, a, bwd_ctas<A, S>(a.rows * a.heads, sms), S::kBlock, stream);
+      return launch_early(norm_bwd_kernel<A, S>, a, bwd_ctas<A, S>(a.rows * a.heads, sms), S::kBlock, stream,
+                          kShared<A, S>);
     });
   });
 }

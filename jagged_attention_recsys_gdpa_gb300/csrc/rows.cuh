@@ -70,13 +70,18 @@ struct RotaryTablesArgs {
 
 // A launch that may be set up while the kernel before it ends (kernels call wait_for_dependency first).
 template <typename Args>
-cudaError_t launch_early(void (*kernel)(Args), const Args& a, int64_t ctas, int threads, cudaStream_t stream) {
+cudaError_t launch_early(void (*kernel)(Args), const Args& a, int64_t ctas, int threads, cudaStream_t stream, int shared = 0) {
+  if (shared > 16 << 10) {  // with what the kernel declares itself it may pass what a launch gets unasked
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(static_cast<unsigned>(ctas));
   c.blockDim = dim3(static_cast<unsigned>(threads));
+  c.dynamicSmemBytes = static_cast<size_t>(shared);
   c.stream = stream;
   c.attrs = &early;
   c.numAttrs = 1;
