@@ -446,6 +446,9 @@ typedef struct {
   int weight_type;    /* of weight, bias and their gradients: `type` or JATTN_F32 */
   float eps;          /* > 0 and finite (forward only) */
   int zero_behind;    /* 0 / 1 */
+  int64_t x_row_stride, x_head_stride;
+  int64_t y_row_stride, y_head_stride;   /* of y (forward) or dx (backward) */
+  int64_t dy_row_stride, dy_head_stride; /* backward only */
 } jattn_norm_t;
 
 /* Layer norm of every row: with m = mean(x) and v = mean((x - m)^2),
@@ -455,9 +458,8 @@ typedef struct {
  * in fp32 about the row's mean, and y is rounded once. y may be x itself (the same
  * pointer and strides); any other overlap of an output is refused
  * (JATTN_ERR_INVALID). */
-int jattn_layer_norm(const jattn_norm_t* p, const int64_t* live_rows, const void* x, int64_t x_row_stride,
-                     int64_t x_head_stride, const void* weight, const void* bias, void* y, int64_t y_row_stride,
-                     int64_t y_head_stride, float* mean, float* rstd, void* workspace, size_t workspace_bytes,
+int jattn_layer_norm(const jattn_norm_t* p, const int64_t* live_rows, const void* x, const void* weight,
+                     const void* bias, void* y, float* mean, float* rstd, void* workspace, size_t workspace_bytes,
                      void* stream);
 
 /* Its backward: with g = dy weight, h = (x - mean) rstd (the forward's statistics),
@@ -470,11 +472,10 @@ int jattn_layer_norm(const jattn_norm_t* p, const int64_t* live_rows, const void
  * one each. The size depends on rows, heads, N and type, and is asked for with the
  * device current that the call runs on. Without rows dweight and dbias are zero. */
 int jattn_layer_norm_bwd_scratch_size(const jattn_norm_t* p, size_t* bytes);
-int jattn_layer_norm_bwd(const jattn_norm_t* p, const int64_t* live_rows, const void* dy, int64_t dy_row_stride,
-                         int64_t dy_head_stride, const void* x, int64_t x_row_stride, int64_t x_head_stride,
-                         const void* weight, const float* mean, const float* rstd, void* dx, int64_t dx_row_stride,
-                         int64_t dx_head_stride, void* dweight, void* dbias, void* scratch, size_t scratch_bytes,
-                         void* workspace, size_t workspace_bytes, void* stream);
+int jattn_layer_norm_bwd(const jattn_norm_t* p, const int64_t* live_rows, const void* dy, const void* x,
+                         const void* weight, const float* mean, const float* rstd, void* dx, void* dweight,
+                         void* dbias, void* scratch, size_t scratch_bytes, void* workspace, size_t workspace_bytes,
+                         void* stream);
 
 /* Rotary positions of rows in either layout, for all columns of a head or its
  * first ones. With R = 2 * half <= D, c and s row pos of the tables
@@ -505,11 +506,13 @@ typedef struct {
   int layout;         /* JATTN_ROTARY_* */
   int inverse;        /* 0 / 1 */
   int zero_behind;    /* 0 / 1 */
+  int64_t table_rows; /* 1 .. 2^31 - 1 */
+  int64_t x_row_stride, x_head_stride;
+  int64_t y_row_stride, y_head_stride;
 } jattn_rotary_t;
 
 int jattn_rotary(const jattn_rotary_t* p, const int64_t* off, const int64_t* start, const float* cos, const float* sin,
-                 int64_t table_rows, const void* x, int64_t x_row_stride, int64_t x_head_stride, void* y,
-                 int64_t y_row_stride, int64_t y_head_stride, void* workspace, size_t workspace_bytes, void* stream);
+                 const void* x, void* y, void* workspace, size_t workspace_bytes, void* stream);
 
 /* The tables: cos and sin (fp32 [rows, half], 4-byte aligned) of amplitude * (pos *
  * theta_m) for pos = first .. first + rows - 1 and m < half, R = 2 * half.
@@ -570,8 +573,10 @@ int jattn_rotary_tables(const jattn_rotary_tables_t* p, float* cos, float* sin, 
  * back once, by the caller's care.
  *
  * page_size: a power of two from 1 to 4096; max_pages * page_size < 2^31. scratch:
- * jattn_page_scratch_size bytes, 256-byte aligned, of any content, one per call that
- * may run at the same time. workspace as for the paged cache. Buffers must not overlap. */
+ * jattn_page_scratch_size bytes (total: the rows of jattn_page_assign, -1 for
+ * jattn_page_release; 0 bytes, and NULL, for small calls), 256-byte aligned, of any content, one
+ * per call that may run at the same time. workspace as for the paged cache. Buffers
+ * must not overlap. */
 typedef struct {
   int64_t n_pages;    /* 1 .. 2^31 - 1 */
   int page_size;
@@ -579,7 +584,7 @@ typedef struct {
   int64_t* count;
 } jattn_page_pool_t;
 
-int jattn_page_scratch_size(int64_t B, size_t* bytes);
+int jattn_page_scratch_size(int64_t B, int64_t total, int64_t max_pages, size_t* bytes);
 int jattn_page_assign(const jattn_page_pool_t* pool, int64_t B, int64_t total, const int64_t* off, const int64_t* start,
                       int32_t* page_table, int64_t max_pages, int64_t* slots, void* scratch, size_t scratch_bytes,
                       void* workspace, size_t workspace_bytes, void* stream);

@@ -96,6 +96,9 @@ class Norm(ctypes.Structure):
         ("weight_type", ctypes.c_int),
         ("eps", ctypes.c_float),
         ("zero_behind", ctypes.c_int),
+        ("x_strides", ctypes.c_int64 * 2),
+        ("y_strides", ctypes.c_int64 * 2),
+        ("dy_strides", ctypes.c_int64 * 2),
     ]
 
 
@@ -110,6 +113,9 @@ class Rotary(ctypes.Structure):
         ("layout", ctypes.c_int),
         ("inverse", ctypes.c_int),
         ("zero_behind", ctypes.c_int),
+        ("table_rows", ctypes.c_int64),
+        ("x_strides", ctypes.c_int64 * 2),
+        ("y_strides", ctypes.c_int64 * 2),
     ]
 
 
@@ -198,19 +204,18 @@ def load(path: str | None = None):
     lib.jattn_decode.argtypes = [P, C, vp, vp, vp, i64, vp, vp, vp, vp, ctypes.c_size_t, vp, ctypes.c_size_t, vp]
     lib.jattn_decode.restype = i32
     N, Z = ctypes.POINTER(Norm), ctypes.c_size_t
-    lib.jattn_layer_norm.argtypes = [N, vp, vp, i64, i64, vp, vp, vp, i64, i64, vp, vp, vp, Z, vp]
+    lib.jattn_layer_norm.argtypes = [N] + [vp] * 8 + [Z, vp]
     lib.jattn_layer_norm.restype = i32
     lib.jattn_layer_norm_bwd_scratch_size.argtypes = [N, ctypes.POINTER(Z)]
     lib.jattn_layer_norm_bwd_scratch_size.restype = i32
-    lib.jattn_layer_norm_bwd.argtypes = [N, vp] + [vp, i64, i64] * 2 + [vp] * 3 + [vp, i64, i64] + [vp] * 3 + \
-        [Z, vp, Z, vp]
+    lib.jattn_layer_norm_bwd.argtypes = [N] + [vp] * 10 + [Z, vp, Z, vp]
     lib.jattn_layer_norm_bwd.restype = i32
-    lib.jattn_rotary.argtypes = [ctypes.POINTER(Rotary)] + [vp] * 4 + [i64] + [vp, i64, i64] * 2 + [vp, Z, vp]
+    lib.jattn_rotary.argtypes = [ctypes.POINTER(Rotary)] + [vp] * 7 + [Z, vp]
     lib.jattn_rotary.restype = i32
     lib.jattn_rotary_tables.argtypes = [ctypes.POINTER(RotaryTables), vp, vp, vp]
     lib.jattn_rotary_tables.restype = i32
     G = ctypes.POINTER(PagePool)
-    lib.jattn_page_scratch_size.argtypes = [i64, ctypes.POINTER(Z)]
+    lib.jattn_page_scratch_size.argtypes = [i64, i64, i64, ctypes.POINTER(Z)]
     lib.jattn_page_scratch_size.restype = i32
     lib.jattn_page_assign.argtypes = [G, i64, i64, vp, vp, vp, i64, vp, vp, Z, vp, Z, vp]
     lib.jattn_page_assign.restype = i32
@@ -360,60 +365,30 @@ def decode(p, c, q_off, kv_lens, page_table, q, o, lse, scratch: int, scratch_by
         check(rc, "jattn_decode")
 
 
-# A row tensor is passed as (address, row stride, head stride), strides in elements.
-def layer_norm(p, live: int | None, x, weight, bias, y, mean, rstd, ws: int, ws_bytes: int, stream: int):
-    rc = (_lib or load()).jattn_layer_norm(p, live, *x, ptr(weight), ptr(bias), *y, ptr(mean), ptr(rstd), ws, ws_bytes,
-                                           stream)
-    if rc:
-        check(rc, "jattn_layer_norm")
-
-
 def layer_norm_bwd_scratch_size(p) -> int:
     n = ctypes.c_size_t(0)
     check((_lib or load()).jattn_layer_norm_bwd_scratch_size(p, ctypes.byref(n)), "jattn_layer_norm_bwd_scratch_size")
     return n.value
 
 
-def layer_norm_bwd(p, live: int | None, dy, x, weight, mean, rstd, dx, dweight, dbias, scratch, scratch_bytes: int,
-                   ws: int, ws_bytes: int, stream: int):
-    rc = (_lib or load()).jattn_layer_norm_bwd(p, live, *dy, *x, ptr(weight), mean.data_ptr(), rstd.data_ptr(), *dx,
-                                               ptr(dweight), ptr(dbias), ptr(scratch), scratch_bytes, ws, ws_bytes,
-                                               stream)
-    if rc:
-        check(rc, "jattn_layer_norm_bwd")
-
-
-def rotary(p, off, start, cos, sin, x, y, ws: int, ws_bytes: int, stream: int):
-    rc = (_lib or load()).jattn_rotary(p, ptr(off), ptr(start), cos.data_ptr(), sin.data_ptr(), cos.shape[0], *x, *y, ws,
-                                       ws_bytes, stream)
-    if rc:
-        check(rc, "jattn_rotary")
-
-
-def rotary_tables(p, cos, sin, stream: int):
-    rc = (_lib or load()).jattn_rotary_tables(p, cos.data_ptr(), sin.data_ptr(), stream)
-    if rc:
-        check(rc, "jattn_rotary_tables")
-
-
-def page_scratch_size(B: int) -> int:
+def page_scratch_size(B: int, total: int, max_pages: int) -> int:
     n = ctypes.c_size_t(0)
-    check((_lib or load()).jattn_page_scratch_size(B, ctypes.byref(n)), "jattn_page_scratch_size")
+    check((_lib or load()).jattn_page_scratch_size(B, total, max_pages, ctypes.byref(n)), "jattn_page_scratch_size")
     return n.value
 
 
-def page_assign(pool, B: int, total: int, off, start, page_table, slots, scratch, scratch_bytes: int, ws: int,
-                ws_bytes: int, stream: int):
-    rc = (_lib or load()).jattn_page_assign(pool, B, total, ptr(off), start.data_ptr(), page_table.data_ptr(),
-                                            page_table.shape[1], ptr(slots), scratch.data_ptr(), scratch_bytes, ws,
-                                            ws_bytes, stream)
+def page_assign(pool, B: int, total: int, off, start, page_table, max_pages: int, slots, scratch, scratch_bytes: int,
+                ws: int, ws_bytes: int, stream: int):
+    rc = (_lib or load()).jattn_page_assign(pool, B, total, off, start, page_table, max_pages, slots, scratch,
+                                            scratch_bytes, ws, ws_bytes, stream)
     if rc:
         check(rc, "jattn_page_assign")
 
 
-def page_release(pool, B: int, lens, keep, page_table, scratch, scratch_bytes: int, ws: int, ws_bytes: int, stream: int):
-    rc = (_lib or load()).jattn_page_release(pool, B, lens.data_ptr(), ptr(keep), page_table.data_ptr(),
-                                             page_table.shape[1], scratch.data_ptr(), scratch_bytes, ws, ws_bytes, stream)
+def page_release(pool, B: int, lens, keep, page_table, max_pages: int, scratch, scratch_bytes: int, ws: int,
+                 ws_bytes: int, stream: int):
+    rc = (_lib or load()).jattn_page_release(pool, B, lens, keep, page_table, max_pages, scratch, scratch_bytes, ws,
+                                             ws_bytes, stream)
     if rc:
         check(rc, "jattn_page_release")
 

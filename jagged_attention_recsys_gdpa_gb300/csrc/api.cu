@@ -1211,13 +1211,12 @@ NormArgs norm_args(const jattn_norm_t& p, const int64_t* live, const RowTensor& 
 }  // namespace
 }  // namespace jattn
 
-int jattn_layer_norm(const jattn_norm_t* p, const int64_t* live_rows, const void* xp, int64_t x_row, int64_t x_head,
-                     const void* weight, const void* bias, void* yp, int64_t y_row, int64_t y_head, float* mean,
-                     float* rstd, void* ws, size_t ws_bytes, void* stream) {
+int jattn_layer_norm(const jattn_norm_t* p, const int64_t* live_rows, const void* xp, const void* weight,
+                     const void* bias, void* yp, float* mean, float* rstd, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_norm(p);
   if (rc != JATTN_OK) return rc;
   if (!(p->eps > 0.0f) || !std::isfinite(p->eps)) return JATTN_ERR_INVALID;
-  const RowTensor x{xp, x_row, x_head}, y{yp, y_row, y_head};
+  const RowTensor x{xp, p->x_row_stride, p->x_head_stride}, y{yp, p->y_row_stride, p->y_head_stride};
   if ((p->rows > 0 && (!xp || !yp)) || (bias && !weight) || !mean != !rstd) return JATTN_ERR_INVALID;
   if (bad_strides(x) || bad_strides(y) || rows_overlap(y, p->rows, p->heads, p->N)) return JATTN_ERR_INVALID;
   const int size = type_bytes(p->type), wsize = type_bytes(p->weight_type);
@@ -1257,14 +1256,13 @@ int jattn_layer_norm_bwd_scratch_size(const jattn_norm_t* p, size_t* bytes) {
   return JATTN_OK;
 }
 
-int jattn_layer_norm_bwd(const jattn_norm_t* p, const int64_t* live_rows, const void* dyp, int64_t dy_row,
-                         int64_t dy_head, const void* xp, int64_t x_row, int64_t x_head, const void* weight,
-                         const float* mean, const float* rstd, void* dxp, int64_t dx_row, int64_t dx_head,
-                         void* dweight, void* dbias, void* scratch, size_t scratch_bytes, void* ws, size_t ws_bytes,
-                         void* stream) {
+int jattn_layer_norm_bwd(const jattn_norm_t* p, const int64_t* live_rows, const void* dyp, const void* xp,
+                         const void* weight, const float* mean, const float* rstd, void* dxp, void* dweight,
+                         void* dbias, void* scratch, size_t scratch_bytes, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_norm(p);
   if (rc != JATTN_OK) return rc;
-  const RowTensor x{xp, x_row, x_head}, dy{dyp, dy_row, dy_head}, dx{dxp, dx_row, dx_head};
+  const RowTensor x{xp, p->x_row_stride, p->x_head_stride}, dy{dyp, p->dy_row_stride, p->dy_head_stride},
+      dx{dxp, p->y_row_stride, p->y_head_stride};
   if (p->rows > 0 && (!xp || !dyp || !dxp || !mean || !rstd)) return JATTN_ERR_INVALID;
   if ((dweight && !weight) || (dbias && !dweight)) return JATTN_ERR_INVALID;
   if (bad_strides(x) || bad_strides(dy) || bad_strides(dx) || rows_overlap(dx, p->rows, p->heads, p->N))
@@ -1310,8 +1308,7 @@ int jattn_layer_norm_bwd(const jattn_norm_t* p, const int64_t* live_rows, const 
 }
 
 int jattn_rotary(const jattn_rotary_t* p, const int64_t* off, const int64_t* start, const float* cos, const float* sin,
-                 int64_t table_rows, const void* xp, int64_t x_row, int64_t x_head, void* yp, int64_t y_row,
-                 int64_t y_head, void* ws, size_t ws_bytes, void* stream) {
+                 const void* xp, void* yp, void* ws, size_t ws_bytes, void* stream) {
   if (!p || p->total < 0 || p->total > INT32_MAX || p->heads < 1 || p->D < 2 || p->D > kMaxRow) return JATTN_ERR_INVALID;
   if (p->half < 1 || p->half > p->D / 2 || !known_type(p->type)) return JATTN_ERR_INVALID;
   if (off ? p->B < 1 || p->B > INT32_MAX : p->B != p->total) return JATTN_ERR_INVALID;
@@ -1319,8 +1316,8 @@ int jattn_rotary(const jattn_rotary_t* p, const int64_t* off, const int64_t* sta
   if ((p->layout != JATTN_ROTARY_INTERLEAVED && p->layout != JATTN_ROTARY_HALF) || (p->inverse != 0 && p->inverse != 1) ||
       (p->zero_behind != 0 && p->zero_behind != 1))
     return JATTN_ERR_INVALID;
-  if (!cos || !sin || table_rows < 1 || table_rows > INT32_MAX) return JATTN_ERR_INVALID;
-  const RowTensor x{xp, x_row, x_head}, y{yp, y_row, y_head};
+  if (!cos || !sin || p->table_rows < 1 || p->table_rows > INT32_MAX) return JATTN_ERR_INVALID;
+  const RowTensor x{xp, p->x_row_stride, p->x_head_stride}, y{yp, p->y_row_stride, p->y_head_stride};
   if ((p->total > 0 && (!xp || !yp)) || bad_strides(x) || bad_strides(y) || rows_overlap(y, p->total, p->heads, p->D))
     return JATTN_ERR_INVALID;
   const int size = type_bytes(p->type);
@@ -1328,7 +1325,7 @@ int jattn_rotary(const jattn_rotary_t* p, const int64_t* off, const int64_t* sta
   int rc = check_status_ws(ws, ws_bytes);
   if (rc != JATTN_OK) return rc;
   const Piece in = piece(x, p->total, p->heads, p->D, size), out = piece(y, p->total, p->heads, p->D, size);
-  const int64_t table = table_rows * p->half * 4;
+  const int64_t table = p->table_rows * p->half * 4;
   if ((meet(out, in) && !same_place(x, y)) ||
       meet_any(out, {Piece{cos, table}, Piece{sin, table}, Piece{off, (p->B + 1) * 8}, Piece{start, p->B * 8}}))
     return JATTN_ERR_INVALID;
@@ -1337,26 +1334,34 @@ int jattn_rotary(const jattn_rotary_t* p, const int64_t* off, const int64_t* sta
   clear_stale_error();
   if (p->total == 0) return JATTN_OK;
   RotaryArgs a{};
-  a.x = RowsIn{xp, x_row, x_head};
-  a.y = RowsOut{yp, y_row, y_head};
+  a.x = RowsIn{xp, x.row, x.head};
+  a.y = RowsOut{yp, y.row, y.head};
   a.off = off;
   a.start = start;
   a.cos_t = cos;
   a.sin_t = sin;
   a.B = p->B;
   a.total = p->total;
-  a.table_rows = table_rows;
+  a.table_rows = p->table_rows;
   a.heads = p->heads;
   a.D = p->D;
   a.half = p->half;
   a.inverse = p->inverse != 0;
   a.zero_behind = p->zero_behind != 0;
   a.status = static_cast<DevStatus*>(ws);
-  // units of whole vectors: the pairs' and the copied columns'
-  const bool vectors = in_vectors(x, p->total, p->heads, p->D, size) && in_vectors(y, p->total, p->heads, p->D, size) &&
-                       p->half * size % 16 == 0 && aligned16(cos) && aligned16(sin);
-  const cudaError_t e = launch_rotary(p->type, vectors, p->layout == JATTN_ROTARY_HALF, a, dev.sms,
-                                      static_cast<cudaStream_t>(stream));
+  // Vectors of 16 bytes: of the half layout a head's halves (and its table rows) have to be whole ones. Else two values at
+  // a time (fp32 in the half layout gains nothing by that).
+  const bool half_layout = p->layout == JATTN_ROTARY_HALF;
+  const bool aligned = in_vectors(x, p->total, p->heads, p->D, size) && in_vectors(y, p->total, p->heads, p->D, size);
+  a.vector_tables = p->half * 4 % 16 == 0 && aligned16(cos) && aligned16(sin);
+  if (!half_layout) a.vector_tables = a.vector_tables && p->half % (8 / size) == 0;
+  const auto even = [&](const RowTensor& t) {
+    return reinterpret_cast<uintptr_t>(t.p) % (2 * size) == 0 && t.row % 2 == 0 && t.head % 2 == 0;
+  };
+  RotaryPath path = RotaryPath::kValues;
+  if (aligned && (!half_layout || (p->half * size % 16 == 0 && a.vector_tables))) path = RotaryPath::kVectors;
+  else if (even(x) && even(y) && p->D % 2 == 0 && (!half_layout || p->half % 2 == 0)) path = RotaryPath::kPairs;
+  const cudaError_t e = launch_rotary(p->type, path, half_layout, a, dev.sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? JATTN_OK : cuda_fail("rotary positions launch", e);
 }
 
@@ -1385,7 +1390,7 @@ int jattn_rotary_tables(const jattn_rotary_tables_t* p, float* cos, float* sin, 
   const double R = 2.0 * p->half;
   const double base = p->scaling == JATTN_SCALE_NTK ? p->base * std::pow(p->factor, R / (R - 2.0)) : p->base;
   if (!std::isfinite(base)) return JATTN_ERR_INVALID;
-  RotaryTablesArgs a;
+  RotaryTablesArgs<512> a;
   for (int m = 0; m < p->half; ++m) {
     double theta = std::pow(base, -2.0 * m / R);
     if (p->scaling == JATTN_SCALE_LINEAR) theta /= p->factor;
@@ -1407,9 +1412,10 @@ int jattn_rotary_tables(const jattn_rotary_tables_t* p, float* cos, float* sin, 
   return e == cudaSuccess ? JATTN_OK : cuda_fail("rotary tables launch", e);
 }
 
-int jattn_page_scratch_size(int64_t B, size_t* bytes) {
-  if (!bytes || B < 1 || B > INT32_MAX) return JATTN_ERR_INVALID;
-  *bytes = al256(page_scratch_bytes(B));
+int jattn_page_scratch_size(int64_t B, int64_t total, int64_t max_pages, size_t* bytes) {
+  if (!bytes || B < 1 || B > INT32_MAX || total < -1 || total > INT32_MAX || max_pages < 1 || max_pages > INT32_MAX)
+    return JATTN_ERR_INVALID;
+  *bytes = al256(page_scratch_bytes(B, total, max_pages));
   return JATTN_OK;
 }
 
@@ -1417,8 +1423,8 @@ namespace jattn {
 namespace {
 
 // What assigning and giving back check alike; index: what the call reads of 64-bit numbers besides.
-int check_pool(const jattn_page_pool_t* pool, int64_t B, std::initializer_list<Piece> index, int32_t* table,
-               int64_t max_pages, void* scratch, size_t scratch_bytes, void* ws, size_t ws_bytes) {
+int check_pool(const jattn_page_pool_t* pool, int64_t B, int64_t total, std::initializer_list<Piece> index,
+               int32_t* table, int64_t max_pages, void* scratch, size_t scratch_bytes, void* ws, size_t ws_bytes) {
   if (!pool || pool->n_pages < 1 || pool->n_pages > INT32_MAX || !pool->free_pages || !pool->count) return JATTN_ERR_INVALID;
   const int ps = pool->page_size;
   if (ps < 1 || ps > 4096 || (ps & (ps - 1))) return JATTN_ERR_INVALID;
@@ -1429,8 +1435,9 @@ int check_pool(const jattn_page_pool_t* pool, int64_t B, std::initializer_list<P
   const int rc = check_status_ws(ws, ws_bytes);
   if (rc != JATTN_OK) return rc;
   size_t need = 0;
-  (void)jattn_page_scratch_size(B, &need);
-  if (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) || scratch_bytes < need) return JATTN_ERR_WORKSPACE;
+  (void)jattn_page_scratch_size(B, total, max_pages, &need);
+  if (need > 0 && (!scratch || (reinterpret_cast<uintptr_t>(scratch) & 255u) || scratch_bytes < need))
+    return JATTN_ERR_WORKSPACE;
   const Piece f{pool->free_pages, pool->n_pages * 4}, c{pool->count, 8}, t{table, B * max_pages * 4},
       s{scratch, static_cast<int64_t>(need)};
   if (meet(f, c) || meet(f, t) || meet(f, s) || meet(c, t) || meet(c, s) || meet(t, s)) return JATTN_ERR_INVALID;
@@ -1462,7 +1469,7 @@ int jattn_page_assign(const jattn_page_pool_t* pool, int64_t B, int64_t total, c
                       void* ws, size_t ws_bytes, void* stream) {
   if (!start || total < 0 || total > INT32_MAX || (!off && total != B)) return JATTN_ERR_INVALID;
   const Piece o{off, (B + 1) * 8}, st{start, B * 8}, sl{slots, total * 8};
-  int rc = check_pool(pool, B, {o, st, sl}, page_table, max_pages, scratch, scratch_bytes, ws, ws_bytes);
+  int rc = check_pool(pool, B, total, {o, st, sl}, page_table, max_pages, scratch, scratch_bytes, ws, ws_bytes);
   if (rc != JATTN_OK) return rc;
   if (meet(sl, o) || meet(sl, st)) return JATTN_ERR_INVALID;
   DeviceInfo dev;
@@ -1482,7 +1489,7 @@ int jattn_page_release(const jattn_page_pool_t* pool, int64_t B, const int64_t* 
                        size_t ws_bytes, void* stream) {
   if (!lens) return JATTN_ERR_INVALID;
   const Piece l{lens, B * 8}, k{keep, B * 8};
-  int rc = check_pool(pool, B, {l, k}, page_table, max_pages, scratch, scratch_bytes, ws, ws_bytes);
+  int rc = check_pool(pool, B, -1, {l, k}, page_table, max_pages, scratch, scratch_bytes, ws, ws_bytes);
   if (rc != JATTN_OK) return rc;
   DeviceInfo dev;
   if ((rc = device_info(dev)) != JATTN_OK) return rc;

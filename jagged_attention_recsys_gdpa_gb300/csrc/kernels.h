@@ -15,6 +15,7 @@ struct DevStatus;
 struct NormArgs;
 struct NormJoinArgs;
 struct RotaryArgs;
+template <int PAIRS>
 struct RotaryTablesArgs;
 struct PageArgs;
 
@@ -140,12 +141,14 @@ int norm_bwd_parts(int type, NormPath path, int64_t rows, int N, int sms);
 cudaError_t launch_norm_bwd(int type, NormPath path, const NormArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_norm_join(int weight_type, const NormJoinArgs& a, cudaStream_t stream);
 
-// Rotary positions of rows and their tables (rotary.cu); `vectors`: everything is aligned to 16 bytes.
-cudaError_t launch_rotary(int type, bool vectors, bool half_layout, const RotaryArgs& a, int sms, cudaStream_t stream);
-cudaError_t launch_rotary_tables(const RotaryTablesArgs& a, bool vectors, int sms, cudaStream_t stream);
+// Rotary positions of rows (rotary.cu), read in vectors of 16 bytes, two values at a time or one by one, and their tables
+// (`vectors`: in 16 bytes).
+enum class RotaryPath { kVectors, kPairs, kValues };
+cudaError_t launch_rotary(int type, RotaryPath path, bool half_layout, const RotaryArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_rotary_tables(const RotaryTablesArgs<512>& a, bool vectors, int sms, cudaStream_t stream);
 
-// Page pool (pages.cu).
-size_t page_scratch_bytes(int64_t B);
+// Page pool (pages.cu); total: an assign's rows, -1 for a release.
+size_t page_scratch_bytes(int64_t B, int64_t total, int64_t max_pages);
 cudaError_t launch_page_assign(const PageArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_page_release(const PageArgs& a, int sms, cudaStream_t stream);
 

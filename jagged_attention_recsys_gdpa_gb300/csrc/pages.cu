@@ -2,9 +2,9 @@
 //
 // Whole numbers throughout, so each order is fixed: the i-th page that a call wants, sequence by sequence, is the i-th
 // from the top of the stack of free pages, and the i-th that it gives back becomes the i-th from the top. One CTA adds
-// the sequences' counts up (and moves the pool's height); then every page and every row finds its sequence by
-// bisection and needs nothing from the others. Small calls do both in that CTA, with one launch: they are bound by
-// latency. Large ones are bound by the slots' stores, 8 bytes a row.
+// the sequences' counts up (and moves the pool's height); then every page finds its sequence by bisection, needs nothing
+// from the others, and gives its rows their slots, which are consecutive numbers. Small calls do both in that CTA, with one
+// launch: they are bound by latency. Large ones are bound by the slots' stores, 8 bytes a row.
 #include <algorithm>
 #include <cstdint>
 
@@ -18,19 +18,24 @@ namespace {
 
 constexpr int kPlanBlock = 1024;
 constexpr int kFillBlock = 256;
-constexpr int kFillRows = 8;  // rows of a thread of the large calls
+constexpr int kFillRows = 8192;  // rows of a CTA of the large calls, about
 
 // What the counts' sum leaves in scratch for the pages and rows: the prefix sums follow it.
 struct Plan {
   int64_t top;    // height of the stack that pages are taken from, or that the pages given back reach
   int64_t pages;  // pages that move; 0 where the call is refused
-  int64_t ok;
+  int64_t units;  // assign: pages that hold new rows (or, of a sequence that is skipped, would)
+  int32_t ok;
+  int32_t prefix; // assign: the offsets are prefix sums
 };
 constexpr int64_t kPlanBytes = 256;
 __device__ __forceinline__ Plan* plan_of(const PageArgs& a) { return static_cast<Plan*>(a.scratch); }
 __device__ __forceinline__ int64_t* first_of(const PageArgs& a) {
   return reinterpret_cast<int64_t*>(static_cast<char*>(a.scratch) + kPlanBytes);
 }
+
+// Prefix sums of the sequences' units.
+__device__ __forceinline__ int64_t* units_of(const PageArgs& a) { return first_of(a) + a.B; }
 
 __device__ __forceinline__ int64_t pages_for(const PageArgs& a, int64_t rows) {
   return (rows + a.page_size - 1) >> a.page_shift;
@@ -127,13 +132,14 @@ __device__ __forceinline__ int64_t slot_of(const PageArgs& a, const int64_t* fir
   return (static_cast<int64_t>(page) << a.page_shift) + (pos & (a.page_size - 1));
 }
 
-__device__ __forceinline__ int64_t row_slot(const PageArgs& a, const int64_t* first, const Plan& plan, int64_t low,
-                                            int64_t high, int64_t r) {
+// off: a.off or a copy of it.
+__device__ __forceinline__ int64_t row_slot(const PageArgs& a, const int64_t* first, const int64_t* off, const Plan& plan,
+                                            int64_t r) {
   if (!plan.ok) return -1;
-  if (a.off == nullptr) return slot_of(a, first, plan.top, r, r);
-  if (r >= a.off[a.B]) return -1;
-  const int64_t b = bisect(a.off, low, high, r);
-  return r < a.off[b + 1] ? slot_of(a, first, plan.top, b, r) : -1;
+  if (off == nullptr) return slot_of(a, first, plan.top, r, r);
+  if (r >= off[a.B]) return -1;
+  const int64_t b = bisect(off, 0, a.B - 1, r);
+  return r < off[b + 1] ? slot_of(a, first, plan.top, b, r) : -1;
 }
 
 __global__ void __launch_bounds__(kFillBlock) page_count_kernel(PageArgs a) {
@@ -149,12 +155,18 @@ __global__ void __launch_bounds__(kFillBlock) page_count_kernel(PageArgs a) {
 // Adds the counts up. SMALL: counts the pages of a release itself, and moves pages and fills slots.
 template <bool RELEASE, bool SMALL>
 __global__ void __launch_bounds__(kPlanBlock) page_plan_kernel(PageArgs a) {
-  __shared__ int64_t warp_sum[32];
-  __shared__ int64_t own[SMALL ? kPlanBlock + 1 : 1];
+  constexpr bool UNITS = !RELEASE && !SMALL;
+  __shared__ int64_t warp_sum[2][32];
+  __shared__ int64_t own[SMALL ? kPlanBlock : 1], own_off[SMALL && !RELEASE ? kPlanBlock + 1 : 1];
   __shared__ Plan plan;
+  __shared__ int bad;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   int64_t* first = SMALL ? own : first_of(a);
   wait_for_dependency();
+  if (threadIdx.x == 0) bad = 0;
+  if constexpr (SMALL && !RELEASE)
+    if (a.off != nullptr)
+      for (int64_t b = threadIdx.x; b <= a.B; b += kPlanBlock) own_off[b] = a.off[b];
   if constexpr (SMALL && RELEASE) {
     for (int64_t b = warp; b < a.B; b += kPlanBlock / 32) {
       const int64_t n = pages_back(a, b, lane);
@@ -162,36 +174,59 @@ __global__ void __launch_bounds__(kPlanBlock) page_plan_kernel(PageArgs a) {
     }
     __syncthreads();
   }
-  int64_t total = 0;
+  __syncthreads();
+  int64_t total = 0, total_units = 0;
   for (int64_t base = 0; base < a.B; base += kPlanBlock) {
     const int64_t b = base + threadIdx.x;
-    int64_t n = 0;
+    int64_t n = 0, units = 0;
     if (b < a.B) {
       if constexpr (RELEASE) {
         n = first[b];
       } else {
         Span e;
-        span_of<false>(a, b, e);
+        const bool taken = span_of<false>(a, b, e);
         n = max(e.high - e.low, int64_t(0));
+        if constexpr (UNITS)
+          if (a.off != nullptr) {
+            const int64_t from = a.off[b], rows = a.off[b + 1] - from;
+            if (from < 0 || rows < 0 || rows > a.total - from || (b == 0 && from != 0)) bad = 1;
+            else units = taken ? (rows > 0 ? e.high - (a.start[b] >> a.page_shift) : 0) : pages_for(a, rows);
+          }
       }
     }
-    int64_t sum = n;
+    int64_t sum = n, sum_units = units;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
       const int64_t below = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += below;
+      const int64_t below_units = UNITS ? __shfl_up_sync(0xffffffffu, sum_units, d) : 0;
+      if (lane >= d) {
+        sum += below;
+        sum_units += below_units;
+      }
     }
-    if (lane == 31) warp_sum[warp] = sum;
+    if (lane == 31) {
+      warp_sum[0][warp] = sum;
+      warp_sum[1][warp] = sum_units;
+    }
     __syncthreads();
-    int64_t s = warp_sum[lane];
+    int64_t s = warp_sum[0][lane], su = warp_sum[1][lane];
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
       const int64_t below = __shfl_up_sync(0xffffffffu, s, d);
-      if (lane >= d) s += below;
+      const int64_t below_units = UNITS ? __shfl_up_sync(0xffffffffu, su, d) : 0;
+      if (lane >= d) {
+        s += below;
+        su += below_units;
+      }
     }
     const int64_t before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
-    if (b < a.B) first[b] = total + (warp > 0 ? before : 0) + sum - n;
+    const int64_t before_units = __shfl_sync(0xffffffffu, su, max(warp - 1, 0));
+    if (b < a.B) {
+      first[b] = total + (warp > 0 ? before : 0) + sum - n;
+      if constexpr (UNITS) units_of(a)[b] = total_units + (warp > 0 ? before_units : 0) + sum_units - units;
+    }
     total += __shfl_sync(0xffffffffu, s, 31);
+    total_units += __shfl_sync(0xffffffffu, su, 31);
     __syncthreads();
   }
   if (threadIdx.x == 0) {
@@ -200,6 +235,8 @@ __global__ void __launch_bounds__(kPlanBlock) page_plan_kernel(PageArgs a) {
     p.ok = height >= 0 && height <= a.n_pages && (RELEASE ? total <= a.n_pages - height : total <= height);
     if (!p.ok) record_error(a.status, JATTN_ERR_POOL, 95, 0);
     p.pages = p.ok ? total : 0;
+    p.units = total_units;
+    p.prefix = UNITS && a.off != nullptr && !bad && a.off[a.B] <= a.total;
     p.top = RELEASE ? height + total : height;
     if (p.pages > 0) *a.count = RELEASE ? height + total : height - total;
     if constexpr (SMALL) plan = p;
@@ -211,36 +248,89 @@ __global__ void __launch_bounds__(kPlanBlock) page_plan_kernel(PageArgs a) {
     if constexpr (!RELEASE)
       if (a.slots != nullptr)
         for (int64_t r = threadIdx.x; r < a.total; r += kPlanBlock)
-          a.slots[r] = row_slot(a, first, plan, 0, a.B - 1, r);
+          a.slots[r] = row_slot(a, first, a.off != nullptr ? own_off : nullptr, plan, r);
     for (int64_t i = threadIdx.x; i < plan.pages; i += kPlanBlock) move_page<RELEASE>(a, first, plan.top, i);
   }
 }
 
-template <bool RELEASE>
-__global__ void __launch_bounds__(kFillBlock) page_fill_kernel(PageArgs a) {
-  __shared__ int64_t ends[2];
+__global__ void __launch_bounds__(kFillBlock) page_return_kernel(PageArgs a) {
+  wait_for_dependency();
+  const Plan plan = *plan_of(a);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kFillBlock + threadIdx.x; i < plan.pages;
+       i += static_cast<int64_t>(gridDim.x) * kFillBlock)
+    move_page<true>(a, first_of(a), plan.top, i);
+}
+
+// Pages and slots of a large call. A thread finds one unit: a sequence's page with new rows; then a few lanes each (no
+// more than a page has rows) write the slots of the CTA's units, two numbers at a time.
+__global__ void __launch_bounds__(kFillBlock) page_assign_kernel(PageArgs a) {
+  struct Unit {
+    int64_t row, end, slot;  // rows [row, end), the first one's slot; -1: none
+  };
+  __shared__ Unit unit[kFillBlock];
   wait_for_dependency();
   const Plan plan = *plan_of(a);
   const int64_t* first = first_of(a);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kFillBlock + threadIdx.x; i < plan.pages;
-       i += static_cast<int64_t>(gridDim.x) * kFillBlock)
-    move_page<RELEASE>(a, first, plan.top, i);
-  if constexpr (!RELEASE) {
-    if (a.slots == nullptr) return;
-    constexpr int64_t kChunk = kFillBlock * kFillRows;
-    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kChunk; row0 < a.total;
-         row0 += static_cast<int64_t>(gridDim.x) * kChunk) {
-      // the sequences of the chunk's first and last rows bound those between them
-      if (threadIdx.x < 2 && a.off != nullptr)
-        ends[threadIdx.x] = bisect(a.off, 0, a.B - 1, threadIdx.x == 0 ? row0 : min(row0 + kChunk, a.total) - 1);
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kFillRows; ++i) {
-        const int64_t r = row0 + i * kFillBlock + threadIdx.x;
-        if (r < a.total) a.slots[r] = row_slot(a, first, plan, ends[0], ends[1], r);
+  const int64_t thread = static_cast<int64_t>(blockIdx.x) * kFillBlock + threadIdx.x;
+  const int64_t threads = static_cast<int64_t>(gridDim.x) * kFillBlock;
+  if (!plan.ok || !plan.prefix) {  // refused calls, one row each, and offsets that are no prefix sums: row by row
+    for (int64_t i = thread; i < plan.pages; i += threads) move_page<false>(a, first, plan.top, i);
+    if (a.slots != nullptr)
+      for (int64_t r = thread; r < a.total; r += threads) a.slots[r] = row_slot(a, first, a.off, plan, r);
+    return;
+  }
+  if (a.slots != nullptr)
+    for (int64_t r = a.off[a.B] + thread; r < a.total; r += threads) a.slots[r] = -1;
+  const int64_t* units = units_of(a);
+  const int lanes = min(32, a.page_size), lane = threadIdx.x % lanes;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * a.units; base < plan.units;
+       base += static_cast<int64_t>(gridDim.x) * a.units) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(a.units), plan.units - base));
+    if (static_cast<int>(threadIdx.x) < n) {
+      const int64_t i = base + threadIdx.x, b = bisect(units, 0, a.B - 1, i);
+      const int64_t from = a.off[b], rows = a.off[b + 1] - from, k = i - units[b];
+      Span e;
+      Unit u;
+      if (span_of<false>(a, b, e)) {
+        const int64_t start = a.start[b], j = (start >> a.page_shift) + k, begin = j << a.page_shift;
+        int32_t* entry = a.table + b * a.max_pages + j;
+        int32_t page = -1;
+        if (j >= e.low || a.slots != nullptr) {
+          page = j < e.low ? *entry : a.free_pages[plan.top - 1 - (first[b] + j - e.low)];
+          if (!is_page(a, page, b)) page = -1;
+          if (j >= e.low) *entry = page;
+        }
+        const int64_t at = max(start, begin);  // position of the unit's first row
+        u.row = from + at - start;
+        u.end = from + min(rows, begin + a.page_size - start);
+        u.slot = page < 0 ? -1 : (static_cast<int64_t>(page) << a.page_shift) + at - begin;
+      } else {
+        u.row = from + (k << a.page_shift);
+        u.end = min(from + rows, u.row + a.page_size);
+        u.slot = -1;
       }
-      __syncthreads();
+      unit[threadIdx.x] = u;
     }
+    __syncthreads();
+    if (a.slots != nullptr)
+      for (int i = threadIdx.x / lanes; i < n; i += kFillBlock / lanes) {
+        const Unit u = unit[i];
+        const int64_t step = u.slot < 0 ? 0 : 1;
+        // pairs lie at even rows of 16-byte aligned slots
+        const bool aligned = reinterpret_cast<uintptr_t>(a.slots) % 16 == 0;
+        for (int64_t r = (aligned ? u.row & ~int64_t(1) : u.row) + (aligned ? 2 : 1) * lane; r < u.end;
+             r += (aligned ? 2 : 1) * lanes) {
+          if (aligned && r >= u.row && r + 1 < u.end) {
+            const int64_t slot = u.slot + step * (r - u.row);
+            *reinterpret_cast<longlong2*>(a.slots + r) = make_longlong2(slot, slot + step);
+          } else if (r >= u.row) {
+            a.slots[r] = u.slot + step * (r - u.row);
+          } else if (r + 1 < u.end) {
+            a.slots[r + 1] = u.slot + step * (r + 1 - u.row);
+          }
+        }
+      }
+    __syncthreads();
   }
 }
 
@@ -250,30 +340,33 @@ int64_t ctas_for(int64_t n, int64_t per_cta, int sms) {
 
 // Calls that one CTA serves: all sequences in its shared memory, and a few turns of its threads at most for their rows
 // and pages.
-bool small_assign(const PageArgs& a) {
-  return a.B <= kPlanBlock && a.total <= 4 * kPlanBlock;
-}
-bool small_release(const PageArgs& a) {
-  return a.B <= kPlanBlock && a.B * a.max_pages <= 32 * kPlanBlock;
+bool small_call(int64_t B, int64_t total, int64_t max_pages) {
+  return B <= kPlanBlock && (total >= 0 ? total <= 4 * kPlanBlock : B * max_pages <= 32 * kPlanBlock);
 }
 
 }  // namespace
 
-size_t page_scratch_bytes(int64_t B) { return kPlanBytes + 8 * static_cast<size_t>(B); }
+size_t page_scratch_bytes(int64_t B, int64_t total, int64_t max_pages) {
+  return small_call(B, total, max_pages) ? 0 : kPlanBytes + 16 * static_cast<size_t>(B);
+}
 
 cudaError_t launch_page_assign(const PageArgs& a, int sms, cudaStream_t stream) {
-  if (small_assign(a)) return launch_early(page_plan_kernel<false, true>, a, 1, kPlanBlock, stream);
+  if (small_call(a.B, a.total, a.max_pages)) return launch_early(page_plan_kernel<false, true>, a, 1, kPlanBlock, stream);
   const cudaError_t e = launch_early(page_plan_kernel<false, false>, a, 1, kPlanBlock, stream);
   if (e != cudaSuccess) return e;
-  return launch_early(page_fill_kernel<false>, a, ctas_for(a.total, kFillBlock * kFillRows, sms), kFillBlock, stream);
+  PageArgs f = a;
+  f.units = std::max(1, std::min(kFillBlock, kFillRows / a.page_size));
+  // about as many units as the rows fill pages, and one more for each sequence
+  const int64_t units = a.off != nullptr ? a.total / a.page_size + a.B : a.total;
+  return launch_early(page_assign_kernel, f, ctas_for(units, f.units, sms), kFillBlock, stream);
 }
 
 cudaError_t launch_page_release(const PageArgs& a, int sms, cudaStream_t stream) {
-  if (small_release(a)) return launch_early(page_plan_kernel<true, true>, a, 1, kPlanBlock, stream);
+  if (small_call(a.B, -1, a.max_pages)) return launch_early(page_plan_kernel<true, true>, a, 1, kPlanBlock, stream);
   cudaError_t e = launch_early(page_count_kernel, a, ctas_for(a.B, kFillBlock / 32, sms), kFillBlock, stream);
   if (e == cudaSuccess) e = launch_early(page_plan_kernel<true, false>, a, 1, kPlanBlock, stream);
   if (e != cudaSuccess) return e;
-  return launch_early(page_fill_kernel<true>, a, ctas_for(a.B * a.max_pages, kFillBlock * 4, sms), kFillBlock, stream);
+  return launch_early(page_return_kernel, a, ctas_for(a.B * a.max_pages, kFillBlock * 4, sms), kFillBlock, stream);
 }
 
 }  // namespace jattn

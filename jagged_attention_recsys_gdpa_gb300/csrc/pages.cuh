@@ -16,6 +16,7 @@ struct PageArgs {
   int64_t* slots;       // assign: [total], nullptr: not wanted
   int64_t n_pages, B, total, max_pages;
   int page_size, page_shift;
+  int units;            // set by the launch: pages that a CTA of a large call looks up at a time
   void* scratch;
   DevStatus* status;
 };

@@ -284,6 +284,11 @@ __device__ __forceinline__ void copy_async16(void* shared, const void* global, i
 __device__ __forceinline__ void copy_async16(void* shared, const void* global) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(shared)), "l"(global) : "memory");
 }
+template <int BYTES>  // 4, 8 or 16
+__device__ __forceinline__ void copy_async(void* shared, const void* global) {
+  if constexpr (BYTES == 16) copy_async16(shared, global);
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(shared)), "l"(global), "n"(BYTES) : "memory");
+}
 // Ends a group of copies; waits until all but the last N groups of this thread are there.
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

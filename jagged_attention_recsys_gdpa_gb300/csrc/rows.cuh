@@ -54,13 +54,17 @@ struct RotaryArgs {
   const float* sin_t;
   int64_t B, total, table_rows;
   int heads, D, half;
-  int rows, copied;      // set by the launch: rows of a CTA, vectors of a head that are copied
+  int rows;              // of a CTA
+  int turned, copied;    // units of a head whose pairs turn, and units that are copied
+  int step, to_b;        // columns from a pair to the next one, and from its first value to its second
   bool inverse, zero_behind;
+  bool vector_tables;    // half is a multiple of a vector's pairs: table rows are read in vectors
   DevStatus* status;
 };
 
+template <int PAIRS>
 struct RotaryTablesArgs {
-  uint64_t turn[512];  // per pair: 2^-64 turns a position
+  uint64_t turn[PAIRS];  // per pair: 2^-64 turns a position
   float* cos_t;
   float* sin_t;
   int64_t first, rows;
@@ -90,11 +94,11 @@ cudaError_t launch_early(void (*kernel)(Args), const Args& a, int64_t ctas, int 
 
 // V neighbouring values as they lie in memory.
 template <typename T, int V>
-using Raw = std::conditional_t<V * sizeof(T) == 16, uint4, T>;
+using Raw = std::conditional_t<V == 1, T, std::conditional_t<V * sizeof(T) == 16, uint4,
+                                                             std::conditional_t<V * sizeof(T) == 8, uint2, uint32_t>>>;
 
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> load_raw(const T* p) {
-  static_assert(V == 1 || V * sizeof(T) == 16, "single values or 16 bytes");
   return *reinterpret_cast<const Raw<T, V>*>(p);
 }
 
@@ -107,9 +111,11 @@ __device__ __forceinline__ void unpack(const Raw<T, V>& w, float (&x)[V]) {
   if constexpr (V == 1) {
     x[0] = to_float(w);
   } else {
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+    constexpr int W = V * sizeof(T) / 4;
+    uint32_t in[W];
+    *reinterpret_cast<Raw<T, V>*>(in) = w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < W; ++i) {
       if constexpr (std::is_same_v<T, float>) {
         x[i] = __uint_as_float(in[i]);
       } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
@@ -129,6 +135,9 @@ template <int V>
 __device__ __forceinline__ void unpack_table(const float* p, float (&x)[V]) {
   if constexpr (V == 1) {
     x[0] = *p;
+  } else if constexpr (V % 4) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = p[i];
   } else {
 #pragma unroll
     for (int i = 0; i < V; i += 4) {
@@ -154,9 +163,10 @@ __device__ __forceinline__ void store_values(T* p, const float (&x)[V]) {
   if constexpr (V == 1) {
     *p = from_float<T>(x[0]);
   } else {
-    uint32_t out[4];
+    constexpr int W = V * sizeof(T) / 4;
+    uint32_t out[W];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < W; ++i) {
       if constexpr (std::is_same_v<T, float>) {
         out[i] = __float_as_uint(x[i]);
       } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
@@ -166,7 +176,7 @@ __device__ __forceinline__ void store_values(T* p, const float (&x)[V]) {
         out[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(out[0], out[1], out[2], out[3]);
+    *reinterpret_cast<Raw<T, V>*>(p) = *reinterpret_cast<const Raw<T, V>*>(out);
   }
 }
 

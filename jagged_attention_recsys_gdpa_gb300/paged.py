@@ -176,10 +176,20 @@ def _launch(cache, fn, *args):
 
 
 def launch_on(index, fn, *args):
-    if torch.cuda.current_device() != index:
+    """fn(*args, status word, its bytes, stream) with the device current."""
+    if _C_device() != index:
         with torch.cuda.device(index):
             return launch_on(index, fn, *args)
-    fn(*args, status_block(index).data_ptr(), 256, torch._C._cuda_getCurrentRawStream(index))
+    fn(*args, _status_addresses.get(index) or _status_address(index), 256, _C_stream(index))
+
+
+# the calls behind torch.cuda.current_device and current_stream (a tensor on the device is there, so CUDA is up)
+_C_device, _C_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+_status_addresses: dict = {}
+
+
+def _status_address(index: int) -> int:
+    return _status_addresses.setdefault(index, status_block(index).data_ptr())
 
 
 def cache_append(cache, k, v, page_table, start, off=None, rope=None):
@@ -282,9 +292,9 @@ def decode(q, cache, page_table, kv_lens, q_off=None, act="softmax", causal=Fals
     return out, lse
 
 
-def _page_scratch(pool, nb):
-    n = B.page_scratch_size(nb)
-    return torch.empty(n, dtype=torch.uint8, device=pool._device), n
+def _page_scratch(pool, nb, total, max_pages):
+    n = B.page_scratch_size(nb, total, max_pages)
+    return (torch.empty(n, dtype=torch.uint8, device=pool._device) if n else None), n
 
 
 def page_assign(pool, page_table, start, off=None, total=None, slots=True):
@@ -310,8 +320,10 @@ def page_assign(pool, page_table, start, off=None, total=None, slots=True):
         _check_index(pool, slots, total, "slots")
     else:
         slots = torch.empty(total, dtype=torch.int64, device=pool._device) if slots else None
-    scratch, n = _page_scratch(pool, nb)
-    launch_on(pool._index, B.page_assign, pool._ref, nb, total, off, start, page_table, slots, scratch, n)
+    max_pages = page_table.shape[1]
+    scratch, n = _page_scratch(pool, nb, total, max_pages)
+    launch_on(pool._index, B.page_assign, pool._ref, nb, total, B.ptr(off),
+              start.data_ptr(), page_table.data_ptr(), max_pages, B.ptr(slots), B.ptr(scratch), n)
     return slots
 
 
@@ -324,5 +336,7 @@ def page_release(pool, page_table, lens, keep=None):
     _check_index(pool, lens, nb, "lens")
     if keep is not None:
         _check_index(pool, keep, nb, "keep")
-    scratch, n = _page_scratch(pool, nb)
-    launch_on(pool._index, B.page_release, pool._ref, nb, lens, keep, page_table, scratch, n)
+    max_pages = page_table.shape[1]
+    scratch, n = _page_scratch(pool, nb, -1, max_pages)
+    launch_on(pool._index, B.page_release, pool._ref, nb, lens.data_ptr(), B.ptr(keep), page_table.data_ptr(), max_pages,
+              B.ptr(scratch), n)

@@ -81,13 +81,13 @@ def test_pool_reference_restores_what_it_lends():
 def norm(lib, p=None, live=None, x=F, xr=256, xh=128, w=F * 2, b=F * 3, y=F * 4, yr=256, yh=128, mean=F * 5, rstd=F * 6,
          ws=None, ws_bytes=256, **kw):
     f = dict(rows=5, heads=2, N=128, type=1, weight_type=0, eps=1e-5, zero_behind=0)
-    f.update(kw)
-    return lib.jattn_layer_norm(ctypes.byref(B.Norm(**f)), live, x, xr, xh, w, b, y, yr, yh, mean, rstd, ws, ws_bytes, None)
+    f.update(kw, x_strides=(xr, xh), y_strides=(yr, yh))
+    return lib.jattn_layer_norm(ctypes.byref(B.Norm(**f)), live, x, w, b, y, mean, rstd, ws, ws_bytes, None)
 
 
 def test_layer_norm_refusals(lib):
     assert norm(lib) == WORKSPACE  # all else is fine
-    assert lib.jattn_layer_norm(None, None, F, 1, 1, F, F, F, 1, 1, F, F, F, 256, None) == INVALID
+    assert lib.jattn_layer_norm(None, None, F, F, F, F, F, F, F, 256, None) == INVALID
     for kw in (dict(rows=-1), dict(heads=0), dict(N=0), dict(N=16385), dict(rows=1 << 31, heads=1), dict(rows=1 << 30, heads=2),
                dict(type=3), dict(weight_type=2), dict(type=0, weight_type=1), dict(zero_behind=2), dict(eps=0.0), dict(eps=-1.0),
                dict(eps=float("nan")), dict(eps=float("inf")), dict(x=None), dict(y=None), dict(w=None), dict(mean=None),
@@ -111,9 +111,8 @@ def test_layer_norm_refusals(lib):
 def norm_bwd(lib, live=None, dy=F, dyr=256, dyh=128, x=2 * F, xr=256, xh=128, w=3 * F, mean=4 * F, rstd=5 * F, dx=6 * F, dxr=256,
              dxh=128, dw=7 * F, db=8 * F, scratch=9 * F, n=1 << 30, ws=None, **kw):
     f = dict(rows=5, heads=2, N=128, type=1, weight_type=0, eps=0.0, zero_behind=0)
-    f.update(kw)
-    return lib.jattn_layer_norm_bwd(ctypes.byref(B.Norm(**f)), live, dy, dyr, dyh, x, xr, xh, w, mean, rstd, dx, dxr, dxh, dw, db,
-                                    scratch, n, ws, 256, None)
+    f.update(kw, x_strides=(xr, xh), y_strides=(dxr, dxh), dy_strides=(dyr, dyh))
+    return lib.jattn_layer_norm_bwd(ctypes.byref(B.Norm(**f)), live, dy, x, w, mean, rstd, dx, dw, db, scratch, n, ws, 256, None)
 
 
 def test_layer_norm_backward_refusals(lib):
@@ -131,8 +130,8 @@ def test_layer_norm_backward_refusals(lib):
 
 def rotary(lib, off=None, start=F, cos=2 * F, sin=3 * F, rows=100, x=4 * F, xr=256, xh=128, y=5 * F, yr=256, yh=128, ws=None, **kw):
     f = dict(B=6, total=6, heads=2, D=128, half=64, type=1, layout=0, inverse=0, zero_behind=0)
-    f.update(kw)
-    return lib.jattn_rotary(ctypes.byref(B.Rotary(**f)), off, start, cos, sin, rows, x, xr, xh, y, yr, yh, ws, 256, None)
+    f.update(kw, table_rows=rows, x_strides=(xr, xh), y_strides=(yr, yh))
+    return lib.jattn_rotary(ctypes.byref(B.Rotary(**f)), off, start, cos, sin, x, y, ws, 256, None)
 
 
 def test_rotary_refusals(lib):
@@ -185,9 +184,12 @@ def release(lib, nb=3, lens=F, keep=2 * F, table=3 * F, max_pages=4, scratch=5 *
 
 def test_page_pool_refusals(lib):
     size = ctypes.c_size_t(0)
-    assert lib.jattn_page_scratch_size(5, ctypes.byref(size)) == 0 and size.value >= 8 * 5
-    assert lib.jattn_page_scratch_size(0, ctypes.byref(size)) == INVALID
-    assert lib.jattn_page_scratch_size(5, None) == INVALID
+    for total in (-1, 7):  # small calls need none
+        assert lib.jattn_page_scratch_size(5, total, 4, ctypes.byref(size)) == 0 and size.value == 0
+        assert lib.jattn_page_scratch_size(5000, total, 4, ctypes.byref(size)) == 0 and size.value >= 8 * 5000
+    for args in ((0, 1, 1), (1 << 31, 1, 1), (1, -2, 1), (1, 1 << 31, 1), (1, 1, 0)):
+        assert lib.jattn_page_scratch_size(*args, ctypes.byref(size)) == INVALID, args
+    assert lib.jattn_page_scratch_size(5, 1, 1, None) == INVALID
     both = (dict(n_pages=0), dict(n_pages=1 << 31), dict(page_size=0), dict(page_size=24), dict(page_size=8192), dict(free_pages=None),
             dict(count=None), dict(nb=0), dict(table=None), dict(max_pages=0), dict(max_pages=1 << 28))
     for call in (assign, release):
@@ -196,11 +198,14 @@ def test_page_pool_refusals(lib):
             assert call(lib, **kw) == INVALID, kw
         for kw in (dict(free_pages=6 * F + 2), dict(count=7 * F + 4), dict(table=3 * F + 2)):
             assert call(lib, **kw) == ALIGN, kw
-        ok = dict(ws=8 * F)
+        ok = dict(ws=10 * F)
+        large = dict(nb=5000, table=11 * F, slots=12 * F) if call is assign else dict(nb=5000, table=11 * F)
         for kw in (dict(scratch=None), dict(scratch=5 * F + 8), dict(n=8)):
-            assert call(lib, **ok, **kw) == WORKSPACE, kw
-        for kw in (dict(count=6 * F + 32), dict(table=6 * F + 36), dict(scratch=6 * F), dict(table=5 * F), dict(count=3 * F + 40)):
+            assert call(lib, **ok, **large, **kw) == WORKSPACE, kw
+        for kw in (dict(count=6 * F + 32), dict(table=6 * F + 36), dict(count=3 * F + 40)):
             assert call(lib, **ok, **kw) == INVALID, kw
+        for kw in (dict(scratch=6 * F), dict(table=5 * F), dict(scratch=F)):
+            assert call(lib, **dict(dict(ok, **large), **kw)) == INVALID, kw
     for kw in (dict(start=None), dict(total=-1), dict(total=1 << 31), dict(off=None)):
         assert assign(lib, **kw) == INVALID, kw
     for kw in (dict(off=None, total=3), dict(slots=None), dict(total=0)):
