@@ -16,9 +16,9 @@ namespace {
 // (60 M values in rows of 2,048 / 8,192): 512 threads 44 / 52 us, 1,024 38 / 42; fp32 (8 values a lane, rows of 1,024): 512 in
 // CTAs of 512 43 us, 768 in CTAs of 256 39.
 template <typename A, typename S>
-constexpr int kThreads = S::L <= 32 || A::V == 1 ? 512 : A::V * S::K <= 8 ? 768 : A::V * S::K <= 16 ? 1024 : 512;
+constexpr int kThreads = S::L <= 32 || A::V == 1 ? 512 : A::SHIFT || A::V * S::K <= 8 ? 768 : A::V * S::K <= 16 ? 1024 : 512;
 template <typename A>
-constexpr int kWide = A::V == 4 ? 256 : 512;
+constexpr int kWide = A::V == 4 || A::SHIFT ? 256 : 512;
 
 template <typename A, typename S>
 __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBlock)) norm_kernel(NormArgs a) {
@@ -36,6 +36,9 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
   const T* const x = static_cast<const T*>(a.x.data);
   T* const y = static_cast<T*>(a.y.data);
   const int first = lane * V - (SHIFT ? shift_of<T, V>(a.x.data, row_at(a.x, a.split, r)) : 0);  // column of vector 0
+  uint32_t mine[K];  // which values of the lane's vectors are the row's
+#pragma unroll
+  for (int k = 0; k < K; ++k) mine[k] = inside<V, SHIFT>(first + k * L * V, a.N);
   float w[KEPT ? E : V], b[KEPT ? E : V];
   if constexpr (KEPT)
 #pragma unroll
@@ -46,7 +49,7 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
   RowQueue<A, S, 1> queue;
   constexpr int kAhead = decltype(queue)::kAhead;
   const auto fetch = [&](uint32_t row, int slot) {
-    if (row < live) queue.fetch(ring, slot, x, x + row_at(a.x, a.split, row), first, a.N);
+    if (row < live) queue.fetch(ring, slot, x, x + row_at(a.x, a.split, row), first, mine);
     copies_commit();
   };
 #pragma unroll
@@ -57,15 +60,13 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
     float v[E], s1[1], s2[2];
     if constexpr (kAhead == 0) fetch(r, 0);
     copies_wait<kAhead == 0 ? 0 : kAhead - 1>();
-    queue.take(ring, slot, first, a.N, v);
+    queue.take(ring, slot, mine, v);
     if constexpr (kAhead > 0) {
       fetch(r + kAhead * step, free_slot);
       slot = slot == kAhead ? 0 : slot + 1;
       free_slot = free_slot == kAhead ? 0 : free_slot + 1;
     }
-    if constexpr (SHIFT)
-#pragma unroll
-      for (int k = 0; k < K; ++k) clear_outside<T, V, SHIFT>(first + k * L * V, a.N, vector_of<V>(v, k));
+    if constexpr (SHIFT) clear_outside<V, SHIFT>(mine[0], vector_of<V>(v, 0));  // values of the row before
     uint64_t sum = f2(0.0f, 0.0f);
     pairwise<E>([&](int i, int j) { sum = fadd2(sum, pair(v, i, j)); });
     s1[0] = both(sum);
@@ -73,7 +74,7 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
     const float m = s1[0] * a.inv_n;
     pairwise<E>([&](int i, int j) { unpair(fadd2(pair(v, i, j), f2(-m, -m)), v, i, j); });
 #pragma unroll
-    for (int k = 0; k < K; ++k) clear_outside<T, V, SHIFT>(first + k * L * V, a.N, vector_of<V>(v, k));
+    for (int k = 0; k < K; ++k) clear_outside<V, SHIFT>(mine[k], vector_of<V>(v, k));
     uint64_t square = f2(0.0f, 0.0f);
     sum = square;
     pairwise<E>([&](int i, int j) {
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
 #pragma unroll
       for (int i = 0; i < E; ++i) v[i] = 0.0f;
 #pragma unroll
-    for (int k = 0; k < K; ++k) store_at<T, V, SHIFT>(to, first + k * L * V, a.N, vector_of<V>(v, k));
+    for (int k = 0; k < K; ++k) store_at<T, V, SHIFT>(to + first + k * L * V, mine[k], vector_of<V>(v, k));
   }
 }
 

@@ -62,10 +62,15 @@ __device__ __forceinline__ float both(uint64_t p) {
 
 // Rows whose values do not start at 16-byte boundaries (an odd N): the first vector of a row begins `shift` values before it.
 // Rows that are a multiple of V apart share their shift, so a group of lanes that takes every V-th row (or a multiple) has
-// the same columns in each, and only the vectors at a row's ends are read and written value by value.
-template <typename T, int V>
-__device__ __forceinline__ bool whole(int c, int n) {
-  return c >= 0 && c + V <= n;
+// the same columns in each, and only the vectors at a row's ends are written value by value.
+
+// Which values of a vector of columns c .. c + V - 1 are the row's, a bit each: all or none but at the ends of shifted rows.
+template <int V, bool SHIFT>
+__device__ __forceinline__ uint32_t inside(int c, int n) {
+  constexpr uint32_t kAll = (1u << V) - 1;
+  if constexpr (!SHIFT) return c < n ? kAll : 0u;
+  const int low = max(-c, 0), high = min(n - c, V);
+  return high <= low ? 0u : (kAll >> (V - high)) & (kAll << low);
 }
 
 // Rows on their way: every thread copies its own K vectors of a row into its own places in shared memory, kAhead rows
@@ -87,37 +92,39 @@ struct RowQueue {
     return reinterpret_cast<uint4*>(ring) + (slot * K + k) * S::kBlock + threadIdx.x;
   }
   // Row at `row`, of which this lane's first vector starts at column `first`; base: the tensor's first value.
-  __device__ __forceinline__ void fetch(char* ring, int slot, const T* base, const T* row, int first, int n) {
+  __device__ __forceinline__ void fetch(char* ring, int slot, const T* base, const T* row, int first,
+                                        const uint32_t (&mine)[K]) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
+      if (mine[k] == 0) continue;
       const int c = first + k * L * V;
       if constexpr (V == 1) {
-        if (c < n) next[k] = row[c];
+        next[k] = row[c];
       } else {
         uint4* to = place(ring, slot, k);
         const T* from = row + c;
-        if (A::SHIFT && from < base && c < n) {
+        if constexpr (!A::SHIFT) {
+          copy_async16(to, from);
+        } else if (k == 0 && c < 0 && from < base) {
           T* v = reinterpret_cast<T*>(to);
 #pragma unroll
           for (int i = 0; i < V; ++i)
-            if (c + i >= 0 && c + i < n) v[i] = row[c + i];
-        } else if (!A::SHIFT) {
-          if (c < n) copy_async16(to, from);
-        } else if (c < n) {
-          copy_async16(to, from, min(n - c, V) * static_cast<int>(sizeof(T)));
+            if (mine[k] >> i & 1) v[i] = from[i];
+        } else {
+          copy_async16(to, from, (32 - __clz(mine[k])) * static_cast<int>(sizeof(T)));  // up to the row's end
         }
       }
     }
   }
-  __device__ __forceinline__ void take(char* ring, int slot, int first, int n, float (&x)[K * V]) {
+  __device__ __forceinline__ void take(char* ring, int slot, const uint32_t (&mine)[K], float (&x)[K * V]) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       float(&v)[V] = *reinterpret_cast<float(*)[V]>(&x[k * V]);
       Raw<T, V> w{};
       if constexpr (V == 1) {
-        if (first + k * L < n) w = next[k];
+        if (mine[k]) w = next[k];
       } else {
-        if (first + k * L * V < n) w = *place(ring, slot, k);
+        if (mine[k]) w = *place(ring, slot, k);
       }
       unpack<T, V>(w, v);
     }
@@ -125,23 +132,25 @@ struct RowQueue {
 };
 
 template <typename T, int V, bool SHIFT>
-__device__ __forceinline__ void store_at(T* row, int c, int n, const float (&x)[V]) {
-  if (!SHIFT ? c < n : whole<T, V>(c, n)) {
-    store_values<T, V>(row + c, x);
+__device__ __forceinline__ void store_at(T* to, uint32_t mine, const float (&x)[V]) {
+  constexpr uint32_t kAll = (1u << V) - 1;
+  if (!SHIFT ? mine != 0 : mine == kAll) {
+    store_values<T, V>(to, x);
   } else if constexpr (SHIFT) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (c + i >= 0 && c + i < n) row[c + i] = from_float<T>(x[i]);
+      if (mine >> i & 1) to[i] = from_float<T>(x[i]);
   }
 }
 
 // Zeros in the places of a vector that are not the row's.
-template <typename T, int V, bool SHIFT>
-__device__ __forceinline__ void clear_outside(int c, int n, float (&x)[V]) {
-  if (!SHIFT ? c < n : whole<T, V>(c, n)) return;
+template <int V, bool SHIFT>
+__device__ __forceinline__ void clear_outside(uint32_t mine, float (&x)[V]) {
+  constexpr uint32_t kAll = (1u << V) - 1;
+  if (mine == kAll) return;
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (!(SHIFT && c + i >= 0 && c + i < n)) x[i] = 0.0f;
+    if (!SHIFT || !(mine >> i & 1)) x[i] = 0.0f;
 }
 
 // Vector k of a lane's K vectors of V values.

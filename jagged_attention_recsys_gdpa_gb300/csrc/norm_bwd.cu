@@ -35,6 +35,9 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
   const T* const dy = static_cast<const T*>(a.dy.data);
   T* const dx = static_cast<T*>(a.y.data);
   const int first = lane * V - (SHIFT ? shift_of<T, V>(a.x.data, row_at(a.x, a.split, r)) : 0);  // column of vector 0
+  uint32_t mine[K];  // which values of the lane's vectors are the row's
+#pragma unroll
+  for (int k = 0; k < K; ++k) mine[k] = inside<V, SHIFT>(first + k * L * V, a.N);
   float w[KEPT ? E : V], dw[E], db[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
@@ -48,8 +51,8 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
   float next_m = 0.0f, next_rstd = 0.0f;
   const auto fetch = [&](uint32_t row, int slot) {
     if (row < live) {
-      queue_x.fetch(ring, slot, x, x + row_at(a.x, a.split, row), first, a.N);
-      queue_dy.fetch(ring_dy, slot, dy, dy + row_at(a.dy, a.split, row), first, a.N);
+      queue_x.fetch(ring, slot, x, x + row_at(a.x, a.split, row), first, mine);
+      queue_dy.fetch(ring_dy, slot, dy, dy + row_at(a.dy, a.split, row), first, mine);
     }
     copies_commit();
   };
@@ -68,19 +71,17 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
     fetch_stats(r + step);
     if constexpr (kAhead == 0) fetch(r, 0);
     copies_wait<kAhead == 0 ? 0 : kAhead - 1>();
-    queue_x.take(ring, slot, first, a.N, d);
-    queue_dy.take(ring_dy, slot, first, a.N, g);
+    queue_x.take(ring, slot, mine, d);
+    queue_dy.take(ring_dy, slot, mine, g);
     if constexpr (kAhead > 0) {
       fetch(r + kAhead * step, free_slot);
       slot = slot == kAhead ? 0 : slot + 1;
       free_slot = free_slot == kAhead ? 0 : free_slot + 1;
     }
-    if constexpr (SHIFT)
-#pragma unroll
-      for (int k = 0; k < K; ++k) clear_outside<T, V, SHIFT>(first + k * L * V, a.N, vector_of<V>(g, k));
+    if constexpr (SHIFT) clear_outside<V, SHIFT>(mine[0], vector_of<V>(g, 0));  // values of the row before
     pairwise<E>([&](int i, int j) { unpair(fadd2(pair(d, i, j), f2(-m, -m)), d, i, j); });
 #pragma unroll
-    for (int k = 0; k < K; ++k) clear_outside<T, V, SHIFT>(first + k * L * V, a.N, vector_of<V>(d, k));
+    for (int k = 0; k < K; ++k) clear_outside<V, SHIFT>(mine[k], vector_of<V>(d, k));
     uint64_t s0 = f2(0.0f, 0.0f), s1 = s0, s2 = s0;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
       }
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) store_at<T, V, SHIFT>(to, first + k * L * V, a.N, vector_of<V>(d, k));
+    for (int k = 0; k < K; ++k) store_at<T, V, SHIFT>(to + first + k * L * V, mine[k], vector_of<V>(d, k));
   }
   if (a.partial == nullptr) return;
   launch_dependents();

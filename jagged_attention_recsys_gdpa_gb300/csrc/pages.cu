@@ -16,6 +16,13 @@
 namespace jattn {
 namespace {
 
+// First in each kernel: the one behind it may be set up too (several follow each other in a large call), and nothing is read or
+// written before the one before it has ended.
+__device__ __forceinline__ void begin() {
+  launch_dependents();
+  wait_for_dependency();
+}
+
 constexpr int kPlanBlock = 1024;
 constexpr int kFillBlock = 256;
 constexpr int kFillRows = 8192;  // rows of a CTA of the large calls, about
@@ -88,16 +95,31 @@ __device__ __forceinline__ int64_t pages_back(const PageArgs& a, int64_t b, int 
   Span e;
   if (!span_of<true>(a, b, e)) return 0;
   bool good = true;
-  for (int64_t j = e.low + lane; j < e.high; j += 32) good = is_page(a, a.table[b * a.max_pages + j], b) && good;
+  constexpr int kAtOnce = 8;  // entries of a lane that are on their way together
+  const int32_t* entries = a.table + b * a.max_pages;
+  for (int64_t j = e.low + lane; j < e.high; j += 32 * kAtOnce) {
+    int32_t page[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) page[i] = j + 32 * i < e.high ? entries[j + 32 * i] : 0;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) good = is_page(a, page[i], b) && good;
+  }
   return __all_sync(0xffffffffu, good) ? e.high - e.low : 0;
 }
 
-// The last b in [low, high] with first[b] <= i.
-__device__ __forceinline__ int64_t bisect(const int64_t* first, int64_t low, int64_t high, int64_t i) {
+// The last b in [0, n) with first[b] <= i: seven probes at a time.
+__device__ __forceinline__ int64_t bisect(const int64_t* first, int64_t n, int64_t i) {
+  int64_t low = 0, high = n - 1;
   while (low < high) {
-    const int64_t mid = (low + high + 1) >> 1;
-    if (first[mid] <= i) low = mid;
-    else high = mid - 1;
+    const int64_t step = (high - low + 8) >> 3;
+    int64_t below = 0;
+#pragma unroll
+    for (int k = 1; k < 8; ++k) {
+      const int64_t at = low + k * step;
+      if (at <= high && first[at] <= i) below = k;
+    }
+    low += below * step;
+    high = min(high, low + step - 1);
   }
   return low;
 }
@@ -105,7 +127,7 @@ __device__ __forceinline__ int64_t bisect(const int64_t* first, int64_t low, int
 // Page number i of the call's pages.
 template <bool RELEASE>
 __device__ __forceinline__ void move_page(const PageArgs& a, const int64_t* first, int64_t top, int64_t i) {
-  const int64_t b = bisect(first, 0, a.B - 1, i);
+  const int64_t b = bisect(first, a.B, i);
   Span e;
   span_of<RELEASE>(a, b, e);
   int32_t* entry = a.table + b * a.max_pages + e.low + (i - first[b]);
@@ -138,12 +160,12 @@ __device__ __forceinline__ int64_t row_slot(const PageArgs& a, const int64_t* fi
   if (!plan.ok) return -1;
   if (off == nullptr) return slot_of(a, first, plan.top, r, r);
   if (r >= off[a.B]) return -1;
-  const int64_t b = bisect(off, 0, a.B - 1, r);
+  const int64_t b = bisect(off, a.B, r);
   return r < off[b + 1] ? slot_of(a, first, plan.top, b, r) : -1;
 }
 
 __global__ void __launch_bounds__(kFillBlock) page_count_kernel(PageArgs a) {
-  wait_for_dependency();
+  begin();
   const int lane = threadIdx.x % 32;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kFillBlock / 32);
   for (int64_t b = static_cast<int64_t>(blockIdx.x) * (kFillBlock / 32) + threadIdx.x / 32; b < a.B; b += warps) {
@@ -162,8 +184,12 @@ __global__ void __launch_bounds__(kPlanBlock) page_plan_kernel(PageArgs a) {
   __shared__ int bad;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   int64_t* first = SMALL ? own : first_of(a);
-  wait_for_dependency();
-  if (threadIdx.x == 0) bad = 0;
+  begin();
+  int64_t height = 0;
+  if (threadIdx.x == 0) {
+    bad = 0;
+    height = *a.count;
+  }
   if constexpr (SMALL && !RELEASE)
     if (a.off != nullptr)
       for (int64_t b = threadIdx.x; b <= a.B; b += kPlanBlock) own_off[b] = a.off[b];
@@ -230,7 +256,6 @@ __global__ void __launch_bounds__(kPlanBlock) page_plan_kernel(PageArgs a) {
     __syncthreads();
   }
   if (threadIdx.x == 0) {
-    const int64_t height = *a.count;
     Plan p;
     p.ok = height >= 0 && height <= a.n_pages && (RELEASE ? total <= a.n_pages - height : total <= height);
     if (!p.ok) record_error(a.status, JATTN_ERR_POOL, 95, 0);
@@ -254,7 +279,7 @@ __global__ void __launch_bounds__(kPlanBlock) page_plan_kernel(PageArgs a) {
 }
 
 __global__ void __launch_bounds__(kFillBlock) page_return_kernel(PageArgs a) {
-  wait_for_dependency();
+  begin();
   const Plan plan = *plan_of(a);
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kFillBlock + threadIdx.x; i < plan.pages;
        i += static_cast<int64_t>(gridDim.x) * kFillBlock)
@@ -268,7 +293,7 @@ __global__ void __launch_bounds__(kFillBlock) page_assign_kernel(PageArgs a) {
     int64_t row, end, slot;  // rows [row, end), the first one's slot; -1: none
   };
   __shared__ Unit unit[kFillBlock];
-  wait_for_dependency();
+  begin();
   const Plan plan = *plan_of(a);
   const int64_t* first = first_of(a);
   const int64_t thread = static_cast<int64_t>(blockIdx.x) * kFillBlock + threadIdx.x;
@@ -287,7 +312,7 @@ __global__ void __launch_bounds__(kFillBlock) page_assign_kernel(PageArgs a) {
        base += static_cast<int64_t>(gridDim.x) * a.units) {
     const int n = static_cast<int>(min(static_cast<int64_t>(a.units), plan.units - base));
     if (static_cast<int>(threadIdx.x) < n) {
-      const int64_t i = base + threadIdx.x, b = bisect(units, 0, a.B - 1, i);
+      const int64_t i = base + threadIdx.x, b = bisect(units, a.B, i);
       const int64_t from = a.off[b], rows = a.off[b + 1] - from, k = i - units[b];
       Span e;
       Unit u;
