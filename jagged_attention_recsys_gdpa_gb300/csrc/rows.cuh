@@ -56,6 +56,7 @@ struct RotaryArgs {
   int heads, D, half;
   int rows;              // of a CTA
   int turned, copied;    // units of a head whose pairs turn, and units that are copied
+  bool apart;            // the CTA's units that turn before those that are copied, else row by row
   int step, to_b;        // columns from a pair to the next one, and from its first value to its second
   bool inverse, zero_behind;
   bool vector_tables;    // half is a multiple of a vector's pairs: table rows are read in vectors
