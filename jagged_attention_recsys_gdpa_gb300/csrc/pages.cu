@@ -289,9 +289,11 @@ __global__ void __launch_bounds__(kFillBlock) page_return_kernel(PageArgs a) {
 // Pages and slots of a large call. A thread finds one unit: a sequence's page with new rows; then a few lanes each (no
 // more than a page has rows) write the slots of the CTA's units, two numbers at a time.
 __global__ void __launch_bounds__(kFillBlock) page_assign_kernel(PageArgs a) {
-  struct Unit {
-    int64_t row, end, slot;  // rows [row, end), the first one's slot; -1: none
+  struct __align__(16) Unit {
+    int row, end;  // rows [row, end)
+    int64_t base;  // a row's slot is base and its number; kNone: they have none
   };
+  constexpr int64_t kNone = INT64_MIN;
   __shared__ Unit unit[kFillBlock];
   begin();
   const Plan plan = *plan_of(a);
@@ -308,6 +310,7 @@ __global__ void __launch_bounds__(kFillBlock) page_assign_kernel(PageArgs a) {
     for (int64_t r = a.off[a.B] + thread; r < a.total; r += threads) a.slots[r] = -1;
   const int64_t* units = units_of(a);
   const int lanes = min(32, a.page_size), lane = threadIdx.x % lanes;
+  const bool pairs = reinterpret_cast<uintptr_t>(a.slots) % 16 == 0;  // at even rows
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * a.units; base < plan.units;
        base += static_cast<int64_t>(gridDim.x) * a.units) {
     const int n = static_cast<int>(min(static_cast<int64_t>(a.units), plan.units - base));
@@ -326,13 +329,13 @@ __global__ void __launch_bounds__(kFillBlock) page_assign_kernel(PageArgs a) {
           if (j >= e.low) *entry = page;
         }
         const int64_t at = max(start, begin);  // position of the unit's first row
-        u.row = from + at - start;
-        u.end = from + min(rows, begin + a.page_size - start);
-        u.slot = page < 0 ? -1 : (static_cast<int64_t>(page) << a.page_shift) + at - begin;
+        u.row = static_cast<int>(from + at - start);
+        u.end = static_cast<int>(from + min(rows, begin + a.page_size - start));
+        u.base = page < 0 ? kNone : (static_cast<int64_t>(page) << a.page_shift) + at - begin - u.row;
       } else {
-        u.row = from + (k << a.page_shift);
-        u.end = min(from + rows, u.row + a.page_size);
-        u.slot = -1;
+        u.row = static_cast<int>(from + (k << a.page_shift));
+        u.end = static_cast<int>(min(from + rows, static_cast<int64_t>(u.row) + a.page_size));
+        u.base = kNone;
       }
       unit[threadIdx.x] = u;
     }
@@ -340,18 +343,15 @@ __global__ void __launch_bounds__(kFillBlock) page_assign_kernel(PageArgs a) {
     if (a.slots != nullptr)
       for (int i = threadIdx.x / lanes; i < n; i += kFillBlock / lanes) {
         const Unit u = unit[i];
-        const int64_t step = u.slot < 0 ? 0 : 1;
-        // pairs lie at even rows of 16-byte aligned slots
-        const bool aligned = reinterpret_cast<uintptr_t>(a.slots) % 16 == 0;
-        for (int64_t r = (aligned ? u.row & ~int64_t(1) : u.row) + (aligned ? 2 : 1) * lane; r < u.end;
-             r += (aligned ? 2 : 1) * lanes) {
-          if (aligned && r >= u.row && r + 1 < u.end) {
-            const int64_t slot = u.slot + step * (r - u.row);
-            *reinterpret_cast<longlong2*>(a.slots + r) = make_longlong2(slot, slot + step);
+        const bool none = u.base == kNone;
+        for (int r = pairs ? (u.row & ~1) + 2 * lane : u.row + lane; r < u.end; r += pairs ? 2 * lanes : lanes) {
+          const int64_t v = none ? -1 : u.base + r, w = none ? -1 : v + 1;
+          if (pairs && r >= u.row && r + 1 < u.end) {
+            *reinterpret_cast<longlong2*>(a.slots + r) = make_longlong2(v, w);
           } else if (r >= u.row) {
-            a.slots[r] = u.slot + step * (r - u.row);
+            a.slots[r] = v;
           } else if (r + 1 < u.end) {
-            a.slots[r + 1] = u.slot + step * (r + 1 - u.row);
+            a.slots[r + 1] = w;
           }
         }
       }
