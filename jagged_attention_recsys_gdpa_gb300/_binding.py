@@ -8,6 +8,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 from . import build as _build
@@ -241,6 +242,27 @@ def load(path: str | None = None):
     return lib
 
 
+_host = None
+
+
+def host():
+    """The extension module of the row operators' and the page pool's calls, bound to the loaded library."""
+    global _host
+    if _host is None:
+        from .paged import status_address
+
+        path = _build.HOST
+        if not os.path.exists(path):
+            raise RuntimeError(f"_host.so not found at {path}; build it with "
+                               "`python -m jagged_attention_recsys_gdpa_gb300.build` (no other path exists)")
+        spec = importlib.util.spec_from_file_location("_host", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(load()._handle, check, status_address)
+        _host = module
+    return _host
+
+
 def error_string(code: int) -> str:
     return load().jattn_error_string(int(code)).decode()
 
@@ -363,34 +385,6 @@ def decode(p, c, q_off, kv_lens, page_table, q, o, lse, scratch: int, scratch_by
                                        scratch_bytes, ws, ws_bytes, stream)
     if rc:
         check(rc, "jattn_decode")
-
-
-def layer_norm_bwd_scratch_size(p) -> int:
-    n = ctypes.c_size_t(0)
-    check((_lib or load()).jattn_layer_norm_bwd_scratch_size(p, ctypes.byref(n)), "jattn_layer_norm_bwd_scratch_size")
-    return n.value
-
-
-def page_scratch_size(B: int, total: int, max_pages: int) -> int:
-    n = ctypes.c_size_t(0)
-    check((_lib or load()).jattn_page_scratch_size(B, total, max_pages, ctypes.byref(n)), "jattn_page_scratch_size")
-    return n.value
-
-
-def page_assign(pool, B: int, total: int, off, start, page_table, max_pages: int, slots, scratch, scratch_bytes: int,
-                ws: int, ws_bytes: int, stream: int):
-    rc = (_lib or load()).jattn_page_assign(pool, B, total, off, start, page_table, max_pages, slots, scratch,
-                                            scratch_bytes, ws, ws_bytes, stream)
-    if rc:
-        check(rc, "jattn_page_assign")
-
-
-def page_release(pool, B: int, lens, keep, page_table, max_pages: int, scratch, scratch_bytes: int, ws: int,
-                 ws_bytes: int, stream: int):
-    rc = (_lib or load()).jattn_page_release(pool, B, lens, keep, page_table, max_pages, scratch, scratch_bytes, ws,
-                                             ws_bytes, stream)
-    if rc:
-        check(rc, "jattn_page_release")
 
 
 def schedule(p: Params, q_off, kv_off, row_tile, col_tile, transposed, tiles, max_tiles, n_tiles, ws, ws_bytes,

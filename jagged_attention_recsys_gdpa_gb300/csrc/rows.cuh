@@ -76,7 +76,7 @@ struct RotaryTablesArgs {
 // A launch that may be set up while the kernel before it ends (kernels call wait_for_dependency first).
 template <typename Args>
 cudaError_t launch_early(void (*kernel)(Args), const Args& a, int64_t ctas, int threads, cudaStream_t stream, int shared = 0) {
-  if (shared > 16 << 10) {  // with what the kernel declares itself it may pass what a launch gets unasked
+  if (shared > 40 << 10) {  // with what the kernel declares itself it may pass the 48 KB that a launch gets unasked
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
     if (e != cudaSuccess) return e;
   }

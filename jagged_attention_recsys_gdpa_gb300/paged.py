@@ -53,6 +53,10 @@ def status_block(index: int) -> torch.Tensor:
     return t
 
 
+def status_address(index: int) -> int:
+    return status_block(index).data_ptr()
+
+
 class PagedCache:
     """Page buffers k, v [n_pages, H, page_size, D] (bf16, or uint8 E4M3 codes with uint8 E8M0 exponents k_scales,
     v_scales [n_pages, H, page_size, D/32]); the layout is jattn_cache_t's. Holds the tensors it is given."""
@@ -111,7 +115,7 @@ class PagePool:
     [1]) are a stack of free pages, the next one to be taken last. Holds the tensors it is given. Calls on one pool follow
     each other (one stream, or events between streams), as those on a cache do."""
 
-    __slots__ = ("_free", "_count", "_c", "_ref", "_device", "_index", "_page")
+    __slots__ = ("_free", "_count", "_page")
 
     def __init__(self, free_pages, count, page_size):
         if free_pages.dtype is not torch.int32 or free_pages.dim() != 1 or not free_pages.is_cuda \
@@ -122,15 +126,12 @@ class PagePool:
         if page_size < 1 or page_size > 4096 or page_size & (page_size - 1):
             raise ValueError("page_size must be a power of two from 1 to 4096")
         self._free, self._count, self._page = free_pages, count, int(page_size)
-        self._c = B.PagePool(free_pages.numel(), self._page, free_pages.data_ptr(), count.data_ptr())
-        self._ref = ctypes.byref(self._c)
-        self._device, self._index = free_pages.device, free_pages.device.index
 
     free_pages = property(lambda self: self._free)
     count = property(lambda self: self._count)
-    n_pages = property(lambda self: self._c.n_pages)
+    n_pages = property(lambda self: self._free.numel())
     page_size = property(lambda self: self._page)
-    device = property(lambda self: self._device)
+    device = property(lambda self: self._free.device)
 
 
 def page_pool(n_pages, page_size, device="cuda") -> PagePool:
@@ -172,24 +173,11 @@ def _check_rope(cache, rope):
 
 def _launch(cache, fn, *args):
     """fn(*args, workspace, its bytes, stream) with the cache's device current."""
-    launch_on(cache._index, fn, *args)
-
-
-def launch_on(index, fn, *args):
-    """fn(*args, status word, its bytes, stream) with the device current."""
-    if _C_device() != index:
+    index = cache._index
+    if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
-            return launch_on(index, fn, *args)
-    fn(*args, _status_addresses.get(index) or _status_address(index), 256, _C_stream(index))
-
-
-# the calls behind torch.cuda.current_device and current_stream (a tensor on the device is there, so CUDA is up)
-_C_device, _C_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
-_status_addresses: dict = {}
-
-
-def _status_address(index: int) -> int:
-    return _status_addresses.setdefault(index, status_block(index).data_ptr())
+            return _launch(cache, fn, *args)
+    fn(*args, status_block(index).data_ptr(), 256, torch._C._cuda_getCurrentRawStream(index))
 
 
 def cache_append(cache, k, v, page_table, start, off=None, rope=None):
@@ -292,11 +280,6 @@ def decode(q, cache, page_table, kv_lens, q_off=None, act="softmax", causal=Fals
     return out, lse
 
 
-def _page_scratch(pool, nb, total, max_pages):
-    n = B.page_scratch_size(nb, total, max_pages)
-    return (torch.empty(n, dtype=torch.uint8, device=pool._device) if n else None), n
-
-
 def page_assign(pool, page_table, start, off=None, total=None, slots=True):
     """Give every sequence the pages that its new rows need: rows start[b] .. start[b] + n - 1 (start int64 [B], the rows
     before, whose pages page_table holds already; negative skips the sequence), n from the prefix sums ``off`` int64 [B+1] (None:
@@ -304,39 +287,14 @@ def page_assign(pool, page_table, start, off=None, total=None, slots=True):
     rows' slots int64 [total], page * page_size + place in the page (-1 for rows without one and rows behind off[B]);
     ``slots`` may be a tensor to write them to, or False for none. ``total`` defaults to off[-1] (a host read) or the rows
     of ``slots``. Where the pool has too few pages none is assigned (``device_status``). See jattn_page_assign."""
-    _check_table(pool, page_table)
-    nb = page_table.shape[0]
-    _check_index(pool, start, nb, "start")
-    if isinstance(slots, torch.Tensor):
-        total = slots.shape[0] if total is None and slots.dim() == 1 else total
-    if off is None:
-        if total is not None and total != nb:
-            raise ValueError("without off there is one row per sequence")
-        total = nb
-    else:
-        _check_index(pool, off, nb + 1, "off")
-        total = int(off[-1].item()) if total is None else int(total)
-    if isinstance(slots, torch.Tensor):
-        _check_index(pool, slots, total, "slots")
-    else:
-        slots = torch.empty(total, dtype=torch.int64, device=pool._device) if slots else None
-    max_pages = page_table.shape[1]
-    scratch, n = _page_scratch(pool, nb, total, max_pages)
-    launch_on(pool._index, B.page_assign, pool._ref, nb, total, B.ptr(off),
-              start.data_ptr(), page_table.data_ptr(), max_pages, B.ptr(slots), B.ptr(scratch), n)
-    return slots
+    if off is not None and total is None and not isinstance(slots, torch.Tensor):
+        total = int(off[-1].item())
+    return (B._host or B.host()).page_assign(pool._free, pool._count, pool._page, page_table, start, off,
+                                             -1 if total is None else total, slots)
 
 
 def page_release(pool, page_table, lens, keep=None):
     """Take back the pages of rows keep[b] .. lens[b] - 1 (int64 [B]; keep None: all rows, negative: the sequence is left as it
     is) that hold none of the rows kept; their entries in page_table become -1. The next page_assign takes them first, the first sequence's first
     page before all others. See jattn_page_release."""
-    _check_table(pool, page_table)
-    nb = page_table.shape[0]
-    _check_index(pool, lens, nb, "lens")
-    if keep is not None:
-        _check_index(pool, keep, nb, "keep")
-    max_pages = page_table.shape[1]
-    scratch, n = _page_scratch(pool, nb, -1, max_pages)
-    launch_on(pool._index, B.page_release, pool._ref, nb, lens.data_ptr(), B.ptr(keep), page_table.data_ptr(), max_pages,
-              B.ptr(scratch), n)
+    (B._host or B.host()).page_release(pool._free, pool._count, pool._page, page_table, lens, keep)

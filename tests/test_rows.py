@@ -223,7 +223,7 @@ def test_error_string_of_the_pool(lib):
     assert "pool" in B.error_string(12) and B.error_string(13) == "unknown error code"
 
 
-def test_python_refuses_host_tensors():
+def test_python_refuses_host_tensors(lib):
     import jagged_attention_recsys_gdpa_gb300 as J
 
     x = torch.zeros(4, 2, 8)
