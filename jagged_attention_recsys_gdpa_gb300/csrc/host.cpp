@@ -60,6 +60,11 @@ int64_t integer(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw Raised{};
   return v;
 }
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v == 1;
+}
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw Raised{};
@@ -243,7 +248,7 @@ PyObject* layer_norm(PyObject* const* a) {
 PyObject* layer_norm_bwd(PyObject* const* a) {
   const Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[1], "x"), &mean = tensor(a[3], "mean"), &rstd = tensor(a[4], "rstd");
   const Tensor *weight = optional(a[2], "weight"), *off = optional(a[5], "off"), *out = optional(a[7], "out");
-  const bool wants_bias = PyObject_IsTrue(a[6]) == 1;
+  const bool wants_bias = truth(a[6]);
   jattn_norm_t p = norm_params(x, weight, out);
   check_like(dy, x, "dy");
   const Strides ds = strides_of(dy, "dy");
@@ -305,7 +310,7 @@ PyObject* rotary(PyObject* const* a) {
   p.half = static_cast<int>(cos.size(1));
   p.type = type_of(x);
   p.layout = static_cast<int>(integer(a[5]));
-  p.inverse = PyObject_IsTrue(a[6]) == 1;
+  p.inverse = truth(a[6]);
   p.zero_behind = out == nullptr;
   p.table_rows = cos.size(0);
   const Strides ys = out ? strides_of(*out, "out") : Strides{heads * D, D};
@@ -401,7 +406,7 @@ PyObject* page_assign(PyObject* const* a) {
     total = c.B;
   }
   if (to) c.check(*to, total, "slots");
-  const bool wanted = to || PyObject_IsTrue(a[7]) == 1;
+  const bool wanted = to || truth(a[7]);
   Place place(c.free.get_device());
   Tensor slots, scratch;
   int rc;

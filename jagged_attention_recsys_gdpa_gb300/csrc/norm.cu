@@ -16,7 +16,9 @@ namespace {
 // (60 M values in rows of 2,048 / 8,192): 512 threads 44 / 52 us, 1,024 38 / 42; fp32 (8 values a lane, rows of 1,024): 512 in
 // CTAs of 512 43 us, 768 in CTAs of 256 39.
 template <typename A, typename S>
-constexpr int kThreads = S::L <= 32 || A::V == 1 ? 512 : A::SHIFT || A::V * S::K <= 8 ? 768 : A::V * S::K <= 16 ? 1024 : 512;
+constexpr int kThreads = S::L <= 32 || A::V == 1 || A::V * S::K > 16 ? 512
+                         : A::SHIFT || A::V * S::K <= 8              ? 768
+                                                                     : 1024;
 template <typename A>
 constexpr int kWide = A::V == 4 || A::SHIFT ? 256 : 512;
 
@@ -24,7 +26,7 @@ template <typename A, typename S>
 __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBlock)) norm_kernel(NormArgs a) {
   using T = typename A::Type;
   constexpr int V = A::V, L = S::L, K = S::K, G = S::kGroups, E = K * V;
-  constexpr bool SHIFT = A::SHIFT, KEPT = E <= 16;  // weights in registers
+  constexpr bool SHIFT = A::SHIFT, KEPT = E <= 24;  // weights in registers
   extern __shared__ __align__(16) char ring[];
   __shared__ float slots1[G][kSumWarps<L>][1], slots2[G][kSumWarps<L>][2];
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
 cudaError_t launch_norm(int type, NormPath path, const NormArgs& a, int sms, cudaStream_t stream) {
   return with_norm_access(type, path, [&](auto access) {
     using A = decltype(access);
-    return with_norm_shape<A::V, 256, kWide<A>>(norm_vectors<A>(a.N), [&](auto shape) {
+    return with_norm_shape<A::V, true, 256, kWide<A>>(norm_vectors<A>(a.N), [&](auto shape) {
       using S = decltype(shape);
       const int64_t most = static_cast<int64_t>(sms) * std::max(1, kThreads<A, S> / S::kBlock);
       return launch_early(norm_kernel<A, S>, a, norm_ctas<A, S>(a.rows * a.heads, most), S::kBlock, stream,
