@@ -146,6 +146,11 @@ void check_out(const Tensor& out, const Tensor& x) {
                     "outputs are written without a gradient: pass tensors that need none");
 }
 
+// A tensor that a call has written: autograd refuses a backward pass that needs what it held before.
+void written(const Tensor& out) {
+  if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
+}
+
 void check_index(const Tensor& t, c10::Device device, const char* name) {
   TORCH_CHECK_VALUE(t.scalar_type() == at::kLong && t.dim() == 1 && t.device() == device && t.is_contiguous(), name,
                     " must be a contiguous int64 tensor of one dimension on the other tensors' device");
@@ -241,6 +246,7 @@ PyObject* layer_norm(PyObject* const* a) {
                         place.stream);
   }
   finish(rc, "jattn_layer_norm");
+  if (out) written(*out);
   return pack(out ? given(a[5]) : wrap(y), wrap(mean), wrap(rstd));
 }
 
@@ -280,6 +286,7 @@ PyObject* layer_norm_bwd(PyObject* const* a) {
                               place.status, kStatusBytes, place.stream);
   }
   finish(rc, "jattn_layer_norm_bwd");
+  if (out) written(*out);
   return pack(out ? given(a[7]) : wrap(dx), weight ? wrap(dw) : none(), weight && wants_bias ? wrap(db) : none());
 }
 
@@ -329,6 +336,7 @@ PyObject* rotary(PyObject* const* a) {
                     kStatusBytes, place.stream);
   }
   finish(rc, "jattn_rotary");
+  if (out) written(*out);
   return out ? given(a[7]) : wrap(y);
 }
 

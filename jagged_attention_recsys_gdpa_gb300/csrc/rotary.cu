@@ -196,7 +196,7 @@ cudaError_t launch_shape(RotaryArgs a, bool few, cudaStream_t stream) {
   a.apart = !few && a.copied > 0 && 2 * a.half * sizeof(typename S::T) % 128 == 0 && a.D * sizeof(typename S::T) % 128 == 0;
   // few: what the threads hold at a time; else six times as much (rotary_histories / rotary_back_part with four times 131 / 42 us,
   // eight 135 / 41)
-    const int64_t units = (few ? 1 : 6) * kRotaryBlock;
+  const int64_t units = (few ? 1 : 6) * kRotaryBlock;
   a.rows = static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, units / per_row), kRotaryRows));
   return launch_early(rotary_kernel<S>, a, (a.total + a.rows - 1) / a.rows, kRotaryBlock, stream, S::kShared);
 }

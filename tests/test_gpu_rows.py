@@ -401,6 +401,27 @@ def test_layer_norm_on_streams_and_in_graphs():
     assert J.device_status() == 0
 
 
+def test_in_place_calls_count_as_writes():
+    """Autograd refuses a backward pass through rows that a call has overwritten since."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    tables = J.rotary_tables(8, 16)
+    for write in (lambda x: J.layer_norm_forward(x, out=x), lambda x: J.rotary(x, tables, out=x),
+                  lambda x: J.layer_norm_backward(torch.ones_like(x), x, None, x[..., 0].contiguous(), x[..., 0].contiguous(), out=x)):
+        x = rand((8, 2, 16), FP32, 1).cuda()
+        w = torch.ones(16, device="cuda", requires_grad=True)
+        loss = (x * w).sum()  # keeps x for w's gradient
+        write(x)
+        with pytest.raises(RuntimeError, match="inplace"):
+            loss.backward()
+        with torch.inference_mode():
+            z = torch.ones(8, 2, 16, device="cuda")
+            write(z)
+        write(z)
+    assert J.device_status() == 0
+
+
 def test_layer_norm_python_refusals():
     import jagged_attention_recsys_gdpa_gb300 as J
 
