@@ -57,7 +57,7 @@ def _build_host() -> None:
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", inc, "-isystem",
            os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
            os.path.join(CSRC, "host.cpp"), "-o", tmp, "-L", libs, f"-Wl,-rpath,{libs}", "-lc10", "-lc10_cuda", "-ltorch_cpu",
-           "-ltorch_python", "-ldl"]
+           "-ltorch_cuda", "-ltorch_python", "-ldl"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on host.cpp:\n{r.stderr[-6000:]}")

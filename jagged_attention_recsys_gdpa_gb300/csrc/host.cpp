@@ -15,7 +15,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -117,9 +117,11 @@ int type_of(const Tensor& t) {
   }
 }
 
-Tensor empty(at::IntArrayRef sizes, const Tensor& like, at::ScalarType type) {
-  return at::empty(sizes, at::TensorOptions().dtype(type).device(like.device()));
+// From PyTorch's allocator without its dispatcher.
+Tensor empty(at::IntArrayRef sizes, c10::Device device, at::ScalarType type) {
+  return Tensor(at::detail::empty_cuda(sizes, type, device, std::nullopt));
 }
+Tensor empty(at::IntArrayRef sizes, const Tensor& like, at::ScalarType type) { return empty(sizes, like.device(), type); }
 
 struct Strides {
   int64_t row, head;
@@ -359,13 +361,13 @@ PyObject* rotary_tables(PyObject* const* a) {
   p.beta_slow = number(a[7]);
   if (index < 0) index = c10::cuda::current_device();
   Place place(static_cast<int>(index));
-  const auto options = at::TensorOptions().dtype(at::kFloat).device(at::kCUDA, static_cast<c10::DeviceIndex>(index));
+  const c10::Device device(at::kCUDA, static_cast<c10::DeviceIndex>(index));
   Tensor cos, sin;
   int rc;
   {
     Unlocked unlocked;
-    cos = at::empty({rows, dim / 2}, options);
-    sin = at::empty({rows, dim / 2}, options);
+    cos = empty({rows, dim / 2}, device, at::kFloat);
+    sin = empty({rows, dim / 2}, device, at::kFloat);
     rc = lib.rotary_tables(&p, static_cast<float*>(cos.data_ptr()), static_cast<float*>(sin.data_ptr()), place.stream);
   }
   finish(rc, "jattn_rotary_tables");

@@ -116,9 +116,11 @@ def rotary_tables(rows, dim, base=10000.0, scaling=None, factor=1.0, original=No
         raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
     if scaling == "yarn" and original is None:
         raise ValueError("yarn needs the original context")
-    device = torch.device(device)
-    if device.type != "cuda":
-        raise ValueError("tables are made on a CUDA device")
-    index = -1 if device.index is None else device.index  # the current one
+    index = -1  # the current device
+    if device != "cuda":
+        device = torch.device(device)
+        if device.type != "cuda":
+            raise ValueError("tables are made on a CUDA device")
+        index = -1 if device.index is None else device.index
     return (B._host or B.host()).rotary_tables(rows, dim, base, _SCALINGS[scaling], factor, original or 0.0, beta_fast,
                                                beta_slow, first, index)
