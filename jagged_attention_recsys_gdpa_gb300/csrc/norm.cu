@@ -19,6 +19,12 @@ template <typename A, typename S>
 constexpr int kThreads = S::L <= 32 || A::V == 1 || A::V * S::K > 16 ? 512
                          : A::SHIFT || A::V * S::K <= 8              ? 768
                                                                      : 1024;
+// Shifted rows whose weights do not fit the registers: they lie in shared memory, arranged for the lanes of a row, and the
+// rows of a CTA share their shift.
+template <typename A, typename S>
+constexpr bool kHeld = A::SHIFT && S::K * A::V > 24;
+template <typename A, typename S>
+constexpr int kHeldBytes = kHeld<A, S> ? 2 * S::L * S::K * A::V * 4 : 0;
 template <typename A>
 constexpr int kWide = A::V == 4 || A::SHIFT ? 256 : 512;
 
@@ -26,7 +32,7 @@ template <typename A, typename S>
 __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBlock)) norm_kernel(NormArgs a) {
   using T = typename A::Type;
   constexpr int V = A::V, L = S::L, K = S::K, G = S::kGroups, E = K * V;
-  constexpr bool SHIFT = A::SHIFT, KEPT = E <= 24;  // weights in registers
+  constexpr bool SHIFT = A::SHIFT, KEPT = E <= 24, HELD = kHeld<A, S>;  // KEPT: weights in registers
   extern __shared__ __align__(16) char ring[];
   __shared__ float slots1[G][kSumWarps<L>][1], slots2[G][kSumWarps<L>][2];
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
@@ -34,7 +40,8 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
   const uint32_t live = static_cast<uint32_t>(live_rows(a.live, a.rows, a.status) * a.heads);
   const uint32_t total = static_cast<uint32_t>(a.rows * a.heads);
   const uint32_t step = gridDim.x * G;
-  uint32_t r = blockIdx.x * G + group;
+  uint32_t base = HELD ? blockIdx.x / V * (V * G) + blockIdx.x % V : blockIdx.x * G;
+  uint32_t r = base + (HELD ? group * V : group);
   const T* const x = static_cast<const T*>(a.x.data);
   T* const y = static_cast<T*>(a.y.data);
   const int first = lane * V - (SHIFT ? shift_of<T, V>(a.x.data, row_at(a.x, a.split, r)) : 0);  // column of vector 0
@@ -48,6 +55,21 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
       load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, k));
       load_weight<T, V, SHIFT>(a.b, a.wide_weight, first + k * L * V, a.N, 0.0f, vector_of<V>(b, k));
     }
+  float4* const held = reinterpret_cast<float4*>(ring + RowQueue<A, S, 1>::kBytes) + lane;  // [w, b][E / 4][L]
+  if constexpr (HELD) {
+    if (group == 0)
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, w);
+        load_weight<T, V, SHIFT>(a.b, a.wide_weight, first + k * L * V, a.N, 0.0f, b);
+#pragma unroll
+        for (int i = 0; i < V; i += 4) {
+          held[(k * V + i) / 4 * L] = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+          held[(E + k * V + i) / 4 * L] = make_float4(b[i], b[i + 1], b[i + 2], b[i + 3]);
+        }
+      }
+    __syncthreads();
+  }
   RowQueue<A, S, 1> queue;
   constexpr int kAhead = decltype(queue)::kAhead;
   const auto fetch = [&](uint32_t row, int slot) {
@@ -58,7 +80,7 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
   for (int i = 0; i < kAhead; ++i) fetch(r + i * step, i);
   int slot = 0, free_slot = kAhead;
   // the rows of a warp, and of a CTA that shares one, end together
-  for (uint32_t base = blockIdx.x * G; base < total; base += step, r += step) {
+  for (; base < total; base += step, r += step) {
     float v[E], s1[1], s2[2];
     if constexpr (kAhead == 0) fetch(r, 0);
     copies_wait<kAhead == 0 ? 0 : kAhead - 1>();
@@ -103,8 +125,17 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
     } else {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, 0));
-        load_weight<T, V, SHIFT>(a.b, a.wide_weight, first + k * L * V, a.N, 0.0f, vector_of<V>(b, 0));
+        if constexpr (HELD) {
+#pragma unroll
+          for (int i = 0; i < V; i += 4) {
+            const float4 w4 = held[(k * V + i) / 4 * L], b4 = held[(E + k * V + i) / 4 * L];
+            w[i] = w4.x, w[i + 1] = w4.y, w[i + 2] = w4.z, w[i + 3] = w4.w;
+            b[i] = b4.x, b[i + 1] = b4.y, b[i + 2] = b4.z, b[i + 3] = b4.w;
+          }
+        } else {
+          load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, 0));
+          load_weight<T, V, SHIFT>(a.b, a.wide_weight, first + k * L * V, a.N, 0.0f, vector_of<V>(b, 0));
+        }
         float(&d)[V] = vector_of<V>(v, k);
         pairwise<V>([&](int i, int j) {
           unpair(ffma2(ffma2(pair(d, i, j), scale, shift), pair(w, i, j), pair(b, i, j)), d, i, j);
@@ -124,11 +155,11 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
 cudaError_t launch_norm(int type, NormPath path, const NormArgs& a, int sms, cudaStream_t stream) {
   return with_norm_access(type, path, [&](auto access) {
     using A = decltype(access);
-    return with_norm_shape<A::V, true, 256, kWide<A>>(norm_vectors<A>(a.N), [&](auto shape) {
+    return with_norm_shape<A::V, true, A::SHIFT, 256, kWide<A>>(norm_vectors<A>(a.N), [&](auto shape) {
       using S = decltype(shape);
       const int64_t most = static_cast<int64_t>(sms) * std::max(1, kThreads<A, S> / S::kBlock);
-      return launch_early(norm_kernel<A, S>, a, norm_ctas<A, S>(a.rows * a.heads, most), S::kBlock, stream,
-                          RowQueue<A, S, 1>::kBytes);
+      return launch_early(norm_kernel<A, S>, a, norm_ctas<A, S, kHeld<A, S>>(a.rows * a.heads, most), S::kBlock, stream,
+                          RowQueue<A, S, 1>::kBytes + kHeldBytes<A, S>);
     });
   });
 }

@@ -134,12 +134,14 @@ struct RowQueue {
 template <typename T, int V, bool SHIFT>
 __device__ __forceinline__ void store_at(T* to, uint32_t mine, const float (&x)[V]) {
   constexpr uint32_t kAll = (1u << V) - 1;
+  const Raw<T, V> w = pack_values<T, V>(x);
   if (!SHIFT ? mine != 0 : mine == kAll) {
-    store_values<T, V>(to, x);
+    *reinterpret_cast<Raw<T, V>*>(to) = w;
   } else if constexpr (SHIFT) {
+    const T* v = reinterpret_cast<const T*>(&w);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (mine >> i & 1) to[i] = from_float<T>(x[i]);
+      if (mine >> i & 1) to[i] = v[i];
   }
 }
 
@@ -200,8 +202,9 @@ struct NormShape {
 
 // Calls f(shape) with the smallest shape whose L * K vectors hold a row of n, in CTAs of NARROW threads for rows of up
 // to a warp's lanes, else of WIDE. THREE: three vectors a lane too, which the forward's registers hold (30 M values in rows of
-// 129 / 555 / 768: 32 / 31 / 20 us with them, 51 / 46 / 23 without) and the backward's do not.
-template <int V, bool THREE, int NARROW, int WIDE, typename F>
+// 129 / 555 / 768: 32 / 31 / 20 us with them, 51 / 46 / 23 without) and the backward's do not. FOUR: four vectors a lane for
+// long rows, which halves what a row costs besides its vectors: its ends' single values, sums, addresses.
+template <int V, bool THREE, bool FOUR, int NARROW, int WIDE, typename F>
 cudaError_t with_norm_shape(int n, F&& f) {
   if constexpr (V == 1) {
     if (n <= 8) return f(NormShape<8, 1, NARROW, WIDE>{});
@@ -221,6 +224,13 @@ cudaError_t with_norm_shape(int n, F&& f) {
       if (n > 64 && n <= 96) return f(NormShape<32, 3, NARROW, WIDE>{});
       if (n > 128 && n <= 192) return f(NormShape<64, 3, NARROW, WIDE>{});
       if (n > 256 && n <= 384) return f(NormShape<128, 3, NARROW, WIDE>{});
+      if (n > 512 && n <= 768) return f(NormShape<256, 3, NARROW, WIDE>{});
+    }
+    if constexpr (FOUR) {
+      if (n > 64 && n <= 128) return f(NormShape<32, 4, NARROW, WIDE>{});
+      if (V == 4 && n > 128 && n <= 256) return f(NormShape<64, 4, NARROW, WIDE>{});
+      if (V == 4 && n > 256 && n <= 512) return f(NormShape<128, 4, NARROW, WIDE>{});
+      if (n > 512 && n <= 1024) return f(NormShape<256, 4, NARROW, WIDE>{});
     }
     if (n <= 16) return f(NormShape<8, 2, NARROW, WIDE>{});
     if (n <= 32) return f(NormShape<16, 2, NARROW, WIDE>{});
@@ -262,12 +272,13 @@ template <typename A>
 int norm_vectors(int n) {
   return A::SHIFT ? (n + 2 * A::V - 2) / A::V : (n + A::V - 1) / A::V;
 }
-// CTAs of a persistent grid; shifted rows keep their alignment where the groups' number is a multiple of V.
-template <typename A, typename S>
+// CTAs of a persistent grid; shifted rows keep their alignment where the groups' number is a multiple of V. APART: a CTA's
+// groups take rows that are V apart, so that they share it.
+template <typename A, typename S, bool APART = false>
 int64_t norm_ctas(int64_t rows, int64_t most) {
   const int64_t ctas = std::min((rows + S::kGroups - 1) / S::kGroups, most);
-  if (!A::SHIFT || S::kGroups % A::V == 0) return ctas;
-  constexpr int64_t step = A::V / S::kGroups > 0 ? A::V / S::kGroups : 1;
+  if (!A::SHIFT || (!APART && S::kGroups % A::V == 0)) return ctas;
+  constexpr int64_t step = APART ? A::V : A::V / S::kGroups > 0 ? A::V / S::kGroups : 1;
   return (ctas + step - 1) / step * step;
 }
 

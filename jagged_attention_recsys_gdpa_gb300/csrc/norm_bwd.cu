@@ -190,7 +190,7 @@ int norm_bwd_parts(int type, NormPath path, int64_t rows, int N, int sms) {
   int64_t parts = 0;
   with_norm_access(type, path, [&](auto access) {
     using A = decltype(access);
-    return with_norm_shape<A::V, false, kNarrow, kWide>(norm_vectors<A>(N), [&](auto shape) {
+    return with_norm_shape<A::V, false, false, kNarrow, kWide>(norm_vectors<A>(N), [&](auto shape) {
       parts = bwd_ctas<A, decltype(shape)>(rows, sms);
       return cudaSuccess;
     });
@@ -201,7 +201,7 @@ int norm_bwd_parts(int type, NormPath path, int64_t rows, int N, int sms) {
 cudaError_t launch_norm_bwd(int type, NormPath path, const NormArgs& a, int sms, cudaStream_t stream) {
   return with_norm_access(type, path, [&](auto access) {
     using A = decltype(access);
-    return with_norm_shape<A::V, false, kNarrow, kWide>(norm_vectors<A>(a.N), [&](auto shape) {
+    return with_norm_shape<A::V, false, false, kNarrow, kWide>(norm_vectors<A>(a.N), [&](auto shape) {
       using S = decltype(shape);
       return launch_early(norm_bwd_kernel<A, S>, a, bwd_ctas<A, S>(a.rows * a.heads, sms), S::kBlock, stream,
                           kShared<A, S>);

@@ -160,12 +160,12 @@ __device__ __forceinline__ T from_float(float x) {
 
 // Rounded once, to nearest even.
 template <typename T, int V>
-__device__ __forceinline__ void store_values(T* p, const float (&x)[V]) {
+__device__ __forceinline__ Raw<T, V> pack_values(const float (&x)[V]) {
   if constexpr (V == 1) {
-    *p = from_float<T>(x[0]);
+    return from_float<T>(x[0]);
   } else {
     constexpr int W = V * sizeof(T) / 4;
-    uint32_t out[W];
+    alignas(16) uint32_t out[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       if constexpr (std::is_same_v<T, float>) {
@@ -177,8 +177,12 @@ __device__ __forceinline__ void store_values(T* p, const float (&x)[V]) {
         out[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
-    *reinterpret_cast<Raw<T, V>*>(p) = *reinterpret_cast<const Raw<T, V>*>(out);
+    return *reinterpret_cast<const Raw<T, V>*>(out);
   }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_values(T* p, const float (&x)[V]) {
+  *reinterpret_cast<Raw<T, V>*>(p) = pack_values<T, V>(x);
 }
 
 // Rows before the padding: *live, which a prefix sum over `rows` rows ends with (nullptr: all rows).
