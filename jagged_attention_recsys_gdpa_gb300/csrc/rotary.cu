@@ -51,6 +51,8 @@ struct RotaryShape {
   static constexpr int kBytes = V * sizeof(T);
   static constexpr bool kQueued = kBytes >= 4;  // what asynchronous copies can bring
   static constexpr int kShared = kQueued ? 2 * HG * kVectors * kRotaryBlock * kBytes : 0;
+  // of an SM, for which the registers leave room (rotary_back_part: 2 / 3 / 4 of them 42 / 37 / 39 us)
+  static constexpr int kCtas = std::min(3, (224 << 10) / (kShared + (3 << 10)));
 };
 
 struct Unit {
@@ -58,7 +60,7 @@ struct Unit {
 };
 
 template <typename S>
-__global__ void __launch_bounds__(kRotaryBlock) rotary_kernel(RotaryArgs a) {
+__global__ void __launch_bounds__(kRotaryBlock, S::kCtas) rotary_kernel(RotaryArgs a) {
   using T = typename S::T;
   constexpr int V = S::V, HG = S::HG, P = S::kPairs;
   constexpr bool INSIDE = S::INSIDE;
@@ -189,15 +191,21 @@ __global__ void __launch_bounds__(kRotaryBlock) rotary_kernel(RotaryArgs a) {
 }
 
 template <typename S>
-cudaError_t launch_shape(RotaryArgs a, bool few, cudaStream_t stream) {
+cudaError_t launch_shape(RotaryArgs a, bool few, int sms, cudaStream_t stream) {
   const int64_t per_row = static_cast<int64_t>(a.turned + a.copied) * ((a.heads + S::HG - 1) / S::HG);
   // Lines of 128 bytes are not torn: half of 128 columns turning, 256 bytes a head, 39.6 us apart and 42.6 in turn; 20 of 80
   // columns 74 and 46.
   a.apart = !few && a.copied > 0 && 2 * a.half * sizeof(typename S::T) % 128 == 0 && a.D * sizeof(typename S::T) % 128 == 0;
-  // few: what the threads hold at a time; else six times as much (rotary_histories / rotary_back_part with four times 131 / 42 us,
-  // eight 135 / 41)
+  // few: what the threads hold at a time; else up to six times as much, in whole waves of the CTAs that run at a time
+  // (rotary_back_part 37 us, 41 without the waves)
   const int64_t units = (few ? 1 : 6) * kRotaryBlock;
-  a.rows = static_cast<int>(std::min<int64_t>(std::max<int64_t>(1, units / per_row), kRotaryRows));
+  int64_t rows = std::max<int64_t>(1, units / per_row);
+  const int64_t wave = static_cast<int64_t>(sms) * S::kCtas;
+  if (const int64_t ctas = (a.total + rows - 1) / rows; !few && ctas > wave) {
+    const int64_t whole = (ctas + wave - 1) / wave * wave;
+    rows = (a.total + whole - 1) / whole;
+  }
+  a.rows = static_cast<int>(std::min<int64_t>(rows, kRotaryRows));
   return launch_early(rotary_kernel<S>, a, (a.total + a.rows - 1) / a.rows, kRotaryBlock, stream, S::kShared);
 }
 
@@ -215,23 +223,23 @@ cudaError_t launch_typed(RotaryArgs a, int sms, cudaStream_t stream) {
     a.copied = stay ? 0 : (a.D - 2 * a.half) / V;
   }
   if (a.total * a.heads * (a.turned + a.copied) <= static_cast<int64_t>(sms) * 2048)
-    return launch_shape<RotaryShape<T, V, INSIDE, 1>>(a, true, stream);
+    return launch_shape<RotaryShape<T, V, INSIDE, 1>>(a, true, sms, stream);
   int best = 1;
   const auto cost = [&](int hg) { return (a.heads + hg - 1) / hg * (hg + 1); };
   for (const int hg : {2, 3, 4, 6, 8})
     if (hg <= (V * sizeof(T) < 16 ? 4 : INSIDE ? 8 : 4) && (V * sizeof(T) == 16 || hg % 2 == 0) && cost(hg) < cost(best)) best = hg;
   switch (best) {
-    case 2: return launch_shape<RotaryShape<T, V, INSIDE, 2>>(a, false, stream);
-    case 4: return launch_shape<RotaryShape<T, V, INSIDE, 4>>(a, false, stream);
+    case 2: return launch_shape<RotaryShape<T, V, INSIDE, 2>>(a, false, sms, stream);
+    case 4: return launch_shape<RotaryShape<T, V, INSIDE, 4>>(a, false, sms, stream);
   }
   if constexpr (V * sizeof(T) == 16) {
-    if (best == 3) return launch_shape<RotaryShape<T, V, INSIDE, 3>>(a, false, stream);
+    if (best == 3) return launch_shape<RotaryShape<T, V, INSIDE, 3>>(a, false, sms, stream);
     if constexpr (INSIDE) {
-      if (best == 6) return launch_shape<RotaryShape<T, V, INSIDE, 6>>(a, false, stream);
-      if (best == 8) return launch_shape<RotaryShape<T, V, INSIDE, 8>>(a, false, stream);
+      if (best == 6) return launch_shape<RotaryShape<T, V, INSIDE, 6>>(a, false, sms, stream);
+      if (best == 8) return launch_shape<RotaryShape<T, V, INSIDE, 8>>(a, false, sms, stream);
     }
   }
-  return launch_shape<RotaryShape<T, V, INSIDE, 1>>(a, false, stream);
+  return launch_shape<RotaryShape<T, V, INSIDE, 1>>(a, false, sms, stream);
 }
 
 template <typename T>
