@@ -348,7 +348,12 @@ __global__ void __launch_bounds__(kFillBlock) page_assign_kernel(PageArgs a) {
         const int64_t none = u.base == kNone ? -1 : 0;
         int64_t* to = a.slots + u.row + lane;
         int64_t slot = u.base + u.row + lane;
-        for (int left = u.end - u.row - lane; left > 0; left -= lanes, to += lanes, slot += lanes) *to = slot | none;
+        int left = u.end - u.row - lane;
+        for (; left > 32; left -= 64, to += 64, slot += 64) {  // (pages of more than 32 rows: 32 lanes)
+          to[0] = slot | none;
+          to[32] = (slot + 32) | none;
+        }
+        if (left > 0) *to = slot | none;
       }
     __syncthreads();
   }
