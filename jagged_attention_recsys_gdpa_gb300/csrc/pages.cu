@@ -3,8 +3,9 @@
 // Whole numbers throughout, so each order is fixed: the i-th page that a call wants, sequence by sequence, is the i-th
 // from the top of the stack of free pages, and the i-th that it gives back becomes the i-th from the top. One CTA adds
 // the sequences' counts up (and moves the pool's height); then every page finds its sequence by bisection, needs nothing
-// from the others, and gives its rows their slots, which are consecutive numbers. Small calls do both in that CTA, with one
-// launch: they are bound by latency. Large ones are bound by the slots' stores, 8 bytes a row.
+// from the others, and gives its rows their slots, which are consecutive numbers. Small calls do both in one CTA and
+// launch, a thread a sequence: they are bound by the chain of loads (lengths, then entries or free pages) and the launch.
+// Large ones are bound by the slots' stores, 8 bytes a row, and their instructions.
 #include <algorithm>
 #include <cstdint>
 
@@ -110,14 +111,15 @@ __device__ __forceinline__ int64_t pages_back(const PageArgs& a, int64_t b, int 
 }
 
 // The last b in [0, n) with first[b] <= i: seven probes at a time.
-__device__ __forceinline__ int64_t bisect(const int64_t* first, int64_t n, int64_t i) {
-  int64_t low = 0, high = n - 1;
+template <typename I>
+__device__ __forceinline__ I bisect(const I* first, I n, I i) {
+  I low = 0, high = n - 1;
   while (low < high) {
-    const int64_t step = (high - low + 8) >> 3;
-    int64_t below = 0;
+    const I step = (high - low + 8) >> 3;
+    I below = 0;
 #pragma unroll
     for (int k = 1; k < 8; ++k) {
-      const int64_t at = low + k * step;
+      const I at = low + k * step;
       if (at <= high && first[at] <= i) below = k;
     }
     low += below * step;
@@ -176,31 +178,147 @@ __global__ void __launch_bounds__(kFillBlock) page_count_kernel(PageArgs a) {
   }
 }
 
-// Adds the counts up. SMALL: counts the pages of a release itself, and moves pages and fills slots.
-template <bool RELEASE, bool SMALL>
+// A call's sums over the CTA's threads: n of those before this one, and of all.
+struct Sum {
+  int before, all;
+};
+__device__ __forceinline__ Sum sum_before(int n, int (&warp_sum)[32]) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  int sum = n;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int below = __shfl_up_sync(0xffffffffu, sum, d);
+    if (lane >= d) sum += below;
+  }
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  int s = warp_sum[lane];
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int below = __shfl_up_sync(0xffffffffu, s, d);
+    if (lane >= d) s += below;
+  }
+  const int before = __shfl_sync(0xffffffffu, s, max(warp - 1, 0));
+  return Sum{(warp > 0 ? before : 0) + sum - n, __shfl_sync(0xffffffffu, s, 31)};
+}
+
+// What a small call keeps of its sequences.
+struct Sequences {
+  int first[kPlanBlock], low[kPlanBlock], high[kPlanBlock];
+  int warp_sum[32];
+};
+
+// Small calls: a thread takes a sequence, then pages, then rows. The counts fit 32 bits: a release looks at 32 K entries at
+// most (small_call), an assign has 4 K rows.
+__global__ void __launch_bounds__(kPlanBlock) page_release_small_kernel(PageArgs a) {
+  __shared__ Sequences q;
+  __shared__ bool refused[kPlanBlock];
+  __shared__ int any_refused;
+  begin();
+  const int b = threadIdx.x, B = static_cast<int>(a.B);
+  const int64_t height = *a.count;
+  Span e{0, 0};
+  if (b < B) span_of<true>(a, b, e);
+  int n = static_cast<int>(max(e.high - e.low, int64_t(0)));
+  if (b == 0) any_refused = 0;
+  refused[b] = false;
+  Sum sum = sum_before(n, q.warp_sum);
+  q.first[b] = sum.before;
+  q.low[b] = static_cast<int>(e.low);
+  __syncthreads();
+  const auto entry = [&](int i, int& s) {
+    s = bisect(q.first, B, i);
+    return a.table + s * a.max_pages + q.low[s] + (i - q.first[s]);
+  };
+  for (int i = threadIdx.x; i < sum.all; i += kPlanBlock) {
+    int s;
+    const int32_t page = *entry(i, s);
+    if (!is_page(a, page, s)) refused[s] = true, any_refused = 1;
+  }
+  __syncthreads();
+  if (any_refused) {  // their sequences keep all they have
+    if (refused[b]) n = 0;
+    sum = sum_before(n, q.warp_sum);
+    q.first[b] = sum.before;
+    __syncthreads();
+  }
+  const bool ok = height >= 0 && height <= a.n_pages && sum.all <= a.n_pages - height;
+  if (!ok) {
+    if (b == 0) record_error(a.status, JATTN_ERR_POOL, 95, 0);
+    return;
+  }
+  int32_t* const top = a.free_pages + (height + sum.all - 1);
+  for (int i = threadIdx.x; i < sum.all; i += kPlanBlock) {
+    int s;
+    int32_t* from = entry(i, s);
+    top[-i] = *from;
+    *from = -1;
+  }
+  if (b == 0 && sum.all > 0) *a.count = height + sum.all;
+}
+
+__global__ void __launch_bounds__(kPlanBlock) page_assign_small_kernel(PageArgs a) {
+  __shared__ Sequences q;
+  __shared__ int64_t start[kPlanBlock], off[kPlanBlock + 1];  // start: -1 where the sequence is skipped
+  begin();
+  const int b = threadIdx.x, B = static_cast<int>(a.B);
+  const int64_t height = *a.count;
+  const bool ragged = a.off != nullptr;
+  Span e{0, 0};
+  bool taken = false;
+  if (b < B) taken = span_of<false>(a, b, e);
+  if (ragged)
+    for (int i = b; i <= B; i += kPlanBlock) off[i] = a.off[i];
+  start[b] = taken ? a.start[b] : -1;
+  const Sum sum = sum_before(static_cast<int>(max(e.high - e.low, int64_t(0))), q.warp_sum);
+  q.first[b] = sum.before;
+  q.low[b] = static_cast<int>(e.low);
+  q.high[b] = static_cast<int>(e.high);
+  __syncthreads();
+  const bool ok = height >= 0 && height <= a.n_pages && sum.all <= height;
+  if (!ok && b == 0) record_error(a.status, JATTN_ERR_POOL, 95, 0);
+  const int32_t* const top = a.free_pages + (height - 1);
+  // a row's page is in the table, or still on the stack
+  const auto slot_of_row = [&](int64_t r) -> int64_t {
+    int64_t i = 0;
+    int s = static_cast<int>(r);
+    if (ragged) {
+      if (r >= off[B]) return -1;
+      s = static_cast<int>(bisect(off, static_cast<int64_t>(B), r));
+      i = r - off[s];
+      if (i < 0 || r >= off[s + 1]) return -1;
+    }
+    if (start[s] < 0) return -1;
+    const int64_t pos = start[s] + i, j = pos >> a.page_shift;
+    if (j >= q.high[s]) return -1;
+    const int32_t page = j < q.low[s] ? a.table[s * a.max_pages + j] : top[-(q.first[s] + (j - q.low[s]))];
+    if (!is_page(a, page, s)) return -1;
+    return (static_cast<int64_t>(page) << a.page_shift) + (pos & (a.page_size - 1));
+  };
+  if (a.slots != nullptr)
+    for (int64_t r = threadIdx.x; r < a.total; r += kPlanBlock) a.slots[r] = ok ? slot_of_row(r) : -1;
+  if (!ok) return;
+  for (int i = threadIdx.x; i < sum.all; i += kPlanBlock) {
+    const int s = bisect(q.first, B, i);
+    const int32_t page = top[-i];
+    a.table[s * a.max_pages + q.low[s] + (i - q.first[s])] = is_page(a, page, s) ? page : -1;
+  }
+  if (b == 0 && sum.all > 0) *a.count = height - sum.all;
+}
+
+// Adds the counts of a large call up.
+template <bool RELEASE>
 __global__ void __launch_bounds__(kPlanBlock) page_plan_kernel(PageArgs a) {
-  constexpr bool UNITS = !RELEASE && !SMALL;
+  constexpr bool UNITS = !RELEASE;
   __shared__ int64_t warp_sum[2][32];
-  __shared__ int64_t own[SMALL ? kPlanBlock : 1], own_off[SMALL && !RELEASE ? kPlanBlock + 1 : 1];
-  __shared__ Plan plan;
   __shared__ int bad;
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  int64_t* first = SMALL ? own : first_of(a);
+  int64_t* first = first_of(a);
   begin();
   int64_t height = 0;
   if (threadIdx.x == 0) {
     bad = 0;
     height = *a.count;
-  }
-  if constexpr (SMALL && !RELEASE)
-    if (a.off != nullptr)
-      for (int64_t b = threadIdx.x; b <= a.B; b += kPlanBlock) own_off[b] = a.off[b];
-  if constexpr (SMALL && RELEASE) {
-    for (int64_t b = warp; b < a.B; b += kPlanBlock / 32) {
-      const int64_t n = pages_back(a, b, lane);
-      if (lane == 0) own[b] = n;
-    }
-    __syncthreads();
   }
   __syncthreads();
   int64_t total = 0, total_units = 0;
@@ -266,17 +384,7 @@ __global__ void __launch_bounds__(kPlanBlock) page_plan_kernel(PageArgs a) {
     p.prefix = UNITS && a.off != nullptr && !bad && a.off[a.B] <= a.total;
     p.top = RELEASE ? height + total : height;
     if (p.pages > 0) *a.count = RELEASE ? height + total : height - total;
-    if constexpr (SMALL) plan = p;
-    else *plan_of(a) = p;
-  }
-  if constexpr (SMALL) {
-    __syncthreads();
-    // slots first: a row's page may be in the table or still on the stack
-    if constexpr (!RELEASE)
-      if (a.slots != nullptr)
-        for (int64_t r = threadIdx.x; r < a.total; r += kPlanBlock)
-          a.slots[r] = row_slot(a, first, a.off != nullptr ? own_off : nullptr, plan, r);
-    for (int64_t i = threadIdx.x; i < plan.pages; i += kPlanBlock) move_page<RELEASE>(a, first, plan.top, i);
+    *plan_of(a) = p;
   }
 }
 
@@ -376,8 +484,8 @@ size_t page_scratch_bytes(int64_t B, int64_t total, int64_t max_pages) {
 }
 
 cudaError_t launch_page_assign(const PageArgs& a, int sms, cudaStream_t stream) {
-  if (small_call(a.B, a.total, a.max_pages)) return launch_early(page_plan_kernel<false, true>, a, 1, kPlanBlock, stream);
-  const cudaError_t e = launch_early(page_plan_kernel<false, false>, a, 1, kPlanBlock, stream);
+  if (small_call(a.B, a.total, a.max_pages)) return launch_early(page_assign_small_kernel, a, 1, kPlanBlock, stream);
+  const cudaError_t e = launch_early(page_plan_kernel<false>, a, 1, kPlanBlock, stream);
   if (e != cudaSuccess) return e;
   PageArgs f = a;
   f.units = std::max(1, std::min(kFillBlock, kFillRows / a.page_size));
@@ -387,9 +495,9 @@ cudaError_t launch_page_assign(const PageArgs& a, int sms, cudaStream_t stream) 
 }
 
 cudaError_t launch_page_release(const PageArgs& a, int sms, cudaStream_t stream) {
-  if (small_call(a.B, -1, a.max_pages)) return launch_early(page_plan_kernel<true, true>, a, 1, kPlanBlock, stream);
+  if (small_call(a.B, -1, a.max_pages)) return launch_early(page_release_small_kernel, a, 1, kPlanBlock, stream);
   cudaError_t e = launch_early(page_count_kernel, a, ctas_for(a.B, kFillBlock / 32, sms), kFillBlock, stream);
-  if (e == cudaSuccess) e = launch_early(page_plan_kernel<true, false>, a, 1, kPlanBlock, stream);
+  if (e == cudaSuccess) e = launch_early(page_plan_kernel<true>, a, 1, kPlanBlock, stream);
   if (e != cudaSuccess) return e;
   return launch_early(page_return_kernel, a, ctas_for(a.B * a.max_pages, kFillBlock * 4, sms), kFillBlock, stream);
 }
