@@ -228,8 +228,8 @@ cudaError_t with_norm_shape(int n, F&& f) {
     }
     if constexpr (FOUR) {
       if (n > 64 && n <= 128) return f(NormShape<32, 4, NARROW, WIDE>{});
-      if (V == 4 && n > 128 && n <= 256) return f(NormShape<64, 4, NARROW, WIDE>{});
-      if (V == 4 && n > 256 && n <= 512) return f(NormShape<128, 4, NARROW, WIDE>{});
+      if (V < 8 && n > 128 && n <= 256) return f(NormShape<64, 4, NARROW, WIDE>{});
+      if (V < 8 && n > 256 && n <= 512) return f(NormShape<128, 4, NARROW, WIDE>{});
       if (n > 512 && n <= 1024) return f(NormShape<256, 4, NARROW, WIDE>{});
     }
     if (n <= 16) return f(NormShape<8, 2, NARROW, WIDE>{});
@@ -239,8 +239,9 @@ cudaError_t with_norm_shape(int n, F&& f) {
     if (n <= 256) return f(NormShape<128, 2, NARROW, WIDE>{});
     if (n <= 512) return f(NormShape<256, 2, NARROW, WIDE>{});
     if (n <= 1024) return f(NormShape<512, 2, NARROW, WIDE>{});
-    if (V == 8 || n <= 2048) return f(NormShape<1024, 2, NARROW, WIDE>{});
-    return f(NormShape<1024, 4, NARROW, WIDE>{});
+    if constexpr (V < 8)
+      if (n > 2048) return f(NormShape<1024, 4, NARROW, WIDE>{});
+    return f(NormShape<1024, 2, NARROW, WIDE>{});
   }
 }
 

@@ -202,108 +202,184 @@ __device__ __forceinline__ Sum sum_before(int n, int (&warp_sum)[32]) {
   return Sum{(warp > 0 ? before : 0) + sum - n, __shfl_sync(0xffffffffu, s, 31)};
 }
 
-// What a small call keeps of its sequences.
-struct Sequences {
-  int first[kPlanBlock], low[kPlanBlock], high[kPlanBlock];
-  int warp_sum[32];
-};
+// Small calls: a thread takes a sequence. The counts fit 32 bits: a release looks at 64 K entries at most (small_call), an
+// assign has 4 K rows. Where no sequence moves more than kOwn pages (or has more rows), as in a step of serving, its thread
+// moves them itself; finding a page's sequence by bisection, even in shared memory, costs the one SM more than all else
+// (916 sequences of 4 rows placed and given back: 6.7 us against 17.4).
+constexpr int kOwn = 4;
 
-// Small calls: a thread takes a sequence, then pages, then rows. The counts fit 32 bits: a release looks at 32 K entries at
-// most (small_call), an assign has 4 K rows.
 __global__ void __launch_bounds__(kPlanBlock) page_release_small_kernel(PageArgs a) {
-  __shared__ Sequences q;
+  __shared__ int first[kPlanBlock], low[kPlanBlock], moves[kPlanBlock], warp_sum[32];
   __shared__ bool refused[kPlanBlock];
-  __shared__ int any_refused;
   begin();
   const int b = threadIdx.x, B = static_cast<int>(a.B);
   const int64_t height = *a.count;
   Span e{0, 0};
   if (b < B) span_of<true>(a, b, e);
   int n = static_cast<int>(max(e.high - e.low, int64_t(0)));
-  if (b == 0) any_refused = 0;
-  refused[b] = false;
-  Sum sum = sum_before(n, q.warp_sum);
-  q.first[b] = sum.before;
-  q.low[b] = static_cast<int>(e.low);
-  __syncthreads();
-  const auto entry = [&](int i, int& s) {
-    s = bisect(q.first, B, i);
-    return a.table + s * a.max_pages + q.low[s] + (i - q.first[s]);
+  int32_t* const mine = a.table + b * a.max_pages + e.low;
+  int32_t page[kOwn];
+#pragma unroll
+  for (int j = 0; j < kOwn; ++j) page[j] = j < n ? mine[j] : 0;
+  Sum sum = sum_before(n, warp_sum);
+  const auto fits = [&] {
+    const bool ok = height >= 0 && height <= a.n_pages && sum.all <= a.n_pages - height;
+    if (!ok && b == 0) record_error(a.status, JATTN_ERR_POOL, 95, 0);
+    return ok;
   };
-  for (int i = threadIdx.x; i < sum.all; i += kPlanBlock) {
-    int s;
-    const int32_t page = *entry(i, s);
-    if (!is_page(a, page, s)) refused[s] = true, any_refused = 1;
-  }
-  __syncthreads();
-  if (any_refused) {  // their sequences keep all they have
-    if (refused[b]) n = 0;
-    sum = sum_before(n, q.warp_sum);
-    q.first[b] = sum.before;
+  if (!__syncthreads_or(n > kOwn)) {
+    bool good = true;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j)
+      if (j < n) good = is_page(a, page[j], b) && good;
+    if (__syncthreads_or(!good)) {  // their sequences keep all they have
+      if (!good) n = 0;
+      sum = sum_before(n, warp_sum);
+    }
+    if (!fits()) return;
+    int32_t* const to = a.free_pages + (height + sum.all - 1 - sum.before);
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j)
+      if (j < n) {
+        to[-j] = page[j];
+        mine[j] = -1;
+      }
+  } else {
+    // a few lanes a sequence, so that all threads have work, or eight
+    int width = kPlanBlock;
+    while (width > 8 && width * B > kPlanBlock) width /= 2;
+    const int group = b / width, lane = b % width;
+    constexpr int kAtOnce = 8;  // entries of a lane that are on their way together
+    const auto each = [&](auto&& f) {
+      for (int s = group; s < B; s += kPlanBlock / width)
+        for (int j = lane; j < moves[s]; j += width * kAtOnce) {
+          int32_t* const from = a.table + s * a.max_pages + low[s] + j;
+          int32_t got[kAtOnce];
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i) got[i] = j + i * width < moves[s] ? from[i * width] : 0;
+#pragma unroll
+          for (int i = 0; i < kAtOnce; ++i)
+            if (j + i * width < moves[s]) f(s, j + i * width, got[i], from + i * width);
+        }
+    };
+    first[b] = sum.before;
+    low[b] = static_cast<int>(e.low);
+    moves[b] = n;
+    refused[b] = false;
     __syncthreads();
-  }
-  const bool ok = height >= 0 && height <= a.n_pages && sum.all <= a.n_pages - height;
-  if (!ok) {
-    if (b == 0) record_error(a.status, JATTN_ERR_POOL, 95, 0);
-    return;
-  }
-  int32_t* const top = a.free_pages + (height + sum.all - 1);
-  for (int i = threadIdx.x; i < sum.all; i += kPlanBlock) {
-    int s;
-    int32_t* from = entry(i, s);
-    top[-i] = *from;
-    *from = -1;
+    bool good = true;
+    each([&](int s, int, int32_t got, int32_t*) {
+      if (!is_page(a, got, s)) good = false, refused[s] = true;
+    });
+    if (__syncthreads_or(!good)) {
+      if (refused[b]) n = 0;
+      sum = sum_before(n, warp_sum);
+      first[b] = sum.before;
+      moves[b] = n;
+      __syncthreads();
+    }
+    if (!fits()) return;
+    int32_t* const top = a.free_pages + (height + sum.all - 1);
+    each([&](int s, int j, int32_t got, int32_t* from) {
+      top[-(first[s] + j)] = got;
+      *from = -1;
+    });
   }
   if (b == 0 && sum.all > 0) *a.count = height + sum.all;
 }
 
 __global__ void __launch_bounds__(kPlanBlock) page_assign_small_kernel(PageArgs a) {
-  __shared__ Sequences q;
+  __shared__ int first[kPlanBlock], low[kPlanBlock], high[kPlanBlock], warp_sum[32];
   __shared__ int64_t start[kPlanBlock], off[kPlanBlock + 1];  // start: -1 where the sequence is skipped
   begin();
   const int b = threadIdx.x, B = static_cast<int>(a.B);
   const int64_t height = *a.count;
   const bool ragged = a.off != nullptr;
   Span e{0, 0};
-  bool taken = false;
-  if (b < B) taken = span_of<false>(a, b, e);
-  if (ragged)
-    for (int i = b; i <= B; i += kPlanBlock) off[i] = a.off[i];
-  start[b] = taken ? a.start[b] : -1;
-  const Sum sum = sum_before(static_cast<int>(max(e.high - e.low, int64_t(0))), q.warp_sum);
-  q.first[b] = sum.before;
-  q.low[b] = static_cast<int>(e.low);
-  q.high[b] = static_cast<int>(e.high);
-  __syncthreads();
+  bool taken = false, few = true;
+  int64_t from = b, rows = b < B ? 1 : 0;
+  if (b < B) {
+    taken = span_of<false>(a, b, e);
+    if (ragged) {
+      from = a.off[b];
+      rows = a.off[b + 1] - from;
+      // a thread writes its sequence's rows where the offsets are prefix sums
+      few = from >= 0 && rows >= 0 && rows <= kOwn && rows <= a.total - from && (b > 0 || from == 0);
+    }
+  }
+  const int64_t begins = taken ? a.start[b] : -1;
+  const int n = static_cast<int>(max(e.high - e.low, int64_t(0)));
+  few = few && n <= kOwn;
+  const Sum sum = sum_before(n, warp_sum);
   const bool ok = height >= 0 && height <= a.n_pages && sum.all <= height;
   if (!ok && b == 0) record_error(a.status, JATTN_ERR_POOL, 95, 0);
   const int32_t* const top = a.free_pages + (height - 1);
-  // a row's page is in the table, or still on the stack
-  const auto slot_of_row = [&](int64_t r) -> int64_t {
-    int64_t i = 0;
-    int s = static_cast<int>(r);
-    if (ragged) {
-      if (r >= off[B]) return -1;
-      s = static_cast<int>(bisect(off, static_cast<int64_t>(B), r));
-      i = r - off[s];
-      if (i < 0 || r >= off[s + 1]) return -1;
-    }
-    if (start[s] < 0) return -1;
-    const int64_t pos = start[s] + i, j = pos >> a.page_shift;
-    if (j >= q.high[s]) return -1;
-    const int32_t page = j < q.low[s] ? a.table[s * a.max_pages + j] : top[-(q.first[s] + (j - q.low[s]))];
-    if (!is_page(a, page, s)) return -1;
+  const auto slot_at = [&](int32_t page, int64_t pos) {
     return (static_cast<int64_t>(page) << a.page_shift) + (pos & (a.page_size - 1));
   };
-  if (a.slots != nullptr)
-    for (int64_t r = threadIdx.x; r < a.total; r += kPlanBlock) a.slots[r] = ok ? slot_of_row(r) : -1;
-  if (!ok) return;
-  for (int i = threadIdx.x; i < sum.all; i += kPlanBlock) {
-    const int s = bisect(q.first, B, i);
-    const int32_t page = top[-i];
-    a.table[s * a.max_pages + q.low[s] + (i - q.first[s])] = is_page(a, page, s) ? page : -1;
+  if (!__syncthreads_or(!few)) {
+    int32_t* const mine = a.table + b * a.max_pages + e.low;
+    int32_t page[kOwn + 1];  // the one that rows share with earlier ones, and the new ones
+    const bool shared = ok && taken && a.slots != nullptr && rows > 0 && (begins & (a.page_size - 1)) != 0;
+    page[0] = shared ? mine[-1] : -1;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) page[j + 1] = ok && j < n ? top[-(sum.before + j)] : -1;
+    if (shared && !is_page(a, page[0], b)) page[0] = -1;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j)
+      if (ok && j < n) {
+        if (!is_page(a, page[j + 1], b)) page[j + 1] = -1;
+        mine[j] = page[j + 1];
+      }
+    if (a.slots != nullptr) {
+      if (ragged)
+        for (int64_t r = a.off[B] + b; r < a.total; r += kPlanBlock) a.slots[r] = -1;
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i)
+        if (i < rows) {
+          const int64_t pos = begins + i;
+          const int which = static_cast<int>((pos >> a.page_shift) - e.low) + 1;
+          int32_t p = page[0];
+#pragma unroll
+          for (int j = 1; j <= kOwn; ++j)
+            if (which == j) p = page[j];
+          a.slots[from + i] = taken && p >= 0 ? slot_at(p, pos) : -1;
+        }
+    }
+  } else {
+    if (ragged)
+      for (int i = b; i <= B; i += kPlanBlock) off[i] = a.off[i];
+    start[b] = begins;
+    first[b] = sum.before;
+    low[b] = static_cast<int>(e.low);
+    high[b] = static_cast<int>(e.high);
+    __syncthreads();
+    // a row's page is in the table, or still on the stack
+    const auto slot_of_row = [&](int64_t r) -> int64_t {
+      int64_t i = 0;
+      int s = static_cast<int>(r);
+      if (ragged) {
+        if (r >= off[B]) return -1;
+        s = static_cast<int>(bisect(off, static_cast<int64_t>(B), r));
+        i = r - off[s];
+        if (i < 0 || r >= off[s + 1]) return -1;
+      }
+      if (start[s] < 0) return -1;
+      const int64_t pos = start[s] + i, j = pos >> a.page_shift;
+      if (j >= high[s]) return -1;
+      const int32_t page = j < low[s] ? a.table[s * a.max_pages + j] : top[-(first[s] + (j - low[s]))];
+      return is_page(a, page, s) ? slot_at(page, pos) : -1;
+    };
+    if (a.slots != nullptr)
+      for (int64_t r = threadIdx.x; r < a.total; r += kPlanBlock) a.slots[r] = ok ? slot_of_row(r) : -1;
+    if (ok)
+      for (int i = threadIdx.x; i < sum.all; i += kPlanBlock) {
+        const int s = bisect(first, B, i);
+        const int32_t page = top[-i];
+        a.table[s * a.max_pages + low[s] + (i - first[s])] = is_page(a, page, s) ? page : -1;
+      }
   }
-  if (b == 0 && sum.all > 0) *a.count = height - sum.all;
+  if (b == 0 && ok && sum.all > 0) *a.count = height - sum.all;
 }
 
 // Adds the counts of a large call up.
@@ -474,7 +550,7 @@ int64_t ctas_for(int64_t n, int64_t per_cta, int sms) {
 // Calls that one CTA serves: all sequences in its shared memory, and a few turns of its threads at most for their rows
 // and pages.
 bool small_call(int64_t B, int64_t total, int64_t max_pages) {
-  return B <= kPlanBlock && (total >= 0 ? total <= 4 * kPlanBlock : B * max_pages <= 32 * kPlanBlock);
+  return B <= kPlanBlock && (total >= 0 ? total <= 4 * kPlanBlock : B * max_pages <= 64 * kPlanBlock);
 }
 
 }  // namespace

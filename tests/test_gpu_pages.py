@@ -174,6 +174,85 @@ def test_page_errors_leave_everything_else_alone(B):
     assert J.device_status() == 0 and np.array_equal(table.cpu().numpy(), t)
 
 
+@pytest.mark.parametrize("B", [3, 900])
+@pytest.mark.parametrize("rows", [1, 3, 4, 5])
+def test_page_errors_of_a_few_rows_each(B, rows):
+    """Calls whose sequences move no more pages than a thread holds, and one more: sequences past their table, bad offsets, short
+    pools, numbers that are no pages, padding, each against the list or in what it may touch."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    page, P_ = 2, 6
+    n_pages = B * 5
+    new = np.full(B, rows, np.int64)
+    total = B * rows + 3
+    for first in (0, 1, 2, 5):
+        pool, ref = J.page_pool(n_pages, page), R.Pool(n_pages, page)
+        t = np.full((B, P_), -1, np.int32)
+        before = np.full(B, first, np.int64)
+        assert ref.assign(t, np.zeros(B, np.int64), before, first * B) is not None
+        table = torch.from_numpy(np.full((B, P_), -1, np.int32)).cuda()
+        J.page_assign(pool, table, cu(np.zeros(B)), off=cu(prefix(before)))
+        agree(pool, table, ref, t)
+
+        def copies():
+            p2, r2 = J.PagePool(pool.free_pages.clone(), pool.count.clone(), page), R.Pool(n_pages, page)
+            r2.free = list(ref.free)
+            return p2, table.clone(), r2, t.copy()
+
+        # rows behind the table, sequences that are skipped
+        p2, table2, r2, t2 = copies()
+        start = before.copy()
+        start[1], start[2] = 2**40, -5
+        want = r2.assign(t2, start, new, total)
+        slots = J.page_assign(p2, table2, cu(start), off=cu(prefix(new)), total=total)
+        assert J.device_status() == LENGTH and np.array_equal(slots.cpu().numpy(), want)
+        agree(p2, table2, r2, t2)
+        # without slots, and given back: all as before
+        p2, table2, r2, t2 = copies()
+        assert J.page_assign(p2, table2, cu(before), off=cu(prefix(new)), total=total, slots=False) is None
+        assert r2.assign(t2, before, new, total) is not None
+        agree(p2, table2, r2, t2)
+        J.page_release(p2, table2, cu(before + rows), keep=cu(before))
+        assert J.device_status() == 0
+        agree(p2, table2, ref, t)
+        # offsets that are no prefix sums
+        for at, value in ((1, total + 9), (2, 0), (0, 1), (0, -2), (B, total + 5), (1, -7), (1, 2**62), (2, -2**62)):
+            p2, table2, r2, t2 = copies()
+            off = prefix(new)
+            off[at] = value
+            slots = J.page_assign(p2, table2, cu(before), off=cu(off), total=total)
+            assert J.device_status() in (OFFSETS, LENGTH, POOL), (at, value)
+            assert bool(((slots >= -1) & (slots < n_pages * page)).all())
+            taken = table2[table2 >= 0]
+            assert len(set(taken.tolist())) == taken.numel() == n_pages - int(p2.count.item())
+        # a pool without enough
+        p2, table2, r2, t2 = copies()
+        need = int((-(-(first + rows) // page) - (-(-first // page))) * B)
+        if need > 0:
+            p2.count.fill_(need - 1)
+            slots = J.page_assign(p2, table2, cu(before), off=cu(prefix(new)), total=total)
+            assert J.device_status() == POOL and bool((slots == -1).all()) and torch.equal(table2, table)
+            assert int(p2.count.item()) == need - 1
+            # a number that is no page on top of the stack: the first sequence's first page
+            p2, table2, r2, t2 = copies()
+            good = p2.free_pages.clone()
+            p2.free_pages[len(r2.free) - 1] = -3
+            slots = J.page_assign(p2, table2, cu(before), off=cu(prefix(new)), total=total)
+            assert J.device_status() == PAGES
+            p3 = J.PagePool(good, pool.count.clone(), page)
+            table3 = table.clone()
+            all_good = J.page_assign(p3, table3, cu(before), off=cu(prefix(new)), total=total)
+            at = -(-first // page)
+            bad = all_good == -2  # none
+            lo = max(0, at * page - first)
+            bad[lo:min(rows, lo + page)] = True
+            assert bool((slots[bad] == -1).all()) and torch.equal(slots[~bad], all_good[~bad])
+            table3[0, at] = -1
+            assert torch.equal(table2, table3)
+    assert J.device_status() == 0
+
+
 def test_pages_in_graphs_and_on_streams():
     """A captured serving step (pages, append, decode) replayed while lengths grow, and two pools on two streams."""
     import jagged_attention_recsys_gdpa_gb300 as J
