@@ -203,10 +203,10 @@ __device__ __forceinline__ Sum sum_before(int n, int (&warp_sum)[32]) {
 }
 
 // Small calls: a thread takes a sequence. The counts fit 32 bits: a release looks at 64 K entries at most (small_call), an
-// assign has 4 K rows. Where no sequence moves more than kOwn pages (or has more rows), as in a step of serving, its thread
-// moves them itself; finding a page's sequence by bisection, even in shared memory, costs the one SM more than all else
+// assign has 4 K rows. Where no sequence moves more than kOwn pages or has more than kOwnRows rows, as in a step of serving, its thread
+// moves and writes them itself; finding a page's sequence by bisection, even in shared memory, costs the one SM more than all else
 // (916 sequences of 4 rows placed and given back: 6.7 us against 17.4).
-constexpr int kOwn = 4;
+constexpr int kOwn = 4, kOwnRows = 8;
 
 __global__ void __launch_bounds__(kPlanBlock) page_release_small_kernel(PageArgs a) {
   __shared__ int first[kPlanBlock], low[kPlanBlock], moves[kPlanBlock], warp_sum[32];
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kPlanBlock) page_assign_small_kernel(PageArgs 
       from = a.off[b];
       rows = a.off[b + 1] - from;
       // a thread writes its sequence's rows where the offsets are prefix sums
-      few = from >= 0 && rows >= 0 && rows <= kOwn && rows <= a.total - from && (b > 0 || from == 0);
+      few = from >= 0 && rows >= 0 && rows <= kOwnRows && rows <= a.total - from && (b > 0 || from == 0);
     }
   }
   const int64_t begins = taken ? a.start[b] : -1;
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kPlanBlock) page_assign_small_kernel(PageArgs 
       if (ragged)
         for (int64_t r = a.off[B] + b; r < a.total; r += kPlanBlock) a.slots[r] = -1;
 #pragma unroll
-      for (int i = 0; i < kOwn; ++i)
+      for (int i = 0; i < kOwnRows; ++i)
         if (i < rows) {
           const int64_t pos = begins + i;
           const int which = static_cast<int>((pos >> a.page_shift) - e.low) + 1;

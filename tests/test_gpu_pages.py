@@ -175,15 +175,15 @@ def test_page_errors_leave_everything_else_alone(B):
 
 
 @pytest.mark.parametrize("B", [3, 900])
-@pytest.mark.parametrize("rows", [1, 3, 4, 5])
+@pytest.mark.parametrize("rows", [1, 3, 4, 5, 8, 9])
 def test_page_errors_of_a_few_rows_each(B, rows):
     """Calls whose sequences move no more pages than a thread holds, and one more: sequences past their table, bad offsets, short
     pools, numbers that are no pages, padding, each against the list or in what it may touch."""
     import jagged_attention_recsys_gdpa_gb300 as J
 
     clear(J)
-    page, P_ = 2, 6
-    n_pages = B * 5
+    page, P_ = 2, 7
+    n_pages = B * 7
     new = np.full(B, rows, np.int64)
     total = B * rows + 3
     for first in (0, 1, 2, 5):
