@@ -123,6 +123,26 @@ Tensor empty(at::IntArrayRef sizes, c10::Device device, at::ScalarType type) {
 }
 Tensor empty(at::IntArrayRef sizes, const Tensor& like, at::ScalarType type) { return empty(sizes, like.device(), type); }
 
+// Two fp32 tensors of a shape that are used together, from one allocation (each starts at 256 bytes).
+struct Pair {
+  Tensor first, second;
+  Pair() = default;
+  Pair(at::IntArrayRef sizes, c10::Device device) {
+    const int64_t n = (c10::multiply_integers(sizes) + 63) / 64 * 64;
+    const Tensor both = empty({2 * n}, device, at::kFloat);
+    first = part(both, sizes, 0);
+    second = part(both, sizes, n);
+  }
+
+ private:
+  static Tensor part(const Tensor& both, at::IntArrayRef sizes, int64_t offset) {
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(both.storage()), both.key_set(), both.dtype());
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+    t.unsafeGetTensorImpl()->set_storage_offset(offset);
+    return t;
+  }
+};
+
 struct Strides {
   int64_t row, head;
 };
@@ -235,21 +255,21 @@ PyObject* layer_norm(PyObject* const* a) {
   }
   const int64_t* live = live_rows(x, off);
   Place place(x.get_device());
-  Tensor y, mean, rstd;
+  Tensor y;
+  Pair stats;
   int rc;
   {
     Unlocked unlocked;
     if (!out) y = empty(x.sizes(), x, x.scalar_type());
     const auto rows = x.sizes().slice(0, x.dim() - 1);
-    mean = empty(rows, x, at::kFloat);
-    rstd = empty(rows, x, at::kFloat);
+    stats = Pair(rows, x.device());
     rc = lib.layer_norm(&p, live, x.data_ptr(), address(weight), address(bias), (out ? *out : y).data_ptr(),
-                        static_cast<float*>(mean.data_ptr()), static_cast<float*>(rstd.data_ptr()), place.status, kStatusBytes,
-                        place.stream);
+                        static_cast<float*>(stats.first.data_ptr()), static_cast<float*>(stats.second.data_ptr()),
+                        place.status, kStatusBytes, place.stream);
   }
   finish(rc, "jattn_layer_norm");
   if (out) written(*out);
-  return pack(out ? given(a[5]) : wrap(y), wrap(mean), wrap(rstd));
+  return pack(out ? given(a[5]) : wrap(y), wrap(stats.first), wrap(stats.second));
 }
 
 // (dy, x, weight, mean, rstd, off, bias, out) -> (dx, dweight, dbias)
@@ -362,16 +382,16 @@ PyObject* rotary_tables(PyObject* const* a) {
   if (index < 0) index = c10::cuda::current_device();
   Place place(static_cast<int>(index));
   const c10::Device device(at::kCUDA, static_cast<c10::DeviceIndex>(index));
-  Tensor cos, sin;
+  Pair tables;
   int rc;
   {
     Unlocked unlocked;
-    cos = empty({rows, dim / 2}, device, at::kFloat);
-    sin = empty({rows, dim / 2}, device, at::kFloat);
-    rc = lib.rotary_tables(&p, static_cast<float*>(cos.data_ptr()), static_cast<float*>(sin.data_ptr()), place.stream);
+    tables = Pair({rows, dim / 2}, device);
+    rc = lib.rotary_tables(&p, static_cast<float*>(tables.first.data_ptr()), static_cast<float*>(tables.second.data_ptr()),
+                           place.stream);
   }
   finish(rc, "jattn_rotary_tables");
-  return pack(wrap(cos), wrap(sin));
+  return pack(wrap(tables.first), wrap(tables.second));
 }
 
 // What both page calls are given first: free pages, count, page size (checked when the pool was made), page table.
