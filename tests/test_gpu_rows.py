@@ -106,6 +106,61 @@ def test_layer_norm_sizes(n, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [249, 253, 381, 505, 509, 761, 763, 1009, 1010, 1019, 1533, 2041, 2045, 3001, 4087, 4091, 6129, 6133, 6137, 8177, 8185])
+def test_layer_norm_rows_that_start_anywhere(n, dtype):
+    """Odd widths around each shape's limits, of rows that share a shift in fewer and more than one turn of the grid."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    w, b = rand((n,), FP32, n + 1, 1.0).cuda(), rand((n,), FP32, n + 2).cuda()
+    for rows in (1, 9, 70):
+        check_norm(J, rand((rows, n), dtype, n, 0.7).cuda(), w, b, rand((rows, n), dtype, n + 3).cuda())
+    # many rows: each as in a small call that starts at the same place
+    x = rand((64, n), dtype, n).cuda()
+    y, mean, rstd = J.layer_norm_forward(x, w, b)
+    y2, mean2, rstd2 = J.layer_norm_forward(x.repeat(100, 1), w, b)
+    assert torch.equal(y2, y.repeat(100, 1)) and torch.equal(mean2, mean.repeat(100)) and torch.equal(rstd2, rstd.repeat(100))
+    assert J.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [101, 1001, 5001, 7001])
+def test_layer_norm_in_padded_buffers(n, dtype):
+    """Odd widths in buffers whose rows are whole vectors, with heads beside them, from an odd place on: what lies around the rows
+    is NaN and stays as it is."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    wide = -(-(n + 3) // 8) * 8
+    x, dy = (rand((41, 2, n), dtype, s, 0.3) for s in (1, 2))
+    w, b = rand((n,), dtype, 3, 1.0).cuda(), rand((n,), dtype, 4).cuda()
+
+    def inside(t, start):
+        whole = torch.full((41, 3, wide), float("nan"), dtype=dtype, device="cuda")
+        view = whole[:, :2, start:start + n]
+        if t is not None:
+            view.copy_(t)
+        return whole, view
+
+    for start in (0, 3):
+        xs, ds = inside(x, start)[1], inside(dy, start)[1]
+        whole, out = inside(None, start)
+        y, mean, rstd = J.layer_norm_forward(xs, w, b, out=out)
+        bounds = R.layer_norm_bounds(np64(x), np64(w), np64(b), float(np.float32(1e-5)), dtype)
+        for got, v, e in zip((y, mean, rstd), R.layer_norm(np64(x), np64(w), np64(b), 1e-5), bounds):
+            within(got, v, e)
+        grads, gout = inside(None, start)
+        got = J.layer_norm_backward(ds, xs, w, mean, rstd, out=gout)
+        args = np64(dy), np64(x), np64(w), np64(rstd)
+        for g, v, e in zip(got, R.layer_norm_grads(*args), R.layer_norm_grad_bounds(*args, dtype, dtype, 82 + 64)):
+            within(g, v, e)
+        for buffer in (whole, grads):
+            buffer[:, :2, start:start + n] = float("nan")
+            assert bool(torch.isnan(buffer).all())
+    assert J.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("how", ["dense", "fused", "odd", "heads first"])
 @pytest.mark.parametrize("n", [64, 128, 100, 1024])
 def test_layer_norm_heads_and_strides(n, how, dtype):
