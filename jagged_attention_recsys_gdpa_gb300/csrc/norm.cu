@@ -48,6 +48,15 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
   uint32_t mine[K];  // which values of the lane's vectors are the row's
 #pragma unroll
   for (int k = 0; k < K; ++k) mine[k] = inside<V, SHIFT>(first + k * L * V, a.N);
+  // the first rows fly while the weights are fetched
+  RowQueue<A, S, 1> queue;
+  constexpr int kAhead = decltype(queue)::kAhead;
+  const auto fetch = [&](uint32_t row, int slot) {
+    if (row < live) queue.fetch(ring, slot, x, x + row_at(a.x, a.split, row), first, mine);
+    copies_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(r + i * step, i);
   float w[KEPT ? E : V], b[KEPT ? E : V];
   if constexpr (KEPT)
 #pragma unroll
@@ -57,27 +66,16 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
     }
   float4* const held = reinterpret_cast<float4*>(ring + RowQueue<A, S, 1>::kBytes) + lane;  // [w, b][E / 4][L]
   if constexpr (HELD) {
-    if (group == 0)
+    for (int part = group; part < 2 * K; part += G) {  // vector part / 2 of w or b
+      const int k = part / 2;
+      const bool bias = part % 2;
+      load_weight<T, V, SHIFT>(bias ? a.b : a.w, a.wide_weight, first + k * L * V, a.N, bias ? 0.0f : 1.0f, w);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, w);
-        load_weight<T, V, SHIFT>(a.b, a.wide_weight, first + k * L * V, a.N, 0.0f, b);
-#pragma unroll
-        for (int i = 0; i < V; i += 4) {
-          held[(k * V + i) / 4 * L] = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-          held[(E + k * V + i) / 4 * L] = make_float4(b[i], b[i + 1], b[i + 2], b[i + 3]);
-        }
-      }
+      for (int i = 0; i < V; i += 4)
+        held[((bias ? E : 0) + k * V + i) / 4 * L] = make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
     __syncthreads();
   }
-  RowQueue<A, S, 1> queue;
-  constexpr int kAhead = decltype(queue)::kAhead;
-  const auto fetch = [&](uint32_t row, int slot) {
-    if (row < live) queue.fetch(ring, slot, x, x + row_at(a.x, a.split, row), first, mine);
-    copies_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) fetch(r + i * step, i);
   int slot = 0, free_slot = kAhead;
   // the rows of a warp, and of a CTA that shares one, end together
   for (; base < total; base += step, r += step) {

@@ -38,13 +38,7 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
   uint32_t mine[K];  // which values of the lane's vectors are the row's
 #pragma unroll
   for (int k = 0; k < K; ++k) mine[k] = inside<V, SHIFT>(first + k * L * V, a.N);
-  float w[KEPT ? E : V], dw[E], db[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
-  if constexpr (KEPT)
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-      load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, k));
+  // the first rows fly while the weights are fetched
   RowQueue<A, S, 2> queue_x, queue_dy;
   constexpr int kAhead = decltype(queue_x)::kAhead;
   char* const ring_dy = ring + queue_x.kBytes;
@@ -64,6 +58,13 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
   fetch_stats(r);
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) fetch(r + i * step, i);
+  float w[KEPT ? E : V], dw[E], db[E];
+#pragma unroll
+  for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
+  if constexpr (KEPT)
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, k));
   int turn = 0, slot = 0, free_slot = kAhead;
   for (uint32_t base = blockIdx.x * G; base < total; base += step, r += step, turn ^= 1) {
     float d[E], g[E], s[3];
