@@ -2,8 +2,8 @@
 //
 // Whole numbers throughout, so each order is fixed: the i-th page that a call wants, sequence by sequence, is the i-th
 // from the top of the stack of free pages, and the i-th that it gives back becomes the i-th from the top. One CTA adds
-// the sequences' counts up (and moves the pool's height); then every page finds its sequence by bisection, needs nothing
-// from the others, and gives its rows their slots, which are consecutive numbers. Small calls do both in one CTA and
+// the sequences' counts up (and moves the pool's height); then warps move their sequences' pages back, or every page that
+// is taken finds its sequence by bisection and gives its rows their slots, which are consecutive numbers. Small calls do both in one CTA and
 // launch, a thread a sequence: they are bound by the chain of loads (lengths, then entries or free pages) and the launch.
 // Large ones are bound by the slots' stores, 8 bytes a row, and their instructions.
 #include <algorithm>
@@ -128,21 +128,13 @@ __device__ __forceinline__ I bisect(const I* first, I n, I i) {
   return low;
 }
 
-// Page number i of the call's pages.
-template <bool RELEASE>
-__device__ __forceinline__ void move_page(const PageArgs& a, const int64_t* first, int64_t top, int64_t i) {
+// Page number i that a call takes.
+__device__ __forceinline__ void take_page(const PageArgs& a, const int64_t* first, int64_t top, int64_t i) {
   const int64_t b = bisect(first, a.B, i);
   Span e;
-  span_of<RELEASE>(a, b, e);
-  int32_t* entry = a.table + b * a.max_pages + e.low + (i - first[b]);
-  int32_t* slot = a.free_pages + (top - 1 - i);
-  if constexpr (RELEASE) {
-    *slot = *entry;
-    *entry = -1;
-  } else {
-    const int32_t page = *slot;
-    *entry = is_page(a, page, b) ? page : -1;
-  }
+  span_of<false>(a, b, e);
+  const int32_t page = a.free_pages[top - 1 - i];
+  a.table[b * a.max_pages + e.low + (i - first[b])] = is_page(a, page, b) ? page : -1;
 }
 
 // Slot of row r of sequence b: from the table where its page was there before, else from the stack.
@@ -464,12 +456,33 @@ __global__ void __launch_bounds__(kPlanBlock) page_plan_kernel(PageArgs a) {
   }
 }
 
+// A few warps a sequence (a.units of them) move its pages: two rounds of loads, where finding each page's sequence by bisection
+// took seven.
 __global__ void __launch_bounds__(kFillBlock) page_return_kernel(PageArgs a) {
   begin();
+  const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kFillBlock + threadIdx.x) / 32, b = warp / a.units;
+  if (b >= a.B) return;
   const Plan plan = *plan_of(a);
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kFillBlock + threadIdx.x; i < plan.pages;
-       i += static_cast<int64_t>(gridDim.x) * kFillBlock)
-    move_page<true>(a, first_of(a), plan.top, i);
+  const int64_t* first = first_of(a);
+  const int64_t own = first[b], next = b + 1 < a.B ? first[b + 1] : plan.pages;
+  const int64_t keep = a.keep != nullptr ? a.keep[b] : 0;
+  if (plan.pages == 0 || next <= own) return;
+  constexpr int kAtOnce = 8;  // entries of a lane that are on their way together
+  int32_t* const from = a.table + b * a.max_pages + pages_for(a, keep);
+  int32_t* const to = a.free_pages + (plan.top - 1 - own);
+  const int64_t n = next - own;
+  for (int64_t j = (warp - b * a.units) * 32 * kAtOnce + threadIdx.x % 32; j < n; j += static_cast<int64_t>(a.units) * 32 * kAtOnce) {
+    int32_t page[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (j + 32 * i < n) page[i] = from[j + 32 * i];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (j + 32 * i < n) {
+        to[-(j + 32 * i)] = page[i];
+        from[j + 32 * i] = -1;
+      }
+  }
 }
 
 // Pages and slots of a large call. A thread finds one unit: a sequence's page with new rows; then a few lanes each (no
@@ -488,7 +501,7 @@ __global__ void __launch_bounds__(kFillBlock) page_assign_kernel(PageArgs a) {
   const int64_t thread = static_cast<int64_t>(blockIdx.x) * kFillBlock + threadIdx.x;
   const int64_t threads = static_cast<int64_t>(gridDim.x) * kFillBlock;
   if (!plan.ok || !plan.prefix) {  // refused calls, one row each, and offsets that are no prefix sums: row by row
-    for (int64_t i = thread; i < plan.pages; i += threads) move_page<false>(a, first, plan.top, i);
+    for (int64_t i = thread; i < plan.pages; i += threads) take_page(a, first, plan.top, i);
     if (a.slots != nullptr)
       for (int64_t r = thread; r < a.total; r += threads) a.slots[r] = row_slot(a, first, a.off, plan, r);
     return;
@@ -575,7 +588,10 @@ cudaError_t launch_page_release(const PageArgs& a, int sms, cudaStream_t stream)
   cudaError_t e = launch_early(page_count_kernel, a, ctas_for(a.B, kFillBlock / 32, sms), kFillBlock, stream);
   if (e == cudaSuccess) e = launch_early(page_plan_kernel<true>, a, 1, kPlanBlock, stream);
   if (e != cudaSuccess) return e;
-  return launch_early(page_return_kernel, a, ctas_for(a.B * a.max_pages, kFillBlock * 4, sms), kFillBlock, stream);
+  // warps of a sequence: those that its table has work for, and no more than run at a time
+  PageArgs f = a;
+  f.units = static_cast<int>(std::max<int64_t>(1, std::min((a.max_pages + 255) / 256, static_cast<int64_t>(sms) * 64 / a.B)));
+  return launch_early(page_return_kernel, f, (a.B * f.units + kFillBlock / 32 - 1) / (kFillBlock / 32), kFillBlock, stream);
 }
 
 }  // namespace jattn

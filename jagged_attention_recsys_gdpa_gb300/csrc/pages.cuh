@@ -16,7 +16,7 @@ struct PageArgs {
   int64_t* slots;       // assign: [total], nullptr: not wanted
   int64_t n_pages, B, total, max_pages;
   int page_size, page_shift;
-  int units;            // set by the launch: pages that a CTA of a large call looks up at a time
+  int units;            // set by the launch of a large call: pages that a CTA looks up at a time; release: warps of a sequence
   void* scratch;
   DevStatus* status;
 };
