@@ -27,7 +27,7 @@ __device__ __forceinline__ void begin() {
 constexpr int kPlanBlock = 1024;
 constexpr int kFillBlock = 256;
 // Rows of a CTA of the large calls, about: its lookups, a chain of loads, are hidden behind other CTAs' stores (5.8 M rows, assigned
-// and given back, when these were measured: 2,048 27.5 us, 4,096 26.7, 8,192 30.5; now 24).
+// and given back, when these were measured: 2,048 27.5 us, 4,096 26.7, 8,192 30.5; now 21).
 constexpr int kFillRows = 4096;
 
 // What the counts' sum leaves in scratch for the pages and rows: the prefix sums follow it.
