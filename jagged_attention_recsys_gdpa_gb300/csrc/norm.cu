@@ -4,8 +4,8 @@
 // A row stays in the registers of its lanes between the sums, so x is read once and y written once: a copy, bound by
 // memory. d is formed with the rounded mean m~ of a first sum; a second sum over d gives both mean(d^2) and mean(d) =
 // m - m~, which corrects the mean and the variance, so rows whose mean is far larger than their spread keep fp32's
-// accuracy. Rows of up to 32 lanes share a CTA; longer ones have one of their own. The grid is persistent: a lane has the
-// same columns in every row that it takes, keeps their weights in registers, and loads the next row before it works on one.
+// accuracy. Rows share a CTA where their lanes leave room. The grid is persistent: a lane has the same columns in every row
+// that it takes, keeps their weights in registers (or shared memory), and has two more rows on their way.
 #include "norm.cuh"
 
 namespace jattn {
