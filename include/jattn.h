@@ -467,8 +467,8 @@ int jattn_layer_norm(const jattn_norm_t* p, const int64_t* live_rows, const void
  *   dweight = sum over all rows of dy h,  dbias = sum over all rows of dy,
  * the sums in fp32, in an order that depends on the sizes and the GPU alone, and
  * rounded once to weight_type. dweight needs weight and dbias needs dweight; either may
- * be NULL. dx may be dy or x itself (the same pointer and strides). scratch: jattn_layer_norm_bwd_scratch_size bytes (0 without
- * dweight), 256-byte aligned, of any content; calls that run at the same time need
+ * be NULL. dx may be dy or x itself (the same pointer and strides). scratch: jattn_layer_norm_bwd_scratch_size bytes (none without
+ * dweight, and 0, and NULL, for a few rows), 256-byte aligned, of any content; calls that run at the same time need
  * one each. The size depends on rows, heads, N and type, and is asked for with the
  * device current that the call runs on. Without rows dweight and dbias are zero. */
 int jattn_layer_norm_bwd_scratch_size(const jattn_norm_t* p, size_t* bytes);

@@ -1252,7 +1252,7 @@ int jattn_layer_norm_bwd_scratch_size(const jattn_norm_t* p, size_t* bytes) {
   int parts = 0;
   for (const NormPath path : {NormPath::kVectors, NormPath::kShifted, NormPath::kValues})
     parts = std::max(parts, norm_bwd_parts(p->type, path, p->rows * p->heads, p->N, dev.sms));
-  *bytes = al256(static_cast<size_t>(parts) * 2 * p->N * sizeof(float));
+  *bytes = parts < 2 ? 0 : al256(static_cast<size_t>(parts) * 2 * p->N * sizeof(float));
   return JATTN_OK;
 }
 
@@ -1294,14 +1294,19 @@ int jattn_layer_norm_bwd(const jattn_norm_t* p, const int64_t* live_rows, const 
   NormArgs a = norm_args(*p, live_rows, x, dy, dx, weight, nullptr, ws, &path);
   a.mean = const_cast<float*>(mean);
   a.rstd = const_cast<float*>(rstd);
-  a.partial = dweight ? static_cast<float*>(scratch) : nullptr;
+  const int parts = dweight && p->rows > 0 ? norm_bwd_parts(p->type, path, p->rows * p->heads, p->N, dev.sms) : 0;
+  if (parts == 1) {
+    a.dw = dweight;
+    a.db = dbias;
+  } else if (parts > 1) {
+    a.partial = static_cast<float*>(scratch);
+  }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (p->rows > 0) {
     const cudaError_t e = launch_norm_bwd(p->type, path, a, dev.sms, st);
     if (e != cudaSuccess) return cuda_fail("layer norm backward launch", e);
   }
-  if (!dweight) return JATTN_OK;
-  const int parts = p->rows > 0 ? norm_bwd_parts(p->type, path, p->rows * p->heads, p->N, dev.sms) : 0;
+  if (!dweight || parts == 1) return JATTN_OK;
   const NormJoinArgs j{a.partial, dweight, dbias, parts, p->N};
   const cudaError_t e = launch_norm_join(p->weight_type, j, st);
   return e == cudaSuccess ? JATTN_OK : cuda_fail("layer norm gradient launch", e);

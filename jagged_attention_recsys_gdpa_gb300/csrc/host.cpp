@@ -298,13 +298,13 @@ PyObject* layer_norm_bwd(PyObject* const* a) {
       rc = lib.layer_norm_bwd_scratch_size(&p, &bytes);
       dw = empty(weight->sizes(), x, weight->scalar_type());
       if (wants_bias) db = empty(weight->sizes(), x, weight->scalar_type());
-      scratch = empty({static_cast<int64_t>(bytes)}, x, at::kByte);
+      if (bytes > 0) scratch = empty({static_cast<int64_t>(bytes)}, x, at::kByte);
     }
     if (rc == 0)
       rc = lib.layer_norm_bwd(&p, live, dy.data_ptr(), x.data_ptr(), address(weight),
                               static_cast<const float*>(mean.data_ptr()), static_cast<const float*>(rstd.data_ptr()),
                               (out ? *out : dx).data_ptr(), weight ? dw.data_ptr() : nullptr,
-                              weight && wants_bias ? db.data_ptr() : nullptr, weight ? scratch.data_ptr() : nullptr, bytes,
+                              weight && wants_bias ? db.data_ptr() : nullptr, bytes > 0 ? scratch.data_ptr() : nullptr, bytes,
                               place.status, kStatusBytes, place.stream);
   }
   finish(rc, "jattn_layer_norm_bwd");

@@ -5,7 +5,8 @@
 // The sum of d = x - mean is taken along: mean(d) is what the fp32 mean lost by its rounding (see norm.cu).
 // A persistent grid keeps dw and db of its rows in registers, each lane those of its own columns, and loads the next row
 // before it works on one; a CTA adds its groups in shared memory and writes one partial row to scratch, and a second
-// kernel adds the partial rows. Every order is fixed, so results are the same from call to call.
+// kernel adds the partial rows. (Of rows that one CTA takes at once it writes dw and db itself.) Every order is fixed, so results
+// are the same from call to call.
 #include "norm.cuh"
 
 namespace jattn {
@@ -127,20 +128,29 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
 #pragma unroll
     for (int k = 0; k < K; ++k) store_at<T, V, SHIFT>(to + first + k * L * V, mine[k], vector_of<V>(d, k));
   }
-  if (a.partial == nullptr) return;
+  if (a.partial == nullptr && a.dw == nullptr) return;
   launch_dependents();
-  float* to = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
+  const auto put = [&](int half, int c, float v) {
+    if (a.partial != nullptr) {
+      a.partial[(static_cast<int64_t>(blockIdx.x) * 2 + half) * a.N + c] = v;
+    } else if (void* const to = half == 0 ? a.dw : a.db; to != nullptr) {
+      if (a.wide_weight) static_cast<float*>(to)[c] = v;
+      else static_cast<T*>(to)[c] = from_float<T>(v);
+    }
+  };
   float* joined = reinterpret_cast<float*>(ring);  // [groups][N], where rows have been
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     if constexpr (G > 1) __syncthreads();
-    float* own = G > 1 ? joined + group * a.N : to + half * a.N;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int c = first + k * L * V + i;
-        if (c >= 0 && c < a.N) own[c] = half == 0 ? dw[k * V + i] : db[k * V + i];
+        if (c < 0 || c >= a.N) continue;
+        const float v = half == 0 ? dw[k * V + i] : db[k * V + i];
+        if constexpr (G > 1) joined[group * a.N + c] = v;
+        else put(half, c, v);
       }
     if constexpr (G > 1) {
       __syncthreads();
@@ -148,7 +158,7 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
         float t = 0.0f;
 #pragma unroll
         for (int i = 0; i < G; ++i) t += joined[i * a.N + c];
-        to[half * a.N + c] = t;
+        put(half, c, t);
       }
     }
   }

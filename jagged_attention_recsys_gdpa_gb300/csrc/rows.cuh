@@ -27,7 +27,9 @@ struct NormArgs {
   const void* b;      // forward only; nullptr: zeros
   float* mean;        // [rows, heads]: written by the forward (nullptr: not kept), read by the backward
   float* rstd;
-  float* partial;     // backward: [parts][2][N], nullptr: no gradient of the weight is asked for
+  float* partial;     // backward: [parts][2][N], nullptr: no gradient of the weight is asked for, or one CTA writes it
+  void* dw;           // backward in one CTA: the weight's and the bias' gradients, else nullptr
+  void* db;           // nullptr: not asked for
   const int64_t* live;  // device: rows that count (nullptr: all)
   int64_t rows;
   int heads, N;
