@@ -14,8 +14,10 @@
 #include <string>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/TracerMode.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -173,6 +175,12 @@ void written(const Tensor& out) {
   if (!out.is_inference()) out.unsafeGetTensorImpl()->bump_version();
 }
 
+// Whether autograd follows t: a gradient is asked for, or a tangent (forward mode, in any grad mode) comes with it.
+bool followed(const Tensor& t) {
+  return (at::GradMode::is_enabled() && t.requires_grad()) ||
+         (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined());
+}
+
 void check_index(const Tensor& t, c10::Device device, const char* name) {
   TORCH_CHECK_VALUE(t.scalar_type() == at::kLong && t.dim() == 1 && t.device() == device && t.is_contiguous(), name,
                     " must be a contiguous int64 tensor of one dimension on the other tensors' device");
@@ -310,6 +318,13 @@ PyObject* layer_norm_bwd(PyObject* const* a) {
   finish(rc, "jattn_layer_norm_bwd");
   if (out) written(*out);
   return pack(out ? given(a[7]) : wrap(dx), weight ? wrap(dw) : none(), weight && wants_bias ? wrap(db) : none());
+}
+
+// (x, cos, sin) -> whether the rotation of x has to go through its autograd function: autograd follows x, or a trace is recorded.
+PyObject* rotary_followed(PyObject* const* a) {
+  TORCH_CHECK_VALUE(!followed(tensor(a[1], "cos")) && !followed(tensor(a[2], "sin")),
+                    "tables take no gradient: pass detached tensors");
+  return PyBool_FromLong(followed(tensor(a[0], "x")) || at::tracer::impl::is_dispatch_enabled());
 }
 
 // (x, cos, sin, off, start, layout, inverse, out) -> y
@@ -527,6 +542,7 @@ PyMethodDef methods[] = {def<bind, 3>("bind"),
                          def<layer_norm, 6>("layer_norm"),
                          def<layer_norm_bwd, 8>("layer_norm_bwd"),
                          def<rotary, 8>("rotary"),
+                         def<rotary_followed, 3>("rotary_followed"),
                          def<rotary_tables, 10>("rotary_tables"),
                          def<page_assign, 8>("page_assign"),
                          def<page_release, 6>("page_release"),

@@ -73,17 +73,32 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, off=None):
 class _Rotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, cos, sin, off, start, layout, inverse):
+        ctx.set_materialize_grads(False)
         ctx.save_for_backward(cos, sin, off, start)
+        ctx.save_for_forward(cos, sin, off, start)
         ctx.how = layout, inverse
         return B.host().rotary(x, cos, sin, off, start, layout, inverse, None)
 
     @staticmethod
     def backward(ctx, dy):
+        return _Rotary._turn(ctx, dy, True), None, None, None, None, None, None
+
+    @staticmethod
+    def jvp(ctx, dx, dcos, dsin, *others):
+        if dcos is not None or dsin is not None:
+            raise ValueError("tables take no gradient: pass detached tensors")
+        return _Rotary._turn(ctx, dx, False)
+
+    @staticmethod
+    def _turn(ctx, d, back):
+        """A gradient turned back, or a tangent turned as the rows are."""
+        if d is None:
+            return None
         cos, sin, off, start = ctx.saved_tensors
         layout, inverse = ctx.how
-        if dy.stride(-1) != 1:
-            dy = dy.contiguous()
-        return _Rotary.apply(dy, cos, sin, off, start, layout, not inverse), None, None, None, None, None, None
+        if d.stride(-1) != 1:
+            d = d.contiguous()
+        return _Rotary.apply(d, cos, sin, off, start, layout, inverse != back)
 
 
 def rotary(x, tables, off=None, start=None, layout="interleaved", inverse=False, out=None):
@@ -91,19 +106,17 @@ def rotary(x, tables, off=None, start=None, layout="interleaved", inverse=False,
     first R columns of every head, (2m, 2m + 1) in layout "interleaved" or (m, m + R/2) in layout "half", turn by the angles
     of the row's position (back, with ``inverse``); the other columns stay. Row i of sequence b (``off`` int64 [B+1])
     stands at start[b] + i (``start`` int64 [B], None: 0); without off row r stands at start[r] (int64 [total], None: r).
-    A negative start skips its rows as padding is. ``out`` may be x. With autograd (the gradient turns back), but for ``out``.
-    See jattn_rotary."""
+    A negative start skips its rows as padding is. ``out`` may be x. With autograd in both modes (the gradient turns back, a
+    tangent as the rows do) and in traces, but for ``out``. See jattn_rotary."""
     cos, sin = tables
     if layout not in _LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}")
-    if torch.is_grad_enabled():
-        if cos.requires_grad or sin.requires_grad:
-            raise ValueError("tables take no gradient: pass detached tensors")
-        if x.requires_grad:
-            if out is not None:
-                raise ValueError("out is written without a gradient: call under torch.no_grad() or on a detached x")
-            return _Rotary.apply(x, cos, sin, off, start, _LAYOUTS[layout], bool(inverse))
-    return (B._host or B.host()).rotary(x, cos, sin, off, start, _LAYOUTS[layout], inverse, out)
+    host = B._host or B.host()
+    if host.rotary_followed(x, cos, sin):
+        if out is not None:
+            raise ValueError("out is written without a gradient: call under torch.no_grad() or on a detached x")
+        return _Rotary.apply(x, cos, sin, off, start, _LAYOUTS[layout], bool(inverse))
+    return host.rotary(x, cos, sin, off, start, _LAYOUTS[layout], inverse, out)
 
 
 def rotary_tables(rows, dim, base=10000.0, scaling=None, factor=1.0, original=None, beta_fast=32.0, beta_slow=1.0, first=0,
