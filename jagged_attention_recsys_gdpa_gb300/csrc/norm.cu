@@ -108,10 +108,12 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
     s2[1] = both(square);
     row_sum<L, 2>(s2, slots2[group]);
     const float off = s2[0] * a.inv_n;
-    const float rstd = rsqrtf(fmaxf(fmaf(-off, off, s2[1] * a.inv_n), 0.0f) + a.eps);
+    const float variance = fmaf(-off, off, s2[1] * a.inv_n);
+    const float rstd = rsqrtf((variance < 0.0f ? 0.0f : variance) + a.eps);  // (a NaN stays one)
     if (r >= total || (r >= live && !a.zero_behind)) continue;
     if (lane == 0 && a.mean != nullptr) {
-      a.mean[r] = r < live ? m + off : 0.0f;
+      // of a row with an infinity m is the mean already, and off is inf - inf
+      a.mean[r] = r < live ? (isfinite(off) ? m + off : m) : 0.0f;
       a.rstd[r] = r < live ? rstd : 0.0f;
     }
     T* to = y + row_at(a.y, a.split, r);

@@ -12,6 +12,29 @@ from tests.test_gpu_rows import BF16, FP16, FP32, TYPES, clear, cu, rand, within
 pytestmark = pytest.mark.gpu
 
 
+# ------------------------------------------------------------------ statistics
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n", [1, 7, 64, 100, 1001, 2048, 9000])
+def test_statistics_of_rows_that_are_not_finite(n, dtype):
+    """The formulas' own: a NaN makes both NaN, an infinity is its row's mean and leaves no spread that is a number."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    inf, nan = float("inf"), float("nan")
+    x = rand((6, n), dtype, 1)
+    x[1, n // 2], x[2, n - 1], x[3, 0], x[4, :] = nan, inf, -inf, inf
+    y, mean, rstd = J.layer_norm_forward(x.cuda())
+    want = x.double().mean(-1).numpy()
+    got = np64(mean)
+    assert np.isnan(got[1]) and got[2] == inf and got[3] == -inf and got[4] == inf
+    assert np.isfinite(got[[0, 5]]).all() and np.isfinite(want[[0, 5]]).all()
+    assert bool(torch.isnan(rstd[1:5]).all()) and bool(torch.isfinite(rstd[[0, 5]]).all())
+    assert bool(torch.isnan(y[1:5]).all()) and bool(torch.isfinite(y[[0, 5]]).all())
+    dx, _, _ = J.layer_norm_backward(x.cuda(), x.cuda(), None, mean, rstd)
+    assert bool(torch.isnan(dx[1:5]).all()) and bool(torch.isfinite(dx[[0, 5]]).all())
+    assert J.device_status() == 0
+
+
 # ------------------------------------------------------------------ derivatives of the rotation
 def rotations():
     """Tables and positions of 40 rows: padding, a sequence that is skipped, positions behind the tables."""
