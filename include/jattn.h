@@ -449,6 +449,7 @@ typedef struct {
   int64_t x_row_stride, x_head_stride;
   int64_t y_row_stride, y_head_stride;   /* of y (forward) or dx (backward) */
   int64_t dy_row_stride, dy_head_stride; /* backward only */
+  int zero_stats;     /* 0 / 1 (forward only): padding's mean and rstd are set to zero even where y's rows are left */
 } jattn_norm_t;
 
 /* Layer norm of every row: with m = mean(x) and v = mean((x - m)^2),

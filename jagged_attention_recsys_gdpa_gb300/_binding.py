@@ -100,6 +100,7 @@ class Norm(ctypes.Structure):
         ("x_strides", ctypes.c_int64 * 2),
         ("y_strides", ctypes.c_int64 * 2),
         ("dy_strides", ctypes.c_int64 * 2),
+        ("zero_stats", ctypes.c_int),
     ]
 
 

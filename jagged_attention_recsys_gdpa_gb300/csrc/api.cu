@@ -1159,6 +1159,7 @@ int check_norm(const jattn_norm_t* p) {
   if (p->rows > INT32_MAX || p->rows * p->heads > INT32_MAX) return JATTN_ERR_INVALID;
   if (!known_type(p->type) || (p->weight_type != p->type && p->weight_type != JATTN_F32)) return JATTN_ERR_INVALID;
   if (p->zero_behind != 0 && p->zero_behind != 1) return JATTN_ERR_INVALID;
+  if (p->zero_stats != 0 && p->zero_stats != 1) return JATTN_ERR_INVALID;
   return JATTN_OK;
 }
 
@@ -1180,6 +1181,7 @@ NormArgs norm_args(const jattn_norm_t& p, const int64_t* live, const RowTensor& 
   a.inv_n = 1.0f / static_cast<float>(p.N);
   a.wide_weight = p.weight_type == JATTN_F32;
   a.zero_behind = p.zero_behind != 0;
+  a.zero_stats = a.zero_behind || p.zero_stats != 0;
   a.status = static_cast<DevStatus*>(ws);
   // where a row's stride is all its heads' the rows of all heads follow each other by the head's
   const auto even = [&](const RowTensor& t) { return !t.p || t.row == p.heads * t.head; };

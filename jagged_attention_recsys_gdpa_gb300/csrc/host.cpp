@@ -255,6 +255,7 @@ PyObject* layer_norm(PyObject* const* a) {
   TORCH_CHECK_VALUE(eps > 0.0 && std::isfinite(eps), "eps must be positive and finite");
   jattn_norm_t p = norm_params(x, weight, out);
   p.eps = static_cast<float>(eps);
+  p.zero_stats = true;  // the statistics are always this call's own
   if (out) check_out(*out, x);
   if (weight) check_weight(x, *weight, "weight");
   if (bias) {

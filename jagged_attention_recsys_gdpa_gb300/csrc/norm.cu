@@ -110,12 +110,13 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
     const float off = s2[0] * a.inv_n;
     const float variance = fmaf(-off, off, s2[1] * a.inv_n);
     const float rstd = rsqrtf((variance < 0.0f ? 0.0f : variance) + a.eps);  // (a NaN stays one)
-    if (r >= total || (r >= live && !a.zero_behind)) continue;
-    if (lane == 0 && a.mean != nullptr) {
+    if (r >= total) continue;
+    if (lane == 0 && a.mean != nullptr && (r < live || a.zero_stats)) {
       // of a row with an infinity m is the mean already, and off is inf - inf
       a.mean[r] = r < live ? (isfinite(off) ? m + off : m) : 0.0f;
       a.rstd[r] = r < live ? rstd : 0.0f;
     }
+    if (r >= live && !a.zero_behind) continue;
     T* to = y + row_at(a.y, a.split, r);
     const uint64_t scale = f2(rstd, rstd), shift = f2(-off * rstd, -off * rstd);
     if constexpr (KEPT) {

@@ -37,6 +37,7 @@ struct NormArgs {
   float eps, inv_n;   // inv_n: 1 / N
   bool wide_weight;   // w and b are fp32 whatever x is
   bool zero_behind;   // rows behind the live ones are set to zero, else left as they are
+  bool zero_stats;    // forward: so are their mean and rstd (always with zero_behind)
   DevStatus* status;
 };
 

@@ -13,6 +13,35 @@ pytestmark = pytest.mark.gpu
 
 
 # ------------------------------------------------------------------ statistics
+def poisoned(n):
+    """Memory that the next calls' outputs are likely to get: NaN."""
+    blocks = [torch.full((n,), float("nan"), device="cuda") for _ in range(16)]
+    torch.cuda.synchronize()
+    del blocks
+
+
+@pytest.mark.parametrize("n", [128, 100, 1001])
+@pytest.mark.parametrize("heads", [1, 3])
+def test_statistics_of_padding_are_zero(n, heads):
+    """mean and rstd are outputs that the call allocates: zero behind the last sequence, also where y is the caller's and its
+    padding stays as it was."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    for live, total in ((0, 5), (29, 40), (100, 300), (40, 40)):
+        off = cu(np.array([0, live // 2, live]))
+        x = rand((total, heads, n), BF16, 1).cuda()
+        out = torch.full_like(x, 5.0)
+        want = J.layer_norm_forward(x, off=off)
+        for _ in range(4):
+            poisoned(2 * (-(-total * heads // 64) * 64))
+            y, mean, rstd = J.layer_norm_forward(x, off=off, out=out)
+            assert torch.equal(mean, want[1]) and torch.equal(rstd, want[2])
+            assert bool((mean[live:] == 0).all()) and bool((rstd[live:] == 0).all())
+            assert bool((y[live:] == 5.0).all()) and torch.equal(y[:live], want[0][:live])
+    assert J.device_status() == 0
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n", [1, 7, 64, 100, 1001, 2048, 9000])
 def test_statistics_of_rows_that_are_not_finite(n, dtype):
