@@ -256,6 +256,10 @@ def host():
         if not os.path.exists(path):
             raise RuntimeError(f"_host.so not found at {path}; build it with "
                                "`python -m jagged_attention_recsys_gdpa_gb300.build` (no other path exists)")
+        built = _build.host_misfit()
+        if built:
+            raise RuntimeError(f"_host.so was built for {built}, which is not what is installed; build it again with "
+                               "`python -m jagged_attention_recsys_gdpa_gb300.build`")
         spec = importlib.util.spec_from_file_location("_host", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

@@ -3,8 +3,9 @@
 Each translation unit is compiled by its own nvcc process (in parallel),
 then linked into ``_build/libjattn.so`` next to this file. The host calls of the
 row operators and the page pool (``csrc/host.cpp``, on CPython's C API and
-PyTorch's headers) become the extension module ``_build/_host.so``. Nothing is
-installed; the binding loads both from that path.
+PyTorch's headers) become the extension module ``_build/_host.so``, which fits
+the PyTorch and the Python that it was built for (``_build/_host.for``) and is built
+again for others. Nothing is installed; the binding loads both from that path.
 """
 from __future__ import annotations
 
@@ -20,6 +21,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libjattn.so")
 HOST = os.path.join(BUILD, "_host.so")
+HOST_FOR = os.path.join(BUILD, "_host.for")
 SOURCES = ["api.cu", "sched.cu", "fwd.cu", "fwd_block.cu", "fwd_hilo.cu", "fwd_block_hilo.cu", "bwd.cu",
            "bwd_hilo.cu", "fwd_mx.cu", "bwd_mx.cu", "pma.cu", "rope.cu", "mx.cu", "cache.cu", "decode.cu",
            "norm.cu", "norm_bwd.cu", "rotary.cu", "pages.cu", "partition.cpp"]
@@ -45,6 +47,23 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _installed() -> str:
+    """What _host.so depends on beside its sources."""
+    import torch
+
+    return f"PyTorch {torch.__version__} {torch.version.git_version}, Python {sysconfig.get_config_var('SOABI')}"
+
+
+def host_misfit() -> str:
+    """What _host.so was built for, where that is not what is installed, else nothing."""
+    try:
+        with open(HOST_FOR) as f:
+            built = f.read()
+    except FileNotFoundError:
+        built = "an unknown PyTorch"
+    return "" if built == _installed() else built
+
+
 def _build_host() -> None:
     """The extension module, compiled against the PyTorch that is installed."""
     import torch
@@ -62,12 +81,18 @@ def _build_host() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on host.cpp:\n{r.stderr[-6000:]}")
     os.replace(tmp, HOST)
+    with open(tmp, "w") as f:
+        f.write(_installed())
+    os.replace(tmp, HOST_FOR)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     deps = _deps()
-    if not force and not _stale(LIB, deps) and not _stale(HOST, deps):
+    library, host = force or _stale(LIB, deps), force or _stale(HOST, deps) or host_misfit() != ""
+    if host and not library:
+        _build_host()
+    if not library:
         return LIB
     nvcc = _nvcc()
 
@@ -82,9 +107,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        host = ex.submit(_build_host)
+        module = ex.submit(_build_host) if host else None
         objs = list(ex.map(compile_one, SOURCES))
-        host.result()
+        if module is not None:
+            module.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
