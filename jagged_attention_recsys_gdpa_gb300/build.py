@@ -87,13 +87,23 @@ def _build_host() -> None:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """The library's path. Where the extension module fails, the error comes after the library has been built: attention and
+    the paged cache need nothing of it."""
     os.makedirs(BUILD, exist_ok=True)
     deps = _deps()
     library, host = force or _stale(LIB, deps), force or _stale(HOST, deps) or host_misfit() != ""
-    if host and not library:
-        _build_host()
-    if not library:
-        return LIB
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        module = ex.submit(_build_host) if host else None
+        if library:
+            _build_library()
+    if module is not None:
+        module.result()
+    if verbose and library:
+        print(f"built {LIB}", file=sys.stderr)
+    return LIB
+
+
+def _build_library() -> None:
     nvcc = _nvcc()
 
     def compile_one(src):
@@ -106,20 +116,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr[-6000:]}")
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        module = ex.submit(_build_host) if host else None
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        if module is not None:
-            module.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
     os.replace(tmp, LIB)
-    if verbose:
-        print(f"built {LIB}", file=sys.stderr)
-    return LIB
 
 
 if __name__ == "__main__":

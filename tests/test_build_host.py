@@ -58,3 +58,16 @@ def test_a_module_for_another_pytorch_is_built_again_and_nothing_else(elsewhere,
     (elsewhere / "_host.for").write_text("PyTorch 1.0, Python cpython-39")
     build_mod.build()
     assert [c[0] for c in commands] == ["g++"] and build_mod.host_misfit() == ""
+
+
+def test_a_module_that_fails_leaves_the_library(elsewhere, compilers):
+    """The error is raised, and attention and the paged cache have their library all the same."""
+    commands, failing = compilers
+    failing.add("g++")
+    with pytest.raises(RuntimeError, match="host.cpp"):
+        build_mod.build()
+    assert (elsewhere / "libjattn.so").exists() and not (elsewhere / "_host.so").exists()
+    del commands[:]
+    failing.clear()
+    build_mod.build()  # what is missing, and nothing else
+    assert [c[0] for c in commands] == ["g++"] and (elsewhere / "_host.so").exists()
