@@ -64,6 +64,54 @@ def test_statistics_of_rows_that_are_not_finite(n, dtype):
     assert J.device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,stride", [(1001, 1008), (1001, 3003), (1004, 2008), (4100, 8200), (100, 600), (127, 127 * 3)])
+def test_layer_norm_of_rows_laid_out_unlike_the_output(n, stride, dtype):
+    """Rows of a wider buffer, widths that are no whole vectors, dense outputs; gradients that are dense or as wide as x."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    x, dy = (rand((37, n), dtype, s, 0.3) for s in (1, 2))
+    w, b = rand((n,), FP32, 3, 1.0).cuda(), rand((n,), FP32, 4).cuda()
+
+    def inside(t, first):
+        whole = torch.full((37, stride), float("nan"), dtype=dtype, device="cuda")
+        view = whole[:, first:first + n]
+        view.copy_(t)
+        return view
+
+    y, mean, rstd = J.layer_norm_forward(x.cuda(), w, b)
+    bounds = R.layer_norm_bounds(np64(x), np64(w), np64(b), float(np.float32(1e-5)), dtype)
+    args = np64(dy), np64(x), np64(w), np64(rstd)
+    for first in {0, 3, stride - n}:
+        if first + n > stride:
+            continue
+        xs = inside(x, first)
+        for got, v, e in zip(J.layer_norm_forward(xs, w, b), R.layer_norm(np64(x), np64(w), np64(b), 1e-5), bounds):
+            within(got, v, e)
+        for ds in (dy.cuda(), inside(dy, first), inside(dy, 0)):
+            got = J.layer_norm_backward(ds, xs, w, mean, rstd)
+            for g, v, e in zip(got, R.layer_norm_grads(*args), R.layer_norm_grad_bounds(*args, dtype, FP32, 37 + 64)):
+                within(g, v, e)
+    assert J.device_status() == 0
+
+
+def test_layer_norm_gradient_of_a_frozen_weight():
+    """A weight that does not learn: x's gradient is the one that it has beside a weight that does."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    for dtype, wt in ((BF16, FP32), (FP32, FP32), (FP16, FP16)):
+        base, dy = rand((33, 4, 128), dtype, 1, 0.3).cuda(), rand((33, 4, 128), dtype, 4).cuda()
+        w, b = rand((128,), wt, 2, 1.0).cuda(), rand((128,), wt, 3).cuda()
+        _, mean, rstd = J.layer_norm_forward(base, w, b)
+        x = base.clone().requires_grad_(True)
+        J.layer_norm(x, w, b).backward(dy)
+        assert torch.equal(x.grad, J.layer_norm_backward(dy, base, w, mean, rstd)[0])
+        assert w.grad is None and b.grad is None
+    assert J.device_status() == 0
+
+
 # ------------------------------------------------------------------ derivatives of the rotation
 def rotations():
     """Tables and positions of 40 rows: padding, a sequence that is skipped, positions behind the tables."""
@@ -147,3 +195,192 @@ def test_rotary_is_recorded_by_a_trace():
     traced = torch.jit.trace(lambda z: J.rotary(z, t, off=off), x, check_trace=False)
     assert torch.equal(traced(other), J.rotary(other, t, off=off))
     J.device_status()
+
+
+# ------------------------------------------------------------------ every number of heads of a thread
+def turned(x, c, s, layout):
+    """x [n, H, D] by its rows' c and s [n, half] in fp32, each product and sum rounded by itself, rounded once to its type."""
+    half = c.shape[1]
+    y = x.to(FP32, copy=True)
+    ia = torch.arange(half, device="cuda") * (1 if layout == "half" else 2)
+    ib = ia + (half if layout == "half" else 1)
+    a, b = y[..., ia], y[..., ib]
+    c, s = c[:, None], s[:, None]
+    y[..., ia], y[..., ib] = a * c - b * s, a * s + b * c
+    return y.to(x.dtype)
+
+
+@pytest.mark.parametrize("how", ["dense", "fused", "pairs", "odd"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+def test_rotary_heads_of_a_thread(layout, dtype, how):
+    """Calls with more units than the GPU holds threads, where a thread takes 1 to 8 heads: head counts that select each number
+    and leave the last group short, whole heads, parts that end inside a vector, both directions, in place, padding."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    for heads in (1, 2, 3, 4, 5, 6, 7, 8, 9, 10):
+        for D, half, inverse, place in ((128, 64, False, True), (128, 29, True, False), (64, 20, True, True), (72, 13, False, False)):
+            n = 8_000_000 // (heads * D)  # at least 900,000 vectors of 16 bytes, a thread's head at a time 300,000
+            lens = torch.tensor([n // 3, 0, 1, n - n // 3 - 1 - 50])
+            off = torch.cat([torch.zeros(1, dtype=torch.int64), lens.cumsum(0)]).cuda()
+            live = n - 50
+            data = torch.randn(n, heads, D, generator=g, device="cuda").to(dtype)
+            if how == "dense":
+                x = data
+            elif how == "fused":
+                x = torch.empty(n, heads + 1, D, dtype=dtype, device="cuda")[:, 1:].copy_(data)
+            elif how == "pairs":  # two values off 16 bytes
+                x = torch.empty(n * heads * D + 2, dtype=dtype, device="cuda")[2:].view(n, heads, D).copy_(data)
+            else:
+                x = torch.empty(n * (heads * D + 1) + 1, dtype=dtype, device="cuda")[1:].view(n, heads * D + 1)[:, :heads * D]
+                x = x.unflatten(1, (heads, D)).copy_(data)
+            start = torch.randint(0, 1000, (4,), generator=g, device="cuda")
+            cos, sin = (torch.randn(int(lens.max()) + 1000, half, generator=g, device="cuda") for _ in range(2))
+            b = torch.repeat_interleave(torch.arange(4, device="cuda"), lens.cuda())
+            pos = torch.arange(live, device="cuda") - off[b] + start[b]
+            want = turned(data[:live], cos[pos], -sin[pos] if inverse else sin[pos], layout)
+            y = J.rotary(x, (cos, sin), off=off, start=start, layout=layout, inverse=inverse)
+            assert torch.equal(y[:live], want) and bool((y[live:] == 0).all()), (heads, D, half)
+            if place:
+                assert J.rotary(x, (cos, sin), off=off, start=start, layout=layout, inverse=inverse, out=x) is x
+                assert torch.equal(x[:live], want) and torch.equal(x[live:], data[live:]), (heads, D, half)
+    assert J.device_status() == 0
+
+
+# ------------------------------------------------------------------ uses beside the plain call
+def test_rotary_beyond_32_bit_offsets():
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    heads, D = 8, 128
+    n = (1 << 32) // (heads * D) + 300
+    if torch.cuda.mem_get_info()[0] < 6 * n * heads * D * 2:
+        pytest.skip("not enough free memory")
+    tables = J.rotary_tables(700, 128)
+    off = cu(np.array([0, n - 600, n - 5]))
+    start = cu(np.array([-1, 90]))
+    for layout in ("interleaved", "half"):
+        x = torch.zeros(n, heads, D, dtype=BF16, device="cuda")
+        x[-600:] = rand((600, heads, D), BF16, 7).cuda()
+        want = J.rotary(x[-600:], tables, start=torch.arange(90, 690, device="cuda"), layout=layout)
+        y = J.rotary(x, tables, off=off, start=start, layout=layout)
+        assert torch.equal(y[-600:-5], want[:-5]) and bool((y[-5:] == 0).all()) and bool((y[:5] == 0).all())
+        del y
+        J.rotary(x, tables, off=off, start=start, layout=layout, out=x)
+        assert torch.equal(x[-600:-5], want[:-5])
+        del x
+    assert J.device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_layer_norm_of_windows(dtype):
+    """Rows that share memory with their neighbours (a window that moves along): read as any rows are, and refused as an output."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    flat = rand((4000,), dtype, 5).cuda()
+    for n, step in ((128, 8), (127, 7), (1001, 1), (100, 3), (64, 32), (5, 2)):
+        x = flat.unfold(0, n, step)
+        y, mean, rstd = J.layer_norm_forward(x)
+        bounds = R.layer_norm_bounds(np64(x), None, None, float(np.float32(1e-5)), dtype)
+        for got, v, e in zip((y, mean, rstd), R.layer_norm(np64(x), None, None, 1e-5), bounds):
+            within(got, v, e)
+        dy = rand(tuple(x.shape), dtype, 6).cuda()
+        args = np64(dy), np64(x), None, np64(rstd)
+        within(J.layer_norm_backward(dy, x, None, mean, rstd)[0], R.layer_norm_grads(*args)[0],
+               R.layer_norm_grad_bounds(*args, dtype, dtype, 64)[0])
+        with pytest.raises(J.JattnError):
+            J.layer_norm_forward(x, out=x)
+    assert J.device_status() == 0
+
+
+def test_inference_mode():
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    x = rand((40, 3, 48), BF16, 1).cuda()
+    t, off, start = rotations()
+    want = J.rotary(x, t, off=off), J.layer_norm(x)
+    with torch.inference_mode():
+        z = x.clone()
+        assert torch.equal(J.rotary(z, t, off=off), want[0]) and torch.equal(J.layer_norm(z), want[1])
+        assert J.rotary(z, t, off=off, out=z) is z and torch.equal(z[:33], want[0][:33])
+        tables = J.rotary_tables(50, 40)
+    torch.equal(J.rotary(x, tables), J.rotary(x, J.rotary_tables(50, 40)))
+    assert J.device_status() == 0
+
+
+def test_a_training_step_through_autograd_in_a_graph():
+    """Norm and rotation with their backward pass, captured and replayed on new rows: bit for bit the eager step."""
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    tables = J.rotary_tables(300, 64)
+    off = cu(np.array([0, 200, 290]))
+    leaves = [rand((300, 8, 128), BF16, 1).cuda(), rand((128,), FP32, 2, 1.0).cuda(), rand((128,), FP32, 3).cuda()]
+    for t in leaves:
+        t.requires_grad_(True)
+    dy = rand((300, 6, 128), BF16, 4).cuda()
+
+    def step():
+        x, w, b = leaves
+        y = J.rotary(J.layer_norm(x[:, 1:7], w, b, off=off), tables, off=off, layout="half")
+        return (y.detach(), *torch.autograd.grad(y, leaves, dy))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for turn in range(3):
+        with torch.no_grad():
+            leaves[0].copy_(rand((300, 8, 128), BF16, 10 + turn))
+            leaves[0][290:] = float("nan")
+            leaves[1].mul_(1.25)
+            dy.copy_(rand((300, 6, 128), BF16, 20 + turn))
+            dy[290:] = float("nan")
+        graph.replay()
+        want = step()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+        assert bool((got[1][290:] == 0).all()) and bool((got[1][:, [0, 7]] == 0).all())
+    assert J.device_status() == 0
+
+
+def test_calls_from_several_threads():
+    """Each thread on a stream of its own, with nothing in common but the inputs."""
+    import threading
+
+    import jagged_attention_recsys_gdpa_gb300 as J
+
+    clear(J)
+    x, w = rand((2000, 4, 128), BF16, 1).cuda(), rand((128,), FP32, 2, 1.0).cuda()
+    tables = J.rotary_tables(2000, 128)
+    y, mean, rstd = J.layer_norm_forward(x, w, w)
+    want = (J.rotary(y, tables), *J.layer_norm_backward(y, x, w, mean, rstd))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    y, mean, rstd = J.layer_norm_forward(x, w, w)
+                    got = (J.rotary(y, tables), *J.layer_norm_backward(y, x, w, mean, rstd))
+                    if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                        bad.append("results differ")
+        except Exception as e:  # noqa: BLE001
+            bad.append(e)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+    assert J.device_status() == 0
