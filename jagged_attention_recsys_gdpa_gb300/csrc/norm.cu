@@ -32,7 +32,8 @@ template <typename A, typename S>
 __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBlock)) norm_kernel(NormArgs a) {
   using T = typename A::Type;
   constexpr int V = A::V, L = S::L, K = S::K, G = S::kGroups, E = K * V;
-  constexpr bool SHIFT = A::SHIFT, KEPT = E <= 24, HELD = kHeld<A, S>;  // KEPT: weights in registers
+  constexpr bool SHIFT = A::SHIFT, HELD = kHeld<A, S>, KEPT = !HELD;  // KEPT: weights in registers
+  static_assert(HELD || E <= 24, "the registers hold a lane's weights");
   extern __shared__ __align__(16) char ring[];
   __shared__ float slots1[G][kSumWarps<L>][1], slots2[G][kSumWarps<L>][2];
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
@@ -126,16 +127,11 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
     } else {
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if constexpr (HELD) {
 #pragma unroll
-          for (int i = 0; i < V; i += 4) {
-            const float4 w4 = held[(k * V + i) / 4 * L], b4 = held[(E + k * V + i) / 4 * L];
-            w[i] = w4.x, w[i + 1] = w4.y, w[i + 2] = w4.z, w[i + 3] = w4.w;
-            b[i] = b4.x, b[i + 1] = b4.y, b[i + 2] = b4.z, b[i + 3] = b4.w;
-          }
-        } else {
-          load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, 0));
-          load_weight<T, V, SHIFT>(a.b, a.wide_weight, first + k * L * V, a.N, 0.0f, vector_of<V>(b, 0));
+        for (int i = 0; i < V; i += 4) {
+          const float4 w4 = held[(k * V + i) / 4 * L], b4 = held[(E + k * V + i) / 4 * L];
+          w[i] = w4.x, w[i + 1] = w4.y, w[i + 2] = w4.z, w[i + 3] = w4.w;
+          b[i] = b4.x, b[i + 1] = b4.y, b[i + 2] = b4.z, b[i + 3] = b4.w;
         }
         float(&d)[V] = vector_of<V>(v, k);
         pairwise<V>([&](int i, int j) {

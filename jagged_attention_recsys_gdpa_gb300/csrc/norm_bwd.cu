@@ -23,7 +23,8 @@ template <typename A, typename S>
 __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBlock)) norm_bwd_kernel(NormArgs a) {
   using T = typename A::Type;
   constexpr int V = A::V, L = S::L, K = S::K, G = S::kGroups, E = K * V;
-  constexpr bool SHIFT = A::SHIFT, KEPT = E <= 16;
+  constexpr bool SHIFT = A::SHIFT;
+  static_assert(E <= 16, "a lane's weights and their gradients' sums stay in registers");
   extern __shared__ __align__(16) char ring[];
   __shared__ float slots[G][2][kSumWarps<L>][3];
   const int lane = threadIdx.x % L, group = threadIdx.x / L;
@@ -59,13 +60,12 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
   fetch_stats(r);
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) fetch(r + i * step, i);
-  float w[KEPT ? E : V], dw[E], db[E];
+  float w[E], dw[E], db[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
-  if constexpr (KEPT)
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, k));
+  for (int k = 0; k < K; ++k)
+    load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, k));
   int turn = 0, slot = 0, free_slot = kAhead;
   for (uint32_t base = blockIdx.x * G; base < total; base += step, r += step, turn ^= 1) {
     float d[E], g[E], s[3];
@@ -86,17 +86,14 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
     for (int k = 0; k < K; ++k) clear_outside<V, SHIFT>(mine[k], vector_of<V>(d, k));
     uint64_t s0 = f2(0.0f, 0.0f), s1 = s0, s2 = s0;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if constexpr (!KEPT)
-        load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, 0));
+    for (int k = 0; k < K; ++k)
       pairwise<V>([&](int i, int j) {
         const uint64_t dd = pair(vector_of<V>(d, k), i, j);
-        const uint64_t gw = fmul2(pair(vector_of<V>(g, k), i, j), pair(vector_of<V>(w, KEPT ? k : 0), i, j));
+        const uint64_t gw = fmul2(pair(vector_of<V>(g, k), i, j), pair(vector_of<V>(w, k), i, j));
         s0 = fadd2(s0, dd);
         s1 = fadd2(s1, gw);
         s2 = ffma2(gw, dd, s2);
       });
-    }
     s[0] = both(s0);
     s[1] = both(s1);
     s[2] = both(s2);
@@ -112,18 +109,15 @@ __global__ void __launch_bounds__(S::kBlock, std::max(1, kThreads<A, S> / S::kBl
       const float mg = -rstd * (s[1] * a.inv_n), mh = -rstd * mgh;
       const uint64_t scale = f2(rstd, rstd), shift = f2(t, t), mg2 = f2(mg, mg), mh2 = f2(mh, mh);
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if constexpr (!KEPT)
-          load_weight<T, V, SHIFT>(a.w, a.wide_weight, first + k * L * V, a.N, 1.0f, vector_of<V>(w, 0));
+      for (int k = 0; k < K; ++k)
         pairwise<V>([&](int i, int j) {
           const uint64_t gg = pair(vector_of<V>(g, k), i, j);
           const uint64_t h = ffma2(pair(vector_of<V>(d, k), i, j), scale, shift);
-          const uint64_t gw = fmul2(gg, pair(vector_of<V>(w, KEPT ? k : 0), i, j));
+          const uint64_t gw = fmul2(gg, pair(vector_of<V>(w, k), i, j));
           unpair(ffma2(gg, h, pair(vector_of<V>(dw, k), i, j)), vector_of<V>(dw, k), i, j);
           unpair(fadd2(gg, pair(vector_of<V>(db, k), i, j)), vector_of<V>(db, k), i, j);
           unpair(ffma2(h, mh2, ffma2(gw, scale, mg2)), vector_of<V>(d, k), i, j);
         });
-      }
     }
 #pragma unroll
     for (int k = 0; k < K; ++k) store_at<T, V, SHIFT>(to + first + k * L * V, mine[k], vector_of<V>(d, k));

@@ -49,7 +49,6 @@ class _LayerNorm(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps, off):
         y, mean, rstd = layer_norm_forward(x, weight, bias, eps, off)
         ctx.save_for_backward(x, weight, mean, rstd, off)
-        ctx.bias = bias is not None
         return y
 
     @staticmethod
