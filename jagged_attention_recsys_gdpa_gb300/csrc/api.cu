@@ -1181,7 +1181,7 @@ NormArgs norm_args(const jattn_norm_t& p, const int64_t* live, const RowTensor& 
   a.inv_n = 1.0f / static_cast<float>(p.N);
   a.wide_weight = p.weight_type == JATTN_F32;
   a.zero_behind = p.zero_behind != 0;
-  a.zero_stats = a.zero_behind || p.zero_stats != 0;
+  a.zero_stats = !a.zero_behind && p.zero_stats != 0;
   a.status = static_cast<DevStatus*>(ws);
   // where a row's stride is all its heads' the rows of all heads follow each other by the head's
   const auto even = [&](const RowTensor& t) { return !t.p || t.row == p.heads * t.head; };

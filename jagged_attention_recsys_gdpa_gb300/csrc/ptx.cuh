@@ -276,6 +276,13 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The larger of two, or a NaN where one of them is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
+
 // ---------------------------------------------------------------- asynchronous copies of a thread
 // 16 bytes from global to shared memory, of which `bytes` are read and the others zero; both aligned to 16 bytes.
 __device__ __forceinline__ void copy_async16(void* shared, const void* global, int bytes) {

@@ -1,5 +1,6 @@
 // Row operators (layer norm, rotary positions): tensors [rows, heads, N] of fp32, bf16 or fp16 with strides, read and
-// written in vectors of 16 bytes where everything is aligned to them, else value by value.
+// written in vectors of 16 bytes where everything is aligned to them. Else layer norm takes vectors that start before the rows
+// where all tensors are laid out alike (norm.cuh), and rotary positions two values at a time; else value by value.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -37,7 +38,7 @@ struct NormArgs {
   float eps, inv_n;   // inv_n: 1 / N
   bool wide_weight;   // w and b are fp32 whatever x is
   bool zero_behind;   // rows behind the live ones are set to zero, else left as they are
-  bool zero_stats;    // forward: so are their mean and rstd (always with zero_behind)
+  bool zero_stats;    // forward: not y's rows behind the live ones, but their mean and rstd are set to zero
   DevStatus* status;
 };
 
