@@ -427,13 +427,18 @@ int jattn_decode(const jattn_params_t* p, const jattn_cache_t* cache, const int6
  * elements: value (r, h, c) lies at r * row_stride + h * head_stride + c, so a view
  * of a fused projection is one. Strides of inputs may be anything >= 0 (0: a row
  * that is broadcast); rows of an output must not overlap each other. rows * heads
- * < 2^31. Pointers are aligned to their elements; where pointers, strides and N are
- * multiples of 16 bytes rows move in vectors, else value by value, with the same
- * results up to the order of sums.
+ * < 2^31. Pointers are aligned to their elements. Results are the same up to the
+ * order of sums however rows move: in vectors of 16 bytes where pointers, strides and
+ * N are multiples of them; layer norm's in vectors that start before the rows where
+ * all tensors have their rows at the same places within 16 bytes (dense tensors of any
+ * N do) and every V-th row, V values being 16 bytes, has its place again (heads
+ * beside others: strides in multiples of V), rotary positions two values at a time;
+ * else value by value, which takes several times as long.
  *
  * live_rows (device int64, NULL: all rows): rows at and behind *live_rows are
  * padding (a batch's last offset is passed here), which takes no part. Their rows in
- * the outputs are left as they were, or set to zero with zero_behind. A value outside
+ * the outputs are left as they were, or set to zero with zero_behind (layer norm's
+ * statistics by themselves with zero_stats). A value outside
  * [0, rows] sets JATTN_ERR_OFFSETS and counts as 0 or as rows. workspace: 256 bytes,
  * the status word alone, as for the paged cache. */
 enum { JATTN_F32 = 0, JATTN_BF16 = 1, JATTN_F16 = 2 };
@@ -515,18 +520,21 @@ typedef struct {
 int jattn_rotary(const jattn_rotary_t* p, const int64_t* off, const int64_t* start, const float* cos, const float* sin,
                  const void* x, void* y, void* workspace, size_t workspace_bytes, void* stream);
 
-/* The tables: cos and sin (fp32 [rows, half], 4-byte aligned) of amplitude * (pos *
- * theta_m) for pos = first .. first + rows - 1 and m < half, R = 2 * half.
+/* The tables: amplitude * cos(pos * theta_m) and amplitude * sin(pos * theta_m) (fp32
+ * [rows, half], 4-byte aligned) for pos = first .. first + rows - 1, m < half, R = 2 * half.
  *   JATTN_SCALE_NONE    theta_m = base^(-2m / R), amplitude 1
  *   JATTN_SCALE_LINEAR  theta_m / factor (positions interpolated)
  *   JATTN_SCALE_NTK     base * factor^(R / (R - 2)) in place of base (half >= 2)
  *   JATTN_SCALE_YARN    (1 - k) theta_m / factor + k theta_m, where k rises from 0 to 1
  *                       as the turns original * theta_m / 2 pi of the original context
- *                       go from beta_slow to beta_fast (Peng et al. 2023, "YaRN"),
- *                       amplitude 0.1 ln(factor) + 1
- * theta_m is formed on the host in 64 bits and becomes a 64-bit fraction of a turn per
- * position; multiples wrap exactly, so far positions keep their accuracy (theta's
- * own 2^-53 times the position). Values are within 2^-22 amplitude of the exact ones
+ *                       go from beta_slow to beta_fast, amplitude 0.1 ln(factor) + 1.
+ *                       The ramp is linear in the turns, as in the paper (Peng et al.
+ *                       2023, "YaRN"); programs that ramp over the pair's index m
+ *                       between the pairs of beta_fast and beta_slow turns have other
+ *                       angles in between
+ * theta_m is formed on the host in 64 bits and becomes a fraction of a turn per
+ * position, cut to a multiple of 2^-64; multiples wrap exactly, so far positions keep
+ * their accuracy (theta's own 2^-53, relative, and that cut, times the position). Values are within 2^-22 amplitude of the exact ones
  * for positions up to 2^24. rows * half < 2^40. */
 enum { JATTN_SCALE_NONE = 0, JATTN_SCALE_LINEAR = 1, JATTN_SCALE_NTK = 2, JATTN_SCALE_YARN = 3 };
 

@@ -202,7 +202,8 @@ struct NormShape {
 
 // Calls f(shape) with the smallest shape whose L * K vectors hold a row of n, in CTAs of NARROW threads for rows of up
 // to a warp's lanes, else of WIDE. THREE: three vectors a lane too, which the forward's registers hold (30 M values in rows of
-// 129 / 555 / 768 / 5,001: 32 / 31 / 20 / 31 us with them, 51 / 46 / 23 / 50 without) and the backward's do not. FOUR: four
+// 129 / 555 / 768 / 5,001: 32 / 31 / 20 / 31 us with them, 51 / 46 / 23 / 50 without) and the backward's do not (its 16-bit kernels
+// of three spill 476 to 604 bytes a thread at 128 registers; fp32 ones would fit and have not been measured). FOUR: four
 // vectors a lane of shifted rows, which halves what a row costs besides its vectors: its ends' single values, sums, addresses
 // (1,001 fp16 values 23.3 us, 27.1 without them, 8,001 31 against 35, 15 M fp32 values in rows of 2,999 / 4,001 22 / 24 against 33 / 29;
 // 2,001 and 4,001 fp16 values are no faster with them).

@@ -15,6 +15,8 @@ namespace {
 // Threads of an SM, for which the registers have to leave room, in CTAs of 256 (rows of up to 32 lanes: with 512 the
 // registers spill, 129 us against 103 on norm_back_histories) or 512, whose groups join their sums: with a CTA for each
 // row of 1,024 the partial rows were 10 MB and adding them took a fifth of the call (61 us against 77).
+// Rows of 1,024 lanes leave 64 registers a thread, which two 16-bit vectors or four of fp32 do not fit: 488 to 580 bytes spill (60 M
+// bf16 values in rows of 8,192 74 us, of 12,288 / 16,384 243 / 207). So do single values, sixteen a lane (704 to 1,184 bytes).
 constexpr int kNarrow = 256, kWide = 512;
 template <typename A, typename S>
 constexpr int kThreads = A::V * S::K > 8 || S::L > 32 ? 512 : 768;

@@ -285,7 +285,8 @@ def page_assign(pool, page_table, start, off=None, total=None, slots=True):
     before, whose pages page_table holds already; negative skips the sequence), n from the prefix sums ``off`` int64 [B+1] (None:
     one row each). Page numbers are written into page_table int32 [B, max_pages] where they are missing. Returns the new
     rows' slots int64 [total], page * page_size + place in the page (-1 for rows without one and rows behind off[B]);
-    ``slots`` may be a tensor to write them to, or False for none. ``total`` defaults to off[-1] (a host read) or the rows
+    ``slots`` may be a tensor to write them to, or False for none: the cache's own calls find rows by page_table, slots are for
+    a program's own kernels and buffers [n_pages * page_size, ...], and a large call is faster without. ``total`` defaults to off[-1] (a host read) or the rows
     of ``slots``. Where the pool has too few pages none is assigned (``device_status``). See jattn_page_assign."""
     if off is not None and total is None and not isinstance(slots, torch.Tensor):
         total = int(off[-1].item())

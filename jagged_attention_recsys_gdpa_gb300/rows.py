@@ -2,8 +2,9 @@
 
 * ``layer_norm(x, weight, bias, eps=..., off=...)``: layer norm over the last
   dimension with autograd; ``layer_norm_forward`` -> (y, mean, rstd) and
-  ``layer_norm_backward`` -> (dx, dweight, dbias): the raw passes. Query/key norm is
-  a layer norm of [total, H, D] rows with a weight of D values.
+  ``layer_norm_backward`` -> (dx, dweight, dbias): the raw passes, which autograd does
+  not follow. Query/key norm is a layer norm of [total, H, D] rows with a weight of D
+  values. There is no forward mode (a tangent is refused) and no second derivative.
 * ``rotary(x, tables, off=..., start=..., layout=..., inverse=...)``: rotary
   positions in either layout, on all of a head's columns or the first ones, with
   autograd. ``rope`` rotates the same pairs of neighbours for ``attention`` and
@@ -123,7 +124,8 @@ def rotary_tables(rows, dim, base=10000.0, scaling=None, factor=1.0, original=No
     """(cos, sin) fp32 [rows, dim/2] of positions first .. first + rows - 1: angle pos * theta_m, theta_m = base^(-2m/dim).
     ``scaling`` for contexts ``factor`` times as long as the model was trained on: "linear" (theta_m / factor), "ntk" (a larger base) or "yarn"
     (fast pairs as they are, slow ones / factor, by their turns within ``original`` positions, and values times 0.1
-    ln(factor) + 1). Angles are exact to 2^-53 of theta however far the position lies. See jattn_rotary_tables."""
+    ln(factor) + 1; the ramp between ``beta_slow`` and ``beta_fast`` is linear in the turns, the paper's, not in the pair's index
+    as in some programs). Angles are exact to 2^-53 of theta however far the position lies. See jattn_rotary_tables."""
     if scaling not in _SCALINGS:
         raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
     if scaling == "yarn" and original is None:
